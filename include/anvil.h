@@ -218,6 +218,183 @@ anvil_status anvil_adam_step(float* param, const float* grad, float* exp_avg, fl
                              size_t count, float beta1, float beta2, float eps, float step_size,
                              float eff_wd, void* stream);
 
+/* ---- operators around the banks: the layers whose gradients a bank or Adam step takes,
+ * and the loss.  Layer norm, the linear layer with its bias, activation and residual, and
+ * the log probabilities of given tokens, each forward and backward.
+ *
+ * Common rules.  DEVICE pointers, caller-owned.  A matrix argument is row-major with
+ * contiguous rows and a row stride ld* in elements (at least the row's length; not read
+ * when there is at most one row), so a view of wider rows is fine.  Pointers are aligned
+ * to their element size; rows on 16-byte boundaries are faster.  Sums, statistics and
+ * accumulators are fp32; a result is rounded to its type once, to nearest even.  rows may
+ * be 0: forward calls then do nothing, gradients of parameters become 0.  Results are the
+ * same bits on every call with the same arguments (no atomics).  Written buffers must not
+ * overlap any other buffer of the call except where said; views that interleave in one
+ * buffer without sharing an element are fine if their row strides are the same.  Calls
+ * allocate nothing and never synchronise, so they may be captured in a CUDA graph; where
+ * a call needs scratch, its workspace is as for anvil_multi_bank_step. */
+typedef enum { ANVIL_F32 = 0, ANVIL_BF16 = 1, ANVIL_F16 = 2 } anvil_dtype;
+
+#define ANVIL_MAX_ROWS (1 << 30)     /* largest rows of these operators */
+#define ANVIL_MAX_WIDTH 16384        /* largest layer-norm width */
+#define ANVIL_MAX_FEATURES (1 << 20) /* largest n or k of a linear layer */
+#define ANVIL_MAX_VOCAB (1 << 24)    /* largest vocabulary */
+#define ANVIL_MAX_TOP 32             /* most alternatives per row */
+
+/* Layer norm of every row of x [rows, width]:
+ *   mean = sum x / width,  rstd = 1 / sqrt(sum (x - mean)^2 / width + eps),
+ *   y = (x - mean) rstd weight + bias.
+ * x and y have type dtype; weight and bias [width] have type weight_dtype, fp32 or dtype,
+ * or are NULL (1 and 0).  mean and rstd [rows] fp32 are written for the backward pass, or
+ * NULL.  y may be x itself (same pointer and stride). */
+typedef struct {
+    const void* x;
+    const void* weight;
+    const void* bias;
+    void* y;
+    float* mean;
+    float* rstd;
+    int64_t rows;
+    int64_t ldx, ldy;
+    int width;
+    int dtype, weight_dtype;
+    float eps;
+} anvil_layernorm_desc;
+anvil_status anvil_layernorm_forward(const anvil_layernorm_desc* desc, void* stream);
+
+/* Its gradient, for dy = dL/dy and the mean and rstd of the forward pass; with
+ * h = (x - mean) rstd and g = dy weight:
+ *   dx = rstd (g - mean(g) - h mean(g h)) [+ residual_grad],
+ *   dweight = sum over rows of dy h,  dbias = sum over rows of dy.
+ * residual_grad [rows, width] of type dtype, or NULL: the gradient that reaches x past the
+ * norm.  dx, dweight and dbias may each be NULL (not computed); dweight and dbias are fp32.
+ * dx may be dy, x or residual_grad itself (same pointer and stride). */
+typedef struct {
+    const void* dy;
+    const void* x;
+    const float* mean;
+    const float* rstd;
+    const void* weight;
+    const void* residual_grad;
+    void* dx;
+    float* dweight;
+    float* dbias;
+    int64_t rows;
+    int64_t lddy, ldx, ldr, lddx;
+    int width;
+    int dtype, weight_dtype;
+} anvil_layernorm_grad_desc;
+size_t anvil_layernorm_backward_workspace_bytes(const anvil_layernorm_grad_desc* desc);
+anvil_status anvil_layernorm_backward(const anvil_layernorm_grad_desc* desc, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+typedef enum {
+    ANVIL_ACT_NONE = 0,
+    ANVIL_ACT_RELU = 1,
+    ANVIL_ACT_RELU2 = 2,     /* max(z, 0)^2 */
+    ANVIL_ACT_GELU = 3,      /* z Phi(z) */
+    ANVIL_ACT_GELU_TANH = 4, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    ANVIL_ACT_SILU = 5       /* z / (1 + e^-z) */
+} anvil_activation;
+
+/* The linear layer:  z = x W^T + bias,  y = act(z) + residual.
+ * x [rows, k], residual and y [rows, n], W: [n, k], or stored as its transpose [k, n] when
+ * weight_transposed != 0 (one bank of one shape can hold both projections of a block), all
+ * of type dtype (ANVIL_BF16 or ANVIL_F16).  bias [n] of type bias_dtype (fp32 or dtype) or
+ * NULL; residual may be NULL.  preact [rows, n], or NULL, receives z (rounded; y comes from
+ * the unrounded z) for the backward pass.  From one row to many: few rows read the weight
+ * once.  y may be residual itself (same pointer and stride). */
+typedef struct {
+    const void* x;
+    const void* weight;
+    const void* bias;
+    const void* residual;
+    void* y;
+    void* preact;
+    int64_t rows;
+    int64_t ldx, ldw, ldr, ldy, ldz;
+    int n, k;
+    int dtype, bias_dtype;
+    int activation;
+    int weight_transposed;
+} anvil_linear_desc;
+/* Scratch of a call (0 for invalid descriptors and where none is needed): copies of
+ * operands whose rows are not on 16-byte boundaries.  Depends on the pointers' alignment. */
+size_t anvil_linear_workspace_bytes(const anvil_linear_desc* desc);
+anvil_status anvil_linear_forward(const anvil_linear_desc* desc, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient, for dy = dL/dy and z = preact (not read for ANVIL_ACT_NONE):
+ *   dz = dy act'(z),  dx = dz W,  dweight = dz^T x,  dbias = sum over rows of dz.
+ * dx [rows, k] of type dtype; dweight in W's layout (weight_transposed), of type
+ * dweight_dtype: dtype or ANVIL_F32 (what the bank step takes); dbias [n] fp32.  Each may be
+ * NULL (not computed); x is read for dweight only, weight for dx only.  dz is rounded to
+ * dtype as the products' operand; dbias sums the unrounded dz.  accumulate != 0: dweight
+ * and dbias are added to what they hold.  The residual's gradient is dy itself. */
+typedef struct {
+    const void* dy;
+    const void* x;
+    const void* weight;
+    const void* preact;
+    void* dx;
+    void* dweight;
+    float* dbias;
+    int64_t rows;
+    int64_t lddy, ldx, ldw, ldz, lddx, lddw;
+    int n, k;
+    int dtype, dweight_dtype;
+    int activation;
+    int weight_transposed;
+    int accumulate;
+} anvil_linear_grad_desc;
+size_t anvil_linear_backward_workspace_bytes(const anvil_linear_grad_desc* desc);
+anvil_status anvil_linear_backward(const anvil_linear_grad_desc* desc, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Log probabilities of given tokens under logits [rows, vocab] of type dtype:
+ *   lse = log sum_j e^x_j,  logprob = x_target - lse,  entropy = lse - sum_j p_j x_j,
+ *   and the `top` (0..ANVIL_MAX_TOP, at most vocab) largest x_j - lse with their columns,
+ *   largest first, equal values by the lower column.
+ * targets [rows] int32 (int64 when targets_int64 != 0), or NULL with logprob NULL.  A negative target
+ * marks a position that does not count: its log probability is 0; one of vocab or more
+ * gives NaN.  logprob, entropy and lse [rows] fp32 may each be NULL; top_logprob fp32 and
+ * top_index int32 are [rows, top], contiguous.  A logit of -inf is a token that cannot be;
+ * a row of nothing else has lse, logprob and top_logprob -inf and entropy 0.  A row with a
+ * NaN or +inf comes out NaN (its top_index then means nothing). */
+typedef struct {
+    const void* logits;
+    const void* targets;
+    float* logprob;
+    float* entropy;
+    float* lse;
+    float* top_logprob;
+    int32_t* top_index;
+    int64_t rows;
+    int64_t ld;
+    int vocab, top;
+    int dtype, targets_int64;
+} anvil_logprob_desc;
+anvil_status anvil_token_logprobs(const anvil_logprob_desc* desc, void* stream);
+
+/* Their gradient, for u = dL/dlogprob (NULL: 0) and v = dL/dentropy (NULL: 0) [rows] fp32
+ * and the lse (and entropy, with v) of the forward pass, p_j = e^(x_j - lse):
+ *   dlogits_j = u ([j = target] - p_j) - v p_j (x_j - lse + entropy),
+ * of type dtype [rows, vocab].  u is taken as 0 where the target is negative; a row whose
+ * lse is -inf has the gradient 0.  dlogits may be logits itself (same pointer and stride). */
+typedef struct {
+    const void* logits;
+    const void* targets;
+    const float* lse;
+    const float* entropy;
+    const float* grad_logprob;
+    const float* grad_entropy;
+    void* dlogits;
+    int64_t rows;
+    int64_t ld, ldd;
+    int vocab;
+    int dtype, targets_int64;
+} anvil_logprob_grad_desc;
+anvil_status anvil_token_logprobs_backward(const anvil_logprob_grad_desc* desc, void* stream);
+
 /* Per-stage dumps of one bank step, for parity testing (not the hot path).
  * DEVICE pointers, each optional (NULL = skip), in the page's layout:
  *   X_raw [g, m, n] bf16            bf16 cast of the momentum lookahead
@@ -263,7 +440,8 @@ anvil_status anvil_selftest_wait_timeout(unsigned timeout_us, void* stream);
 
 /* Per-launch timing for benchmarks.  Between anvil_profile_begin and
  * anvil_profile_end, every kernel launch of anvil_multi_bank_step, anvil_bank_step,
- * anvil_update_tail and anvil_adam_step in the process is bracketed by two CUDA events
+ * anvil_update_tail, anvil_adam_step and the operators around the banks in the process is
+ * bracketed by two CUDA events
  * recorded on the call's stream (at most max_records launches; later ones are
  * not timed).  begin creates the events (a host call: do not begin, or step
  * with profiling on, while a stream is capturing).  end synchronises, writes up
@@ -284,7 +462,15 @@ typedef enum {
     ANVIL_KERNEL_TAIL_SCALE = 9,   /* update tail: lane energies and scales */
     ANVIL_KERNEL_TAIL_APPLY = 10,  /* update tail: equalise + sign-aligned decay update */
     ANVIL_KERNEL_ADAM = 11,        /* Adam step */
-    ANVIL_KERNEL_CASCADE = 12      /* the whole cascade (every product of every map) */
+    ANVIL_KERNEL_CASCADE = 12,     /* the whole cascade (every product of every map) */
+    ANVIL_KERNEL_NORM_FORWARD = 13,      /* layer norm */
+    ANVIL_KERNEL_NORM_BACKWARD = 14,     /* its row pass: dx and partial column sums */
+    ANVIL_KERNEL_NORM_GRADS = 15,        /* dweight and dbias from the partial sums */
+    ANVIL_KERNEL_LINEAR_PREPARE = 16,    /* copies of unaligned operands; dz = dy act'(z) and its partial column sums */
+    ANVIL_KERNEL_LINEAR_PRODUCT = 17,    /* a product of the linear layer */
+    ANVIL_KERNEL_LINEAR_SUM = 18,        /* sums of split products and of dbias */
+    ANVIL_KERNEL_LOGPROB = 19,           /* token log probabilities */
+    ANVIL_KERNEL_LOGPROB_BACKWARD = 20   /* their gradient */
 } anvil_kernel_kind;
 
 typedef struct { int kind; float ms; } anvil_profile_record;

@@ -9,6 +9,10 @@ fallback of any kind.
 Tensors are torch tensors on the current CUDA device: grad fp32 [g, m, n], velocity
 fp32 [2, g, m, n], out bf16 [g, m, n], all contiguous.  Calls are enqueued on
 ``torch.cuda.current_stream()`` unless a stream is given.
+
+The operators around the banks (layer norm, the linear layer, token log probabilities)
+take matrices whose rows may be a view of wider ones and allocate the results they
+return, and their scratch, on the stream they run on.
 """
 from __future__ import annotations
 
@@ -34,8 +38,11 @@ STATUS = {0: "ANVIL_OK", 1: "ANVIL_ERR_INVALID_ARG", 2: "ANVIL_ERR_UNSUPPORTED_S
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, ERR_ALIGNMENT, ERR_ALIAS, ERR_WORKSPACE, \
     ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE, ERR_UNAVAILABLE = range(10)
 KERNEL_KINDS = ("momentum", "norm_d", "normalize", "gram_norm", "gram", "sqpoly", "xupdate",
-                "xupdate_out", "tail_power", "tail_scale", "tail_apply", "adam", "cascade")
+                "xupdate_out", "tail_power", "tail_scale", "tail_apply", "adam", "cascade",
+                "norm_forward", "norm_backward", "norm_grads", "linear_prepare", "linear_product",
+                "linear_sum", "logprob", "logprob_backward")
 MAX_MAPS, MAX_BANKS = 16, 8
+MAX_TOP = 32
 
 
 class AnvilError(RuntimeError):
@@ -78,6 +85,49 @@ class ScheduleRun(ctypes.Structure):
                 ("nmat", ctypes.c_int), ("begin", ctypes.c_int), ("tiles", ctypes.c_int)]
 
 
+_P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+
+
+class LayernormDesc(ctypes.Structure):
+    _fields_ = [("x", _P), ("weight", _P), ("bias", _P), ("y", _P), ("mean", _P), ("rstd", _P),
+                ("rows", _L), ("ldx", _L), ("ldy", _L), ("width", _I), ("dtype", _I),
+                ("weight_dtype", _I), ("eps", ctypes.c_float)]
+
+
+class LayernormGradDesc(ctypes.Structure):
+    _fields_ = [("dy", _P), ("x", _P), ("mean", _P), ("rstd", _P), ("weight", _P),
+                ("residual_grad", _P), ("dx", _P), ("dweight", _P), ("dbias", _P),
+                ("rows", _L), ("lddy", _L), ("ldx", _L), ("ldr", _L), ("lddx", _L),
+                ("width", _I), ("dtype", _I), ("weight_dtype", _I)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("x", _P), ("weight", _P), ("bias", _P), ("residual", _P), ("y", _P), ("preact", _P),
+                ("rows", _L), ("ldx", _L), ("ldw", _L), ("ldr", _L), ("ldy", _L), ("ldz", _L),
+                ("n", _I), ("k", _I), ("dtype", _I), ("bias_dtype", _I), ("activation", _I),
+                ("weight_transposed", _I)]
+
+
+class LinearGradDesc(ctypes.Structure):
+    _fields_ = [("dy", _P), ("x", _P), ("weight", _P), ("preact", _P), ("dx", _P), ("dweight", _P),
+                ("dbias", _P), ("rows", _L), ("lddy", _L), ("ldx", _L), ("ldw", _L), ("ldz", _L),
+                ("lddx", _L), ("lddw", _L), ("n", _I), ("k", _I), ("dtype", _I),
+                ("dweight_dtype", _I), ("activation", _I), ("weight_transposed", _I),
+                ("accumulate", _I)]
+
+
+class LogprobDesc(ctypes.Structure):
+    _fields_ = [("logits", _P), ("targets", _P), ("logprob", _P), ("entropy", _P), ("lse", _P),
+                ("top_logprob", _P), ("top_index", _P), ("rows", _L), ("ld", _L), ("vocab", _I),
+                ("top", _I), ("dtype", _I), ("targets_int64", _I)]
+
+
+class LogprobGradDesc(ctypes.Structure):
+    _fields_ = [("logits", _P), ("targets", _P), ("lse", _P), ("entropy", _P), ("grad_logprob", _P),
+                ("grad_entropy", _P), ("dlogits", _P), ("rows", _L), ("ld", _L), ("ldd", _L),
+                ("vocab", _I), ("dtype", _I), ("targets_int64", _I)]
+
+
 class ProfileRecord(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int), ("ms", ctypes.c_float)]
 
@@ -106,6 +156,21 @@ _lib.anvil_update_tail.argtypes = [ctypes.POINTER(TailDesc), _i, _vp, _sz, _vp]
 _lib.anvil_update_tail.restype = _i
 _lib.anvil_adam_step.argtypes = [_vp, _vp, _vp, _vp, _sz, _f, _f, _f, _f, _f, _vp]
 _lib.anvil_adam_step.restype = _i
+_lib.anvil_layernorm_forward.argtypes = [ctypes.POINTER(LayernormDesc), _vp]
+_lib.anvil_layernorm_backward_workspace_bytes.argtypes = [ctypes.POINTER(LayernormGradDesc)]
+_lib.anvil_layernorm_backward_workspace_bytes.restype = _sz
+_lib.anvil_layernorm_backward.argtypes = [ctypes.POINTER(LayernormGradDesc), _vp, _sz, _vp]
+_lib.anvil_linear_workspace_bytes.argtypes = [ctypes.POINTER(LinearDesc)]
+_lib.anvil_linear_workspace_bytes.restype = _sz
+_lib.anvil_linear_forward.argtypes = [ctypes.POINTER(LinearDesc), _vp, _sz, _vp]
+_lib.anvil_linear_backward_workspace_bytes.argtypes = [ctypes.POINTER(LinearGradDesc)]
+_lib.anvil_linear_backward_workspace_bytes.restype = _sz
+_lib.anvil_linear_backward.argtypes = [ctypes.POINTER(LinearGradDesc), _vp, _sz, _vp]
+_lib.anvil_token_logprobs.argtypes = [ctypes.POINTER(LogprobDesc), _vp]
+_lib.anvil_token_logprobs_backward.argtypes = [ctypes.POINTER(LogprobGradDesc), _vp]
+for _f_name in ("layernorm_forward", "layernorm_backward", "linear_forward", "linear_backward",
+                "token_logprobs", "token_logprobs_backward"):
+    getattr(_lib, "anvil_" + _f_name).restype = _i
 _lib.anvil_device_error.argtypes = [_i]
 _lib.anvil_device_error.restype = _i
 _lib.anvil_last_device_error.argtypes = [_vp]
@@ -400,6 +465,418 @@ def adam_step(param, grad, exp_avg, exp_avg_sq, beta1, beta2, eps, step_size, ef
     st = _lib.anvil_adam_step(param.data_ptr(), grad.data_ptr(), exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
                               param.numel(), beta1, beta2, eps, step_size, eff_wd, _stream_arg(stream))
     _check(st, "anvil_adam_step")
+
+
+# ---- the operators around the banks
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
+_F32, _BF16, _F16 = range(3)
+_dtype_codes = {}
+_torch = None
+
+# The checks below run on every call, ahead of kernels that may take two microseconds, so
+# they are written for few Python operations.
+
+
+def _get_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _dtype_codes.update({torch.float32: _F32, torch.bfloat16: _BF16, torch.float16: _F16})
+        _torch = torch
+    return _torch
+
+
+def _dtype_code(t, what):
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be fp32, bf16 or fp16, not {t.dtype}")
+    return code
+
+
+def _rows_of(t, what):
+    """(rows, width, row stride) of a tensor [..., width] taken as a matrix of contiguous
+    rows with one stride; refuses layouts that are not."""
+    shape = t.shape
+    if len(shape) == 2:
+        rows, width = shape
+        ld, inner = t.stride()
+    elif len(shape) < 1:
+        raise ValueError(f"{what} must have at least one dimension")
+    else:
+        strides = t.stride()
+        width, inner = shape[-1], strides[-1]
+        rows, ld = 1, width
+        for n, s in zip(shape[-2::-1], strides[-2::-1]):
+            if n != 1:
+                if rows == 1:
+                    ld = s
+                elif s != ld * rows:
+                    raise ValueError(f"{what}: leading dimensions without one common row stride; use .contiguous()")
+                rows *= n
+    if inner != 1 and width > 1 and rows:
+        raise ValueError(f"{what}: rows must be contiguous (last stride 1); use .contiguous()")
+    if ld < width:
+        if rows > 1:
+            raise ValueError(f"{what}: rows overlap (row stride {ld}, width {width}); use .contiguous()")
+        ld = width
+    return rows, width, ld
+
+
+def _vector(t, n, dtypes, what):
+    """Pointer of a contiguous vector of n values."""
+    if t.dtype not in dtypes or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+        raise ValueError(f"{what} must be a contiguous vector of {n} values of {' or '.join(map(str, dtypes))}")
+    return t.data_ptr()
+
+
+def _per_row(t, rows, what):
+    """Pointer of an optional contiguous fp32 tensor of one value per row."""
+    if t is None:
+        return 0
+    if t.dtype != _torch.float32 or t.numel() != rows or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous fp32, one value per row")
+    return t.data_ptr()
+
+
+def _same_form(t, shape, dtype, what, like):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{what} must have {like}")
+
+
+def _current_stream(what, tensors):
+    """Handle of the current stream, after checking that every tensor is on the current GPU."""
+    if not tensors[0].is_cuda:
+        raise ValueError(f"{what}: every tensor must be on the current CUDA device")
+    index = _torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{what}: every tensor must be on the current CUDA device")
+    return _torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_stream(stream, call, tensors):
+    """Runs call() with `stream` current, so that its results and scratch belong to it, and
+    tells the allocator that the inputs are in use there."""
+    torch = _get_torch()
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(s)
+        return call()
+
+
+def _scratch(nbytes, workspace, ref):
+    """(tensor to keep, pointer, bytes) of a call's workspace: the caller's, or a new one."""
+    if workspace is not None:
+        return (workspace,) + _workspace_arg(workspace, ref)
+    if nbytes == 0:
+        return None, 0, 0
+    t = _torch.empty(nbytes, dtype=_torch.uint8, device=ref.device)
+    return t, t.data_ptr(), nbytes
+
+
+def layernorm_forward(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
+    """Layer norm over the last dimension of x (fp32, bf16 or fp16).
+
+    weight and bias: vectors of the width, fp32 or x's type, or None.  Returns (y, mean,
+    rstd); mean and rstd are fp32 of x's leading shape, for layernorm_backward.  out may be
+    x itself.
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: layernorm_forward(x, weight, bias, eps, out), (x, weight, bias, out))
+    torch = _torch or _get_torch()
+    code, dtype = _dtype_code(x, "x"), x.dtype
+    rows, width, ldx = _rows_of(x, "x")
+    wcode, wp, bp = code, 0, 0
+    if weight is not None or bias is not None:
+        wt = (bias if weight is None else weight).dtype
+        if wt != dtype:
+            if wt != torch.float32:
+                raise ValueError("weight and bias must be fp32 or of x's type")
+            wcode = _F32
+        if weight is not None:
+            wp = _vector(weight, width, (wt,), "weight")
+        if bias is not None:
+            bp = _vector(bias, width, (wt,), "bias")
+    s = _current_stream("layernorm_forward", (x, weight, bias, out))
+    if out is None:
+        y, ldy = torch.empty(x.shape, dtype=dtype, device=x.device), width
+    else:
+        y = out
+        _same_form(y, x.shape, dtype, "out", "x's shape and type")
+        ldy = _rows_of(y, "out")[2]
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    d = LayernormDesc(x.data_ptr(), wp, bp, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows, ldx, ldy, width,
+                      code, wcode, eps)
+    st = _lib.anvil_layernorm_forward(d, s)
+    if st:
+        _check(st, "anvil_layernorm_forward")
+    return y, mean, rstd
+
+
+def layernorm_backward(dy, x, mean, rstd, weight=None, residual_grad=None, out=None, weight_grads=True,
+                       workspace=None, stream=None):
+    """Gradient of layernorm_forward: returns (dx, dweight, dbias), dweight and dbias fp32
+    (None without weight_grads).
+
+    residual_grad (x's shape and type) is added to dx: the gradient that reaches x past the
+    norm.  out (dx) may be dy, x or residual_grad itself.
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: layernorm_backward(dy, x, mean, rstd, weight, residual_grad, out,
+                                                             weight_grads, workspace),
+                          (dy, x, mean, rstd, weight, residual_grad, out, workspace))
+    torch = _torch or _get_torch()
+    code, dtype, shape = _dtype_code(x, "x"), x.dtype, x.shape
+    rows, width, ldx = _rows_of(x, "x")
+    _same_form(dy, shape, dtype, "dy", "x's shape and type")
+    lddy, ldr, rp = _rows_of(dy, "dy")[2], 0, 0
+    if residual_grad is not None:
+        _same_form(residual_grad, shape, dtype, "residual_grad", "x's shape and type")
+        ldr, rp = _rows_of(residual_grad, "residual_grad")[2], residual_grad.data_ptr()
+    mp, sp = _per_row(mean, rows, "mean"), _per_row(rstd, rows, "rstd")
+    wcode, wp = code, 0
+    if weight is not None:
+        if weight.dtype != dtype:
+            if weight.dtype != torch.float32:
+                raise ValueError("weight must be fp32 or of x's type")
+            wcode = _F32
+        wp = _vector(weight, width, (weight.dtype,), "weight")
+    s = _current_stream("layernorm_backward", (x, dy, mean, rstd, weight, residual_grad, out, workspace))
+    if out is None:
+        dx, lddx = torch.empty(shape, dtype=dtype, device=x.device), width
+    else:
+        dx = out
+        _same_form(dx, shape, dtype, "out", "x's shape and type")
+        lddx = _rows_of(dx, "out")[2]
+    dw, db, dwp, dbp = None, None, 0, 0
+    if weight_grads:
+        dw = torch.empty((width,), dtype=torch.float32, device=x.device)
+        db = torch.empty_like(dw)
+        dwp, dbp = dw.data_ptr(), db.data_ptr()
+    d = LayernormGradDesc(dy.data_ptr(), x.data_ptr(), mp, sp, wp, rp, dx.data_ptr(), dwp, dbp, rows, lddy, ldx, ldr,
+                          lddx, width, code, wcode)
+    keep, wsp, wsb = _scratch(_lib.anvil_layernorm_backward_workspace_bytes(d), workspace, x)
+    st = _lib.anvil_layernorm_backward(d, wsp, wsb, s)
+    if st:
+        _check(st, "anvil_layernorm_backward")
+    return dx, dw, db
+
+
+def _weight_of(w, dtype, what):
+    """(n, k, row stride, transposed) of a weight [n, k] stored by rows or by columns."""
+    shape = w.shape
+    if len(shape) != 2 or w.dtype != dtype:
+        raise ValueError(f"{what} must be [n, k] of {dtype}")
+    (n, k), (s0, s1) = shape, w.stride()
+    if (s1 == 1 or k == 1) and (s0 >= k or n == 1):
+        return n, k, s0 if s0 > k else k, 0
+    if (s0 == 1 or n == 1) and (s1 >= n or k == 1):
+        return n, k, s1 if s1 > n else n, 1
+    raise ValueError(f"{what} must be stored by rows or by columns; use .contiguous()")
+
+
+def _activation(name):
+    code = 0 if name is None else ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
+    return code
+
+
+def _linear_sizes(x, weight):
+    code = _dtype_code(x, "x")
+    if code == _F32:
+        raise ValueError("x must be bf16 or fp16")
+    rows, k, ldx = _rows_of(x, "x")
+    n, wk, ldw, tr = _weight_of(weight, x.dtype, "weight")
+    if wk != k:
+        raise ValueError(f"weight must be [n, {k}]")
+    return code, rows, k, ldx, n, ldw, tr
+
+
+def linear_forward(x, weight, bias=None, activation=None, residual=None, save_preact=False, out=None,
+                   workspace=None, stream=None):
+    """y = act(x weight^T + bias) + residual, bf16 or fp16, for x [..., k] and weight [n, k].
+
+    weight may be stored by rows or by columns (``bank[i].t()``); bias [n] is fp32 or x's
+    type; activation is a key of ACTIVATIONS.  Returns y, or (y, preact) with save_preact:
+    what linear_backward takes.  out may be residual itself.
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: linear_forward(x, weight, bias, activation, residual, save_preact, out,
+                                                         workspace),
+                          (x, weight, bias, residual, out, workspace))
+    torch = _torch or _get_torch()
+    code, rows, k, ldx, n, ldw, tr = _linear_sizes(x, weight)
+    act = _activation(activation)
+    dtype, bp, bcode, rp, ldr, zp = x.dtype, 0, code, 0, 0, 0
+    if bias is not None:
+        bp = _vector(bias, n, (dtype, torch.float32), "bias")
+        if bias.dtype != dtype:
+            bcode = _F32
+    shape = x.shape[:-1] + (n,)
+    if residual is not None:
+        _same_form(residual, shape, dtype, "residual", "the result's shape and type")
+        rp, ldr = residual.data_ptr(), _rows_of(residual, "residual")[2]
+    s = _current_stream("linear_forward", (x, weight, bias, residual, out, workspace))
+    if out is None:
+        y, ldy = torch.empty(shape, dtype=dtype, device=x.device), n
+    else:
+        y = out
+        _same_form(y, shape, dtype, "out", "the result's shape and type")
+        ldy = _rows_of(y, "out")[2]
+    z = None
+    if save_preact:
+        z = torch.empty(shape, dtype=dtype, device=x.device)
+        zp = z.data_ptr()
+    d = LinearDesc(x.data_ptr(), weight.data_ptr(), bp, rp, y.data_ptr(), zp, rows, ldx, ldw, ldr, ldy, n, n, k, code,
+                   bcode, act, tr)
+    keep, wsp, wsb = _scratch(_lib.anvil_linear_workspace_bytes(d), workspace, x)
+    st = _lib.anvil_linear_forward(d, wsp, wsb, s)
+    if st:
+        _check(st, "anvil_linear_forward")
+    return (y, z) if save_preact else y
+
+
+def linear_backward(dy, x, weight, preact=None, activation=None, need_dx=True, need_dweight=True, bias_grad=True,
+                    dweight_dtype=None, dweight=None, dbias=None, accumulate=False, workspace=None, stream=None):
+    """Gradient of linear_forward: returns (dx, dweight, dbias), None where not asked for.
+
+    preact is the forward call's z (needed with an activation).  dweight has weight's shape
+    and order and dweight_dtype: x's type (default) or fp32, what the bank step takes; dbias
+    is fp32.  dweight and dbias may be given (with accumulate they are added to).  The
+    residual's gradient is dy itself.
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: linear_backward(dy, x, weight, preact, activation, need_dx, need_dweight,
+                                                          bias_grad, dweight_dtype, dweight, dbias, accumulate,
+                                                          workspace),
+                          (dy, x, weight, preact, dweight, dbias, workspace))
+    torch = _torch or _get_torch()
+    code, rows, k, ldx, n, ldw, tr = _linear_sizes(x, weight)
+    act, dtype = _activation(activation), x.dtype
+    _same_form(dy, x.shape[:-1] + (n,), dtype, "dy", "the forward result's shape and type")
+    lddy, zp, ldz = _rows_of(dy, "dy")[2], 0, 0
+    if act:
+        if preact is None:
+            raise ValueError("preact is needed with an activation")
+        _same_form(preact, dy.shape, dtype, "preact", "the forward result's shape and type")
+        zp, ldz = preact.data_ptr(), _rows_of(preact, "preact")[2]
+    if accumulate and ((need_dweight and dweight is None) or (bias_grad and dbias is None)):
+        raise ValueError("accumulate needs dweight and dbias to add to")
+    wt = dweight.dtype if dweight is not None else dweight_dtype or dtype
+    if wt != dtype and wt != torch.float32:
+        raise ValueError("dweight must be fp32 or of x's type")
+    s = _current_stream("linear_backward", (x, dy, weight, preact, dweight, dbias, workspace))
+    dx, dxp, dwp, lddw, dbp = None, 0, 0, 0, 0
+    if need_dx:
+        dx = torch.empty(x.shape, dtype=dtype, device=x.device)
+        dxp = dx.data_ptr()
+    if need_dweight:
+        if dweight is None:
+            dweight = torch.empty((k, n) if tr else (n, k), dtype=wt, device=x.device)
+            lddw = n if tr else k
+            if tr:
+                dweight = dweight.t()
+        else:
+            dn, dk, lddw, dtr = _weight_of(dweight, wt, "dweight")
+            if (dn, dk) != (n, k) or (dtr != tr and n > 1 and k > 1):
+                raise ValueError("dweight must have weight's shape and order")
+        dwp = dweight.data_ptr()
+    if bias_grad:
+        if dbias is None:
+            dbias = torch.empty((n,), dtype=torch.float32, device=x.device)
+        dbp = _vector(dbias, n, (torch.float32,), "dbias")
+    d = LinearGradDesc(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), zp, dxp, dwp, dbp, rows, lddy, ldx, ldw, ldz, k,
+                       lddw, n, k, code, code if wt == dtype else _F32, act, tr, 1 if accumulate else 0)
+    keep, wsp, wsb = _scratch(_lib.anvil_linear_backward_workspace_bytes(d), workspace, x)
+    st = _lib.anvil_linear_backward(d, wsp, wsb, s)
+    if st:
+        _check(st, "anvil_linear_backward")
+    return dx, dweight if need_dweight else None, dbias if bias_grad else None
+
+
+def _targets_arg(targets, rows):
+    """(pointer, whether int64) of optional target tokens."""
+    if targets is None:
+        return 0, 0
+    wide = targets.dtype == _torch.int64
+    if not (wide or targets.dtype == _torch.int32) or targets.numel() != rows or not targets.is_contiguous():
+        raise ValueError("targets must be contiguous int64 or int32, one per row")
+    return targets.data_ptr(), 1 if wide else 0
+
+
+def token_logprobs(logits, targets=None, top=0, stream=None):
+    """Log probabilities of the target tokens under logits [..., vocab] (fp32, bf16, fp16).
+
+    Returns (logprob, entropy, lse, top_logprob, top_index): fp32 of the leading shape, and
+    [..., top] with int32 columns (both None for top = 0; logprob None without targets).
+    A negative target does not count (0); a logit of -inf is a token that cannot be.
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: token_logprobs(logits, targets, top), (logits, targets))
+    torch = _torch or _get_torch()
+    code = _dtype_code(logits, "logits")
+    rows, vocab, ld = _rows_of(logits, "logits")
+    if not 0 <= top <= (vocab if vocab < MAX_TOP else MAX_TOP):
+        raise ValueError(f"top must be between 0 and {MAX_TOP} and at most the vocabulary")
+    tp, t64 = _targets_arg(targets, rows)
+    s = _current_stream("token_logprobs", (logits, targets))
+    lead, dev = logits.shape[:-1], logits.device
+    lse = torch.empty(lead, dtype=torch.float32, device=dev)
+    ent = torch.empty_like(lse)
+    lp, lpp, tv, ti, tvp, tip = None, 0, None, None, 0, 0
+    if tp:
+        lp = torch.empty_like(lse)
+        lpp = lp.data_ptr()
+    elif targets is not None:
+        lp = torch.empty_like(lse)  # no rows
+    if top:
+        tv = torch.empty(lead + (top,), dtype=torch.float32, device=dev)
+        ti = torch.empty(lead + (top,), dtype=torch.int32, device=dev)
+        tvp, tip = tv.data_ptr(), ti.data_ptr()
+    d = LogprobDesc(logits.data_ptr(), tp, lpp, ent.data_ptr(), lse.data_ptr(), tvp, tip, rows, ld, vocab, top, code,
+                    t64)
+    st = _lib.anvil_token_logprobs(d, s)
+    if st:
+        _check(st, "anvil_token_logprobs")
+    return lp, ent, lse, tv, ti
+
+
+def token_logprobs_backward(logits, targets, lse, grad_logprob=None, entropy=None, grad_entropy=None, out=None,
+                            stream=None):
+    """dlogits of token_logprobs for the gradients of logprob and (with the forward call's
+    entropy) of the entropy, fp32 one per row.  out may be logits itself."""
+    if stream is not None:
+        return _on_stream(stream, lambda: token_logprobs_backward(logits, targets, lse, grad_logprob, entropy,
+                                                                  grad_entropy, out),
+                          (logits, targets, lse, grad_logprob, entropy, grad_entropy, out))
+    torch = _torch or _get_torch()
+    code = _dtype_code(logits, "logits")
+    rows, vocab, ld = _rows_of(logits, "logits")
+    tp, t64 = _targets_arg(targets, rows)
+    if grad_logprob is not None and targets is None:
+        raise ValueError("grad_logprob needs targets")
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
+    if lse is None:
+        raise ValueError("lse is needed")
+    lp, ep = _per_row(lse, rows, "lse"), _per_row(entropy, rows, "entropy")
+    up, vp = _per_row(grad_logprob, rows, "grad_logprob"), _per_row(grad_entropy, rows, "grad_entropy")
+    s = _current_stream("token_logprobs_backward", (logits, targets, lse, grad_logprob, entropy, grad_entropy, out))
+    if out is None:
+        dl, ldd = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), vocab
+    else:
+        dl = out
+        _same_form(dl, logits.shape, logits.dtype, "out", "the logits' shape and type")
+        ldd = _rows_of(dl, "out")[2]
+    d = LogprobGradDesc(logits.data_ptr(), tp, lp, ep, up, vp, dl.data_ptr(), rows, ld, ldd, vocab, code, t64)
+    st = _lib.anvil_token_logprobs_backward(d, s)
+    if st:
+        _check(st, "anvil_token_logprobs_backward")
+    return dl
 
 
 def schedule_runs(shapes, nmaps=6):

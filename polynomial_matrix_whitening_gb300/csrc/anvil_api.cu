@@ -25,8 +25,10 @@
 
 
 #include "../../include/anvil.h"
+#include "anvil_host.h"
 #include "anvil_internal.h"
 #include "anvil_adam.h"
+#include "anvil_linear.h"
 #include "anvil_schedule.h"
 #include "anvil_tail.h"
 
@@ -37,13 +39,21 @@ static_assert(TL_ITEMS == ANVIL_TIMELINE_ITEMS && TL_FIELDS == 16, "timeline lay
 static_assert(sizeof(CascadeParams) <= 32764, "cascade parameters exceed the kernel parameter limit");
 
 namespace {
-
 thread_local char g_last_error[256] = "";
+}  // namespace
+
+namespace anvil {
+
+void set_error_text(const char* text) { snprintf(g_last_error, sizeof(g_last_error), "%s", text); }
 
 anvil_status cuda_fail(cudaError_t e, const char* where) {
     snprintf(g_last_error, sizeof(g_last_error), "%s: %s", where, cudaGetErrorString(e));
     return ANVIL_ERR_CUDA;
 }
+
+}  // namespace anvil
+
+namespace {
 
 // ANVIL_MAPS as printed on the page (the ANVIL section of anvil.py, record #360).
 const anvil_map kAnvilMaps[6] = {
@@ -56,18 +66,13 @@ const anvil_map kAnvilMaps[6] = {
 };
 
 // ---------------------------------------------------------------- per-device set-up
-struct DeviceState {
-    bool ready = false;
-    unsigned* err = nullptr;
-    int sm_count = 0;
-};
 std::mutex g_dev_mutex;
 DeviceState g_dev[64];
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
+
+namespace anvil {
+
 EncodeTiledFn g_encode = nullptr;
 
 // Checks the device is sm_103, sets kernel attributes, finds the error word and the
@@ -99,7 +104,7 @@ anvil_status device_setup(DeviceState** out) {
                                  "cuTensorMapEncodeTiled lookup");
             g_encode = reinterpret_cast<EncodeTiledFn>(fn);
         }
-        if ((e = gemm_prepare())) return cuda_fail(e, "cudaFuncSetAttribute");
+        if ((e = gemm_prepare()) || (e = linear_prepare())) return cuda_fail(e, "cudaFuncSetAttribute");
         if ((e = cudaDeviceGetAttribute(&st.sm_count, cudaDevAttrMultiProcessorCount, dev)))
             return cuda_fail(e, "cudaDeviceGetAttribute");
         st.err = device_error_word();
@@ -110,33 +115,11 @@ anvil_status device_setup(DeviceState** out) {
     return ANVIL_OK;
 }
 
-// ---------------------------------------------------------------- launch profiling
-struct Profiler {
-    std::mutex mu;
-    bool active = false;
-    int cap = 0, used = 0;
-    cudaEvent_t* ev = nullptr;  // 2 * cap events
-    int* kind = nullptr;
-};
 Profiler g_prof;
 
-// Runs `launch`, bracketed by two events on `stream` when profiling is on.  A timed
-// launch holds the profiler's lock throughout, so anvil_profile_end on another thread
-// cannot destroy its events in between.
-template <class F>
-cudaError_t profiled(int kind, cudaStream_t stream, F&& launch) {
-    std::unique_lock<std::mutex> lock(g_prof.mu);
-    if (!g_prof.active || g_prof.used >= g_prof.cap) {
-        lock.unlock();
-        return launch();
-    }
-    const int slot = g_prof.used++;
-    g_prof.kind[slot] = kind;
-    cudaError_t e;
-    if ((e = cudaEventRecord(g_prof.ev[2 * slot], stream))) return e;
-    if ((e = launch())) return e;
-    return cudaEventRecord(g_prof.ev[2 * slot + 1], stream);
-}
+}  // namespace anvil
+
+namespace {
 
 // ---------------------------------------------------------------- geometry and layout
 struct Geom {
@@ -150,8 +133,6 @@ struct Layout {
     size_t part_elems, y_elems, a_elems;
     size_t off_d, off_cnt, off_part, off_y0, off_y1, off_a, off_b, total;
 };
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The cascade kernel's bank order: the call's banks, heaviest tiles first (they open
 // every phase), ties in call order.
@@ -206,11 +187,6 @@ anvil_status make_layout(const anvil_bank_desc* banks, int nbanks, Layout* L) {
     L->total = align256(L->off_b + 2 * L->a_elems);
     return ANVIL_OK;
 }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
 anvil_status check_banks(const anvil_bank_desc* banks, int nbanks) {
     Range rg[ANVIL_MAX_BANKS][4];

@@ -1,0 +1,767 @@
+// anvil_block_api.cu -- the C ABI of the operators around the banks (include/anvil.h):
+// layer norm, the linear layer and token log probabilities.  Argument checks (before any
+// CUDA call), workspace layouts, tensor maps, and the choice of kernel and tile shape from
+// the sizes, types and alignment.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "../../include/anvil.h"
+#include "anvil_host.h"
+#include "anvil_linear.h"
+#include "anvil_logprob.h"
+#include "anvil_norm.h"
+
+using namespace anvil;
+
+static_assert(ANVIL_ACT_SILU == ACT_SILU && ANVIL_ACT_RELU2 == ACT_RELU2, "activation codes of include/anvil.h");
+static_assert(ANVIL_MAX_TOP == LOGPROB_MAX_TOP, "ANVIL_MAX_TOP");
+
+namespace {
+
+int size_of(int dtype) { return dtype == ANVIL_F32 ? 4 : 2; }
+bool valid_dtype(int dtype) { return dtype == ANVIL_F32 || dtype == ANVIL_BF16 || dtype == ANVIL_F16; }
+
+// A row-major array of the call: `rows` rows of `width` bytes, `ld` bytes apart.
+struct Area {
+    uintptr_t p;
+    int64_t rows, ld, width;
+    bool written;
+};
+
+Area area(const void* p, int64_t rows, int64_t cols, int64_t ld, int es, bool written) {
+    return {reinterpret_cast<uintptr_t>(p), rows, rows > 1 ? ld * es : cols * es, cols * es, written};
+}
+
+// Whether two areas share a byte.  Interleaved rows (the same row stride) share none when
+// their columns are disjoint; other areas are taken as the whole range they span.
+bool share(const Area& a, const Area& b) {
+    if (!a.p || !b.p || a.rows < 1 || b.rows < 1) return false;
+    const Range ra = {a.p, a.p + static_cast<uintptr_t>((a.rows - 1) * a.ld + a.width)};
+    const Range rb = {b.p, b.p + static_cast<uintptr_t>((b.rows - 1) * b.ld + b.width)};
+    if (!overlap(ra, rb)) return false;
+    if (a.rows > 1 && b.rows > 1 && a.ld == b.ld) {
+        const int64_t off = b.p >= a.p ? static_cast<int64_t>((b.p - a.p) % static_cast<uintptr_t>(a.ld))
+                                       : (a.ld - static_cast<int64_t>((a.p - b.p) % static_cast<uintptr_t>(a.ld))) % a.ld;
+        return !(off >= a.width && off + b.width <= a.ld);
+    }
+    return true;
+}
+bool same(const Area& a, const Area& b) { return a.p == b.p && a.rows == b.rows && a.ld == b.ld && a.width == b.width; }
+
+// Every written area against every other; `inplace` lists the pairs (written, other) that
+// may be the very same array.
+anvil_status check_areas(const Area* a, int n, const int (*inplace)[2], int npairs) {
+    for (int i = 0; i < n; ++i) {
+        if (!a[i].written) continue;
+        for (int j = 0; j < n; ++j) {
+            if (j == i || (a[j].written && j < i) || !share(a[i], a[j])) continue;
+            bool ok = false;
+            for (int q = 0; q < npairs; ++q)
+                ok = ok || (inplace[q][0] == i && inplace[q][1] == j && same(a[i], a[j]));
+            if (!ok) return ANVIL_ERR_ALIAS;
+        }
+    }
+    return ANVIL_OK;
+}
+
+bool misaligned(const void* p, int es) { return (reinterpret_cast<uintptr_t>(p) & (es - 1)) != 0; }
+bool bad_ld(int64_t rows, int64_t cols, int64_t ld) { return rows > 1 && ld < cols; }
+
+anvil_status check_workspace(const void* ws, size_t bytes, size_t need, const Area* a, int n) {
+    if (need == 0) return ANVIL_OK;
+    if (!ws || bytes < need) return ANVIL_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return ANVIL_ERR_ALIGNMENT;
+    const Area w = {reinterpret_cast<uintptr_t>(ws), 1, static_cast<int64_t>(need), static_cast<int64_t>(need), true};
+    for (int i = 0; i < n; ++i)
+        if (share(w, a[i])) return ANVIL_ERR_ALIAS;
+    return ANVIL_OK;
+}
+
+// ---------------------------------------------------------------- layer norm
+anvil_status check_norm_sizes(int64_t rows, int width, int dtype, int weight_dtype) {
+    if (rows < 0 || width < 1 || !valid_dtype(dtype)) return ANVIL_ERR_INVALID_ARG;
+    if (weight_dtype != ANVIL_F32 && weight_dtype != dtype) return ANVIL_ERR_INVALID_ARG;
+    if (rows > ANVIL_MAX_ROWS || width > ANVIL_MAX_WIDTH) return ANVIL_ERR_UNSUPPORTED_SHAPE;
+    return ANVIL_OK;
+}
+
+// The SM count the backward pass is sized for (one constant, so that the workspace needs
+// no device query and the order of the column sums is the same everywhere).
+constexpr int PLAN_SMS = 152;
+
+size_t norm_bwd_bytes(const anvil_layernorm_grad_desc* d) {
+    if (d->rows == 0 || (!d->dweight && !d->dbias)) return 0;
+    const int blocks = norm_bwd_blocks(d->rows, d->width, d->dtype, PLAN_SMS);
+    return blocks > 1 ? align256(sizeof(float) * 2 * static_cast<size_t>(blocks) * d->width) : 0;
+}
+
+// ---------------------------------------------------------------- the linear layer
+bool aligned16(const void* p, int64_t ld, int es, int64_t rows) {
+    return !(reinterpret_cast<uintptr_t>(p) & 15) && (rows <= 1 || (ld * es) % 16 == 0);
+}
+
+anvil_status check_linear_sizes(int64_t rows, int n, int k, int dtype, int act) {
+    if (rows < 0 || n < 1 || k < 1 || (dtype != ANVIL_BF16 && dtype != ANVIL_F16) || act < 0 || act >= ACT_COUNT)
+        return ANVIL_ERR_INVALID_ARG;
+    if (rows > ANVIL_MAX_ROWS || n > ANVIL_MAX_FEATURES || k > ANVIL_MAX_FEATURES) return ANVIL_ERR_UNSUPPORTED_SHAPE;
+    // 32-bit tile numbers
+    const int64_t t = (rows + 127) / 128;
+    if (t * ((n + 127) / 128) >= (1ll << 30) || t * ((k + 127) / 128) >= (1ll << 30)) return ANVIL_ERR_UNSUPPORTED_SHAPE;
+    return ANVIL_OK;
+}
+
+// A 16-bit matrix operand as it is stored: `rows` rows of `cols` elements.
+struct Stored {
+    const void* p;
+    int64_t rows, ld;
+    int cols;
+};
+
+// Bytes of the 16-byte-aligned copy an operand needs (0: none).
+size_t copy_bytes(const Stored& s) {
+    if (aligned16(s.p, s.ld, 2, s.rows)) return 0;
+    return align256(2 * static_cast<size_t>(s.rows) * ((s.cols + 7) & ~7));
+}
+Stored with_copy(const Stored& s, void* copy) {
+    Stored r = s;
+    r.p = copy;
+    r.ld = (s.cols + 7) & ~7;
+    return r;
+}
+
+anvil_status encode(CUtensorMap* map, int es, bool f16, const void* base, int64_t inner, int64_t outer, int64_t ld,
+                    int64_t planes, int64_t plane_stride, int box0, int box1) {
+    // a row stride is only used where there are several rows; keep it a multiple of 16 bytes
+    const int64_t ldb = outer > 1 ? ld * es : (inner * es + 15) / 16 * 16;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                                static_cast<cuuint64_t>(planes)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldb),
+                                   static_cast<cuuint64_t>(planes > 1 ? plane_stride * es : ldb)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType type = es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : f16   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = g_encode(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        char text[64];
+        snprintf(text, sizeof(text), "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+        set_error_text(text);
+        return ANVIL_ERR_CUDA;
+    }
+    return ANVIL_OK;
+}
+
+// One product C [rows, cols] = A B^T over k, from operands on 16-byte rows: A as stored
+// [rows][k] (or [k][rows] when a_mn), B as [cols][k] (or [k][cols] when b_mn).
+struct Product {
+    Stored a, b;
+    bool a_mn, b_mn;
+    int64_t rows;
+    int cols;
+    int64_t k;
+    bool f16;
+    GemmEpilogue epi;
+    float* part;  // split products' scratch (from plan)
+};
+
+// How a product runs.
+struct Plan {
+    bool few;      // row_gemm_kernel
+    int bn;        // output columns of a pair's tile, or B rows of a block
+    int splits;    // of the contraction
+    int kb;        // k-blocks per split
+    size_t part;   // bytes of split partial products
+};
+
+constexpr int FEW_ROWS = 128;
+
+Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32, bool may_split) {
+    Plan p = {};
+    const int64_t kb = (k + GEMM_BK - 1) / GEMM_BK;
+    if (rows <= FEW_ROWS && !a_mn && !out_f32) {
+        p.few = true;
+        p.bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+        const int64_t tiles = static_cast<int64_t>((cols + ROW_TILE_A - 1) / ROW_TILE_A) * ((rows + p.bn - 1) / p.bn);
+        p.splits = 1;
+        while (p.splits < 8 && tiles * p.splits * 2 <= PLAN_SMS) {
+            const int64_t per = (kb + p.splits * 2 - 1) / (p.splits * 2);
+            if (per * (p.splits * 2 - 1) >= kb) break;  // every split has work
+            p.splits *= 2;
+        }
+        p.kb = static_cast<int>((kb + p.splits - 1) / p.splits);
+        return p;
+    }
+    // The tile width and the number of splits with the least estimated time, in SM cycles:
+    // whole turns of the grid's pairs, each its k-blocks and a fixed cost for filling the
+    // pipeline and the epilogue, and for splits a pass over their partial products.
+    const int64_t pairs = PLAN_SMS / 2;
+    double best = 0;
+    for (int bn = 256; bn >= 128; bn -= 128) {
+        const int64_t tiles = ((rows + PAIR_ROWS - 1) / PAIR_ROWS) * ((cols + bn - 1) / bn);
+        for (int s = 1; s <= (may_split ? 64 : 1); ++s) {
+            const int64_t per = (kb + s - 1) / s;
+            if (s > 1 && (per * (s - 1) >= kb || per < 8 || tiles * s > 4 * pairs)) continue;
+            const double turns = static_cast<double>((tiles * s + pairs - 1) / pairs);
+            double cost = turns * (per * (bn == 256 ? 560.0 : 360.0) + (bn == 256 ? 2500.0 : 1800.0));
+            if (s > 1) cost += 5000.0 + static_cast<double>(rows) * cols * 8.0 * s / 2600.0;
+            if (best == 0 || cost < best) {
+                best = cost;
+                p.bn = bn;
+                p.splits = s;
+                p.kb = static_cast<int>(per);
+            }
+        }
+    }
+    if (p.splits > 1) p.part = align256(4 * static_cast<size_t>(p.splits) * rows * ((cols + 3) & ~3));
+    return p;
+}
+
+anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, cudaStream_t s) {
+    anvil_status st;
+    cudaError_t e;
+    if (plan.few) {
+        RowGemmParams g;
+        memset(&g, 0, sizeof(g));
+        // the output's columns run along B's rows: B is the M side of the MMA
+        if ((st = encode(&g.tm_a, 2, q.f16, q.b.p, q.b.cols, q.b.rows, q.b.ld, 1, 0, 64, q.b_mn ? 64 : ROW_TILE_A))) return st;
+        if ((st = encode(&g.tm_b, 2, q.f16, q.a.p, q.a.cols, q.a.rows, q.a.ld, 1, 0, 64, plan.bn))) return st;
+        g.epi = q.epi;
+        g.na = q.cols;
+        g.nb = static_cast<int>(q.rows);
+        g.k = static_cast<int>(q.k);
+        g.a_mn = q.b_mn;
+        g.f16 = q.f16;
+        g.splits = plan.splits;
+        g.kb_per_split = plan.kb;
+        g.err = dev->err;
+        e = profiled(ANVIL_KERNEL_LINEAR_PRODUCT, s, [&] { return launch_row_gemm(g, plan.bn, s); });
+        return e ? cuda_fail(e, "linear product launch") : ANVIL_OK;
+    }
+    PairGemmParams g;
+    memset(&g, 0, sizeof(g));
+    if ((st = encode(&g.tm_a, 2, q.f16, q.a.p, q.a.cols, q.a.rows, q.a.ld, 1, 0, 64, q.a_mn ? 64 : 128))) return st;
+    if ((st = encode(&g.tm_b, 2, q.f16, q.b.p, q.b.cols, q.b.rows, q.b.ld, 1, 0, 64, q.b_mn ? 64 : plan.bn / 2))) return st;
+    g.epi = q.epi;
+    g.rows = static_cast<int>(q.rows);
+    g.cols = q.cols;
+    g.k = static_cast<int>(q.k);
+    g.a_mn = q.a_mn;
+    g.b_mn = q.b_mn;
+    g.f16 = q.f16;
+    g.tiles_r = static_cast<int>((q.rows + PAIR_ROWS - 1) / PAIR_ROWS);
+    g.tiles_c = (q.cols + plan.bn - 1) / plan.bn;
+    g.splits = plan.splits;
+    g.kb_per_split = plan.kb;
+    g.err = dev->err;
+    const GemmEpilogue& ep = q.epi;
+    const int es = ep.out_f32 ? 4 : 2;
+    const int64_t ldp = (q.cols + 3) & ~3;
+    if (plan.splits > 1) {
+        // fp32 partial products; the epilogue moves to split_sum_kernel
+        memset(&g.epi, 0, sizeof(g.epi));
+        g.epi.out_f32 = 1;
+        if ((st = encode(&g.tm_out, 4, false, q.part, q.cols, q.rows, ldp, plan.splits, ldp * q.rows, 32, 128))) return st;
+    } else {
+        g.out_tma = aligned16(ep.out, ep.ldout, es, q.rows);
+        g.in_tma = ep.in && aligned16(ep.in, ep.ldin, es, q.rows);
+        g.z_tma = ep.z && aligned16(ep.z, ep.ldz, es, q.rows);
+        const int box = 128 / es;
+        if (g.out_tma && (st = encode(&g.tm_out, es, q.f16, ep.out, q.cols, q.rows, ep.ldout, 1, 0, box, 128))) return st;
+        if (g.in_tma && (st = encode(&g.tm_in, es, q.f16, ep.in, q.cols, q.rows, ep.ldin, 1, 0, box, 128))) return st;
+        if (g.z_tma && (st = encode(&g.tm_z, es, q.f16, ep.z, q.cols, q.rows, ep.ldz, 1, 0, box, 128))) return st;
+    }
+    e = profiled(ANVIL_KERNEL_LINEAR_PRODUCT, s, [&] { return launch_pair_gemm(g, plan.bn, dev->sm_count, s); });
+    if (e) return cuda_fail(e, "linear product launch");
+    if (plan.splits > 1) {
+        SplitSumParams t;
+        memset(&t, 0, sizeof(t));
+        t.part = q.part;
+        t.in = ep.in;
+        t.out = ep.out;
+        t.ld_part = ldp;
+        t.ldin = ep.ldin;
+        t.ldout = ep.ldout;
+        t.rows = static_cast<int>(q.rows);
+        t.cols = q.cols;
+        t.splits = plan.splits;
+        t.out_f32 = ep.out_f32;
+        t.f16 = q.f16;
+        e = profiled(ANVIL_KERNEL_LINEAR_SUM, s, [&] { return launch_split_sum(t, s); });
+        if (e) return cuda_fail(e, "split sum launch");
+    }
+    return ANVIL_OK;
+}
+
+anvil_status copy_operand(Stored* s, void* copy, cudaStream_t stream) {
+    RepackParams r;
+    r.src = static_cast<const uint16_t*>(s->p);
+    r.dst = static_cast<uint16_t*>(copy);
+    r.rows = s->rows;
+    r.lds = s->ld;
+    r.cols = s->cols;
+    *s = with_copy(*s, copy);
+    r.ldd = s->ld;
+    const cudaError_t e = profiled(ANVIL_KERNEL_LINEAR_PREPARE, stream, [&] { return launch_repack(r, stream); });
+    return e ? cuda_fail(e, "operand copy launch") : ANVIL_OK;
+}
+
+Stored stored_weight(const void* w, int n, int k, int64_t ldw, bool transposed) {
+    return transposed ? Stored{w, k, ldw, n} : Stored{w, n, ldw, k};
+}
+
+struct LinearLayout {
+    Stored x, w;
+    size_t off_x, off_w, total;
+};
+LinearLayout linear_layout(const anvil_linear_desc* d) {
+    LinearLayout L;
+    L.x = {d->x, d->rows, d->ldx, d->k};
+    L.w = stored_weight(d->weight, d->n, d->k, d->ldw, d->weight_transposed != 0);
+    L.off_x = 0;
+    L.off_w = L.off_x + copy_bytes(L.x);
+    L.total = L.off_w + copy_bytes(L.w);
+    return L;
+}
+
+anvil_status check_linear(const anvil_linear_desc* d) {
+    if (!d) return ANVIL_ERR_INVALID_ARG;
+    anvil_status st = check_linear_sizes(d->rows, d->n, d->k, d->dtype, d->activation);
+    if (st != ANVIL_OK) return st;
+    if (d->bias && d->bias_dtype != ANVIL_F32 && d->bias_dtype != d->dtype) return ANVIL_ERR_INVALID_ARG;
+    if (d->rows == 0) return ANVIL_OK;
+    if (!d->x || !d->weight || !d->y) return ANVIL_ERR_INVALID_ARG;
+    const bool tr = d->weight_transposed != 0;
+    if (bad_ld(d->rows, d->k, d->ldx) || bad_ld(tr ? d->k : d->n, tr ? d->n : d->k, d->ldw) || bad_ld(d->rows, d->n, d->ldy) ||
+        (d->residual && bad_ld(d->rows, d->n, d->ldr)) || (d->preact && bad_ld(d->rows, d->n, d->ldz)))
+        return ANVIL_ERR_INVALID_ARG;
+    if (misaligned(d->x, 2) || misaligned(d->weight, 2) || misaligned(d->y, 2) || misaligned(d->residual, 2) ||
+        misaligned(d->preact, 2) || (d->bias && misaligned(d->bias, size_of(d->bias_dtype))))
+        return ANVIL_ERR_ALIGNMENT;
+    return ANVIL_OK;
+}
+
+struct LinearGradLayout {
+    Stored dz, x, w;
+    bool prep;        // act_grad_kernel runs
+    bool dz_made;     // and writes dz
+    Plan pdx, pdw;
+    int rows_per_block, blocks_r;
+    size_t off_dz, off_x, off_w, off_sum, off_part, total;
+};
+
+LinearGradLayout linear_grad_layout(const anvil_linear_grad_desc* d) {
+    LinearGradLayout L;
+    memset(&L, 0, sizeof(L));
+    const bool tr = d->weight_transposed != 0;
+    L.dz = {d->dy, d->rows, d->lddy, d->n};
+    L.x = {d->x, d->rows, d->ldx, d->k};
+    L.w = stored_weight(d->weight, d->n, d->k, d->ldw, tr);
+    const bool products = d->dx || d->dweight;
+    L.dz_made = products && (d->activation != ANVIL_ACT_NONE || copy_bytes(L.dz) != 0);
+    L.prep = L.dz_made || d->dbias;
+    size_t at = 0;
+    L.off_dz = at;
+    if (L.dz_made) at += align256(2 * static_cast<size_t>(d->rows) * ((d->n + 7) & ~7));
+    L.off_x = at;
+    if (d->dweight) at += copy_bytes(L.x);
+    L.off_w = at;
+    if (d->dx) at += copy_bytes(L.w);
+    L.off_sum = at;
+    if (L.prep) {
+        // about four blocks per SM over the whole array, at least 32 rows each
+        const int64_t cb = (d->n + ACT_GRAD_COLS - 1) / ACT_GRAD_COLS;
+        int64_t br = (4 * PLAN_SMS + cb - 1) / cb;
+        const int64_t most = (d->rows + 31) / 32;
+        if (br > most) br = most;
+        L.rows_per_block = static_cast<int>((d->rows + br - 1) / br);
+        L.blocks_r = static_cast<int>((d->rows + L.rows_per_block - 1) / L.rows_per_block);
+        if (d->dbias) at += align256(sizeof(float) * static_cast<size_t>(L.blocks_r) * d->n);
+    }
+    L.off_part = at;
+    if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, false, false, false);
+    if (d->dweight) {
+        L.pdw = plan_product(tr ? d->k : d->n, tr ? d->n : d->k, d->rows, true, d->dweight_dtype == ANVIL_F32, true);
+        at += L.pdw.part;
+    }
+    L.total = at;
+    return L;
+}
+
+anvil_status check_linear_grad(const anvil_linear_grad_desc* d) {
+    if (!d) return ANVIL_ERR_INVALID_ARG;
+    anvil_status st = check_linear_sizes(d->rows, d->n, d->k, d->dtype, d->activation);
+    if (st != ANVIL_OK) return st;
+    if (d->dweight && d->dweight_dtype != ANVIL_F32 && d->dweight_dtype != d->dtype) return ANVIL_ERR_INVALID_ARG;
+    const bool tr = d->weight_transposed != 0;
+    if (d->dweight && bad_ld(tr ? d->k : d->n, tr ? d->n : d->k, d->lddw)) return ANVIL_ERR_INVALID_ARG;
+    if ((d->dweight && misaligned(d->dweight, size_of(d->dweight_dtype))) || misaligned(d->dbias, 4))
+        return ANVIL_ERR_ALIGNMENT;
+    if (d->rows == 0) return ANVIL_OK;
+    if (!d->dx && !d->dweight && !d->dbias) return ANVIL_OK;
+    const bool act = d->activation != ANVIL_ACT_NONE;
+    if (!d->dy || (d->dweight && !d->x) || (d->dx && !d->weight) || (act && !d->preact)) return ANVIL_ERR_INVALID_ARG;
+    if (bad_ld(d->rows, d->n, d->lddy) || (d->dweight && bad_ld(d->rows, d->k, d->ldx)) ||
+        (d->dx && (bad_ld(tr ? d->k : d->n, tr ? d->n : d->k, d->ldw) || bad_ld(d->rows, d->k, d->lddx))) ||
+        (act && bad_ld(d->rows, d->n, d->ldz)))
+        return ANVIL_ERR_INVALID_ARG;
+    if (misaligned(d->dy, 2) || misaligned(d->x, 2) || misaligned(d->weight, 2) || misaligned(d->preact, 2) ||
+        misaligned(d->dx, 2))
+        return ANVIL_ERR_ALIGNMENT;
+    return ANVIL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+anvil_status anvil_layernorm_forward(const anvil_layernorm_desc* d, void* stream) {
+    if (!d) return ANVIL_ERR_INVALID_ARG;
+    anvil_status st = check_norm_sizes(d->rows, d->width, d->dtype, d->weight_dtype);
+    if (st != ANVIL_OK) return st;
+    if (d->rows == 0) return ANVIL_OK;
+    if (!d->x || !d->y || bad_ld(d->rows, d->width, d->ldx) || bad_ld(d->rows, d->width, d->ldy)) return ANVIL_ERR_INVALID_ARG;
+    const int es = size_of(d->dtype), ws = size_of(d->weight_dtype);
+    if (misaligned(d->x, es) || misaligned(d->y, es) || misaligned(d->weight, ws) || misaligned(d->bias, ws) ||
+        misaligned(d->mean, 4) || misaligned(d->rstd, 4))
+        return ANVIL_ERR_ALIGNMENT;
+    const Area a[6] = {area(d->x, d->rows, d->width, d->ldx, es, false), area(d->weight, 1, d->width, 0, ws, false),
+                       area(d->bias, 1, d->width, 0, ws, false),         area(d->y, d->rows, d->width, d->ldy, es, true),
+                       area(d->mean, 1, d->rows, 0, 4, true),            area(d->rstd, 1, d->rows, 0, 4, true)};
+    const int inplace[1][2] = {{3, 0}};
+    if ((st = check_areas(a, 6, inplace, 1)) != ANVIL_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+    NormFwdParams p;
+    p.x = d->x;
+    p.weight = d->weight;
+    p.bias = d->bias;
+    p.y = d->y;
+    p.mean = d->mean;
+    p.rstd = d->rstd;
+    p.rows = d->rows;
+    p.ldx = d->ldx;
+    p.ldy = d->ldy;
+    p.width = d->width;
+    p.dtype = d->dtype;
+    p.weight_dtype = d->weight_dtype;
+    p.eps = d->eps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = profiled(ANVIL_KERNEL_NORM_FORWARD, s, [&] { return launch_norm_fwd(p, s); });
+    return e ? cuda_fail(e, "layer norm launch") : ANVIL_OK;
+}
+
+size_t anvil_layernorm_backward_workspace_bytes(const anvil_layernorm_grad_desc* d) {
+    if (!d || check_norm_sizes(d->rows, d->width, d->dtype, d->weight_dtype) != ANVIL_OK) return 0;
+    return norm_bwd_bytes(d);
+}
+
+anvil_status anvil_layernorm_backward(const anvil_layernorm_grad_desc* d, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+    if (!d) return ANVIL_ERR_INVALID_ARG;
+    anvil_status st = check_norm_sizes(d->rows, d->width, d->dtype, d->weight_dtype);
+    if (st != ANVIL_OK) return st;
+    if (!d->dx && !d->dweight && !d->dbias) return ANVIL_OK;
+    if (misaligned(d->dweight, 4) || misaligned(d->dbias, 4)) return ANVIL_ERR_ALIGNMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    DeviceState* dev = nullptr;
+    if (d->rows == 0) {
+        if (!d->dweight && !d->dbias) return ANVIL_OK;
+        if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+        if ((d->dweight && (e = cudaMemsetAsync(d->dweight, 0, sizeof(float) * d->width, s))) ||
+            (d->dbias && (e = cudaMemsetAsync(d->dbias, 0, sizeof(float) * d->width, s))))
+            return cuda_fail(e, "cudaMemsetAsync");
+        return ANVIL_OK;
+    }
+    if (!d->dy || !d->x || !d->mean || !d->rstd || bad_ld(d->rows, d->width, d->lddy) || bad_ld(d->rows, d->width, d->ldx) ||
+        (d->dx && bad_ld(d->rows, d->width, d->lddx)) || (d->residual_grad && bad_ld(d->rows, d->width, d->ldr)))
+        return ANVIL_ERR_INVALID_ARG;
+    const int es = size_of(d->dtype), ws = size_of(d->weight_dtype);
+    if (misaligned(d->dy, es) || misaligned(d->x, es) || misaligned(d->dx, es) || misaligned(d->residual_grad, es) ||
+        misaligned(d->weight, ws) || misaligned(d->mean, 4) || misaligned(d->rstd, 4))
+        return ANVIL_ERR_ALIGNMENT;
+    const Area a[9] = {area(d->dy, d->rows, d->width, d->lddy, es, false),
+                       area(d->x, d->rows, d->width, d->ldx, es, false),
+                       area(d->mean, 1, d->rows, 0, 4, false),
+                       area(d->rstd, 1, d->rows, 0, 4, false),
+                       area(d->weight, 1, d->width, 0, ws, false),
+                       area(d->residual_grad, d->rows, d->width, d->ldr, es, false),
+                       area(d->dx, d->rows, d->width, d->lddx, es, true),
+                       area(d->dweight, 1, d->width, 0, 4, true),
+                       area(d->dbias, 1, d->width, 0, 4, true)};
+    const int inplace[3][2] = {{6, 0}, {6, 1}, {6, 5}};
+    if ((st = check_areas(a, 9, inplace, 3)) != ANVIL_OK) return st;
+    const size_t need = norm_bwd_bytes(d);
+    if ((st = check_workspace(workspace, workspace_bytes, need, a, 9)) != ANVIL_OK) return st;
+    if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+    NormBwdParams p;
+    p.dy = d->dy;
+    p.x = d->x;
+    p.mean = d->mean;
+    p.rstd = d->rstd;
+    p.weight = d->weight;
+    p.res = d->dx ? d->residual_grad : nullptr;
+    p.dx = d->dx;
+    p.dweight = d->dweight;
+    p.dbias = d->dbias;
+    p.part = static_cast<float*>(workspace);
+    p.rows = d->rows;
+    p.lddy = d->lddy;
+    p.ldx = d->ldx;
+    p.ldr = d->ldr;
+    p.lddx = d->lddx;
+    p.width = d->width;
+    p.dtype = d->dtype;
+    p.weight_dtype = d->weight_dtype;
+    p.blocks = norm_bwd_blocks(d->rows, d->width, d->dtype, PLAN_SMS);
+    if ((e = profiled(ANVIL_KERNEL_NORM_BACKWARD, s, [&] { return launch_norm_bwd(p, s); })))
+        return cuda_fail(e, "layer norm gradient launch");
+    if (p.blocks > 1 && (p.dweight || p.dbias) &&
+        (e = profiled(ANVIL_KERNEL_NORM_GRADS, s, [&] { return launch_norm_grads(p, s); })))
+        return cuda_fail(e, "layer norm gradient launch");
+    return ANVIL_OK;
+}
+
+size_t anvil_linear_workspace_bytes(const anvil_linear_desc* d) {
+    if (check_linear(d) != ANVIL_OK || d->rows == 0) return 0;
+    return linear_layout(d).total;
+}
+
+anvil_status anvil_linear_forward(const anvil_linear_desc* d, void* workspace, size_t workspace_bytes, void* stream) {
+    anvil_status st = check_linear(d);
+    if (st != ANVIL_OK || d->rows == 0) return st;
+    const bool tr = d->weight_transposed != 0;
+    const int bs = d->bias ? size_of(d->bias_dtype) : 2;
+    const Area a[6] = {area(d->x, d->rows, d->k, d->ldx, 2, false),
+                       area(d->weight, tr ? d->k : d->n, tr ? d->n : d->k, d->ldw, 2, false),
+                       area(d->bias, 1, d->n, 0, bs, false),
+                       area(d->residual, d->rows, d->n, d->ldr, 2, false),
+                       area(d->y, d->rows, d->n, d->ldy, 2, true),
+                       area(d->preact, d->rows, d->n, d->ldz, 2, true)};
+    const int inplace[1][2] = {{4, 3}};
+    if ((st = check_areas(a, 6, inplace, 1)) != ANVIL_OK) return st;
+    LinearLayout L = linear_layout(d);
+    if ((st = check_workspace(workspace, workspace_bytes, L.total, a, 6)) != ANVIL_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (copy_bytes(L.x) && (st = copy_operand(&L.x, ws + L.off_x, s)) != ANVIL_OK) return st;
+    if (copy_bytes(L.w) && (st = copy_operand(&L.w, ws + L.off_w, s)) != ANVIL_OK) return st;
+    Product q;
+    memset(&q, 0, sizeof(q));
+    q.a = L.x;
+    q.b = L.w;
+    q.b_mn = tr;
+    q.rows = d->rows;
+    q.cols = d->n;
+    q.k = d->k;
+    q.f16 = d->dtype == ANVIL_F16;
+    q.epi.bias = d->bias;
+    q.epi.bias_f32 = d->bias && d->bias_dtype == ANVIL_F32;
+    q.epi.act = d->activation;
+    q.epi.in = d->residual;
+    q.epi.ldin = d->ldr;
+    q.epi.z = d->preact;
+    q.epi.ldz = d->ldz;
+    q.epi.out = d->y;
+    q.epi.ldout = d->ldy;
+    return run_product(q, plan_product(d->rows, d->n, d->k, false, false, false), dev, s);
+}
+
+size_t anvil_linear_backward_workspace_bytes(const anvil_linear_grad_desc* d) {
+    if (check_linear_grad(d) != ANVIL_OK || d->rows == 0) return 0;
+    return linear_grad_layout(d).total;
+}
+
+anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* workspace, size_t workspace_bytes, void* stream) {
+    anvil_status st = check_linear_grad(d);
+    if (st != ANVIL_OK) return st;
+    if (!d->dx && !d->dweight && !d->dbias) return ANVIL_OK;
+    const bool tr = d->weight_transposed != 0;
+    const int dws = size_of(d->dweight_dtype);
+    const int64_t wr = tr ? d->k : d->n, wc = tr ? d->n : d->k;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    DeviceState* dev = nullptr;
+    if (d->rows == 0) {
+        if (d->accumulate || (!d->dweight && !d->dbias)) return ANVIL_OK;
+        if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+        if ((d->dweight && (e = cudaMemset2DAsync(d->dweight, (wr > 1 ? d->lddw : wc) * dws, 0, wc * dws, wr, s))) ||
+            (d->dbias && (e = cudaMemsetAsync(d->dbias, 0, sizeof(float) * d->n, s))))
+            return cuda_fail(e, "cudaMemsetAsync");
+        return ANVIL_OK;
+    }
+    const bool act = d->activation != ANVIL_ACT_NONE;
+    const Area a[7] = {area(d->dy, d->rows, d->n, d->lddy, 2, false),
+                       area(d->dweight ? d->x : nullptr, d->rows, d->k, d->ldx, 2, false),
+                       area(d->dx ? d->weight : nullptr, wr, wc, d->ldw, 2, false),
+                       area(act ? d->preact : nullptr, d->rows, d->n, d->ldz, 2, false),
+                       area(d->dx, d->rows, d->k, d->lddx, 2, true),
+                       area(d->dweight, wr, wc, d->lddw, dws, true),
+                       area(d->dbias, 1, d->n, 0, 4, true)};
+    if ((st = check_areas(a, 7, nullptr, 0)) != ANVIL_OK) return st;
+    LinearGradLayout L = linear_grad_layout(d);
+    if ((st = check_workspace(workspace, workspace_bytes, L.total, a, 7)) != ANVIL_OK) return st;
+    if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const bool f16 = d->dtype == ANVIL_F16;
+    if (L.prep) {
+        ActGradParams p;
+        memset(&p, 0, sizeof(p));
+        p.dy = d->dy;
+        p.z = act ? d->preact : nullptr;
+        p.dz = L.dz_made ? ws + L.off_dz : nullptr;
+        p.part = d->dbias ? reinterpret_cast<float*>(ws + L.off_sum) : nullptr;
+        p.rows = d->rows;
+        p.lddy = d->lddy;
+        p.ldz = d->ldz;
+        p.cols = d->n;
+        p.act = d->activation;
+        p.f16 = f16;
+        p.rows_per_block = L.rows_per_block;
+        p.blocks_r = L.blocks_r;
+        if (L.dz_made) {
+            L.dz = with_copy(L.dz, ws + L.off_dz);
+            p.ldd = L.dz.ld;
+        }
+        if ((e = profiled(ANVIL_KERNEL_LINEAR_PREPARE, s, [&] { return launch_act_grad(p, s); })))
+            return cuda_fail(e, "activation gradient launch");
+        if (d->dbias && (e = profiled(ANVIL_KERNEL_LINEAR_SUM, s, [&] {
+                             return launch_column_sum(p.part, p.blocks_r, d->n, d->dbias, d->accumulate, s);
+                         })))
+            return cuda_fail(e, "bias gradient launch");
+    }
+    if (d->dx) {
+        if (copy_bytes(L.w) && (st = copy_operand(&L.w, ws + L.off_w, s)) != ANVIL_OK) return st;
+        Product q;
+        memset(&q, 0, sizeof(q));
+        q.a = L.dz;
+        q.b = L.w;
+        q.b_mn = !tr;
+        q.rows = d->rows;
+        q.cols = d->k;
+        q.k = d->n;
+        q.f16 = f16;
+        q.epi.out = d->dx;
+        q.epi.ldout = d->lddx;
+        if ((st = run_product(q, L.pdx, dev, s)) != ANVIL_OK) return st;
+    }
+    if (d->dweight) {
+        if (copy_bytes(L.x) && (st = copy_operand(&L.x, ws + L.off_x, s)) != ANVIL_OK) return st;
+        Product q;
+        memset(&q, 0, sizeof(q));
+        q.a = tr ? L.x : L.dz;
+        q.b = tr ? L.dz : L.x;
+        q.a_mn = q.b_mn = true;
+        q.rows = wr;
+        q.cols = static_cast<int>(wc);
+        q.k = d->rows;
+        q.f16 = f16;
+        q.epi.out = d->dweight;
+        q.epi.ldout = d->lddw;
+        q.epi.out_f32 = d->dweight_dtype == ANVIL_F32;
+        if (d->accumulate) {
+            q.epi.in = d->dweight;
+            q.epi.ldin = d->lddw;
+        }
+        q.part = reinterpret_cast<float*>(ws + L.off_part);
+        if ((st = run_product(q, L.pdw, dev, s)) != ANVIL_OK) return st;
+    }
+    return ANVIL_OK;
+}
+
+anvil_status anvil_token_logprobs(const anvil_logprob_desc* d, void* stream) {
+    if (!d || d->rows < 0 || d->vocab < 1 || !valid_dtype(d->dtype) || d->top < 0 || d->top > ANVIL_MAX_TOP ||
+        d->top > d->vocab)
+        return ANVIL_ERR_INVALID_ARG;
+    if (d->rows > ANVIL_MAX_ROWS || d->vocab > ANVIL_MAX_VOCAB) return ANVIL_ERR_UNSUPPORTED_SHAPE;
+    if (d->rows == 0) return ANVIL_OK;
+    if (!d->logits || bad_ld(d->rows, d->vocab, d->ld) || (d->logprob && !d->targets) ||
+        (d->top && (!d->top_logprob || !d->top_index)))
+        return ANVIL_ERR_INVALID_ARG;
+    const int es = size_of(d->dtype), ts = d->targets_int64 ? 8 : 4;
+    if (misaligned(d->logits, es) || misaligned(d->targets, ts) || misaligned(d->logprob, 4) || misaligned(d->entropy, 4) ||
+        misaligned(d->lse, 4) || misaligned(d->top_logprob, 4) || misaligned(d->top_index, 4))
+        return ANVIL_ERR_ALIGNMENT;
+    const int64_t nt = d->rows * d->top;
+    const Area a[7] = {area(d->logits, d->rows, d->vocab, d->ld, es, false),
+                       area(d->targets, 1, d->rows, 0, ts, false),
+                       area(d->logprob, 1, d->rows, 0, 4, true),
+                       area(d->entropy, 1, d->rows, 0, 4, true),
+                       area(d->lse, 1, d->rows, 0, 4, true),
+                       area(d->top ? d->top_logprob : nullptr, 1, nt, 0, 4, true),
+                       area(d->top ? d->top_index : nullptr, 1, nt, 0, 4, true)};
+    anvil_status st;
+    if ((st = check_areas(a, 7, nullptr, 0)) != ANVIL_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+    LogprobParams p;
+    p.logits = d->logits;
+    p.targets = d->targets;
+    p.logprob = d->logprob;
+    p.entropy = d->entropy;
+    p.lse = d->lse;
+    p.top_logprob = d->top_logprob;
+    p.top_index = d->top_index;
+    p.rows = d->rows;
+    p.ld = d->ld;
+    p.vocab = d->vocab;
+    p.top = d->top;
+    p.dtype = d->dtype;
+    p.target64 = d->targets_int64 != 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = profiled(ANVIL_KERNEL_LOGPROB, s, [&] { return launch_logprob_fwd(p, dev->sm_count, s); });
+    return e ? cuda_fail(e, "token log-probability launch") : ANVIL_OK;
+}
+
+anvil_status anvil_token_logprobs_backward(const anvil_logprob_grad_desc* d, void* stream) {
+    if (!d || d->rows < 0 || d->vocab < 1 || !valid_dtype(d->dtype)) return ANVIL_ERR_INVALID_ARG;
+    if (d->rows > ANVIL_MAX_ROWS || d->vocab > ANVIL_MAX_VOCAB || d->rows * logprob_bwd_segments(d->vocab, d->dtype) > INT32_MAX)
+        return ANVIL_ERR_UNSUPPORTED_SHAPE;
+    if (d->rows == 0) return ANVIL_OK;
+    if (!d->logits || !d->dlogits || !d->lse || (d->grad_logprob && !d->targets) || (d->grad_entropy && !d->entropy) ||
+        bad_ld(d->rows, d->vocab, d->ld) || bad_ld(d->rows, d->vocab, d->ldd))
+        return ANVIL_ERR_INVALID_ARG;
+    const int es = size_of(d->dtype), ts = d->targets_int64 ? 8 : 4;
+    if (misaligned(d->logits, es) || misaligned(d->dlogits, es) || misaligned(d->targets, ts) || misaligned(d->lse, 4) ||
+        misaligned(d->entropy, 4) || misaligned(d->grad_logprob, 4) || misaligned(d->grad_entropy, 4))
+        return ANVIL_ERR_ALIGNMENT;
+    const Area a[7] = {area(d->logits, d->rows, d->vocab, d->ld, es, false),
+                       area(d->targets, 1, d->rows, 0, ts, false),
+                       area(d->lse, 1, d->rows, 0, 4, false),
+                       area(d->entropy, 1, d->rows, 0, 4, false),
+                       area(d->grad_logprob, 1, d->rows, 0, 4, false),
+                       area(d->grad_entropy, 1, d->rows, 0, 4, false),
+                       area(d->dlogits, d->rows, d->vocab, d->ldd, es, true)};
+    const int inplace[1][2] = {{6, 0}};
+    anvil_status st;
+    if ((st = check_areas(a, 7, inplace, 1)) != ANVIL_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+    LogprobGradParams p;
+    p.logits = d->logits;
+    p.targets = d->targets;
+    p.lse = d->lse;
+    p.entropy = d->entropy;
+    p.grad_logprob = d->grad_logprob;
+    p.grad_entropy = d->grad_entropy;
+    p.dlogits = d->dlogits;
+    p.rows = d->rows;
+    p.ld = d->ld;
+    p.ldd = d->ldd;
+    p.vocab = d->vocab;
+    p.dtype = d->dtype;
+    p.target64 = d->targets_int64 != 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = profiled(ANVIL_KERNEL_LOGPROB_BACKWARD, s, [&] { return launch_logprob_bwd(p, s); });
+    return e ? cuda_fail(e, "token log-probability gradient launch") : ANVIL_OK;
+}
+
+}  // extern "C"

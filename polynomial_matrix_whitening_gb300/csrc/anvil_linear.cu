@@ -1,0 +1,989 @@
+// anvil_linear.cu -- the linear layer's products for sm_103a: C = A B^T with 16-bit
+// operands and fp32 accumulation on the 5th-generation tensor cores, and what follows the
+// accumulator fused into the epilogue.
+//
+//   forward        z = x W^T + b,  y = act(z) + r
+//   input's grad   dx = dz W
+//   weight's grad  dW = dz^T x  (16 bit, or fp32, optionally added to what is there)
+//
+// Two kernels share the work.
+//
+// pair_gemm_kernel: clusters of two CTAs compute 256 x BN output tiles (BN = 256 or 128)
+// with tcgen05.mma.cta_group::2; CTA rank r loads rows 128r.. of the tile's A operand and
+// columns BN/2 r.. of its B operand by TMA into a ring of stages, and holds output rows
+// 128r.. in its TMEM.  Two accumulators alternate, so a tile's epilogue overlaps the next
+// tile's products.  Operands are taken in the order they are stored: K-major, or MN-major
+// as 64 x 64 boxes, so no operand is ever transposed in memory.  The grid is persistent
+// (one pair per two SMs), its tiles in groups of eight rows of tiles for the L2.
+// fp32 results: the tensor cores add with truncation, a bias that grows with the length
+// of the chain (about 1e-9 of the result per 16-deep step), so the product is taken in
+// chains of 512 and the epilogue adds the chains up in registers, rounding to nearest.
+//
+// row_gemm_kernel: few rows (tokens).  The weight's 128-row blocks are the MMA's M side and
+// the tokens its N side (16 to 128), so a weight is read once, and a cluster of up to eight
+// CTAs splits the contraction, so that enough SMs read it; the partial accumulators are
+// joined through distributed shared memory in rank order.
+//
+// Every wait is bounded (anvil_device.cuh): one that gives up sets the device error word
+// and an abort flag; loads in flight are waited for (bounded), the TMEM is freed and the
+// CTA returns.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "anvil_device.cuh"
+#include "anvil_linear.h"
+#include "anvil_types.cuh"
+
+namespace anvil {
+
+namespace {
+
+constexpr int CTA_ROWS = 128;
+constexpr int QBOX = 16384;             // one staging box: 128 rows of 128 bytes
+constexpr int A_STAGE = CTA_ROWS * 128; // 16 KB: this CTA's A rows of a k-block
+constexpr int EPI_GROUPS = 2;           // epilogue warp groups, one per half of the columns
+constexpr int EPI_WARP0 = 4;            // warps 4-11; warp 0: TMA producer, warp 1: MMA issuer and TMEM owner
+constexpr int PAIR_THREADS = 32 * (EPI_WARP0 + 4 * EPI_GROUPS);
+constexpr int CHAIN_KB = 8;             // k-blocks of one chain of an fp32 result (512 deep)
+constexpr int RASTER_ROWS = 8;          // rows of tiles per raster group
+
+// kind::f16 instruction descriptor with fp32 accumulation; the operands' type is both
+// bf16 (1) or both fp16 (0).
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool a_mn, bool b_mn, bool f16) {
+    const uint32_t fmt = f16 ? 0u : 1u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+__device__ __forceinline__ float act_value(int act, float z) {
+    switch (act) {
+        case ACT_RELU: return z < 0.f ? 0.f : z;
+        case ACT_RELU2: return z < 0.f ? 0.f : z * z;
+        case ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+        case ACT_GELU_TANH: {
+            const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);  // 2 sqrt(2/pi) (...)
+            return __fdividef(z, 1.f + __expf(-u2));                              // z (1 + tanh(u2 / 2)) / 2
+        }
+        case ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
+        default: return z;
+    }
+}
+__device__ __forceinline__ float act_slope(int act, float z) {
+    switch (act) {
+        case ACT_RELU: return z > 0.f ? 1.f : 0.f;
+        case ACT_RELU2: return z < 0.f ? 0.f : 2.f * z;
+        case ACT_GELU:
+            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+        case ACT_GELU_TANH: {
+            const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
+            const float du2 = 1.5957691216057308f * (1.f + 0.134145f * z * z);
+            const float s = 1.f / (1.f + __expf(-u2));
+            return s + z * s * (1.f - s) * du2;
+        }
+        case ACT_SILU: {
+            const float s = 1.f / (1.f + __expf(-z));
+            return s * (1.f + z * (1.f - s));
+        }
+        default: return 1.f;
+    }
+}
+// The activation of N values, the choice made once.
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
+    switch (act) {
+        case ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_RELU, v[i]);
+            break;
+        case ACT_RELU2:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_RELU2, v[i]);
+            break;
+        case ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_GELU, v[i]);
+            break;
+        case ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_GELU_TANH, v[i]);
+            break;
+        case ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_SILU, v[i]);
+            break;
+        default: break;
+    }
+}
+
+// ---------------------------------------------------------------- the pair kernel
+template <int BN>
+struct PairShape {
+    static constexpr int B_STAGE = BN / 2 * 128;
+    static constexpr int STAGE = A_STAGE + B_STAGE;
+    static constexpr int STAGES = BN == 256 ? 5 : 6;
+    static constexpr int BOXES = 2 * EPI_GROUPS;
+    static constexpr int SMEM = STAGES * STAGE + BOXES * QBOX + 1024;  // + alignment slack
+    static constexpr uint32_t TMEM_COLS = 2 * BN;
+};
+
+// Work unit u -> tile row, tile column, split.  Groups of RASTER_ROWS rows of tiles, column
+// by column inside a group, so that the pairs running at one time share operand panels.
+struct Unit {
+    int tr, tc, split;
+};
+__device__ __forceinline__ Unit unit_of(const PairGemmParams& p, int u) {
+    const int tiles = p.tiles_r * p.tiles_c;
+    Unit r;
+    r.split = u / tiles;
+    const int t = u - r.split * tiles;
+    const int per = RASTER_ROWS * p.tiles_c;
+    const int g = t / per;
+    const int rows = min(RASTER_ROWS, p.tiles_r - g * RASTER_ROWS);
+    const int q = t - g * per;
+    r.tc = q / rows;
+    r.tr = g * RASTER_ROWS + (q - r.tc * rows);
+    return r;
+}
+__device__ __forceinline__ void unit_kblocks(const PairGemmParams& p, const Unit& u, int* kb0, int* nkb) {
+    const int all = (p.k + GEMM_BK - 1) / GEMM_BK;
+    *kb0 = u.split * p.kb_per_split;
+    *nkb = max(0, min(p.kb_per_split, all - *kb0));
+}
+
+// A staging box: 128 rows of 128 bytes, 16-byte chunk j of row r at chunk j ^ (r % 8).
+__device__ __forceinline__ uint32_t box_addr(uint32_t box, int r, int j) {
+    return box + static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4));
+}
+
+// Rows that TMA cannot take (not 16-byte aligned): the 32 box rows of this warp to or from
+// global memory, one row at a time, neighbouring lanes on neighbouring elements.
+template <typename E>
+__device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, int row0, int col0, int rows, int cols,
+                                            int quad, int lane) {
+    constexpr int N = 128 / sizeof(E);  // elements per box row
+    for (int i = 0; i < 32; ++i) {
+        const int r = quad * 32 + i;
+        if (row0 + r >= rows) break;
+#pragma unroll
+        for (int h = 0; h < N / 32; ++h) {
+            const int c = h * 32 + lane;
+            if (col0 + c < cols) {
+                const uint32_t a = box_addr(box, r, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
+                E v;
+                if constexpr (sizeof(E) == 2) {
+                    uint16_t b;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(a) : "memory");
+                    v = b;
+                } else {
+                    uint32_t b;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b) : "r"(a) : "memory");
+                    v = b;
+                }
+                dst[static_cast<size_t>(row0 + r) * ld + col0 + c] = v;
+            }
+        }
+    }
+}
+template <typename E>
+__device__ __forceinline__ void rows_to_box(uint32_t box, const E* src, long long ld, int row0, int col0, int rows,
+                                            int cols, int quad, int lane) {
+    constexpr int N = 128 / sizeof(E);
+    for (int i = 0; i < 32; ++i) {
+        const int r = quad * 32 + i;
+        if (row0 + r >= rows) break;
+#pragma unroll
+        for (int h = 0; h < N / 32; ++h) {
+            const int c = h * 32 + lane;
+            if (col0 + c < cols) {
+                const uint32_t a = box_addr(box, r, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
+                const E v = src[static_cast<size_t>(row0 + r) * ld + col0 + c];
+                if constexpr (sizeof(E) == 2) sts16(a, v);
+                else asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+            }
+        }
+    }
+}
+
+// Per-thread epilogue state of one group (128 threads, two staging boxes).
+struct EpiState {
+    uint32_t boxes;      // shared address of the group's two boxes
+    uint64_t* in_bar;    // the group's two input-load barriers
+    int r, quad, lane, grp;
+    bool leader;
+    bool fail;
+    int loads[2];        // input loads armed per box (parity of the barrier)
+};
+
+// Sends one box of results out: by TMA (the group's leader, after every thread's writes),
+// or row by row by the warps themselves.
+template <typename E>
+__device__ __forceinline__ void send_box(const EpiState& x, const CUtensorMap* tm, int by_tma, uint32_t box, void* dst,
+                                         long long ld, int row0, int col0, int rows, int cols) {
+    if (by_tma) {
+        fence_proxy_async_smem();
+        named_barrier_sync(1 + x.grp, 128);
+        if (x.leader) {
+            if (row0 < rows && col0 < cols)
+                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
+                             "r"(box), "r"(col0), "r"(row0), "r"(0)
+                             : "memory");
+            bulk_commit_group();
+        }
+    } else {
+        __syncwarp();
+        box_to_rows<E>(box, static_cast<E*>(dst), ld, row0, col0, rows, cols, x.quad, x.lane);
+        fence_proxy_async_smem();  // before an input load into this box
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void arm_input(EpiState& x, const CUtensorMap* tm, int b, int col0, int row0) {
+    if (x.leader) {
+        mbar_arrive_expect_tx(&x.in_bar[b], QBOX);
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(x.boxes + b * QBOX),
+            "l"(tm), "r"(smem_u32(&x.in_bar[b])), "r"(col0), "r"(row0), "r"(0)
+            : "memory");
+    }
+    ++x.loads[b];
+}
+
+// 32 bias values (those past `cols` read as 0).
+template <typename T>
+__device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int cols, float (&v)[32]) {
+    if (e.bias_f32) {
+        const float* b = static_cast<const float*>(e.bias);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += col0 + i < cols ? __ldg(b + col0 + i) : 0.f;
+    } else {
+        const T* b = static_cast<const T*>(e.bias);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += col0 + i < cols ? Elem<T>::load(b[col0 + i]) : 0.f;
+    }
+}
+
+// The 16-bit epilogue of this group's half of a tile, 64 columns (one box row) at a time.
+template <typename T, int BN>
+__device__ __forceinline__ void epilogue_16(const PairGemmParams& p, EpiState& x, uint32_t tacc, uint32_t tempty, int row0,
+                                            int col0) {
+    constexpr int PIECES = BN / 2 / 64;
+    const GemmEpilogue& e = p.epi;
+    const bool in_tma = e.in && p.in_tma && !e.z;
+    if (in_tma && x.leader) bulk_wait_read_all();  // the boxes' earlier stores have been read
+    if (in_tma) {
+        for (int q = 0; q < PIECES; ++q) arm_input(x, &p.tm_in, q & 1, col0 + 64 * q, row0);
+    }
+#pragma unroll 1
+    for (int q = 0; q < PIECES; ++q) {
+        const int pc = col0 + 64 * q;
+        // z leaves through box 0 and y through box 1 where both are stored
+        const int yb = e.z ? 1 : q & 1;
+        const uint32_t ybox = x.boxes + yb * QBOX, zbox = x.boxes;
+        if (in_tma) {
+            if (!mbar_wait(&x.in_bar[yb], static_cast<uint32_t>(x.loads[yb] - 1) & 1u, p.err)) x.fail = true;
+        } else {
+            if (x.leader) bulk_wait_read_all();
+            named_barrier_sync(1 + x.grp, 128);
+            if (e.in) {
+                rows_to_box<uint16_t>(ybox, static_cast<const uint16_t*>(e.in), e.ldin, row0, pc, p.rows, p.cols, x.quad,
+                                      x.lane);
+                __syncwarp();
+            }
+        }
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            float v[32];
+            tmem_ld_32x32b_x32(tacc + q * 64 + h * 32, v);
+            if (e.bias) add_bias<T>(e, pc + h * 32, p.cols, v);
+            if (e.z) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sts128(box_addr(zbox, x.r, h * 4 + j), Elem<T>::pack(v + 8 * j));
+            }
+            act_values<32>(e.act, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = box_addr(ybox, x.r, h * 4 + j);
+                if (e.in) {
+                    float f[8];
+                    Elem<T>::unpack(lds128(a), f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];
+                }
+                sts128(a, Elem<T>::pack(v + 8 * j));
+            }
+        }
+        if (q == PIECES - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (x.lane == 0) mbar_arrive_cluster(tempty);  // the accumulator is read
+        }
+        if (e.z) send_box<uint16_t>(x, &p.tm_z, p.z_tma, zbox, e.z, e.ldz, row0, pc, p.rows, p.cols);
+        send_box<uint16_t>(x, &p.tm_out, p.out_tma, ybox, e.out, e.ldout, row0, pc, p.rows, p.cols);
+    }
+}
+
+// The fp32 results of this group's half of a tile (sums of all chains, in registers), 32
+// columns (one box row) at a time, to out or to this split's partial product.
+template <int BN>
+__device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, float (&sum)[BN / 2], int row0, int col0,
+                                          int split) {
+    const GemmEpilogue& e = p.epi;
+    const bool partial = p.splits > 1;
+    const bool in = e.in && !partial;
+    // (tm_out is then a map of the partial products [splits][rows][cols])
+#pragma unroll
+    for (int q = 0; q < BN / 2 / 32; ++q) {
+        const int pc = col0 + 32 * q;
+        const uint32_t box = x.boxes + (q & 1) * QBOX;
+        if (x.leader) bulk_wait_read_but_one();  // this box's store, two pieces ago
+        named_barrier_sync(1 + x.grp, 128);
+        if (in) {
+            if (p.in_tma) {
+                arm_input(x, &p.tm_in, q & 1, pc, row0);
+                if (!mbar_wait(&x.in_bar[q & 1], static_cast<uint32_t>(x.loads[q & 1] - 1) & 1u, p.err)) x.fail = true;
+            } else {
+                rows_to_box<uint32_t>(box, static_cast<const uint32_t*>(e.in), e.ldin, row0, pc, p.rows, p.cols, x.quad,
+                                      x.lane);
+                __syncwarp();
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t a = box_addr(box, x.r, j);
+            float f[4] = {sum[32 * q + 4 * j], sum[32 * q + 4 * j + 1], sum[32 * q + 4 * j + 2], sum[32 * q + 4 * j + 3]};
+            if (in) {
+                float o[4];
+                Elem<float>::unpack(lds128(a), o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] += o[i];
+            }
+            sts128(a, Elem<float>::pack(f));
+        }
+        if (partial || p.out_tma) {
+            fence_proxy_async_smem();
+            named_barrier_sync(1 + x.grp, 128);
+            if (x.leader) {
+                if (row0 < p.rows && pc < p.cols)
+                    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                                     &p.tm_out),
+                                 "r"(box), "r"(pc), "r"(row0), "r"(partial ? split : 0)
+                                 : "memory");
+                bulk_commit_group();
+            }
+        } else {
+            __syncwarp();
+            box_to_rows<uint32_t>(box, static_cast<uint32_t*>(e.out), e.ldout, row0, pc, p.rows, p.cols, x.quad, x.lane);
+            fence_proxy_async_smem();  // before an input load into this box
+            __syncwarp();
+        }
+    }
+}
+
+// T: type of 16-bit results (float: fp32 results, taken in chains of CHAIN_KB k-blocks)
+template <typename T, int BN>
+__global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid_constant__ PairGemmParams p) {
+    using S = PairShape<BN>;
+    constexpr bool F32 = sizeof(T) == 4;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[S::STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[S::STAGES];
+    __shared__ __align__(8) uint64_t tfull_bar[2];
+    __shared__ __align__(8) uint64_t tempty_bar[2];
+    __shared__ __align__(8) uint64_t in_bar[EPI_GROUPS][2];
+    __shared__ __align__(8) uint64_t mma_done_bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int aborted;
+
+    pdl_allow_next();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();  // 0 = leader (issues the MMAs)
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int units = p.tiles_r * p.tiles_c * p.splits;
+    uint8_t* smem =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull_bar[b], 1);
+            mbar_init(&tempty_bar[b], 2 * 4 * EPI_GROUPS);  // each epilogue warp of both CTAs
+            for (int g = 0; g < EPI_GROUPS; ++g) mbar_init(&in_bar[g][b], 1);
+        }
+        mbar_init(&mma_done_bar, 1);
+        fence_mbar_init();
+        aborted = 0;
+        tma_prefetch_desc(&p.tm_a);
+        tma_prefetch_desc(&p.tm_b);
+    }
+    if (warp == 1) tmem_alloc_pair(&tmem_slot, S::TMEM_COLS);
+    tc_fence_before();
+    cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
+    tc_fence_after();
+    pdl_wait_previous();
+    const uint32_t tmem = tmem_slot;
+    int issued = 0;  // producer: k-blocks whose loads were armed
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer
+            int it = 0;
+            for (int u = pair; u < units; u += npairs) {
+                const Unit t = unit_of(p, u);
+                int kb0, nkb;
+                unit_kblocks(p, t, &kb0, &nkb);
+                const int arow = t.tr * PAIR_ROWS + CTA_ROWS * static_cast<int>(rank);
+                const int brow = t.tc * BN + BN / 2 * static_cast<int>(rank);
+                bool ok = true;
+                for (int kb = kb0; kb < kb0 + nkb; ++kb, ++it) {
+                    const int s = it % S::STAGES;
+                    if (!mbar_wait(&empty_bar[s], ((it / S::STAGES) & 1) ^ 1, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * S::STAGE);
+                    const uint32_t fb = map_to_rank(&full_bar[s], 0);
+                    uint8_t* sa = smem + s * S::STAGE;
+                    uint8_t* sb = sa + A_STAGE;
+                    const int kc = kb * GEMM_BK;
+                    if (p.a_mn) {
+                        tma_load_3d_pair(sa, &p.tm_a, fb, arow, kc, 0);
+                        tma_load_3d_pair(sa + 8192, &p.tm_a, fb, arow + 64, kc, 0);
+                    } else {
+                        tma_load_3d_pair(sa, &p.tm_a, fb, kc, arow, 0);
+                    }
+                    if (p.b_mn) {
+#pragma unroll
+                        for (int h = 0; h < BN / 128; ++h)
+                            tma_load_3d_pair(sb + h * 8192, &p.tm_b, fb, brow + 64 * h, kc, 0);
+                    } else {
+                        tma_load_3d_pair(sb, &p.tm_b, fb, kc, brow, 0);
+                    }
+                    issued = it + 1;
+                }
+                if (!ok) {
+                    aborted = 1;
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer (leader CTA): the next stage's barrier is tested while
+            // this k-block's MMAs run, and waited for only when that test found it not loaded
+            const uint32_t stage0 = smem_u32(smem);
+            const uint32_t idesc = idesc_16(PAIR_ROWS, BN, p.a_mn, p.b_mn, p.f16);
+            const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
+            const uint32_t a_lbo = p.a_mn ? 8192 : 16, b_lbo = p.b_mn ? 8192 : 16;
+            int s = 0, acc = 0;
+            uint32_t ph = 0;
+            bool ready = false, ok = true;
+            for (int u = pair; u < units && ok; u += npairs) {
+                const Unit t = unit_of(p, u);
+                int kb0, nkb;
+                unit_kblocks(p, t, &kb0, &nkb);
+                for (int c0 = 0; c0 < nkb && ok; c0 += F32 ? CHAIN_KB : nkb, ++acc) {
+                    const int cn = F32 ? min(CHAIN_KB, nkb - c0) : nkb;
+                    const int ab = acc & 1;
+                    if (!mbar_wait(&tempty_bar[ab], ((acc >> 1) & 1) ^ 1, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t dacc = tmem + static_cast<uint32_t>(ab * BN);
+                    for (int kb = 0; kb < cn; ++kb) {
+                        if (!ready && !mbar_wait(&full_bar[s], ph, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a0 = stage0 + static_cast<uint32_t>(s * S::STAGE);
+                        const uint32_t a_lo = sw128_desc_lo(a0, a_lbo), b_lo = sw128_desc_lo(a0 + A_STAGE, b_lbo);
+#pragma unroll
+                        for (int kk = 0; kk < GEMM_BK / 16; ++kk)
+                            umma_bf16_pair(dacc, sw128_desc(a_lo + kk * a_step), sw128_desc(b_lo + kk * b_step), idesc,
+                                           (kb | kk) != 0 ? 1u : 0u);
+                        const int s_next = s + 1 == S::STAGES ? 0 : s + 1;
+                        const uint32_t ph_next = s_next == 0 ? ph ^ 1u : ph;
+                        ready = mbar_test_wait(smem_u32(&full_bar[s_next]), ph_next);
+                        umma_commit_pair(&empty_bar[s], 3);  // frees stage s in both CTAs
+                        s = s_next;
+                        ph = ph_next;
+                    }
+                    if (ok) umma_commit_pair(&tfull_bar[ab], 3);  // accumulator complete in both CTAs
+                }
+            }
+            if (!ok) aborted = 1;
+            umma_commit_pair(&mma_done_bar, 3);
+            mbar_wait(&mma_done_bar, 0, p.err);
+        } else if (lane == 0) {
+            mbar_wait(&mma_done_bar, 0, p.err);  // peer: the leader's MMAs write this CTA's TMEM
+        }
+    } else if (warp >= EPI_WARP0) {
+        // ---------------- epilogue: TMEM lane quadrant = warp % 4
+        EpiState x;
+        x.quad = warp & 3;
+        x.grp = (warp - EPI_WARP0) >> 2;
+        x.lane = lane;
+        x.r = x.quad * 32 + lane;
+        x.leader = x.quad == 0 && lane == 0;
+        x.boxes = smem_u32(smem + S::STAGES * S::STAGE + x.grp * 2 * QBOX);
+        x.in_bar = in_bar[x.grp];
+        x.fail = false;
+        x.loads[0] = x.loads[1] = 0;
+        const uint32_t te[2] = {map_to_rank(&tempty_bar[0], 0), map_to_rank(&tempty_bar[1], 0)};
+        int acc = 0;
+        for (int u = pair; u < units; u += npairs) {
+            // the group stops together once any wait of any role gave up
+            if (named_barrier_or(1 + x.grp, 128, x.fail || aborted)) {
+                aborted = 1;
+                break;
+            }
+            const Unit t = unit_of(p, u);
+            int kb0, nkb;
+            unit_kblocks(p, t, &kb0, &nkb);
+            const int row0 = t.tr * PAIR_ROWS + CTA_ROWS * static_cast<int>(rank);
+            const int col0 = t.tc * BN + BN / 2 * x.grp;
+            const uint32_t tlane = tmem + (static_cast<uint32_t>(x.quad * 32) << 16) + static_cast<uint32_t>(BN / 2 * x.grp);
+            if constexpr (F32) {
+                float sum[BN / 2];
+#pragma unroll
+                for (int i = 0; i < BN / 2; ++i) sum[i] = 0.f;
+                for (int c0 = 0; c0 < nkb; c0 += CHAIN_KB, ++acc) {
+                    const int ab = acc & 1;
+                    if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
+                    tc_fence_after();
+#pragma unroll
+                    for (int q = 0; q < BN / 2 / 32; ++q) {
+                        float v[32];
+                        tmem_ld_32x32b_x32(tlane + ab * BN + q * 32, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sum[q * 32 + i] += v[i];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(te[ab]);
+                }
+                store_f32<BN>(p, x, sum, row0, col0, t.split);
+            } else {
+                const int ab = acc & 1;
+                if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
+                tc_fence_after();
+                epilogue_16<T, BN>(p, x, tlane + ab * BN, te[ab], row0, col0);
+                ++acc;
+            }
+        }
+        if (x.leader) {
+            bulk_wait_all();  // every store of this group has completed
+            for (int b = 0; b < 2; ++b)
+                if (x.loads[b]) mbar_wait(&x.in_bar[b], static_cast<uint32_t>(x.loads[b] - 1) & 1u, p.err);
+        }
+    }
+
+    __syncthreads();
+    if (aborted && warp == 0 && lane == 0 && rank == 0) {
+        // the pair's loads in flight land before its shared memory goes away
+        for (int kb = issued - S::STAGES < 0 ? 0 : issued - S::STAGES; kb < issued; ++kb)
+            mbar_wait(&full_bar[kb % S::STAGES], (kb / S::STAGES) & 1, p.err);
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, S::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------- few rows
+constexpr int ROW_THREADS = 192;  // warp 0: TMA producer, warp 1: MMA issuer and TMEM owner, warps 2-5: epilogue
+template <int BN>
+struct RowShape {
+    static constexpr int STAGE = A_STAGE + BN * 128;
+    static constexpr int STAGES = BN <= 64 ? 8 : 6;
+    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static constexpr uint32_t TMEM_COLS = BN < 32 ? 32 : BN;
+    static_assert(BN * ROW_TILE_A * 4 <= STAGES * STAGE, "the partial accumulator reuses the stages");
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// bias, activation, residual and stores of one element (row = B's row, col = A's row)
+template <typename T>
+__device__ __forceinline__ void finish_element(const GemmEpilogue& e, float v, float bias, long long row, int col) {
+    v += bias;
+    if (e.z) static_cast<T*>(e.z)[row * e.ldz + col] = Elem<T>::store(v);
+    v = act_value(e.act, v);
+    if (e.in) v += Elem<T>::load(static_cast<const T*>(e.in)[row * e.ldin + col]);
+    static_cast<T*>(e.out)[row * e.ldout + col] = Elem<T>::store(v);
+}
+
+template <typename T, int BN>
+__global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_constant__ RowGemmParams p) {
+    using S = RowShape<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[S::STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[S::STAGES];
+    __shared__ __align__(8) uint64_t done_bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int aborted;
+
+    pdl_allow_next();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x % p.splits;  // rank in the cluster
+    const int a0 = blockIdx.x / p.splits * ROW_TILE_A;
+    const int b0 = blockIdx.y * BN;
+    const int all = (p.k + GEMM_BK - 1) / GEMM_BK;
+    const int kb0 = split * p.kb_per_split;
+    const int nkb = max(0, min(p.kb_per_split, all - kb0));
+    uint8_t* smem =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        mbar_init(&done_bar, 1);
+        fence_mbar_init();
+        aborted = 0;
+        tma_prefetch_desc(&p.tm_a);
+        tma_prefetch_desc(&p.tm_b);
+    }
+    if (warp == 1) tmem_alloc(&tmem_slot, S::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait_previous();
+    const uint32_t tmem = tmem_slot;
+    int issued = 0;  // producer: k-blocks whose loads were armed
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int it = 0; it < nkb; ++it) {
+                const int s = it % S::STAGES;
+                if (!mbar_wait(&empty_bar[s], ((it / S::STAGES) & 1) ^ 1, p.err)) {
+                    aborted = 1;
+                    break;
+                }
+                mbar_arrive_expect_tx(&full_bar[s], S::STAGE);
+                uint8_t* sa = smem + s * S::STAGE;
+                const int kc = (kb0 + it) * GEMM_BK;
+                if (p.a_mn) {
+                    tma_load_3d(sa, &p.tm_a, &full_bar[s], a0, kc, 0);
+                    tma_load_3d(sa + 8192, &p.tm_a, &full_bar[s], a0 + 64, kc, 0);
+                } else {
+                    tma_load_3d(sa, &p.tm_a, &full_bar[s], kc, a0, 0);
+                }
+                tma_load_3d(sa + A_STAGE, &p.tm_b, &full_bar[s], kc, b0, 0);
+                issued = it + 1;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t stage0 = smem_u32(smem);
+            const uint32_t idesc = idesc_16(ROW_TILE_A, BN, p.a_mn, false, p.f16);
+            const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, a_lbo = p.a_mn ? 8192 : 16;
+            for (int it = 0; it < nkb; ++it) {
+                const int s = it % S::STAGES;
+                if (!mbar_wait(&full_bar[s], (it / S::STAGES) & 1, p.err)) {
+                    aborted = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = stage0 + static_cast<uint32_t>(s * S::STAGE);
+                const uint32_t a_lo = sw128_desc_lo(sa, a_lbo), b_lo = sw128_desc_lo(sa + A_STAGE, 16);
+#pragma unroll
+                for (int kk = 0; kk < GEMM_BK / 16; ++kk)
+                    umma_bf16(tmem, sw128_desc(a_lo + kk * a_step), sw128_desc(b_lo + kk * (32 >> 4)), idesc,
+                              (it | kk) != 0 ? 1u : 0u);
+                umma_commit(&empty_bar[s]);
+            }
+            umma_commit(&done_bar);
+            mbar_wait(&done_bar, 0, p.err);
+        }
+    } else {
+        // ---------------- epilogue: thread = one row of A (one output column)
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;
+        const int col = a0 + r;
+        const bool live = col < p.na;
+        const int nb = min(BN, p.nb - b0);
+        const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        float bias = 0.f;
+        if (live && p.epi.bias)
+            bias = p.epi.bias_f32 ? static_cast<const float*>(p.epi.bias)[col] : Elem<T>::load(static_cast<const T*>(p.epi.bias)[col]);
+        mbar_wait(&done_bar, 0, p.err);
+        tc_fence_after();
+        float* own = reinterpret_cast<float*>(smem);  // [BN][128] partial accumulator (the stages are done)
+        for (int q = 0; q * 32 < nb; ++q) {
+            float v[32];
+            tmem_ld_32x32b_x32(tlane + q * 32, v);
+            if (p.splits == 1) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (live && q * 32 + i < nb) finish_element<T>(p.epi, v[i], bias, b0 + q * 32 + i, col);
+            } else {
+                // a split past the end of the contraction holds no product
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (q * 32 + i < nb) own[(q * 32 + i) * ROW_TILE_A + r] = nkb > 0 ? v[i] : 0.f;
+            }
+        }
+        __syncwarp();
+        if (p.splits > 1) {
+            cluster_sync();
+            // every CTA finishes its share of the B rows, the parts added in rank order
+            for (int j = split; j < nb; j += p.splits) {
+                float v = 0.f;
+                for (int s = 0; s < p.splits; ++s)
+                    v += ld_cluster_f32(map_to_rank(&own[j * ROW_TILE_A + r], static_cast<uint32_t>(s)));
+                if (live) finish_element<T>(p.epi, v, bias, b0 + j, col);
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    if (p.splits > 1) {
+        if (warp < 2) cluster_sync();  // the first barrier of the epilogue warps above
+        cluster_sync();                // no CTA leaves while its partial accumulator is read
+    }
+    __syncthreads();
+    if (aborted && threadIdx.x == 0) {
+        // the loads in flight land before the shared memory goes away
+        for (int kb = issued - S::STAGES < 0 ? 0 : issued - S::STAGES; kb < issued; ++kb)
+            mbar_wait(&full_bar[kb % S::STAGES], (kb / S::STAGES) & 1, p.err);
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, S::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------- around the products
+// out = [in +] sum of the splits' partial products, four columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) split_sum_kernel(const SplitSumParams p) {
+    pdl_wait_previous();
+    const long long chunks = p.ld_part / 4;
+    const long long total = chunks * p.rows;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long row = i / chunks;
+        const int c = static_cast<int>(i - row * chunks) * 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < p.splits; ++s) {
+            const float4 f = __ldcs(reinterpret_cast<const float4*>(p.part + (static_cast<size_t>(s) * p.rows + row) * p.ld_part + c));
+            v[0] += f.x;
+            v[1] += f.y;
+            v[2] += f.z;
+            v[3] += f.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < p.cols) {
+                float f = v[e];
+                if (p.in) f += Elem<T>::load(static_cast<const T*>(p.in)[row * p.ldin + c + e]);
+                static_cast<T*>(p.out)[row * p.ldout + c + e] = Elem<T>::store(f);
+            }
+    }
+}
+
+// Eight columns per thread; the last chunk of a row may be partial.
+__global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
+    pdl_wait_previous();
+    const long long chunks = p.ldd / 8;
+    const long long total = chunks * p.rows;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long row = i / chunks;
+        const int c = static_cast<int>(i - row * chunks) * 8;
+        const uint16_t* s = p.src + row * p.lds + c;
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols ? __ldg(s + e) : 0u;
+        *reinterpret_cast<uint4*>(p.dst + row * p.ldd + c) =
+            make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+}
+
+constexpr int AG_LANES = 8;  // rows in flight per block: 32 threads x 8 columns each
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * AG_LANES) act_grad_kernel(const ActGradParams p) {
+    __shared__ float sums[AG_LANES][ACT_GRAD_COLS];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int c = blockIdx.x * ACT_GRAD_COLS + tx * 8;
+    const T* dy = static_cast<const T*>(p.dy);
+    const T* z = static_cast<const T*>(p.z);
+    T* dz = static_cast<T*>(p.dz);
+    pdl_wait_previous();
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const long long r0 = static_cast<long long>(blockIdx.y) * p.rows_per_block;
+    const long long r1 = min(r0 + p.rows_per_block, p.rows);
+    if (c < p.cols) {
+#pragma unroll 2
+        for (long long r = r0 + ty; r < r1; r += AG_LANES) {
+            float g[8], f[8];
+            if constexpr (VEC) {
+                Elem<T>::unpack(ldg_stream(dy + r * p.lddy + c), g);
+                if (z) Elem<T>::unpack(ldg_stream(z + r * p.ldz + c), f);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    g[e] = c + e < p.cols ? Elem<T>::load(dy[r * p.lddy + c + e]) : 0.f;
+                    f[e] = z && c + e < p.cols ? Elem<T>::load(z[r * p.ldz + c + e]) : 0.f;
+                }
+            }
+            if (z) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] *= act_slope(p.act, f[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += g[e];
+            if (dz) *reinterpret_cast<uint4*>(dz + r * p.ldd + c) = Elem<T>::pack(g);
+        }
+    }
+    if (!p.part) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[ty][tx * 8 + e] = acc[e];
+    __syncthreads();
+    const int cc = blockIdx.x * ACT_GRAD_COLS + threadIdx.x;
+    if (cc < p.cols) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < AG_LANES; ++k) s += sums[k][threadIdx.x];
+        p.part[static_cast<size_t>(blockIdx.y) * p.cols + cc] = s;
+    }
+}
+
+constexpr int CS_LANES = 16;
+__global__ void __launch_bounds__(32 * CS_LANES) column_sum_kernel(const float* part, int blocks, int cols, float* out,
+                                                                  int accumulate) {
+    __shared__ float s[CS_LANES][32];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + x;
+    pdl_wait_previous();
+    float a = 0.f;
+    if (c < cols)
+        for (int b = y; b < blocks; b += CS_LANES) a += part[static_cast<size_t>(b) * cols + c];
+    s[y][x] = a;
+    __syncthreads();
+    if (y == 0 && c < cols) {
+        for (int k = 1; k < CS_LANES; ++k) a += s[k][x];
+        out[c] = accumulate ? out[c] + a : a;
+    }
+}
+
+template <typename T, int BN>
+cudaError_t run_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(PAIR_THREADS);
+    cfg.dynamicSmemBytes = PairShape<BN>::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const int units = p.tiles_r * p.tiles_c * p.splits;
+    const int most = sm_count / 2;
+    cfg.gridDim = dim3(2 * (units < most ? units : most));
+    return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<T, BN>, p);
+}
+
+template <typename T, int BN>
+cudaError_t run_row(const RowGemmParams& p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((p.na + ROW_TILE_A - 1) / ROW_TILE_A * p.splits, (p.nb + BN - 1) / BN);
+    cfg.blockDim = dim3(ROW_THREADS);
+    cfg.dynamicSmemBytes = RowShape<BN>::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, row_gemm_kernel<T, BN>, p);
+}
+
+int blocks_for(long long items) {
+    const long long b = (items + 255) / 256;
+    return static_cast<int>(b < 1 ? 1 : b < 152 * 16 ? b : 152 * 16);
+}
+
+}  // namespace
+
+cudaError_t linear_prepare() {
+    cudaError_t e;
+#define ANVIL_SMEM(kernel, bytes) \
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return e
+    ANVIL_SMEM((pair_gemm_kernel<__nv_bfloat16, 256>), PairShape<256>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<__nv_bfloat16, 128>), PairShape<128>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<__half, 256>), PairShape<256>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<__half, 128>), PairShape<128>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<float, 256>), PairShape<256>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<float, 128>), PairShape<128>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 16>), RowShape<16>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 32>), RowShape<32>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 64>), RowShape<64>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 128>), RowShape<128>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__half, 16>), RowShape<16>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__half, 32>), RowShape<32>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__half, 64>), RowShape<64>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__half, 128>), RowShape<128>::SMEM);
+#undef ANVIL_SMEM
+    return cudaSuccess;
+}
+
+cudaError_t launch_pair_gemm(const PairGemmParams& p, int bn, int sm_count, cudaStream_t s) {
+    if (p.epi.out_f32) return bn == 256 ? run_pair<float, 256>(p, sm_count, s) : run_pair<float, 128>(p, sm_count, s);
+    if (p.f16) return bn == 256 ? run_pair<__half, 256>(p, sm_count, s) : run_pair<__half, 128>(p, sm_count, s);
+    return bn == 256 ? run_pair<__nv_bfloat16, 256>(p, sm_count, s) : run_pair<__nv_bfloat16, 128>(p, sm_count, s);
+}
+
+cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t s) {
+    switch (bn) {
+        case 16: return p.f16 ? run_row<__half, 16>(p, s) : run_row<__nv_bfloat16, 16>(p, s);
+        case 32: return p.f16 ? run_row<__half, 32>(p, s) : run_row<__nv_bfloat16, 32>(p, s);
+        case 64: return p.f16 ? run_row<__half, 64>(p, s) : run_row<__nv_bfloat16, 64>(p, s);
+        default: return p.f16 ? run_row<__half, 128>(p, s) : run_row<__nv_bfloat16, 128>(p, s);
+    }
+}
+
+cudaError_t launch_split_sum(const SplitSumParams& p, cudaStream_t s) {
+    const dim3 grid(blocks_for(p.ld_part / 4 * p.rows));
+    if (p.out_f32) return launch_pdl(split_sum_kernel<float>, grid, dim3(256), 0, s, p);
+    if (p.f16) return launch_pdl(split_sum_kernel<__half>, grid, dim3(256), 0, s, p);
+    return launch_pdl(split_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p);
+}
+
+cudaError_t launch_repack(const RepackParams& p, cudaStream_t s) {
+    return launch_pdl(repack_kernel, dim3(blocks_for(p.ldd / 8 * p.rows)), dim3(256), 0, s, p);
+}
+
+cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t s) {
+    auto ok = [](const void* q, long long ld) { return !(reinterpret_cast<uintptr_t>(q) & 15) && ld % 8 == 0; };
+    const bool vec = p.cols % 8 == 0 && ok(p.dy, p.lddy) && ok(p.z, p.z ? p.ldz : 0);
+    const dim3 grid((p.cols + ACT_GRAD_COLS - 1) / ACT_GRAD_COLS, p.blocks_r), block(32 * AG_LANES);
+    if (p.f16)
+        return vec ? launch_pdl(act_grad_kernel<__half, true>, grid, block, 0, s, p)
+                   : launch_pdl(act_grad_kernel<__half, false>, grid, block, 0, s, p);
+    return vec ? launch_pdl(act_grad_kernel<__nv_bfloat16, true>, grid, block, 0, s, p)
+               : launch_pdl(act_grad_kernel<__nv_bfloat16, false>, grid, block, 0, s, p);
+}
+
+cudaError_t launch_column_sum(const float* part, int blocks, int cols, float* out, int accumulate, cudaStream_t s) {
+    return launch_pdl(column_sum_kernel, dim3((cols + 31) / 32), dim3(32 * CS_LANES), 0, s, part, blocks, cols, out,
+                      accumulate);
+}
+
+}  // namespace anvil

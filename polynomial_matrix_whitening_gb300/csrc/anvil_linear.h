@@ -1,0 +1,99 @@
+// anvil_linear.h -- parameter blocks and launchers of the linear layer's kernels (internal
+// to libanvil).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace anvil {
+
+// activation codes of include/anvil.h (anvil_activation)
+enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_RELU2 = 2, ACT_GELU = 3, ACT_GELU_TANH = 4, ACT_SILU = 5, ACT_COUNT = 6 };
+
+// What follows a product's fp32 accumulator v at (row, col):
+//   v += bias[col];  z = v (stored if z);  v = act(v);  v += in;  out = v
+struct GemmEpilogue {
+    const void* bias;     // [cols] or null
+    const void* in;       // residual (16 bit) or the gradient so far (out's type), or null
+    void* z;              // or null
+    void* out;
+    long long ldin, ldz, ldout;
+    int bias_f32;         // bias is fp32 (else the operands' type)
+    int act;
+    int out_f32;          // out (and in) are fp32
+};
+
+// C [rows, cols] = sum_k A[row, k] B[col, k].  An operand is K-major (stored [row][k]) or
+// MN-major (stored [k][row]).
+struct PairGemmParams {
+    CUtensorMap tm_a, tm_b, tm_in, tm_out, tm_z;
+    GemmEpilogue epi;
+    int rows, cols, k;
+    int a_mn, b_mn;
+    int f16;                        // operands are fp16 (else bf16)
+    int in_tma, out_tma, z_tma;     // through tensor maps (16-byte aligned rows)
+    int tiles_r, tiles_c, splits;   // work units: tiles_r * tiles_c * splits
+    int kb_per_split;               // 64-deep k-blocks of a split
+    unsigned* err;                  // splits > 1: tm_out maps the partial products [splits][rows][cols]
+};
+// A = the operand whose rows run along the output's contiguous dimension ("cols" above),
+// B = the few rows: out[b][a].
+struct RowGemmParams {
+    CUtensorMap tm_a, tm_b;
+    GemmEpilogue epi;               // columns are A's rows, rows are B's rows
+    int na, nb, k;                  // A's rows, B's rows, contraction
+    int a_mn;                       // A MN-major (B is always K-major)
+    int f16;
+    int splits;                     // cluster size along k
+    int kb_per_split;
+    unsigned* err;
+};
+
+constexpr int GEMM_BK = 64;    // k-block: one 128-byte swizzle row of 16-bit elements
+constexpr int PAIR_ROWS = 256; // output rows of a CTA pair's tile
+constexpr int ROW_TILE_A = 128;
+
+cudaError_t linear_prepare();
+// bn: output columns of a pair's tile (256 or 128)
+cudaError_t launch_pair_gemm(const PairGemmParams& p, int bn, int sm_count, cudaStream_t stream);
+// bn: B's rows per block (16, 32, 64 or 128)
+cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t stream);
+
+// out (+)= sum over splits of part [splits][rows][ld_part], in split order.
+struct SplitSumParams {
+    const float* part;
+    const void* in;
+    void* out;
+    long long ld_part, ldin, ldout;
+    int rows, cols, splits;
+    int out_f32, f16;
+};
+cudaError_t launch_split_sum(const SplitSumParams& p, cudaStream_t stream);
+
+// dst [rows, ldd] <- src [rows, cols] (row stride lds), 16-bit elements, ldd % 8 == 0.
+struct RepackParams {
+    const uint16_t* src;
+    uint16_t* dst;
+    long long rows, lds, ldd;
+    int cols;
+};
+cudaError_t launch_repack(const RepackParams& p, cudaStream_t stream);
+
+// dz = dy * act'(z) (rounded to the operands' type for the products; may be null) and the
+// column sums of the unrounded dz (partial rows; may be null).
+struct ActGradParams {
+    const void* dy;
+    const void* z;       // null: dz = dy
+    void* dz;            // [rows, ldd] or null
+    float* part;         // [blocks_r][cols] or null
+    long long rows, lddy, ldz, ldd;
+    int cols, act, f16;
+    int rows_per_block, blocks_r;
+};
+constexpr int ACT_GRAD_COLS = 256;  // columns per block
+cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream);
+// out[c] (+)= sum of part[b][c] over b, in order.
+cudaError_t launch_column_sum(const float* part, int blocks, int cols, float* out, int accumulate, cudaStream_t stream);
+
+}  // namespace anvil

@@ -1,0 +1,430 @@
+// anvil_logprob.cu -- log probabilities of given tokens, with entropy and the top
+// alternatives, and their gradient, for sm_103a.
+//
+//   forward   lse = log sum_j e^{x_j},  logprob = x_t - lse,  H = lse - sum_j p_j x_j,
+//             the k largest x_j - lse (ties: the lowest index first), p_j = e^{x_j - lse}
+//   backward  dx_j = u ([j = t] - p_j) - v p_j (log p_j + H)
+//             for u = dL/dlogprob, v = dL/dH
+//
+// The forward pass reads the logits once: every thread keeps a running maximum m, the sum
+// s of e^{x - m} and the sum q of e^{x - m} (x - m) (in fp32, rescaled when the maximum
+// grows), from which lse = m + log s and H = log s - q / s.  The top k are found in the
+// same pass: each warp holds the best k so far, one per lane in order, and only a lane
+// that sees a value above the k-th opens the (rare) insertion path.  HBM bounds both
+// passes where there are many rows; where rows are fewer than the SMs, a cluster of up to
+// eight blocks takes a row's segments and the first block joins their results through
+// distributed shared memory, in a fixed order.
+//
+// A row in which every logit is -inf has no distribution: lse and the log probabilities
+// are -inf, the entropy is 0 and the gradient is zero.  A masked logit (-inf, or so low
+// that e^{x - m} is 0) adds nothing: its exponent is held at -200 (in base 2), where e is
+// 0, so that no product of 0 and infinity arises.  A NaN or +inf makes its row NaN.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "anvil_device.cuh"
+#include "anvil_logprob.h"
+#include "anvil_types.cuh"
+
+namespace anvil {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr int KEY_NONE = INT32_MIN;  // below every key of a value
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float d;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+    return d;
+}
+
+// Running statistics: maximum m, s = sum 2^{y}, q = sum 2^{y} y with y = (x - m) log2 e.
+struct Stats {
+    float m, s, q;
+};
+// a and b over the larger of their maxima; empty sides have m = -inf, s = q = 0.
+__device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
+    Stats r;
+    r.m = fmaxf(a.m, b.m);
+    const float m0 = r.m == -INFINITY ? 0.f : r.m;
+    const float da = fmaxf((a.m - m0) * LOG2E, -200.f), db = fmaxf((b.m - m0) * LOG2E, -200.f);
+    const float ca = ex2(da), cb = ex2(db);
+    r.s = a.s * ca + b.s * cb;
+    r.q = ca * (a.q + da * a.s) + cb * (b.q + db * b.s);
+    return r;
+}
+
+// Order of the alternatives: larger value first, then lower index.  Floats compare as the
+// integers of their order (-0 as +0).
+__device__ __forceinline__ int order_key(float v) {
+    const int b = __float_as_int(v + 0.f);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+__device__ __forceinline__ bool better(int ka, int ia, int kb, int ib) { return ka > kb || (ka == kb && ia < ib); }
+
+// A warp's list of its best `top` entries: lane l holds the l-th.
+struct TopList {
+    int key, idx;  // this lane's entry
+    int kth_key, kth_idx;
+    float thr;  // value of the top-th entry (NaN while the list is not full)
+};
+__device__ __forceinline__ void top_init(TopList& L) {
+    L.key = L.kth_key = KEY_NONE;
+    L.idx = L.kth_idx = INT32_MAX;
+    L.thr = __int_as_float(0x7fc00000);
+}
+// Every lane offers one entry (cand false: none); the warp inserts those that belong.
+__device__ __forceinline__ void top_offer(TopList& L, int top, int lane, bool cand, int key, int idx) {
+    unsigned todo = __ballot_sync(0xffffffffu, cand && better(key, idx, L.kth_key, L.kth_idx));
+    while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int k = __shfl_sync(0xffffffffu, key, src), i = __shfl_sync(0xffffffffu, idx, src);
+        const int pk = __shfl_up_sync(0xffffffffu, L.key, 1), pi = __shfl_up_sync(0xffffffffu, L.idx, 1);
+        const bool mine = better(L.key, L.idx, k, i);              // my entry stays ahead of the new one
+        const bool prev = lane > 0 && !better(pk, pi, k, i);       // the one before me moves down to me
+        if (!mine) {
+            L.key = prev ? pk : k;
+            L.idx = prev ? pi : i;
+        }
+        L.kth_key = __shfl_sync(0xffffffffu, L.key, top - 1);
+        L.kth_idx = __shfl_sync(0xffffffffu, L.idx, top - 1);
+        todo &= __ballot_sync(0xffffffffu, better(key, idx, L.kth_key, L.kth_idx));
+    }
+    L.thr = L.kth_key == KEY_NONE ? __int_as_float(0x7fc00000) : key_value(L.kth_key);
+}
+
+constexpr int FWD_THREADS = 256;
+constexpr int FWD_WARPS = FWD_THREADS / 32;
+constexpr int UNROLL = 4;  // 16-byte loads in flight per thread
+
+struct BlockResult {
+    Stats st;
+    int key[LOGPROB_MAX_TOP], idx[LOGPROB_MAX_TOP];
+};
+
+// N values of a thread (masked slots hold -inf) into its statistics.
+template <int N>
+__device__ __forceinline__ float take(Stats& st, const float (&v)[N]) {
+    float mx = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) mx = fmaxf(mx, v[i]);
+    if (mx > st.m) {  // the first values, and then ever more rarely
+        if (st.m != -INFINITY) {
+            const float d = fmaxf((st.m - mx) * LOG2E, -200.f), c = ex2(d);
+            st.q = c * (st.q + d * st.s);
+            st.s *= c;
+        }
+        st.m = mx;
+    }
+    // the difference before the factor log2 e: a maximum of the type's lowest value (a row
+    // masked with it) times log2 e would overflow
+    const float m0 = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float y = max_nan((v[i] - m0) * LOG2E, -200.f);
+        const float e = ex2(y);
+        st.s += e;
+        st.q = fmaf(e, y, st.q);
+    }
+    return mx;
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobParams p, int csize) {
+    constexpr int E = Elem<T>::VEC;
+    constexpr int CH = E * UNROLL;
+    __shared__ Stats wst[FWD_WARPS];
+    __shared__ int wkey[TOP ? FWD_WARPS : 1][LOGPROB_MAX_TOP], widx[TOP ? FWD_WARPS : 1][LOGPROB_MAX_TOP];
+    __shared__ BlockResult res;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long row = blockIdx.x / csize;
+    const int rank = blockIdx.x % csize;
+    const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+
+    // The row from its first 16-byte boundary: `head` elements before it, then whole
+    // vectors, then `tail` elements.  Block `rank` of the cluster takes a run of vectors;
+    // the first block also takes the head, the last one the tail.
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const int head = min(mis ? E - mis : 0, p.vocab);
+    const int nvec = (p.vocab - head) / E;
+    const int tail0 = head + nvec * E;
+    const int per = (nvec + csize - 1) / csize;
+    const int v0 = min(rank * per, nvec), v1 = min(v0 + per, nvec);
+
+    Stats st = {-INFINITY, 0.f, 0.f};
+    TopList L;
+    top_init(L);
+    // at most E - 1 single elements of the head and of the tail, a lane each of warp 0; the
+    // tail comes after the vectors, so that warp 0 too sees its indexes grow
+    auto singles = [&](int c0, int cnt) {
+        const bool in = lane < cnt;
+        const float v[1] = {in ? Elem<T>::load(x[c0 + lane]) : -INFINITY};
+        take<1>(st, v);
+        if (TOP) top_offer(L, p.top, lane, in, order_key(v[0]), c0 + lane);
+    };
+    if (warp == 0 && rank == 0) singles(0, head);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+    for (int base = v0; base < v1; base += FWD_THREADS * UNROLL) {
+        // a warp's UNROLL vectors per lane are one run of 32 * UNROLL vectors, so the indexes
+        // a warp sees grow from turn to turn (an equal value later never displaces)
+        const int wbase = base + warp * 32 * UNROLL + lane;
+        uint4 raw[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            if (wbase + u * 32 < v1) raw[u] = __ldcs(xv + wbase + u * 32);
+        float v[CH];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            if (wbase + u * 32 < v1) {
+                Elem<T>::unpack(raw[u], v + u * E);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[u * E + e] = -INFINITY;
+            }
+        }
+        // slots past the end hold -inf and add 0 to s and q
+        const float mx = take<CH>(st, v);
+        if constexpr (TOP) {
+            // not (mx <= thr): a value above the k-th best, or a list that is not full
+            if (__any_sync(0xffffffffu, !(mx <= L.thr))) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int vec = wbase + (i / E) * 32;
+                    top_offer(L, p.top, lane, vec < v1, order_key(v[i]), head + vec * E + i % E);
+                }
+            }
+        }
+    }
+    if (warp == 0 && rank == csize - 1) singles(tail0, p.vocab - tail0);
+    // the block's result: lanes, then warps, in a fixed order
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stats b;
+        b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+        b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+        b.q = __shfl_xor_sync(0xffffffffu, st.q, o);
+        st = (lane & o) ? join(b, st) : join(st, b);
+    }
+    if (lane == 0) wst[warp] = st;
+    if constexpr (TOP) {
+        if (lane < p.top) {
+            wkey[warp][lane] = L.key;
+            widx[warp][lane] = L.idx;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        st = wst[0];
+        for (int w = 1; w < FWD_WARPS; ++w) st = join(st, wst[w]);
+        if constexpr (TOP) {
+            for (int w = 1; w < FWD_WARPS; ++w) {
+                const bool in = lane < p.top;
+                const int k = in ? wkey[w][lane] : KEY_NONE, i = in ? widx[w][lane] : INT32_MAX;
+                top_offer(L, p.top, lane, in && k != KEY_NONE, k, i);
+            }
+        }
+        if (csize > 1) {
+            if (lane == 0) res.st = st;
+            if (TOP && lane < p.top) {
+                res.key[lane] = L.key;
+                res.idx[lane] = L.idx;
+            }
+        }
+    }
+    __syncwarp();
+    if (csize > 1) {
+        cluster_sync();
+        if (rank == 0 && warp == 0) {
+            for (int r = 1; r < csize; ++r) {
+                const uint32_t a = map_to_rank(&res, r);
+                Stats b;
+                int k = KEY_NONE, i = INT32_MAX;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(a) : "memory");
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(a + 4) : "memory");
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.q) : "r"(a + 8) : "memory");
+                st = join(st, b);
+                if constexpr (TOP) {
+                    const bool in = lane < p.top;
+                    if (in) {
+                        const uint32_t ak = a + offsetof(BlockResult, key) + 4 * lane;
+                        const uint32_t ai = a + offsetof(BlockResult, idx) + 4 * lane;
+                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(k) : "r"(ak) : "memory");
+                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(i) : "r"(ai) : "memory");
+                    }
+                    top_offer(L, p.top, lane, in && k != KEY_NONE, k, i);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no block leaves while its result may still be read
+    }
+    if (rank != 0 || warp != 0) return;
+    const bool none = st.m == -INFINITY && st.s == 0.f;  // no logit above -inf (and no NaN)
+    const float ls = logf(st.s);
+    const float lse = none ? -INFINITY : st.m + ls;
+    if (lane == 0) {
+        if (p.lse) p.lse[row] = lse;
+        if (p.entropy) p.entropy[row] = none ? 0.f : ls - LN2 * (st.q / st.s);
+        if (p.logprob) {
+            const long long t = p.target64 ? static_cast<const long long*>(p.targets)[row]
+                                           : static_cast<const int*>(p.targets)[row];
+            float lp = 0.f;  // a negative target: a position that does not count
+            if (t >= p.vocab) lp = __int_as_float(0x7fc00000);  // no such token
+            else if (t >= 0) lp = none ? -INFINITY : (Elem<T>::load(x[t]) - st.m) - ls;
+            p.logprob[row] = lp;
+        }
+    }
+    if (TOP && lane < p.top) {
+        p.top_index[row * p.top + lane] = L.idx;
+        p.top_logprob[row * p.top + lane] = none ? -INFINITY : (key_value(L.key) - st.m) - ls;
+    }
+}
+
+constexpr int BWD_THREADS = 256;
+
+// What every element of a row needs: u, v, lse, H, the target's column (or -1).
+struct GradRow {
+    float u, v, lse, h;
+    int hit;
+    bool none;
+};
+
+template <typename T, bool ENT>
+__device__ __forceinline__ float grad_of(float x, int col, const GradRow& r) {
+    const float y = max_nan((x - r.lse) * LOG2E, -200.f);
+    const float pr = ex2(y);
+    float d = ENT ? -pr * fmaf(r.v, fmaf(y, LN2, r.h), r.u) : -pr * r.u;
+    if (col == r.hit) d += r.u;
+    return r.none ? 0.f : d;
+}
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobGradParams p, int segs) {
+    constexpr int E = Elem<T>::VEC;
+    const long long row = blockIdx.x / segs;
+    const int seg = blockIdx.x % segs;
+    const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+    T* dx = static_cast<T*>(p.dlogits) + row * p.ldd;
+    GradRow r;
+    r.lse = p.lse[row];
+    r.none = r.lse == -INFINITY;
+    r.u = p.grad_logprob ? p.grad_logprob[row] : 0.f;
+    r.v = ENT ? p.grad_entropy[row] : 0.f;
+    r.h = ENT ? p.entropy[row] : 0.f;
+    r.hit = -1;
+    if (p.grad_logprob) {
+        const long long t = p.target64 ? static_cast<const long long*>(p.targets)[row]
+                                       : static_cast<const int*>(p.targets)[row];
+        if (t < 0) r.u = 0.f;  // its log probability is the constant 0
+        else if (t >= p.vocab) r.u = __int_as_float(0x7fc00000);
+        else r.hit = static_cast<int>(t);
+    }
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+    if (vec) {
+        const int head = min(mis ? E - mis : 0, p.vocab);
+        const int nvec = (p.vocab - head) / E;
+        const int tail0 = head + nvec * E;
+        const int per = (nvec + segs - 1) / segs;
+        const int v0 = min(seg * per, nvec), v1 = min(v0 + per, nvec);
+        if (seg == 0 && threadIdx.x < head)
+            dx[threadIdx.x] = Elem<T>::store(grad_of<T, ENT>(Elem<T>::load(x[threadIdx.x]), threadIdx.x, r));
+        if (seg == segs - 1 && threadIdx.x < p.vocab - tail0) {
+            const int c = tail0 + threadIdx.x;
+            dx[c] = Elem<T>::store(grad_of<T, ENT>(Elem<T>::load(x[c]), c, r));
+        }
+        const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+        uint4* dv = reinterpret_cast<uint4*>(dx + head);
+        for (int base = v0 + threadIdx.x; base < v1; base += BWD_THREADS * UNROLL) {
+            uint4 raw[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+                if (base + u * BWD_THREADS < v1) raw[u] = __ldcs(xv + base + u * BWD_THREADS);
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int i = base + u * BWD_THREADS;
+                if (i < v1) {
+                    float f[E];
+                    Elem<T>::unpack(raw[u], f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) f[e] = grad_of<T, ENT>(f[e], head + i * E + e, r);
+                    __stcs(dv + i, Elem<T>::pack(f));
+                }
+            }
+        }
+    } else {
+        // logits and gradient rows that sit differently to a 16-byte boundary: single elements
+        const int per = (p.vocab + segs - 1) / segs;
+        const int c1 = min((seg + 1) * per, p.vocab);
+        for (int c = seg * per + threadIdx.x; c < c1; c += BWD_THREADS)
+            dx[c] = Elem<T>::store(grad_of<T, ENT>(Elem<T>::load(x[c]), c, r));
+    }
+}
+
+template <typename T, bool TOP>
+cudaError_t run_fwd(const LogprobParams& p, int csize, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = csize;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.rows * csize));
+    cfg.blockDim = dim3(FWD_THREADS);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, logprob_fwd_kernel<T, TOP>, p, csize);
+}
+
+template <typename T>
+cudaError_t run_bwd(const LogprobGradParams& p, int segs, cudaStream_t s) {
+    const unsigned blocks = static_cast<unsigned>(p.rows * segs);
+    if (p.grad_entropy) logprob_bwd_kernel<T, true><<<blocks, BWD_THREADS, 0, s>>>(p, segs);
+    else logprob_bwd_kernel<T, false><<<blocks, BWD_THREADS, 0, s>>>(p, segs);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_logprob_fwd(const LogprobParams& p, int sm_count, cudaStream_t s) {
+    // blocks per row: more where the rows alone do not fill the SMs, as long as a block
+    // still has a full turn of loads (16 KB)
+    const long long bytes = static_cast<long long>(p.vocab) * dtype_size(p.dtype);
+    int csize = 1;
+    while (csize < 8 && p.rows * csize * 2 <= 2 * sm_count && bytes / (csize * 2) >= FWD_THREADS * UNROLL * 16 / 2) csize *= 2;
+    switch (p.dtype) {
+        case DT_F32: return p.top ? run_fwd<float, true>(p, csize, s) : run_fwd<float, false>(p, csize, s);
+        case DT_BF16: return p.top ? run_fwd<__nv_bfloat16, true>(p, csize, s) : run_fwd<__nv_bfloat16, false>(p, csize, s);
+        default: return p.top ? run_fwd<__half, true>(p, csize, s) : run_fwd<__half, false>(p, csize, s);
+    }
+}
+
+int logprob_bwd_segments(int vocab, int dtype) {
+    // whole turns of a block's loads (16 KB)
+    const long long bytes = static_cast<long long>(vocab) * dtype_size(dtype);
+    const long long turn = BWD_THREADS * UNROLL * 16;
+    return static_cast<int>((bytes + turn - 1) / turn);
+}
+
+cudaError_t launch_logprob_bwd(const LogprobGradParams& p, cudaStream_t s) {
+    const int segs = logprob_bwd_segments(p.vocab, p.dtype);
+    switch (p.dtype) {
+        case DT_F32: return run_bwd<float>(p, segs, s);
+        case DT_BF16: return run_bwd<__nv_bfloat16>(p, segs, s);
+        default: return run_bwd<__half>(p, segs, s);
+    }
+}
+
+}  // namespace anvil

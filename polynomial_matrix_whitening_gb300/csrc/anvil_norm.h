@@ -1,0 +1,46 @@
+// anvil_norm.h -- parameter blocks of the layer-norm kernels (internal to libanvil).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace anvil {
+
+struct NormFwdParams {
+    const void* x;        // [rows, width], row stride ldx elements
+    const void* weight;   // [width] or null
+    const void* bias;     // [width] or null
+    void* y;              // [rows, width], row stride ldy
+    float* mean;          // [rows] or null
+    float* rstd;          // [rows] or null
+    long long rows, ldx, ldy;
+    int width;
+    int dtype, weight_dtype;
+    float eps;
+};
+
+struct NormBwdParams {
+    const void* dy;
+    const void* x;
+    const float* mean;
+    const float* rstd;
+    const void* weight;    // or null (1)
+    const void* res;       // gradient added to dx, or null
+    void* dx;
+    float* dweight;        // [width] or null
+    float* dbias;          // [width] or null
+    float* part;           // [blocks][2][width] partial sums (blocks > 1)
+    long long rows, lddy, ldx, ldr, lddx;
+    int width;
+    int dtype, weight_dtype;
+    int blocks;            // of the row pass; 1: it writes dweight and dbias itself
+};
+
+// Blocks of the backward row pass (a function of the sizes and the SM count alone): also
+// the number of partial rows the workspace holds.
+int norm_bwd_blocks(long long rows, int width, int dtype, int sm_count);
+cudaError_t launch_norm_fwd(const NormFwdParams& p, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormBwdParams& p, cudaStream_t stream);
+cudaError_t launch_norm_grads(const NormBwdParams& p, cudaStream_t stream);
+
+}  // namespace anvil

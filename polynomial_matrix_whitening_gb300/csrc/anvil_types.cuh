@@ -1,0 +1,106 @@
+// anvil_types.cuh -- the element types of the training-block operators (fp32, bf16, fp16):
+// conversion to and from fp32 one by one and in 16-byte vectors, and the reductions over a
+// team of threads.  Every sum is held in fp32; a value is rounded to its type once, as it
+// is stored (round to nearest even).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace anvil {
+
+// dtype codes of include/anvil.h (anvil_dtype)
+enum : int { DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2 };
+constexpr int dtype_size(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+    static constexpr int VEC = 4;  // elements in 16 bytes
+    static __device__ __forceinline__ float load(float v) { return v; }
+    static __device__ __forceinline__ float store(float v) { return v; }
+    static __device__ __forceinline__ void unpack(uint4 w, float* f) {
+        f[0] = __uint_as_float(w.x);
+        f[1] = __uint_as_float(w.y);
+        f[2] = __uint_as_float(w.z);
+        f[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr int VEC = 8;
+    static __device__ __forceinline__ float load(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 store(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ void unpack2(uint32_t w, float* f) {
+        f[0] = __uint_as_float(w << 16);
+        f[1] = __uint_as_float(w & 0xffff0000u);
+    }
+    static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+        uint32_t d;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
+    static __device__ __forceinline__ void unpack(uint4 w, float* f) {
+        unpack2(w.x, f);
+        unpack2(w.y, f + 2);
+        unpack2(w.z, f + 4);
+        unpack2(w.w, f + 6);
+    }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    }
+};
+template <>
+struct Elem<__half> {
+    static constexpr int VEC = 8;
+    static __device__ __forceinline__ float load(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half store(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ void unpack2(uint32_t w, float* f) {
+        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        f[0] = r.x;
+        f[1] = r.y;
+    }
+    static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ void unpack(uint4 w, float* f) {
+        unpack2(w.x, f);
+        unpack2(w.y, f + 2);
+        unpack2(w.z, f + 4);
+        unpack2(w.w, f + 6);
+    }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    }
+};
+
+// Streaming 16-byte load (read once) and store (not read again soon).
+__device__ __forceinline__ uint4 ldg_stream(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ void stg_stream(void* p, uint4 v) { __stcs(reinterpret_cast<uint4*>(p), v); }
+
+// Sum over a team of TPR consecutive threads (8 or 32: inside a warp; more: the whole
+// block, through `red`, one float per warp).  Every thread of the team gets the same sum,
+// in an order fixed by the thread numbers.  `red` may be reused after the next
+// team_sum (its leading barrier) -- callers alternate two arrays.
+template <int TPR>
+__device__ __forceinline__ float team_sum(float v, float* red) {
+    constexpr int W = TPR < 32 ? TPR : 32;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 32; ++w) v += red[w];
+    }
+    return v;
+}
+
+}  // namespace anvil
