@@ -132,14 +132,14 @@ Stored with_copy(const Stored& s, void* copy) {
     return r;
 }
 
-anvil_status encode(CUtensorMap* map, int es, bool f16, const void* base, int64_t inner, int64_t outer, int64_t ld,
-                    int64_t planes, int64_t plane_stride, int box0, int box1) {
+// Tensor map of a row-major matrix [outer][inner], boxes of box1 rows by box0 elements
+// (128 bytes, 128-byte swizzle).  A third dimension of one, for the 3-D copies.
+anvil_status encode(CUtensorMap* map, int es, bool f16, const void* base, int64_t inner, int64_t outer, int64_t ld, int box0,
+                    int box1) {
     // a row stride is only used where there are several rows; keep it a multiple of 16 bytes
     const int64_t ldb = outer > 1 ? ld * es : (inner * es + 15) / 16 * 16;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
-                                static_cast<cuuint64_t>(planes)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldb),
-                                   static_cast<cuuint64_t>(planes > 1 ? plane_stride * es : ldb)};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer), 1};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldb), static_cast<cuuint64_t>(ldb)};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUtensorMapDataType type = es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -167,21 +167,22 @@ struct Product {
     int64_t k;
     bool f16;
     GemmEpilogue epi;
-    float* part;  // split products' scratch (from plan)
+    float* part;  // scratch of the tail tiles' parts
 };
 
 // How a product runs.
 struct Plan {
     bool few;      // row_gemm_kernel
-    int bn;        // output columns of a pair's tile, or B rows of a block
-    int splits;    // of the contraction
+    int bn;        // few: B rows of a block
+    int whole;     // tiles in one piece (the others are split along k)
+    int splits;    // of a tail tile, or of the contraction (few)
     int kb;        // k-blocks per split
-    size_t part;   // bytes of split partial products
+    size_t part;   // bytes of the tail tiles' parts
 };
 
 constexpr int FEW_ROWS = 128;
 
-Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32, bool may_split) {
+Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32) {
     Plan p = {};
     const int64_t kb = (k + GEMM_BK - 1) / GEMM_BK;
     if (rows <= FEW_ROWS && !a_mn && !out_f32) {
@@ -197,28 +198,31 @@ Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32, bo
         p.kb = static_cast<int>((kb + p.splits - 1) / p.splits);
         return p;
     }
-    // The tile width and the number of splits with the least estimated time, in SM cycles:
-    // whole turns of the grid's pairs, each its k-blocks and a fixed cost for filling the
-    // pipeline and the epilogue, and for splits a pass over their partial products.
+    // Whole turns of the grid's pairs go over tiles in one piece; the tiles left over for a
+    // turn that would not be full are split, if the turn's time saved is more than the parts'
+    // way through memory.  Times in SM cycles: 560 for a k-block, 2500 for filling the
+    // pipeline and the epilogue of a unit, the parts written and read at 2600 bytes a cycle,
+    // 6000 for the second kernel.
     const int64_t pairs = PLAN_SMS / 2;
-    double best = 0;
-    for (int bn = 256; bn >= 128; bn -= 128) {
-        const int64_t tiles = ((rows + PAIR_ROWS - 1) / PAIR_ROWS) * ((cols + bn - 1) / bn);
-        for (int s = 1; s <= (may_split ? 64 : 1); ++s) {
-            const int64_t per = (kb + s - 1) / s;
-            if (s > 1 && (per * (s - 1) >= kb || per < 8 || tiles * s > 4 * pairs)) continue;
-            const double turns = static_cast<double>((tiles * s + pairs - 1) / pairs);
-            double cost = turns * (per * (bn == 256 ? 560.0 : 360.0) + (bn == 256 ? 2500.0 : 1800.0));
-            if (s > 1) cost += 5000.0 + static_cast<double>(rows) * cols * 8.0 * s / 2600.0;
-            if (best == 0 || cost < best) {
-                best = cost;
-                p.bn = bn;
-                p.splits = s;
-                p.kb = static_cast<int>(per);
-            }
+    const int64_t tiles = ((rows + PAIR_ROWS - 1) / PAIR_ROWS) * ((cols + PAIR_COLS - 1) / PAIR_COLS);
+    const int64_t tail = tiles % pairs;
+    p.whole = static_cast<int>(tiles);
+    p.splits = 1;
+    p.kb = static_cast<int>(kb);
+    double best = kb * 560.0 + 2500.0;  // the last turn in one piece
+    for (int64_t s = 2; tail && s <= 64 && s <= kb; ++s) {
+        const int64_t per = (kb + s - 1) / s;
+        if (per * (s - 1) >= kb) continue;  // every split has work
+        const int64_t turns = (tail * s + pairs - 1) / pairs;
+        const double cost = turns * (per * 560.0 + 2500.0) + 6000.0 + tail * s * (2.0 * 4 * PAIR_ROWS * PAIR_COLS / 2600.0);
+        if (cost < best) {
+            best = cost;
+            p.whole = static_cast<int>(tiles - tail);
+            p.splits = static_cast<int>(s);
+            p.kb = static_cast<int>(per);
+            p.part = static_cast<size_t>(tail * s) * 4 * PAIR_ROWS * PAIR_COLS;
         }
     }
-    if (p.splits > 1) p.part = align256(4 * static_cast<size_t>(p.splits) * rows * ((cols + 3) & ~3));
     return p;
 }
 
@@ -229,8 +233,8 @@ anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, c
         RowGemmParams g;
         memset(&g, 0, sizeof(g));
         // the output's columns run along B's rows: B is the M side of the MMA
-        if ((st = encode(&g.tm_a, 2, q.f16, q.b.p, q.b.cols, q.b.rows, q.b.ld, 1, 0, 64, q.b_mn ? 64 : ROW_TILE_A))) return st;
-        if ((st = encode(&g.tm_b, 2, q.f16, q.a.p, q.a.cols, q.a.rows, q.a.ld, 1, 0, 64, plan.bn))) return st;
+        if ((st = encode(&g.tm_a, 2, q.f16, q.b.p, q.b.cols, q.b.rows, q.b.ld, 64, q.b_mn ? 64 : ROW_TILE_A))) return st;
+        if ((st = encode(&g.tm_b, 2, q.f16, q.a.p, q.a.cols, q.a.rows, q.a.ld, 64, plan.bn))) return st;
         g.epi = q.epi;
         g.na = q.cols;
         g.nb = static_cast<int>(q.rows);
@@ -245,8 +249,8 @@ anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, c
     }
     PairGemmParams g;
     memset(&g, 0, sizeof(g));
-    if ((st = encode(&g.tm_a, 2, q.f16, q.a.p, q.a.cols, q.a.rows, q.a.ld, 1, 0, 64, q.a_mn ? 64 : 128))) return st;
-    if ((st = encode(&g.tm_b, 2, q.f16, q.b.p, q.b.cols, q.b.rows, q.b.ld, 1, 0, 64, q.b_mn ? 64 : plan.bn / 2))) return st;
+    if ((st = encode(&g.tm_a, 2, q.f16, q.a.p, q.a.cols, q.a.rows, q.a.ld, 64, q.a_mn ? 64 : 128))) return st;
+    if ((st = encode(&g.tm_b, 2, q.f16, q.b.p, q.b.cols, q.b.rows, q.b.ld, 64, q.b_mn ? 64 : PAIR_COLS / 2))) return st;
     g.epi = q.epi;
     g.rows = static_cast<int>(q.rows);
     g.cols = q.cols;
@@ -255,45 +259,41 @@ anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, c
     g.b_mn = q.b_mn;
     g.f16 = q.f16;
     g.tiles_r = static_cast<int>((q.rows + PAIR_ROWS - 1) / PAIR_ROWS);
-    g.tiles_c = (q.cols + plan.bn - 1) / plan.bn;
+    g.tiles_c = (q.cols + PAIR_COLS - 1) / PAIR_COLS;
+    g.whole = plan.whole;
     g.splits = plan.splits;
+    const int tail = g.tiles_r * g.tiles_c - plan.whole;
+    g.units = plan.whole + tail * plan.splits;
     g.kb_per_split = plan.kb;
     g.err = dev->err;
     const GemmEpilogue& ep = q.epi;
     const int es = ep.out_f32 ? 4 : 2;
-    const int64_t ldp = (q.cols + 3) & ~3;
-    if (plan.splits > 1) {
-        // fp32 partial products; the epilogue moves to split_sum_kernel
-        memset(&g.epi, 0, sizeof(g.epi));
-        g.epi.out_f32 = 1;
-        if ((st = encode(&g.tm_out, 4, false, q.part, q.cols, q.rows, ldp, plan.splits, ldp * q.rows, 32, 128))) return st;
-    } else {
-        g.out_tma = aligned16(ep.out, ep.ldout, es, q.rows);
-        g.in_tma = ep.in && aligned16(ep.in, ep.ldin, es, q.rows);
-        g.z_tma = ep.z && aligned16(ep.z, ep.ldz, es, q.rows);
-        const int box = 128 / es;
-        if (g.out_tma && (st = encode(&g.tm_out, es, q.f16, ep.out, q.cols, q.rows, ep.ldout, 1, 0, box, 128))) return st;
-        if (g.in_tma && (st = encode(&g.tm_in, es, q.f16, ep.in, q.cols, q.rows, ep.ldin, 1, 0, box, 128))) return st;
-        if (g.z_tma && (st = encode(&g.tm_z, es, q.f16, ep.z, q.cols, q.rows, ep.ldz, 1, 0, box, 128))) return st;
-    }
-    e = profiled(ANVIL_KERNEL_LINEAR_PRODUCT, s, [&] { return launch_pair_gemm(g, plan.bn, dev->sm_count, s); });
+    const int box = 128 / es;
+    g.out_tma = aligned16(ep.out, ep.ldout, es, q.rows);
+    g.in_tma = ep.in && aligned16(ep.in, ep.ldin, es, q.rows);
+    g.z_tma = ep.z && aligned16(ep.z, ep.ldz, es, q.rows);
+    if (g.out_tma && (st = encode(&g.tm_out, es, q.f16, ep.out, q.cols, q.rows, ep.ldout, box, 128))) return st;
+    if (g.in_tma && (st = encode(&g.tm_in, es, q.f16, ep.in, q.cols, q.rows, ep.ldin, box, 128))) return st;
+    if (g.z_tma && (st = encode(&g.tm_z, es, q.f16, ep.z, q.cols, q.rows, ep.ldz, box, 128))) return st;
+    if (tail && (st = encode(&g.tm_part, 4, false, q.part, PAIR_COLS, static_cast<int64_t>(tail) * plan.splits * PAIR_ROWS,
+                             PAIR_COLS, 32, 128)))
+        return st;
+    e = profiled(ANVIL_KERNEL_LINEAR_PRODUCT, s, [&] { return launch_pair_gemm(g, dev->sm_count, s); });
     if (e) return cuda_fail(e, "linear product launch");
-    if (plan.splits > 1) {
-        SplitSumParams t;
+    if (tail) {
+        TailSumParams t;
         memset(&t, 0, sizeof(t));
+        t.epi = ep;
         t.part = q.part;
-        t.in = ep.in;
-        t.out = ep.out;
-        t.ld_part = ldp;
-        t.ldin = ep.ldin;
-        t.ldout = ep.ldout;
-        t.rows = static_cast<int>(q.rows);
-        t.cols = q.cols;
+        t.rows = g.rows;
+        t.cols = g.cols;
+        t.tiles_r = g.tiles_r;
+        t.tiles_c = g.tiles_c;
+        t.whole = plan.whole;
         t.splits = plan.splits;
-        t.out_f32 = ep.out_f32;
         t.f16 = q.f16;
-        e = profiled(ANVIL_KERNEL_LINEAR_SUM, s, [&] { return launch_split_sum(t, s); });
-        if (e) return cuda_fail(e, "split sum launch");
+        e = profiled(ANVIL_KERNEL_LINEAR_SUM, s, [&] { return launch_tail_sum(t, s); });
+        if (e) return cuda_fail(e, "split product sum launch");
     }
     return ANVIL_OK;
 }
@@ -317,7 +317,8 @@ Stored stored_weight(const void* w, int n, int k, int64_t ldw, bool transposed) 
 
 struct LinearLayout {
     Stored x, w;
-    size_t off_x, off_w, total;
+    Plan plan;
+    size_t off_x, off_w, off_part, total;
 };
 LinearLayout linear_layout(const anvil_linear_desc* d) {
     LinearLayout L;
@@ -325,7 +326,9 @@ LinearLayout linear_layout(const anvil_linear_desc* d) {
     L.w = stored_weight(d->weight, d->n, d->k, d->ldw, d->weight_transposed != 0);
     L.off_x = 0;
     L.off_w = L.off_x + copy_bytes(L.x);
-    L.total = L.off_w + copy_bytes(L.w);
+    L.off_part = L.off_w + copy_bytes(L.w);
+    L.plan = plan_product(d->rows, d->n, d->k, false, false);
+    L.total = L.off_part + L.plan.part;
     return L;
 }
 
@@ -384,12 +387,10 @@ LinearGradLayout linear_grad_layout(const anvil_linear_grad_desc* d) {
         if (d->dbias) at += align256(sizeof(float) * static_cast<size_t>(L.blocks_r) * d->n);
     }
     L.off_part = at;
-    if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, false, false, false);
-    if (d->dweight) {
-        L.pdw = plan_product(tr ? d->k : d->n, tr ? d->n : d->k, d->rows, true, d->dweight_dtype == ANVIL_F32, true);
-        at += L.pdw.part;
-    }
-    L.total = at;
+    // the two products run one after the other: they share the scratch of their parts
+    if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, false, false);
+    if (d->dweight) L.pdw = plan_product(tr ? d->k : d->n, tr ? d->n : d->k, d->rows, true, d->dweight_dtype == ANVIL_F32);
+    L.total = at + (L.pdx.part > L.pdw.part ? L.pdx.part : L.pdw.part);
     return L;
 }
 
@@ -572,7 +573,8 @@ anvil_status anvil_linear_forward(const anvil_linear_desc* d, void* workspace, s
     q.epi.ldz = d->ldz;
     q.epi.out = d->y;
     q.epi.ldout = d->ldy;
-    return run_product(q, plan_product(d->rows, d->n, d->k, false, false, false), dev, s);
+    q.part = reinterpret_cast<float*>(ws + L.off_part);
+    return run_product(q, L.plan, dev, s);
 }
 
 size_t anvil_linear_backward_workspace_bytes(const anvil_linear_grad_desc* d) {
@@ -651,6 +653,7 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
         q.f16 = f16;
         q.epi.out = d->dx;
         q.epi.ldout = d->lddx;
+        q.part = reinterpret_cast<float*>(ws + L.off_part);
         if ((st = run_product(q, L.pdx, dev, s)) != ANVIL_OK) return st;
     }
     if (d->dweight) {

@@ -8,13 +8,22 @@
 //
 // Two kernels share the work.
 //
-// pair_gemm_kernel: clusters of two CTAs compute 256 x BN output tiles (BN = 256 or 128)
-// with tcgen05.mma.cta_group::2; CTA rank r loads rows 128r.. of the tile's A operand and
-// columns BN/2 r.. of its B operand by TMA into a ring of stages, and holds output rows
+// pair_gemm_kernel: clusters of two CTAs compute 256 x 256 output tiles with
+// tcgen05.mma.cta_group::2; CTA rank r loads rows 128r.. of the tile's A operand and
+// columns 128r.. of its B operand by TMA into a ring of five stages, and holds output rows
 // 128r.. in its TMEM.  Two accumulators alternate, so a tile's epilogue overlaps the next
 // tile's products.  Operands are taken in the order they are stored: K-major, or MN-major
 // as 64 x 64 boxes, so no operand is ever transposed in memory.  The grid is persistent
-// (one pair per two SMs), its tiles in groups of eight rows of tiles for the L2.
+// (one pair per two SMs), its tiles in groups of eight rows of tiles for the L2.  Tiles
+// that would leave the last turn of the grid partly idle (or all of them, where they are
+// few) are split along the contraction: the parts go to scratch in fp32 and
+// tail_sum_kernel adds them up, in order, and finishes the elements.
+// What bounds it: at 16384 x 4096 x 4096 the products, within a few percent of the
+// library's own rate; a tile narrower than 256 columns gains nothing (128 columns measured
+// 660 SM cycles per 64-deep k-block against 560: a k-block's time is the L2 round trip of
+// the stages in flight, not its bytes).  For short contractions the epilogue: the tensor
+// pipe already takes about 96 of the 128 bytes per clock that shared memory gives, so every
+// staged byte and every load instruction of the epilogue delays the products.
 // fp32 results: the tensor cores add with truncation, a bias that grows with the length
 // of the chain (about 1e-9 of the result per 16-deep step), so the product is taken in
 // chains of 512 and the epilogue adds the chains up in registers, rounding to nearest.
@@ -56,87 +65,140 @@ __host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool a_mn, bool b_
            ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
-__device__ __forceinline__ float act_value(int act, float z) {
-    switch (act) {
-        case ACT_RELU: return z < 0.f ? 0.f : z;
-        case ACT_RELU2: return z < 0.f ? 0.f : z * z;
-        case ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-        case ACT_GELU_TANH: {
-            const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);  // 2 sqrt(2/pi) (...)
-            return __fdividef(z, 1.f + __expf(-u2));                              // z (1 + tanh(u2 / 2)) / 2
-        }
-        case ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
-        default: return z;
-    }
+// Phi(z), the normal distribution, and e = exp(-z^2/2): the complementary error function by
+// Hastings' rational approximation (Abramowitz and Stegun 7.1.26, |error| <= 1.5e-7 in
+// erf), the tail taken directly so that Phi keeps its relative accuracy far below zero.
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+    const float a = fabsf(z) * 0.70710678118654752f;
+    const float t = __fdividef(1.f, fmaf(0.3275911f, a, 1.f));
+    float q = fmaf(t, 1.061405429f, -1.453152027f);
+    q = fmaf(t, q, 1.421413741f);
+    q = fmaf(t, q, -0.284496736f);
+    q = fmaf(t, q, 0.254829592f);
+    *e = __expf(-a * a);
+    const float tail = 0.5f * t * q * *e;
+    return z < 0.f ? tail : 1.f - tail;
 }
-__device__ __forceinline__ float act_slope(int act, float z) {
-    switch (act) {
-        case ACT_RELU: return z > 0.f ? 1.f : 0.f;
-        case ACT_RELU2: return z < 0.f ? 0.f : 2.f * z;
-        case ACT_GELU:
-            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
-        case ACT_GELU_TANH: {
-            const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
-            const float du2 = 1.5957691216057308f * (1.f + 0.134145f * z * z);
-            const float s = 1.f / (1.f + __expf(-u2));
-            return s + z * s * (1.f - s) * du2;
-        }
-        case ACT_SILU: {
-            const float s = 1.f / (1.f + __expf(-z));
-            return s * (1.f + z * (1.f - s));
-        }
-        default: return 1.f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == ACT_RELU) return z < 0.f ? 0.f : z;
+    if constexpr (ACT == ACT_RELU2) return z < 0.f ? 0.f : z * z;
+    if constexpr (ACT == ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, &e);
     }
+    if constexpr (ACT == ACT_GELU_TANH) {
+        const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);  // 2 sqrt(2/pi) (...)
+        return __fdividef(z, 1.f + __expf(-u2));                              // z (1 + tanh(u2 / 2)) / 2
+    }
+    if constexpr (ACT == ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if constexpr (ACT == ACT_RELU2) return z < 0.f ? 0.f : 2.f * z;
+    if constexpr (ACT == ACT_GELU) {
+        float e;
+        const float c = normal_cdf(z, &e);
+        return fmaf(z * 0.3989422804014327f, e, c);
+    }
+    if constexpr (ACT == ACT_GELU_TANH) {
+        const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
+        const float du2 = 1.5957691216057308f * (1.f + 0.134145f * z * z);
+        const float s = __fdividef(1.f, 1.f + __expf(-u2));
+        return s + z * s * (1.f - s) * du2;
+    }
+    if constexpr (ACT == ACT_SILU) {
+        const float s = __fdividef(1.f, 1.f + __expf(-z));
+        return s * (1.f + z * (1.f - s));
+    }
+    return 1.f;
 }
 // The activation of N values, the choice made once.
 template <int N>
 __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
+#define ANVIL_ACT_CASE(A)                                         \
+    case A:                                                       \
+        _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = act_value<A>(v[i]); \
+        break
     switch (act) {
-        case ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_RELU, v[i]);
-            break;
-        case ACT_RELU2:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_RELU2, v[i]);
-            break;
-        case ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_GELU, v[i]);
-            break;
-        case ACT_GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_GELU_TANH, v[i]);
-            break;
-        case ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value(ACT_SILU, v[i]);
-            break;
+        ANVIL_ACT_CASE(ACT_RELU);
+        ANVIL_ACT_CASE(ACT_RELU2);
+        ANVIL_ACT_CASE(ACT_GELU);
+        ANVIL_ACT_CASE(ACT_GELU_TANH);
+        ANVIL_ACT_CASE(ACT_SILU);
         default: break;
+    }
+#undef ANVIL_ACT_CASE
+}
+
+// N bias values from column col0 (those at `cols` and beyond read as 0) added to v.
+template <typename T, int N>
+__device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int cols, float (&v)[N]) {
+    const bool vec = col0 + N <= cols && !(reinterpret_cast<uintptr_t>(e.bias) & 15);
+    if (e.bias_f32) {
+        const float* b = static_cast<const float*>(e.bias) + col0;
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(b + i));
+                v[i] += f.x;
+                v[i + 1] += f.y;
+                v[i + 2] += f.z;
+                v[i + 3] += f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += col0 + i < cols ? __ldg(b + i) : 0.f;
+        }
+    } else {
+        const T* b = static_cast<const T*>(e.bias) + col0;
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < N; i += 8) {
+                float f[8];
+                Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(b + i)), f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[i + k] += f[k];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += col0 + i < cols ? Elem<T>::load(b[i]) : 0.f;
+        }
     }
 }
 
 // ---------------------------------------------------------------- the pair kernel
-template <int BN>
-struct PairShape {
-    static constexpr int B_STAGE = BN / 2 * 128;
-    static constexpr int STAGE = A_STAGE + B_STAGE;
-    static constexpr int STAGES = BN == 256 ? 5 : 6;
-    static constexpr int BOXES = 2 * EPI_GROUPS;
-    static constexpr int SMEM = STAGES * STAGE + BOXES * QBOX + 1024;  // + alignment slack
-    static constexpr uint32_t TMEM_COLS = 2 * BN;
-};
+constexpr int BN = PAIR_COLS;
+constexpr int B_STAGE = BN / 2 * 128;  // 16 KB: this CTA's half of the B columns of a k-block
+constexpr int STAGE = A_STAGE + B_STAGE;
+constexpr int STAGES = 5;
+constexpr int BOXES = 2 * EPI_GROUPS;
+constexpr int PAIR_SMEM = STAGES * STAGE + BOXES * QBOX + 1024;  // + alignment slack
+constexpr uint32_t PAIR_TMEM = 2 * BN;
 
-// Work unit u -> tile row, tile column, split.  Groups of RASTER_ROWS rows of tiles, column
-// by column inside a group, so that the pairs running at one time share operand panels.
+// Work unit u: a whole tile, or a split of a tail tile (part: its place in the scratch).
+// Tiles go in groups of RASTER_ROWS rows of tiles, column by column inside a group, so that
+// the pairs running at one time share operand panels.
 struct Unit {
-    int tr, tc, split;
+    int tr, tc, part, kb0, nkb;
 };
 __device__ __forceinline__ Unit unit_of(const PairGemmParams& p, int u) {
-    const int tiles = p.tiles_r * p.tiles_c;
     Unit r;
-    r.split = u / tiles;
-    const int t = u - r.split * tiles;
+    const int all = (p.k + GEMM_BK - 1) / GEMM_BK;
+    int t = u;
+    r.part = -1;
+    r.kb0 = 0;
+    r.nkb = all;
+    if (u >= p.whole) {
+        r.part = u - p.whole;
+        const int q = r.part / p.splits;
+        t = p.whole + q;
+        r.kb0 = (r.part - q * p.splits) * p.kb_per_split;
+        r.nkb = max(0, min(p.kb_per_split, all - r.kb0));
+    }
     const int per = RASTER_ROWS * p.tiles_c;
     const int g = t / per;
     const int rows = min(RASTER_ROWS, p.tiles_r - g * RASTER_ROWS);
@@ -145,11 +207,6 @@ __device__ __forceinline__ Unit unit_of(const PairGemmParams& p, int u) {
     r.tr = g * RASTER_ROWS + (q - r.tc * rows);
     return r;
 }
-__device__ __forceinline__ void unit_kblocks(const PairGemmParams& p, const Unit& u, int* kb0, int* nkb) {
-    const int all = (p.k + GEMM_BK - 1) / GEMM_BK;
-    *kb0 = u.split * p.kb_per_split;
-    *nkb = max(0, min(p.kb_per_split, all - *kb0));
-}
 
 // A staging box: 128 rows of 128 bytes, 16-byte chunk j of row r at chunk j ^ (r % 8).
 __device__ __forceinline__ uint32_t box_addr(uint32_t box, int r, int j) {
@@ -157,55 +214,61 @@ __device__ __forceinline__ uint32_t box_addr(uint32_t box, int r, int j) {
 }
 
 // Rows that TMA cannot take (not 16-byte aligned): the 32 box rows of this warp to or from
-// global memory, one row at a time, neighbouring lanes on neighbouring elements.
+// global memory, neighbouring lanes on neighbouring elements, eight rows in flight.
 template <typename E>
 __device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, int row0, int col0, int rows, int cols,
                                             int quad, int lane) {
-    constexpr int N = 128 / sizeof(E);  // elements per box row
-    for (int i = 0; i < 32; ++i) {
-        const int r = quad * 32 + i;
-        if (row0 + r >= rows) break;
+    constexpr int H = 128 / sizeof(E) / 32;  // elements per lane of a box row
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32; i0 += 8) {
+        E v[8][H];
 #pragma unroll
-        for (int h = 0; h < N / 32; ++h) {
-            const int c = h * 32 + lane;
-            if (col0 + c < cols) {
-                const uint32_t a = box_addr(box, r, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
-                E v;
-                if constexpr (sizeof(E) == 2) {
-                    uint16_t b;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(a) : "memory");
-                    v = b;
-                } else {
-                    uint32_t b;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b) : "r"(a) : "memory");
-                    v = b;
-                }
-                dst[static_cast<size_t>(row0 + r) * ld + col0 + c] = v;
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int c = h * 32 + lane;
+                const uint32_t a = box_addr(box, quad * 32 + i0 + i, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
+                if constexpr (sizeof(E) == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[i][h]) : "r"(a) : "memory");
+                else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[i][h]) : "r"(a) : "memory");
             }
-        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int r = row0 + quad * 32 + i0 + i, c = col0 + h * 32 + lane;
+                if (r < rows && c < cols) dst[static_cast<size_t>(r) * ld + c] = v[i][h];
+            }
     }
 }
 template <typename E>
 __device__ __forceinline__ void rows_to_box(uint32_t box, const E* src, long long ld, int row0, int col0, int rows,
                                             int cols, int quad, int lane) {
-    constexpr int N = 128 / sizeof(E);
-    for (int i = 0; i < 32; ++i) {
-        const int r = quad * 32 + i;
-        if (row0 + r >= rows) break;
+    constexpr int H = 128 / sizeof(E) / 32;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32; i0 += 8) {
+        E v[8][H];
 #pragma unroll
-        for (int h = 0; h < N / 32; ++h) {
-            const int c = h * 32 + lane;
-            if (col0 + c < cols) {
-                const uint32_t a = box_addr(box, r, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
-                const E v = src[static_cast<size_t>(row0 + r) * ld + col0 + c];
-                if constexpr (sizeof(E) == 2) sts16(a, v);
-                else asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int r = row0 + quad * 32 + i0 + i, c = col0 + h * 32 + lane;
+                v[i][h] = r < rows && c < cols ? src[static_cast<size_t>(r) * ld + c] : E(0);
             }
-        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int c = h * 32 + lane;
+                const uint32_t a = box_addr(box, quad * 32 + i0 + i, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
+                if constexpr (sizeof(E) == 2) sts16(a, v[i][h]);
+                else asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v[i][h]) : "memory");
+            }
     }
 }
 
-// Per-thread epilogue state of one group (128 threads, two staging boxes).
+// Per-thread epilogue state of one group (128 threads, two staging boxes).  The group's
+// stores alternate between its boxes, one commit group each, so a box is free again once
+// all but the latest store have been read.
 struct EpiState {
     uint32_t boxes;      // shared address of the group's two boxes
     uint64_t* in_bar;    // the group's two input-load barriers
@@ -215,27 +278,33 @@ struct EpiState {
     int loads[2];        // input loads armed per box (parity of the barrier)
 };
 
+__device__ __forceinline__ void box_free(const EpiState& x) {
+    if (x.leader) bulk_wait_read_but_one();
+    named_barrier_sync(1 + x.grp, 128);
+}
+
+__device__ __forceinline__ void tma_store_box(const CUtensorMap* tm, uint32_t box, int col, int row) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm), "r"(box),
+                 "r"(col), "r"(row), "r"(0)
+                 : "memory");
+}
+
 // Sends one box of results out: by TMA (the group's leader, after every thread's writes),
-// or row by row by the warps themselves.
+// or by the warps themselves, each its own rows.
 template <typename E>
 __device__ __forceinline__ void send_box(const EpiState& x, const CUtensorMap* tm, int by_tma, uint32_t box, void* dst,
                                          long long ld, int row0, int col0, int rows, int cols) {
     if (by_tma) {
         fence_proxy_async_smem();
         named_barrier_sync(1 + x.grp, 128);
-        if (x.leader) {
-            if (row0 < rows && col0 < cols)
-                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
-                             "r"(box), "r"(col0), "r"(row0), "r"(0)
-                             : "memory");
-            bulk_commit_group();
-        }
+        if (x.leader && row0 < rows && col0 < cols) tma_store_box(tm, box, col0, row0);
     } else {
         __syncwarp();
         box_to_rows<E>(box, static_cast<E*>(dst), ld, row0, col0, rows, cols, x.quad, x.lane);
         fence_proxy_async_smem();  // before an input load into this box
         __syncwarp();
     }
+    if (x.leader) bulk_commit_group();
 }
 
 __device__ __forceinline__ void arm_input(EpiState& x, const CUtensorMap* tm, int b, int col0, int row0) {
@@ -249,146 +318,115 @@ __device__ __forceinline__ void arm_input(EpiState& x, const CUtensorMap* tm, in
     }
     ++x.loads[b];
 }
-
-// 32 bias values (those past `cols` read as 0).
-template <typename T>
-__device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int cols, float (&v)[32]) {
-    if (e.bias_f32) {
-        const float* b = static_cast<const float*>(e.bias);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += col0 + i < cols ? __ldg(b + col0 + i) : 0.f;
-    } else {
-        const T* b = static_cast<const T*>(e.bias);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += col0 + i < cols ? Elem<T>::load(b[col0 + i]) : 0.f;
-    }
+__device__ __forceinline__ void wait_input(EpiState& x, int b, unsigned* err) {
+    if (!mbar_wait(&x.in_bar[b], static_cast<uint32_t>(x.loads[b] - 1) & 1u, err)) x.fail = true;
 }
 
+// The accumulator is read: its next products may start.
+__device__ __forceinline__ void release_acc(const EpiState& x, uint32_t tempty) {
+    tc_fence_before();
+    __syncwarp();
+    if (x.lane == 0) mbar_arrive_cluster(tempty);
+}
+
+// Whether a whole 16-bit tile's residual comes by TMA (into the result's boxes, ahead of
+// the accumulator): not where z takes one of the two boxes.
+__device__ __forceinline__ bool early_input(const PairGemmParams& p) { return p.epi.in && p.in_tma && !p.epi.z; }
+
 // The 16-bit epilogue of this group's half of a tile, 64 columns (one box row) at a time.
-template <typename T, int BN>
+template <typename T>
 __device__ __forceinline__ void epilogue_16(const PairGemmParams& p, EpiState& x, uint32_t tacc, uint32_t tempty, int row0,
                                             int col0) {
     constexpr int PIECES = BN / 2 / 64;
     const GemmEpilogue& e = p.epi;
-    const bool in_tma = e.in && p.in_tma && !e.z;
-    if (in_tma && x.leader) bulk_wait_read_all();  // the boxes' earlier stores have been read
-    if (in_tma) {
-        for (int q = 0; q < PIECES; ++q) arm_input(x, &p.tm_in, q & 1, col0 + 64 * q, row0);
-    }
+    const bool early = early_input(p);
 #pragma unroll 1
     for (int q = 0; q < PIECES; ++q) {
         const int pc = col0 + 64 * q;
         // z leaves through box 0 and y through box 1 where both are stored
         const int yb = e.z ? 1 : q & 1;
         const uint32_t ybox = x.boxes + yb * QBOX, zbox = x.boxes;
-        if (in_tma) {
-            if (!mbar_wait(&x.in_bar[yb], static_cast<uint32_t>(x.loads[yb] - 1) & 1u, p.err)) x.fail = true;
-        } else {
-            if (x.leader) bulk_wait_read_all();
-            named_barrier_sync(1 + x.grp, 128);
-            if (e.in) {
-                rows_to_box<uint16_t>(ybox, static_cast<const uint16_t*>(e.in), e.ldin, row0, pc, p.rows, p.cols, x.quad,
-                                      x.lane);
-                __syncwarp();
-            }
+        float v[64];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_ld_32x32b_x32(tacc + q * 64 + h * 32, reinterpret_cast<float(&)[32]>(v[32 * h]));
+        if (q == PIECES - 1) release_acc(x, tempty);
+        if (e.bias) add_bias<T, 64>(e, pc, p.cols, v);
+        if (e.z) {
+            box_free(x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sts128(box_addr(zbox, x.r, j), Elem<T>::pack(v + 8 * j));
+            send_box<uint16_t>(x, &p.tm_z, p.z_tma, zbox, e.z, e.ldz, row0, pc, p.rows, p.cols);
         }
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            float v[32];
-            tmem_ld_32x32b_x32(tacc + q * 64 + h * 32, v);
-            if (e.bias) add_bias<T>(e, pc + h * 32, p.cols, v);
-            if (e.z) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sts128(box_addr(zbox, x.r, h * 4 + j), Elem<T>::pack(v + 8 * j));
-            }
-            act_values<32>(e.act, v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t a = box_addr(ybox, x.r, h * 4 + j);
-                if (e.in) {
-                    float f[8];
-                    Elem<T>::unpack(lds128(a), f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];
-                }
-                sts128(a, Elem<T>::pack(v + 8 * j));
-            }
-        }
-        if (q == PIECES - 1) {
-            tc_fence_before();
+        act_values<64>(e.act, v);
+        if (early) wait_input(x, yb, p.err);
+        else box_free(x);
+        if (e.in && !early) {
+            rows_to_box<uint16_t>(ybox, static_cast<const uint16_t*>(e.in), e.ldin, row0, pc, p.rows, p.cols, x.quad, x.lane);
             __syncwarp();
-            if (x.lane == 0) mbar_arrive_cluster(tempty);  // the accumulator is read
         }
-        if (e.z) send_box<uint16_t>(x, &p.tm_z, p.z_tma, zbox, e.z, e.ldz, row0, pc, p.rows, p.cols);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t a = box_addr(ybox, x.r, j);
+            if (e.in) {
+                float f[8];
+                Elem<T>::unpack(lds128(a), f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];
+            }
+            sts128(a, Elem<T>::pack(v + 8 * j));
+        }
         send_box<uint16_t>(x, &p.tm_out, p.out_tma, ybox, e.out, e.ldout, row0, pc, p.rows, p.cols);
     }
 }
 
-// The fp32 results of this group's half of a tile (sums of all chains, in registers), 32
-// columns (one box row) at a time, to out or to this split's partial product.
-template <int BN>
-__device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, float (&sum)[BN / 2], int row0, int col0,
-                                          int split) {
+// 32 fp32 columns of this thread's row through box b: to the scratch of split `part`, or to
+// the fp32 result (with what it held).
+__device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, const float* v, int b, int part, int lrow, int lcol,
+                                          int row0, int col0) {
     const GemmEpilogue& e = p.epi;
-    const bool partial = p.splits > 1;
-    const bool in = e.in && !partial;
-    // (tm_out is then a map of the partial products [splits][rows][cols])
-#pragma unroll
-    for (int q = 0; q < BN / 2 / 32; ++q) {
-        const int pc = col0 + 32 * q;
-        const uint32_t box = x.boxes + (q & 1) * QBOX;
-        if (x.leader) bulk_wait_read_but_one();  // this box's store, two pieces ago
-        named_barrier_sync(1 + x.grp, 128);
-        if (in) {
-            if (p.in_tma) {
-                arm_input(x, &p.tm_in, q & 1, pc, row0);
-                if (!mbar_wait(&x.in_bar[q & 1], static_cast<uint32_t>(x.loads[q & 1] - 1) & 1u, p.err)) x.fail = true;
-            } else {
-                rows_to_box<uint32_t>(box, static_cast<const uint32_t*>(e.in), e.ldin, row0, pc, p.rows, p.cols, x.quad,
-                                      x.lane);
-                __syncwarp();
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t a = box_addr(box, x.r, j);
-            float f[4] = {sum[32 * q + 4 * j], sum[32 * q + 4 * j + 1], sum[32 * q + 4 * j + 2], sum[32 * q + 4 * j + 3]};
-            if (in) {
-                float o[4];
-                Elem<float>::unpack(lds128(a), o);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] += o[i];
-            }
-            sts128(a, Elem<float>::pack(f));
-        }
-        if (partial || p.out_tma) {
-            fence_proxy_async_smem();
-            named_barrier_sync(1 + x.grp, 128);
-            if (x.leader) {
-                if (row0 < p.rows && pc < p.cols)
-                    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                                     &p.tm_out),
-                                 "r"(box), "r"(pc), "r"(row0), "r"(partial ? split : 0)
-                                 : "memory");
-                bulk_commit_group();
-            }
+    const uint32_t box = x.boxes + b * QBOX;
+    const bool in = e.in && part < 0;
+    box_free(x);
+    if (in) {
+        if (p.in_tma) {
+            arm_input(x, &p.tm_in, b, col0, row0);
+            wait_input(x, b, p.err);
         } else {
-            __syncwarp();
-            box_to_rows<uint32_t>(box, static_cast<uint32_t*>(e.out), e.ldout, row0, pc, p.rows, p.cols, x.quad, x.lane);
-            fence_proxy_async_smem();  // before an input load into this box
+            rows_to_box<uint32_t>(box, static_cast<const uint32_t*>(e.in), e.ldin, row0, col0, p.rows, p.cols, x.quad, x.lane);
             __syncwarp();
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t a = box_addr(box, x.r, j);
+        float f[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+        if (in) {
+            float o[4];
+            Elem<float>::unpack(lds128(a), o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] += o[i];
+        }
+        sts128(a, Elem<float>::pack(f));
+    }
+    if (part >= 0) {
+        fence_proxy_async_smem();
+        named_barrier_sync(1 + x.grp, 128);
+        if (x.leader) {
+            tma_store_box(&p.tm_part, box, lcol, part * PAIR_ROWS + lrow);
+            bulk_commit_group();
+        }
+    } else {
+        send_box<uint32_t>(x, &p.tm_out, p.out_tma, box, e.out, e.ldout, row0, col0, p.rows, p.cols);
     }
 }
 
 // T: type of 16-bit results (float: fp32 results, taken in chains of CHAIN_KB k-blocks)
-template <typename T, int BN>
+template <typename T>
 __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid_constant__ PairGemmParams p) {
-    using S = PairShape<BN>;
     constexpr bool F32 = sizeof(T) == 4;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[S::STAGES];
-    __shared__ __align__(8) uint64_t empty_bar[S::STAGES];
+    __shared__ __align__(8) uint64_t full_bar[STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[STAGES];
     __shared__ __align__(8) uint64_t tfull_bar[2];
     __shared__ __align__(8) uint64_t tempty_bar[2];
     __shared__ __align__(8) uint64_t in_bar[EPI_GROUPS][2];
@@ -400,12 +438,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();  // 0 = leader (issues the MMAs)
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int units = p.tiles_r * p.tiles_c * p.splits;
+    const int units = p.units;
     uint8_t* smem =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S::STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
@@ -420,7 +458,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
         tma_prefetch_desc(&p.tm_a);
         tma_prefetch_desc(&p.tm_b);
     }
-    if (warp == 1) tmem_alloc_pair(&tmem_slot, S::TMEM_COLS);
+    if (warp == 1) tmem_alloc_pair(&tmem_slot, PAIR_TMEM);
     tc_fence_before();
     cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
     tc_fence_after();
@@ -434,20 +472,18 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
             int it = 0;
             for (int u = pair; u < units; u += npairs) {
                 const Unit t = unit_of(p, u);
-                int kb0, nkb;
-                unit_kblocks(p, t, &kb0, &nkb);
                 const int arow = t.tr * PAIR_ROWS + CTA_ROWS * static_cast<int>(rank);
                 const int brow = t.tc * BN + BN / 2 * static_cast<int>(rank);
                 bool ok = true;
-                for (int kb = kb0; kb < kb0 + nkb; ++kb, ++it) {
-                    const int s = it % S::STAGES;
-                    if (!mbar_wait(&empty_bar[s], ((it / S::STAGES) & 1) ^ 1, p.err)) {
+                for (int kb = t.kb0; kb < t.kb0 + t.nkb; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    if (!mbar_wait(&empty_bar[s], ((it / STAGES) & 1) ^ 1, p.err)) {
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * S::STAGE);
+                    if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * STAGE);
                     const uint32_t fb = map_to_rank(&full_bar[s], 0);
-                    uint8_t* sa = smem + s * S::STAGE;
+                    uint8_t* sa = smem + s * STAGE;
                     uint8_t* sb = sa + A_STAGE;
                     const int kc = kb * GEMM_BK;
                     if (p.a_mn) {
@@ -457,9 +493,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                         tma_load_3d_pair(sa, &p.tm_a, fb, kc, arow, 0);
                     }
                     if (p.b_mn) {
-#pragma unroll
-                        for (int h = 0; h < BN / 128; ++h)
-                            tma_load_3d_pair(sb + h * 8192, &p.tm_b, fb, brow + 64 * h, kc, 0);
+                        tma_load_3d_pair(sb, &p.tm_b, fb, brow, kc, 0);
+                        tma_load_3d_pair(sb + 8192, &p.tm_b, fb, brow + 64, kc, 0);
                     } else {
                         tma_load_3d_pair(sb, &p.tm_b, fb, kc, brow, 0);
                     }
@@ -483,9 +518,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
             uint32_t ph = 0;
             bool ready = false, ok = true;
             for (int u = pair; u < units && ok; u += npairs) {
-                const Unit t = unit_of(p, u);
-                int kb0, nkb;
-                unit_kblocks(p, t, &kb0, &nkb);
+                const int nkb = unit_of(p, u).nkb;
                 for (int c0 = 0; c0 < nkb && ok; c0 += F32 ? CHAIN_KB : nkb, ++acc) {
                     const int cn = F32 ? min(CHAIN_KB, nkb - c0) : nkb;
                     const int ab = acc & 1;
@@ -501,13 +534,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t a0 = stage0 + static_cast<uint32_t>(s * S::STAGE);
+                        const uint32_t a0 = stage0 + static_cast<uint32_t>(s * STAGE);
                         const uint32_t a_lo = sw128_desc_lo(a0, a_lbo), b_lo = sw128_desc_lo(a0 + A_STAGE, b_lbo);
 #pragma unroll
                         for (int kk = 0; kk < GEMM_BK / 16; ++kk)
                             umma_bf16_pair(dacc, sw128_desc(a_lo + kk * a_step), sw128_desc(b_lo + kk * b_step), idesc,
                                            (kb | kk) != 0 ? 1u : 0u);
-                        const int s_next = s + 1 == S::STAGES ? 0 : s + 1;
+                        const int s_next = s + 1 == STAGES ? 0 : s + 1;
                         const uint32_t ph_next = s_next == 0 ? ph ^ 1u : ph;
                         ready = mbar_test_wait(smem_u32(&full_bar[s_next]), ph_next);
                         umma_commit_pair(&empty_bar[s], 3);  // frees stage s in both CTAs
@@ -531,11 +564,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
         x.lane = lane;
         x.r = x.quad * 32 + lane;
         x.leader = x.quad == 0 && lane == 0;
-        x.boxes = smem_u32(smem + S::STAGES * S::STAGE + x.grp * 2 * QBOX);
+        x.boxes = smem_u32(smem + STAGES * STAGE + x.grp * 2 * QBOX);
         x.in_bar = in_bar[x.grp];
         x.fail = false;
         x.loads[0] = x.loads[1] = 0;
         const uint32_t te[2] = {map_to_rank(&tempty_bar[0], 0), map_to_rank(&tempty_bar[1], 0)};
+        const int lrow = CTA_ROWS * static_cast<int>(rank), lcol = BN / 2 * x.grp;  // within the tile
         int acc = 0;
         for (int u = pair; u < units; u += npairs) {
             // the group stops together once any wait of any role gave up
@@ -544,16 +578,14 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                 break;
             }
             const Unit t = unit_of(p, u);
-            int kb0, nkb;
-            unit_kblocks(p, t, &kb0, &nkb);
-            const int row0 = t.tr * PAIR_ROWS + CTA_ROWS * static_cast<int>(rank);
-            const int col0 = t.tc * BN + BN / 2 * x.grp;
-            const uint32_t tlane = tmem + (static_cast<uint32_t>(x.quad * 32) << 16) + static_cast<uint32_t>(BN / 2 * x.grp);
+            const int row0 = t.tr * PAIR_ROWS + lrow;
+            const int col0 = t.tc * BN + lcol;
+            const uint32_t tlane = tmem + (static_cast<uint32_t>(x.quad * 32) << 16) + static_cast<uint32_t>(lcol);
             if constexpr (F32) {
                 float sum[BN / 2];
 #pragma unroll
                 for (int i = 0; i < BN / 2; ++i) sum[i] = 0.f;
-                for (int c0 = 0; c0 < nkb; c0 += CHAIN_KB, ++acc) {
+                for (int c0 = 0; c0 < t.nkb; c0 += CHAIN_KB, ++acc) {
                     const int ab = acc & 1;
                     if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
                     tc_fence_after();
@@ -564,16 +596,31 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sum[q * 32 + i] += v[i];
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(te[ab]);
+                    release_acc(x, te[ab]);
                 }
-                store_f32<BN>(p, x, sum, row0, col0, t.split);
+#pragma unroll
+                for (int q = 0; q < BN / 2 / 32; ++q)
+                    store_f32(p, x, sum + 32 * q, q & 1, t.part, lrow, lcol + 32 * q, row0, col0 + 32 * q);
             } else {
                 const int ab = acc & 1;
+                if (t.part < 0 && early_input(p)) {
+                    // the residual, once the boxes' earlier stores have been read
+                    if (x.leader) bulk_wait_read_all();
+                    for (int q = 0; q < BN / 2 / 64; ++q) arm_input(x, &p.tm_in, q & 1, col0 + 64 * q, row0);
+                }
                 if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
                 tc_fence_after();
-                epilogue_16<T, BN>(p, x, tlane + ab * BN, te[ab], row0, col0);
+                if (t.part < 0) {
+                    epilogue_16<T>(p, x, tlane + ab * BN, te[ab], row0, col0);
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < BN / 2 / 32; ++q) {
+                        float v[32];
+                        tmem_ld_32x32b_x32(tlane + ab * BN + q * 32, v);
+                        if (q == BN / 2 / 32 - 1) release_acc(x, te[ab]);
+                        store_f32(p, x, v, q & 1, t.part, lrow, lcol + 32 * q, row0, col0 + 32 * q);
+                    }
+                }
                 ++acc;
             }
         }
@@ -587,13 +634,86 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
     __syncthreads();
     if (aborted && warp == 0 && lane == 0 && rank == 0) {
         // the pair's loads in flight land before its shared memory goes away
-        for (int kb = issued - S::STAGES < 0 ? 0 : issued - S::STAGES; kb < issued; ++kb)
-            mbar_wait(&full_bar[kb % S::STAGES], (kb / S::STAGES) & 1, p.err);
+        for (int kb = issued - STAGES < 0 ? 0 : issued - STAGES; kb < issued; ++kb)
+            mbar_wait(&full_bar[kb % STAGES], (kb / STAGES) & 1, p.err);
     }
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc_pair(tmem, S::TMEM_COLS);
+    if (warp == 1) tmem_dealloc_pair(tmem, PAIR_TMEM);
+}
+
+// The tail tiles of pair_gemm_kernel: the parts of each element, in order, then what follows
+// the accumulator.  A block takes 16 rows of a tile, a thread four columns at a time.
+constexpr int TAIL_ROWS = 16;
+template <typename T>
+__global__ void __launch_bounds__(256) tail_sum_kernel(const __grid_constant__ TailSumParams p) {
+    pdl_allow_next();
+    const GemmEpilogue& e = p.epi;
+    const int tile = blockIdx.x / (PAIR_ROWS / TAIL_ROWS), r0 = blockIdx.x % (PAIR_ROWS / TAIL_ROWS) * TAIL_ROWS;
+    int tr, tc;
+    {
+        const int t = p.whole + tile;
+        const int per = RASTER_ROWS * p.tiles_c;
+        const int g = t / per;
+        const int rows = min(RASTER_ROWS, p.tiles_r - g * RASTER_ROWS);
+        const int q = t - g * per;
+        tc = q / rows;
+        tr = g * RASTER_ROWS + (q - tc * rows);
+    }
+    const int c = threadIdx.x % 64 * 4, col = tc * PAIR_COLS + c;
+    pdl_wait_previous();
+    if (col >= p.cols) return;
+    const float* base = p.part + static_cast<size_t>(tile) * p.splits * PAIR_ROWS * PAIR_COLS + c;
+    float v[TAIL_ROWS / 4][4];
+#pragma unroll
+    for (int i = 0; i < TAIL_ROWS / 4; ++i) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+    for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+        for (int i = 0; i < TAIL_ROWS / 4; ++i) {
+            const int r = r0 + i * 4 + threadIdx.x / 64;
+            const float4 f = __ldcs(reinterpret_cast<const float4*>(base + (static_cast<size_t>(s) * PAIR_ROWS + r) * PAIR_COLS));
+            v[i][0] += f.x;
+            v[i][1] += f.y;
+            v[i][2] += f.z;
+            v[i][3] += f.w;
+        }
+    }
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (sizeof(T) == 2) {
+        if (e.bias) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (col + k < p.cols)
+                    bias[k] = e.bias_f32 ? static_cast<const float*>(e.bias)[col + k]
+                                         : Elem<T>::load(static_cast<const T*>(e.bias)[col + k]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < TAIL_ROWS / 4; ++i) {
+        const long long row = tr * PAIR_ROWS + r0 + i * 4 + threadIdx.x / 64;
+        if (row >= p.rows) continue;
+        float in[4] = {0.f, 0.f, 0.f, 0.f};
+        if (e.in) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (col + k < p.cols) in[k] = Elem<T>::load(static_cast<const T*>(e.in)[row * e.ldin + col + k]);
+        }
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i][k] += bias[k];
+            if (e.z) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (col + k < p.cols) static_cast<T*>(e.z)[row * e.ldz + col + k] = Elem<T>::store(v[i][k]);
+            }
+            act_values<4>(e.act, v[i]);
+        }
+        T* out = static_cast<T*>(e.out) + row * e.ldout + col;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (col + k < p.cols) out[k] = Elem<T>::store(v[i][k] + in[k]);
+    }
 }
 
 // ---------------------------------------------------------------- few rows
@@ -607,20 +727,37 @@ struct RowShape {
     static_assert(BN * ROW_TILE_A * 4 <= STAGES * STAGE, "the partial accumulator reuses the stages");
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
     return v;
 }
 
-// bias, activation, residual and stores of one element (row = B's row, col = A's row)
-template <typename T>
-__device__ __forceinline__ void finish_element(const GemmEpilogue& e, float v, float bias, long long row, int col) {
-    v += bias;
-    if (e.z) static_cast<T*>(e.z)[row * e.ldz + col] = Elem<T>::store(v);
-    v = act_value(e.act, v);
-    if (e.in) v += Elem<T>::load(static_cast<const T*>(e.in)[row * e.ldin + col]);
-    static_cast<T*>(e.out)[row * e.ldout + col] = Elem<T>::store(v);
+// bias, activation, residual and stores of up to N rows (B's) of one column (A's row);
+// neighbouring lanes are neighbouring columns.  The loads go out together.
+template <typename T, int N>
+__device__ __forceinline__ void finish_rows(const GemmEpilogue& e, float (&v)[N], float bias, long long row, int rows, int col) {
+    float in[N];
+    if (e.in) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            in[i] = i < rows ? Elem<T>::load(static_cast<const T*>(e.in)[(row + i) * e.ldin + col]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += bias;
+    if (e.z) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < rows) static_cast<T*>(e.z)[(row + i) * e.ldz + col] = Elem<T>::store(v[i]);
+    }
+    act_values<N>(e.act, v);
+    if (e.in) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += in[i];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < rows) static_cast<T*>(e.out)[(row + i) * e.ldout + col] = Elem<T>::store(v[i]);
 }
 
 template <typename T, int BN>
@@ -719,31 +856,60 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
             bias = p.epi.bias_f32 ? static_cast<const float*>(p.epi.bias)[col] : Elem<T>::load(static_cast<const T*>(p.epi.bias)[col]);
         mbar_wait(&done_bar, 0, p.err);
         tc_fence_after();
-        float* own = reinterpret_cast<float*>(smem);  // [BN][128] partial accumulator (the stages are done)
+        // the partial accumulator, in place of the stages (which are done): four B rows of one
+        // A row side by side, [BN / 4][128] of them
+        float4* own = reinterpret_cast<float4*>(smem);
         for (int q = 0; q * 32 < nb; ++q) {
             float v[32];
             tmem_ld_32x32b_x32(tlane + q * 32, v);
             if (p.splits == 1) {
+                if (live) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (live && q * 32 + i < nb) finish_element<T>(p.epi, v[i], bias, b0 + q * 32 + i, col);
+                    for (int h = 0; h < 4; ++h)
+                        if (q * 32 + 8 * h < nb)
+                            finish_rows<T, 8>(p.epi, reinterpret_cast<float(&)[8]>(v[8 * h]), bias, b0 + q * 32 + 8 * h,
+                                              nb - q * 32 - 8 * h, col);
+                }
             } else {
-                // a split past the end of the contraction holds no product
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (q * 32 + i < nb) own[(q * 32 + i) * ROW_TILE_A + r] = nkb > 0 ? v[i] : 0.f;
+                for (int h = 0; h < 8; ++h)
+                    if (q * 32 + 4 * h < nb)
+                        own[(q * 8 + h) * ROW_TILE_A + r] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
             }
         }
         __syncwarp();
         if (p.splits > 1) {
             cluster_sync();
-            // every CTA finishes its share of the B rows, the parts added in rank order
-            for (int j = split; j < nb; j += p.splits) {
-                float v = 0.f;
-                for (int s = 0; s < p.splits; ++s)
-                    v += ld_cluster_f32(map_to_rank(&own[j * ROW_TILE_A + r], static_cast<uint32_t>(s)));
-                if (live) finish_element<T>(p.epi, v, bias, b0 + j, col);
+            // every CTA finishes its share of the B rows, two fours at a time, the parts added in
+            // rank order
+            const int quads = (nb + 3) / 4;
+            for (int j = split; j < quads; j += 2 * p.splits) {
+                const int j2 = j + p.splits;
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                const uint32_t mine = smem_u32(&own[j * ROW_TILE_A + r]), next = smem_u32(&own[j2 * ROW_TILE_A + r]);
+#pragma unroll 4
+                for (int s = 0; s < p.splits; ++s) {
+                    uint32_t a, a2;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(mine), "r"(s));
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a2) : "r"(next), "r"(s));
+                    const float4 f = ld_cluster_f4(a);
+                    const float4 g = j2 < quads ? ld_cluster_f4(a2) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[0] += f.x;
+                    v[1] += f.y;
+                    v[2] += f.z;
+                    v[3] += f.w;
+                    v[4] += g.x;
+                    v[5] += g.y;
+                    v[6] += g.z;
+                    v[7] += g.w;
+                }
+                if (live) {
+                    finish_rows<T, 4>(p.epi, reinterpret_cast<float(&)[4]>(v[0]), bias, b0 + 4 * j, nb - 4 * j, col);
+                    if (j2 < quads)
+                        finish_rows<T, 4>(p.epi, reinterpret_cast<float(&)[4]>(v[4]), bias, b0 + 4 * j2, nb - 4 * j2, col);
+                }
             }
+            __syncwarp();
         }
         tc_fence_before();
     }
@@ -764,33 +930,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- around the products
-// out = [in +] sum of the splits' partial products, four columns per thread.
-template <typename T>
-__global__ void __launch_bounds__(256) split_sum_kernel(const SplitSumParams p) {
-    pdl_wait_previous();
-    const long long chunks = p.ld_part / 4;
-    const long long total = chunks * p.rows;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long row = i / chunks;
-        const int c = static_cast<int>(i - row * chunks) * 4;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < p.splits; ++s) {
-            const float4 f = __ldcs(reinterpret_cast<const float4*>(p.part + (static_cast<size_t>(s) * p.rows + row) * p.ld_part + c));
-            v[0] += f.x;
-            v[1] += f.y;
-            v[2] += f.z;
-            v[3] += f.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < p.cols) {
-                float f = v[e];
-                if (p.in) f += Elem<T>::load(static_cast<const T*>(p.in)[row * p.ldin + c + e]);
-                static_cast<T*>(p.out)[row * p.ldout + c + e] = Elem<T>::store(f);
-            }
-    }
-}
-
 // Eight columns per thread; the last chunk of a row may be partial.
 __global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
     pdl_wait_previous();
@@ -808,40 +947,56 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
     }
 }
 
-constexpr int AG_LANES = 8;  // rows in flight per block: 32 threads x 8 columns each
-template <typename T, bool VEC>
+constexpr int AG_LANES = 8;   // rows at a time per block: 32 threads x 8 columns each
+constexpr int AG_UNROLL = 4;  // turns whose loads are in flight together
+template <typename T, int ACT, bool VEC>
 __global__ void __launch_bounds__(32 * AG_LANES) act_grad_kernel(const ActGradParams p) {
     __shared__ float sums[AG_LANES][ACT_GRAD_COLS];
+    constexpr bool Z = ACT != ACT_NONE;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int c = blockIdx.x * ACT_GRAD_COLS + tx * 8;
-    const T* dy = static_cast<const T*>(p.dy);
-    const T* z = static_cast<const T*>(p.z);
+    const T* dy = static_cast<const T*>(p.dy) + c;
+    const T* z = static_cast<const T*>(p.z) + c;
     T* dz = static_cast<T*>(p.dz);
+    pdl_allow_next();
     pdl_wait_previous();
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const long long r0 = static_cast<long long>(blockIdx.y) * p.rows_per_block;
     const long long r1 = min(r0 + p.rows_per_block, p.rows);
     if (c < p.cols) {
-#pragma unroll 2
-        for (long long r = r0 + ty; r < r1; r += AG_LANES) {
-            float g[8], f[8];
+        auto fetch = [&](const T* q) {
             if constexpr (VEC) {
-                Elem<T>::unpack(ldg_stream(dy + r * p.lddy + c), g);
-                if (z) Elem<T>::unpack(ldg_stream(z + r * p.ldz + c), f);
+                return ldg_stream(q);
             } else {
+                uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    g[e] = c + e < p.cols ? Elem<T>::load(dy[r * p.lddy + c + e]) : 0.f;
-                    f[e] = z && c + e < p.cols ? Elem<T>::load(z[r * p.ldz + c + e]) : 0.f;
+                for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols ? __ldcs(reinterpret_cast<const uint16_t*>(q) + e) : 0u;
+                return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+            }
+        };
+        for (long long rb = r0 + ty; rb < r1; rb += AG_LANES * AG_UNROLL) {
+            uint4 rg[AG_UNROLL], rz[AG_UNROLL];
+#pragma unroll
+            for (int k = 0; k < AG_UNROLL; ++k) {
+                const long long r = rb + k * AG_LANES;
+                rg[k] = r < r1 ? fetch(dy + r * p.lddy) : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (Z) rz[k] = r < r1 ? fetch(z + r * p.ldz) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < AG_UNROLL; ++k) {
+                const long long r = rb + k * AG_LANES;
+                float g[8];
+                Elem<T>::unpack(rg[k], g);
+                if constexpr (Z) {
+                    float f[8];
+                    Elem<T>::unpack(rz[k], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(f[e]);
                 }
-            }
-            if (z) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] *= act_slope(p.act, f[e]);
+                for (int e = 0; e < 8; ++e) acc[e] += g[e];
+                if (dz && r < r1) *reinterpret_cast<uint4*>(dz + r * p.ldd + c) = Elem<T>::pack(g);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] += g[e];
-            if (dz) *reinterpret_cast<uint4*>(dz + r * p.ldd + c) = Elem<T>::pack(g);
         }
     }
     if (!p.part) return;
@@ -875,7 +1030,7 @@ __global__ void __launch_bounds__(32 * CS_LANES) column_sum_kernel(const float* 
     }
 }
 
-template <typename T, int BN>
+template <typename T>
 cudaError_t run_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -886,14 +1041,13 @@ cudaError_t run_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.blockDim = dim3(PAIR_THREADS);
-    cfg.dynamicSmemBytes = PairShape<BN>::SMEM;
+    cfg.dynamicSmemBytes = PAIR_SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const int units = p.tiles_r * p.tiles_c * p.splits;
     const int most = sm_count / 2;
-    cfg.gridDim = dim3(2 * (units < most ? units : most));
-    return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<T, BN>, p);
+    cfg.gridDim = dim3(2 * (p.units < most ? p.units : most));
+    return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<T>, p);
 }
 
 template <typename T, int BN>
@@ -926,12 +1080,9 @@ cudaError_t linear_prepare() {
     cudaError_t e;
 #define ANVIL_SMEM(kernel, bytes) \
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return e
-    ANVIL_SMEM((pair_gemm_kernel<__nv_bfloat16, 256>), PairShape<256>::SMEM);
-    ANVIL_SMEM((pair_gemm_kernel<__nv_bfloat16, 128>), PairShape<128>::SMEM);
-    ANVIL_SMEM((pair_gemm_kernel<__half, 256>), PairShape<256>::SMEM);
-    ANVIL_SMEM((pair_gemm_kernel<__half, 128>), PairShape<128>::SMEM);
-    ANVIL_SMEM((pair_gemm_kernel<float, 256>), PairShape<256>::SMEM);
-    ANVIL_SMEM((pair_gemm_kernel<float, 128>), PairShape<128>::SMEM);
+    ANVIL_SMEM(pair_gemm_kernel<__nv_bfloat16>, PAIR_SMEM);
+    ANVIL_SMEM(pair_gemm_kernel<__half>, PAIR_SMEM);
+    ANVIL_SMEM(pair_gemm_kernel<float>, PAIR_SMEM);
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 16>), RowShape<16>::SMEM);
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 32>), RowShape<32>::SMEM);
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 64>), RowShape<64>::SMEM);
@@ -944,10 +1095,16 @@ cudaError_t linear_prepare() {
     return cudaSuccess;
 }
 
-cudaError_t launch_pair_gemm(const PairGemmParams& p, int bn, int sm_count, cudaStream_t s) {
-    if (p.epi.out_f32) return bn == 256 ? run_pair<float, 256>(p, sm_count, s) : run_pair<float, 128>(p, sm_count, s);
-    if (p.f16) return bn == 256 ? run_pair<__half, 256>(p, sm_count, s) : run_pair<__half, 128>(p, sm_count, s);
-    return bn == 256 ? run_pair<__nv_bfloat16, 256>(p, sm_count, s) : run_pair<__nv_bfloat16, 128>(p, sm_count, s);
+cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t s) {
+    if (p.epi.out_f32) return run_pair<float>(p, sm_count, s);
+    return p.f16 ? run_pair<__half>(p, sm_count, s) : run_pair<__nv_bfloat16>(p, sm_count, s);
+}
+
+cudaError_t launch_tail_sum(const TailSumParams& p, cudaStream_t s) {
+    const dim3 grid((p.tiles_r * p.tiles_c - p.whole) * (PAIR_ROWS / TAIL_ROWS));
+    if (p.epi.out_f32) return launch_pdl(tail_sum_kernel<float>, grid, dim3(256), 0, s, p);
+    if (p.f16) return launch_pdl(tail_sum_kernel<__half>, grid, dim3(256), 0, s, p);
+    return launch_pdl(tail_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p);
 }
 
 cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t s) {
@@ -959,26 +1116,36 @@ cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t s) {
     }
 }
 
-cudaError_t launch_split_sum(const SplitSumParams& p, cudaStream_t s) {
-    const dim3 grid(blocks_for(p.ld_part / 4 * p.rows));
-    if (p.out_f32) return launch_pdl(split_sum_kernel<float>, grid, dim3(256), 0, s, p);
-    if (p.f16) return launch_pdl(split_sum_kernel<__half>, grid, dim3(256), 0, s, p);
-    return launch_pdl(split_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p);
-}
-
 cudaError_t launch_repack(const RepackParams& p, cudaStream_t s) {
     return launch_pdl(repack_kernel, dim3(blocks_for(p.ldd / 8 * p.rows)), dim3(256), 0, s, p);
 }
 
-cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t s) {
+namespace {
+template <typename T>
+cudaError_t run_act_grad(const ActGradParams& p, cudaStream_t s) {
     auto ok = [](const void* q, long long ld) { return !(reinterpret_cast<uintptr_t>(q) & 15) && ld % 8 == 0; };
     const bool vec = p.cols % 8 == 0 && ok(p.dy, p.lddy) && ok(p.z, p.z ? p.ldz : 0);
     const dim3 grid((p.cols + ACT_GRAD_COLS - 1) / ACT_GRAD_COLS, p.blocks_r), block(32 * AG_LANES);
-    if (p.f16)
-        return vec ? launch_pdl(act_grad_kernel<__half, true>, grid, block, 0, s, p)
-                   : launch_pdl(act_grad_kernel<__half, false>, grid, block, 0, s, p);
-    return vec ? launch_pdl(act_grad_kernel<__nv_bfloat16, true>, grid, block, 0, s, p)
-               : launch_pdl(act_grad_kernel<__nv_bfloat16, false>, grid, block, 0, s, p);
+#define ANVIL_ACT_CASE(A)                                                             \
+    case A:                                                                           \
+        return vec ? launch_pdl(act_grad_kernel<T, A, true>, grid, block, 0, s, p)    \
+                   : launch_pdl(act_grad_kernel<T, A, false>, grid, block, 0, s, p)
+    switch (p.act) {
+        ANVIL_ACT_CASE(ACT_RELU);
+        ANVIL_ACT_CASE(ACT_RELU2);
+        ANVIL_ACT_CASE(ACT_GELU);
+        ANVIL_ACT_CASE(ACT_GELU_TANH);
+        ANVIL_ACT_CASE(ACT_SILU);
+        default: break;
+    }
+    return vec ? launch_pdl(act_grad_kernel<T, ACT_NONE, true>, grid, block, 0, s, p)
+               : launch_pdl(act_grad_kernel<T, ACT_NONE, false>, grid, block, 0, s, p);
+#undef ANVIL_ACT_CASE
+}
+}  // namespace
+
+cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t s) {
+    return p.f16 ? run_act_grad<__half>(p, s) : run_act_grad<__nv_bfloat16>(p, s);
 }
 
 cudaError_t launch_column_sum(const float* part, int blocks, int cols, float* out, int accumulate, cudaStream_t s) {

@@ -27,15 +27,25 @@ struct GemmEpilogue {
 // C [rows, cols] = sum_k A[row, k] B[col, k].  An operand is K-major (stored [row][k]) or
 // MN-major (stored [k][row]).
 struct PairGemmParams {
-    CUtensorMap tm_a, tm_b, tm_in, tm_out, tm_z;
+    CUtensorMap tm_a, tm_b, tm_in, tm_out, tm_z, tm_part;
     GemmEpilogue epi;
     int rows, cols, k;
     int a_mn, b_mn;
     int f16;                        // operands are fp16 (else bf16)
     int in_tma, out_tma, z_tma;     // through tensor maps (16-byte aligned rows)
-    int tiles_r, tiles_c, splits;   // work units: tiles_r * tiles_c * splits
+    int tiles_r, tiles_c;           // 256 x 256 output tiles
+    // The first `whole` tiles are computed in one piece; each of the others in `splits` along
+    // k, whose fp32 parts go to tm_part: [tail tile][split] blocks of 256 x 256.
+    int whole, splits, units;       // units = whole + tail tiles * splits
     int kb_per_split;               // 64-deep k-blocks of a split
-    unsigned* err;                  // splits > 1: tm_out maps the partial products [splits][rows][cols]
+    unsigned* err;
+};
+// The sums of the tail tiles' parts, and the epilogue.
+struct TailSumParams {
+    GemmEpilogue epi;
+    const float* part;
+    int rows, cols, tiles_r, tiles_c, whole, splits;
+    int f16;
 };
 // A = the operand whose rows run along the output's contiguous dimension ("cols" above),
 // B = the few rows: out[b][a].
@@ -51,25 +61,15 @@ struct RowGemmParams {
 };
 
 constexpr int GEMM_BK = 64;    // k-block: one 128-byte swizzle row of 16-bit elements
-constexpr int PAIR_ROWS = 256; // output rows of a CTA pair's tile
+constexpr int PAIR_ROWS = 256; // output rows and columns of a CTA pair's tile
+constexpr int PAIR_COLS = 256;
 constexpr int ROW_TILE_A = 128;
 
 cudaError_t linear_prepare();
-// bn: output columns of a pair's tile (256 or 128)
-cudaError_t launch_pair_gemm(const PairGemmParams& p, int bn, int sm_count, cudaStream_t stream);
+cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_tail_sum(const TailSumParams& p, cudaStream_t stream);
 // bn: B's rows per block (16, 32, 64 or 128)
 cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t stream);
-
-// out (+)= sum over splits of part [splits][rows][ld_part], in split order.
-struct SplitSumParams {
-    const float* part;
-    const void* in;
-    void* out;
-    long long ld_part, ldin, ldout;
-    int rows, cols, splits;
-    int out_f32, f16;
-};
-cudaError_t launch_split_sum(const SplitSumParams& p, cudaStream_t stream);
 
 // dst [rows, ldd] <- src [rows, cols] (row stride lds), 16-bit elements, ldd % 8 == 0.
 struct RepackParams {

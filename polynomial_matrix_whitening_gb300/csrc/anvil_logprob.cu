@@ -8,17 +8,27 @@
 //
 // The forward pass reads the logits once: every thread keeps a running maximum m, the sum
 // s of e^{x - m} and the sum q of e^{x - m} (x - m) (in fp32, rescaled when the maximum
-// grows), from which lse = m + log s and H = log s - q / s.  The top k are found in the
-// same pass: each warp holds the best k so far, one per lane in order, and only a lane
-// that sees a value above the k-th opens the (rare) insertion path.  HBM bounds both
-// passes where there are many rows; where rows are fewer than the SMs, a cluster of up to
-// eight blocks takes a row's segments and the first block joins their results through
-// distributed shared memory, in a fixed order.
+// grows), from which lse = m + log s and H = log s - q / s.  The arithmetic runs on packed
+// fp32 pairs: about 4.5 instructions per element, where scalar ones took 8 and the issue
+// rate, not HBM, was the bound.
+//
+// The top k are found in the same pass.  A warp holds the best k it has met, one per lane
+// in order; putting one in costs tens of cycles, so few may be tried.  Each thread of a
+// block has the largest of its 32 (fp32: 16) values of a turn at hand; the k-th largest of those 256
+// maxima is a value that at least k elements reach, so everything below it is passed over.
+// It is found on the upper 16 bits of the ordered values by 16 counting barriers, on the
+// first turn and whenever more than 2k threads of a turn hold something new.  In the end
+// every entry of the eight lists counts the entries ahead of it: its place.
+//
+// HBM bounds both passes where there are many rows; where rows are fewer than the SMs, a
+// cluster of up to eight blocks takes a row's segments and the first block joins their
+// results through distributed shared memory, in a fixed order.
 //
 // A row in which every logit is -inf has no distribution: lse and the log probabilities
 // are -inf, the entropy is 0 and the gradient is zero.  A masked logit (-inf, or so low
-// that e^{x - m} is 0) adds nothing: its exponent is held at -200 (in base 2), where e is
-// 0, so that no product of 0 and infinity arises.  A NaN or +inf makes its row NaN.
+// that the difference overflows) adds nothing: where a chunk's sum of e y comes out NaN,
+// from 0 times infinity, the chunk is taken again with the exponents held at -200 (in base
+// 2), where e is 0.  A NaN or +inf makes its row NaN.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stddef.h>
@@ -76,23 +86,22 @@ __device__ __forceinline__ bool better(int ka, int ia, int kb, int ib) { return 
 struct TopList {
     int key, idx;  // this lane's entry
     int kth_key, kth_idx;
-    float thr;  // value of the top-th entry (NaN while the list is not full)
 };
 __device__ __forceinline__ void top_init(TopList& L) {
     L.key = L.kth_key = KEY_NONE;
     L.idx = L.kth_idx = INT32_MAX;
-    L.thr = __int_as_float(0x7fc00000);
 }
 // Every lane offers one entry (cand false: none); the warp inserts those that belong.
 __device__ __forceinline__ void top_offer(TopList& L, int top, int lane, bool cand, int key, int idx) {
-    unsigned todo = __ballot_sync(0xffffffffu, cand && better(key, idx, L.kth_key, L.kth_idx));
+    cand = cand && better(key, idx, L.kth_key, L.kth_idx);
+    unsigned todo = __ballot_sync(0xffffffffu, cand);
     while (todo) {
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
         const int k = __shfl_sync(0xffffffffu, key, src), i = __shfl_sync(0xffffffffu, idx, src);
         const int pk = __shfl_up_sync(0xffffffffu, L.key, 1), pi = __shfl_up_sync(0xffffffffu, L.idx, 1);
-        const bool mine = better(L.key, L.idx, k, i);              // my entry stays ahead of the new one
-        const bool prev = lane > 0 && !better(pk, pi, k, i);       // the one before me moves down to me
+        const bool mine = better(L.key, L.idx, k, i);         // my entry stays ahead of the new one
+        const bool prev = lane > 0 && !better(pk, pi, k, i);  // the one before me moves down to me
         if (!mine) {
             L.key = prev ? pk : k;
             L.idx = prev ? pi : i;
@@ -101,7 +110,6 @@ __device__ __forceinline__ void top_offer(TopList& L, int top, int lane, bool ca
         L.kth_idx = __shfl_sync(0xffffffffu, L.idx, top - 1);
         todo &= __ballot_sync(0xffffffffu, better(key, idx, L.kth_key, L.kth_idx));
     }
-    L.thr = L.kth_key == KEY_NONE ? __int_as_float(0x7fc00000) : key_value(L.kth_key);
 }
 
 constexpr int FWD_THREADS = 256;
@@ -113,13 +121,9 @@ struct BlockResult {
     int key[LOGPROB_MAX_TOP], idx[LOGPROB_MAX_TOP];
 };
 
-// N values of a thread (masked slots hold -inf) into its statistics.
-template <int N>
-__device__ __forceinline__ float take(Stats& st, const float (&v)[N]) {
-    float mx = v[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) mx = fmaxf(mx, v[i]);
-    if (mx > st.m) {  // the first values, and then ever more rarely
+// A maximum mx into the statistics: the first values, and then ever more rarely, raise m.
+__device__ __forceinline__ void raise_max(Stats& st, float mx) {
+    if (mx > st.m) {
         if (st.m != -INFINITY) {
             const float d = fmaxf((st.m - mx) * LOG2E, -200.f), c = ex2(d);
             st.q = c * (st.q + d * st.s);
@@ -127,17 +131,51 @@ __device__ __forceinline__ float take(Stats& st, const float (&v)[N]) {
         }
         st.m = mx;
     }
-    // the difference before the factor log2 e: a maximum of the type's lowest value (a row
-    // masked with it) times log2 e would overflow
+}
+// One value (-inf: none).
+__device__ __forceinline__ void take_one(Stats& st, float v) {
+    raise_max(st, v);
+    const float y = max_nan((v - (st.m == -INFINITY ? 0.f : st.m)) * LOG2E, -200.f);
+    const float e = ex2(y);
+    st.s += e;
+    st.q = fmaf(e, y, st.q);
+}
+// N values, none above st.m.  The difference comes before the factor log2 e: a maximum of
+// the type's lowest value (a row masked with it) times log2 e would overflow.
+template <int N>
+__device__ __forceinline__ void take(Stats& st, const float (&v)[N]) {
     const float m0 = st.m == -INFINITY ? 0.f : st.m;
+    const uint64_t nm = f2_pack(-m0, -m0), l2e = f2_pack(LOG2E, LOG2E);
+    uint64_t s2 = 0, q2 = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float y = max_nan((v[i] - m0) * LOG2E, -200.f);
-        const float e = ex2(y);
-        st.s += e;
-        st.q = fmaf(e, y, st.q);
+    for (int i = 0; i < N; i += 2) {
+        const uint64_t y = f2_mul(f2_add(f2_pack(v[i], v[i + 1]), nm), l2e);
+        const uint64_t e = f2_pack(ex2(f2_lo(y)), ex2(f2_hi(y)));
+        s2 = f2_add(s2, e);
+        q2 = f2_fma(e, y, q2);
     }
-    return mx;
+    float s = f2_lo(s2) + f2_hi(s2), q = f2_lo(q2) + f2_hi(q2);
+    if (q != q) {
+        s = q = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float y = max_nan((v[i] - m0) * LOG2E, -200.f);
+            const float e = ex2(y);
+            s += e;
+            q = fmaf(e, y, q);
+        }
+    }
+    st.s += s;
+    st.q += q;
+}
+
+// Place of entry (key, idx) among the first cnt[w] entries of each list w.
+__device__ __forceinline__ int place_of(int key, int idx, const int (*keys)[LOGPROB_MAX_TOP], const int (*idxs)[LOGPROB_MAX_TOP],
+                                        const int* cnt, int lists) {
+    int place = 0;
+    for (int w = 0; w < lists; ++w)
+        for (int j = 0; j < cnt[w]; ++j) place += better(keys[w][j], idxs[w][j], key, idx) ? 1 : 0;
+    return place;
 }
 
 template <typename T, bool TOP>
@@ -146,6 +184,7 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
     constexpr int CH = E * UNROLL;
     __shared__ Stats wst[FWD_WARPS];
     __shared__ int wkey[TOP ? FWD_WARPS : 1][LOGPROB_MAX_TOP], widx[TOP ? FWD_WARPS : 1][LOGPROB_MAX_TOP];
+    __shared__ int wcnt[FWD_WARPS];
     __shared__ BlockResult res;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x / csize;
@@ -153,8 +192,8 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
     const T* x = static_cast<const T*>(p.logits) + row * p.ld;
 
     // The row from its first 16-byte boundary: `head` elements before it, then whole
-    // vectors, then `tail` elements.  Block `rank` of the cluster takes a run of vectors;
-    // the first block also takes the head, the last one the tail.
+    // vectors, then the tail.  Block `rank` of the cluster takes a run of vectors; the
+    // first block also takes the head, the last one the tail.
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
     const int head = min(mis ? E - mis : 0, p.vocab);
     const int nvec = (p.vocab - head) / E;
@@ -165,13 +204,15 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
     Stats st = {-INFINITY, 0.f, 0.f};
     TopList L;
     top_init(L);
+    int tau = KEY_NONE;  // at least `top` elements so far reach it: only larger ones matter
     // at most E - 1 single elements of the head and of the tail, a lane each of warp 0; the
     // tail comes after the vectors, so that warp 0 too sees its indexes grow
     auto singles = [&](int c0, int cnt) {
         const bool in = lane < cnt;
-        const float v[1] = {in ? Elem<T>::load(x[c0 + lane]) : -INFINITY};
-        take<1>(st, v);
-        if (TOP) top_offer(L, p.top, lane, in, order_key(v[0]), c0 + lane);
+        const float v = in ? Elem<T>::load(x[c0 + lane]) : -INFINITY;
+        if (in) take_one(st, v);
+        __syncwarp();
+        if (TOP) top_offer(L, p.top, lane, in, order_key(v), c0 + lane);
     };
     if (warp == 0 && rank == 0) singles(0, head);
     const uint4* xv = reinterpret_cast<const uint4*>(x + head);
@@ -182,26 +223,44 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
         uint4 raw[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u)
-            if (wbase + u * 32 < v1) raw[u] = __ldcs(xv + wbase + u * 32);
+            raw[u] = wbase + u * 32 < v1 ? __ldcs(xv + wbase + u * 32)
+                                         : make_uint4(Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF);
+        uint32_t mw = Elem<T>::max_word(Elem<T>::max_word(raw[0].x, raw[0].y), Elem<T>::max_word(raw[0].z, raw[0].w));
+#pragma unroll
+        for (int u = 1; u < UNROLL; ++u)
+            mw = Elem<T>::max_word(mw, Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w)));
+        const float mx = Elem<T>::word_max(mw);
+        raise_max(st, mx);
         float v[CH];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            if (wbase + u * 32 < v1) {
-                Elem<T>::unpack(raw[u], v + u * E);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[u * E + e] = -INFINITY;
-            }
-        }
-        // slots past the end hold -inf and add 0 to s and q
-        const float mx = take<CH>(st, v);
+        for (int u = 0; u < UNROLL; ++u) Elem<T>::unpack(raw[u], v + u * E);
+        take<CH>(st, v);  // slots past the end hold -inf and add 0
         if constexpr (TOP) {
-            // not (mx <= thr): a value above the k-th best, or a list that is not full
-            if (__any_sync(0xffffffffu, !(mx <= L.thr))) {
+            const int mk = wbase < v1 ? order_key(mx) : KEY_NONE;
+            const bool first = base == v0;
+            bool hold = wbase < v1 && (first || mk > tau);
+            int need = tau + 1;  // the least key that matters in this turn
+            const int holds = __syncthreads_count(hold);
+            if (first || holds > 2 * p.top) {
+                // the largest T of 16 bits that `top` of the threads' maxima reach (0 where the
+                // threads are fewer); keys in unsigned order
+                const uint32_t uk = static_cast<uint32_t>(mk) ^ 0x80000000u;
+                uint32_t t = 0;
+#pragma unroll 1
+                for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
+                    if (__syncthreads_count(hold && uk >= (t | bit)) >= p.top) t |= bit;
+                const int tk = static_cast<int>(t ^ 0x80000000u);
+                need = tk > need ? tk : need;
+                tau = tk > tau ? tk : tau;
+                hold = hold && mk >= need;
+            }
+            if (holds && __any_sync(0xffffffffu, hold)) {
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
                     const int vec = wbase + (i / E) * 32;
-                    top_offer(L, p.top, lane, vec < v1, order_key(v[i]), head + vec * E + i % E);
+                    const int key = order_key(v[i]);
+                    const bool cand = hold && vec < v1 && key >= need;
+                    if (__any_sync(0xffffffffu, cand)) top_offer(L, p.top, lane, cand, key, head + vec * E + i % E);
                 }
             }
         }
@@ -218,52 +277,72 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
     }
     if (lane == 0) wst[warp] = st;
     if constexpr (TOP) {
-        if (lane < p.top) {
+        const bool entry = lane < p.top && L.key != KEY_NONE;
+        if (entry) {
             wkey[warp][lane] = L.key;
             widx[warp][lane] = L.idx;
         }
+        const int n = __popc(__ballot_sync(0xffffffffu, entry));
+        if (lane == 0) wcnt[warp] = n;
     }
     __syncthreads();
-    if (warp == 0) {
-        st = wst[0];
-        for (int w = 1; w < FWD_WARPS; ++w) st = join(st, wst[w]);
-        if constexpr (TOP) {
-            for (int w = 1; w < FWD_WARPS; ++w) {
-                const bool in = lane < p.top;
-                const int k = in ? wkey[w][lane] : KEY_NONE, i = in ? widx[w][lane] : INT32_MAX;
-                top_offer(L, p.top, lane, in && k != KEY_NONE, k, i);
+    st = wst[0];
+    for (int w = 1; w < FWD_WARPS; ++w) st = join(st, wst[w]);
+    if constexpr (TOP) {
+        // lane l of warp w: the l-th entry of list w
+        if (tid < LOGPROB_MAX_TOP) {
+            res.key[tid] = KEY_NONE;
+            res.idx[tid] = 0;
+        }
+        __syncthreads();
+        if (lane < wcnt[warp]) {
+            const int place = place_of(L.key, L.idx, wkey, widx, wcnt, FWD_WARPS);
+            if (place < p.top) {
+                res.key[place] = L.key;
+                res.idx[place] = L.idx;
             }
         }
-        if (csize > 1) {
-            if (lane == 0) res.st = st;
-            if (TOP && lane < p.top) {
-                res.key[lane] = L.key;
-                res.idx[lane] = L.idx;
-            }
-        }
+        __syncthreads();
     }
-    __syncwarp();
     if (csize > 1) {
+        if (tid == 0) res.st = st;
+        __syncwarp();
         cluster_sync();
-        if (rank == 0 && warp == 0) {
+        if (rank == 0) {
             for (int r = 1; r < csize; ++r) {
                 const uint32_t a = map_to_rank(&res, r);
                 Stats b;
-                int k = KEY_NONE, i = INT32_MAX;
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(a) : "memory");
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(a + 4) : "memory");
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.q) : "r"(a + 8) : "memory");
                 st = join(st, b);
-                if constexpr (TOP) {
-                    const bool in = lane < p.top;
-                    if (in) {
-                        const uint32_t ak = a + offsetof(BlockResult, key) + 4 * lane;
-                        const uint32_t ai = a + offsetof(BlockResult, idx) + 4 * lane;
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(k) : "r"(ak) : "memory");
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(i) : "r"(ai) : "memory");
-                    }
-                    top_offer(L, p.top, lane, in && k != KEY_NONE, k, i);
+            }
+            if constexpr (TOP) {
+                // warp w takes the list of the cluster's block w
+                int k = KEY_NONE, i = INT32_MAX;
+                if (warp < csize && lane < p.top) {
+                    const uint32_t a = map_to_rank(&res, warp);
+                    const uint32_t ak = a + offsetof(BlockResult, key) + 4 * lane, ai = a + offsetof(BlockResult, idx) + 4 * lane;
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(k) : "r"(ak) : "memory");
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(i) : "r"(ai) : "memory");
                 }
+                const bool entry = k != KEY_NONE;
+                const int n = __popc(__ballot_sync(0xffffffffu, entry));
+                __syncthreads();  // every read of this block's own lists is over
+                if (lane < LOGPROB_MAX_TOP) {
+                    wkey[warp][lane] = k;
+                    widx[warp][lane] = i;
+                }
+                if (lane == 0) wcnt[warp] = n;
+                __syncthreads();
+                if (entry) {
+                    const int place = place_of(k, i, wkey, widx, wcnt, csize);
+                    if (place < p.top) {
+                        res.key[place] = k;
+                        res.idx[place] = i;
+                    }
+                }
+                __syncthreads();
             }
         }
         __syncwarp();
@@ -286,8 +365,8 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
         }
     }
     if (TOP && lane < p.top) {
-        p.top_index[row * p.top + lane] = L.idx;
-        p.top_logprob[row * p.top + lane] = none ? -INFINITY : (key_value(L.key) - st.m) - ls;
+        p.top_index[row * p.top + lane] = res.idx[lane];
+        p.top_logprob[row * p.top + lane] = none ? -INFINITY : (key_value(res.key[lane]) - st.m) - ls;
     }
 }
 
@@ -297,16 +376,41 @@ constexpr int BWD_THREADS = 256;
 struct GradRow {
     float u, v, lse, h;
     int hit;
-    bool none;
 };
 
-template <typename T, bool ENT>
+// Gradients of N elements (the target's own term apart), in place.
+template <int N, bool ENT>
+__device__ __forceinline__ void grads_of(float (&f)[N], const GradRow& r) {
+    const uint64_t nl = f2_pack(-r.lse, -r.lse), l2e = f2_pack(LOG2E, LOG2E), nu = f2_pack(-r.u, -r.u);
+    const uint64_t ln2 = f2_pack(LN2, LN2), h = f2_pack(r.h, r.h), nv = f2_pack(-r.v, -r.v);
+    float d[N];
+    float bad = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const uint64_t y = f2_mul(f2_add(f2_pack(f[i], f[i + 1]), nl), l2e);
+        const uint64_t pr = f2_pack(ex2(f2_lo(y)), ex2(f2_hi(y)));
+        // p (-v (log p + H) - u)
+        const uint64_t g = f2_mul(pr, ENT ? f2_fma(nv, f2_fma(y, ln2, h), nu) : nu);
+        d[i] = f2_lo(g);
+        d[i + 1] = f2_hi(g);
+        if (ENT) bad += d[i] + d[i + 1];
+    }
+    if (ENT && bad != bad) {  // a masked logit: 0 times infinity
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float y = max_nan((f[i] - r.lse) * LOG2E, -200.f);
+            d[i] = ex2(y) * fmaf(-r.v, fmaf(y, LN2, r.h), -r.u);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = d[i];
+}
+template <bool ENT>
 __device__ __forceinline__ float grad_of(float x, int col, const GradRow& r) {
     const float y = max_nan((x - r.lse) * LOG2E, -200.f);
-    const float pr = ex2(y);
-    float d = ENT ? -pr * fmaf(r.v, fmaf(y, LN2, r.h), r.u) : -pr * r.u;
+    float d = ENT ? ex2(y) * fmaf(-r.v, fmaf(y, LN2, r.h), -r.u) : -ex2(y) * r.u;
     if (col == r.hit) d += r.u;
-    return r.none ? 0.f : d;
+    return d;
 }
 
 template <typename T, bool ENT>
@@ -318,7 +422,7 @@ __global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobG
     T* dx = static_cast<T*>(p.dlogits) + row * p.ldd;
     GradRow r;
     r.lse = p.lse[row];
-    r.none = r.lse == -INFINITY;
+    const bool none = r.lse == -INFINITY;  // no distribution: the gradient is zero
     r.u = p.grad_logprob ? p.grad_logprob[row] : 0.f;
     r.v = ENT ? p.grad_entropy[row] : 0.f;
     r.h = ENT ? p.entropy[row] : 0.f;
@@ -330,6 +434,7 @@ __global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobG
         else if (t >= p.vocab) r.u = __int_as_float(0x7fc00000);
         else r.hit = static_cast<int>(t);
     }
+    auto one = [&](int c) { dx[c] = Elem<T>::store(none ? 0.f : grad_of<ENT>(Elem<T>::load(x[c]), c, r)); };
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
     const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
     if (vec) {
@@ -338,14 +443,11 @@ __global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobG
         const int tail0 = head + nvec * E;
         const int per = (nvec + segs - 1) / segs;
         const int v0 = min(seg * per, nvec), v1 = min(v0 + per, nvec);
-        if (seg == 0 && threadIdx.x < head)
-            dx[threadIdx.x] = Elem<T>::store(grad_of<T, ENT>(Elem<T>::load(x[threadIdx.x]), threadIdx.x, r));
-        if (seg == segs - 1 && threadIdx.x < p.vocab - tail0) {
-            const int c = tail0 + threadIdx.x;
-            dx[c] = Elem<T>::store(grad_of<T, ENT>(Elem<T>::load(x[c]), c, r));
-        }
+        if (seg == 0 && threadIdx.x < head) one(threadIdx.x);
+        if (seg == segs - 1 && threadIdx.x < p.vocab - tail0) one(tail0 + threadIdx.x);
         const uint4* xv = reinterpret_cast<const uint4*>(x + head);
         uint4* dv = reinterpret_cast<uint4*>(dx + head);
+        const int hitv = r.hit >= head ? (r.hit - head) / E : -1;  // the vector of the target
         for (int base = v0 + threadIdx.x; base < v1; base += BWD_THREADS * UNROLL) {
             uint4 raw[UNROLL];
 #pragma unroll
@@ -357,8 +459,18 @@ __global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobG
                 if (i < v1) {
                     float f[E];
                     Elem<T>::unpack(raw[u], f);
+                    if (none) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) f[e] = grad_of<T, ENT>(f[e], head + i * E + e, r);
+                        for (int e = 0; e < E; ++e) f[e] = 0.f;
+                    } else {
+                        grads_of<E, ENT>(f, r);
+                        if (i == hitv) {
+                            const int at = r.hit - head - i * E;
+#pragma unroll
+                            for (int e = 0; e < E; ++e)
+                                if (e == at) f[e] += r.u;
+                        }
+                    }
                     __stcs(dv + i, Elem<T>::pack(f));
                 }
             }
@@ -367,8 +479,7 @@ __global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobG
         // logits and gradient rows that sit differently to a 16-byte boundary: single elements
         const int per = (p.vocab + segs - 1) / segs;
         const int c1 = min((seg + 1) * per, p.vocab);
-        for (int c = seg * per + threadIdx.x; c < c1; c += BWD_THREADS)
-            dx[c] = Elem<T>::store(grad_of<T, ENT>(Elem<T>::load(x[c]), c, r));
+        for (int c = seg * per + threadIdx.x; c < c1; c += BWD_THREADS) one(c);
     }
 }
 

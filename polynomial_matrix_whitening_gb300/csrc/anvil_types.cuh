@@ -19,6 +19,12 @@ struct Elem;
 template <>
 struct Elem<float> {
     static constexpr int VEC = 4;  // elements in 16 bytes
+    static constexpr uint32_t NEG_INF = 0xff800000u;  // a 32-bit word of -inf values
+    // the larger of two words' values, NaN ignored
+    static __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    static __device__ __forceinline__ float word_max(uint32_t w) { return __uint_as_float(w); }
     static __device__ __forceinline__ float load(float v) { return v; }
     static __device__ __forceinline__ float store(float v) { return v; }
     static __device__ __forceinline__ void unpack(uint4 w, float* f) {
@@ -34,6 +40,15 @@ struct Elem<float> {
 template <>
 struct Elem<__nv_bfloat16> {
     static constexpr int VEC = 8;
+    static constexpr uint32_t NEG_INF = 0xff80ff80u;
+    static __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ float word_max(uint32_t w) {
+        return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
     static __device__ __forceinline__ float load(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __forceinline__ __nv_bfloat16 store(float v) { return __float2bfloat16_rn(v); }
     static __device__ __forceinline__ void unpack2(uint32_t w, float* f) {
@@ -58,6 +73,16 @@ struct Elem<__nv_bfloat16> {
 template <>
 struct Elem<__half> {
     static constexpr int VEC = 8;
+    static constexpr uint32_t NEG_INF = 0xfc00fc00u;
+    static __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ float word_max(uint32_t w) {
+        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        return fmaxf(r.x, r.y);
+    }
     static __device__ __forceinline__ float load(__half v) { return __half2float(v); }
     static __device__ __forceinline__ __half store(float v) { return __float2half_rn(v); }
     static __device__ __forceinline__ void unpack2(uint32_t w, float* f) {
@@ -79,6 +104,15 @@ struct Elem<__half> {
         return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
     }
 };
+
+// (a.x b.x + c.x, a.y b.y + c.y) on packed fp32 pairs, one rounding each
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float f2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
 // Streaming 16-byte load (read once) and store (not read again soon).
 __device__ __forceinline__ uint4 ldg_stream(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
