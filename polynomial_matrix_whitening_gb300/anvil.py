@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libanvil (include/anvil.h), the ANVIL bank step on GB300.
+"""Thin binding of libanvil (include/anvil.h), the ANVIL bank step on GB300: ctypes, and for
+the operators around the banks a native module that does the same with less time per call.
 
 Argument marshalling only: every step of the computation runs in libanvil's CUDA
 kernels.  Importing this module loads ``libanvil.so`` from this package directory and
@@ -41,8 +42,7 @@ KERNEL_KINDS = ("momentum", "norm_d", "normalize", "gram_norm", "gram", "sqpoly"
                 "xupdate_out", "tail_power", "tail_scale", "tail_apply", "adam", "cascade",
                 "norm_forward", "norm_backward", "norm_grads", "linear_prepare", "linear_product",
                 "linear_sum", "logprob", "logprob_backward")
-MAX_MAPS, MAX_BANKS = 16, 8
-MAX_TOP = 32
+MAX_MAPS, MAX_BANKS, MAX_TOP = 16, 8, 32
 
 
 class AnvilError(RuntimeError):
@@ -469,111 +469,37 @@ def adam_step(param, grad, exp_avg, exp_avg_sq, beta1, beta2, eps, step_size, ef
 
 # ---- the operators around the banks
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
-_F32, _BF16, _F16 = range(3)
-_dtype_codes = {}
-_torch = None
-
-# The checks below run on every call, ahead of kernels that may take two microseconds, so
-# they are written for few Python operations.
+_native = None
+_ENTRY_POINTS = ("layernorm_forward", "layernorm_backward_workspace_bytes", "layernorm_backward",
+                 "linear_workspace_bytes", "linear_forward", "linear_backward_workspace_bytes",
+                 "linear_backward", "token_logprobs", "token_logprobs_backward")
 
 
-def _get_torch():
-    global _torch
-    if _torch is None:
-        import torch
-        _dtype_codes.update({torch.float32: _F32, torch.bfloat16: _BF16, torch.float16: _F16})
-        _torch = torch
-    return _torch
-
-
-def _dtype_code(t, what):
-    code = _dtype_codes.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{what} must be fp32, bf16 or fp16, not {t.dtype}")
-    return code
-
-
-def _rows_of(t, what):
-    """(rows, width, row stride) of a tensor [..., width] taken as a matrix of contiguous
-    rows with one stride; refuses layouts that are not."""
-    shape = t.shape
-    if len(shape) == 2:
-        rows, width = shape
-        ld, inner = t.stride()
-    elif len(shape) < 1:
-        raise ValueError(f"{what} must have at least one dimension")
-    else:
-        strides = t.stride()
-        width, inner = shape[-1], strides[-1]
-        rows, ld = 1, width
-        for n, s in zip(shape[-2::-1], strides[-2::-1]):
-            if n != 1:
-                if rows == 1:
-                    ld = s
-                elif s != ld * rows:
-                    raise ValueError(f"{what}: leading dimensions without one common row stride; use .contiguous()")
-                rows *= n
-    if inner != 1 and width > 1 and rows:
-        raise ValueError(f"{what}: rows must be contiguous (last stride 1); use .contiguous()")
-    if ld < width:
-        if rows > 1:
-            raise ValueError(f"{what}: rows overlap (row stride {ld}, width {width}); use .contiguous()")
-        ld = width
-    return rows, width, ld
-
-
-def _vector(t, n, dtypes, what):
-    """Pointer of a contiguous vector of n values."""
-    if t.dtype not in dtypes or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
-        raise ValueError(f"{what} must be a contiguous vector of {n} values of {' or '.join(map(str, dtypes))}")
-    return t.data_ptr()
-
-
-def _per_row(t, rows, what):
-    """Pointer of an optional contiguous fp32 tensor of one value per row."""
-    if t is None:
-        return 0
-    if t.dtype != _torch.float32 or t.numel() != rows or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous fp32, one value per row")
-    return t.data_ptr()
-
-
-def _same_form(t, shape, dtype, what, like):
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{what} must have {like}")
-
-
-def _current_stream(what, tensors):
-    """Handle of the current stream, after checking that every tensor is on the current GPU."""
-    if not tensors[0].is_cuda:
-        raise ValueError(f"{what}: every tensor must be on the current CUDA device")
-    index = _torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{what}: every tensor must be on the current CUDA device")
-    return _torch._C._cuda_getCurrentRawStream(index)
+def _load_native():
+    """The native module that checks the arguments of the calls below, allocates their
+    results and calls libanvil (csrc/binding.cpp; build.py makes it)."""
+    global _native
+    import torch
+    try:
+        from . import _anvil_binding as native
+    except ImportError as e:
+        raise ImportError("_anvil_binding is not built; run the package's build.py") from e
+    native.set_library(tuple(ctypes.cast(getattr(_lib, "anvil_" + n), ctypes.c_void_p).value
+                             for n in _ENTRY_POINTS), _check, torch.OutOfMemoryError)
+    _native = native
+    return native
 
 
 def _on_stream(stream, call, tensors):
     """Runs call() with `stream` current, so that its results and scratch belong to it, and
     tells the allocator that the inputs are in use there."""
-    torch = _get_torch()
+    import torch
     s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
         for t in tensors:
             if t is not None and t.is_cuda:
                 t.record_stream(s)
         return call()
-
-
-def _scratch(nbytes, workspace, ref):
-    """(tensor to keep, pointer, bytes) of a call's workspace: the caller's, or a new one."""
-    if workspace is not None:
-        return (workspace,) + _workspace_arg(workspace, ref)
-    if nbytes == 0:
-        return None, 0, 0
-    t = _torch.empty(nbytes, dtype=_torch.uint8, device=ref.device)
-    return t, t.data_ptr(), nbytes
 
 
 def layernorm_forward(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
@@ -585,35 +511,7 @@ def layernorm_forward(x, weight=None, bias=None, eps=1e-5, out=None, stream=None
     """
     if stream is not None:
         return _on_stream(stream, lambda: layernorm_forward(x, weight, bias, eps, out), (x, weight, bias, out))
-    torch = _torch or _get_torch()
-    code, dtype = _dtype_code(x, "x"), x.dtype
-    rows, width, ldx = _rows_of(x, "x")
-    wcode, wp, bp = code, 0, 0
-    if weight is not None or bias is not None:
-        wt = (bias if weight is None else weight).dtype
-        if wt != dtype:
-            if wt != torch.float32:
-                raise ValueError("weight and bias must be fp32 or of x's type")
-            wcode = _F32
-        if weight is not None:
-            wp = _vector(weight, width, (wt,), "weight")
-        if bias is not None:
-            bp = _vector(bias, width, (wt,), "bias")
-    s = _current_stream("layernorm_forward", (x, weight, bias, out))
-    if out is None:
-        y, ldy = torch.empty(x.shape, dtype=dtype, device=x.device), width
-    else:
-        y = out
-        _same_form(y, x.shape, dtype, "out", "x's shape and type")
-        ldy = _rows_of(y, "out")[2]
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
-    d = LayernormDesc(x.data_ptr(), wp, bp, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows, ldx, ldy, width,
-                      code, wcode, eps)
-    st = _lib.anvil_layernorm_forward(d, s)
-    if st:
-        _check(st, "anvil_layernorm_forward")
-    return y, mean, rstd
+    return (_native or _load_native()).layernorm_forward(x, weight, bias, eps, out)
 
 
 def layernorm_backward(dy, x, mean, rstd, weight=None, residual_grad=None, out=None, weight_grads=True,
@@ -628,54 +526,8 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, residual_grad=None, out=N
         return _on_stream(stream, lambda: layernorm_backward(dy, x, mean, rstd, weight, residual_grad, out,
                                                              weight_grads, workspace),
                           (dy, x, mean, rstd, weight, residual_grad, out, workspace))
-    torch = _torch or _get_torch()
-    code, dtype, shape = _dtype_code(x, "x"), x.dtype, x.shape
-    rows, width, ldx = _rows_of(x, "x")
-    _same_form(dy, shape, dtype, "dy", "x's shape and type")
-    lddy, ldr, rp = _rows_of(dy, "dy")[2], 0, 0
-    if residual_grad is not None:
-        _same_form(residual_grad, shape, dtype, "residual_grad", "x's shape and type")
-        ldr, rp = _rows_of(residual_grad, "residual_grad")[2], residual_grad.data_ptr()
-    mp, sp = _per_row(mean, rows, "mean"), _per_row(rstd, rows, "rstd")
-    wcode, wp = code, 0
-    if weight is not None:
-        if weight.dtype != dtype:
-            if weight.dtype != torch.float32:
-                raise ValueError("weight must be fp32 or of x's type")
-            wcode = _F32
-        wp = _vector(weight, width, (weight.dtype,), "weight")
-    s = _current_stream("layernorm_backward", (x, dy, mean, rstd, weight, residual_grad, out, workspace))
-    if out is None:
-        dx, lddx = torch.empty(shape, dtype=dtype, device=x.device), width
-    else:
-        dx = out
-        _same_form(dx, shape, dtype, "out", "x's shape and type")
-        lddx = _rows_of(dx, "out")[2]
-    dw, db, dwp, dbp = None, None, 0, 0
-    if weight_grads:
-        dw = torch.empty((width,), dtype=torch.float32, device=x.device)
-        db = torch.empty_like(dw)
-        dwp, dbp = dw.data_ptr(), db.data_ptr()
-    d = LayernormGradDesc(dy.data_ptr(), x.data_ptr(), mp, sp, wp, rp, dx.data_ptr(), dwp, dbp, rows, lddy, ldx, ldr,
-                          lddx, width, code, wcode)
-    keep, wsp, wsb = _scratch(_lib.anvil_layernorm_backward_workspace_bytes(d), workspace, x)
-    st = _lib.anvil_layernorm_backward(d, wsp, wsb, s)
-    if st:
-        _check(st, "anvil_layernorm_backward")
-    return dx, dw, db
-
-
-def _weight_of(w, dtype, what):
-    """(n, k, row stride, transposed) of a weight [n, k] stored by rows or by columns."""
-    shape = w.shape
-    if len(shape) != 2 or w.dtype != dtype:
-        raise ValueError(f"{what} must be [n, k] of {dtype}")
-    (n, k), (s0, s1) = shape, w.stride()
-    if (s1 == 1 or k == 1) and (s0 >= k or n == 1):
-        return n, k, s0 if s0 > k else k, 0
-    if (s0 == 1 or n == 1) and (s1 >= n or k == 1):
-        return n, k, s1 if s1 > n else n, 1
-    raise ValueError(f"{what} must be stored by rows or by columns; use .contiguous()")
+    return (_native or _load_native()).layernorm_backward(dy, x, mean, rstd, weight, residual_grad, out, weight_grads,
+                                                          workspace)
 
 
 def _activation(name):
@@ -683,17 +535,6 @@ def _activation(name):
     if code is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
     return code
-
-
-def _linear_sizes(x, weight):
-    code = _dtype_code(x, "x")
-    if code == _F32:
-        raise ValueError("x must be bf16 or fp16")
-    rows, k, ldx = _rows_of(x, "x")
-    n, wk, ldw, tr = _weight_of(weight, x.dtype, "weight")
-    if wk != k:
-        raise ValueError(f"weight must be [n, {k}]")
-    return code, rows, k, ldx, n, ldw, tr
 
 
 def linear_forward(x, weight, bias=None, activation=None, residual=None, save_preact=False, out=None,
@@ -708,35 +549,8 @@ def linear_forward(x, weight, bias=None, activation=None, residual=None, save_pr
         return _on_stream(stream, lambda: linear_forward(x, weight, bias, activation, residual, save_preact, out,
                                                          workspace),
                           (x, weight, bias, residual, out, workspace))
-    torch = _torch or _get_torch()
-    code, rows, k, ldx, n, ldw, tr = _linear_sizes(x, weight)
-    act = _activation(activation)
-    dtype, bp, bcode, rp, ldr, zp = x.dtype, 0, code, 0, 0, 0
-    if bias is not None:
-        bp = _vector(bias, n, (dtype, torch.float32), "bias")
-        if bias.dtype != dtype:
-            bcode = _F32
-    shape = x.shape[:-1] + (n,)
-    if residual is not None:
-        _same_form(residual, shape, dtype, "residual", "the result's shape and type")
-        rp, ldr = residual.data_ptr(), _rows_of(residual, "residual")[2]
-    s = _current_stream("linear_forward", (x, weight, bias, residual, out, workspace))
-    if out is None:
-        y, ldy = torch.empty(shape, dtype=dtype, device=x.device), n
-    else:
-        y = out
-        _same_form(y, shape, dtype, "out", "the result's shape and type")
-        ldy = _rows_of(y, "out")[2]
-    z = None
-    if save_preact:
-        z = torch.empty(shape, dtype=dtype, device=x.device)
-        zp = z.data_ptr()
-    d = LinearDesc(x.data_ptr(), weight.data_ptr(), bp, rp, y.data_ptr(), zp, rows, ldx, ldw, ldr, ldy, n, n, k, code,
-                   bcode, act, tr)
-    keep, wsp, wsb = _scratch(_lib.anvil_linear_workspace_bytes(d), workspace, x)
-    st = _lib.anvil_linear_forward(d, wsp, wsb, s)
-    if st:
-        _check(st, "anvil_linear_forward")
+    y, z = (_native or _load_native()).linear_forward(x, weight, bias, _activation(activation), residual, save_preact,
+                                                      out, workspace)
     return (y, z) if save_preact else y
 
 
@@ -754,58 +568,12 @@ def linear_backward(dy, x, weight, preact=None, activation=None, need_dx=True, n
                                                           bias_grad, dweight_dtype, dweight, dbias, accumulate,
                                                           workspace),
                           (dy, x, weight, preact, dweight, dbias, workspace))
-    torch = _torch or _get_torch()
-    code, rows, k, ldx, n, ldw, tr = _linear_sizes(x, weight)
-    act, dtype = _activation(activation), x.dtype
-    _same_form(dy, x.shape[:-1] + (n,), dtype, "dy", "the forward result's shape and type")
-    lddy, zp, ldz = _rows_of(dy, "dy")[2], 0, 0
-    if act:
-        if preact is None:
-            raise ValueError("preact is needed with an activation")
-        _same_form(preact, dy.shape, dtype, "preact", "the forward result's shape and type")
-        zp, ldz = preact.data_ptr(), _rows_of(preact, "preact")[2]
-    if accumulate and ((need_dweight and dweight is None) or (bias_grad and dbias is None)):
-        raise ValueError("accumulate needs dweight and dbias to add to")
-    wt = dweight.dtype if dweight is not None else dweight_dtype or dtype
-    if wt != dtype and wt != torch.float32:
+    fp32 = dweight_dtype is not None and dweight_dtype != x.dtype
+    if fp32 and str(dweight_dtype) != "torch.float32":
         raise ValueError("dweight must be fp32 or of x's type")
-    s = _current_stream("linear_backward", (x, dy, weight, preact, dweight, dbias, workspace))
-    dx, dxp, dwp, lddw, dbp = None, 0, 0, 0, 0
-    if need_dx:
-        dx = torch.empty(x.shape, dtype=dtype, device=x.device)
-        dxp = dx.data_ptr()
-    if need_dweight:
-        if dweight is None:
-            dweight = torch.empty((k, n) if tr else (n, k), dtype=wt, device=x.device)
-            lddw = n if tr else k
-            if tr:
-                dweight = dweight.t()
-        else:
-            dn, dk, lddw, dtr = _weight_of(dweight, wt, "dweight")
-            if (dn, dk) != (n, k) or (dtr != tr and n > 1 and k > 1):
-                raise ValueError("dweight must have weight's shape and order")
-        dwp = dweight.data_ptr()
-    if bias_grad:
-        if dbias is None:
-            dbias = torch.empty((n,), dtype=torch.float32, device=x.device)
-        dbp = _vector(dbias, n, (torch.float32,), "dbias")
-    d = LinearGradDesc(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), zp, dxp, dwp, dbp, rows, lddy, ldx, ldw, ldz, k,
-                       lddw, n, k, code, code if wt == dtype else _F32, act, tr, 1 if accumulate else 0)
-    keep, wsp, wsb = _scratch(_lib.anvil_linear_backward_workspace_bytes(d), workspace, x)
-    st = _lib.anvil_linear_backward(d, wsp, wsb, s)
-    if st:
-        _check(st, "anvil_linear_backward")
-    return dx, dweight if need_dweight else None, dbias if bias_grad else None
-
-
-def _targets_arg(targets, rows):
-    """(pointer, whether int64) of optional target tokens."""
-    if targets is None:
-        return 0, 0
-    wide = targets.dtype == _torch.int64
-    if not (wide or targets.dtype == _torch.int32) or targets.numel() != rows or not targets.is_contiguous():
-        raise ValueError("targets must be contiguous int64 or int32, one per row")
-    return targets.data_ptr(), 1 if wide else 0
+    return (_native or _load_native()).linear_backward(dy, x, weight, preact, _activation(activation), need_dx,
+                                                       need_dweight, bias_grad, fp32, dweight, dbias, accumulate,
+                                                       workspace)
 
 
 def token_logprobs(logits, targets=None, top=0, stream=None):
@@ -817,32 +585,7 @@ def token_logprobs(logits, targets=None, top=0, stream=None):
     """
     if stream is not None:
         return _on_stream(stream, lambda: token_logprobs(logits, targets, top), (logits, targets))
-    torch = _torch or _get_torch()
-    code = _dtype_code(logits, "logits")
-    rows, vocab, ld = _rows_of(logits, "logits")
-    if not 0 <= top <= (vocab if vocab < MAX_TOP else MAX_TOP):
-        raise ValueError(f"top must be between 0 and {MAX_TOP} and at most the vocabulary")
-    tp, t64 = _targets_arg(targets, rows)
-    s = _current_stream("token_logprobs", (logits, targets))
-    lead, dev = logits.shape[:-1], logits.device
-    lse = torch.empty(lead, dtype=torch.float32, device=dev)
-    ent = torch.empty_like(lse)
-    lp, lpp, tv, ti, tvp, tip = None, 0, None, None, 0, 0
-    if tp:
-        lp = torch.empty_like(lse)
-        lpp = lp.data_ptr()
-    elif targets is not None:
-        lp = torch.empty_like(lse)  # no rows
-    if top:
-        tv = torch.empty(lead + (top,), dtype=torch.float32, device=dev)
-        ti = torch.empty(lead + (top,), dtype=torch.int32, device=dev)
-        tvp, tip = tv.data_ptr(), ti.data_ptr()
-    d = LogprobDesc(logits.data_ptr(), tp, lpp, ent.data_ptr(), lse.data_ptr(), tvp, tip, rows, ld, vocab, top, code,
-                    t64)
-    st = _lib.anvil_token_logprobs(d, s)
-    if st:
-        _check(st, "anvil_token_logprobs")
-    return lp, ent, lse, tv, ti
+    return (_native or _load_native()).token_logprobs(logits, targets, top)
 
 
 def token_logprobs_backward(logits, targets, lse, grad_logprob=None, entropy=None, grad_entropy=None, out=None,
@@ -853,30 +596,8 @@ def token_logprobs_backward(logits, targets, lse, grad_logprob=None, entropy=Non
         return _on_stream(stream, lambda: token_logprobs_backward(logits, targets, lse, grad_logprob, entropy,
                                                                   grad_entropy, out),
                           (logits, targets, lse, grad_logprob, entropy, grad_entropy, out))
-    torch = _torch or _get_torch()
-    code = _dtype_code(logits, "logits")
-    rows, vocab, ld = _rows_of(logits, "logits")
-    tp, t64 = _targets_arg(targets, rows)
-    if grad_logprob is not None and targets is None:
-        raise ValueError("grad_logprob needs targets")
-    if grad_entropy is not None and entropy is None:
-        raise ValueError("grad_entropy needs entropy")
-    if lse is None:
-        raise ValueError("lse is needed")
-    lp, ep = _per_row(lse, rows, "lse"), _per_row(entropy, rows, "entropy")
-    up, vp = _per_row(grad_logprob, rows, "grad_logprob"), _per_row(grad_entropy, rows, "grad_entropy")
-    s = _current_stream("token_logprobs_backward", (logits, targets, lse, grad_logprob, entropy, grad_entropy, out))
-    if out is None:
-        dl, ldd = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), vocab
-    else:
-        dl = out
-        _same_form(dl, logits.shape, logits.dtype, "out", "the logits' shape and type")
-        ldd = _rows_of(dl, "out")[2]
-    d = LogprobGradDesc(logits.data_ptr(), tp, lp, ep, up, vp, dl.data_ptr(), rows, ld, ldd, vocab, code, t64)
-    st = _lib.anvil_token_logprobs_backward(d, s)
-    if st:
-        _check(st, "anvil_token_logprobs_backward")
-    return dl
+    return (_native or _load_native()).token_logprobs_backward(logits, targets, lse, grad_logprob, entropy,
+                                                               grad_entropy, out)
 
 
 def schedule_runs(shapes, nmaps=6):

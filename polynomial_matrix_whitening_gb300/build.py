@@ -3,12 +3,14 @@
 Each .cu under csrc/ compiles to its own object in parallel; the objects link into
 ``polynomial_matrix_whitening_gb300/libanvil.so`` with the CUDA runtime linked
 statically, so the library loads (and exports its symbols) on a machine without a
-GPU driver as well.
+GPU driver as well.  csrc/binding.cpp, the native part of the Python binding, compiles with
+g++ against the installed PyTorch's headers into ``_anvil_binding.so`` beside it.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -28,6 +30,10 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-r
               "-I" + os.path.join(ROOT, "include")] + ARCH
 
 
+# The native part of the Python binding: a CPython extension module.
+BINDING = os.path.join(PKG, "_anvil_binding.so")
+
+
 def nvcc():
     path = shutil.which("nvcc")
     if path:
@@ -43,6 +49,22 @@ def _stale(target, deps):
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def binding_command():
+    """The g++ call that compiles csrc/binding.cpp into a file named last."""
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found: its headers are required to build the binding")
+    torch = spec.submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    lib = os.path.join(torch, "lib")
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall"]
+            + ["-isystem" + d for d in inc] + [os.path.join(CSRC, "binding.cpp"), "-L" + lib, "-ltorch_python",
+                                               "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib, "-o"])
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), timeline: bool = False) -> str:
@@ -61,6 +83,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), timeline: 
         obj = os.path.join(build_dir, os.path.basename(src)[:-3] + ".o")
         if force or _stale(obj, [src] + headers):
             jobs.append([cc, "-c", src, "-o", obj] + NVCC_FLAGS + list(extra_flags))
+    linked = bool(jobs)
+    binding = os.path.join(CSRC, "binding.cpp")
+    binding_tmp = BINDING + f".tmp{os.getpid()}"
+    # named by the interpreter's torch too: a module built against another one is stale
+    stamp = os.path.join(BUILD, "binding.torch")
+    flags = " ".join(binding_command())
+    make_binding = force or _stale(BINDING, [binding] + headers) or not os.path.exists(stamp) \
+        or open(stamp).read() != flags
+    if make_binding:
+        jobs.append(binding_command() + [binding_tmp])
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
             results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -68,9 +100,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), timeline: 
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed on {cmd[2]}")
+                raise RuntimeError(f"{os.path.basename(cmd[0])} failed on "
+                                   + next(a for a in cmd if a.endswith((".cu", ".cpp"))))
+    if make_binding:
+        os.replace(binding_tmp, BINDING)
+        os.makedirs(BUILD, exist_ok=True)
+        with open(stamp, "w") as f:
+            f.write(flags)
     objs = [os.path.join(build_dir, os.path.basename(s)[:-3] + ".o") for s in sources]
-    if force or jobs or _stale(lib, objs):
+    if force or linked or _stale(lib, objs):
         tmp = lib + f".tmp{os.getpid()}"
         cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static"]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -13,12 +13,13 @@
 // rate, not HBM, was the bound.
 //
 // The top k are found in the same pass.  A warp holds the best k it has met, one per lane
-// in order; putting one in costs tens of cycles, so few may be tried.  Each thread of a
-// block has the largest of its 32 (fp32: 16) values of a turn at hand; the k-th largest of those 256
-// maxima is a value that at least k elements reach, so everything below it is passed over.
-// It is found on the upper 16 bits of the ordered values by 16 counting barriers, on the
-// first turn and whenever more than 2k threads of a turn hold something new.  In the end
-// every entry of the eight lists counts the entries ahead of it: its place.
+// in order; putting one in costs tens of instructions, so few may be tried.  Each of a
+// block's eight warps publishes its four best values (first the largest of its threads'
+// maxima of the first turn, later the head of its list); the k-th largest of those 32 is a
+// value that at least k elements reach, and what lies below it is passed over.  It is read
+// without a barrier (a stale one is only lower), and a warp looks at single values only of
+// vectors whose maximum reaches it.  In the end every entry of the eight lists counts the
+// entries ahead of it: its place.
 //
 // HBM bounds both passes where there are many rows; where rows are fewer than the SMs, a
 // cluster of up to eight blocks takes a row's segments and the first block joins their
@@ -61,16 +62,28 @@ __device__ __forceinline__ float ex2(float x) {
 struct Stats {
     float m, s, q;
 };
-// a and b over the larger of their maxima; empty sides have m = -inf, s = q = 0.
-__device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
-    Stats r;
-    r.m = fmaxf(a.m, b.m);
-    const float m0 = r.m == -INFINITY ? 0.f : r.m;
-    const float da = fmaxf((a.m - m0) * LOG2E, -200.f), db = fmaxf((b.m - m0) * LOG2E, -200.f);
-    const float ca = ex2(da), cb = ex2(db);
-    r.s = a.s * ca + b.s * cb;
-    r.q = ca * (a.q + da * a.s) + cb * (b.q + db * b.s);
-    return r;
+// Statistics over a larger maximum.
+__device__ __forceinline__ Stats over(Stats a, float m) {
+    const float d = fmaxf((a.m - (m == -INFINITY ? 0.f : m)) * LOG2E, -200.f), c = ex2(d);
+    a.q = c * (a.q + d * a.s);
+    a.s *= c;
+    a.m = m;
+    return a;
+}
+// The statistics of W lanes together, in every one of them: one rescaling to their common
+// maximum, then plain sums.  Empty lanes have m = -inf, s = q = 0.
+template <int W>
+__device__ __forceinline__ Stats join(Stats a) {
+    float m = a.m;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    a = over(a, m);
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+        a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+        a.q += __shfl_xor_sync(0xffffffffu, a.q, o);
+    }
+    return a;
 }
 
 // Order of the alternatives: larger value first, then lower index.  Floats compare as the
@@ -112,6 +125,16 @@ __device__ __forceinline__ void top_offer(TopList& L, int top, int lane, bool ca
     }
 }
 
+// The k-th largest of 32 lanes' keys, to 16 bits (below it where cut).
+__device__ __forceinline__ int kth_largest(int key, int k) {
+    const uint32_t u = static_cast<uint32_t>(key) ^ 0x80000000u;
+    uint32_t cut = 0;
+#pragma unroll
+    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
+        if (__popc(__ballot_sync(0xffffffffu, u >= (cut | bit))) >= k) cut |= bit;
+    return static_cast<int>(cut ^ 0x80000000u);
+}
+
 constexpr int FWD_THREADS = 256;
 constexpr int FWD_WARPS = FWD_THREADS / 32;
 constexpr int UNROLL = 4;  // 16-byte loads in flight per thread
@@ -140,29 +163,48 @@ __device__ __forceinline__ void take_one(Stats& st, float v) {
     st.s += e;
     st.q = fmaf(e, y, st.q);
 }
-// N values, none above st.m.  The difference comes before the factor log2 e: a maximum of
-// the type's lowest value (a row masked with it) times log2 e would overflow.
-template <int N>
-__device__ __forceinline__ void take(Stats& st, const float (&v)[N]) {
+// The first `cnt` of N vectors of values, none above st.m.  The difference comes before the factor log2 e: a
+// maximum of the type's lowest value (a row masked with it) times log2 e would overflow.
+template <typename T, int N>
+__device__ __forceinline__ void take(Stats& st, const uint4 (&raw)[N], int cnt) {
+    constexpr int E = Elem<T>::VEC;
     const float m0 = st.m == -INFINITY ? 0.f : st.m;
-    const uint64_t nm = f2_pack(-m0, -m0), l2e = f2_pack(LOG2E, LOG2E);
+    const uint64_t nm = f2_make(-m0, -m0), l2e = f2_make(LOG2E, LOG2E);
     uint64_t s2 = 0, q2 = 0;
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const uint64_t y = f2_mul(f2_add(f2_pack(v[i], v[i + 1]), nm), l2e);
-        const uint64_t e = f2_pack(ex2(f2_lo(y)), ex2(f2_hi(y)));
-        s2 = f2_add(s2, e);
-        q2 = f2_fma(e, y, q2);
+    for (int u = 0; u < N; ++u) {
+        if (u >= cnt) break;
+        uint64_t v[E / 2];
+        Elem<T>::unpack_pairs(raw[u], v);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            const uint64_t y = f2_mul(f2_add(v[i], nm), l2e);
+            float y0, y1;
+            f2_split(y, &y0, &y1);
+            const uint64_t e = f2_make(ex2(y0), ex2(y1));
+            s2 = f2_add(s2, e);
+            q2 = f2_fma(e, y, q2);
+        }
     }
-    float s = f2_lo(s2) + f2_hi(s2), q = f2_lo(q2) + f2_hi(q2);
+    float s, q, sh, qh;
+    f2_split(s2, &s, &sh);
+    f2_split(q2, &q, &qh);
+    s += sh;
+    q += qh;
     if (q != q) {
         s = q = 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float y = max_nan((v[i] - m0) * LOG2E, -200.f);
-            const float e = ex2(y);
-            s += e;
-            q = fmaf(e, y, q);
+        for (int u = 0; u < N; ++u) {
+            if (u >= cnt) break;
+            float v[E];
+            Elem<T>::unpack(raw[u], v);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float y = max_nan((v[i] - m0) * LOG2E, -200.f);
+                const float e = ex2(y);
+                s += e;
+                q = fmaf(e, y, q);
+            }
         }
     }
     st.s += s;
@@ -181,10 +223,10 @@ __device__ __forceinline__ int place_of(int key, int idx, const int (*keys)[LOGP
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobParams p, int csize) {
     constexpr int E = Elem<T>::VEC;
-    constexpr int CH = E * UNROLL;
     __shared__ Stats wst[FWD_WARPS];
     __shared__ int wkey[TOP ? FWD_WARPS : 1][LOGPROB_MAX_TOP], widx[TOP ? FWD_WARPS : 1][LOGPROB_MAX_TOP];
     __shared__ int wcnt[FWD_WARPS];
+    __shared__ int best[32];  // the four best values of each warp
     __shared__ BlockResult res;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x / csize;
@@ -204,7 +246,6 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
     Stats st = {-INFINITY, 0.f, 0.f};
     TopList L;
     top_init(L);
-    int tau = KEY_NONE;  // at least `top` elements so far reach it: only larger ones matter
     // at most E - 1 single elements of the head and of the tail, a lane each of warp 0; the
     // tail comes after the vectors, so that warp 0 too sees its indexes grow
     auto singles = [&](int c0, int cnt) {
@@ -216,86 +257,90 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
     };
     if (warp == 0 && rank == 0) singles(0, head);
     const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+    // A warp's UNROLL vectors per lane are one run of 32 * UNROLL vectors, so the indexes a
+    // warp sees grow from turn to turn.
+    int tau = KEY_NONE;  // at least `top` of the block's elements reach it
     for (int base = v0; base < v1; base += FWD_THREADS * UNROLL) {
-        // a warp's UNROLL vectors per lane are one run of 32 * UNROLL vectors, so the indexes
-        // a warp sees grow from turn to turn (an equal value later never displaces)
-        const int wbase = base + warp * 32 * UNROLL + lane;
+        const int at = base + warp * 32 * UNROLL + lane;
         uint4 raw[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u)
-            raw[u] = wbase + u * 32 < v1 ? __ldcs(xv + wbase + u * 32)
-                                         : make_uint4(Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF);
-        uint32_t mw = Elem<T>::max_word(Elem<T>::max_word(raw[0].x, raw[0].y), Elem<T>::max_word(raw[0].z, raw[0].w));
+            raw[u] = at + u * 32 < v1 ? __ldcs(xv + at + u * 32)
+                                      : make_uint4(Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF);
+        uint32_t mw[UNROLL];  // the largest of each vector, as a word
 #pragma unroll
-        for (int u = 1; u < UNROLL; ++u)
-            mw = Elem<T>::max_word(mw, Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w)));
-        const float mx = Elem<T>::word_max(mw);
+        for (int u = 0; u < UNROLL; ++u)
+            mw[u] = Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w));
+        const float mx = Elem<T>::word_max(Elem<T>::max_word(Elem<T>::max_word(mw[0], mw[1]), Elem<T>::max_word(mw[2], mw[3])));
         raise_max(st, mx);
-        float v[CH];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) Elem<T>::unpack(raw[u], v + u * E);
-        take<CH>(st, v);  // slots past the end hold -inf and add 0
+        take<T, UNROLL>(st, raw, (v1 - at + 31) / 32);  // vectors at + 32 u < v1
         if constexpr (TOP) {
-            const int mk = wbase < v1 ? order_key(mx) : KEY_NONE;
-            const bool first = base == v0;
-            bool hold = wbase < v1 && (first || mk > tau);
-            int need = tau + 1;  // the least key that matters in this turn
-            const int holds = __syncthreads_count(hold);
-            if (first || holds > 2 * p.top) {
-                // the largest T of 16 bits that `top` of the threads' maxima reach (0 where the
-                // threads are fewer); keys in unsigned order
-                const uint32_t uk = static_cast<uint32_t>(mk) ^ 0x80000000u;
-                uint32_t t = 0;
-#pragma unroll 1
-                for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
-                    if (__syncthreads_count(hold && uk >= (t | bit)) >= p.top) t |= bit;
-                const int tk = static_cast<int>(t ^ 0x80000000u);
-                need = tk > need ? tk : need;
-                tau = tk > tau ? tk : tau;
-                hold = hold && mk >= need;
-            }
-            if (holds && __any_sync(0xffffffffu, hold)) {
+            const int mk = at < v1 ? order_key(mx) : KEY_NONE;
+            if (base == v0) {
+                int rest = mk;
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int vec = wbase + (i / E) * 32;
-                    const int key = order_key(v[i]);
-                    const bool cand = hold && vec < v1 && key >= need;
-                    if (__any_sync(0xffffffffu, cand)) top_offer(L, p.top, lane, cand, key, head + vec * E + i % E);
+                for (int c = 0; c < 4; ++c) {
+                    const int m = __reduce_max_sync(0xffffffffu, rest);
+                    const unsigned who = __ballot_sync(0xffffffffu, rest == m);
+                    if (lane == __ffs(who) - 1) rest = KEY_NONE;
+                    if (lane == 0) best[warp * 4 + c] = m;
                 }
+                __syncthreads();
+            }
+            if (__any_sync(0xffffffffu, mk >= tau && mk > L.kth_key)) {
+                const int r = kth_largest(static_cast<volatile int*>(best)[lane], p.top);
+                tau = r > tau ? r : tau;
+                bool more = false;
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u) {
+                    const int vec = at + u * 32;
+                    const int vk = vec < v1 ? order_key(Elem<T>::word_max(mw[u])) : KEY_NONE;
+                    const bool hold = vk >= tau && vk > L.kth_key;
+                    if (__any_sync(0xffffffffu, hold)) {
+                        more = true;
+                        float v[E];
+                        Elem<T>::unpack(raw[u], v);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const int key = order_key(v[e]);
+                            const bool cand = hold && key >= tau;
+                            if (__any_sync(0xffffffffu, cand)) top_offer(L, p.top, lane, cand, key, head + vec * E + e);
+                        }
+                    }
+                }
+                if (more && lane < 4 && lane < p.top && L.key > best[warp * 4 + lane])
+                    static_cast<volatile int*>(best)[warp * 4 + lane] = L.key;
             }
         }
     }
     if (warp == 0 && rank == csize - 1) singles(tail0, p.vocab - tail0);
     // the block's result: lanes, then warps, in a fixed order
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stats b;
-        b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-        b.q = __shfl_xor_sync(0xffffffffu, st.q, o);
-        st = (lane & o) ? join(b, st) : join(st, b);
-    }
+    st = join<32>(st);
     if (lane == 0) wst[warp] = st;
     if constexpr (TOP) {
-        const bool entry = lane < p.top && L.key != KEY_NONE;
+        // the tail of the row and the lists as they ended (an empty block never published)
+        if (lane < 4 && lane < p.top) best[warp * 4 + lane] = L.key;
+        else if (lane < 4) best[warp * 4 + lane] = KEY_NONE;
+    }
+    __syncthreads();
+    if (warp == 0) st = join<FWD_WARPS>(wst[lane % FWD_WARPS]);
+    if constexpr (TOP) {
+        // the entries that may still count, a few more than `top`: lane l of warp w holds the
+        // l-th of list w
+        const int r = kth_largest(best[lane], p.top);
+        const bool entry = lane < p.top && L.key != KEY_NONE && L.key >= r;
         if (entry) {
             wkey[warp][lane] = L.key;
             widx[warp][lane] = L.idx;
         }
         const int n = __popc(__ballot_sync(0xffffffffu, entry));
         if (lane == 0) wcnt[warp] = n;
-    }
-    __syncthreads();
-    st = wst[0];
-    for (int w = 1; w < FWD_WARPS; ++w) st = join(st, wst[w]);
-    if constexpr (TOP) {
-        // lane l of warp w: the l-th entry of list w
         if (tid < LOGPROB_MAX_TOP) {
             res.key[tid] = KEY_NONE;
             res.idx[tid] = 0;
         }
         __syncthreads();
-        if (lane < wcnt[warp]) {
+        if (entry) {
             const int place = place_of(L.key, L.idx, wkey, widx, wcnt, FWD_WARPS);
             if (place < p.top) {
                 res.key[place] = L.key;
@@ -309,13 +354,15 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
         __syncwarp();
         cluster_sync();
         if (rank == 0) {
-            for (int r = 1; r < csize; ++r) {
-                const uint32_t a = map_to_rank(&res, r);
+            if (warp == 0) {
+                // eight lanes, four times over: the cluster's blocks (8 at most, a power of two)
+                const uint32_t a = map_to_rank(&res, lane % csize);
                 Stats b;
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(a) : "memory");
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(a + 4) : "memory");
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.q) : "r"(a + 8) : "memory");
-                st = join(st, b);
+                if ((lane & 7) >= csize) b = {-INFINITY, 0.f, 0.f};
+                st = join<8>(b);
             }
             if constexpr (TOP) {
                 // warp w takes the list of the cluster's block w
@@ -378,32 +425,37 @@ struct GradRow {
     int hit;
 };
 
-// Gradients of N elements (the target's own term apart), in place.
-template <int N, bool ENT>
-__device__ __forceinline__ void grads_of(float (&f)[N], const GradRow& r) {
-    const uint64_t nl = f2_pack(-r.lse, -r.lse), l2e = f2_pack(LOG2E, LOG2E), nu = f2_pack(-r.u, -r.u);
-    const uint64_t ln2 = f2_pack(LN2, LN2), h = f2_pack(r.h, r.h), nv = f2_pack(-r.v, -r.v);
-    float d[N];
-    float bad = 0.f;
+// Gradients of a vector of elements (the target's own term apart).
+template <typename T, bool ENT>
+__device__ __forceinline__ void grads_of(uint4 raw, float (&d)[Elem<T>::VEC], const GradRow& r) {
+    constexpr int E = Elem<T>::VEC;
+    const uint64_t nl = f2_make(-r.lse, -r.lse), l2e = f2_make(LOG2E, LOG2E), nu = f2_make(-r.u, -r.u);
+    const uint64_t ln2 = f2_make(LN2, LN2), h = f2_make(r.h, r.h), nv = f2_make(-r.v, -r.v);
+    uint64_t x[E / 2];
+    Elem<T>::unpack_pairs(raw, x);
+    uint64_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const uint64_t y = f2_mul(f2_add(f2_pack(f[i], f[i + 1]), nl), l2e);
-        const uint64_t pr = f2_pack(ex2(f2_lo(y)), ex2(f2_hi(y)));
+    for (int i = 0; i < E / 2; ++i) {
+        const uint64_t y = f2_mul(f2_add(x[i], nl), l2e);
+        float y0, y1;
+        f2_split(y, &y0, &y1);
+        const uint64_t pr = f2_make(ex2(y0), ex2(y1));
         // p (-v (log p + H) - u)
         const uint64_t g = f2_mul(pr, ENT ? f2_fma(nv, f2_fma(y, ln2, h), nu) : nu);
-        d[i] = f2_lo(g);
-        d[i + 1] = f2_hi(g);
-        if (ENT) bad += d[i] + d[i + 1];
+        f2_split(g, &d[2 * i], &d[2 * i + 1]);
+        if (ENT) sum = f2_add(sum, g);
     }
-    if (ENT && bad != bad) {  // a masked logit: 0 times infinity
+    float a, b;
+    f2_split(sum, &a, &b);
+    if (ENT && a + b != a + b) {  // a masked logit: 0 times infinity
+        float f[E];
+        Elem<T>::unpack(raw, f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < E; ++i) {
             const float y = max_nan((f[i] - r.lse) * LOG2E, -200.f);
             d[i] = ex2(y) * fmaf(-r.v, fmaf(y, LN2, r.h), -r.u);
         }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = d[i];
 }
 template <bool ENT>
 __device__ __forceinline__ float grad_of(float x, int col, const GradRow& r) {
@@ -458,12 +510,11 @@ __global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobG
                 const int i = base + u * BWD_THREADS;
                 if (i < v1) {
                     float f[E];
-                    Elem<T>::unpack(raw[u], f);
                     if (none) {
 #pragma unroll
                         for (int e = 0; e < E; ++e) f[e] = 0.f;
                     } else {
-                        grads_of<E, ENT>(f, r);
+                        grads_of<T, ENT>(raw[u], f, r);
                         if (i == hitv) {
                             const int at = r.hit - head - i * E;
 #pragma unroll

@@ -7,16 +7,20 @@
 //             dw_j = sum over rows of dy_j h_j,  db_j = sum over rows of dy_j
 //
 // Both passes read each input once and write each output once, so HBM bounds them.  A row
-// belongs to a team of threads that keeps it in registers between the reductions and the
-// store (the variance is taken from the centred values, in a second pass over registers,
-// not from a difference of large sums).
+// belongs to a team of threads that keeps it in registers, as it was loaded, between the
+// reductions and the store (the variance is taken from the centred values, in a second pass
+// over registers, not from a difference of large sums).  A block takes row after row, so a
+// thread has the same columns every time: it holds their weights in registers (loaded again
+// for every row, fp32 weights of 16-bit rows were four of the six 16-byte accesses per
+// vector, and shared memory's pipe the bound), and the next row's loads go out before this
+// row's sums.
 //
-// The weight's and bias's gradients are sums down the columns.  A thread holds the same
-// columns for every row its team takes, so the row pass adds them up in registers, then
-// across the teams of the block through shared memory, and leaves one row of partial sums
-// per block; norm_grads_kernel adds those up.  The order of every sum is fixed by the
-// sizes: no atomics, the same bits every time.
+// The weight's and bias's gradients are sums down the columns: a thread adds up its columns
+// in registers, the teams of a block join theirs through shared memory, and each block
+// leaves one row of partial sums; norm_grads_kernel adds those up.  The order of every sum
+// is fixed by the sizes: no atomics, the same bits every time.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "anvil_device.cuh"
@@ -36,17 +40,64 @@ struct Shape {
     static constexpr int CAP = TPR * NV * E;  // widest row
 };
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_unit(const T* p, float* f) {
-    if constexpr (VEC) Elem<T>::unpack(ldg_stream(p), f);
-    else f[0] = Elem<T>::load(*p);
+// Resident blocks per SM: the backward row pass 512 threads, at up to 128 registers each;
+// the forward one 1024 threads at 64 where a thread has at most 8 columns, else 512.
+constexpr int bwd_blocks_per_sm(int tpr) { return tpr <= 32 ? 2 : 512 / tpr; }
+constexpr int fwd_blocks_per_sm(int tpr, int columns) {
+    return tpr <= 32 ? 3 : (columns <= 8 ? 1024 : columns <= 16 ? 768 : 512) / tpr > 0 ? (columns <= 8 ? 1024 : columns <= 16 ? 768 : 512) / tpr : 1;
 }
+
+// A unit as it was loaded, unpacked where it is used (half the registers of fp32 values of
+// 16-bit types), and the arithmetic on it: packed fp32 pairs for vectors, one value else.
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_unit(T* p, const float* f) {
-    if constexpr (VEC) stg_stream(p, Elem<T>::pack(f));
-    else *p = Elem<T>::store(f[0]);
+struct RawUnit {
+    static constexpr int P = Elem<T>::VEC / 2;
+    using F = uint64_t;
+    uint4 r;
+    __device__ __forceinline__ void load(const T* p) { r = ldg_stream(p); }
+    __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(F* f) const { Elem<T>::unpack_pairs(r, f); }
+    static __device__ __forceinline__ void put(T* p, const F* f) { stg_stream(p, Elem<T>::pack_pairs(f)); }
+};
+template <typename T>
+struct RawUnit<T, false> {
+    static constexpr int P = 1;
+    using F = float;
+    T r;
+    __device__ __forceinline__ void load(const T* p) { r = __ldcs(p); }
+    __device__ __forceinline__ void zero() { r = Elem<T>::store(0.f); }
+    __device__ __forceinline__ void get(F* f) const { f[0] = Elem<T>::load(r); }
+    static __device__ __forceinline__ void put(T* p, const F* f) { __stcs(p, Elem<T>::store(f[0])); }
+};
+__device__ __forceinline__ float p_add(float a, float b) { return a + b; }
+__device__ __forceinline__ float p_mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float p_fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float p_sum(float a) { return a; }
+__device__ __forceinline__ uint64_t p_add(uint64_t a, uint64_t b) { return f2_add(a, b); }
+__device__ __forceinline__ uint64_t p_mul(uint64_t a, uint64_t b) { return f2_mul(a, b); }
+__device__ __forceinline__ uint64_t p_fma(uint64_t a, uint64_t b, uint64_t c) { return f2_fma(a, b, c); }
+__device__ __forceinline__ float p_sum(uint64_t a) {
+    float lo, hi;
+    f2_split(a, &lo, &hi);
+    return lo + hi;
 }
-// E weights (fp32 or the rows' type) at column c; cached loads, shared by every row.
+// 1 / sqrt(v): the hardware's estimate (2 ulp) and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float v) {
+    const float r = rsqrtf(v);
+    return v > 0.f && v < INFINITY ? fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r) : r;
+}
+template <typename F>
+__device__ __forceinline__ F p_all(float v) {
+    if constexpr (sizeof(F) == 8) return f2_make(v, v);
+    else return v;
+}
+template <typename F>
+__device__ __forceinline__ void p_split(F v, float* f) {
+    if constexpr (sizeof(F) == 8) f2_split(v, f, f + 1);
+    else f[0] = v;
+}
+
+// E weights (fp32 or the rows' type) at column c.
 template <typename W, int E>
 __device__ __forceinline__ void load_weight(const W* w, int c, float* f) {
     if constexpr (E == 1) {
@@ -56,111 +107,130 @@ __device__ __forceinline__ void load_weight(const W* w, int c, float* f) {
         for (int e = 0; e < E; e += Elem<W>::VEC) Elem<W>::unpack(__ldg(reinterpret_cast<const uint4*>(w + c + e)), f + e);
     }
 }
-
-template <typename T, typename W, bool VEC, int TPR, int NV>
-__global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS) norm_fwd_kernel(const NormFwdParams p) {
-    using S = Shape<T, VEC, TPR, NV>;
-    constexpr int E = S::E;
-    __shared__ float red[2][TPR > 32 ? TPR / 32 : 1];
-    const int t = threadIdx.x % TPR;
-    const long long row = blockIdx.x * static_cast<long long>(S::TEAMS) + threadIdx.x / TPR;
-    const bool live = row < p.rows;  // a team past the end takes part in the shuffles only
-    const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * p.ldx;
-    float v[NV][E];
-    float sum = 0.f;
+// A unit's columns of an optional weight vector (null: every value is `none`).
+template <typename W, int E, typename F>
+__device__ __forceinline__ void weight_unit(const W* w, int c, int width, float none, F* f) {
+    if (w && c < width) {
+        float v[E];
+        load_weight<W, E>(w, c, v);
+        if constexpr (sizeof(F) == 8) {
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        const int c = (t + u * TPR) * E;
-        if (live && c < p.width) {
-            load_unit<T, VEC>(x + c, v[u]);
+            for (int e = 0; e < E; e += 2) f[e / 2] = f2_make(v[e], v[e + 1]);
         } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+            f[0] = v[0];
         }
-    }
+    } else {
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum += v[u][e];
-    const float n = static_cast<float>(p.width);
-    const float mean = team_sum<TPR>(sum, red[0]) / n;
-    float sq = 0.f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        if ((t + u * TPR) * E < p.width) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                v[u][e] -= mean;
-                sq += v[u][e] * v[u][e];
-            }
-        }
-    }
-    const float rstd = 1.f / sqrtf(team_sum<TPR>(sq, red[1]) / n + p.eps);
-    if (!live) return;
-    if (t == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-    T* y = static_cast<T*>(p.y) + row * p.ldy;
-    const W* w = static_cast<const W*>(p.weight);
-    const W* b = static_cast<const W*>(p.bias);
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        const int c = (t + u * TPR) * E;
-        if (c >= p.width) break;
-        float f[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[u][e] *= rstd;
-        if (w) {
-            load_weight<W, E>(w, c, f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[u][e] *= f[e];
-        }
-        if (b) {
-            load_weight<W, E>(b, c, f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[u][e] += f[e];
-        }
-        store_unit<T, VEC>(y + c, v[u]);
+        for (int e = 0; e < (sizeof(F) == 8 ? E / 2 : 1); ++e) f[e] = p_all<F>(none);
     }
 }
 
-// A unit as it was loaded, unpacked where it is used: half the registers of fp32 values.
-template <typename T, bool VEC>
-struct RawUnit {
-    uint4 r;
-    __device__ __forceinline__ void load(const T* p) { r = ldg_stream(p); }
-    __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float* f) const { Elem<T>::unpack(r, f); }
-};
-template <typename T>
-struct RawUnit<T, false> {
-    T r;
-    __device__ __forceinline__ void load(const T* p) { r = *p; }
-    __device__ __forceinline__ void zero() { r = Elem<T>::store(0.f); }
-    __device__ __forceinline__ void get(float* f) const { f[0] = Elem<T>::load(r); }
-};
+template <typename T, typename W, bool VEC, int TPR, int NV>
+__global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, fwd_blocks_per_sm(TPR, NV * Shape<T, VEC, TPR, NV>::E))
+    norm_fwd_kernel(const NormFwdParams p) {
+    using S = Shape<T, VEC, TPR, NV>;
+    using Raw = RawUnit<T, VEC>;
+    constexpr int E = S::E;
+    __shared__ __align__(16) float red[2][2][TPR > 32 ? TPR / 32 : 4];
+    const int t = threadIdx.x % TPR;
+    const int team = threadIdx.x / TPR;
+    const float inv_n = 1.f / static_cast<float>(p.width);
+    constexpr int P = Raw::P;
+    using F = typename Raw::F;
+    F w[NV][P], b[NV][P];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        weight_unit<W, E>(static_cast<const W*>(p.weight), (t + u * TPR) * E, p.width, 1.f, w[u]);
+        weight_unit<W, E>(static_cast<const W*>(p.bias), (t + u * TPR) * E, p.width, 0.f, b[u]);
+    }
+    bool in[NV];  // which of this thread's units lie in the row
+#pragma unroll
+    for (int u = 0; u < NV; ++u) in[u] = (t + u * TPR) * E < p.width;
+    const long long step = static_cast<long long>(gridDim.x) * S::TEAMS;
+    const long long first = blockIdx.x * static_cast<long long>(S::TEAMS);
+    long long row = first + team;
+    // this thread's first unit of the row to be loaded next, and of the row to be stored
+    const T* xp = static_cast<const T*>(p.x) + row * p.ldx + t * E;
+    T* yp = static_cast<T*>(p.y) + row * p.ldy + t * E;
+    const long long xstep = step * p.ldx, ystep = step * p.ldy;
+    auto fetch = [&](bool live, Raw (&xo)[NV]) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (live && in[u]) xo[u].load(xp + u * TPR * E);
+            else xo[u].zero();
+        }
+        xp += xstep;
+    };
+    Raw xr[NV], xn[NV];
+    fetch(row < p.rows, xr);
+    int it = 0;
+    // every team of the block makes the same number of turns (the reductions are collective)
+    for (long long base = first; base < p.rows; base += step, row += step, yp += ystep, it ^= 1) {
+        fetch(row + step < p.rows, xn);
+        F acc = p_all<F>(0.f);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            F v[P];
+            xr[u].get(v);
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc = p_add(acc, v[i]);
+        }
+        const float mean = team_sum<TPR>(p_sum(acc), red[it][0]) * inv_n;
+        const F nm = p_all<F>(-mean);
+        acc = p_all<F>(0.f);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (in[u]) {
+                F v[P];
+                xr[u].get(v);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const F d = p_add(v[i], nm);
+                    acc = p_fma(d, d, acc);
+                }
+            }
+        }
+        const float rstd = inv_sqrt(fmaf(team_sum<TPR>(p_sum(acc), red[it][1]), inv_n, p.eps));
+        if (row < p.rows) {
+            if (t == 0) {
+                if (p.mean) p.mean[row] = mean;
+                if (p.rstd) p.rstd[row] = rstd;
+            }
+            const F rs = p_all<F>(rstd);
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                if (!in[u]) break;
+                F v[P];
+                xr[u].get(v);
+#pragma unroll
+                for (int i = 0; i < P; ++i) v[i] = p_fma(p_mul(p_add(v[i], nm), rs), w[u][i], b[u][i]);
+                Raw::put(yp + u * TPR * E, v);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u) xr[u] = xn[u];
+    }
+}
 
 // The column sums of a thread: in registers, or (SUMS_SMEM, rows over 8192 wide, whose
 // sums would take more registers than the SM has) in shared memory, which no other thread
-// of the block touches.
+// of the block touches; such a block reads its weights for every row.
 template <typename T, typename W, bool VEC, int TPR, int NV, bool SUMS_SMEM>
-__global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS) norm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_per_sm(TPR)) norm_bwd_kernel(const NormBwdParams p) {
     using S = Shape<T, VEC, TPR, NV>;
+    using Raw = RawUnit<T, VEC>;
     constexpr int E = S::E;
     static_assert(!SUMS_SMEM || S::TEAMS == 1, "sums in shared memory are one team's");
-    __shared__ float red[2][2][TPR > 32 ? TPR / 32 : 1];
+    __shared__ __align__(16) float2 red[2][TPR > 32 ? TPR / 32 : 2];
     extern __shared__ __align__(16) float cols[];  // [2][width]
     const int t = threadIdx.x % TPR;
     const int team = threadIdx.x / TPR;
-    const float n = static_cast<float>(p.width);
+    const float inv_n = 1.f / static_cast<float>(p.width);
     const W* w = static_cast<const W*>(p.weight);
+    constexpr int P = Raw::P;
+    using F = typename Raw::F;
     constexpr int NA = SUMS_SMEM ? 1 : NV;
-    float aw[NA][E], ab[NA][E];
-#pragma unroll
-    for (int u = 0; u < NA; ++u)
-#pragma unroll
-        for (int e = 0; e < E; ++e) aw[u][e] = ab[u][e] = 0.f;
+    F aw[NA][P], ab[NA][P], wv[NA][P];
     if constexpr (SUMS_SMEM) {
 #pragma unroll
         for (int u = 0; u < NV; ++u)
@@ -169,100 +239,120 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS) norm_bwd_kern
                 const int c = (t + u * TPR) * E + e;
                 if (c < p.width) cols[c] = cols[p.width + c] = 0.f;
             }
-    }
-    const long long step = static_cast<long long>(gridDim.x) * S::TEAMS;
-    const long long first = blockIdx.x * static_cast<long long>(S::TEAMS);
-    using Raw = RawUnit<T, VEC>;
-    Raw xr[NV], gr[NV];
-    float mean = 0.f, rstd = 0.f;
-    auto fetch = [&](long long row, Raw (&xo)[NV], Raw (&go)[NV], float& mo, float& so) {
-        const bool live = row < p.rows;
-        const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * p.ldx;
-        const T* dy = static_cast<const T*>(p.dy) + (live ? row : 0) * p.lddy;
-        mo = live ? p.mean[row] : 0.f;
-        so = live ? p.rstd[row] : 0.f;
+    } else {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            const int c = (t + u * TPR) * E;
-            if (live && c < p.width) {
-                xo[u].load(x + c);
-                go[u].load(dy + c);
+            weight_unit<W, E>(w, (t + u * TPR) * E, p.width, 1.f, wv[u]);
+#pragma unroll
+            for (int i = 0; i < P; ++i) aw[u][i] = ab[u][i] = p_all<F>(0.f);
+        }
+    }
+    auto weight_of = [&](int u, F (&f)[P]) {
+        if constexpr (SUMS_SMEM) {
+            weight_unit<W, E>(w, (t + u * TPR) * E, p.width, 1.f, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) f[i] = wv[u][i];
+        }
+    };
+    bool in[NV];  // which of this thread's units lie in the row
+#pragma unroll
+    for (int u = 0; u < NV; ++u) in[u] = (t + u * TPR) * E < p.width;
+    const long long step = static_cast<long long>(gridDim.x) * S::TEAMS;
+    const long long first = blockIdx.x * static_cast<long long>(S::TEAMS);
+    long long row = first + team;
+    // this thread's first unit: of the row to be loaded next (x, dy), of this row (res, dx)
+    const T* xp = static_cast<const T*>(p.x) + row * p.ldx + t * E;
+    const T* gp = static_cast<const T*>(p.dy) + row * p.lddy + t * E;
+    const T* rp = static_cast<const T*>(p.res) + row * p.ldr + t * E;
+    T* dp = static_cast<T*>(p.dx) + row * p.lddx + t * E;
+    const long long xstep = step * p.ldx, gstep = step * p.lddy, rstep = step * p.ldr, dstep = step * p.lddx;
+    Raw xr[NV], gr[NV];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](long long r, Raw (&xo)[NV], Raw (&go)[NV], float& mo, float& so) {
+        const bool live = r < p.rows;
+        mo = live ? p.mean[r] : 0.f;
+        so = live ? p.rstd[r] : 0.f;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (live && in[u]) {
+                xo[u].load(xp + u * TPR * E);
+                go[u].load(gp + u * TPR * E);
             } else {
                 xo[u].zero();
                 go[u].zero();
             }
         }
+        xp += xstep;
+        gp += gstep;
     };
-    fetch(first + team, xr, gr, mean, rstd);
+    fetch(row, xr, gr, mean, rstd);
     int it = 0;
     // every team of the block makes the same number of turns (the reductions are collective)
-    for (long long base = first; base < p.rows; base += step, it ^= 1) {
-        const long long row = base + team;
+    for (long long base = first; base < p.rows; base += step, row += step, rp += rstep, dp += dstep, it ^= 1) {
         const bool live = row < p.rows;
-        // the next row and this row's residual gradient are on their way during the sums
         Raw xn[NV], gn[NV], rr[NV];
         float mean_n = 0.f, rstd_n = 0.f;
-        if (base + step < p.rows) fetch(row + step, xn, gn, mean_n, rstd_n);
+        fetch(row + step, xn, gn, mean_n, rstd_n);
         if (p.res && live) {
-            const T* r = static_cast<const T*>(p.res) + row * p.ldr;
 #pragma unroll
             for (int u = 0; u < NV; ++u)
-                if ((t + u * TPR) * E < p.width) rr[u].load(r + (t + u * TPR) * E);
+                if (in[u]) rr[u].load(rp + u * TPR * E);
         }
-        float s1 = 0.f, s2 = 0.f;
+        const F nm = p_all<F>(-mean), rs = p_all<F>(rstd);
+        F a1 = p_all<F>(0.f), a2 = p_all<F>(0.f);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
+            if (!in[u]) break;
             const int c = (t + u * TPR) * E;
-            if (c >= p.width) break;
-            float f[E], h[E], g[E];
+            F f[P], h[P], g[P];
             xr[u].get(h);
             gr[u].get(g);
-            if (w) {
-                load_weight<W, E>(w, c, f);
-            } else {
+            weight_of(u, f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) f[e] = 1.f;
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                h[e] = (h[e] - mean) * rstd;
+            for (int i = 0; i < P; ++i) {
+                h[i] = p_mul(p_add(h[i], nm), rs);
                 if constexpr (SUMS_SMEM) {
-                    cols[c + e] += g[e] * h[e];
-                    cols[p.width + c + e] += g[e];
+                    float hv[2], gv[2];
+                    p_split(h[i], hv);
+                    p_split(g[i], gv);
+#pragma unroll
+                    for (int k = 0; k < E / P; ++k) {
+                        cols[c + i * (E / P) + k] += gv[k] * hv[k];
+                        cols[p.width + c + i * (E / P) + k] += gv[k];
+                    }
                 } else {
-                    aw[u][e] += g[e] * h[e];
-                    ab[u][e] += g[e];
+                    aw[u][i] = p_fma(g[i], h[i], aw[u][i]);
+                    ab[u][i] = p_add(ab[u][i], g[i]);
                 }
-                g[e] *= f[e];
-                s1 += g[e];
-                s2 += g[e] * h[e];
+                g[i] = p_mul(g[i], f[i]);
+                a1 = p_add(a1, g[i]);
+                a2 = p_fma(g[i], h[i], a2);
             }
         }
-        s1 = team_sum<TPR>(s1, red[it][0]) / n;
-        s2 = team_sum<TPR>(s2, red[it][1]) / n;
+        float s1 = p_sum(a1), s2 = p_sum(a2);
+        team_sum2<TPR>(s1, s2, red[it]);
         if (live && p.dx) {
-            T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+            // rstd (g - s1 - h s2) = rstd g - (rstd s1) - h (rstd s2)
+            const F k1 = p_all<F>(-rstd * (s1 * inv_n)), k2 = p_all<F>(-rstd * (s2 * inv_n));
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
-                const int c = (t + u * TPR) * E;
-                if (c >= p.width) break;
-                float f[E], h[E], g[E];
+                if (!in[u]) break;
+                F f[P], h[P], g[P];
                 xr[u].get(h);
                 gr[u].get(g);
-                if (w) {
-                    load_weight<W, E>(w, c, f);
+                weight_of(u, f);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) g[e] *= f[e];
+                for (int i = 0; i < P; ++i) {
+                    h[i] = p_fma(p_mul(p_add(h[i], nm), rs), k2, k1);
+                    g[i] = p_fma(p_mul(g[i], f[i]), rs, h[i]);
                 }
                 if (p.res) {
                     rr[u].get(f);
-                } else {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) f[e] = 0.f;
+                    for (int i = 0; i < P; ++i) g[i] = p_add(g[i], f[i]);
                 }
-#pragma unroll
-                for (int e = 0; e < E; ++e) f[e] += rstd * (g[e] - s1 - (h[e] - mean) * rstd * s2);
-                store_unit<T, VEC>(dx + c, f);
+                Raw::put(dp + u * TPR * E, g);
             }
         }
 #pragma unroll
@@ -275,6 +365,16 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS) norm_bwd_kern
     }
     if (!p.dweight && !p.dbias) return;
     // the block's column sums: team 0's registers, then every other team's in turn
+    float cw[SUMS_SMEM ? 1 : NV][E], cb[SUMS_SMEM ? 1 : NV][E];
+    if constexpr (!SUMS_SMEM) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                p_split(aw[u][i], &cw[u][i * (E / P)]);
+                p_split(ab[u][i], &cb[u][i * (E / P)]);
+            }
+    }
     if constexpr (S::TEAMS > 1) {
         for (int k = 1; k < S::TEAMS; ++k) {
             __syncthreads();
@@ -285,8 +385,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS) norm_bwd_kern
                     for (int e = 0; e < E; ++e) {
                         const int c = (t + u * TPR) * E + e;
                         if (c < p.width) {
-                            cols[c] = aw[u][e];
-                            cols[p.width + c] = ab[u][e];
+                            cols[c] = cw[u][e];
+                            cols[p.width + c] = cb[u][e];
                         }
                     }
             }
@@ -298,8 +398,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS) norm_bwd_kern
                     for (int e = 0; e < E; ++e) {
                         const int c = (t + u * TPR) * E + e;
                         if (c < p.width) {
-                            aw[u][e] += cols[c];
-                            ab[u][e] += cols[p.width + c];
+                            cw[u][e] += cols[c];
+                            cb[u][e] += cols[p.width + c];
                         }
                     }
             }
@@ -314,8 +414,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS) norm_bwd_kern
         for (int e = 0; e < E; ++e) {
             const int c = (t + u * TPR) * E + e;
             if (c < p.width) {
-                if (p.dweight) pw[c] = SUMS_SMEM ? cols[c] : aw[SUMS_SMEM ? 0 : u][e];
-                if (p.dbias) pb[c] = SUMS_SMEM ? cols[p.width + c] : ab[SUMS_SMEM ? 0 : u][e];
+                if (p.dweight) pw[c] = SUMS_SMEM ? cols[c] : cw[SUMS_SMEM ? 0 : u][e];
+                if (p.dbias) pb[c] = SUMS_SMEM ? cols[p.width + c] : cb[SUMS_SMEM ? 0 : u][e];
             }
         }
 }
@@ -351,8 +451,9 @@ bool aligned16(const void* p, long long ld, int es, long long rows) {
 template <typename T, typename W, bool VEC, int TPR, int NV>
 cudaError_t run_fwd(const NormFwdParams& p, cudaStream_t s) {
     using S = Shape<T, VEC, TPR, NV>;
-    const long long blocks = (p.rows + S::TEAMS - 1) / S::TEAMS;
-    norm_fwd_kernel<T, W, VEC, TPR, NV><<<static_cast<unsigned>(blocks), S::THREADS, 0, s>>>(p);
+    const long long want = (p.rows + S::TEAMS - 1) / S::TEAMS;
+    const long long cap = 152ll * fwd_blocks_per_sm(TPR, NV * S::E);  // one wave of resident blocks
+    norm_fwd_kernel<T, W, VEC, TPR, NV><<<static_cast<unsigned>(want < cap ? want : cap), S::THREADS, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -370,9 +471,9 @@ cudaError_t run_bwd(const NormBwdParams& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// The narrowest team that holds the row: fewer threads per row means fewer barriers and
-// more rows in flight per block.  16-byte units where every array is 16-byte aligned row
-// by row, single elements otherwise.
+// The narrowest team that holds the row, 8 to 16 columns a thread: fewer threads per row
+// means fewer barriers and more rows in flight per block.  16-byte units where every array
+// is 16-byte aligned row by row, single elements otherwise.
 template <typename T, typename W>
 cudaError_t pick_fwd(const NormFwdParams& p, bool vec, cudaStream_t s) {
     constexpr int E = Elem<T>::VEC;
@@ -380,38 +481,38 @@ cudaError_t pick_fwd(const NormFwdParams& p, bool vec, cudaStream_t s) {
     if (vec) {
         if (w <= 8 * E) return run_fwd<T, W, true, 8, 1>(p, s);
         if (w <= 32 * E) return run_fwd<T, W, true, 32, 1>(p, s);
-        if (w <= 96 * E) return run_fwd<T, W, true, 32, 3>(p, s);
-        if (w <= 256 * E) return run_fwd<T, W, true, 128, 2>(p, s);
-        if (w <= 384 * E) return run_fwd<T, W, true, 128, 3>(p, s);
-        if (w <= 512 * E) return run_fwd<T, W, true, 128, 4>(p, s);
-        if (w <= 1024 * E) return run_fwd<T, W, true, 256, 4>(p, s);
-        return run_fwd<T, W, true, 512, 8>(p, s);
+        if (w <= 1024) return run_fwd<T, W, true, 128, 8 / E>(p, s);
+        if (w <= 2048) return run_fwd<T, W, true, 128, 16 / E>(p, s);
+        if (w <= 4096) return run_fwd<T, W, true, 256, 16 / E>(p, s);
+        if (w <= 8192) return run_fwd<T, W, true, 512, 16 / E>(p, s);
+        return run_fwd<T, W, true, 512, 32 / E>(p, s);
     }
     if (w <= 64) return run_fwd<T, W, false, 8, 8>(p, s);
     if (w <= 256) return run_fwd<T, W, false, 32, 8>(p, s);
     if (w <= 1024) return run_fwd<T, W, false, 128, 8>(p, s);
+    if (w <= 2048) return run_fwd<T, W, false, 128, 16>(p, s);
     if (w <= 4096) return run_fwd<T, W, false, 256, 16>(p, s);
+    if (w <= 8192) return run_fwd<T, W, false, 512, 16>(p, s);
     return run_fwd<T, W, false, 512, 32>(p, s);
 }
 
 template <typename T, typename W>
 cudaError_t pick_bwd(const NormBwdParams& p, bool vec, cudaStream_t s) {
     constexpr int E = Elem<T>::VEC;
-    constexpr int NW = 16 / E;  // units of 16 elements per thread
     const int w = p.width;
     if (vec) {
         if (w <= 8 * E) return run_bwd<T, W, true, 8, 1>(p, s);
         if (w <= 32 * E) return run_bwd<T, W, true, 32, 1>(p, s);
-        if (w <= 96 * E) return run_bwd<T, W, true, 32, 3>(p, s);
-        if (w <= 256 * E) return run_bwd<T, W, true, 128, 2>(p, s);
-        if (w <= 384 * E) return run_bwd<T, W, true, 128, 3>(p, s);
-        if (w <= 4096) return run_bwd<T, W, true, 256, NW>(p, s);
-        if (w <= 8192) return run_bwd<T, W, true, 512, NW>(p, s);
-        return run_bwd<T, W, true, 512, 2 * NW, true>(p, s);
+        if (w <= 1024) return run_bwd<T, W, true, 128, 8 / E>(p, s);
+        if (w <= 2048) return run_bwd<T, W, true, 128, 16 / E>(p, s);
+        if (w <= 4096) return run_bwd<T, W, true, 256, 16 / E>(p, s);
+        if (w <= 8192) return run_bwd<T, W, true, 512, 16 / E>(p, s);
+        return run_bwd<T, W, true, 512, 32 / E, true>(p, s);
     }
     if (w <= 64) return run_bwd<T, W, false, 8, 8>(p, s);
     if (w <= 256) return run_bwd<T, W, false, 32, 8>(p, s);
     if (w <= 1024) return run_bwd<T, W, false, 128, 8>(p, s);
+    if (w <= 2048) return run_bwd<T, W, false, 128, 16>(p, s);
     if (w <= 4096) return run_bwd<T, W, false, 256, 16>(p, s);
     if (w <= 8192) return run_bwd<T, W, false, 512, 16>(p, s);
     return run_bwd<T, W, false, 512, 32, true>(p, s);
@@ -436,10 +537,12 @@ cudaError_t launch_norm_fwd(const NormFwdParams& p, cudaStream_t s) {
 
 int norm_bwd_blocks(long long rows, int width, int dtype, int sm_count) {
     // narrow rows: teams of 8 or 32 threads, 32 or 8 rows per block and turn; else one row
+    // and a team of 128 threads or more, 16 columns of a row per thread
     const int unit = 16 / dtype_size(dtype);
-    const int per_block = width <= 64 ? 32 : width <= 96 * unit ? 8 : 1;
+    const int per_block = width <= 64 ? 32 : width <= 32 * unit ? 8 : 1;
+    const int tpr = width <= 32 * unit ? 32 : width <= 2048 ? 128 : width <= 4096 ? 256 : 512;
     const long long want = (rows + per_block - 1) / per_block;
-    const long long cap = static_cast<long long>(sm_count) * (width <= 256 * unit ? 4 : 2);
+    const long long cap = static_cast<long long>(sm_count) * bwd_blocks_per_sm(tpr);
     return static_cast<int>(want < 1 ? 1 : want < cap ? want : cap);
 }
 

@@ -14,6 +14,16 @@ namespace anvil {
 enum : int { DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2 };
 constexpr int dtype_size(int dt) { return dt == DT_F32 ? 4 : 2; }
 
+// two fp32 in one 64-bit register pair
+__device__ __forceinline__ uint64_t f2_make(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float* lo, float* hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+
 template <typename T>
 struct Elem;
 template <>
@@ -35,6 +45,17 @@ struct Elem<float> {
     }
     static __device__ __forceinline__ uint4 pack(const float* f) {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    // the same as packed fp32 pairs
+    static __device__ __forceinline__ void unpack_pairs(uint4 w, uint64_t* p) {
+        p[0] = f2_make(__uint_as_float(w.x), __uint_as_float(w.y));
+        p[1] = f2_make(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+    static __device__ __forceinline__ uint4 pack_pairs(const uint64_t* p) {
+        float f[4];
+        f2_split(p[0], f, f + 1);
+        f2_split(p[1], f + 2, f + 3);
+        return pack(f);
     }
 };
 template <>
@@ -68,6 +89,25 @@ struct Elem<__nv_bfloat16> {
     }
     static __device__ __forceinline__ uint4 pack(const float* f) {
         return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    }
+    static __device__ __forceinline__ uint64_t word_pair(uint32_t w) {
+        float f[2];
+        unpack2(w, f);
+        return f2_make(f[0], f[1]);
+    }
+    static __device__ __forceinline__ uint32_t pair_word(uint64_t p) {
+        float lo, hi;
+        f2_split(p, &lo, &hi);
+        return pack2(lo, hi);
+    }
+    static __device__ __forceinline__ void unpack_pairs(uint4 w, uint64_t* p) {
+        p[0] = word_pair(w.x);
+        p[1] = word_pair(w.y);
+        p[2] = word_pair(w.z);
+        p[3] = word_pair(w.w);
+    }
+    static __device__ __forceinline__ uint4 pack_pairs(const uint64_t* p) {
+        return make_uint4(pair_word(p[0]), pair_word(p[1]), pair_word(p[2]), pair_word(p[3]));
     }
 };
 template <>
@@ -103,6 +143,25 @@ struct Elem<__half> {
     static __device__ __forceinline__ uint4 pack(const float* f) {
         return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
     }
+    static __device__ __forceinline__ uint64_t word_pair(uint32_t w) {
+        float f[2];
+        unpack2(w, f);
+        return f2_make(f[0], f[1]);
+    }
+    static __device__ __forceinline__ uint32_t pair_word(uint64_t p) {
+        float lo, hi;
+        f2_split(p, &lo, &hi);
+        return pack2(lo, hi);
+    }
+    static __device__ __forceinline__ void unpack_pairs(uint4 w, uint64_t* p) {
+        p[0] = word_pair(w.x);
+        p[1] = word_pair(w.y);
+        p[2] = word_pair(w.z);
+        p[3] = word_pair(w.w);
+    }
+    static __device__ __forceinline__ uint4 pack_pairs(const uint64_t* p) {
+        return make_uint4(pair_word(p[0]), pair_word(p[1]), pair_word(p[2]), pair_word(p[3]));
+    }
 };
 
 // (a.x b.x + c.x, a.y b.y + c.y) on packed fp32 pairs, one rounding each
@@ -111,17 +170,14 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-__device__ __forceinline__ float f2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-
 // Streaming 16-byte load (read once) and store (not read again soon).
 __device__ __forceinline__ uint4 ldg_stream(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ void stg_stream(void* p, uint4 v) { __stcs(reinterpret_cast<uint4*>(p), v); }
 
 // Sum over a team of TPR consecutive threads (8 or 32: inside a warp; more: the whole
 // block, through `red`, one float per warp).  Every thread of the team gets the same sum,
-// in an order fixed by the thread numbers.  `red` may be reused after the next
-// team_sum (its leading barrier) -- callers alternate two arrays.
+// in an order fixed by the thread numbers.  Callers alternate between arrays (16-byte
+// aligned): one may be written again once every thread has passed another barrier.
 template <int TPR>
 __device__ __forceinline__ float team_sum(float v, float* red) {
     constexpr int W = TPR < 32 ? TPR : 32;
@@ -132,9 +188,39 @@ __device__ __forceinline__ float team_sum(float v, float* red) {
         __syncthreads();
         v = 0.f;
 #pragma unroll
-        for (int w = 0; w < TPR / 32; ++w) v += red[w];
+        for (int w = 0; w < TPR / 32; w += 4) {  // four warps' sums per load
+            const float4 f = *reinterpret_cast<const float4*>(red + w);
+            v += f.x;
+            v += f.y;
+            v += f.z;
+            v += f.w;
+        }
     }
     return v;
+}
+
+// Two sums at once (one barrier).
+template <int TPR>
+__device__ __forceinline__ void team_sum2(float& a, float& b, float2* red) {
+    constexpr int W = TPR < 32 ? TPR : 32;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 32; w += 2) {  // two warps' sums per load
+            const float4 f = *reinterpret_cast<const float4*>(red + w);
+            a += f.x;
+            b += f.y;
+            a += f.z;
+            b += f.w;
+        }
+    }
 }
 
 }  // namespace anvil
