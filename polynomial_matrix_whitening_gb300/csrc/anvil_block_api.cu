@@ -182,7 +182,8 @@ struct Plan {
 
 constexpr int FEW_ROWS = 128;
 
-Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32) {
+// epilogue: SM cycles that the epilogue of a whole tile takes beyond the products.
+Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32, double epilogue) {
     Plan p = {};
     const int64_t kb = (k + GEMM_BK - 1) / GEMM_BK;
     if (rows <= FEW_ROWS && !a_mn && !out_f32) {
@@ -198,32 +199,51 @@ Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32) {
         p.kb = static_cast<int>((kb + p.splits - 1) / p.splits);
         return p;
     }
-    // Whole turns of the grid's pairs go over tiles in one piece; the tiles left over for a
-    // turn that would not be full are split, if the turn's time saved is more than the parts'
-    // way through memory.  Times in SM cycles: 560 for a k-block, 2500 for filling the
-    // pipeline and the epilogue of a unit, the parts written and read at 2600 bytes a cycle,
-    // 6000 for the second kernel.
+    // Tiles in one piece, turn by turn of the grid's pairs; the tiles left over for a last turn
+    // that would not be full, or all of them, may go in parts instead (split along k, or whole
+    // but with the epilogue left to the second kernel).  Estimated times in SM cycles, fitted
+    // to measurements: 550 for a k-block, 2500 for filling the pipeline; an epilogue overlaps
+    // the next tile's products; parts cost 8000 for the second kernel and 200 a unit for their
+    // way through memory.
     const int64_t pairs = PLAN_SMS / 2;
     const int64_t tiles = ((rows + PAIR_ROWS - 1) / PAIR_ROWS) * ((cols + PAIR_COLS - 1) / PAIR_COLS);
-    const int64_t tail = tiles % pairs;
+    const double products = kb * 550.0, turn = products > epilogue ? products : epilogue;
     p.whole = static_cast<int>(tiles);
     p.splits = 1;
     p.kb = static_cast<int>(kb);
-    double best = kb * 560.0 + 2500.0;  // the last turn in one piece
-    for (int64_t s = 2; tail && s <= 64 && s <= kb; ++s) {
-        const int64_t per = (kb + s - 1) / s;
-        if (per * (s - 1) >= kb) continue;  // every split has work
-        const int64_t turns = (tail * s + pairs - 1) / pairs;
-        const double cost = turns * (per * 560.0 + 2500.0) + 6000.0 + tail * s * (2.0 * 4 * PAIR_ROWS * PAIR_COLS / 2600.0);
-        if (cost < best) {
-            best = cost;
-            p.whole = static_cast<int>(tiles - tail);
-            p.splits = static_cast<int>(s);
-            p.kb = static_cast<int>(per);
-            p.part = static_cast<size_t>(tail * s) * 4 * PAIR_ROWS * PAIR_COLS;
+    double best = static_cast<double>((tiles + pairs - 1) / pairs) * turn + (products < epilogue ? products : epilogue) + 2500.0;
+    for (int64_t tail = tiles % pairs;; tail = tiles) {
+        const int64_t whole = tiles - tail;
+        for (int64_t s = 1; tail && s <= 64 && s <= kb; ++s) {
+            const int64_t per = (kb + s - 1) / s;
+            if (per * (s - 1) >= kb) continue;  // every split has work
+            const int64_t turns = (tail * s + pairs - 1) / pairs;
+            const double cost = whole / pairs * turn + turns * (per * 550.0 + 2500.0) + 8000.0 + tail * s * 200.0;
+            if (cost < best) {
+                best = cost;
+                p.whole = static_cast<int>(whole);
+                p.splits = static_cast<int>(s);
+                p.kb = static_cast<int>(per);
+                p.part = static_cast<size_t>(tail * s) * 4 * PAIR_ROWS * PAIR_COLS;
+            }
+            if (turns > 4) break;  // parts beyond a few turns only add traffic
         }
+        if (tail == tiles) break;
     }
     return p;
+}
+
+// The epilogue's cost for plan_product, by what it does: measured on 14336 x 6144 x 832
+// (over the plain store) and, for arrays off the 16-byte boundaries, on 1000 x 2815 x 771.
+double epilogue_cycles(const GemmEpilogue& e, int64_t rows) {
+    const int es = e.out_f32 ? 4 : 2;
+    double c = 2500.0;
+    if (e.in) c += aligned16(e.in, e.ldin, es, rows) ? 2000.0 : 12000.0;
+    if (e.z) c += aligned16(e.z, e.ldz, es, rows) ? 2500.0 : 12000.0;
+    if (!aligned16(e.out, e.ldout, es, rows)) c += 12000.0;
+    if (e.act == ACT_GELU || e.act == ACT_GELU_TANH) c += 6000.0;
+    if (e.act == ACT_SILU) c += 3000.0;
+    return c;
 }
 
 anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, cudaStream_t s) {
@@ -315,6 +335,37 @@ Stored stored_weight(const void* w, int n, int k, int64_t ldw, bool transposed) 
     return transposed ? Stored{w, k, ldw, n} : Stored{w, n, ldw, k};
 }
 
+GemmEpilogue forward_epilogue(const anvil_linear_desc* d) {
+    GemmEpilogue e = {};
+    e.bias = d->bias;
+    e.bias_f32 = d->bias && d->bias_dtype == ANVIL_F32;
+    e.act = d->activation;
+    e.in = d->residual;
+    e.ldin = d->ldr;
+    e.z = d->preact;
+    e.ldz = d->ldz;
+    e.out = d->y;
+    e.ldout = d->ldy;
+    return e;
+}
+GemmEpilogue dx_epilogue(const anvil_linear_grad_desc* d) {
+    GemmEpilogue e = {};
+    e.out = d->dx;
+    e.ldout = d->lddx;
+    return e;
+}
+GemmEpilogue dweight_epilogue(const anvil_linear_grad_desc* d) {
+    GemmEpilogue e = {};
+    e.out = d->dweight;
+    e.ldout = d->lddw;
+    e.out_f32 = d->dweight_dtype == ANVIL_F32;
+    if (d->accumulate) {
+        e.in = d->dweight;
+        e.ldin = d->lddw;
+    }
+    return e;
+}
+
 struct LinearLayout {
     Stored x, w;
     Plan plan;
@@ -327,7 +378,7 @@ LinearLayout linear_layout(const anvil_linear_desc* d) {
     L.off_x = 0;
     L.off_w = L.off_x + copy_bytes(L.x);
     L.off_part = L.off_w + copy_bytes(L.w);
-    L.plan = plan_product(d->rows, d->n, d->k, false, false);
+    L.plan = plan_product(d->rows, d->n, d->k, false, false, epilogue_cycles(forward_epilogue(d), d->rows));
     L.total = L.off_part + L.plan.part;
     return L;
 }
@@ -388,8 +439,11 @@ LinearGradLayout linear_grad_layout(const anvil_linear_grad_desc* d) {
     }
     L.off_part = at;
     // the two products run one after the other: they share the scratch of their parts
-    if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, false, false);
-    if (d->dweight) L.pdw = plan_product(tr ? d->k : d->n, tr ? d->n : d->k, d->rows, true, d->dweight_dtype == ANVIL_F32);
+    if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, false, false, epilogue_cycles(dx_epilogue(d), d->rows));
+    const int64_t wr = tr ? d->k : d->n;
+    if (d->dweight)
+        L.pdw = plan_product(wr, tr ? d->n : d->k, d->rows, true, d->dweight_dtype == ANVIL_F32,
+                             epilogue_cycles(dweight_epilogue(d), wr));
     L.total = at + (L.pdx.part > L.pdw.part ? L.pdx.part : L.pdw.part);
     return L;
 }
@@ -564,15 +618,7 @@ anvil_status anvil_linear_forward(const anvil_linear_desc* d, void* workspace, s
     q.cols = d->n;
     q.k = d->k;
     q.f16 = d->dtype == ANVIL_F16;
-    q.epi.bias = d->bias;
-    q.epi.bias_f32 = d->bias && d->bias_dtype == ANVIL_F32;
-    q.epi.act = d->activation;
-    q.epi.in = d->residual;
-    q.epi.ldin = d->ldr;
-    q.epi.z = d->preact;
-    q.epi.ldz = d->ldz;
-    q.epi.out = d->y;
-    q.epi.ldout = d->ldy;
+    q.epi = forward_epilogue(d);
     q.part = reinterpret_cast<float*>(ws + L.off_part);
     return run_product(q, L.plan, dev, s);
 }
@@ -651,8 +697,7 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
         q.cols = d->k;
         q.k = d->n;
         q.f16 = f16;
-        q.epi.out = d->dx;
-        q.epi.ldout = d->lddx;
+        q.epi = dx_epilogue(d);
         q.part = reinterpret_cast<float*>(ws + L.off_part);
         if ((st = run_product(q, L.pdx, dev, s)) != ANVIL_OK) return st;
     }
@@ -667,13 +712,7 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
         q.cols = static_cast<int>(wc);
         q.k = d->rows;
         q.f16 = f16;
-        q.epi.out = d->dweight;
-        q.epi.ldout = d->lddw;
-        q.epi.out_f32 = d->dweight_dtype == ANVIL_F32;
-        if (d->accumulate) {
-            q.epi.in = d->dweight;
-            q.epi.ldin = d->lddw;
-        }
+        q.epi = dweight_epilogue(d);
         q.part = reinterpret_cast<float*>(ws + L.off_part);
         if ((st = run_product(q, L.pdw, dev, s)) != ANVIL_OK) return st;
     }

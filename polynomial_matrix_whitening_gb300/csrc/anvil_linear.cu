@@ -179,9 +179,18 @@ constexpr int BOXES = 2 * EPI_GROUPS;
 constexpr int PAIR_SMEM = STAGES * STAGE + BOXES * QBOX + 1024;  // + alignment slack
 constexpr uint32_t PAIR_TMEM = 2 * BN;
 
+// Tile t: groups of RASTER_ROWS rows of tiles, column by column inside a group, so that the
+// pairs running at one time share operand panels.
+__device__ __forceinline__ void tile_at(int t, int tiles_r, int tiles_c, int* tr, int* tc) {
+    const int per = RASTER_ROWS * tiles_c;
+    const int g = t / per;
+    const int rows = min(RASTER_ROWS, tiles_r - g * RASTER_ROWS);
+    const int q = t - g * per;
+    *tc = q / rows;
+    *tr = g * RASTER_ROWS + (q - *tc * rows);
+}
+
 // Work unit u: a whole tile, or a split of a tail tile (part: its place in the scratch).
-// Tiles go in groups of RASTER_ROWS rows of tiles, column by column inside a group, so that
-// the pairs running at one time share operand panels.
 struct Unit {
     int tr, tc, part, kb0, nkb;
 };
@@ -199,12 +208,7 @@ __device__ __forceinline__ Unit unit_of(const PairGemmParams& p, int u) {
         r.kb0 = (r.part - q * p.splits) * p.kb_per_split;
         r.nkb = max(0, min(p.kb_per_split, all - r.kb0));
     }
-    const int per = RASTER_ROWS * p.tiles_c;
-    const int g = t / per;
-    const int rows = min(RASTER_ROWS, p.tiles_r - g * RASTER_ROWS);
-    const int q = t - g * per;
-    r.tc = q / rows;
-    r.tr = g * RASTER_ROWS + (q - r.tc * rows);
+    tile_at(t, p.tiles_r, p.tiles_c, &r.tr, &r.tc);
     return r;
 }
 
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
             }
         }
         if (x.leader) {
-            bulk_wait_all();  // every store of this group has completed
+            bulk_wait_read_all();  // the group's stores have read their boxes
             for (int b = 0; b < 2; ++b)
                 if (x.loads[b]) mbar_wait(&x.in_bar[b], static_cast<uint32_t>(x.loads[b] - 1) & 1u, p.err);
         }
@@ -644,76 +648,51 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
 }
 
 // The tail tiles of pair_gemm_kernel: the parts of each element, in order, then what follows
-// the accumulator.  A block takes 16 rows of a tile, a thread four columns at a time.
+// the accumulator.  A block takes 16 rows of a tile, a thread one column of them, so that
+// neighbouring lanes are neighbouring elements whatever the arrays' alignment.
 constexpr int TAIL_ROWS = 16;
 template <typename T>
-__global__ void __launch_bounds__(256) tail_sum_kernel(const __grid_constant__ TailSumParams p) {
+__global__ void __launch_bounds__(PAIR_COLS) tail_sum_kernel(const __grid_constant__ TailSumParams p) {
     pdl_allow_next();
     const GemmEpilogue& e = p.epi;
     const int tile = blockIdx.x / (PAIR_ROWS / TAIL_ROWS), r0 = blockIdx.x % (PAIR_ROWS / TAIL_ROWS) * TAIL_ROWS;
     int tr, tc;
-    {
-        const int t = p.whole + tile;
-        const int per = RASTER_ROWS * p.tiles_c;
-        const int g = t / per;
-        const int rows = min(RASTER_ROWS, p.tiles_r - g * RASTER_ROWS);
-        const int q = t - g * per;
-        tc = q / rows;
-        tr = g * RASTER_ROWS + (q - tc * rows);
-    }
-    const int c = threadIdx.x % 64 * 4, col = tc * PAIR_COLS + c;
-    pdl_wait_previous();
-    if (col >= p.cols) return;
-    const float* base = p.part + static_cast<size_t>(tile) * p.splits * PAIR_ROWS * PAIR_COLS + c;
-    float v[TAIL_ROWS / 4][4];
-#pragma unroll
-    for (int i = 0; i < TAIL_ROWS / 4; ++i) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-#pragma unroll
-        for (int i = 0; i < TAIL_ROWS / 4; ++i) {
-            const int r = r0 + i * 4 + threadIdx.x / 64;
-            const float4 f = __ldcs(reinterpret_cast<const float4*>(base + (static_cast<size_t>(s) * PAIR_ROWS + r) * PAIR_COLS));
-            v[i][0] += f.x;
-            v[i][1] += f.y;
-            v[i][2] += f.z;
-            v[i][3] += f.w;
-        }
-    }
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    tile_at(p.whole + tile, p.tiles_r, p.tiles_c, &tr, &tc);
+    const int col = tc * PAIR_COLS + threadIdx.x;
+    const int rows = min(TAIL_ROWS, p.rows - tr * PAIR_ROWS - r0);  // of this block that exist
+    const long long row = static_cast<long long>(tr) * PAIR_ROWS + r0;
+    if (rows <= 0 || col >= p.cols) return;  // (the block's other threads wait for the parts)
+    float bias = 0.f;
     if constexpr (sizeof(T) == 2) {
-        if (e.bias) {
+        if (e.bias)
+            bias = e.bias_f32 ? static_cast<const float*>(e.bias)[col] : Elem<T>::load(static_cast<const T*>(e.bias)[col]);
+    }
+    pdl_wait_previous();
+    const float* part = p.part + (static_cast<size_t>(tile) * p.splits * PAIR_ROWS + r0) * PAIR_COLS + threadIdx.x;
+    float v[TAIL_ROWS], in[TAIL_ROWS];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (col + k < p.cols)
-                    bias[k] = e.bias_f32 ? static_cast<const float*>(e.bias)[col + k]
-                                         : Elem<T>::load(static_cast<const T*>(e.bias)[col + k]);
+    for (int i = 0; i < TAIL_ROWS; ++i) {
+        v[i] = __ldcs(part + i * PAIR_COLS);
+        in[i] = e.in && i < rows ? Elem<T>::load(static_cast<const T*>(e.in)[(row + i) * e.ldin + col]) : 0.f;
+    }
+    for (int s = 1; s < p.splits; ++s) {
+        part += static_cast<size_t>(PAIR_ROWS) * PAIR_COLS;
+#pragma unroll
+        for (int i = 0; i < TAIL_ROWS; ++i) v[i] += __ldcs(part + i * PAIR_COLS);
+    }
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < TAIL_ROWS; ++i) v[i] += bias;
+        if (e.z) {
+#pragma unroll
+            for (int i = 0; i < TAIL_ROWS; ++i)
+                if (i < rows) static_cast<T*>(e.z)[(row + i) * e.ldz + col] = Elem<T>::store(v[i]);
         }
+        act_values<TAIL_ROWS>(e.act, v);
     }
 #pragma unroll
-    for (int i = 0; i < TAIL_ROWS / 4; ++i) {
-        const long long row = tr * PAIR_ROWS + r0 + i * 4 + threadIdx.x / 64;
-        if (row >= p.rows) continue;
-        float in[4] = {0.f, 0.f, 0.f, 0.f};
-        if (e.in) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (col + k < p.cols) in[k] = Elem<T>::load(static_cast<const T*>(e.in)[row * e.ldin + col + k]);
-        }
-        if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[i][k] += bias[k];
-            if (e.z) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (col + k < p.cols) static_cast<T*>(e.z)[row * e.ldz + col + k] = Elem<T>::store(v[i][k]);
-            }
-            act_values<4>(e.act, v[i]);
-        }
-        T* out = static_cast<T*>(e.out) + row * e.ldout + col;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (col + k < p.cols) out[k] = Elem<T>::store(v[i][k] + in[k]);
-    }
+    for (int i = 0; i < TAIL_ROWS; ++i)
+        if (i < rows) static_cast<T*>(e.out)[(row + i) * e.ldout + col] = Elem<T>::store(v[i] + in[i]);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -1102,9 +1081,9 @@ cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t
 
 cudaError_t launch_tail_sum(const TailSumParams& p, cudaStream_t s) {
     const dim3 grid((p.tiles_r * p.tiles_c - p.whole) * (PAIR_ROWS / TAIL_ROWS));
-    if (p.epi.out_f32) return launch_pdl(tail_sum_kernel<float>, grid, dim3(256), 0, s, p);
-    if (p.f16) return launch_pdl(tail_sum_kernel<__half>, grid, dim3(256), 0, s, p);
-    return launch_pdl(tail_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p);
+    if (p.epi.out_f32) return launch_pdl(tail_sum_kernel<float>, grid, dim3(PAIR_COLS), 0, s, p);
+    if (p.f16) return launch_pdl(tail_sum_kernel<__half>, grid, dim3(PAIR_COLS), 0, s, p);
+    return launch_pdl(tail_sum_kernel<__nv_bfloat16>, grid, dim3(PAIR_COLS), 0, s, p);
 }
 
 cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t s) {
