@@ -88,13 +88,13 @@ anvil_status check_norm_sizes(int64_t rows, int width, int dtype, int weight_dty
     return ANVIL_OK;
 }
 
-// The SM count the backward pass is sized for (one constant, so that the workspace needs
-// no device query and the order of the column sums is the same everywhere).
+// The SM count the work is divided for (a GB300's; one constant, so that the workspaces need
+// no device query and the order of the sums is the same everywhere).
 constexpr int PLAN_SMS = 152;
 
 size_t norm_bwd_bytes(const anvil_layernorm_grad_desc* d) {
     if (d->rows == 0 || (!d->dweight && !d->dbias)) return 0;
-    const int blocks = norm_bwd_blocks(d->rows, d->width, d->dtype, PLAN_SMS);
+    const int blocks = norm_bwd_max_blocks(d->rows, d->width, d->dtype);
     return blocks > 1 ? align256(sizeof(float) * 2 * static_cast<size_t>(blocks) * d->width) : 0;
 }
 
@@ -180,24 +180,37 @@ struct Plan {
     size_t part;   // bytes of the tail tiles' parts
 };
 
-constexpr int FEW_ROWS = 128;
+constexpr int FEW_ROWS = 256;  // row_gemm_kernel is considered up to here
 
-// epilogue: SM cycles that the epilogue of a whole tile takes beyond the products.
+// epilogue: SM cycles that the epilogue of a whole tile of the pair kernel takes.
 Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32, double epilogue) {
     Plan p = {};
     const int64_t kb = (k + GEMM_BK - 1) / GEMM_BK;
+    double best = 0;
     if (rows <= FEW_ROWS && !a_mn && !out_f32) {
-        p.few = true;
-        p.bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-        const int64_t tiles = static_cast<int64_t>((cols + ROW_TILE_A - 1) / ROW_TILE_A) * ((rows + p.bn - 1) / p.bn);
-        p.splits = 1;
-        while (p.splits < 8 && tiles * p.splits * 2 <= PLAN_SMS) {
-            const int64_t per = (kb + p.splits * 2 - 1) / (p.splits * 2);
-            if (per * (p.splits * 2 - 1) >= kb) break;  // every split has work
-            p.splits *= 2;
+        // Blocks of 128 weight rows by 16 to 128 tokens, the contraction whole or split over a
+        // cluster.  Estimated times in SM cycles, from the kernel's own time stamps: 545 for a
+        // k-block (the MMA reads its 128-row operand at 32 bytes a cycle, whatever the tokens),
+        // 1700 to the first and from the last, 28 for a token's column; a join 2500, and 250 for
+        // a token's column of each block's share.
+        for (int bn = 16; bn <= 128; bn *= 2) {
+            const int64_t tiles = static_cast<int64_t>((cols + ROW_TILE_A - 1) / ROW_TILE_A) * ((rows + bn - 1) / bn);
+            const double columns = static_cast<double>(bn < rows ? bn : rows) * (epilogue / 2500.0);
+            for (int s = 1; s <= 8; s *= 2) {
+                const int64_t per = (kb + s - 1) / s;
+                if (s > 1 && (per * (s - 1) >= kb || tiles * s > PLAN_SMS)) break;  // every split has work
+                const double turns = static_cast<double>((tiles * s + PLAN_SMS - 1) / PLAN_SMS);
+                const double finish = s == 1 ? 28.0 * columns : 2500.0 + 10.0 * bn + 60.0 * columns / s;
+                const double cost = turns * (per * 545.0 + 1700.0 + finish);
+                if (best == 0 || cost < best) {
+                    best = cost;
+                    p.few = true;
+                    p.bn = bn;
+                    p.splits = s;
+                    p.kb = static_cast<int>(per);
+                }
+            }
         }
-        p.kb = static_cast<int>((kb + p.splits - 1) / p.splits);
-        return p;
     }
     // Tiles in one piece, turn by turn of the grid's pairs; the tiles left over for a last turn
     // that would not be full, or all of them, may go in parts instead (split along k, or whole
@@ -208,19 +221,26 @@ Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32, do
     const int64_t pairs = PLAN_SMS / 2;
     const int64_t tiles = ((rows + PAIR_ROWS - 1) / PAIR_ROWS) * ((cols + PAIR_COLS - 1) / PAIR_COLS);
     const double products = kb * 550.0, turn = products > epilogue ? products : epilogue;
-    p.whole = static_cast<int>(tiles);
-    p.splits = 1;
-    p.kb = static_cast<int>(kb);
-    double best = static_cast<double>((tiles + pairs - 1) / pairs) * turn + (products < epilogue ? products : epilogue) + 2500.0;
+    const double leave = 7500.0;  // filling the pipeline and leaving the kernel
+    const double whole_cost =
+        static_cast<double>((tiles + pairs - 1) / pairs) * turn + (products < epilogue ? products : epilogue) + leave;
+    if (best == 0 || whole_cost < best) {
+        best = whole_cost;
+        p.few = false;
+        p.whole = static_cast<int>(tiles);
+        p.splits = 1;
+        p.kb = static_cast<int>(kb);
+    }
     for (int64_t tail = tiles % pairs;; tail = tiles) {
         const int64_t whole = tiles - tail;
         for (int64_t s = 1; tail && s <= 64 && s <= kb; ++s) {
             const int64_t per = (kb + s - 1) / s;
             if (per * (s - 1) >= kb) continue;  // every split has work
             const int64_t turns = (tail * s + pairs - 1) / pairs;
-            const double cost = whole / pairs * turn + turns * (per * 550.0 + 2500.0) + 8000.0 + tail * s * 200.0;
+            const double cost = whole / pairs * turn + turns * (per * 550.0 + 2500.0) + leave + 8000.0 + tail * s * 200.0;
             if (cost < best) {
                 best = cost;
+                p.few = false;
                 p.whole = static_cast<int>(whole);
                 p.splits = static_cast<int>(s);
                 p.kb = static_cast<int>(per);
@@ -506,6 +526,8 @@ anvil_status anvil_layernorm_forward(const anvil_layernorm_desc* d, void* stream
     p.dtype = d->dtype;
     p.weight_dtype = d->weight_dtype;
     p.eps = d->eps;
+    p.team_rows = 0;
+    p.err = dev->err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = profiled(ANVIL_KERNEL_NORM_FORWARD, s, [&] { return launch_norm_fwd(p, s); });
     return e ? cuda_fail(e, "layer norm launch") : ANVIL_OK;
@@ -574,7 +596,8 @@ anvil_status anvil_layernorm_backward(const anvil_layernorm_grad_desc* d, void* 
     p.width = d->width;
     p.dtype = d->dtype;
     p.weight_dtype = d->weight_dtype;
-    p.blocks = norm_bwd_blocks(d->rows, d->width, d->dtype, PLAN_SMS);
+    p.err = dev->err;
+    norm_bwd_plan(&p);
     if ((e = profiled(ANVIL_KERNEL_NORM_BACKWARD, s, [&] { return launch_norm_bwd(p, s); })))
         return cuda_fail(e, "layer norm gradient launch");
     if (p.blocks > 1 && (p.dweight || p.dbias) &&

@@ -51,11 +51,38 @@ namespace {
 constexpr int CTA_ROWS = 128;
 constexpr int QBOX = 16384;             // one staging box: 128 rows of 128 bytes
 constexpr int A_STAGE = CTA_ROWS * 128; // 16 KB: this CTA's A rows of a k-block
-constexpr int EPI_GROUPS = 2;           // epilogue warp groups, one per half of the columns
-constexpr int EPI_WARP0 = 4;            // warps 4-11; warp 0: TMA producer, warp 1: MMA issuer and TMEM owner
+constexpr int EPI_GROUPS = 4;           // epilogue warp groups, one per quarter of the columns
+constexpr int EPI_WARP0 = 4;            // warps 4-19; warp 1: MMA issuer and TMEM owner; warps 0 and 2: TMA producers
+constexpr int PRODUCERS = 2;
 constexpr int PAIR_THREADS = 32 * (EPI_WARP0 + 4 * EPI_GROUPS);
 constexpr int CHAIN_KB = 8;             // k-blocks of one chain of an fp32 result (512 deep)
 constexpr int RASTER_ROWS = 8;          // rows of tiles per raster group
+
+// 32 lanes x 16 or 8 consecutive fp32 columns of TMEM (as tmem_ld_32x32b_x32).
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 // kind::f16 instruction descriptor with fp32 accumulation; the operands' type is both
 // bf16 (1) or both fp16 (0).
@@ -175,7 +202,8 @@ constexpr int BN = PAIR_COLS;
 constexpr int B_STAGE = BN / 2 * 128;  // 16 KB: this CTA's half of the B columns of a k-block
 constexpr int STAGE = A_STAGE + B_STAGE;
 constexpr int STAGES = 5;
-constexpr int BOXES = 2 * EPI_GROUPS;
+constexpr int BOXES = EPI_GROUPS;
+constexpr int EPI_COLS = BN / EPI_GROUPS;  // 64: one staging box of 16-bit results, two of fp32
 constexpr int PAIR_SMEM = STAGES * STAGE + BOXES * QBOX + 1024;  // + alignment slack
 constexpr uint32_t PAIR_TMEM = 2 * BN;
 
@@ -270,20 +298,19 @@ __device__ __forceinline__ void rows_to_box(uint32_t box, const E* src, long lon
     }
 }
 
-// Per-thread epilogue state of one group (128 threads, two staging boxes).  The group's
-// stores alternate between its boxes, one commit group each, so a box is free again once
-// all but the latest store have been read.
+// Per-thread epilogue state of one group (128 threads, one staging box).
 struct EpiState {
-    uint32_t boxes;      // shared address of the group's two boxes
-    uint64_t* in_bar;    // the group's two input-load barriers
+    uint32_t box;        // shared address of the group's box
+    uint64_t* in_bar;    // the barrier of its input loads
     int r, quad, lane, grp;
     bool leader;
     bool fail;
-    int loads[2];        // input loads armed per box (parity of the barrier)
+    int loads;           // input loads armed (parity of the barrier)
 };
 
+// The box may be written: its last store has been read.
 __device__ __forceinline__ void box_free(const EpiState& x) {
-    if (x.leader) bulk_wait_read_but_one();
+    if (x.leader) bulk_wait_read_all();
     named_barrier_sync(1 + x.grp, 128);
 }
 
@@ -293,37 +320,39 @@ __device__ __forceinline__ void tma_store_box(const CUtensorMap* tm, uint32_t bo
                  : "memory");
 }
 
-// Sends one box of results out: by TMA (the group's leader, after every thread's writes),
-// or by the warps themselves, each its own rows.
+// Sends the box out: by TMA (the group's leader, after every thread's writes), or by the
+// warps themselves, each its own rows.
 template <typename E>
-__device__ __forceinline__ void send_box(const EpiState& x, const CUtensorMap* tm, int by_tma, uint32_t box, void* dst,
-                                         long long ld, int row0, int col0, int rows, int cols) {
+__device__ __forceinline__ void send_box(const EpiState& x, const CUtensorMap* tm, int by_tma, void* dst, long long ld,
+                                         int row0, int col0, int rows, int cols) {
     if (by_tma) {
         fence_proxy_async_smem();
         named_barrier_sync(1 + x.grp, 128);
-        if (x.leader && row0 < rows && col0 < cols) tma_store_box(tm, box, col0, row0);
+        if (x.leader) {
+            if (row0 < rows && col0 < cols) tma_store_box(tm, x.box, col0, row0);
+            bulk_commit_group();
+        }
     } else {
         __syncwarp();
-        box_to_rows<E>(box, static_cast<E*>(dst), ld, row0, col0, rows, cols, x.quad, x.lane);
-        fence_proxy_async_smem();  // before an input load into this box
+        box_to_rows<E>(x.box, static_cast<E*>(dst), ld, row0, col0, rows, cols, x.quad, x.lane);
+        fence_proxy_async_smem();  // before an input load into the box
         __syncwarp();
     }
-    if (x.leader) bulk_commit_group();
 }
 
-__device__ __forceinline__ void arm_input(EpiState& x, const CUtensorMap* tm, int b, int col0, int row0) {
+__device__ __forceinline__ void arm_input(EpiState& x, const CUtensorMap* tm, int col0, int row0) {
     if (x.leader) {
-        mbar_arrive_expect_tx(&x.in_bar[b], QBOX);
+        mbar_arrive_expect_tx(x.in_bar, QBOX);
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(x.boxes + b * QBOX),
-            "l"(tm), "r"(smem_u32(&x.in_bar[b])), "r"(col0), "r"(row0), "r"(0)
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(x.box),
+            "l"(tm), "r"(smem_u32(x.in_bar)), "r"(col0), "r"(row0), "r"(0)
             : "memory");
     }
-    ++x.loads[b];
+    ++x.loads;
 }
-__device__ __forceinline__ void wait_input(EpiState& x, int b, unsigned* err) {
-    if (!mbar_wait(&x.in_bar[b], static_cast<uint32_t>(x.loads[b] - 1) & 1u, err)) x.fail = true;
+__device__ __forceinline__ void wait_input(EpiState& x, unsigned* err) {
+    if (!mbar_wait(x.in_bar, static_cast<uint32_t>(x.loads - 1) & 1u, err)) x.fail = true;
 }
 
 // The accumulator is read: its next products may start.
@@ -333,76 +362,75 @@ __device__ __forceinline__ void release_acc(const EpiState& x, uint32_t tempty) 
     if (x.lane == 0) mbar_arrive_cluster(tempty);
 }
 
-// Whether a whole 16-bit tile's residual comes by TMA (into the result's boxes, ahead of
-// the accumulator): not where z takes one of the two boxes.
+// Whether a whole 16-bit tile's residual comes by TMA ahead of the accumulator: not where z
+// takes the box first.
 __device__ __forceinline__ bool early_input(const PairGemmParams& p) { return p.epi.in && p.in_tma && !p.epi.z; }
 
-// The 16-bit epilogue of this group's half of a tile, 64 columns (one box row) at a time.
+// The 16-bit epilogue of this group's quarter of a tile: z first where it is stored, then y
+// (the accumulator is read again: TMEM is not what bounds it).
 template <typename T>
 __device__ __forceinline__ void epilogue_16(const PairGemmParams& p, EpiState& x, uint32_t tacc, uint32_t tempty, int row0,
                                             int col0) {
-    constexpr int PIECES = BN / 2 / 64;
     const GemmEpilogue& e = p.epi;
     const bool early = early_input(p);
 #pragma unroll 1
-    for (int q = 0; q < PIECES; ++q) {
-        const int pc = col0 + 64 * q;
-        // z leaves through box 0 and y through box 1 where both are stored
-        const int yb = e.z ? 1 : q & 1;
-        const uint32_t ybox = x.boxes + yb * QBOX, zbox = x.boxes;
-        float v[64];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) tmem_ld_32x32b_x32(tacc + q * 64 + h * 32, reinterpret_cast<float(&)[32]>(v[32 * h]));
-        if (q == PIECES - 1) release_acc(x, tempty);
-        if (e.bias) add_bias<T, 64>(e, pc, p.cols, v);
-        if (e.z) {
-            box_free(x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sts128(box_addr(zbox, x.r, j), Elem<T>::pack(v + 8 * j));
-            send_box<uint16_t>(x, &p.tm_z, p.z_tma, zbox, e.z, e.ldz, row0, pc, p.rows, p.cols);
-        }
-        act_values<64>(e.act, v);
-        if (early) wait_input(x, yb, p.err);
+    for (int pass = e.z ? 0 : 1; pass < 2; ++pass) {
+        const bool final = pass == 1;
+        if (final && early) wait_input(x, p.err);
         else box_free(x);
-        if (e.in && !early) {
-            rows_to_box<uint16_t>(ybox, static_cast<const uint16_t*>(e.in), e.ldin, row0, pc, p.rows, p.cols, x.quad, x.lane);
-            __syncwarp();
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t a = box_addr(ybox, x.r, j);
-            if (e.in) {
-                float f[8];
-                Elem<T>::unpack(lds128(a), f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];
+        if (final && e.in && !early) {
+            if (p.in_tma) {
+                arm_input(x, &p.tm_in, col0, row0);
+                wait_input(x, p.err);
+            } else {
+                rows_to_box<uint16_t>(x.box, static_cast<const uint16_t*>(e.in), e.ldin, row0, col0, p.rows, p.cols, x.quad,
+                                      x.lane);
+                __syncwarp();
             }
-            sts128(a, Elem<T>::pack(v + 8 * j));
         }
-        send_box<uint16_t>(x, &p.tm_out, p.out_tma, ybox, e.out, e.ldout, row0, pc, p.rows, p.cols);
+#pragma unroll 1
+        for (int c = 0; c < EPI_COLS / 16; ++c) {
+            float v[16];
+            tmem_ld_16(tacc + c * 16, v);
+            if (e.bias) add_bias<T, 16>(e, col0 + c * 16, p.cols, v);
+            if (final) act_values<16>(e.act, v);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t a = box_addr(x.box, x.r, c * 2 + j);
+                if (final && e.in) {
+                    float f[8];
+                    Elem<T>::unpack(lds128(a), f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];
+                }
+                sts128(a, Elem<T>::pack(v + 8 * j));
+            }
+        }
+        if (final) release_acc(x, tempty);
+        if (final) send_box<uint16_t>(x, &p.tm_out, p.out_tma, e.out, e.ldout, row0, col0, p.rows, p.cols);
+        else send_box<uint16_t>(x, &p.tm_z, p.z_tma, e.z, e.ldz, row0, col0, p.rows, p.cols);
     }
 }
 
-// 32 fp32 columns of this thread's row through box b: to the scratch of split `part`, or to
-// the fp32 result (with what it held).
-__device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, const float* v, int b, int part, int lrow, int lcol,
+// 32 fp32 columns of this thread's row through the box: to the scratch of split `part`, or
+// to the fp32 result (with what it held).
+__device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, const float* v, int part, int lrow, int lcol,
                                           int row0, int col0) {
     const GemmEpilogue& e = p.epi;
-    const uint32_t box = x.boxes + b * QBOX;
     const bool in = e.in && part < 0;
     box_free(x);
     if (in) {
         if (p.in_tma) {
-            arm_input(x, &p.tm_in, b, col0, row0);
-            wait_input(x, b, p.err);
+            arm_input(x, &p.tm_in, col0, row0);
+            wait_input(x, p.err);
         } else {
-            rows_to_box<uint32_t>(box, static_cast<const uint32_t*>(e.in), e.ldin, row0, col0, p.rows, p.cols, x.quad, x.lane);
+            rows_to_box<uint32_t>(x.box, static_cast<const uint32_t*>(e.in), e.ldin, row0, col0, p.rows, p.cols, x.quad, x.lane);
             __syncwarp();
         }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t a = box_addr(box, x.r, j);
+        const uint32_t a = box_addr(x.box, x.r, j);
         float f[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
         if (in) {
             float o[4];
@@ -416,11 +444,11 @@ __device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, 
         fence_proxy_async_smem();
         named_barrier_sync(1 + x.grp, 128);
         if (x.leader) {
-            tma_store_box(&p.tm_part, box, lcol, part * PAIR_ROWS + lrow);
+            tma_store_box(&p.tm_part, x.box, lcol, part * PAIR_ROWS + lrow);
             bulk_commit_group();
         }
     } else {
-        send_box<uint32_t>(x, &p.tm_out, p.out_tma, box, e.out, e.ldout, row0, col0, p.rows, p.cols);
+        send_box<uint32_t>(x, &p.tm_out, p.out_tma, e.out, e.ldout, row0, col0, p.rows, p.cols);
     }
 }
 
@@ -433,10 +461,11 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
     __shared__ __align__(8) uint64_t empty_bar[STAGES];
     __shared__ __align__(8) uint64_t tfull_bar[2];
     __shared__ __align__(8) uint64_t tempty_bar[2];
-    __shared__ __align__(8) uint64_t in_bar[EPI_GROUPS][2];
+    __shared__ __align__(8) uint64_t in_bar[EPI_GROUPS];
     __shared__ __align__(8) uint64_t mma_done_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int aborted;
+    __shared__ volatile int armed[STAGES];  // 1 + the k-block last loaded into each stage (0: none)
 
     pdl_allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -450,12 +479,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
+            armed[s] = 0;
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull_bar[b], 1);
             mbar_init(&tempty_bar[b], 2 * 4 * EPI_GROUPS);  // each epilogue warp of both CTAs
-            for (int g = 0; g < EPI_GROUPS; ++g) mbar_init(&in_bar[g][b], 1);
         }
+        for (int g = 0; g < EPI_GROUPS; ++g) mbar_init(&in_bar[g], 1);
         mbar_init(&mma_done_bar, 1);
         fence_mbar_init();
         aborted = 0;
@@ -468,24 +498,27 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
     tc_fence_after();
     pdl_wait_previous();
     const uint32_t tmem = tmem_slot;
-    int issued = 0;  // producer: k-blocks whose loads were armed
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
         if (lane == 0) {
-            // ---------------- TMA producer
+            // ---------------- TMA producers: arming a stage and issuing its two loads takes one
+            // thread about 500 cycles, as long as its products, so two take turns
             int it = 0;
+            const int mine = warp / 2;
             for (int u = pair; u < units; u += npairs) {
                 const Unit t = unit_of(p, u);
                 const int arow = t.tr * PAIR_ROWS + CTA_ROWS * static_cast<int>(rank);
                 const int brow = t.tc * BN + BN / 2 * static_cast<int>(rank);
                 bool ok = true;
                 for (int kb = t.kb0; kb < t.kb0 + t.nkb; ++kb, ++it) {
+                    if (it % PRODUCERS != mine) continue;
                     const int s = it % STAGES;
                     if (!mbar_wait(&empty_bar[s], ((it / STAGES) & 1) ^ 1, p.err)) {
                         ok = false;
                         break;
                     }
                     if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * STAGE);
+                    armed[s] = it + 1;
                     const uint32_t fb = map_to_rank(&full_bar[s], 0);
                     uint8_t* sa = smem + s * STAGE;
                     uint8_t* sb = sa + A_STAGE;
@@ -502,7 +535,6 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                     } else {
                         tma_load_3d_pair(sb, &p.tm_b, fb, kc, brow, 0);
                     }
-                    issued = it + 1;
                 }
                 if (!ok) {
                     aborted = 1;
@@ -568,12 +600,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
         x.lane = lane;
         x.r = x.quad * 32 + lane;
         x.leader = x.quad == 0 && lane == 0;
-        x.boxes = smem_u32(smem + STAGES * STAGE + x.grp * 2 * QBOX);
-        x.in_bar = in_bar[x.grp];
+        x.box = smem_u32(smem + STAGES * STAGE + x.grp * QBOX);
+        x.in_bar = &in_bar[x.grp];
         x.fail = false;
-        x.loads[0] = x.loads[1] = 0;
+        x.loads = 0;
         const uint32_t te[2] = {map_to_rank(&tempty_bar[0], 0), map_to_rank(&tempty_bar[1], 0)};
-        const int lrow = CTA_ROWS * static_cast<int>(rank), lcol = BN / 2 * x.grp;  // within the tile
+        const int lrow = CTA_ROWS * static_cast<int>(rank), lcol = EPI_COLS * x.grp;  // within the tile
         int acc = 0;
         for (int u = pair; u < units; u += npairs) {
             // the group stops together once any wait of any role gave up
@@ -586,31 +618,31 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
             const int col0 = t.tc * BN + lcol;
             const uint32_t tlane = tmem + (static_cast<uint32_t>(x.quad * 32) << 16) + static_cast<uint32_t>(lcol);
             if constexpr (F32) {
-                float sum[BN / 2];
+                float sum[EPI_COLS];
 #pragma unroll
-                for (int i = 0; i < BN / 2; ++i) sum[i] = 0.f;
+                for (int i = 0; i < EPI_COLS; ++i) sum[i] = 0.f;
                 for (int c0 = 0; c0 < t.nkb; c0 += CHAIN_KB, ++acc) {
                     const int ab = acc & 1;
                     if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
                     tc_fence_after();
 #pragma unroll
-                    for (int q = 0; q < BN / 2 / 32; ++q) {
-                        float v[32];
-                        tmem_ld_32x32b_x32(tlane + ab * BN + q * 32, v);
+                    for (int q = 0; q < EPI_COLS / 16; ++q) {
+                        float v[16];
+                        tmem_ld_16(tlane + ab * BN + q * 16, v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[q * 32 + i] += v[i];
+                        for (int i = 0; i < 16; ++i) sum[q * 16 + i] += v[i];
                     }
                     release_acc(x, te[ab]);
                 }
 #pragma unroll
-                for (int q = 0; q < BN / 2 / 32; ++q)
-                    store_f32(p, x, sum + 32 * q, q & 1, t.part, lrow, lcol + 32 * q, row0, col0 + 32 * q);
+                for (int q = 0; q < EPI_COLS / 32; ++q)
+                    store_f32(p, x, sum + 32 * q, t.part, lrow, lcol + 32 * q, row0, col0 + 32 * q);
             } else {
                 const int ab = acc & 1;
                 if (t.part < 0 && early_input(p)) {
-                    // the residual, once the boxes' earlier stores have been read
+                    // the residual, once the box's earlier store has been read
                     if (x.leader) bulk_wait_read_all();
-                    for (int q = 0; q < BN / 2 / 64; ++q) arm_input(x, &p.tm_in, q & 1, col0 + 64 * q, row0);
+                    arm_input(x, &p.tm_in, col0, row0);
                 }
                 if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
                 tc_fence_after();
@@ -618,28 +650,27 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                     epilogue_16<T>(p, x, tlane + ab * BN, te[ab], row0, col0);
                 } else {
 #pragma unroll 1
-                    for (int q = 0; q < BN / 2 / 32; ++q) {
+                    for (int q = 0; q < EPI_COLS / 32; ++q) {
                         float v[32];
                         tmem_ld_32x32b_x32(tlane + ab * BN + q * 32, v);
-                        if (q == BN / 2 / 32 - 1) release_acc(x, te[ab]);
-                        store_f32(p, x, v, q & 1, t.part, lrow, lcol + 32 * q, row0, col0 + 32 * q);
+                        if (q == EPI_COLS / 32 - 1) release_acc(x, te[ab]);
+                        store_f32(p, x, v, t.part, lrow, lcol + 32 * q, row0, col0 + 32 * q);
                     }
                 }
                 ++acc;
             }
         }
         if (x.leader) {
-            bulk_wait_read_all();  // the group's stores have read their boxes
-            for (int b = 0; b < 2; ++b)
-                if (x.loads[b]) mbar_wait(&x.in_bar[b], static_cast<uint32_t>(x.loads[b] - 1) & 1u, p.err);
+            bulk_wait_read_all();  // the group's last store has read its box
+            if (x.loads) mbar_wait(x.in_bar, static_cast<uint32_t>(x.loads - 1) & 1u, p.err);
         }
     }
 
     __syncthreads();
     if (aborted && warp == 0 && lane == 0 && rank == 0) {
         // the pair's loads in flight land before its shared memory goes away
-        for (int kb = issued - STAGES < 0 ? 0 : issued - STAGES; kb < issued; ++kb)
-            mbar_wait(&full_bar[kb % STAGES], (kb / STAGES) & 1, p.err);
+        for (int s = 0; s < STAGES; ++s)
+            if (armed[s]) mbar_wait(&full_bar[s], ((armed[s] - 1) / STAGES) & 1, p.err);
     }
     tc_fence_before();
     cluster_sync();
@@ -696,7 +727,8 @@ __global__ void __launch_bounds__(PAIR_COLS) tail_sum_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------- few rows
-constexpr int ROW_THREADS = 192;  // warp 0: TMA producer, warp 1: MMA issuer and TMEM owner, warps 2-5: epilogue
+constexpr int ROW_THREADS = 256;  // warp 1: MMA issuer and TMEM owner, warps 2-5: epilogue, warps 0, 6 and 7: TMA producers
+constexpr int ROW_PRODUCERS = 3;
 template <int BN>
 struct RowShape {
     static constexpr int STAGE = A_STAGE + BN * 128;
@@ -748,6 +780,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
     __shared__ __align__(8) uint64_t done_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int aborted;
+    __shared__ volatile int armed[S::STAGES];  // 1 + the k-block last loaded into each stage (0: none)
 
     pdl_allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -763,6 +796,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
         for (int s = 0; s < S::STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
+            armed[s] = 0;
         }
         mbar_init(&done_bar, 1);
         fence_mbar_init();
@@ -776,17 +810,18 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
     tc_fence_after();
     pdl_wait_previous();
     const uint32_t tmem = tmem_slot;
-    int issued = 0;  // producer: k-blocks whose loads were armed
 
-    if (warp == 0) {
+    if (warp == 0 || warp >= 6) {
         if (lane == 0) {
-            for (int it = 0; it < nkb; ++it) {
+            const int mine = warp == 0 ? 0 : warp - 5;
+            for (int it = mine; it < nkb; it += ROW_PRODUCERS) {
                 const int s = it % S::STAGES;
                 if (!mbar_wait(&empty_bar[s], ((it / S::STAGES) & 1) ^ 1, p.err)) {
                     aborted = 1;
                     break;
                 }
                 mbar_arrive_expect_tx(&full_bar[s], S::STAGE);
+                armed[s] = it + 1;
                 uint8_t* sa = smem + s * S::STAGE;
                 const int kc = (kb0 + it) * GEMM_BK;
                 if (p.a_mn) {
@@ -796,7 +831,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
                     tma_load_3d(sa, &p.tm_a, &full_bar[s], kc, a0, 0);
                 }
                 tma_load_3d(sa + A_STAGE, &p.tm_b, &full_bar[s], kc, b0, 0);
-                issued = it + 1;
             }
         }
     } else if (warp == 1) {
@@ -804,9 +838,11 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
             const uint32_t stage0 = smem_u32(smem);
             const uint32_t idesc = idesc_16(ROW_TILE_A, BN, p.a_mn, false, p.f16);
             const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, a_lbo = p.a_mn ? 8192 : 16;
+            int s = 0;
+            uint32_t ph = 0;
+            bool ready = false;
             for (int it = 0; it < nkb; ++it) {
-                const int s = it % S::STAGES;
-                if (!mbar_wait(&full_bar[s], (it / S::STAGES) & 1, p.err)) {
+                if (!ready && !mbar_wait(&full_bar[s], ph, p.err)) {
                     aborted = 1;
                     break;
                 }
@@ -817,7 +853,12 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
                 for (int kk = 0; kk < GEMM_BK / 16; ++kk)
                     umma_bf16(tmem, sw128_desc(a_lo + kk * a_step), sw128_desc(b_lo + kk * (32 >> 4)), idesc,
                               (it | kk) != 0 ? 1u : 0u);
+                const int s_next = s + 1 == S::STAGES ? 0 : s + 1;
+                const uint32_t ph_next = s_next == 0 ? ph ^ 1u : ph;
+                ready = mbar_test_wait(smem_u32(&full_bar[s_next]), ph_next);
                 umma_commit(&empty_bar[s]);
+                s = s_next;
+                ph = ph_next;
             }
             umma_commit(&done_bar);
             mbar_wait(&done_bar, 0, p.err);
@@ -835,58 +876,55 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
             bias = p.epi.bias_f32 ? static_cast<const float*>(p.epi.bias)[col] : Elem<T>::load(static_cast<const T*>(p.epi.bias)[col]);
         mbar_wait(&done_bar, 0, p.err);
         tc_fence_after();
-        // the partial accumulator, in place of the stages (which are done): four B rows of one
-        // A row side by side, [BN / 4][128] of them
-        float4* own = reinterpret_cast<float4*>(smem);
-        for (int q = 0; q * 32 < nb; ++q) {
-            float v[32];
-            tmem_ld_32x32b_x32(tlane + q * 32, v);
-            if (p.splits == 1) {
-                if (live) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                        if (q * 32 + 8 * h < nb)
-                            finish_rows<T, 8>(p.epi, reinterpret_cast<float(&)[8]>(v[8 * h]), bias, b0 + q * 32 + 8 * h,
-                                              nb - q * 32 - 8 * h, col);
-                }
-            } else {
-#pragma unroll
-                for (int h = 0; h < 8; ++h)
-                    if (q * 32 + 4 * h < nb)
-                        own[(q * 8 + h) * ROW_TILE_A + r] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+        if (p.splits == 1) {
+#pragma unroll 1
+            for (int q = 0; q < nb; q += 8) {
+                float v[8];
+                tmem_ld_8(tlane + q, v);
+                if (live) finish_rows<T, 8>(p.epi, v, bias, b0 + q, nb - q, col);
             }
-        }
-        __syncwarp();
-        if (p.splits > 1) {
+        } else {
+            // the partial accumulator, in place of the stages (which are done): four B rows of one
+            // A row side by side, [BN / 4][128] of them
+            float4* own = reinterpret_cast<float4*>(smem);
+            const int quads = (nb + 3) / 4;
+#pragma unroll 1
+            for (int q = 0; q < quads; q += 2) {
+                float v[8];
+                tmem_ld_8(tlane + q * 4, v);
+                own[q * ROW_TILE_A + r] = make_float4(v[0], v[1], v[2], v[3]);
+                own[(q + 1) * ROW_TILE_A + r] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+            __syncwarp();
             cluster_sync();
             // every CTA finishes its share of the B rows, two fours at a time, the parts added in
-            // rank order
-            const int quads = (nb + 3) / 4;
-            for (int j = split; j < quads; j += 2 * p.splits) {
-                const int j2 = j + p.splits;
-                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                const uint32_t mine = smem_u32(&own[j * ROW_TILE_A + r]), next = smem_u32(&own[j2 * ROW_TILE_A + r]);
-#pragma unroll 4
-                for (int s = 0; s < p.splits; ++s) {
-                    uint32_t a, a2;
+            // rank order (rows past nb are computed and not stored)
+#pragma unroll 1
+            for (int j = 2 * split; j < quads; j += 2 * p.splits) {
+                const uint32_t mine = smem_u32(&own[j * ROW_TILE_A + r]);
+                float4 f[8][2];  // every part on its way before the first is used
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    if (s >= p.splits) break;
+                    uint32_t a;
                     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(mine), "r"(s));
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a2) : "r"(next), "r"(s));
-                    const float4 f = ld_cluster_f4(a);
-                    const float4 g = j2 < quads ? ld_cluster_f4(a2) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    v[0] += f.x;
-                    v[1] += f.y;
-                    v[2] += f.z;
-                    v[3] += f.w;
-                    v[4] += g.x;
-                    v[5] += g.y;
-                    v[6] += g.z;
-                    v[7] += g.w;
+                    f[s][0] = ld_cluster_f4(a);
+                    f[s][1] = ld_cluster_f4(a + 16 * ROW_TILE_A);
                 }
-                if (live) {
-                    finish_rows<T, 4>(p.epi, reinterpret_cast<float(&)[4]>(v[0]), bias, b0 + 4 * j, nb - 4 * j, col);
-                    if (j2 < quads)
-                        finish_rows<T, 4>(p.epi, reinterpret_cast<float(&)[4]>(v[4]), bias, b0 + 4 * j2, nb - 4 * j2, col);
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    if (s >= p.splits) break;
+                    v[0] += f[s][0].x;
+                    v[1] += f[s][0].y;
+                    v[2] += f[s][0].z;
+                    v[3] += f[s][0].w;
+                    v[4] += f[s][1].x;
+                    v[5] += f[s][1].y;
+                    v[6] += f[s][1].z;
+                    v[7] += f[s][1].w;
                 }
+                if (live) finish_rows<T, 8>(p.epi, v, bias, b0 + 4 * j, nb - 4 * j, col);
             }
             __syncwarp();
         }
@@ -894,14 +932,14 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
     }
     __syncwarp();
     if (p.splits > 1) {
-        if (warp < 2) cluster_sync();  // the first barrier of the epilogue warps above
+        if (warp < 2 || warp >= 6) cluster_sync();  // the first barrier of the epilogue warps above
         cluster_sync();                // no CTA leaves while its partial accumulator is read
     }
     __syncthreads();
     if (aborted && threadIdx.x == 0) {
         // the loads in flight land before the shared memory goes away
-        for (int kb = issued - S::STAGES < 0 ? 0 : issued - S::STAGES; kb < issued; ++kb)
-            mbar_wait(&full_bar[kb % S::STAGES], (kb / S::STAGES) & 1, p.err);
+        for (int s = 0; s < S::STAGES; ++s)
+            if (armed[s]) mbar_wait(&full_bar[s], ((armed[s] - 1) / S::STAGES) & 1, p.err);
     }
     __syncthreads();
     tc_fence_after();

@@ -12,14 +12,13 @@
 // fp32 pairs: about 4.5 instructions per element, where scalar ones took 8 and the issue
 // rate, not HBM, was the bound.
 //
-// The top k are found in the same pass.  A warp holds the best k it has met, one per lane
-// in order; putting one in costs tens of instructions, so few may be tried.  Each of a
-// block's eight warps publishes its four best values (first the largest of its threads'
-// maxima of the first turn, later the head of its list); the k-th largest of those 32 is a
-// value that at least k elements reach, and what lies below it is passed over.  It is read
-// without a barrier (a stale one is only lower), and a warp looks at single values only of
-// vectors whose maximum reaches it.  In the end every entry of the eight lists counts the
-// entries ahead of it: its place.
+// The top k cost the pass one store a turn: every thread keeps the largest of its values of
+// each turn (32 values, fp32: 16) in shared memory.  The k-th largest of the 256 threads'
+// maxima is a value that at least k elements reach, and hardly more do; the few turns whose
+// maximum reaches it are read again (from L2), their elements that reach it are listed, and
+// each counts the entries ahead of it: its place.  A row with more such elements than the
+// list holds (many equal values) takes a slower walk that keeps, per warp, the best k in
+// order, one per lane.
 //
 // HBM bounds both passes where there are many rows; where rows are fewer than the SMs, a
 // cluster of up to eight blocks takes a row's segments and the first block joins their
@@ -125,19 +124,30 @@ __device__ __forceinline__ void top_offer(TopList& L, int top, int lane, bool ca
     }
 }
 
-// The k-th largest of 32 lanes' keys, to 16 bits (below it where cut).
-__device__ __forceinline__ int kth_largest(int key, int k) {
-    const uint32_t u = static_cast<uint32_t>(key) ^ 0x80000000u;
-    uint32_t cut = 0;
-#pragma unroll
-    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
-        if (__popc(__ballot_sync(0xffffffffu, u >= (cut | bit))) >= k) cut |= bit;
-    return static_cast<int>(cut ^ 0x80000000u);
-}
-
 constexpr int FWD_THREADS = 256;
 constexpr int FWD_WARPS = FWD_THREADS / 32;
+
+// The k-th largest of the block's FWD_THREADS keys, to 16 bits (below it where cut;
+// KEY_NONE where fewer than k threads have one).  Every warp finds it for itself.
+__device__ __forceinline__ int kth_largest(const int* keys, int k, int lane) {
+    uint32_t u[FWD_WARPS];
+#pragma unroll
+    for (int w = 0; w < FWD_WARPS; ++w) u[w] = static_cast<uint32_t>(keys[w * 32 + lane]) ^ 0x80000000u;
+    uint32_t cut = 0;
+#pragma unroll 1
+    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < FWD_WARPS; ++w) n += u[w] >= (cut | bit);
+        if (__reduce_add_sync(0xffffffffu, n) >= k) cut |= bit;
+    }
+    return static_cast<int>(cut ^ 0x80000000u);
+}
 constexpr int UNROLL = 4;  // 16-byte loads in flight per thread
+constexpr int MAX_GROUPS = 16;  // groups of turns whose maxima a thread keeps
+// Listed elements: below k <= 32 threads with vectors there are at most 31 of them, with 32
+// values each, and the elements around the vectors.
+constexpr int TOP_LIST = 1024;
 
 struct BlockResult {
     Stats st;
@@ -211,23 +221,32 @@ __device__ __forceinline__ void take(Stats& st, const uint4 (&raw)[N], int cnt) 
     st.q += q;
 }
 
-// Place of entry (key, idx) among the first cnt[w] entries of each list w.
-__device__ __forceinline__ int place_of(int key, int idx, const int (*keys)[LOGPROB_MAX_TOP], const int (*idxs)[LOGPROB_MAX_TOP],
-                                        const int* cnt, int lists) {
+// Shared memory of the top k (none without them).
+template <bool TOP>
+struct TopShared {
+    int group_max[MAX_GROUPS][FWD_THREADS];  // keys
+    int thread_max[FWD_THREADS];
+    int key[TOP_LIST], idx[TOP_LIST];
+    int count;
+};
+template <>
+struct TopShared<false> {};
+
+// Place of entry (key, idx) among the first n listed.
+template <bool TOP>
+__device__ __forceinline__ int place_of(int key, int idx, const TopShared<TOP>& sh, int n) {
     int place = 0;
-    for (int w = 0; w < lists; ++w)
-        for (int j = 0; j < cnt[w]; ++j) place += better(keys[w][j], idxs[w][j], key, idx) ? 1 : 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) place += better(sh.key[j], sh.idx[j], key, idx) ? 1 : 0;
     return place;
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobParams p, int csize) {
+__global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const LogprobParams p, int csize) {
     constexpr int E = Elem<T>::VEC;
     __shared__ Stats wst[FWD_WARPS];
-    __shared__ int wkey[TOP ? FWD_WARPS : 1][LOGPROB_MAX_TOP], widx[TOP ? FWD_WARPS : 1][LOGPROB_MAX_TOP];
-    __shared__ int wcnt[FWD_WARPS];
-    __shared__ int best[32];  // the four best values of each warp
     __shared__ BlockResult res;
+    __shared__ TopShared<TOP> top;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x / csize;
     const int rank = blockIdx.x % csize;
@@ -244,107 +263,149 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
     const int v0 = min(rank * per, nvec), v1 = min(v0 + per, nvec);
 
     Stats st = {-INFINITY, 0.f, 0.f};
-    TopList L;
-    top_init(L);
-    // at most E - 1 single elements of the head and of the tail, a lane each of warp 0; the
-    // tail comes after the vectors, so that warp 0 too sees its indexes grow
-    auto singles = [&](int c0, int cnt) {
-        const bool in = lane < cnt;
-        const float v = in ? Elem<T>::load(x[c0 + lane]) : -INFINITY;
-        if (in) take_one(st, v);
-        __syncwarp();
-        if (TOP) top_offer(L, p.top, lane, in, order_key(v), c0 + lane);
-    };
-    if (warp == 0 && rank == 0) singles(0, head);
+    // at most E - 1 single elements of the head and of the tail, a lane each of warp 0
+    const int nh = rank == 0 ? head : 0, nt = rank == csize - 1 ? p.vocab - tail0 : 0;
+    if (warp == 0 && lane < nh + nt) take_one(st, Elem<T>::load(x[lane < nh ? lane : tail0 + lane - nh]));
     const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-    // A warp's UNROLL vectors per lane are one run of 32 * UNROLL vectors, so the indexes a
-    // warp sees grow from turn to turn.
-    int tau = KEY_NONE;  // at least `top` of the block's elements reach it
-    for (int base = v0; base < v1; base += FWD_THREADS * UNROLL) {
-        const int at = base + warp * 32 * UNROLL + lane;
+    // A warp's UNROLL vectors per lane are one run of 32 * UNROLL vectors.
+    constexpr int TURN = FWD_THREADS * UNROLL;
+    const int mine = v0 + warp * 32 * UNROLL + lane;  // this thread's first vector
+    const int per_group = ((v1 - v0 + TURN - 1) / TURN + MAX_GROUPS - 1) / MAX_GROUPS;  // turns
+    int key_all = KEY_NONE, key_group = KEY_NONE, in_group = 0, group = 0;
+    for (int base = v0; base < v1; base += TURN) {
+        const int at = mine + (base - v0);
         uint4 raw[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u)
             raw[u] = at + u * 32 < v1 ? __ldcs(xv + at + u * 32)
                                       : make_uint4(Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF);
-        uint32_t mw[UNROLL];  // the largest of each vector, as a word
+        uint32_t mw = raw[0].x;
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u)
-            mw[u] = Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w));
-        const float mx = Elem<T>::word_max(Elem<T>::max_word(Elem<T>::max_word(mw[0], mw[1]), Elem<T>::max_word(mw[2], mw[3])));
+            mw = Elem<T>::max_word(mw, Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w)));
+        const float mx = Elem<T>::word_max(mw);
         raise_max(st, mx);
         take<T, UNROLL>(st, raw, (v1 - at + 31) / 32);  // vectors at + 32 u < v1
         if constexpr (TOP) {
-            const int mk = at < v1 ? order_key(mx) : KEY_NONE;
-            if (base == v0) {
-                int rest = mk;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int m = __reduce_max_sync(0xffffffffu, rest);
-                    const unsigned who = __ballot_sync(0xffffffffu, rest == m);
-                    if (lane == __ffs(who) - 1) rest = KEY_NONE;
-                    if (lane == 0) best[warp * 4 + c] = m;
-                }
-                __syncthreads();
-            }
-            if (__any_sync(0xffffffffu, mk >= tau && mk > L.kth_key)) {
-                const int r = kth_largest(static_cast<volatile int*>(best)[lane], p.top);
-                tau = r > tau ? r : tau;
-                bool more = false;
-#pragma unroll
-                for (int u = 0; u < UNROLL; ++u) {
-                    const int vec = at + u * 32;
-                    const int vk = vec < v1 ? order_key(Elem<T>::word_max(mw[u])) : KEY_NONE;
-                    const bool hold = vk >= tau && vk > L.kth_key;
-                    if (__any_sync(0xffffffffu, hold)) {
-                        more = true;
-                        float v[E];
-                        Elem<T>::unpack(raw[u], v);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const int key = order_key(v[e]);
-                            const bool cand = hold && key >= tau;
-                            if (__any_sync(0xffffffffu, cand)) top_offer(L, p.top, lane, cand, key, head + vec * E + e);
-                        }
-                    }
-                }
-                if (more && lane < 4 && lane < p.top && L.key > best[warp * 4 + lane])
-                    static_cast<volatile int*>(best)[warp * 4 + lane] = L.key;
+            const int key = at < v1 ? order_key(mx) : KEY_NONE;
+            key_group = key > key_group ? key : key_group;
+            key_all = key > key_all ? key : key_all;
+            if (++in_group == per_group || base + TURN >= v1) {
+                top.group_max[group++][tid] = key_group;
+                key_group = KEY_NONE;
+                in_group = 0;
             }
         }
     }
-    if (warp == 0 && rank == csize - 1) singles(tail0, p.vocab - tail0);
     // the block's result: lanes, then warps, in a fixed order
     st = join<32>(st);
     if (lane == 0) wst[warp] = st;
     if constexpr (TOP) {
-        // the tail of the row and the lists as they ended (an empty block never published)
-        if (lane < 4 && lane < p.top) best[warp * 4 + lane] = L.key;
-        else if (lane < 4) best[warp * 4 + lane] = KEY_NONE;
-    }
-    __syncthreads();
-    if (warp == 0) st = join<FWD_WARPS>(wst[lane % FWD_WARPS]);
-    if constexpr (TOP) {
-        // the entries that may still count, a few more than `top`: lane l of warp w holds the
-        // l-th of list w
-        const int r = kth_largest(best[lane], p.top);
-        const bool entry = lane < p.top && L.key != KEY_NONE && L.key >= r;
-        if (entry) {
-            wkey[warp][lane] = L.key;
-            widx[warp][lane] = L.idx;
-        }
-        const int n = __popc(__ballot_sync(0xffffffffu, entry));
-        if (lane == 0) wcnt[warp] = n;
+        top.thread_max[tid] = key_all;
+        if (tid == 0) top.count = 0;
         if (tid < LOGPROB_MAX_TOP) {
             res.key[tid] = KEY_NONE;
             res.idx[tid] = 0;
         }
+    }
+    __syncthreads();
+    if (warp == 0) st = join<FWD_WARPS>(wst[lane % FWD_WARPS]);
+    if constexpr (TOP) {
+        const int reach = kth_largest(top.thread_max, p.top, lane);
+        auto list = [&](float v, int i) {
+            const int key = order_key(v);
+            if (key != KEY_NONE && key >= reach) {
+                const int at = atomicAdd(&top.count, 1);
+                if (at < TOP_LIST) {
+                    top.key[at] = key;
+                    top.idx[at] = i;
+                }
+            }
+        };
+        if (warp == 0 && lane < nh + nt) {
+            const int i = lane < nh ? lane : tail0 + lane - nh;
+            list(Elem<T>::load(x[i]), i);
+        }
+        if (key_all >= reach && mine < v1) {
+            for (int g = 0; g < group; ++g) {
+                if (top.group_max[g][tid] < reach) continue;
+                for (int t = 0; t < per_group; ++t) {
+                    const int at = mine + (g * per_group + t) * TURN;
+                    uint4 raw[UNROLL];
+#pragma unroll
+                    for (int u = 0; u < UNROLL; ++u)
+                        if (at + u * 32 < v1) raw[u] = xv[at + u * 32];
+#pragma unroll
+                    for (int u = 0; u < UNROLL; ++u) {
+                        // (a list that is full already is not what the place is found by)
+                        if (at + u * 32 >= v1 || *static_cast<volatile int*>(&top.count) > TOP_LIST) break;
+                        const uint32_t m = Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w));
+                        if (order_key(Elem<T>::word_max(m)) < reach) continue;
+                        float v[E];
+                        Elem<T>::unpack(raw[u], v);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) list(v[e], head + (at + u * 32) * E + e);
+                    }
+                }
+            }
+        }
         __syncthreads();
-        if (entry) {
-            const int place = place_of(L.key, L.idx, wkey, widx, wcnt, FWD_WARPS);
+        int n = top.count;
+        if (n > TOP_LIST) {
+            // too many to list: every warp walks its elements again, its best in order, and the
+            // lists become the entries
+            TopList L;
+            top_init(L);
+            for (int base = v0; base < v1; base += TURN) {
+                const int at = mine + (base - v0);
+                // indexes grow from turn to turn and from one row of vectors to the next: an equal
+                // value never displaces, and what holds no larger one is passed over
+                uint32_t mw = Elem<T>::NEG_INF;
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u) {
+                    if (at + u * 32 < v1) {
+                        const uint4 r = xv[at + u * 32];
+                        mw = Elem<T>::max_word(mw, Elem<T>::max_word(Elem<T>::max_word(r.x, r.y), Elem<T>::max_word(r.z, r.w)));
+                    }
+                }
+                if (!__any_sync(0xffffffffu, at < v1 && order_key(Elem<T>::word_max(mw)) > L.kth_key)) continue;
+#pragma unroll 1
+                for (int u = 0; u < UNROLL; ++u) {
+                    const int vec = at + u * 32;
+                    float v[E];
+                    int most = KEY_NONE;
+                    if (vec < v1) {
+                        Elem<T>::unpack(xv[vec], v);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) most = max(most, order_key(v[e]));
+                    }
+                    if (!__any_sync(0xffffffffu, most > L.kth_key)) continue;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        top_offer(L, p.top, lane, vec < v1, vec < v1 ? order_key(v[e]) : KEY_NONE, head + vec * E + e);
+                }
+            }
+            if (warp == 0) {
+                const bool in = lane < nh + nt;
+                const int i = lane < nh ? lane : tail0 + lane - nh;
+                top_offer(L, p.top, lane, in, in ? order_key(Elem<T>::load(x[i])) : KEY_NONE, i);
+            }
+            __syncthreads();
+            if (tid == 0) top.count = 0;
+            __syncthreads();
+            if (lane < p.top && L.key != KEY_NONE) {
+                const int at = atomicAdd(&top.count, 1);
+                top.key[at] = L.key;
+                top.idx[at] = L.idx;
+            }
+            __syncthreads();
+            n = top.count;
+        }
+        for (int j = tid; j < n; j += FWD_THREADS) {
+            const int place = place_of(top.key[j], top.idx[j], top, n);
             if (place < p.top) {
-                res.key[place] = L.key;
-                res.idx[place] = L.idx;
+                res.key[place] = top.key[j];
+                res.idx[place] = top.idx[j];
             }
         }
         __syncthreads();
@@ -365,7 +426,7 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
                 st = join<8>(b);
             }
             if constexpr (TOP) {
-                // warp w takes the list of the cluster's block w
+                // the blocks' results are the entries: warp w takes those of block w
                 int k = KEY_NONE, i = INT32_MAX;
                 if (warp < csize && lane < p.top) {
                     const uint32_t a = map_to_rank(&res, warp);
@@ -373,17 +434,13 @@ __global__ void __launch_bounds__(FWD_THREADS) logprob_fwd_kernel(const LogprobP
                     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(k) : "r"(ak) : "memory");
                     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(i) : "r"(ai) : "memory");
                 }
-                const bool entry = k != KEY_NONE;
-                const int n = __popc(__ballot_sync(0xffffffffu, entry));
-                __syncthreads();  // every read of this block's own lists is over
-                if (lane < LOGPROB_MAX_TOP) {
-                    wkey[warp][lane] = k;
-                    widx[warp][lane] = i;
+                if (warp < csize && lane < p.top) {
+                    top.key[warp * p.top + lane] = k;
+                    top.idx[warp * p.top + lane] = k == KEY_NONE ? INT32_MAX : i;
                 }
-                if (lane == 0) wcnt[warp] = n;
                 __syncthreads();
-                if (entry) {
-                    const int place = place_of(k, i, wkey, widx, wcnt, csize);
+                if (k != KEY_NONE) {
+                    const int place = place_of(k, i, top, csize * p.top);
                     if (place < p.top) {
                         res.key[place] = k;
                         res.idx[place] = i;

@@ -19,6 +19,11 @@
 // in registers, the teams of a block join theirs through shared memory, and each block
 // leaves one row of partial sums; norm_grads_kernel adds those up.  The order of every sum
 // is fixed by the sizes: no atomics, the same bits every time.
+//
+// Many rows on 16-byte boundaries (the ring kernels): the rows come by bulk copies into a
+// ring of shared-memory stages per team, several rows ahead.  With one row ahead in
+// registers a block waited out the memory's latency on every row (32768 x 2816 bf16: 150-168
+// us backward, 75 forward).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -420,6 +425,369 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
         }
 }
 
+// ---------------------------------------------------------------- the ring kernels
+// A team of TPR threads (32 to 512) takes a run of consecutive rows; up to RING_MAX stages
+// of `arrays` rows each (x, or x, dy and the residual's gradient) are on their way.  The
+// team's first thread issues the copies of a stage once the team has read what was in it.
+constexpr int RING_MAX = 8;
+constexpr int RING_BLOCK = 256;                  // threads per block, about (512 where a team is that wide)
+constexpr int RING_BYTES = 100 * 1024;           // shared memory of such a block: two per SM
+constexpr int ring_teams(int tpr) { return tpr > RING_BLOCK ? 1 : RING_BLOCK / tpr; }
+constexpr int ring_threads(int tpr) { return ring_teams(tpr) * tpr; }
+constexpr int ring_bytes(int tpr) { return tpr > RING_BLOCK ? 2 * RING_BYTES : RING_BYTES; }
+// Stages per team of a ring of `arrays` rows of `row_bytes` each.
+__host__ __device__ constexpr int ring_stages(int tpr, int arrays, int row_bytes) {
+    const int s = (ring_bytes(tpr) - 1024) / ring_teams(tpr) / (arrays * row_bytes);
+    return s > RING_MAX ? RING_MAX : s;
+}
+
+template <int TPR>
+struct Team {
+    int id, t;  // of the block's teams; thread of the team
+    float4* red;  // [2][TPR / 64] pairs of two warps' sums
+    int flip;
+    __device__ __forceinline__ void sync() const {
+        if constexpr (TPR == 32) __syncwarp();
+        else named_barrier_sync(1 + id, TPR);
+    }
+    // Sums of a and b over the team, the same in every thread; a barrier of the team.
+    __device__ __forceinline__ void sum(float& a, float& b) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        if constexpr (TPR > 32) {
+            // two arrays in turn: one is written again only after the next sum's barrier
+            float4* r = red + flip * (TPR / 64);
+            flip ^= 1;
+            if ((t & 31) == 0) reinterpret_cast<float2*>(r)[t >> 5] = make_float2(a, b);
+            sync();
+            a = b = 0.f;
+#pragma unroll
+            for (int w = 0; w < TPR / 64; ++w) {
+                const float4 f = r[w];
+                a += f.x;
+                b += f.y;
+                a += f.z;
+                b += f.w;
+            }
+        } else {
+            __syncwarp();
+        }
+    }
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// One row's statistics per lane, 32 rows at a time, the next 32 on their way.
+struct RowStats {
+    float mean, rstd, mean_n, rstd_n;
+    __device__ __forceinline__ void start(const NormBwdParams& p, long long row, long long end, int lane) {
+        mean = row + lane < end ? p.mean[row + lane] : 0.f;
+        rstd = row + lane < end ? p.rstd[row + lane] : 0.f;
+        next(p, row + 32, end, lane);
+    }
+    __device__ __forceinline__ void next(const NormBwdParams& p, long long row, long long end, int lane) {
+        mean_n = row + lane < end ? p.mean[row + lane] : 0.f;
+        rstd_n = row + lane < end ? p.rstd[row + lane] : 0.f;
+    }
+};
+
+template <typename T, typename W, int TPR, int NV>
+__global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) norm_bwd_ring_kernel(const NormBwdParams p) {
+    using Raw = RawUnit<T, true>;
+    constexpr int E = Elem<T>::VEC, P = E / 2, TEAMS = ring_teams(TPR);
+    using F = uint64_t;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t full[TEAMS][RING_MAX];
+    __shared__ float4 red[TEAMS][2][TPR > 32 ? TPR / 64 : 1];
+    const int lane = threadIdx.x & 31;
+    Team<TPR> team;
+    team.id = threadIdx.x / TPR;
+    team.t = threadIdx.x % TPR;
+    team.red = &red[team.id][0][0];
+    team.flip = 0;
+    const int row_bytes = p.width * static_cast<int>(sizeof(T));
+    const int arrays = p.res ? 3 : 2;
+    const int stages = ring_stages(TPR, arrays, row_bytes);
+    const uint32_t stage_bytes = static_cast<uint32_t>(arrays * row_bytes);
+    uint8_t* mine = ring + static_cast<size_t>(team.id) * stages * stage_bytes;
+    const long long g = static_cast<long long>(blockIdx.x) * TEAMS + team.id;
+    const long long r0 = g * p.team_rows < p.rows ? g * p.team_rows : p.rows;
+    const long long r1 = r0 + p.team_rows < p.rows ? r0 + p.team_rows : p.rows;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < TEAMS; ++k)
+            for (int s = 0; s < RING_MAX; ++s) mbar_init(&full[k][s], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    auto issue = [&](long long row, int s) {
+        uint64_t* bar = &full[team.id][s];
+        const uint32_t dst = smem_u32(mine + s * stage_bytes);
+        mbar_arrive_expect_tx(bar, stage_bytes);
+        bulk_load(dst, static_cast<const T*>(p.x) + row * p.ldx, row_bytes, bar);
+        bulk_load(dst + row_bytes, static_cast<const T*>(p.dy) + row * p.lddy, row_bytes, bar);
+        if (p.res) bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.res) + row * p.ldr, row_bytes, bar);
+    };
+    if (team.t == 0)
+        for (int s = 0; s < stages && r0 + s < r1; ++s) issue(r0 + s, s);
+    RowStats st;
+    st.start(p, r0, r1, lane);
+    const float inv_n = 1.f / static_cast<float>(p.width);
+    bool in[NV];
+    F aw[NV][P], ab[NV][P], wv[NV][P];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int c = (team.t + u * TPR) * E;
+        in[u] = c < p.width;
+        weight_unit<W, E>(static_cast<const W*>(p.weight), c, p.width, 1.f, wv[u]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) aw[u][i] = ab[u][i] = 0;
+    }
+    T* dp = static_cast<T*>(p.dx) + r0 * p.lddx + team.t * E;
+    bool dead = false;  // a wait gave up: the rest runs to its end without waiting
+    int s = 0;
+    uint32_t phase = 0;
+    for (long long row = r0; row < r1; ++row, dp += p.lddx) {
+        const int k = static_cast<int>(row - r0) & 31;
+        if (k == 0 && row != r0) {
+            st.mean = st.mean_n;
+            st.rstd = st.rstd_n;
+            st.next(p, row + 32, r1, lane);
+        }
+        const float mean = __shfl_sync(0xffffffffu, st.mean, k), rstd = __shfl_sync(0xffffffffu, st.rstd, k);
+        if (!dead) dead = !mbar_wait(&full[team.id][s], phase, p.err);
+        const uint32_t src = smem_u32(mine + s * stage_bytes) + team.t * 16;
+        Raw xr[NV], gr[NV], rr[NV];
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (!in[u]) break;
+            xr[u].r = lds128(src + u * TPR * 16);
+            gr[u].r = lds128(src + row_bytes + u * TPR * 16);
+            if (p.res) rr[u].r = lds128(src + 2 * row_bytes + u * TPR * 16);
+        }
+        const F nm = p_all<F>(-mean), rs = p_all<F>(rstd);
+        F a1 = 0, a2 = 0;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (!in[u]) break;
+            F h[P], d[P];
+            xr[u].get(h);
+            gr[u].get(d);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                h[i] = p_mul(p_add(h[i], nm), rs);
+                aw[u][i] = p_fma(d[i], h[i], aw[u][i]);
+                ab[u][i] = p_add(ab[u][i], d[i]);
+                d[i] = p_mul(d[i], wv[u][i]);
+                a1 = p_add(a1, d[i]);
+                a2 = p_fma(d[i], h[i], a2);
+            }
+        }
+        float s1 = p_sum(a1), s2 = p_sum(a2);
+        team.sum(s1, s2);
+        // every thread of the team has read the stage
+        if (team.t == 0 && row + stages < r1) issue(row + stages, s);
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+        if (!p.dx) continue;
+        // rstd (g - s1 - h s2) = rstd g - (rstd s1) - h (rstd s2)
+        const F k1 = p_all<F>(-rstd * (s1 * inv_n)), k2 = p_all<F>(-rstd * (s2 * inv_n));
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (!in[u]) break;
+            F h[P], d[P];
+            xr[u].get(h);
+            gr[u].get(d);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                h[i] = p_fma(p_mul(p_add(h[i], nm), rs), k2, k1);
+                d[i] = p_fma(p_mul(d[i], wv[u][i]), rs, h[i]);
+            }
+            if (p.res) {
+                rr[u].get(h);
+#pragma unroll
+                for (int i = 0; i < P; ++i) d[i] = p_add(d[i], h[i]);
+            }
+            Raw::put(dp + u * TPR * E, d);
+        }
+    }
+    if (!p.dweight && !p.dbias) return;
+    // the block's column sums, team by team in order, in the ring (every copy has been read)
+    float* cols = reinterpret_cast<float*>(ring);
+    for (int k = 0; k < TEAMS; ++k) {
+        __syncthreads();
+        if (team.id != k) continue;
+        const bool last = k == TEAMS - 1;
+        float* pw = p.blocks > 1 ? p.part + static_cast<size_t>(blockIdx.x) * 2 * p.width : p.dweight;
+        float* pb = p.blocks > 1 ? p.part + static_cast<size_t>(blockIdx.x) * 2 * p.width + p.width : p.dbias;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (!in[u]) break;
+            const int c = (team.t + u * TPR) * E;
+            float w[E], b[E];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                f2_split(aw[u][i], &w[2 * i], &w[2 * i + 1]);
+                f2_split(ab[u][i], &b[2 * i], &b[2 * i + 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (k > 0) {
+                    w[e] += cols[c + e];
+                    b[e] += cols[p.width + c + e];
+                }
+                if (!last) {
+                    cols[c + e] = w[e];
+                    cols[p.width + c + e] = b[e];
+                } else {
+                    if (p.dweight) pw[c + e] = w[e];
+                    if (p.dbias) pb[c + e] = b[e];
+                }
+            }
+        }
+    }
+}
+
+template <typename T, typename W, int TPR, int NV>
+__global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) norm_fwd_ring_kernel(const NormFwdParams p) {
+    using Raw = RawUnit<T, true>;
+    constexpr int E = Elem<T>::VEC, P = E / 2, TEAMS = ring_teams(TPR);
+    using F = uint64_t;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t full[TEAMS][RING_MAX];
+    __shared__ float4 red[TEAMS][2][TPR > 32 ? TPR / 64 : 1];
+    Team<TPR> team;
+    team.id = threadIdx.x / TPR;
+    team.t = threadIdx.x % TPR;
+    team.red = &red[team.id][0][0];
+    team.flip = 0;
+    const uint32_t row_bytes = static_cast<uint32_t>(p.width * sizeof(T));
+    const int stages = ring_stages(TPR, 1, row_bytes);
+    uint8_t* mine = ring + static_cast<size_t>(team.id) * stages * row_bytes;
+    const long long g = static_cast<long long>(blockIdx.x) * TEAMS + team.id;
+    const long long r0 = g * p.team_rows < p.rows ? g * p.team_rows : p.rows;
+    const long long r1 = r0 + p.team_rows < p.rows ? r0 + p.team_rows : p.rows;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < TEAMS; ++k)
+            for (int s = 0; s < RING_MAX; ++s) mbar_init(&full[k][s], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    auto issue = [&](long long row, int s) {
+        uint64_t* bar = &full[team.id][s];
+        mbar_arrive_expect_tx(bar, row_bytes);
+        bulk_load(smem_u32(mine + s * row_bytes), static_cast<const T*>(p.x) + row * p.ldx, row_bytes, bar);
+    };
+    if (team.t == 0)
+        for (int s = 0; s < stages && r0 + s < r1; ++s) issue(r0 + s, s);
+    const float inv_n = 1.f / static_cast<float>(p.width);
+    bool in[NV];
+    F w[NV][P], b[NV][P];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int c = (team.t + u * TPR) * E;
+        in[u] = c < p.width;
+        weight_unit<W, E>(static_cast<const W*>(p.weight), c, p.width, 1.f, w[u]);
+        weight_unit<W, E>(static_cast<const W*>(p.bias), c, p.width, 0.f, b[u]);
+    }
+    T* yp = static_cast<T*>(p.y) + r0 * p.ldy + team.t * E;
+    bool dead = false;  // a wait gave up: the rest runs to its end without waiting
+    int s = 0;
+    uint32_t phase = 0;
+    // two rows at a time: their sums share the team's barriers
+    for (long long row = r0; row < r1; row += 2, yp += 2 * p.ldy) {
+        const bool two = row + 1 < r1;
+        Raw xr[2][NV];
+        int freed[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            freed[k] = s;
+            if (k == 0 || two) {
+                if (!dead) dead = !mbar_wait(&full[team.id][s], phase, p.err);
+                const uint32_t src = smem_u32(mine + s * row_bytes) + team.t * 16;
+#pragma unroll
+                for (int u = 0; u < NV; ++u) {
+                    if (!in[u]) break;
+                    xr[k][u].r = lds128(src + u * TPR * 16);
+                }
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < NV; ++u) xr[k][u].zero();
+            }
+        }
+        float sum[2], sq[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            F acc = 0;
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                if (!in[u]) break;
+                F v[P];
+                xr[k][u].get(v);
+#pragma unroll
+                for (int i = 0; i < P; ++i) acc = p_add(acc, v[i]);
+            }
+            sum[k] = p_sum(acc);
+        }
+        team.sum(sum[0], sum[1]);
+        // every thread of the team has read the stages
+        if (team.t == 0) {
+            if (row + stages < r1) issue(row + stages, freed[0]);
+            if (row + 1 + stages < r1) issue(row + 1 + stages, freed[1]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            sum[k] *= inv_n;
+            const F nm = p_all<F>(-sum[k]);
+            F acc = 0;
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                if (!in[u]) break;
+                F v[P];
+                xr[k][u].get(v);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const F d = p_add(v[i], nm);
+                    acc = p_fma(d, d, acc);
+                }
+            }
+            sq[k] = p_sum(acc);
+        }
+        team.sum(sq[0], sq[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k == 1 && !two) break;
+            const float rstd = inv_sqrt(fmaf(sq[k], inv_n, p.eps));
+            if (team.t == 0) {
+                if (p.mean) p.mean[row + k] = sum[k];
+                if (p.rstd) p.rstd[row + k] = rstd;
+            }
+            const F nm = p_all<F>(-sum[k]), rs = p_all<F>(rstd);
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                if (!in[u]) break;
+                F v[P];
+                xr[k][u].get(v);
+#pragma unroll
+                for (int i = 0; i < P; ++i) v[i] = p_fma(p_mul(p_add(v[i], nm), rs), w[u][i], b[u][i]);
+                Raw::put(yp + k * p.ldy + u * TPR * E, v);
+            }
+        }
+    }
+}
+
 // dweight (blockIdx.y = 0) and dbias (1): 32 columns per block, 16 threads down each, the
 // partial rows taken in order by each and the 16 sums added in order.
 constexpr int GRAD_LANES = 16;
@@ -520,45 +888,131 @@ cudaError_t pick_bwd(const NormBwdParams& p, bool vec, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+
+// Threads of a team of the ring kernels: up to 16 columns each.
+int ring_tpr(int width) {
+    return width <= 512 ? 32 : width <= 1024 ? 64 : width <= 2048 ? 128 : width <= 3072 ? 192 : width <= 4096 ? 256 : 512;
+}
+
+// Teams of the ring kernels on the whole device, and whether they run: rows wider than the
+// narrow teams take, at least four rows for each team (below that there is nothing to run
+// ahead of, and the plain kernels start faster), and two stages that fit.
+bool ring_plan(long long rows, int width, int dtype, int arrays, int* blocks, int* team_rows) {
+    const int es = dtype_size(dtype), tpr = ring_tpr(width);
+    if (width * es < 1024 || width > 8192 || ring_stages(tpr, arrays, width * es) < 2) return false;
+    const int per_block = ring_teams(tpr);
+    const long long teams = 152ll * (tpr > RING_BLOCK ? 1 : 2) * per_block;
+    if (rows < 4 * teams) return false;
+    const long long each = (rows + teams - 1) / teams;
+    *team_rows = static_cast<int>(each);
+    *blocks = static_cast<int>((rows + each * per_block - 1) / (each * per_block));
+    return true;
+}
+
+template <typename K, typename P>
+cudaError_t run_ring(K kernel, const P& p, int tpr, int arrays, int blocks, cudaStream_t s) {
+    const int es = dtype_size(p.dtype);
+    size_t smem = static_cast<size_t>(ring_teams(tpr)) * ring_stages(tpr, arrays, p.width * es) * arrays * p.width * es;
+    const size_t sums = arrays > 1 ? 2 * sizeof(float) * p.width : 0;  // the column sums reuse the ring
+    if (smem < sums) smem = sums;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(tpr));
+    if (e) return e;
+    kernel<<<blocks, ring_threads(tpr), smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, typename W>
+cudaError_t pick_fwd_ring(const NormFwdParams& p, int blocks, cudaStream_t s) {
+    constexpr int NV = 16 / Elem<T>::VEC;
+    const int tpr = ring_tpr(p.width);
+    switch (tpr) {
+        case 32: return run_ring(norm_fwd_ring_kernel<T, W, 32, NV>, p, tpr, 1, blocks, s);
+        case 64: return run_ring(norm_fwd_ring_kernel<T, W, 64, NV>, p, tpr, 1, blocks, s);
+        case 128: return run_ring(norm_fwd_ring_kernel<T, W, 128, NV>, p, tpr, 1, blocks, s);
+        case 192: return run_ring(norm_fwd_ring_kernel<T, W, 192, NV>, p, tpr, 1, blocks, s);
+        case 256: return run_ring(norm_fwd_ring_kernel<T, W, 256, NV>, p, tpr, 1, blocks, s);
+        default: return run_ring(norm_fwd_ring_kernel<T, W, 512, NV>, p, tpr, 1, blocks, s);
+    }
+}
+template <typename T, typename W>
+cudaError_t pick_bwd_ring(const NormBwdParams& p, cudaStream_t s) {
+    constexpr int NV = 16 / Elem<T>::VEC;
+    const int tpr = ring_tpr(p.width), arrays = p.res ? 3 : 2;
+    switch (tpr) {
+        case 32: return run_ring(norm_bwd_ring_kernel<T, W, 32, NV>, p, tpr, arrays, p.blocks, s);
+        case 64: return run_ring(norm_bwd_ring_kernel<T, W, 64, NV>, p, tpr, arrays, p.blocks, s);
+        case 128: return run_ring(norm_bwd_ring_kernel<T, W, 128, NV>, p, tpr, arrays, p.blocks, s);
+        case 192: return run_ring(norm_bwd_ring_kernel<T, W, 192, NV>, p, tpr, arrays, p.blocks, s);
+        case 256: return run_ring(norm_bwd_ring_kernel<T, W, 256, NV>, p, tpr, arrays, p.blocks, s);
+        default: return run_ring(norm_bwd_ring_kernel<T, W, 512, NV>, p, tpr, arrays, p.blocks, s);
+    }
+}
+
+template <typename T, typename W>
+cudaError_t start_fwd(NormFwdParams p, bool vec, cudaStream_t s) {
+    int blocks = 0;
+    if (vec && ring_plan(p.rows, p.width, p.dtype, 1, &blocks, &p.team_rows)) return pick_fwd_ring<T, W>(p, blocks, s);
+    return pick_fwd<T, W>(p, vec, s);
+}
+template <typename T, typename W>
+cudaError_t start_bwd(const NormBwdParams& p, cudaStream_t s) {
+    return p.team_rows ? pick_bwd_ring<T, W>(p, s) : pick_bwd<T, W>(p, p.vec != 0, s);
+}
+
+}  // namespace
+
 cudaError_t launch_norm_fwd(const NormFwdParams& p, cudaStream_t s) {
     const int es = dtype_size(p.dtype), ws = dtype_size(p.weight_dtype);
     const int unit = 16 / es;
     const bool vec = p.width % unit == 0 && aligned16(p.x, p.ldx, es, p.rows) && aligned16(p.y, p.ldy, es, p.rows) &&
                      aligned16(p.weight, 0, ws, 1) && aligned16(p.bias, 0, ws, 1);
     switch (p.dtype) {
-        case DT_F32: return pick_fwd<float, float>(p, vec, s);
+        case DT_F32: return start_fwd<float, float>(p, vec, s);
         case DT_BF16:
-            return p.weight_dtype == DT_F32 ? pick_fwd<__nv_bfloat16, float>(p, vec, s)
-                                            : pick_fwd<__nv_bfloat16, __nv_bfloat16>(p, vec, s);
+            return p.weight_dtype == DT_F32 ? start_fwd<__nv_bfloat16, float>(p, vec, s)
+                                            : start_fwd<__nv_bfloat16, __nv_bfloat16>(p, vec, s);
         default:
-            return p.weight_dtype == DT_F32 ? pick_fwd<__half, float>(p, vec, s) : pick_fwd<__half, __half>(p, vec, s);
+            return p.weight_dtype == DT_F32 ? start_fwd<__half, float>(p, vec, s) : start_fwd<__half, __half>(p, vec, s);
     }
 }
 
-int norm_bwd_blocks(long long rows, int width, int dtype, int sm_count) {
+static int plain_bwd_blocks(long long rows, int width, int dtype) {
     // narrow rows: teams of 8 or 32 threads, 32 or 8 rows per block and turn; else one row
     // and a team of 128 threads or more, 16 columns of a row per thread
     const int unit = 16 / dtype_size(dtype);
     const int per_block = width <= 64 ? 32 : width <= 32 * unit ? 8 : 1;
     const int tpr = width <= 32 * unit ? 32 : width <= 2048 ? 128 : width <= 4096 ? 256 : 512;
     const long long want = (rows + per_block - 1) / per_block;
-    const long long cap = static_cast<long long>(sm_count) * bwd_blocks_per_sm(tpr);
+    const long long cap = 152ll * bwd_blocks_per_sm(tpr);
     return static_cast<int>(want < 1 ? 1 : want < cap ? want : cap);
 }
 
-cudaError_t launch_norm_bwd(const NormBwdParams& p, cudaStream_t s) {
-    const int es = dtype_size(p.dtype), ws = dtype_size(p.weight_dtype);
+int norm_bwd_max_blocks(long long rows, int width, int dtype) {
+    int most = plain_bwd_blocks(rows, width, dtype), blocks = 0, each = 0;
+    for (int arrays = 2; arrays <= 3; ++arrays)
+        if (ring_plan(rows, width, dtype, arrays, &blocks, &each) && blocks > most) most = blocks;
+    return most;
+}
+
+void norm_bwd_plan(NormBwdParams* p) {
+    const int es = dtype_size(p->dtype), ws = dtype_size(p->weight_dtype);
     const int unit = 16 / es;
-    const bool vec = p.width % unit == 0 && aligned16(p.x, p.ldx, es, p.rows) && aligned16(p.dy, p.lddy, es, p.rows) &&
-                     (!p.dx || aligned16(p.dx, p.lddx, es, p.rows)) && (!p.res || aligned16(p.res, p.ldr, es, p.rows)) &&
-                     aligned16(p.weight, 0, ws, 1);
+    p->vec = p->width % unit == 0 && aligned16(p->x, p->ldx, es, p->rows) && aligned16(p->dy, p->lddy, es, p->rows) &&
+             (!p->dx || aligned16(p->dx, p->lddx, es, p->rows)) && (!p->res || aligned16(p->res, p->ldr, es, p->rows)) &&
+             aligned16(p->weight, 0, ws, 1);
+    p->team_rows = 0;
+    if (!p->vec || !ring_plan(p->rows, p->width, p->dtype, p->res ? 3 : 2, &p->blocks, &p->team_rows))
+        p->blocks = plain_bwd_blocks(p->rows, p->width, p->dtype);
+}
+
+cudaError_t launch_norm_bwd(const NormBwdParams& p, cudaStream_t s) {
     switch (p.dtype) {
-        case DT_F32: return pick_bwd<float, float>(p, vec, s);
+        case DT_F32: return start_bwd<float, float>(p, s);
         case DT_BF16:
-            return p.weight_dtype == DT_F32 ? pick_bwd<__nv_bfloat16, float>(p, vec, s)
-                                            : pick_bwd<__nv_bfloat16, __nv_bfloat16>(p, vec, s);
-        default:
-            return p.weight_dtype == DT_F32 ? pick_bwd<__half, float>(p, vec, s) : pick_bwd<__half, __half>(p, vec, s);
+            return p.weight_dtype == DT_F32 ? start_bwd<__nv_bfloat16, float>(p, s)
+                                            : start_bwd<__nv_bfloat16, __nv_bfloat16>(p, s);
+        default: return p.weight_dtype == DT_F32 ? start_bwd<__half, float>(p, s) : start_bwd<__half, __half>(p, s);
     }
 }
 

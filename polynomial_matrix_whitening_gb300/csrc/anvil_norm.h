@@ -16,7 +16,9 @@ struct NormFwdParams {
     long long rows, ldx, ldy;
     int width;
     int dtype, weight_dtype;
+    int team_rows;        // rows of a team of the ring kernel (set by the launcher)
     float eps;
+    unsigned* err;
 };
 
 struct NormBwdParams {
@@ -33,12 +35,17 @@ struct NormBwdParams {
     long long rows, lddy, ldx, ldr, lddx;
     int width;
     int dtype, weight_dtype;
+    // set by norm_bwd_plan:
     int blocks;            // of the row pass; 1: it writes dweight and dbias itself
+    int vec;               // every array on 16-byte boundaries row by row
+    int team_rows;         // rows of a team of the ring kernel (0: the plain kernel)
+    unsigned* err;
 };
 
-// Blocks of the backward row pass (a function of the sizes and the SM count alone): also
-// the number of partial rows the workspace holds.
-int norm_bwd_blocks(long long rows, int width, int dtype, int sm_count);
+// The most blocks the backward row pass takes for these sizes (whatever the alignment): the
+// number of partial rows the workspace holds.
+int norm_bwd_max_blocks(long long rows, int width, int dtype);
+void norm_bwd_plan(NormBwdParams* p);
 cudaError_t launch_norm_fwd(const NormFwdParams& p, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormBwdParams& p, cudaStream_t stream);
 cudaError_t launch_norm_grads(const NormBwdParams& p, cudaStream_t stream);
