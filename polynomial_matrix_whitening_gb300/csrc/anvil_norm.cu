@@ -20,13 +20,15 @@
 // leaves one row of partial sums; norm_grads_kernel adds those up.  The order of every sum
 // is fixed by the sizes: no atomics, the same bits every time.
 //
-// Many rows on 16-byte boundaries (the ring kernels): the rows come by bulk copies into a
-// ring of shared-memory stages per team, several rows ahead.  With one row ahead in
-// registers a block waited out the memory's latency on every row (32768 x 2816 bf16: 150-168
-// us backward, 75 forward).
+// Many rows (the ring kernels): the rows come by bulk copies into a ring of shared-memory
+// stages per team, several rows ahead.  With one row ahead in registers a block waited out
+// the memory's latency on every row (32768 x 2816 bf16: 150-168 us backward, 78 forward;
+// with the ring 121-125 and 71, 5.2-6.1 TB/s; 32768 x 2815, off the 16-byte boundaries: 522
+// and 152, with the ring 199 and 131).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "anvil_device.cuh"
 #include "anvil_norm.h"
@@ -60,6 +62,7 @@ struct RawUnit {
     using F = uint64_t;
     uint4 r;
     __device__ __forceinline__ void load(const T* p) { r = ldg_stream(p); }
+    __device__ __forceinline__ void load_shared(uint32_t a) { r = lds128(a); }
     __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void get(F* f) const { Elem<T>::unpack_pairs(r, f); }
     static __device__ __forceinline__ void put(T* p, const F* f) { stg_stream(p, Elem<T>::pack_pairs(f)); }
@@ -70,6 +73,15 @@ struct RawUnit<T, false> {
     using F = float;
     T r;
     __device__ __forceinline__ void load(const T* p) { r = __ldcs(p); }
+    __device__ __forceinline__ void load_shared(uint32_t a) {
+        if constexpr (sizeof(T) == 2) {
+            uint16_t b;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(a) : "memory");
+            memcpy(&r, &b, 2);
+        } else {
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a) : "memory");
+        }
+    }
     __device__ __forceinline__ void zero() { r = Elem<T>::store(0.f); }
     __device__ __forceinline__ void get(F* f) const { f[0] = Elem<T>::load(r); }
     static __device__ __forceinline__ void put(T* p, const F* f) { __stcs(p, Elem<T>::store(f[0])); }
@@ -429,13 +441,20 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
 // A team of TPR threads (32 to 512) takes a run of consecutive rows; up to RING_MAX stages
 // of `arrays` rows each (x, or x, dy and the residual's gradient) are on their way.  The
 // team's first thread issues the copies of a stage once the team has read what was in it.
+//
+// Rows off the 16-byte boundaries (VEC false): a bulk copy takes the 16-byte pieces that
+// cover the row, so it brings up to 14 bytes of the rows (or padding) before and after,
+// which nothing reads; the array's first and last row, which have no such neighbour on one
+// side, are copied element by element.  A thread then has every TPR-th element.
 constexpr int RING_MAX = 8;
 constexpr int RING_BLOCK = 256;                  // threads per block, about (512 where a team is that wide)
 constexpr int RING_BYTES = 100 * 1024;           // shared memory of such a block: two per SM
 constexpr int ring_teams(int tpr) { return tpr > RING_BLOCK ? 1 : RING_BLOCK / tpr; }
 constexpr int ring_threads(int tpr) { return ring_teams(tpr) * tpr; }
 constexpr int ring_bytes(int tpr) { return tpr > RING_BLOCK ? 2 * RING_BYTES : RING_BYTES; }
-// Stages per team of a ring of `arrays` rows of `row_bytes` each.
+// Bytes of a row's place in a stage.
+__host__ __device__ constexpr int ring_slot(bool vec, int row_bytes) { return vec ? row_bytes : (row_bytes + 31) / 16 * 16; }
+// Stages per team of a ring of `arrays` rows of `row_bytes` (their slots) each.
 __host__ __device__ constexpr int ring_stages(int tpr, int arrays, int row_bytes) {
     const int s = (ring_bytes(tpr) - 1024) / ring_teams(tpr) / (arrays * row_bytes);
     return s > RING_MAX ? RING_MAX : s;
@@ -484,6 +503,32 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// One row (of `rows`) into its slot at `dst` (16-byte aligned): the bytes of bulk copies to
+// expect, and the copies.  A row of whole 16-byte pieces starts at the slot's start, others
+// at their own offset to a 16-byte boundary.
+__device__ __forceinline__ uint32_t slot_offset(const void* row) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15);
+}
+__device__ __forceinline__ uint32_t cover_bytes(const void* row, uint32_t bytes) { return (slot_offset(row) + bytes + 15u) & ~15u; }
+__device__ __forceinline__ void cover_load(uint32_t dst, const void* row, uint32_t bytes, uint64_t* bar) {
+    bulk_load(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(row) & ~static_cast<uintptr_t>(15)),
+              cover_bytes(row, bytes), bar);
+}
+// The same by the team's threads (the array's first and last row).
+template <typename T, int TPR>
+__device__ __forceinline__ void copy_row(uint32_t dst, const T* row, int width, int t) {
+    dst += slot_offset(row);
+    for (int i = t; i < width; i += TPR) {
+        if constexpr (sizeof(T) == 2) {
+            uint16_t b;
+            memcpy(&b, row + i, 2);
+            sts16(dst + 2 * i, b);
+        } else {
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * i), "f"(row[i]) : "memory");
+        }
+    }
+}
+
 // One row's statistics per lane, 32 rows at a time, the next 32 on their way.
 struct RowStats {
     float mean, rstd, mean_n, rstd_n;
@@ -498,11 +543,11 @@ struct RowStats {
     }
 };
 
-template <typename T, typename W, int TPR, int NV>
+template <typename T, typename W, bool VEC, int TPR, int NV>
 __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) norm_bwd_ring_kernel(const NormBwdParams p) {
-    using Raw = RawUnit<T, true>;
-    constexpr int E = Elem<T>::VEC, P = E / 2, TEAMS = ring_teams(TPR);
-    using F = uint64_t;
+    using Raw = RawUnit<T, VEC>;
+    using F = typename Raw::F;
+    constexpr int E = VEC ? Elem<T>::VEC : 1, P = Raw::P, TEAMS = ring_teams(TPR);
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[TEAMS][RING_MAX];
     __shared__ float4 red[TEAMS][2][TPR > 32 ? TPR / 64 : 1];
@@ -514,8 +559,9 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
     team.flip = 0;
     const int row_bytes = p.width * static_cast<int>(sizeof(T));
     const int arrays = p.res ? 3 : 2;
-    const int stages = ring_stages(TPR, arrays, row_bytes);
-    const uint32_t stage_bytes = static_cast<uint32_t>(arrays * row_bytes);
+    const int slot = ring_slot(VEC, row_bytes);
+    const int stages = ring_stages(TPR, arrays, slot);
+    const uint32_t stage_bytes = static_cast<uint32_t>(arrays * slot);
     uint8_t* mine = ring + static_cast<size_t>(team.id) * stages * stage_bytes;
     const long long g = static_cast<long long>(blockIdx.x) * TEAMS + team.id;
     const long long r0 = g * p.team_rows < p.rows ? g * p.team_rows : p.rows;
@@ -529,10 +575,23 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
     auto issue = [&](long long row, int s) {
         uint64_t* bar = &full[team.id][s];
         const uint32_t dst = smem_u32(mine + s * stage_bytes);
-        mbar_arrive_expect_tx(bar, stage_bytes);
-        bulk_load(dst, static_cast<const T*>(p.x) + row * p.ldx, row_bytes, bar);
-        bulk_load(dst + row_bytes, static_cast<const T*>(p.dy) + row * p.lddy, row_bytes, bar);
-        if (p.res) bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.res) + row * p.ldr, row_bytes, bar);
+        const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+        const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+        const T* res = static_cast<const T*>(p.res) + row * p.ldr;
+        if constexpr (VEC) {
+            mbar_arrive_expect_tx(bar, stage_bytes);
+            bulk_load(dst, x, row_bytes, bar);
+            bulk_load(dst + slot, dy, row_bytes, bar);
+            if (p.res) bulk_load(dst + 2 * slot, res, row_bytes, bar);
+        } else if (row == 0 || row == p.rows - 1) {
+            mbar_arrive_cta(bar);  // the team copies this row when it comes to it
+        } else {
+            mbar_arrive_expect_tx(bar, cover_bytes(x, row_bytes) + cover_bytes(dy, row_bytes) +
+                                           (p.res ? cover_bytes(res, row_bytes) : 0u));
+            cover_load(dst, x, row_bytes, bar);
+            cover_load(dst + slot, dy, row_bytes, bar);
+            if (p.res) cover_load(dst + 2 * slot, res, row_bytes, bar);
+        }
     };
     if (team.t == 0)
         for (int s = 0; s < stages && r0 + s < r1; ++s) issue(r0 + s, s);
@@ -547,7 +606,7 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
         in[u] = c < p.width;
         weight_unit<W, E>(static_cast<const W*>(p.weight), c, p.width, 1.f, wv[u]);
 #pragma unroll
-        for (int i = 0; i < P; ++i) aw[u][i] = ab[u][i] = 0;
+        for (int i = 0; i < P; ++i) aw[u][i] = ab[u][i] = p_all<F>(0.f);
     }
     T* dp = static_cast<T*>(p.dx) + r0 * p.lddx + team.t * E;
     bool dead = false;  // a wait gave up: the rest runs to its end without waiting
@@ -562,17 +621,35 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
         }
         const float mean = __shfl_sync(0xffffffffu, st.mean, k), rstd = __shfl_sync(0xffffffffu, st.rstd, k);
         if (!dead) dead = !mbar_wait(&full[team.id][s], phase, p.err);
-        const uint32_t src = smem_u32(mine + s * stage_bytes) + team.t * 16;
+        const uint32_t src = smem_u32(mine + s * stage_bytes);
+        uint32_t ox = 0, og = 0, orr = 0;  // the rows' offsets in their slots
+        if constexpr (!VEC) {
+            const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+            const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+            const T* res = static_cast<const T*>(p.res) + row * p.ldr;
+            ox = slot_offset(x);
+            og = slot_offset(dy);
+            orr = slot_offset(res);
+            if (row == 0 || row == p.rows - 1) {
+                copy_row<T, TPR>(src, x, p.width, team.t);
+                copy_row<T, TPR>(src + slot, dy, p.width, team.t);
+                if (p.res) copy_row<T, TPR>(src + 2 * slot, res, p.width, team.t);
+                fence_proxy_async_smem();  // before the next bulk copies into the stage
+                team.sync();
+            }
+        }
+        constexpr uint32_t UNIT = E * sizeof(T);
         Raw xr[NV], gr[NV], rr[NV];
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             if (!in[u]) break;
-            xr[u].r = lds128(src + u * TPR * 16);
-            gr[u].r = lds128(src + row_bytes + u * TPR * 16);
-            if (p.res) rr[u].r = lds128(src + 2 * row_bytes + u * TPR * 16);
+            const uint32_t at = src + (team.t + u * TPR) * UNIT;
+            xr[u].load_shared(at + ox);
+            gr[u].load_shared(at + slot + og);
+            if (p.res) rr[u].load_shared(at + 2 * slot + orr);
         }
         const F nm = p_all<F>(-mean), rs = p_all<F>(rstd);
-        F a1 = 0, a2 = 0;
+        F a1 = p_all<F>(0.f), a2 = p_all<F>(0.f);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             if (!in[u]) break;
@@ -635,8 +712,8 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
             float w[E], b[E];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                f2_split(aw[u][i], &w[2 * i], &w[2 * i + 1]);
-                f2_split(ab[u][i], &b[2 * i], &b[2 * i + 1]);
+                p_split(aw[u][i], &w[(E / P) * i]);
+                p_split(ab[u][i], &b[(E / P) * i]);
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -656,11 +733,11 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
     }
 }
 
-template <typename T, typename W, int TPR, int NV>
+template <typename T, typename W, bool VEC, int TPR, int NV>
 __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) norm_fwd_ring_kernel(const NormFwdParams p) {
-    using Raw = RawUnit<T, true>;
-    constexpr int E = Elem<T>::VEC, P = E / 2, TEAMS = ring_teams(TPR);
-    using F = uint64_t;
+    using Raw = RawUnit<T, VEC>;
+    using F = typename Raw::F;
+    constexpr int E = VEC ? Elem<T>::VEC : 1, P = Raw::P, TEAMS = ring_teams(TPR);
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[TEAMS][RING_MAX];
     __shared__ float4 red[TEAMS][2][TPR > 32 ? TPR / 64 : 1];
@@ -670,8 +747,9 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
     team.red = &red[team.id][0][0];
     team.flip = 0;
     const uint32_t row_bytes = static_cast<uint32_t>(p.width * sizeof(T));
-    const int stages = ring_stages(TPR, 1, row_bytes);
-    uint8_t* mine = ring + static_cast<size_t>(team.id) * stages * row_bytes;
+    const uint32_t slot = ring_slot(VEC, row_bytes);
+    const int stages = ring_stages(TPR, 1, slot);
+    uint8_t* mine = ring + static_cast<size_t>(team.id) * stages * slot;
     const long long g = static_cast<long long>(blockIdx.x) * TEAMS + team.id;
     const long long r0 = g * p.team_rows < p.rows ? g * p.team_rows : p.rows;
     const long long r1 = r0 + p.team_rows < p.rows ? r0 + p.team_rows : p.rows;
@@ -683,8 +761,16 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
     __syncthreads();
     auto issue = [&](long long row, int s) {
         uint64_t* bar = &full[team.id][s];
-        mbar_arrive_expect_tx(bar, row_bytes);
-        bulk_load(smem_u32(mine + s * row_bytes), static_cast<const T*>(p.x) + row * p.ldx, row_bytes, bar);
+        const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+        if constexpr (VEC) {
+            mbar_arrive_expect_tx(bar, row_bytes);
+            bulk_load(smem_u32(mine + s * slot), x, row_bytes, bar);
+        } else if (row == 0 || row == p.rows - 1) {
+            mbar_arrive_cta(bar);  // the team copies this row when it comes to it
+        } else {
+            mbar_arrive_expect_tx(bar, cover_bytes(x, row_bytes));
+            cover_load(smem_u32(mine + s * slot), x, row_bytes, bar);
+        }
     };
     if (team.t == 0)
         for (int s = 0; s < stages && r0 + s < r1; ++s) issue(r0 + s, s);
@@ -712,11 +798,21 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
             freed[k] = s;
             if (k == 0 || two) {
                 if (!dead) dead = !mbar_wait(&full[team.id][s], phase, p.err);
-                const uint32_t src = smem_u32(mine + s * row_bytes) + team.t * 16;
+                uint32_t src = smem_u32(mine + s * slot);
+                if constexpr (!VEC) {
+                    const T* x = static_cast<const T*>(p.x) + (row + k) * p.ldx;
+                    if (row + k == 0 || row + k == p.rows - 1) {
+                        copy_row<T, TPR>(src, x, p.width, team.t);
+                        fence_proxy_async_smem();  // before the next bulk copy into the stage
+                        team.sync();
+                    }
+                    src += slot_offset(x);
+                }
+                constexpr uint32_t UNIT = E * sizeof(T);
 #pragma unroll
                 for (int u = 0; u < NV; ++u) {
                     if (!in[u]) break;
-                    xr[k][u].r = lds128(src + u * TPR * 16);
+                    xr[k][u].load_shared(src + (team.t + u * TPR) * UNIT);
                 }
                 if (++s == stages) {
                     s = 0;
@@ -730,7 +826,7 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
         float sum[2], sq[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            F acc = 0;
+            F acc = p_all<F>(0.f);
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 if (!in[u]) break;
@@ -751,7 +847,7 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
         for (int k = 0; k < 2; ++k) {
             sum[k] *= inv_n;
             const F nm = p_all<F>(-sum[k]);
-            F acc = 0;
+            F acc = p_all<F>(0.f);
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 if (!in[u]) break;
@@ -891,16 +987,19 @@ cudaError_t pick_bwd(const NormBwdParams& p, bool vec, cudaStream_t s) {
 namespace {
 
 // Threads of a team of the ring kernels: up to 16 columns each.
-int ring_tpr(int width) {
-    return width <= 512 ? 32 : width <= 1024 ? 64 : width <= 2048 ? 128 : width <= 3072 ? 192 : width <= 4096 ? 256 : 512;
+// (2049 to 3072 columns: 192 threads run 32768 x 2816 bf16 forward in 71 us, 256 in 78;
+// backward 256 are faster, 121 against 125.)
+int ring_tpr(int width, int arrays) {
+    return width <= 512 ? 32 : width <= 1024 ? 64 : width <= 2048 ? 128 : width <= 3072 && arrays == 1 ? 192 : width <= 4096 ? 256 : 512;
 }
 
-// Teams of the ring kernels on the whole device, and whether they run: rows wider than the
-// narrow teams take, at least four rows for each team (below that there is nothing to run
-// ahead of, and the plain kernels start faster), and two stages that fit.
-bool ring_plan(long long rows, int width, int dtype, int arrays, int* blocks, int* team_rows) {
-    const int es = dtype_size(dtype), tpr = ring_tpr(width);
-    if (width * es < 1024 || width > 8192 || ring_stages(tpr, arrays, width * es) < 2) return false;
+// Teams of the ring kernels on the whole device, and whether they run: rows of 1 KB (off the
+// 16-byte boundaries 256 bytes; the plain kernels' narrow teams are faster below), at least
+// four rows for each team (below that there is nothing to run ahead of, and the plain
+// kernels start faster), and two stages that fit.
+bool ring_plan(long long rows, int width, int dtype, bool vec, int arrays, int* blocks, int* team_rows) {
+    const int es = dtype_size(dtype), tpr = ring_tpr(width, arrays);
+    if (width * es < (vec ? 1024 : 256) || width > 8192 || ring_stages(tpr, arrays, ring_slot(vec, width * es)) < 2) return false;
     const int per_block = ring_teams(tpr);
     const long long teams = 152ll * (tpr > RING_BLOCK ? 1 : 2) * per_block;
     if (rows < 4 * teams) return false;
@@ -911,9 +1010,9 @@ bool ring_plan(long long rows, int width, int dtype, int arrays, int* blocks, in
 }
 
 template <typename K, typename P>
-cudaError_t run_ring(K kernel, const P& p, int tpr, int arrays, int blocks, cudaStream_t s) {
-    const int es = dtype_size(p.dtype);
-    size_t smem = static_cast<size_t>(ring_teams(tpr)) * ring_stages(tpr, arrays, p.width * es) * arrays * p.width * es;
+cudaError_t run_ring(K kernel, const P& p, bool vec, int tpr, int arrays, int blocks, cudaStream_t s) {
+    const int slot = ring_slot(vec, p.width * dtype_size(p.dtype));
+    size_t smem = static_cast<size_t>(ring_teams(tpr)) * ring_stages(tpr, arrays, slot) * arrays * slot;
     const size_t sums = arrays > 1 ? 2 * sizeof(float) * p.width : 0;  // the column sums reuse the ring
     if (smem < sums) smem = sums;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(tpr));
@@ -922,42 +1021,43 @@ cudaError_t run_ring(K kernel, const P& p, int tpr, int arrays, int blocks, cuda
     return cudaGetLastError();
 }
 
-template <typename T, typename W>
+template <typename T, typename W, bool VEC>
 cudaError_t pick_fwd_ring(const NormFwdParams& p, int blocks, cudaStream_t s) {
-    constexpr int NV = 16 / Elem<T>::VEC;
-    const int tpr = ring_tpr(p.width);
+    constexpr int NV = VEC ? 16 / Elem<T>::VEC : 16;
+    const int tpr = ring_tpr(p.width, 1);
     switch (tpr) {
-        case 32: return run_ring(norm_fwd_ring_kernel<T, W, 32, NV>, p, tpr, 1, blocks, s);
-        case 64: return run_ring(norm_fwd_ring_kernel<T, W, 64, NV>, p, tpr, 1, blocks, s);
-        case 128: return run_ring(norm_fwd_ring_kernel<T, W, 128, NV>, p, tpr, 1, blocks, s);
-        case 192: return run_ring(norm_fwd_ring_kernel<T, W, 192, NV>, p, tpr, 1, blocks, s);
-        case 256: return run_ring(norm_fwd_ring_kernel<T, W, 256, NV>, p, tpr, 1, blocks, s);
-        default: return run_ring(norm_fwd_ring_kernel<T, W, 512, NV>, p, tpr, 1, blocks, s);
+        case 32: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 32, NV>, p, VEC, tpr, 1, blocks, s);
+        case 64: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 64, NV>, p, VEC, tpr, 1, blocks, s);
+        case 128: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 128, NV>, p, VEC, tpr, 1, blocks, s);
+        case 192: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 192, NV>, p, VEC, tpr, 1, blocks, s);
+        case 256: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 256, NV>, p, VEC, tpr, 1, blocks, s);
+        default: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 512, NV>, p, VEC, tpr, 1, blocks, s);
     }
 }
-template <typename T, typename W>
+template <typename T, typename W, bool VEC>
 cudaError_t pick_bwd_ring(const NormBwdParams& p, cudaStream_t s) {
-    constexpr int NV = 16 / Elem<T>::VEC;
-    const int tpr = ring_tpr(p.width), arrays = p.res ? 3 : 2;
+    constexpr int NV = VEC ? 16 / Elem<T>::VEC : 16;
+    const int arrays = p.res ? 3 : 2, tpr = ring_tpr(p.width, arrays);
     switch (tpr) {
-        case 32: return run_ring(norm_bwd_ring_kernel<T, W, 32, NV>, p, tpr, arrays, p.blocks, s);
-        case 64: return run_ring(norm_bwd_ring_kernel<T, W, 64, NV>, p, tpr, arrays, p.blocks, s);
-        case 128: return run_ring(norm_bwd_ring_kernel<T, W, 128, NV>, p, tpr, arrays, p.blocks, s);
-        case 192: return run_ring(norm_bwd_ring_kernel<T, W, 192, NV>, p, tpr, arrays, p.blocks, s);
-        case 256: return run_ring(norm_bwd_ring_kernel<T, W, 256, NV>, p, tpr, arrays, p.blocks, s);
-        default: return run_ring(norm_bwd_ring_kernel<T, W, 512, NV>, p, tpr, arrays, p.blocks, s);
+        case 32: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 32, NV>, p, VEC, tpr, arrays, p.blocks, s);
+        case 64: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 64, NV>, p, VEC, tpr, arrays, p.blocks, s);
+        case 128: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 128, NV>, p, VEC, tpr, arrays, p.blocks, s);
+        case 256: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 256, NV>, p, VEC, tpr, arrays, p.blocks, s);
+        default: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 512, NV>, p, VEC, tpr, arrays, p.blocks, s);
     }
 }
 
 template <typename T, typename W>
 cudaError_t start_fwd(NormFwdParams p, bool vec, cudaStream_t s) {
     int blocks = 0;
-    if (vec && ring_plan(p.rows, p.width, p.dtype, 1, &blocks, &p.team_rows)) return pick_fwd_ring<T, W>(p, blocks, s);
+    if (ring_plan(p.rows, p.width, p.dtype, vec, 1, &blocks, &p.team_rows))
+        return vec ? pick_fwd_ring<T, W, true>(p, blocks, s) : pick_fwd_ring<T, W, false>(p, blocks, s);
     return pick_fwd<T, W>(p, vec, s);
 }
 template <typename T, typename W>
 cudaError_t start_bwd(const NormBwdParams& p, cudaStream_t s) {
-    return p.team_rows ? pick_bwd_ring<T, W>(p, s) : pick_bwd<T, W>(p, p.vec != 0, s);
+    if (!p.team_rows) return pick_bwd<T, W>(p, p.vec != 0, s);
+    return p.vec ? pick_bwd_ring<T, W, true>(p, s) : pick_bwd_ring<T, W, false>(p, s);
 }
 
 }  // namespace
@@ -991,7 +1091,8 @@ static int plain_bwd_blocks(long long rows, int width, int dtype) {
 int norm_bwd_max_blocks(long long rows, int width, int dtype) {
     int most = plain_bwd_blocks(rows, width, dtype), blocks = 0, each = 0;
     for (int arrays = 2; arrays <= 3; ++arrays)
-        if (ring_plan(rows, width, dtype, arrays, &blocks, &each) && blocks > most) most = blocks;
+        for (int vec = 0; vec < 2; ++vec)
+            if (ring_plan(rows, width, dtype, vec != 0, arrays, &blocks, &each) && blocks > most) most = blocks;
     return most;
 }
 
@@ -1002,7 +1103,7 @@ void norm_bwd_plan(NormBwdParams* p) {
              (!p->dx || aligned16(p->dx, p->lddx, es, p->rows)) && (!p->res || aligned16(p->res, p->ldr, es, p->rows)) &&
              aligned16(p->weight, 0, ws, 1);
     p->team_rows = 0;
-    if (!p->vec || !ring_plan(p->rows, p->width, p->dtype, p->res ? 3 : 2, &p->blocks, &p->team_rows))
+    if (!ring_plan(p->rows, p->width, p->dtype, p->vec != 0, p->res ? 3 : 2, &p->blocks, &p->team_rows))
         p->blocks = plain_bwd_blocks(p->rows, p->width, p->dtype);
 }
 
