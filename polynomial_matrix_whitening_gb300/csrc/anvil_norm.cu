@@ -23,8 +23,8 @@
 // Many rows (the ring kernels): the rows come by bulk copies into a ring of shared-memory
 // stages per team, several rows ahead.  With one row ahead in registers a block waited out
 // the memory's latency on every row (32768 x 2816 bf16: 150-168 us backward, 78 forward;
-// with the ring 121-125 and 71, 5.2-6.1 TB/s; 32768 x 2815, off the 16-byte boundaries: 522
-// and 152, with the ring 199 and 131).
+// with the ring 121-125 and 71, 5.2-6.1 TB/s; 32768 x 2815, off the 16-byte boundaries,
+// backward: 522, with the ring 199).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
 // of `arrays` rows each (x, or x, dy and the residual's gradient) are on their way.  The
 // team's first thread issues the copies of a stage once the team has read what was in it.
 //
-// Rows off the 16-byte boundaries (VEC false): a bulk copy takes the 16-byte pieces that
+// Rows off the 16-byte boundaries (VEC false, backward only; forward the plain kernels are as
+// fast): a bulk copy takes the 16-byte pieces that
 // cover the row, so it brings up to 14 bytes of the rows (or padding) before and after,
 // which nothing reads; the array's first and last row, which have no such neighbour on one
 // side, are copied element by element.  A thread then has every TPR-th element.
@@ -733,11 +734,11 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
     }
 }
 
-template <typename T, typename W, bool VEC, int TPR, int NV>
+template <typename T, typename W, int TPR, int NV>
 __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) norm_fwd_ring_kernel(const NormFwdParams p) {
-    using Raw = RawUnit<T, VEC>;
-    using F = typename Raw::F;
-    constexpr int E = VEC ? Elem<T>::VEC : 1, P = Raw::P, TEAMS = ring_teams(TPR);
+    using Raw = RawUnit<T, true>;
+    constexpr int E = Elem<T>::VEC, P = E / 2, TEAMS = ring_teams(TPR);
+    using F = uint64_t;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[TEAMS][RING_MAX];
     __shared__ float4 red[TEAMS][2][TPR > 32 ? TPR / 64 : 1];
@@ -747,9 +748,8 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
     team.red = &red[team.id][0][0];
     team.flip = 0;
     const uint32_t row_bytes = static_cast<uint32_t>(p.width * sizeof(T));
-    const uint32_t slot = ring_slot(VEC, row_bytes);
-    const int stages = ring_stages(TPR, 1, slot);
-    uint8_t* mine = ring + static_cast<size_t>(team.id) * stages * slot;
+    const int stages = ring_stages(TPR, 1, row_bytes);
+    uint8_t* mine = ring + static_cast<size_t>(team.id) * stages * row_bytes;
     const long long g = static_cast<long long>(blockIdx.x) * TEAMS + team.id;
     const long long r0 = g * p.team_rows < p.rows ? g * p.team_rows : p.rows;
     const long long r1 = r0 + p.team_rows < p.rows ? r0 + p.team_rows : p.rows;
@@ -761,16 +761,8 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
     __syncthreads();
     auto issue = [&](long long row, int s) {
         uint64_t* bar = &full[team.id][s];
-        const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-        if constexpr (VEC) {
-            mbar_arrive_expect_tx(bar, row_bytes);
-            bulk_load(smem_u32(mine + s * slot), x, row_bytes, bar);
-        } else if (row == 0 || row == p.rows - 1) {
-            mbar_arrive_cta(bar);  // the team copies this row when it comes to it
-        } else {
-            mbar_arrive_expect_tx(bar, cover_bytes(x, row_bytes));
-            cover_load(smem_u32(mine + s * slot), x, row_bytes, bar);
-        }
+        mbar_arrive_expect_tx(bar, row_bytes);
+        bulk_load(smem_u32(mine + s * row_bytes), static_cast<const T*>(p.x) + row * p.ldx, row_bytes, bar);
     };
     if (team.t == 0)
         for (int s = 0; s < stages && r0 + s < r1; ++s) issue(r0 + s, s);
@@ -798,21 +790,11 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
             freed[k] = s;
             if (k == 0 || two) {
                 if (!dead) dead = !mbar_wait(&full[team.id][s], phase, p.err);
-                uint32_t src = smem_u32(mine + s * slot);
-                if constexpr (!VEC) {
-                    const T* x = static_cast<const T*>(p.x) + (row + k) * p.ldx;
-                    if (row + k == 0 || row + k == p.rows - 1) {
-                        copy_row<T, TPR>(src, x, p.width, team.t);
-                        fence_proxy_async_smem();  // before the next bulk copy into the stage
-                        team.sync();
-                    }
-                    src += slot_offset(x);
-                }
-                constexpr uint32_t UNIT = E * sizeof(T);
+                const uint32_t src = smem_u32(mine + s * row_bytes) + team.t * 16;
 #pragma unroll
                 for (int u = 0; u < NV; ++u) {
                     if (!in[u]) break;
-                    xr[k][u].load_shared(src + (team.t + u * TPR) * UNIT);
+                    xr[k][u].r = lds128(src + u * TPR * 16);
                 }
                 if (++s == stages) {
                     s = 0;
@@ -826,7 +808,7 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
         float sum[2], sq[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            F acc = p_all<F>(0.f);
+            F acc = 0;
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 if (!in[u]) break;
@@ -847,7 +829,7 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
         for (int k = 0; k < 2; ++k) {
             sum[k] *= inv_n;
             const F nm = p_all<F>(-sum[k]);
-            F acc = p_all<F>(0.f);
+            F acc = 0;
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 if (!in[u]) break;
@@ -954,8 +936,8 @@ cudaError_t pick_fwd(const NormFwdParams& p, bool vec, cudaStream_t s) {
     if (w <= 64) return run_fwd<T, W, false, 8, 8>(p, s);
     if (w <= 256) return run_fwd<T, W, false, 32, 8>(p, s);
     if (w <= 1024) return run_fwd<T, W, false, 128, 8>(p, s);
-    if (w <= 2048) return run_fwd<T, W, false, 128, 16>(p, s);
-    if (w <= 4096) return run_fwd<T, W, false, 256, 16>(p, s);
+    if (w <= 2048) return run_fwd<T, W, false, 256, 8>(p, s);
+    if (w <= 4096) return run_fwd<T, W, false, 512, 8>(p, s);
     if (w <= 8192) return run_fwd<T, W, false, 512, 16>(p, s);
     return run_fwd<T, W, false, 512, 32>(p, s);
 }
@@ -986,23 +968,29 @@ cudaError_t pick_bwd(const NormBwdParams& p, bool vec, cudaStream_t s) {
 
 namespace {
 
-// Threads of a team of the ring kernels: up to 16 columns each.
+// Threads of a team of the ring kernels: up to 16 columns each, off the 16-byte boundaries
+// 8 where a block can hold that many threads twice.
 // (2049 to 3072 columns: 192 threads run 32768 x 2816 bf16 forward in 71 us, 256 in 78;
 // backward 256 are faster, 121 against 125.)
-int ring_tpr(int width, int arrays) {
+int ring_tpr(int width, int arrays, bool vec) {
+    if (!vec && width <= 2048) return width <= 512 ? 64 : width <= 1024 ? 128 : 256;
     return width <= 512 ? 32 : width <= 1024 ? 64 : width <= 2048 ? 128 : width <= 3072 && arrays == 1 ? 192 : width <= 4096 ? 256 : 512;
 }
 
-// Teams of the ring kernels on the whole device, and whether they run: rows of 1 KB (off the
-// 16-byte boundaries 256 bytes; the plain kernels' narrow teams are faster below), at least
-// four rows for each team (below that there is nothing to run ahead of, and the plain
-// kernels start faster), and two stages that fit.
+// Teams of the ring kernels on the whole device, and whether they run: two stages fit, rows
+// of 1 KB (off the 16-byte boundaries, backward only, 512 bytes; the plain kernels' narrow
+// teams are faster below), and enough rows per team to make up for a slower start.
+// Measured with bf16, ring against plain, us: forward 1024 columns 42.9/47.2 at 48 rows a
+// team and 22.8/21.4 at 24, 2816 64.9/65.9 at 96 and 35.9/34.0 at 48; backward 2816
+// 19.9/20.4 at 8 and 38/43 at 24; off the boundaries 1023 columns 38.3/39.0 at 24 and
+// 21.6/19.7 at 12, 2815 20.2/26.1 at 6.
 bool ring_plan(long long rows, int width, int dtype, bool vec, int arrays, int* blocks, int* team_rows) {
-    const int es = dtype_size(dtype), tpr = ring_tpr(width, arrays);
-    if (width * es < (vec ? 1024 : 256) || width > 8192 || ring_stages(tpr, arrays, ring_slot(vec, width * es)) < 2) return false;
+    const int es = dtype_size(dtype), tpr = ring_tpr(width, arrays, vec);
+    const int least = arrays == 1 ? 48 : vec ? 8 : width <= 1024 ? 24 : 6;
+    if (width * es < (vec ? 1024 : 512) || width > 8192 || ring_stages(tpr, arrays, ring_slot(vec, width * es)) < 2) return false;
     const int per_block = ring_teams(tpr);
     const long long teams = 152ll * (tpr > RING_BLOCK ? 1 : 2) * per_block;
-    if (rows < 4 * teams) return false;
+    if (rows < least * teams) return false;
     const long long each = (rows + teams - 1) / teams;
     *team_rows = static_cast<int>(each);
     *blocks = static_cast<int>((rows + each * per_block - 1) / (each * per_block));
@@ -1021,43 +1009,51 @@ cudaError_t run_ring(K kernel, const P& p, bool vec, int tpr, int arrays, int bl
     return cudaGetLastError();
 }
 
-template <typename T, typename W, bool VEC>
+template <typename T, typename W>
 cudaError_t pick_fwd_ring(const NormFwdParams& p, int blocks, cudaStream_t s) {
-    constexpr int NV = VEC ? 16 / Elem<T>::VEC : 16;
-    const int tpr = ring_tpr(p.width, 1);
+    constexpr int NV = 16 / Elem<T>::VEC;
+    const int tpr = ring_tpr(p.width, 1, true);
     switch (tpr) {
-        case 32: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 32, NV>, p, VEC, tpr, 1, blocks, s);
-        case 64: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 64, NV>, p, VEC, tpr, 1, blocks, s);
-        case 128: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 128, NV>, p, VEC, tpr, 1, blocks, s);
-        case 192: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 192, NV>, p, VEC, tpr, 1, blocks, s);
-        case 256: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 256, NV>, p, VEC, tpr, 1, blocks, s);
-        default: return run_ring(norm_fwd_ring_kernel<T, W, VEC, 512, NV>, p, VEC, tpr, 1, blocks, s);
+        case 32: return run_ring(norm_fwd_ring_kernel<T, W, 32, NV>, p, true, tpr, 1, blocks, s);
+        case 64: return run_ring(norm_fwd_ring_kernel<T, W, 64, NV>, p, true, tpr, 1, blocks, s);
+        case 128: return run_ring(norm_fwd_ring_kernel<T, W, 128, NV>, p, true, tpr, 1, blocks, s);
+        case 192: return run_ring(norm_fwd_ring_kernel<T, W, 192, NV>, p, true, tpr, 1, blocks, s);
+        case 256: return run_ring(norm_fwd_ring_kernel<T, W, 256, NV>, p, true, tpr, 1, blocks, s);
+        default: return run_ring(norm_fwd_ring_kernel<T, W, 512, NV>, p, true, tpr, 1, blocks, s);
     }
 }
-template <typename T, typename W, bool VEC>
+template <typename T, typename W>
 cudaError_t pick_bwd_ring(const NormBwdParams& p, cudaStream_t s) {
-    constexpr int NV = VEC ? 16 / Elem<T>::VEC : 16;
-    const int arrays = p.res ? 3 : 2, tpr = ring_tpr(p.width, arrays);
+    constexpr int NV = 16 / Elem<T>::VEC;
+    const int arrays = p.res ? 3 : 2, tpr = ring_tpr(p.width, arrays, p.vec != 0);
+    if (!p.vec) {
+        switch (tpr) {
+            case 64: return run_ring(norm_bwd_ring_kernel<T, W, false, 64, 8>, p, false, tpr, arrays, p.blocks, s);
+            case 128: return run_ring(norm_bwd_ring_kernel<T, W, false, 128, 8>, p, false, tpr, arrays, p.blocks, s);
+            case 256:
+                return p.width <= 2048 ? run_ring(norm_bwd_ring_kernel<T, W, false, 256, 8>, p, false, tpr, arrays, p.blocks, s)
+                                       : run_ring(norm_bwd_ring_kernel<T, W, false, 256, 16>, p, false, tpr, arrays, p.blocks, s);
+            default: return run_ring(norm_bwd_ring_kernel<T, W, false, 512, 16>, p, false, tpr, arrays, p.blocks, s);
+        }
+    }
     switch (tpr) {
-        case 32: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 32, NV>, p, VEC, tpr, arrays, p.blocks, s);
-        case 64: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 64, NV>, p, VEC, tpr, arrays, p.blocks, s);
-        case 128: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 128, NV>, p, VEC, tpr, arrays, p.blocks, s);
-        case 256: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 256, NV>, p, VEC, tpr, arrays, p.blocks, s);
-        default: return run_ring(norm_bwd_ring_kernel<T, W, VEC, 512, NV>, p, VEC, tpr, arrays, p.blocks, s);
+        case 32: return run_ring(norm_bwd_ring_kernel<T, W, true, 32, NV>, p, true, tpr, arrays, p.blocks, s);
+        case 64: return run_ring(norm_bwd_ring_kernel<T, W, true, 64, NV>, p, true, tpr, arrays, p.blocks, s);
+        case 128: return run_ring(norm_bwd_ring_kernel<T, W, true, 128, NV>, p, true, tpr, arrays, p.blocks, s);
+        case 256: return run_ring(norm_bwd_ring_kernel<T, W, true, 256, NV>, p, true, tpr, arrays, p.blocks, s);
+        default: return run_ring(norm_bwd_ring_kernel<T, W, true, 512, NV>, p, true, tpr, arrays, p.blocks, s);
     }
 }
 
 template <typename T, typename W>
 cudaError_t start_fwd(NormFwdParams p, bool vec, cudaStream_t s) {
     int blocks = 0;
-    if (ring_plan(p.rows, p.width, p.dtype, vec, 1, &blocks, &p.team_rows))
-        return vec ? pick_fwd_ring<T, W, true>(p, blocks, s) : pick_fwd_ring<T, W, false>(p, blocks, s);
+    if (vec && ring_plan(p.rows, p.width, p.dtype, true, 1, &blocks, &p.team_rows)) return pick_fwd_ring<T, W>(p, blocks, s);
     return pick_fwd<T, W>(p, vec, s);
 }
 template <typename T, typename W>
 cudaError_t start_bwd(const NormBwdParams& p, cudaStream_t s) {
-    if (!p.team_rows) return pick_bwd<T, W>(p, p.vec != 0, s);
-    return p.vec ? pick_bwd_ring<T, W, true>(p, s) : pick_bwd_ring<T, W, false>(p, s);
+    return p.team_rows ? pick_bwd_ring<T, W>(p, s) : pick_bwd<T, W>(p, p.vec != 0, s);
 }
 
 }  // namespace
