@@ -168,89 +168,163 @@ struct Product {
     bool f16;
     GemmEpilogue epi;
     float* part;  // scratch of the tail tiles' parts
+    bool overlap_next, overlap_previous;  // pair_gemm_kernel's flags
 };
 
 // How a product runs.
 struct Plan {
-    bool few;      // row_gemm_kernel
-    int bn;        // few: B rows of a block
-    int whole;     // tiles in one piece (the others are split along k)
-    int splits;    // of a tail tile, or of the contraction (few)
-    int kb;        // k-blocks per split
-    size_t part;   // bytes of the tail tiles' parts
+    bool few;         // row_gemm_kernel
+    int bn;           // few: B rows of a block,
+    int splits, kb;   //      parts of the contraction and the k-blocks of each
+    TileSplit split;  // pair_gemm_kernel
+    int tail, units;  // tiles in parts; units of work
+    size_t part;      // bytes of the parts
+    double cost;      // SM cycles, estimated
 };
 
 constexpr int FEW_ROWS = 256;  // row_gemm_kernel is considered up to here
+constexpr int PLAN_PAIRS = PLAN_SMS / 2;
 
-// epilogue: SM cycles that the epilogue of a whole tile of the pair kernel takes.
-Plan plan_product(int64_t rows, int cols, int64_t k, bool a_mn, bool out_f32, double epilogue) {
-    Plan p = {};
-    const int64_t kb = (k + GEMM_BK - 1) / GEMM_BK;
-    double best = 0;
-    if (rows <= FEW_ROWS && !a_mn && !out_f32) {
-        // Blocks of 128 weight rows by 16 to 128 tokens, the contraction whole or split over a
-        // cluster.  Estimated times in SM cycles, from the kernel's own time stamps: 545 for a
-        // k-block (the MMA reads its 128-row operand at 32 bytes a cycle, whatever the tokens),
-        // 1700 to the first and from the last, 28 for a token's column; a join 2500, and 250 for
-        // a token's column of each block's share.
-        for (int bn = 16; bn <= 128; bn *= 2) {
-            const int64_t tiles = static_cast<int64_t>((cols + ROW_TILE_A - 1) / ROW_TILE_A) * ((rows + bn - 1) / bn);
-            const double columns = static_cast<double>(bn < rows ? bn : rows) * (epilogue / 2500.0);
-            for (int s = 1; s <= 8; s *= 2) {
-                const int64_t per = (kb + s - 1) / s;
-                if (s > 1 && (per * (s - 1) >= kb || tiles * s > PLAN_SMS)) break;  // every split has work
-                const double turns = static_cast<double>((tiles * s + PLAN_SMS - 1) / PLAN_SMS);
-                const double finish = s == 1 ? 28.0 * columns : 2500.0 + 10.0 * bn + 60.0 * columns / s;
-                const double cost = turns * (per * 545.0 + 1700.0 + finish);
-                if (best == 0 || cost < best) {
-                    best = cost;
-                    p.few = true;
-                    p.bn = bn;
-                    p.splits = s;
-                    p.kb = static_cast<int>(per);
-                }
+// What the pair kernel finds when it starts: of the grid's pairs the first `early` are free
+// at once, the others `delay` SM cycles later (the last turn of the product before it).
+struct Start {
+    int early;
+    double delay;
+};
+constexpr Start ALL_FREE = {PLAN_PAIRS, 0.0};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Blocks of 128 weight rows by 16 to 128 tokens, the contraction whole or split over a
+// cluster.  Estimated times in SM cycles, from the kernel's own time stamps: 545 for a
+// k-block (the MMA reads its 128-row operand at 32 bytes a cycle, whatever the tokens),
+// 1700 to the first and from the last, 28 for a token's column; a join 2500, and 250 for
+// a token's column of each block's share.
+void plan_few(int64_t rows, int cols, int64_t kb, double epilogue, Plan* p) {
+    for (int bn = 16; bn <= 128; bn *= 2) {
+        const int64_t tiles = ceil_div(cols, ROW_TILE_A) * ceil_div(rows, bn);
+        const double columns = static_cast<double>(bn < rows ? bn : rows) * (epilogue / 2500.0);
+        for (int s = 1; s <= 8; s *= 2) {
+            const int64_t per = ceil_div(kb, s);
+            if (s > 1 && (per * (s - 1) >= kb || tiles * s > PLAN_SMS)) break;  // every split has work
+            const double turns = static_cast<double>(ceil_div(tiles * s, PLAN_SMS));
+            const double finish = s == 1 ? 28.0 * columns : 2500.0 + 10.0 * bn + 60.0 * columns / s;
+            const double cost = turns * (per * 545.0 + 1700.0 + finish);
+            if (p->cost == 0 || cost < p->cost) {
+                p->cost = cost;
+                p->few = true;
+                p->bn = bn;
+                p->splits = s;
+                p->kb = static_cast<int>(per);
             }
         }
     }
-    // Tiles in one piece, turn by turn of the grid's pairs; the tiles left over for a last turn
-    // that would not be full, or all of them, may go in parts instead (split along k, or whole
-    // but with the epilogue left to the second kernel).  Estimated times in SM cycles, fitted
-    // to measurements: 550 for a k-block, 2500 for filling the pipeline; an epilogue overlaps
-    // the next tile's products; parts cost 8000 for the second kernel and 200 a unit for their
-    // way through memory.
-    const int64_t pairs = PLAN_SMS / 2;
-    const int64_t tiles = ((rows + PAIR_ROWS - 1) / PAIR_ROWS) * ((cols + PAIR_COLS - 1) / PAIR_COLS);
-    const double products = kb * 550.0, turn = products > epilogue ? products : epilogue;
-    const double leave = 7500.0;  // filling the pipeline and leaving the kernel
-    const double whole_cost =
-        static_cast<double>((tiles + pairs - 1) / pairs) * turn + (products < epilogue ? products : epilogue) + leave;
-    if (best == 0 || whole_cost < best) {
-        best = whole_cost;
-        p.few = false;
-        p.whole = static_cast<int>(tiles);
-        p.splits = 1;
-        p.kb = static_cast<int>(kb);
-    }
-    for (int64_t tail = tiles % pairs;; tail = tiles) {
-        const int64_t whole = tiles - tail;
-        for (int64_t s = 1; tail && s <= 64 && s <= kb; ++s) {
-            const int64_t per = (kb + s - 1) / s;
-            if (per * (s - 1) >= kb) continue;  // every split has work
-            const int64_t turns = (tail * s + pairs - 1) / pairs;
-            const double cost = whole / pairs * turn + turns * (per * 550.0 + 2500.0) + leave + 8000.0 + tail * s * 200.0;
-            if (cost < best) {
-                best = cost;
-                p.few = false;
-                p.whole = static_cast<int>(whole);
-                p.splits = static_cast<int>(s);
-                p.kb = static_cast<int>(per);
-                p.part = static_cast<size_t>(tail * s) * 4 * PAIR_ROWS * PAIR_COLS;
-            }
-            if (turns > 4) break;  // parts beyond a few turns only add traffic
+}
+
+// Tiles in one piece, turn by turn of the grid's pairs; the tiles left over for a last turn
+// that would not be full, or all of them, may go in parts instead (split along k, or whole
+// but with the epilogue left to the finishing kernel).  Estimated times in SM cycles, fitted
+// to measurements: 550 for a k-block, 2500 for filling the pipeline, 7500 for starting and
+// leaving the kernel; an epilogue overlaps the next tile's products; parts cost 8000 for
+// the finishing kernel and 200 a unit for their way through memory.
+constexpr double KB_CYCLES = 550.0, FILL_CYCLES = 2500.0, LEAVE_CYCLES = 7500.0, FINISH_CYCLES = 8000.0, PART_CYCLES = 200.0;
+
+int64_t tiles_of(int64_t rows, int cols) { return ceil_div(rows, PAIR_ROWS) * ceil_div(cols, PAIR_COLS); }
+double turn_cycles(int64_t kb, double epilogue) { return kb * KB_CYCLES > epilogue ? kb * KB_CYCLES : epilogue; }
+
+void set_whole(int64_t tiles, double cost, Plan* p) {
+    memset(p, 0, sizeof(*p));
+    p->cost = cost;
+    p->split = {static_cast<int>(tiles), PLAN_PAIRS, PLAN_PAIRS, 0, 1, 0, 1, 0};
+    p->units = static_cast<int>(tiles);
+}
+
+void plan_whole(int64_t tiles, int64_t kb, double epilogue, Start at, Plan* p) {
+    const double products = kb * KB_CYCLES, turn = turn_cycles(kb, epilogue);
+    const int64_t full = tiles / PLAN_PAIRS, rest = tiles % PLAN_PAIRS;
+    double end = full * turn + (full ? at.delay : 0.0);
+    const double last = (full + 1) * turn + (rest > at.early ? at.delay : 0.0);
+    if (rest && last > end) end = last;
+    const double cost = end + (products < epilogue ? products : epilogue) + LEAVE_CYCLES;
+    if (p->cost == 0 || cost < p->cost) set_whole(tiles, cost, p);
+}
+
+// Tail tiles in parts: tiles_a of them in parts of per_a k-blocks for the early pairs, the
+// others in parts of per_b for the late ones.
+void plan_parts(int64_t tiles, int64_t tail, int64_t kb, double turn, Start at, int64_t tiles_a, int64_t per_a, int64_t per_b,
+                Plan* p) {
+    const int64_t sa = ceil_div(kb, per_a), sb = ceil_div(kb, per_b), tiles_b = tail - tiles_a, late = PLAN_PAIRS - at.early;
+    const int64_t parts = tiles_a * sa + tiles_b * sb;
+    const int64_t turns_a = ceil_div(tiles_a * sa, at.early), turns_b = tiles_b ? ceil_div(tiles_b * sb, late) : 0;
+    double end = turns_a * (per_a * KB_CYCLES + FILL_CYCLES);
+    const double end_b = at.delay + turns_b * (per_b * KB_CYCLES + FILL_CYCLES);
+    if (late && end_b > end) end = end_b;
+    const double cost = (tiles - tail) / PLAN_PAIRS * turn + end + LEAVE_CYCLES + FINISH_CYCLES + parts * PART_CYCLES;
+    if (cost >= p->cost) return;
+    memset(p, 0, sizeof(*p));
+    p->cost = cost;
+    p->split = {static_cast<int>(tiles - tail), PLAN_PAIRS,           at.early,
+                static_cast<int>(tiles_a),      static_cast<int>(sa), static_cast<int>(per_a),
+                static_cast<int>(sb),           static_cast<int>(per_b)};
+    p->tail = static_cast<int>(tail);
+    p->units = static_cast<int>(tiles - tail + (turns_a > turns_b ? turns_a : turns_b) * PLAN_PAIRS);
+    p->part = static_cast<size_t>(parts) * 4 * PAIR_ROWS * PAIR_COLS;
+}
+
+// epilogue: SM cycles that the epilogue of a whole tile of the pair kernel takes.
+Plan plan_product(int64_t rows, int cols, int64_t k, bool few, double epilogue, Start at) {
+    Plan p = {};
+    const int64_t kb = ceil_div(k, GEMM_BK), tiles = tiles_of(rows, cols);
+    if (few && rows <= FEW_ROWS) plan_few(rows, cols, kb, epilogue, &p);
+    plan_whole(tiles, kb, epilogue, at, &p);
+    const double turn = turn_cycles(kb, epilogue);
+    for (int64_t tail = tiles % PLAN_PAIRS;; tail = tiles) {
+        if (tail && at.early == PLAN_PAIRS) {
+            // parts beyond a few turns only add traffic
+            for (int64_t s = 1; s <= 64 && s <= kb && tail * s <= 5 * PLAN_PAIRS; ++s)
+                plan_parts(tiles, tail, kb, turn, at, tail, ceil_div(kb, s), kb, &p);
+        } else if (tail) {
+            // so many turns of the early pairs at so many parts, the rest in as many parts as fill
+            // the late pairs for so many turns
+            const int64_t late = PLAN_PAIRS - at.early;
+            for (int64_t ta = 1; ta <= 4; ++ta)
+                for (int64_t sa = 1; sa <= 16 && sa <= kb; ++sa) {
+                    const int64_t most = ta * at.early / sa, tiles_a = most < tail ? most : tail, tiles_b = tail - tiles_a;
+                    if (!tiles_a) break;
+                    if (!tiles_b) {
+                        plan_parts(tiles, tail, kb, turn, at, tiles_a, ceil_div(kb, sa), kb, &p);
+                        continue;
+                    }
+                    for (int64_t tb = 1; tb <= 4; ++tb) {
+                        int64_t sb = tb * late / tiles_b;
+                        if (sb > 64) sb = 64;
+                        if (sb > kb) sb = kb;
+                        if (sb) plan_parts(tiles, tail, kb, turn, at, tiles_a, ceil_div(kb, sa), ceil_div(kb, sb), &p);
+                    }
+                }
         }
         if (tail == tiles) break;
     }
     return p;
+}
+
+// The two products of a backward pass.  The second kernel's pairs start where the first
+// leaves SMs idle, so a last turn of the first that is not full costs nothing when the
+// second's parts are cut to fill it; or both run as they would alone.
+void plan_both(int64_t rows1, int cols1, int64_t k1, double epilogue1, int64_t rows2, int cols2, int64_t k2, double epilogue2,
+               Plan* first, Plan* second) {
+    *first = plan_product(rows1, cols1, k1, true, epilogue1, ALL_FREE);
+    *second = plan_product(rows2, cols2, k2, false, epilogue2, ALL_FREE);
+    if (first->few) return;
+    const int64_t kb = ceil_div(k1, GEMM_BK), tiles = tiles_of(rows1, cols1);
+    const int64_t full = tiles / PLAN_PAIRS, rest = tiles % PLAN_PAIRS;
+    const double turn = turn_cycles(kb, epilogue1);
+    const Start at = {rest ? static_cast<int>(PLAN_PAIRS - rest) : PLAN_PAIRS, rest ? turn : 0.0};
+    const Plan p = plan_product(rows2, cols2, k2, false, epilogue2, at);
+    const double cost = full * turn + LEAVE_CYCLES + p.cost;
+    if (cost >= first->cost + second->cost) return;
+    set_whole(tiles, full * turn + LEAVE_CYCLES, first);
+    *second = p;
 }
 
 // The epilogue's cost for plan_product, by what it does: measured on 14336 x 6144 x 832
@@ -266,7 +340,8 @@ double epilogue_cycles(const GemmEpilogue& e, int64_t rows) {
     return c;
 }
 
-anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, cudaStream_t s) {
+// Launches the product; what is left to add up of it goes to `rest`.
+anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, cudaStream_t s, TailSumParams* rest) {
     anvil_status st;
     cudaError_t e;
     if (plan.few) {
@@ -300,11 +375,10 @@ anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, c
     g.f16 = q.f16;
     g.tiles_r = static_cast<int>((q.rows + PAIR_ROWS - 1) / PAIR_ROWS);
     g.tiles_c = (q.cols + PAIR_COLS - 1) / PAIR_COLS;
-    g.whole = plan.whole;
-    g.splits = plan.splits;
-    const int tail = g.tiles_r * g.tiles_c - plan.whole;
-    g.units = plan.whole + tail * plan.splits;
-    g.kb_per_split = plan.kb;
+    g.split = plan.split;
+    g.units = plan.units;
+    g.overlap_next = q.overlap_next;
+    g.overlap_previous = q.overlap_previous;
     g.err = dev->err;
     const GemmEpilogue& ep = q.epi;
     const int es = ep.out_f32 ? 4 : 2;
@@ -315,41 +389,51 @@ anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, c
     if (g.out_tma && (st = encode(&g.tm_out, es, q.f16, ep.out, q.cols, q.rows, ep.ldout, box, 128))) return st;
     if (g.in_tma && (st = encode(&g.tm_in, es, q.f16, ep.in, q.cols, q.rows, ep.ldin, box, 128))) return st;
     if (g.z_tma && (st = encode(&g.tm_z, es, q.f16, ep.z, q.cols, q.rows, ep.ldz, box, 128))) return st;
-    if (tail && (st = encode(&g.tm_part, 4, false, q.part, PAIR_COLS, static_cast<int64_t>(tail) * plan.splits * PAIR_ROWS,
-                             PAIR_COLS, 32, 128)))
+    if (plan.tail && (st = encode(&g.tm_part, 4, false, q.part, PAIR_COLS,
+                                  static_cast<int64_t>(plan.part / (4 * PAIR_COLS)), PAIR_COLS, 32, 128)))
         return st;
     e = profiled(ANVIL_KERNEL_LINEAR_PRODUCT, s, [&] { return launch_pair_gemm(g, dev->sm_count, s); });
     if (e) return cuda_fail(e, "linear product launch");
-    if (tail) {
-        TailSumParams t;
-        memset(&t, 0, sizeof(t));
-        t.epi = ep;
-        t.part = q.part;
-        t.rows = g.rows;
-        t.cols = g.cols;
-        t.tiles_r = g.tiles_r;
-        t.tiles_c = g.tiles_c;
-        t.whole = plan.whole;
-        t.splits = plan.splits;
-        t.f16 = q.f16;
-        e = profiled(ANVIL_KERNEL_LINEAR_SUM, s, [&] { return launch_tail_sum(t, s); });
-        if (e) return cuda_fail(e, "split product sum launch");
+    if (plan.tail) {
+        rest->epi = ep;
+        rest->part = q.part;
+        rest->rows = g.rows;
+        rest->cols = g.cols;
+        rest->tiles_r = g.tiles_r;
+        rest->tiles_c = g.tiles_c;
+        rest->tiles = plan.tail;
+        rest->split = plan.split;
     }
     return ANVIL_OK;
 }
 
-anvil_status copy_operand(Stored* s, void* copy, cudaStream_t stream) {
-    RepackParams r;
-    r.src = static_cast<const uint16_t*>(s->p);
-    r.dst = static_cast<uint16_t*>(copy);
-    r.rows = s->rows;
-    r.lds = s->ld;
-    r.cols = s->cols;
-    *s = with_copy(*s, copy);
-    r.ldd = s->ld;
-    const cudaError_t e = profiled(ANVIL_KERNEL_LINEAR_PREPARE, stream, [&] { return launch_repack(r, stream); });
-    return e ? cuda_fail(e, "operand copy launch") : ANVIL_OK;
+// The finishing launch, where there is anything to finish.
+anvil_status run_finish(const FinishParams& f, cudaStream_t s) {
+    if (!f.tail[0].tiles && !f.tail[1].tiles && !f.bias.out) return ANVIL_OK;
+    const cudaError_t e = profiled(ANVIL_KERNEL_LINEAR_SUM, s, [&] { return launch_finish(f, s); });
+    return e ? cuda_fail(e, "linear sum launch") : ANVIL_OK;
 }
+
+// Operands off the 16-byte boundaries become copies on them, in one launch.
+struct Copies {
+    RepackParams p;
+    void add(Stored* s, void* copy) {
+        if (!copy_bytes(*s)) return;
+        Repack& r = p.job[p.jobs++];
+        r.src = static_cast<const uint16_t*>(s->p);
+        r.dst = static_cast<uint16_t*>(copy);
+        r.rows = s->rows;
+        r.lds = s->ld;
+        r.cols = s->cols;
+        *s = with_copy(*s, copy);
+        r.ldd = s->ld;
+    }
+    anvil_status run(cudaStream_t s) const {
+        if (!p.jobs) return ANVIL_OK;
+        const cudaError_t e = profiled(ANVIL_KERNEL_LINEAR_PREPARE, s, [&] { return launch_repack(p, s); });
+        return e ? cuda_fail(e, "operand copy launch") : ANVIL_OK;
+    }
+};
 
 Stored stored_weight(const void* w, int n, int k, int64_t ldw, bool transposed) {
     return transposed ? Stored{w, k, ldw, n} : Stored{w, n, ldw, k};
@@ -398,7 +482,7 @@ LinearLayout linear_layout(const anvil_linear_desc* d) {
     L.off_x = 0;
     L.off_w = L.off_x + copy_bytes(L.x);
     L.off_part = L.off_w + copy_bytes(L.w);
-    L.plan = plan_product(d->rows, d->n, d->k, false, false, epilogue_cycles(forward_epilogue(d), d->rows));
+    L.plan = plan_product(d->rows, d->n, d->k, true, epilogue_cycles(forward_epilogue(d), d->rows), ALL_FREE);
     L.total = L.off_part + L.plan.part;
     return L;
 }
@@ -458,13 +542,13 @@ LinearGradLayout linear_grad_layout(const anvil_linear_grad_desc* d) {
         if (d->dbias) at += align256(sizeof(float) * static_cast<size_t>(L.blocks_r) * d->n);
     }
     L.off_part = at;
-    // the two products run one after the other: they share the scratch of their parts
-    if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, false, false, epilogue_cycles(dx_epilogue(d), d->rows));
     const int64_t wr = tr ? d->k : d->n;
-    if (d->dweight)
-        L.pdw = plan_product(wr, tr ? d->n : d->k, d->rows, true, d->dweight_dtype == ANVIL_F32,
-                             epilogue_cycles(dweight_epilogue(d), wr));
-    L.total = at + (L.pdx.part > L.pdw.part ? L.pdx.part : L.pdw.part);
+    const int wc = tr ? d->n : d->k;
+    const double ex = epilogue_cycles(dx_epilogue(d), d->rows), ew = epilogue_cycles(dweight_epilogue(d), wr);
+    if (d->dx && d->dweight) plan_both(d->rows, d->k, d->n, ex, wr, wc, d->rows, ew, &L.pdx, &L.pdw);
+    else if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, true, ex, ALL_FREE);
+    else if (d->dweight) L.pdw = plan_product(wr, wc, d->rows, false, ew, ALL_FREE);
+    L.total = at + L.pdx.part + L.pdw.part;  // the second product may start before the first's parts are added up
     return L;
 }
 
@@ -630,8 +714,10 @@ anvil_status anvil_linear_forward(const anvil_linear_desc* d, void* workspace, s
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (copy_bytes(L.x) && (st = copy_operand(&L.x, ws + L.off_x, s)) != ANVIL_OK) return st;
-    if (copy_bytes(L.w) && (st = copy_operand(&L.w, ws + L.off_w, s)) != ANVIL_OK) return st;
+    Copies copies = {};
+    copies.add(&L.x, ws + L.off_x);
+    copies.add(&L.w, ws + L.off_w);
+    if ((st = copies.run(s)) != ANVIL_OK) return st;
     Product q;
     memset(&q, 0, sizeof(q));
     q.a = L.x;
@@ -643,7 +729,11 @@ anvil_status anvil_linear_forward(const anvil_linear_desc* d, void* workspace, s
     q.f16 = d->dtype == ANVIL_F16;
     q.epi = forward_epilogue(d);
     q.part = reinterpret_cast<float*>(ws + L.off_part);
-    return run_product(q, L.plan, dev, s);
+    FinishParams f;
+    memset(&f, 0, sizeof(f));
+    f.f16 = q.f16;
+    if ((st = run_product(q, L.plan, dev, s, &f.tail[0])) != ANVIL_OK) return st;
+    return run_finish(f, s);
 }
 
 size_t anvil_linear_backward_workspace_bytes(const anvil_linear_grad_desc* d) {
@@ -683,6 +773,9 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const bool f16 = d->dtype == ANVIL_F16;
+    FinishParams f;
+    memset(&f, 0, sizeof(f));
+    f.f16 = f16;
     if (L.prep) {
         ActGradParams p;
         memset(&p, 0, sizeof(p));
@@ -704,13 +797,14 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
         }
         if ((e = profiled(ANVIL_KERNEL_LINEAR_PREPARE, s, [&] { return launch_act_grad(p, s); })))
             return cuda_fail(e, "activation gradient launch");
-        if (d->dbias && (e = profiled(ANVIL_KERNEL_LINEAR_SUM, s, [&] {
-                             return launch_column_sum(p.part, p.blocks_r, d->n, d->dbias, d->accumulate, s);
-                         })))
-            return cuda_fail(e, "bias gradient launch");
+        f.bias = {p.part, d->dbias, p.blocks_r, d->n, d->accumulate};
     }
+    Copies copies = {};
+    if (d->dx) copies.add(&L.w, ws + L.off_w);
+    if (d->dweight) copies.add(&L.x, ws + L.off_x);
+    if ((st = copies.run(s)) != ANVIL_OK) return st;
+    const bool overlap = d->dx && d->dweight && !L.pdx.few;
     if (d->dx) {
-        if (copy_bytes(L.w) && (st = copy_operand(&L.w, ws + L.off_w, s)) != ANVIL_OK) return st;
         Product q;
         memset(&q, 0, sizeof(q));
         q.a = L.dz;
@@ -722,10 +816,10 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
         q.f16 = f16;
         q.epi = dx_epilogue(d);
         q.part = reinterpret_cast<float*>(ws + L.off_part);
-        if ((st = run_product(q, L.pdx, dev, s)) != ANVIL_OK) return st;
+        q.overlap_next = overlap;
+        if ((st = run_product(q, L.pdx, dev, s, &f.tail[0])) != ANVIL_OK) return st;
     }
     if (d->dweight) {
-        if (copy_bytes(L.x) && (st = copy_operand(&L.x, ws + L.off_x, s)) != ANVIL_OK) return st;
         Product q;
         memset(&q, 0, sizeof(q));
         q.a = tr ? L.x : L.dz;
@@ -736,10 +830,11 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
         q.k = d->rows;
         q.f16 = f16;
         q.epi = dweight_epilogue(d);
-        q.part = reinterpret_cast<float*>(ws + L.off_part);
-        if ((st = run_product(q, L.pdw, dev, s)) != ANVIL_OK) return st;
+        q.part = reinterpret_cast<float*>(ws + L.off_part + L.pdx.part);
+        q.overlap_previous = overlap;
+        if ((st = run_product(q, L.pdw, dev, s, &f.tail[1])) != ANVIL_OK) return st;
     }
-    return ANVIL_OK;
+    return run_finish(f, s);
 }
 
 anvil_status anvil_token_logprobs(const anvil_logprob_desc* d, void* stream) {

@@ -17,7 +17,7 @@
 // (one pair per two SMs), its tiles in groups of eight rows of tiles for the L2.  Tiles
 // that would leave the last turn of the grid partly idle (or all of them, where they are
 // few) are split along the contraction: the parts go to scratch in fp32 and
-// tail_sum_kernel adds them up, in order, and finishes the elements.
+// finish_kernel adds them up, in order, and finishes the elements.
 // What bounds it: at 16384 x 4096 x 4096 the products, within a few percent of the
 // library's own rate; a tile narrower than 256 columns gains nothing (128 columns measured
 // 660 SM cycles per 64-deep k-block against 560: a k-block's time is the L2 round trip of
@@ -218,23 +218,31 @@ __device__ __forceinline__ void tile_at(int t, int tiles_r, int tiles_c, int* tr
     *tr = g * RASTER_ROWS + (q - *tc * rows);
 }
 
-// Work unit u: a whole tile, or a split of a tail tile (part: its place in the scratch).
+// Work unit u: a whole tile, or one part of a tail tile (part: its place in the scratch); no
+// work (nkb = 0) where a turn of the tail has none left for its pair.
 struct Unit {
     int tr, tc, part, kb0, nkb;
 };
 __device__ __forceinline__ Unit unit_of(const PairGemmParams& p, int u) {
     Unit r;
+    const TileSplit& s = p.split;
     const int all = (p.k + GEMM_BK - 1) / GEMM_BK;
     int t = u;
     r.part = -1;
     r.kb0 = 0;
     r.nkb = all;
-    if (u >= p.whole) {
-        r.part = u - p.whole;
-        const int q = r.part / p.splits;
-        t = p.whole + q;
-        r.kb0 = (r.part - q * p.splits) * p.kb_per_split;
-        r.nkb = max(0, min(p.kb_per_split, all - r.kb0));
+    if (u >= s.whole) {
+        const int turn = (u - s.whole) / s.pairs, pair = (u - s.whole) - turn * s.pairs;
+        const bool first = pair < s.early;
+        const int parts = first ? s.sa : s.sb, kb = first ? s.kba : s.kbb;
+        const int tiles = first ? s.tiles_a : p.tiles_r * p.tiles_c - s.whole - s.tiles_a;
+        const int i = first ? turn * s.early + pair : turn * (s.pairs - s.early) + pair - s.early;
+        const int q = i / parts;
+        r.part = first ? i : s.tiles_a * s.sa + i;
+        t = s.whole + (first ? q : s.tiles_a + q);
+        r.kb0 = (i - q * parts) * kb;
+        r.nkb = q < tiles ? max(0, min(kb, all - r.kb0)) : 0;
+        if (q >= tiles) t = 0;
     }
     tile_at(t, p.tiles_r, p.tiles_c, &r.tr, &r.tc);
     return r;
@@ -467,7 +475,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
     __shared__ volatile int aborted;
     __shared__ volatile int armed[STAGES];  // 1 + the k-block last loaded into each stage (0: none)
 
-    pdl_allow_next();
+    if (!p.overlap_next) pdl_allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();  // 0 = leader (issues the MMAs)
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -496,7 +504,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
     tc_fence_before();
     cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
     tc_fence_after();
-    pdl_wait_previous();
+    // The two products of a backward pass read nothing of each other's: the first lets the
+    // second start once the kernels before both have ended, and the second's pairs run on the
+    // SMs that the first leaves idle in its last turn.  The second ends after the first, so
+    // that what waits for it has both.
+    if (!p.overlap_previous) pdl_wait_previous();
+    if (p.overlap_next) pdl_allow_next();
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0 || warp == 2) {
@@ -614,6 +627,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                 break;
             }
             const Unit t = unit_of(p, u);
+            if (t.nkb == 0) continue;
             const int row0 = t.tr * PAIR_ROWS + lrow;
             const int col0 = t.tc * BN + lcol;
             const uint32_t tlane = tmem + (static_cast<uint32_t>(x.quad * 32) << 16) + static_cast<uint32_t>(lcol);
@@ -676,19 +690,20 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
     cluster_sync();
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, PAIR_TMEM);
+    if (p.overlap_previous) pdl_wait_previous();
 }
 
 // The tail tiles of pair_gemm_kernel: the parts of each element, in order, then what follows
 // the accumulator.  A block takes 16 rows of a tile, a thread one column of them, so that
 // neighbouring lanes are neighbouring elements whatever the arrays' alignment.
-constexpr int TAIL_ROWS = 16;
+constexpr int FINISH_THREADS = PAIR_COLS;
+constexpr int TAIL_ROWS = 16, TAIL_BLOCKS = PAIR_ROWS / TAIL_ROWS;
 template <typename T>
-__global__ void __launch_bounds__(PAIR_COLS) tail_sum_kernel(const __grid_constant__ TailSumParams p) {
-    pdl_allow_next();
+__device__ __forceinline__ void tail_sum(const TailSumParams& p, int block) {
     const GemmEpilogue& e = p.epi;
-    const int tile = blockIdx.x / (PAIR_ROWS / TAIL_ROWS), r0 = blockIdx.x % (PAIR_ROWS / TAIL_ROWS) * TAIL_ROWS;
+    const int tile = block / TAIL_BLOCKS, r0 = block % TAIL_BLOCKS * TAIL_ROWS;
     int tr, tc;
-    tile_at(p.whole + tile, p.tiles_r, p.tiles_c, &tr, &tc);
+    tile_at(p.split.whole + tile, p.tiles_r, p.tiles_c, &tr, &tc);
     const int col = tc * PAIR_COLS + threadIdx.x;
     const int rows = min(TAIL_ROWS, p.rows - tr * PAIR_ROWS - r0);  // of this block that exist
     const long long row = static_cast<long long>(tr) * PAIR_ROWS + r0;
@@ -699,14 +714,17 @@ __global__ void __launch_bounds__(PAIR_COLS) tail_sum_kernel(const __grid_consta
             bias = e.bias_f32 ? static_cast<const float*>(e.bias)[col] : Elem<T>::load(static_cast<const T*>(e.bias)[col]);
     }
     pdl_wait_previous();
-    const float* part = p.part + (static_cast<size_t>(tile) * p.splits * PAIR_ROWS + r0) * PAIR_COLS + threadIdx.x;
+    const bool first = tile < p.split.tiles_a;
+    const int splits = first ? p.split.sa : p.split.sb;
+    const int part0 = first ? tile * splits : p.split.tiles_a * p.split.sa + (tile - p.split.tiles_a) * splits;
+    const float* part = p.part + (static_cast<size_t>(part0) * PAIR_ROWS + r0) * PAIR_COLS + threadIdx.x;
     float v[TAIL_ROWS], in[TAIL_ROWS];
 #pragma unroll
     for (int i = 0; i < TAIL_ROWS; ++i) {
         v[i] = __ldcs(part + i * PAIR_COLS);
         in[i] = e.in && i < rows ? Elem<T>::load(static_cast<const T*>(e.in)[(row + i) * e.ldin + col]) : 0.f;
     }
-    for (int s = 1; s < p.splits; ++s) {
+    for (int s = 1; s < splits; ++s) {
         part += static_cast<size_t>(PAIR_ROWS) * PAIR_COLS;
 #pragma unroll
         for (int i = 0; i < TAIL_ROWS; ++i) v[i] += __ldcs(part + i * PAIR_COLS);
@@ -724,6 +742,45 @@ __global__ void __launch_bounds__(PAIR_COLS) tail_sum_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < TAIL_ROWS; ++i)
         if (i < rows) static_cast<T*>(e.out)[(row + i) * e.ldout + col] = Elem<T>::store(v[i] + in[i]);
+}
+
+// 32 columns of a bias gradient: the blocks' sums, every eighth of them per warp, in order.
+constexpr int CS_COLS = 32, CS_LANES = FINISH_THREADS / CS_COLS;
+__device__ __forceinline__ void column_sum(const ColumnSumParams& p, int block) {
+    __shared__ float s[CS_LANES][CS_COLS];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int c = block * CS_COLS + x;
+    pdl_wait_previous();
+    float a = 0.f;
+    if (c < p.cols) {
+#pragma unroll 8
+        for (int b = y; b < p.blocks; b += CS_LANES) a += p.part[static_cast<size_t>(b) * p.cols + c];
+    }
+    s[y][x] = a;
+    __syncthreads();
+    if (y == 0 && c < p.cols) {
+        for (int k = 1; k < CS_LANES; ++k) a += s[k][x];
+        p.out[c] = p.accumulate ? p.out[c] + a : a;
+    }
+}
+
+// Everything that is added up after the products: one launch (T: type of 16-bit results).
+template <typename T>
+__global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const __grid_constant__ FinishParams p) {
+    pdl_allow_next();
+    int b = blockIdx.x;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const TailSumParams& t = p.tail[j];
+        const int blocks = t.tiles * TAIL_BLOCKS;
+        if (b < blocks) {
+            if (t.epi.out_f32) tail_sum<float>(t, b);
+            else tail_sum<T>(t, b);
+            return;
+        }
+        b -= blocks;
+    }
+    column_sum(p.bias, b);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -948,8 +1005,9 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
 
 // ---------------------------------------------------------------- around the products
 // Eight columns per thread; the last chunk of a row may be partial.
-__global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
-    pdl_wait_previous();
+__global__ void __launch_bounds__(256) repack_kernel(const RepackParams q) {
+    const Repack p = blockIdx.y ? q.job[1] : q.job[0];
+    pdl_wait_previous();  // (the product starts after this kernel: its shared memory would take the L1 that the loads need)
     const long long chunks = p.ldd / 8;
     const long long total = chunks * p.rows;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
@@ -1029,24 +1087,6 @@ __global__ void __launch_bounds__(32 * AG_LANES) act_grad_kernel(const ActGradPa
     }
 }
 
-constexpr int CS_LANES = 16;
-__global__ void __launch_bounds__(32 * CS_LANES) column_sum_kernel(const float* part, int blocks, int cols, float* out,
-                                                                  int accumulate) {
-    __shared__ float s[CS_LANES][32];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + x;
-    pdl_wait_previous();
-    float a = 0.f;
-    if (c < cols)
-        for (int b = y; b < blocks; b += CS_LANES) a += part[static_cast<size_t>(b) * cols + c];
-    s[y][x] = a;
-    __syncthreads();
-    if (y == 0 && c < cols) {
-        for (int k = 1; k < CS_LANES; ++k) a += s[k][x];
-        out[c] = accumulate ? out[c] + a : a;
-    }
-}
-
 template <typename T>
 cudaError_t run_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
@@ -1117,11 +1157,11 @@ cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t
     return p.f16 ? run_pair<__half>(p, sm_count, s) : run_pair<__nv_bfloat16>(p, sm_count, s);
 }
 
-cudaError_t launch_tail_sum(const TailSumParams& p, cudaStream_t s) {
-    const dim3 grid((p.tiles_r * p.tiles_c - p.whole) * (PAIR_ROWS / TAIL_ROWS));
-    if (p.epi.out_f32) return launch_pdl(tail_sum_kernel<float>, grid, dim3(PAIR_COLS), 0, s, p);
-    if (p.f16) return launch_pdl(tail_sum_kernel<__half>, grid, dim3(PAIR_COLS), 0, s, p);
-    return launch_pdl(tail_sum_kernel<__nv_bfloat16>, grid, dim3(PAIR_COLS), 0, s, p);
+cudaError_t launch_finish(const FinishParams& p, cudaStream_t s) {
+    const int bias = p.bias.out ? (p.bias.cols + CS_COLS - 1) / CS_COLS : 0;
+    const dim3 grid((p.tail[0].tiles + p.tail[1].tiles) * TAIL_BLOCKS + bias);
+    if (p.f16) return launch_pdl(finish_kernel<__half>, grid, dim3(FINISH_THREADS), 0, s, p);
+    return launch_pdl(finish_kernel<__nv_bfloat16>, grid, dim3(FINISH_THREADS), 0, s, p);
 }
 
 cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t s) {
@@ -1134,7 +1174,12 @@ cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t s) {
 }
 
 cudaError_t launch_repack(const RepackParams& p, cudaStream_t s) {
-    return launch_pdl(repack_kernel, dim3(blocks_for(p.ldd / 8 * p.rows)), dim3(256), 0, s, p);
+    long long most = 0;
+    for (int j = 0; j < p.jobs; ++j) {
+        const long long n = p.job[j].ldd / 8 * p.job[j].rows;
+        if (n > most) most = n;
+    }
+    return launch_pdl(repack_kernel, dim3(blocks_for(most), p.jobs), dim3(256), 0, s, p);
 }
 
 namespace {
@@ -1163,11 +1208,6 @@ cudaError_t run_act_grad(const ActGradParams& p, cudaStream_t s) {
 
 cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t s) {
     return p.f16 ? run_act_grad<__half>(p, s) : run_act_grad<__nv_bfloat16>(p, s);
-}
-
-cudaError_t launch_column_sum(const float* part, int blocks, int cols, float* out, int accumulate, cudaStream_t s) {
-    return launch_pdl(column_sum_kernel, dim3((cols + 31) / 32), dim3(32 * CS_LANES), 0, s, part, blocks, cols, out,
-                      accumulate);
 }
 
 }  // namespace anvil

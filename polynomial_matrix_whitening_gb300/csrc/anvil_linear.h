@@ -24,6 +24,15 @@ struct GemmEpilogue {
     int out_f32;          // out (and in) are fp32
 };
 
+// Which tiles are computed in one piece and which in parts.  The first `whole` tiles are
+// whole.  The others (the tail) are split along k, the first `tiles_a` of them into `sa` parts
+// of `kba` 64-deep k-blocks, the rest into `sb` of `kbb`; the fp32 parts go to scratch, a
+// 256 x 256 block each, in that order.  Of `pairs` CTA pairs the first `early` take the parts
+// of the first kind, the others those of the second.
+struct TileSplit {
+    int whole, pairs, early, tiles_a, sa, kba, sb, kbb;
+};
+
 // C [rows, cols] = sum_k A[row, k] B[col, k].  An operand is K-major (stored [row][k]) or
 // MN-major (stored [k][row]).
 struct PairGemmParams {
@@ -34,18 +43,29 @@ struct PairGemmParams {
     int f16;                        // operands are fp16 (else bf16)
     int in_tma, out_tma, z_tma;     // through tensor maps (16-byte aligned rows)
     int tiles_r, tiles_c;           // 256 x 256 output tiles
-    // The first `whole` tiles are computed in one piece; each of the others in `splits` along
-    // k, whose fp32 parts go to tm_part: [tail tile][split] blocks of 256 x 256.
-    int whole, splits, units;       // units = whole + tail tiles * splits
-    int kb_per_split;               // 64-deep k-blocks of a split
+    TileSplit split;
+    int units;                      // of work: whole tiles and the turns of the tail (unit_of)
+    int overlap_next;               // the next kernel may start before this one has ended
+    int overlap_previous;           // and this one before the previous one has (both products of a backward pass)
     unsigned* err;
 };
-// The sums of the tail tiles' parts, and the epilogue.
+// What is added up after the products, in one launch: the tail tiles' parts of up to two
+// products, with what follows the accumulator, and the column sums of a bias gradient.
 struct TailSumParams {
     GemmEpilogue epi;
     const float* part;
-    int rows, cols, tiles_r, tiles_c, whole, splits;
-    int f16;
+    int rows, cols, tiles_r, tiles_c, tiles;  // tiles: of the tail (0: nothing to do)
+    TileSplit split;
+};
+struct ColumnSumParams {
+    const float* part;  // [blocks][cols]
+    float* out;         // (+)= the sum over the blocks, in order (null: nothing to do)
+    int blocks, cols, accumulate;
+};
+struct FinishParams {
+    TailSumParams tail[2];
+    ColumnSumParams bias;
+    int f16;            // 16-bit results are fp16 (else bf16)
 };
 // A = the operand whose rows run along the output's contiguous dimension ("cols" above),
 // B = the few rows: out[b][a].
@@ -67,16 +87,21 @@ constexpr int ROW_TILE_A = 128;
 
 cudaError_t linear_prepare();
 cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t stream);
-cudaError_t launch_tail_sum(const TailSumParams& p, cudaStream_t stream);
+cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream);
 // bn: B's rows per block (16, 32, 64 or 128)
 cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t stream);
 
-// dst [rows, ldd] <- src [rows, cols] (row stride lds), 16-bit elements, ldd % 8 == 0.
-struct RepackParams {
+// dst [rows, ldd] <- src [rows, cols] (row stride lds), 16-bit elements, ldd % 8 == 0, for
+// one or two arrays.
+struct Repack {
     const uint16_t* src;
     uint16_t* dst;
     long long rows, lds, ldd;
     int cols;
+};
+struct RepackParams {
+    Repack job[2];
+    int jobs;
 };
 cudaError_t launch_repack(const RepackParams& p, cudaStream_t stream);
 
@@ -93,7 +118,5 @@ struct ActGradParams {
 };
 constexpr int ACT_GRAD_COLS = 256;  // columns per block
 cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream);
-// out[c] (+)= sum of part[b][c] over b, in order.
-cudaError_t launch_column_sum(const float* part, int blocks, int cols, float* out, int accumulate, cudaStream_t stream);
 
 }  // namespace anvil
