@@ -532,11 +532,11 @@ LinearGradLayout linear_grad_layout(const anvil_linear_grad_desc* d) {
     if (d->dx) at += copy_bytes(L.w);
     L.off_sum = at;
     if (L.prep) {
-        // about four blocks per SM over the whole array, at least 32 rows each
-        const int64_t cb = (d->n + ACT_GRAD_COLS - 1) / ACT_GRAD_COLS;
-        int64_t br = (4 * PLAN_SMS + cb - 1) / cb;
-        const int64_t most = (d->rows + 31) / 32;
+        // one turn of the blocks that the device holds at once, at least 32 rows each
+        const int64_t cb = ceil_div(d->n, ACT_GRAD_COLS), most = ceil_div(d->rows, 32);
+        int64_t br = ACT_GRAD_BLOCKS * PLAN_SMS / cb;
         if (br > most) br = most;
+        if (br < 1) br = 1;
         L.rows_per_block = static_cast<int>((d->rows + br - 1) / br);
         L.blocks_r = static_cast<int>((d->rows + L.rows_per_block - 1) / L.rows_per_block);
         if (d->dbias) at += align256(sizeof(float) * static_cast<size_t>(L.blocks_r) * d->n);

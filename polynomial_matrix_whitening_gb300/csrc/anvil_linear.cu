@@ -1025,7 +1025,7 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackParams q) {
 constexpr int AG_LANES = 8;   // rows at a time per block: 32 threads x 8 columns each
 constexpr int AG_UNROLL = 4;  // turns whose loads are in flight together
 template <typename T, int ACT, bool VEC>
-__global__ void __launch_bounds__(32 * AG_LANES) act_grad_kernel(const ActGradParams p) {
+__global__ void __launch_bounds__(32 * AG_LANES, ACT_GRAD_BLOCKS) act_grad_kernel(const ActGradParams p) {
     __shared__ float sums[AG_LANES][ACT_GRAD_COLS];
     constexpr bool Z = ACT != ACT_NONE;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;

@@ -117,6 +117,7 @@ struct ActGradParams {
     int rows_per_block, blocks_r;
 };
 constexpr int ACT_GRAD_COLS = 256;  // columns per block
+constexpr int ACT_GRAD_BLOCKS = 3;  // blocks that an SM holds
 cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream);
 
 }  // namespace anvil
