@@ -13,12 +13,13 @@
 // rate, not HBM, was the bound.
 //
 // The top k cost the pass one store a turn: every thread keeps the largest of its values of
-// each turn (32 values, fp32: 16) in shared memory.  The k-th largest of the 256 threads'
-// maxima is a value that at least k elements reach, and hardly more do; the few turns whose
-// maximum reaches it are read again (from L2), their elements that reach it are listed, and
-// each counts the entries ahead of it: its place.  A row with more such elements than the
-// list holds (many equal values) takes a slower walk that keeps, per warp, the best k in
-// order, one per lane.
+// each turn (32 values, fp32: 16) in shared memory.  The k-th largest of the 32 lanes' maxima
+// (over the warps) is a value that at least k elements reach, and hardly more do; the few
+// turns whose maximum reaches it are read again (from L2), their elements that reach it are
+// listed, and the entries ahead of each are counted: its place.  Where more elements reach it
+// than the list holds (many equal values, a masked row), the larger ones are listed and the
+// first of the equal ones; where the larger ones alone are too many (they share a few lanes),
+// every warp walks its elements in order and keeps the best k, one per lane.
 //
 // HBM bounds both passes where there are many rows; where rows are fewer than the SMs, a
 // cluster of up to eight blocks takes a row's segments and the first block joins their
@@ -127,31 +128,37 @@ __device__ __forceinline__ void top_offer(TopList& L, int top, int lane, bool ca
 constexpr int FWD_THREADS = 256;
 constexpr int FWD_WARPS = FWD_THREADS / 32;
 
-// The k-th largest of the block's FWD_THREADS keys, to 16 bits (below it where cut;
-// KEY_NONE where fewer than k threads have one).  Every warp finds it for itself.
+// An entry of the alternatives as one number, larger first: the key, then the lower index.
+// 0: none.
+__device__ __forceinline__ uint64_t entry_of(int key, int idx) {
+    return static_cast<uint64_t>(static_cast<uint32_t>(key) ^ 0x80000000u) << 32 | (0xffffffffu - static_cast<uint32_t>(idx));
+}
+__device__ __forceinline__ int entry_key(uint64_t e) { return static_cast<int>(static_cast<uint32_t>(e >> 32) ^ 0x80000000u); }
+__device__ __forceinline__ int entry_index(uint64_t e) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)); }
+
+// The k-th largest of the 32 lanes' keys, a lane's being the largest of its threads in all
+// warps (KEY_NONE where fewer than k lanes have one).  Every warp finds it for itself.
 __device__ __forceinline__ int kth_largest(const int* keys, int k, int lane) {
-    uint32_t u[FWD_WARPS];
+    int key = keys[lane];
 #pragma unroll
-    for (int w = 0; w < FWD_WARPS; ++w) u[w] = static_cast<uint32_t>(keys[w * 32 + lane]) ^ 0x80000000u;
-    uint32_t cut = 0;
-#pragma unroll 1
-    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
-        int n = 0;
+    for (int w = 1; w < FWD_WARPS; ++w) key = max(key, keys[w * 32 + lane]);
+    int place = 0;
 #pragma unroll
-        for (int w = 0; w < FWD_WARPS; ++w) n += u[w] >= (cut | bit);
-        if (__reduce_add_sync(0xffffffffu, n) >= k) cut |= bit;
+    for (int j = 0; j < 32; ++j) {
+        const int other = __shfl_sync(0xffffffffu, key, j);
+        place += other > key || (other == key && j < lane) ? 1 : 0;
     }
-    return static_cast<int>(cut ^ 0x80000000u);
+    return __shfl_sync(0xffffffffu, key, __ffs(__ballot_sync(0xffffffffu, place == k - 1)) - 1);
 }
 constexpr int UNROLL = 4;  // 16-byte loads in flight per thread
 constexpr int MAX_GROUPS = 16;  // groups of turns whose maxima a thread keeps
-// Listed elements: below k <= 32 threads with vectors there are at most 31 of them, with 32
-// values each, and the elements around the vectors.
+// Listed elements.  A block has a list at least for a run of so few vectors that fewer than
+// k <= 32 lanes have one: 31 vectors, and the elements around them.
 constexpr int TOP_LIST = 1024;
 
 struct BlockResult {
+    uint64_t best[LOGPROB_MAX_TOP];  // entries
     Stats st;
-    int key[LOGPROB_MAX_TOP], idx[LOGPROB_MAX_TOP];
 };
 
 // A maximum mx into the statistics: the first values, and then ever more rarely, raise m.
@@ -226,19 +233,24 @@ template <bool TOP>
 struct TopShared {
     int group_max[MAX_GROUPS][FWD_THREADS];  // keys
     int thread_max[FWD_THREADS];
-    int key[TOP_LIST], idx[TOP_LIST];
+    uint64_t list[TOP_LIST];  // entries
     int count;
 };
 template <>
 struct TopShared<false> {};
 
-// Place of entry (key, idx) among the first n listed.
-template <bool TOP>
-__device__ __forceinline__ int place_of(int key, int idx, const TopShared<TOP>& sh, int n) {
-    int place = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) place += better(sh.key[j], sh.idx[j], key, idx) ? 1 : 0;
-    return place;
+// The best `top` of n entries into their places: eight lanes count the entries ahead of one.
+__device__ __forceinline__ void place_best(const uint64_t* list, int n, uint64_t* best, int top, int tid) {
+    const int part = tid & 7;
+    for (int j0 = 0; j0 < n; j0 += FWD_THREADS / 8) {
+        const int j = j0 + tid / 8;
+        const uint64_t mine = j < n ? list[j] : 0;
+        int place = 0;
+        for (int i = part; i < n; i += 8) place += list[i] > mine ? 1 : 0;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+        if (mine && part == 0 && place < top) best[place] = mine;
+    }
 }
 
 template <typename T, bool TOP>
@@ -261,6 +273,14 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
     const int tail0 = head + nvec * E;
     const int per = (nvec + csize - 1) / csize;
     const int v0 = min(rank * per, nvec), v1 = min(v0 + per, nvec);
+
+    // the target's logit, on its way from the start
+    long long target = -1;
+    float at_target = 0.f;
+    if (p.logprob && tid == 0 && rank == 0) {
+        target = p.target64 ? static_cast<const long long*>(p.targets)[row] : static_cast<const int*>(p.targets)[row];
+        if (target >= 0 && target < p.vocab) at_target = Elem<T>::load(x[target]);
+    }
 
     Stats st = {-INFINITY, 0.f, 0.f};
     // at most E - 1 single elements of the head and of the tail, a lane each of warp 0
@@ -303,32 +323,25 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
     if constexpr (TOP) {
         top.thread_max[tid] = key_all;
         if (tid == 0) top.count = 0;
-        if (tid < LOGPROB_MAX_TOP) {
-            res.key[tid] = KEY_NONE;
-            res.idx[tid] = 0;
-        }
+        if (tid < LOGPROB_MAX_TOP) res.best[tid] = 0;
     }
     __syncthreads();
     if (warp == 0) st = join<FWD_WARPS>(wst[lane % FWD_WARPS]);
     if constexpr (TOP) {
         const int reach = kth_largest(top.thread_max, p.top, lane);
-        auto list = [&](float v, int i) {
-            const int key = order_key(v);
-            if (key != KEY_NONE && key >= reach) {
-                const int at = atomicAdd(&top.count, 1);
-                if (at < TOP_LIST) {
-                    top.key[at] = key;
-                    top.idx[at] = i;
+        // lists what reaches `least`
+        auto list_from = [&](int least) {
+            if (warp == 0 && lane < nh + nt) {
+                const int i = lane < nh ? lane : tail0 + lane - nh;
+                const int key = order_key(Elem<T>::load(x[i]));
+                if (key >= least) {
+                    const int at = atomicAdd(&top.count, 1);
+                    if (at < TOP_LIST) top.list[at] = entry_of(key, i);
                 }
             }
-        };
-        if (warp == 0 && lane < nh + nt) {
-            const int i = lane < nh ? lane : tail0 + lane - nh;
-            list(Elem<T>::load(x[i]), i);
-        }
-        if (key_all >= reach && mine < v1) {
+            if (key_all < least || mine >= v1) return;
             for (int g = 0; g < group; ++g) {
-                if (top.group_max[g][tid] < reach) continue;
+                if (top.group_max[g][tid] < least) continue;
                 for (int t = 0; t < per_group; ++t) {
                     const int at = mine + (g * per_group + t) * TURN;
                     uint4 raw[UNROLL];
@@ -340,17 +353,74 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
                         // (a list that is full already is not what the place is found by)
                         if (at + u * 32 >= v1 || *static_cast<volatile int*>(&top.count) > TOP_LIST) break;
                         const uint32_t m = Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w));
-                        if (order_key(Elem<T>::word_max(m)) < reach) continue;
+                        if (order_key(Elem<T>::word_max(m)) < least) continue;
                         float v[E];
                         Elem<T>::unpack(raw[u], v);
+                        unsigned which = 0;
 #pragma unroll
-                        for (int e = 0; e < E; ++e) list(v[e], head + (at + u * 32) * E + e);
+                        for (int e = 0; e < E; ++e) which |= order_key(v[e]) >= least ? 1u << e : 0u;
+                        const int to = atomicAdd(&top.count, __popc(which));
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const int i = to + __popc(which & ((1u << e) - 1u));
+                            if ((which >> e & 1u) && i < TOP_LIST)
+                                top.list[i] = entry_of(order_key(v[e]), head + (at + u * 32) * E + e);
+                        }
                     }
                 }
             }
-        }
+        };
+        list_from(reach);
         __syncthreads();
         int n = top.count;
+        if (n > TOP_LIST) {
+            // many equal values (a masked row): the larger ones, and of the equal ones the first
+            // by index, up to k per warp and turn, until there are k
+            __syncthreads();
+            if (tid == 0) top.count = 0;
+            __syncthreads();
+            list_from(reach + 1);
+            __syncthreads();
+            n = top.count;
+            if (n + (FWD_WARPS + 2) * LOGPROB_MAX_TOP <= TOP_LIST) {
+                __syncthreads();
+                if (warp == 0 && lane < nh + nt) {
+                    const int i = lane < nh ? lane : tail0 + lane - nh;
+                    if (order_key(Elem<T>::load(x[i])) == reach) top.list[atomicAdd(&top.count, 1)] = entry_of(reach, i);
+                }
+                int equal = 0;  // listed by the turns
+                for (int base = v0; base < v1 && equal < p.top; base += TURN) {
+                    const int at = mine + (base - v0);
+                    int before = 0;  // equal values of the warp's earlier vectors
+#pragma unroll 1
+                    for (int u = 0; u < UNROLL && before < p.top; ++u) {
+                        unsigned which = 0;
+                        if (at + u * 32 < v1) {
+                            float v[E];
+                            Elem<T>::unpack(xv[at + u * 32], v);
+#pragma unroll
+                            for (int e = 0; e < E; ++e) which |= order_key(v[e]) == reach ? 1u << e : 0u;
+                        }
+                        const int mine_n = __popc(which);
+                        int upto = mine_n;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int left = __shfl_up_sync(0xffffffffu, upto, o);
+                            if (lane >= o) upto += left;
+                        }
+                        int place = before + upto - mine_n;
+                        for (; which && place < p.top; which &= which - 1, ++place)
+                            top.list[atomicAdd(&top.count, 1)] = entry_of(reach, head + (at + u * 32) * E + __ffs(which) - 1);
+                        before += __shfl_sync(0xffffffffu, upto, 31);
+                    }
+                    equal += __syncthreads_count(lane < min(before, p.top));
+                }
+                __syncthreads();
+                n = top.count;
+            } else {
+                n = TOP_LIST + 1;
+            }
+        }
         if (n > TOP_LIST) {
             // too many to list: every warp walks its elements again, its best in order, and the
             // lists become the entries
@@ -394,20 +464,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
             if (tid == 0) top.count = 0;
             __syncthreads();
             if (lane < p.top && L.key != KEY_NONE) {
-                const int at = atomicAdd(&top.count, 1);
-                top.key[at] = L.key;
-                top.idx[at] = L.idx;
+                top.list[atomicAdd(&top.count, 1)] = entry_of(L.key, L.idx);
             }
             __syncthreads();
             n = top.count;
         }
-        for (int j = tid; j < n; j += FWD_THREADS) {
-            const int place = place_of(top.key[j], top.idx[j], top, n);
-            if (place < p.top) {
-                res.key[place] = top.key[j];
-                res.idx[place] = top.idx[j];
-            }
-        }
+        place_best(top.list, n, res.best, p.top, tid);
         __syncthreads();
     }
     if (csize > 1) {
@@ -417,7 +479,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
         if (rank == 0) {
             if (warp == 0) {
                 // eight lanes, four times over: the cluster's blocks (8 at most, a power of two)
-                const uint32_t a = map_to_rank(&res, lane % csize);
+                const uint32_t a = map_to_rank(&res.st, lane % csize);
                 Stats b;
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(a) : "memory");
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(a + 4) : "memory");
@@ -427,25 +489,14 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
             }
             if constexpr (TOP) {
                 // the blocks' results are the entries: warp w takes those of block w
-                int k = KEY_NONE, i = INT32_MAX;
                 if (warp < csize && lane < p.top) {
-                    const uint32_t a = map_to_rank(&res, warp);
-                    const uint32_t ak = a + offsetof(BlockResult, key) + 4 * lane, ai = a + offsetof(BlockResult, idx) + 4 * lane;
-                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(k) : "r"(ak) : "memory");
-                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(i) : "r"(ai) : "memory");
-                }
-                if (warp < csize && lane < p.top) {
-                    top.key[warp * p.top + lane] = k;
-                    top.idx[warp * p.top + lane] = k == KEY_NONE ? INT32_MAX : i;
+                    const uint32_t a = map_to_rank(&res.best[lane], warp);
+                    uint64_t e;
+                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(e) : "r"(a) : "memory");
+                    top.list[warp * p.top + lane] = e;
                 }
                 __syncthreads();
-                if (k != KEY_NONE) {
-                    const int place = place_of(k, i, top, csize * p.top);
-                    if (place < p.top) {
-                        res.key[place] = k;
-                        res.idx[place] = i;
-                    }
-                }
+                place_best(top.list, csize * p.top, res.best, p.top, tid);
                 __syncthreads();
             }
         }
@@ -460,17 +511,16 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
         if (p.lse) p.lse[row] = lse;
         if (p.entropy) p.entropy[row] = none ? 0.f : ls - LN2 * (st.q / st.s);
         if (p.logprob) {
-            const long long t = p.target64 ? static_cast<const long long*>(p.targets)[row]
-                                           : static_cast<const int*>(p.targets)[row];
             float lp = 0.f;  // a negative target: a position that does not count
-            if (t >= p.vocab) lp = __int_as_float(0x7fc00000);  // no such token
-            else if (t >= 0) lp = none ? -INFINITY : (Elem<T>::load(x[t]) - st.m) - ls;
+            if (target >= p.vocab) lp = __int_as_float(0x7fc00000);  // no such token
+            else if (target >= 0) lp = none ? -INFINITY : (at_target - st.m) - ls;
             p.logprob[row] = lp;
         }
     }
     if (TOP && lane < p.top) {
-        p.top_index[row * p.top + lane] = res.idx[lane];
-        p.top_logprob[row * p.top + lane] = none ? -INFINITY : (key_value(res.key[lane]) - st.m) - ls;
+        const uint64_t e = res.best[lane];
+        p.top_index[row * p.top + lane] = entry_index(e);
+        p.top_logprob[row * p.top + lane] = none ? -INFINITY : (key_value(entry_key(e)) - st.m) - ls;
     }
 }
 

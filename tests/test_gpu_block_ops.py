@@ -448,6 +448,34 @@ def test_logprob_ties_and_signed_zero(A):
     assert ti[3].tolist() == [2990] + list(range(19)) and torch.isinf(tv[3, 1:]).all() and float(tv[3, 0]) == 0.0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows", [1, 400])
+def test_logprob_top_of_uneven_rows(A, rows, dtype):
+    """More candidates than a list holds: few distinct values, a few valid tokens, the large values all in one
+    lane's vectors."""
+    vocab = 40007
+    x = torch.full((rows, vocab), -2.0, device="cuda", dtype=DT[dtype])
+    col = torch.arange(vocab, device="cuda")
+    unit = 16 // x.element_size()
+    kinds = [torch.where(col % 3 == 1, 1.0, -1.0),                                             # two values
+             torch.where((col > 30000) & (col < 30007), 0.25 * (col % 4), -math.inf),          # six tokens, with ties
+             torch.where(col // unit % 32 == 5, (col * 7919 % 20011 - 10005) / 1024.0, -20.0),  # one lane in 32
+             torch.where(col == vocab - 1, 3.0, torch.where(col == 0, 2.0, 0.0)),              # the ends of the row
+             torch.where(col // unit % 32 == 9, 5.0, -20.0 + (col % 64) / 64.0)]               # equal values in one lane
+    for r in range(rows):
+        x[r] = kinds[r % 5]
+    for k, off in enumerate((0, 1, 3)):  # three alignments
+        y = x[:, off:]
+        for top in (1, 8, 32):
+            _, _, _, tv, ti = A.token_logprobs(y, top=top)
+            val, idx = torch.sort(y.double(), dim=1, descending=True, stable=True)
+            assert torch.equal(ti.long(), idx[:, :top]), (off, top)
+    for kind in kinds:  # and alone
+        y = kind.to(DT[dtype])[None]
+        _, idx = torch.sort(y.double(), dim=1, descending=True, stable=True)
+        assert torch.equal(A.token_logprobs(y, top=20)[4].long(), idx[:, :20])
+
+
 def test_logprob_bad_rows_and_targets(A):
     x = randn(1, 6, 1000)
     x[1, 10], x[2, 20] = math.nan, math.inf
