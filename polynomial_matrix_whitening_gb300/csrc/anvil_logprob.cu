@@ -26,10 +26,12 @@
 // results through distributed shared memory, in a fixed order.
 //
 // A row in which every logit is -inf has no distribution: lse and the log probabilities
-// are -inf, the entropy is 0 and the gradient is zero.  A masked logit (-inf, or so low
-// that the difference overflows) adds nothing: where a chunk's sum of e y comes out NaN,
-// from 0 times infinity, the chunk is taken again with the exponents held at -200 (in base
-// 2), where e is 0.  A NaN or +inf makes its row NaN.
+// are -inf, the entropy is 0 and the gradient is zero.  A masked logit (-inf, or the type's
+// lowest value) adds nothing: the forward pass takes values below -1e30 as that (fp16: -inf as
+// the lowest value), which keeps e y = 0 without a test; a row whose maximum, or whose k-th
+// value, is not far above that is taken again value by value.  The gradient, where a vector's
+// sum of e y comes out NaN, from 0 times infinity, takes the vector again with the exponents
+// held at -200 (in base 2), where e is 0.  A NaN or +inf makes its row NaN.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stddef.h>
@@ -151,14 +153,31 @@ __device__ __forceinline__ int kth_largest(const int* keys, int k, int lane) {
     return __shfl_sync(0xffffffffu, key, __ffs(__ballot_sync(0xffffffffu, place == k - 1)) - 1);
 }
 constexpr int UNROLL = 4;  // 16-byte loads in flight per thread
+constexpr int TURN = FWD_THREADS * UNROLL;  // vectors of a block's turn: each warp a run of 32 * UNROLL
 constexpr int MAX_GROUPS = 16;  // groups of turns whose maxima a thread keeps
-// Listed elements.  A block has a list at least for a run of so few vectors that fewer than
-// k <= 32 lanes have one: 31 vectors, and the elements around them.
+// Listed elements, and threads' groups to be read again.  A block has room at least for a run
+// of so few vectors that fewer than k <= 32 lanes have one: 31 vectors, and the elements
+// around them.
 constexpr int TOP_LIST = 1024;
 
 struct BlockResult {
     uint64_t best[LOGPROB_MAX_TOP];  // entries
     Stats st;
+};
+
+// A block's share of a row: whole vectors v0 to v1 of those from the row's first 16-byte
+// boundary on, `head` elements in; and `nh` elements before and `nt` after all the vectors
+// (fewer than a vector each, together a lane each of warp 0).
+template <typename T>
+struct Share {
+    const T* x;
+    int head, tail0, nh, nt, v0, v1;
+    __device__ __forceinline__ const uint4* vectors() const { return reinterpret_cast<const uint4*>(x + head); }
+    __device__ __forceinline__ int first(int tid) const { return v0 + (tid >> 5) * 32 * UNROLL + (tid & 31); }
+    __device__ __forceinline__ int turns() const { return (v1 - v0 + TURN - 1) / TURN; }
+    __device__ __forceinline__ int per_group() const { return (turns() + MAX_GROUPS - 1) / MAX_GROUPS; }
+    __device__ __forceinline__ bool edge(int tid) const { return tid < nh + nt; }
+    __device__ __forceinline__ int edge_index(int tid) const { return tid < nh ? tid : tail0 + tid - nh; }
 };
 
 // A maximum mx into the statistics: the first values, and then ever more rarely, raise m.
@@ -180,13 +199,13 @@ __device__ __forceinline__ void take_one(Stats& st, float v) {
     st.s += e;
     st.q = fmaf(e, y, st.q);
 }
-// The first `cnt` of N vectors of values, none above st.m.  The difference comes before the factor log2 e: a
-// maximum of the type's lowest value (a row masked with it) times log2 e would overflow.
+// The first `cnt` of N vectors of values, none above st.m, none so far below it that the
+// difference overflows.  The difference comes before the factor log2 e: a maximum of the type's
+// lowest value (a row masked with it) times log2 e would overflow.
 template <typename T, int N>
 __device__ __forceinline__ void take(Stats& st, const uint4 (&raw)[N], int cnt) {
     constexpr int E = Elem<T>::VEC;
-    const float m0 = st.m == -INFINITY ? 0.f : st.m;
-    const uint64_t nm = f2_make(-m0, -m0), l2e = f2_make(LOG2E, LOG2E);
+    const uint64_t nm = f2_make(-st.m, -st.m), l2e = f2_make(LOG2E, LOG2E);
     uint64_t s2 = 0, q2 = 0;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
@@ -206,26 +225,8 @@ __device__ __forceinline__ void take(Stats& st, const uint4 (&raw)[N], int cnt) 
     float s, q, sh, qh;
     f2_split(s2, &s, &sh);
     f2_split(q2, &q, &qh);
-    s += sh;
-    q += qh;
-    if (q != q) {
-        s = q = 0.f;
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            if (u >= cnt) break;
-            float v[E];
-            Elem<T>::unpack(raw[u], v);
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float y = max_nan((v[i] - m0) * LOG2E, -200.f);
-                const float e = ex2(y);
-                s += e;
-                q = fmaf(e, y, q);
-            }
-        }
-    }
-    st.s += s;
-    st.q += q;
+    st.s += s + sh;
+    st.q += q + qh;
 }
 
 // Shared memory of the top k (none without them).
@@ -234,10 +235,184 @@ struct TopShared {
     int group_max[MAX_GROUPS][FWD_THREADS];  // keys
     int thread_max[FWD_THREADS];
     uint64_t list[TOP_LIST];  // entries
-    int count;
+    uint16_t again[TOP_LIST];  // groups to be read again: 256 * group + thread
+    int count, agains;
 };
 template <>
 struct TopShared<false> {};
+
+// The statistics and the threads' maxima of a share whose values are not the common ones: in
+// rows where nothing, or fewer than k values, are above what `not_below` makes of the masked
+// ones, or where differences overflow.
+template <typename T, bool TOP>
+__device__ __noinline__ Stats exact_stats(const Share<T> sh, TopShared<TOP>& top, int tid) {
+    constexpr int E = Elem<T>::VEC;
+    Stats st = {-INFINITY, 0.f, 0.f};
+    if (sh.edge(tid)) take_one(st, Elem<T>::load(sh.x[sh.edge_index(tid)]));
+    int key_all = KEY_NONE, key_group = KEY_NONE, in_group = 0, group = 0;
+#pragma unroll 1
+    for (int base = sh.v0; base < sh.v1; base += TURN) {
+        const int at = sh.first(tid) + (base - sh.v0);
+        uint4 raw[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            if (at + u * 32 < sh.v1) raw[u] = sh.vectors()[at + u * 32];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            if (at + u * 32 >= sh.v1) break;
+            float v[E], mx;
+            Elem<T>::unpack(raw[u], v);
+            mx = v[0];
+#pragma unroll
+            for (int i = 1; i < E; ++i) mx = fmaxf(mx, v[i]);
+            raise_max(st, mx);
+            const float m0 = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float y = max_nan((v[i] - m0) * LOG2E, -200.f), e = ex2(y);
+                st.s += e;
+                st.q = fmaf(e, y, st.q);
+            }
+            if (TOP) key_group = max(key_group, order_key(mx));
+        }
+        if constexpr (TOP) {
+            key_all = max(key_all, key_group);
+            if (++in_group == sh.per_group() || base + TURN >= sh.v1) {
+                top.group_max[group++][tid] = key_group;
+                key_group = KEY_NONE;
+                in_group = 0;
+            }
+        }
+    }
+    if constexpr (TOP) top.thread_max[tid] = key_all;
+    return st;
+}
+
+// Lists the share's elements that reach `least` (by the whole block; the list and `again` start
+// empty).  Their number, or more than TOP_LIST where they may not all be listed.
+template <typename T>
+__device__ __forceinline__ int list_from(const Share<T>& sh, int least, TopShared<true>& top, int tid) {
+    constexpr int E = Elem<T>::VEC;
+    if (sh.edge(tid)) {
+        const int i = sh.edge_index(tid), key = order_key(Elem<T>::load(sh.x[i]));
+        if (key >= least) top.list[atomicAdd(&top.count, 1)] = entry_of(key, i);
+    }
+    const int per = sh.per_group();
+    if (top.thread_max[tid] >= least) {
+        for (int g = 0; g * per < sh.turns(); ++g) {
+            if (top.group_max[g][tid] < least) continue;
+            const int at = atomicAdd(&top.agains, 1);
+            if (at < TOP_LIST) top.again[at] = static_cast<uint16_t>(g * FWD_THREADS + tid);
+        }
+    }
+    __syncthreads();
+    const int agains = top.agains, each = per * UNROLL;
+    if (agains > TOP_LIST) return TOP_LIST + 1;
+    for (int j = tid; j < agains * each; j += FWD_THREADS) {
+        const int which_group = j / each, r = j - which_group * each;
+        const int code = top.again[which_group];
+        const int vec = sh.first(code % FWD_THREADS) + (code / FWD_THREADS * per + r / UNROLL) * TURN + r % UNROLL * 32;
+        // (a list that is full already is not what the place is found by)
+        if (vec >= sh.v1 || *static_cast<volatile int*>(&top.count) > TOP_LIST) continue;
+        float v[E];
+        Elem<T>::unpack(sh.vectors()[vec], v);
+        unsigned which = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) which |= order_key(v[e]) >= least ? 1u << e : 0u;
+        if (!which) continue;
+        const int to = atomicAdd(&top.count, __popc(which));
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = to + __popc(which & ((1u << e) - 1u));
+            if ((which >> e & 1u) && i < TOP_LIST) top.list[i] = entry_of(order_key(v[e]), sh.head + vec * E + e);
+        }
+    }
+    __syncthreads();
+    return top.count;
+}
+
+// More elements reach the threshold `reach` than the list holds.  Many equal values (a masked
+// row): the larger ones, and of the equal ones the first by index, up to k per warp and turn,
+// until there are k.  Or the larger ones alone are too many: every warp walks its elements, its
+// best k in order, and the lists become the entries.  The number of entries.
+template <typename T>
+__device__ __noinline__ int list_many(const Share<T> sh, int k, int reach, TopShared<true>& top, int tid) {
+    constexpr int E = Elem<T>::VEC;
+    const int lane = tid & 31;
+    const uint4* xv = sh.vectors();
+    __syncthreads();
+    if (tid == 0) top.count = top.agains = 0;
+    __syncthreads();
+    const int larger = list_from(sh, reach + 1, top, tid);
+    __syncthreads();
+    if (larger + (FWD_WARPS + 2) * LOGPROB_MAX_TOP <= TOP_LIST) {
+        if (sh.edge(tid)) {
+            const int i = sh.edge_index(tid);
+            if (order_key(Elem<T>::load(sh.x[i])) == reach) top.list[atomicAdd(&top.count, 1)] = entry_of(reach, i);
+        }
+        int equal = 0;  // listed by the turns
+        for (int base = sh.v0; base < sh.v1 && equal < k; base += TURN) {
+            int before = 0;  // equal values of the warp's earlier vectors
+#pragma unroll 1
+            for (int u = 0; u < UNROLL && before < k; ++u) {
+                const int at = sh.first(tid) + (base - sh.v0) + u * 32;
+                unsigned which = 0;
+                if (at < sh.v1) {
+                    float v[E];
+                    Elem<T>::unpack(xv[at], v);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) which |= order_key(v[e]) == reach ? 1u << e : 0u;
+                }
+                const int mine = __popc(which);
+                int upto = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int left = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += left;
+                }
+                for (int place = before + upto - mine; which && place < k; which &= which - 1, ++place)
+                    top.list[atomicAdd(&top.count, 1)] = entry_of(reach, sh.head + at * E + __ffs(which) - 1);
+                before += __shfl_sync(0xffffffffu, upto, 31);
+            }
+            equal += __syncthreads_count(lane < min(before, k));
+        }
+        __syncthreads();
+        return top.count;
+    }
+    TopList L;
+    top_init(L);
+    for (int base = sh.v0; base < sh.v1; base += TURN) {
+        const int at = sh.first(tid) + (base - sh.v0);
+        // indexes grow from turn to turn and from one row of vectors to the next: an equal
+        // value never displaces, and what holds no larger one is passed over
+#pragma unroll 1
+        for (int u = 0; u < UNROLL; ++u) {
+            const int vec = at + u * 32;
+            float v[E];
+            int most = KEY_NONE;
+            if (vec < sh.v1) {
+                Elem<T>::unpack(xv[vec], v);
+#pragma unroll
+                for (int e = 0; e < E; ++e) most = max(most, order_key(v[e]));
+            }
+            if (!__any_sync(0xffffffffu, most > L.kth_key)) continue;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                top_offer(L, k, lane, vec < sh.v1, vec < sh.v1 ? order_key(v[e]) : KEY_NONE, sh.head + vec * E + e);
+        }
+    }
+    if (tid < 32) {
+        const bool in = sh.edge(tid);
+        const int i = sh.edge_index(tid);
+        top_offer(L, k, lane, in, in ? order_key(Elem<T>::load(sh.x[i])) : KEY_NONE, i);
+    }
+    __syncthreads();
+    if (tid == 0) top.count = 0;
+    __syncthreads();
+    if (lane < k && L.key != KEY_NONE) top.list[atomicAdd(&top.count, 1)] = entry_of(L.key, L.idx);
+    __syncthreads();
+    return top.count;
+}
 
 // The best `top` of n entries into their places: eight lanes count the entries ahead of one.
 __device__ __forceinline__ void place_best(const uint64_t* list, int n, uint64_t* best, int top, int tid) {
@@ -270,9 +445,15 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
     const int head = min(mis ? E - mis : 0, p.vocab);
     const int nvec = (p.vocab - head) / E;
-    const int tail0 = head + nvec * E;
     const int per = (nvec + csize - 1) / csize;
-    const int v0 = min(rank * per, nvec), v1 = min(v0 + per, nvec);
+    Share<T> sh;
+    sh.x = x;
+    sh.head = head;
+    sh.tail0 = head + nvec * E;
+    sh.v0 = min(rank * per, nvec);
+    sh.v1 = min(sh.v0 + per, nvec);
+    sh.nh = rank == 0 ? head : 0;
+    sh.nt = rank == csize - 1 ? p.vocab - sh.tail0 : 0;
 
     // the target's logit, on its way from the start
     long long target = -1;
@@ -282,35 +463,34 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
         if (target >= 0 && target < p.vocab) at_target = Elem<T>::load(x[target]);
     }
 
+    constexpr uint32_t LOW = Elem<T>::LOW;
     Stats st = {-INFINITY, 0.f, 0.f};
-    // at most E - 1 single elements of the head and of the tail, a lane each of warp 0
-    const int nh = rank == 0 ? head : 0, nt = rank == csize - 1 ? p.vocab - tail0 : 0;
-    if (warp == 0 && lane < nh + nt) take_one(st, Elem<T>::load(x[lane < nh ? lane : tail0 + lane - nh]));
-    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-    // A warp's UNROLL vectors per lane are one run of 32 * UNROLL vectors.
-    constexpr int TURN = FWD_THREADS * UNROLL;
-    const int mine = v0 + warp * 32 * UNROLL + lane;  // this thread's first vector
-    const int per_group = ((v1 - v0 + TURN - 1) / TURN + MAX_GROUPS - 1) / MAX_GROUPS;  // turns
+    if (sh.edge(tid)) take_one(st, Elem<T>::load(x[sh.edge_index(tid)]));
+    const uint4* xv = sh.vectors();
+    const int mine = sh.first(tid), per_group = sh.per_group();
     int key_all = KEY_NONE, key_group = KEY_NONE, in_group = 0, group = 0;
-    for (int base = v0; base < v1; base += TURN) {
-        const int at = mine + (base - v0);
+    for (int base = sh.v0; base < sh.v1; base += TURN) {
+        const int at = mine + (base - sh.v0);
         uint4 raw[UNROLL];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-            raw[u] = at + u * 32 < v1 ? __ldcs(xv + at + u * 32)
-                                      : make_uint4(Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF, Elem<T>::NEG_INF);
-        uint32_t mw = raw[0].x;
+        for (int u = 0; u < UNROLL; ++u) raw[u] = at + u * 32 < sh.v1 ? __ldcs(xv + at + u * 32) : make_uint4(LOW, LOW, LOW, LOW);
+        uint32_t mw = LOW;
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
+        for (int u = 0; u < UNROLL; ++u) {
+            raw[u].x = Elem<T>::not_below(raw[u].x);
+            raw[u].y = Elem<T>::not_below(raw[u].y);
+            raw[u].z = Elem<T>::not_below(raw[u].z);
+            raw[u].w = Elem<T>::not_below(raw[u].w);
             mw = Elem<T>::max_word(mw, Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w)));
+        }
         const float mx = Elem<T>::word_max(mw);
         raise_max(st, mx);
-        take<T, UNROLL>(st, raw, (v1 - at + 31) / 32);  // vectors at + 32 u < v1
+        take<T, UNROLL>(st, raw, (sh.v1 - at + 31) / 32);  // vectors at + 32 u < v1
         if constexpr (TOP) {
-            const int key = at < v1 ? order_key(mx) : KEY_NONE;
+            const int key = at < sh.v1 ? order_key(mx) : KEY_NONE;
             key_group = key > key_group ? key : key_group;
             key_all = key > key_all ? key : key_all;
-            if (++in_group == per_group || base + TURN >= v1) {
+            if (++in_group == per_group || base + TURN >= sh.v1) {
                 top.group_max[group++][tid] = key_group;
                 key_group = KEY_NONE;
                 in_group = 0;
@@ -322,153 +502,27 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
     if (lane == 0) wst[warp] = st;
     if constexpr (TOP) {
         top.thread_max[tid] = key_all;
-        if (tid == 0) top.count = 0;
+        if (tid == 0) top.count = top.agains = 0;
         if (tid < LOGPROB_MAX_TOP) res.best[tid] = 0;
     }
     __syncthreads();
-    if (warp == 0) st = join<FWD_WARPS>(wst[lane % FWD_WARPS]);
-    if constexpr (TOP) {
-        const int reach = kth_largest(top.thread_max, p.top, lane);
-        // lists what reaches `least`
-        auto list_from = [&](int least) {
-            if (warp == 0 && lane < nh + nt) {
-                const int i = lane < nh ? lane : tail0 + lane - nh;
-                const int key = order_key(Elem<T>::load(x[i]));
-                if (key >= least) {
-                    const int at = atomicAdd(&top.count, 1);
-                    if (at < TOP_LIST) top.list[at] = entry_of(key, i);
-                }
-            }
-            if (key_all < least || mine >= v1) return;
-            for (int g = 0; g < group; ++g) {
-                if (top.group_max[g][tid] < least) continue;
-                for (int t = 0; t < per_group; ++t) {
-                    const int at = mine + (g * per_group + t) * TURN;
-                    uint4 raw[UNROLL];
-#pragma unroll
-                    for (int u = 0; u < UNROLL; ++u)
-                        if (at + u * 32 < v1) raw[u] = xv[at + u * 32];
-#pragma unroll
-                    for (int u = 0; u < UNROLL; ++u) {
-                        // (a list that is full already is not what the place is found by)
-                        if (at + u * 32 >= v1 || *static_cast<volatile int*>(&top.count) > TOP_LIST) break;
-                        const uint32_t m = Elem<T>::max_word(Elem<T>::max_word(raw[u].x, raw[u].y), Elem<T>::max_word(raw[u].z, raw[u].w));
-                        if (order_key(Elem<T>::word_max(m)) < least) continue;
-                        float v[E];
-                        Elem<T>::unpack(raw[u], v);
-                        unsigned which = 0;
-#pragma unroll
-                        for (int e = 0; e < E; ++e) which |= order_key(v[e]) >= least ? 1u << e : 0u;
-                        const int to = atomicAdd(&top.count, __popc(which));
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const int i = to + __popc(which & ((1u << e) - 1u));
-                            if ((which >> e & 1u) && i < TOP_LIST)
-                                top.list[i] = entry_of(order_key(v[e]), head + (at + u * 32) * E + e);
-                        }
-                    }
-                }
-            }
-        };
-        list_from(reach);
+    st = join<FWD_WARPS>(wst[lane % FWD_WARPS]);
+    int reach = KEY_NONE;
+    if constexpr (TOP) reach = kth_largest(top.thread_max, p.top, lane);
+    // Above these the values at LOW add nothing, exactly, and no difference overflows.
+    constexpr float LEAST = sizeof(T) == 2 && LOW == Elem<__half>::LOW ? -65000.f : -9e29f;
+    const bool common = st.m > LEAST && st.m < 1e38f && (!TOP || reach == KEY_NONE || key_value(reach) > LEAST);
+    if (!common && sh.v0 < sh.v1) {
         __syncthreads();
-        int n = top.count;
-        if (n > TOP_LIST) {
-            // many equal values (a masked row): the larger ones, and of the equal ones the first
-            // by index, up to k per warp and turn, until there are k
-            __syncthreads();
-            if (tid == 0) top.count = 0;
-            __syncthreads();
-            list_from(reach + 1);
-            __syncthreads();
-            n = top.count;
-            if (n + (FWD_WARPS + 2) * LOGPROB_MAX_TOP <= TOP_LIST) {
-                __syncthreads();
-                if (warp == 0 && lane < nh + nt) {
-                    const int i = lane < nh ? lane : tail0 + lane - nh;
-                    if (order_key(Elem<T>::load(x[i])) == reach) top.list[atomicAdd(&top.count, 1)] = entry_of(reach, i);
-                }
-                int equal = 0;  // listed by the turns
-                for (int base = v0; base < v1 && equal < p.top; base += TURN) {
-                    const int at = mine + (base - v0);
-                    int before = 0;  // equal values of the warp's earlier vectors
-#pragma unroll 1
-                    for (int u = 0; u < UNROLL && before < p.top; ++u) {
-                        unsigned which = 0;
-                        if (at + u * 32 < v1) {
-                            float v[E];
-                            Elem<T>::unpack(xv[at + u * 32], v);
-#pragma unroll
-                            for (int e = 0; e < E; ++e) which |= order_key(v[e]) == reach ? 1u << e : 0u;
-                        }
-                        const int mine_n = __popc(which);
-                        int upto = mine_n;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const int left = __shfl_up_sync(0xffffffffu, upto, o);
-                            if (lane >= o) upto += left;
-                        }
-                        int place = before + upto - mine_n;
-                        for (; which && place < p.top; which &= which - 1, ++place)
-                            top.list[atomicAdd(&top.count, 1)] = entry_of(reach, head + (at + u * 32) * E + __ffs(which) - 1);
-                        before += __shfl_sync(0xffffffffu, upto, 31);
-                    }
-                    equal += __syncthreads_count(lane < min(before, p.top));
-                }
-                __syncthreads();
-                n = top.count;
-            } else {
-                n = TOP_LIST + 1;
-            }
-        }
-        if (n > TOP_LIST) {
-            // too many to list: every warp walks its elements again, its best in order, and the
-            // lists become the entries
-            TopList L;
-            top_init(L);
-            for (int base = v0; base < v1; base += TURN) {
-                const int at = mine + (base - v0);
-                // indexes grow from turn to turn and from one row of vectors to the next: an equal
-                // value never displaces, and what holds no larger one is passed over
-                uint32_t mw = Elem<T>::NEG_INF;
-#pragma unroll
-                for (int u = 0; u < UNROLL; ++u) {
-                    if (at + u * 32 < v1) {
-                        const uint4 r = xv[at + u * 32];
-                        mw = Elem<T>::max_word(mw, Elem<T>::max_word(Elem<T>::max_word(r.x, r.y), Elem<T>::max_word(r.z, r.w)));
-                    }
-                }
-                if (!__any_sync(0xffffffffu, at < v1 && order_key(Elem<T>::word_max(mw)) > L.kth_key)) continue;
-#pragma unroll 1
-                for (int u = 0; u < UNROLL; ++u) {
-                    const int vec = at + u * 32;
-                    float v[E];
-                    int most = KEY_NONE;
-                    if (vec < v1) {
-                        Elem<T>::unpack(xv[vec], v);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) most = max(most, order_key(v[e]));
-                    }
-                    if (!__any_sync(0xffffffffu, most > L.kth_key)) continue;
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        top_offer(L, p.top, lane, vec < v1, vec < v1 ? order_key(v[e]) : KEY_NONE, head + vec * E + e);
-                }
-            }
-            if (warp == 0) {
-                const bool in = lane < nh + nt;
-                const int i = lane < nh ? lane : tail0 + lane - nh;
-                top_offer(L, p.top, lane, in, in ? order_key(Elem<T>::load(x[i])) : KEY_NONE, i);
-            }
-            __syncthreads();
-            if (tid == 0) top.count = 0;
-            __syncthreads();
-            if (lane < p.top && L.key != KEY_NONE) {
-                top.list[atomicAdd(&top.count, 1)] = entry_of(L.key, L.idx);
-            }
-            __syncthreads();
-            n = top.count;
-        }
+        st = join<32>(exact_stats<T, TOP>(sh, top, tid));
+        if (lane == 0) wst[warp] = st;
+        __syncthreads();
+        st = join<FWD_WARPS>(wst[lane % FWD_WARPS]);
+        if constexpr (TOP) reach = kth_largest(top.thread_max, p.top, lane);
+    }
+    if constexpr (TOP) {
+        int n = list_from(sh, reach, top, tid);
+        if (n > TOP_LIST) n = list_many(sh, p.top, reach, top, tid);
         place_best(top.list, n, res.best, p.top, tid);
         __syncthreads();
     }

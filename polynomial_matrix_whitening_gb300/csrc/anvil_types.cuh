@@ -29,7 +29,14 @@ struct Elem;
 template <>
 struct Elem<float> {
     static constexpr int VEC = 4;  // elements in 16 bytes
-    static constexpr uint32_t NEG_INF = 0xff800000u;  // a 32-bit word of -inf values
+    // a word of a very low value (-1e30, fp16: the lowest), and the word's values held to it
+    // from below (NaN stays)
+    static constexpr uint32_t LOW = 0xf1490000u;
+    static __device__ __forceinline__ uint32_t not_below(uint32_t w) {
+        uint32_t d;
+        asm("max.NaN.f32 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(LOW));
+        return d;
+    }
     // the larger of two words' values, NaN ignored
     static __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
         return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
@@ -61,7 +68,12 @@ struct Elem<float> {
 template <>
 struct Elem<__nv_bfloat16> {
     static constexpr int VEC = 8;
-    static constexpr uint32_t NEG_INF = 0xff80ff80u;
+    static constexpr uint32_t LOW = 0xf149f149u;
+    static __device__ __forceinline__ uint32_t not_below(uint32_t w) {
+        uint32_t d;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(LOW));
+        return d;
+    }
     static __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
         uint32_t d;
         asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -113,7 +125,12 @@ struct Elem<__nv_bfloat16> {
 template <>
 struct Elem<__half> {
     static constexpr int VEC = 8;
-    static constexpr uint32_t NEG_INF = 0xfc00fc00u;
+    static constexpr uint32_t LOW = 0xfbfffbffu;
+    static __device__ __forceinline__ uint32_t not_below(uint32_t w) {
+        uint32_t d;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(LOW));
+        return d;
+    }
     static __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
         uint32_t d;
         asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
