@@ -136,6 +136,22 @@ struct Here {
     }
 };
 
+// Small results of 4-byte values that share one allocation (an allocation costs the host about
+// a microsecond, as much as the smallest kernels).
+struct Together {
+    at::Tensor all;
+    int64_t used = 0;
+    Together(int64_t values, const Here& here) : all(here.empty({values}, at::kFloat)) {}
+    at::Tensor next(at::IntArrayRef sizes, at::ScalarType type, int64_t values) {
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                                c10::scalarTypeToTypeMeta(type));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+        t.unsafeGetTensorImpl()->set_storage_offset(used);
+        used += values;
+        return t;
+    }
+};
+
 // A call's scratch: the caller's, or a new one (kept until the call is queued).
 struct Scratch {
     at::Tensor keep;
@@ -214,7 +230,8 @@ PyObject* layernorm_forward(PyObject* const* a) {
     const Here here("layernorm_forward", {&x, weight, bias, out});
     at::Tensor y = result(out, x.sizes(), type, "x's shape and type", &d.ldy, here);
     const auto lead = x.sizes().slice(0, x.dim() - 1);
-    at::Tensor mean = here.empty(lead, at::kFloat), rstd = here.empty(lead, at::kFloat);
+    Together stats(2 * r.rows, here);
+    at::Tensor mean = stats.next(lead, at::kFloat, r.rows), rstd = stats.next(lead, at::kFloat, r.rows);
     d.x = x.data_ptr();
     d.y = y.data_ptr();
     d.mean = static_cast<float*>(mean.data_ptr());
@@ -424,16 +441,18 @@ PyObject* token_logprobs(PyObject* const* a) {
     d.targets = targets_of(t, r.rows, &d.targets_int64);
     const Here here("token_logprobs", {&x, t});
     const auto lead = x.sizes().slice(0, x.dim() - 1);
-    at::Tensor lse = here.empty(lead, at::kFloat), ent = here.empty(lead, at::kFloat), lp, tv, ti;
+    const int64_t best = r.rows * top;
+    Together results((t ? 3 : 2) * r.rows + 2 * best, here);
+    at::Tensor lse = results.next(lead, at::kFloat, r.rows), ent = results.next(lead, at::kFloat, r.rows), lp, tv, ti;
     if (t) {
-        lp = here.empty(lead, at::kFloat);
+        lp = results.next(lead, at::kFloat, r.rows);
         d.logprob = static_cast<float*>(lp.data_ptr());
     }
     if (top) {
         c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
         shape.back() = top;
-        tv = here.empty(shape, at::kFloat);
-        ti = here.empty(shape, at::kInt);
+        tv = results.next(shape, at::kFloat, best);
+        ti = results.next(shape, at::kInt, best);
         d.top_logprob = static_cast<float*>(tv.data_ptr());
         d.top_index = static_cast<int32_t*>(ti.data_ptr());
     }
