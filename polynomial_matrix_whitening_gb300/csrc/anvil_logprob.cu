@@ -38,6 +38,7 @@
 #include <stdint.h>
 
 #include "anvil_device.cuh"
+#include "anvil_internal.h"
 #include "anvil_logprob.h"
 #include "anvil_types.cuh"
 
@@ -455,6 +456,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 6) logprob_fwd_kernel(const Logpr
     sh.nh = rank == 0 ? head : 0;
     sh.nt = rank == csize - 1 ? p.vocab - sh.tail0 : 0;
 
+    pdl_wait_previous();  // (the next kernel starts after this one: its blocks, spread by what is free, would be uneven)
     // the target's logit, on its way from the start
     long long target = -1;
     float at_target = 0.f;
@@ -633,6 +635,8 @@ __global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobG
     const int seg = blockIdx.x % segs;
     const T* x = static_cast<const T*>(p.logits) + row * p.ld;
     T* dx = static_cast<T*>(p.dlogits) + row * p.ldd;
+    pdl_allow_next();
+    pdl_wait_previous();
     GradRow r;
     r.lse = p.lse[row];
     const bool none = r.lse == -INFINITY;  // no distribution: the gradient is zero
@@ -698,25 +702,26 @@ __global__ void __launch_bounds__(BWD_THREADS) logprob_bwd_kernel(const LogprobG
 template <typename T, bool TOP>
 cudaError_t run_fwd(const LogprobParams& p, int csize, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = csize;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = csize;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows * csize));
     cfg.blockDim = dim3(FWD_THREADS);
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = csize > 1 ? 1 : 0;
+    cfg.numAttrs = csize > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, logprob_fwd_kernel<T, TOP>, p, csize);
 }
 
 template <typename T>
 cudaError_t run_bwd(const LogprobGradParams& p, int segs, cudaStream_t s) {
     const unsigned blocks = static_cast<unsigned>(p.rows * segs);
-    if (p.grad_entropy) logprob_bwd_kernel<T, true><<<blocks, BWD_THREADS, 0, s>>>(p, segs);
-    else logprob_bwd_kernel<T, false><<<blocks, BWD_THREADS, 0, s>>>(p, segs);
-    return cudaGetLastError();
+    return launch_pdl(p.grad_entropy ? logprob_bwd_kernel<T, true> : logprob_bwd_kernel<T, false>, dim3(blocks), dim3(BWD_THREADS), 0,
+                      s, p, segs);
 }
 
 }  // namespace

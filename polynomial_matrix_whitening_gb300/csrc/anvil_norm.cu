@@ -154,6 +154,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, fwd_blocks_pe
     const float inv_n = 1.f / static_cast<float>(p.width);
     constexpr int P = Raw::P;
     using F = typename Raw::F;
+    pdl_allow_next();
+    pdl_wait_previous();
     F w[NV][P], b[NV][P];
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
@@ -248,6 +250,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
     using F = typename Raw::F;
     constexpr int NA = SUMS_SMEM ? 1 : NV;
     F aw[NA][P], ab[NA][P], wv[NA][P];
+    pdl_allow_next();
+    pdl_wait_previous();
     if constexpr (SUMS_SMEM) {
 #pragma unroll
         for (int u = 0; u < NV; ++u)
@@ -594,6 +598,8 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
             if (p.res) cover_load(dst + 2 * slot, res, row_bytes, bar);
         }
     };
+    pdl_allow_next();
+    pdl_wait_previous();
     if (team.t == 0)
         for (int s = 0; s < stages && r0 + s < r1; ++s) issue(r0 + s, s);
     RowStats st;
@@ -764,6 +770,8 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
         mbar_arrive_expect_tx(bar, row_bytes);
         bulk_load(smem_u32(mine + s * row_bytes), static_cast<const T*>(p.x) + row * p.ldx, row_bytes, bar);
     };
+    pdl_allow_next();
+    pdl_wait_previous();
     if (team.t == 0)
         for (int s = 0; s < stages && r0 + s < r1; ++s) issue(r0 + s, s);
     const float inv_n = 1.f / static_cast<float>(p.width);
@@ -874,6 +882,7 @@ __global__ void __launch_bounds__(32 * GRAD_LANES) norm_grads_kernel(const NormB
     const int x = threadIdx.x & 31, yy = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + x;
     float* out = blockIdx.y ? p.dbias : p.dweight;
+    pdl_allow_next();
     if (!out) return;
     pdl_wait_previous();
     float a = 0.f;
@@ -899,8 +908,7 @@ cudaError_t run_fwd(const NormFwdParams& p, cudaStream_t s) {
     using S = Shape<T, VEC, TPR, NV>;
     const long long want = (p.rows + S::TEAMS - 1) / S::TEAMS;
     const long long cap = 152ll * fwd_blocks_per_sm(TPR, NV * S::E);  // one wave of resident blocks
-    norm_fwd_kernel<T, W, VEC, TPR, NV><<<static_cast<unsigned>(want < cap ? want : cap), S::THREADS, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(norm_fwd_kernel<T, W, VEC, TPR, NV>, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(S::THREADS), 0, s, p);
 }
 
 template <typename T, typename W, bool VEC, int TPR, int NV, bool SUMS_SMEM = false>
@@ -913,8 +921,7 @@ cudaError_t run_bwd(const NormBwdParams& p, cudaStream_t s) {
                                                    2 * sizeof(float) * S::CAP);
         if (e) return e;
     }
-    kernel<<<p.blocks, S::THREADS, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(kernel, dim3(p.blocks), dim3(S::THREADS), smem, s, p);
 }
 
 // The narrowest team that holds the row, 8 to 16 columns a thread: fewer threads per row
@@ -1005,8 +1012,7 @@ cudaError_t run_ring(K kernel, const P& p, bool vec, int tpr, int arrays, int bl
     if (smem < sums) smem = sums;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(tpr));
     if (e) return e;
-    kernel<<<blocks, ring_threads(tpr), smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(kernel, dim3(blocks), dim3(ring_threads(tpr)), smem, s, p);
 }
 
 template <typename T, typename W>
