@@ -534,6 +534,12 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const T* row, int width, 
     }
 }
 
+// After a wait that gave up: the copies of `rows` rows into `stages` stages, waited for once
+// more before the block's shared memory goes away.
+__device__ __forceinline__ void drain(uint64_t* full, int stages, long long rows, unsigned* err) {
+    for (int s = 0; s < stages && s < rows; ++s) mbar_wait(&full[s], static_cast<uint32_t>((rows - 1 - s) / stages) & 1u, err);
+}
+
 // One row's statistics per lane, 32 rows at a time, the next 32 on their way.
 struct RowStats {
     float mean, rstd, mean_n, rstd_n;
@@ -703,6 +709,7 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
             Raw::put(dp + u * TPR * E, d);
         }
     }
+    if (dead) drain(full[team.id], stages, r1 - r0, p.err);
     if (!p.dweight && !p.dbias) return;
     // the block's column sums, team by team in order, in the ring (every copy has been read)
     float* cols = reinterpret_cast<float*>(ring);
@@ -872,6 +879,7 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
             }
         }
     }
+    if (dead) drain(full[team.id], stages, r1 - r0, p.err);
 }
 
 // dweight (blockIdx.y = 0) and dbias (1): 32 columns per block, 16 threads down each, the
@@ -1005,14 +1013,13 @@ bool ring_plan(long long rows, int width, int dtype, bool vec, int arrays, int* 
 }
 
 template <typename K, typename P>
-cudaError_t run_ring(K kernel, const P& p, bool vec, int tpr, int arrays, int blocks, cudaStream_t s) {
-    const int slot = ring_slot(vec, p.width * dtype_size(p.dtype));
-    size_t smem = static_cast<size_t>(ring_teams(tpr)) * ring_stages(tpr, arrays, slot) * arrays * slot;
-    const size_t sums = arrays > 1 ? 2 * sizeof(float) * p.width : 0;  // the column sums reuse the ring
-    if (smem < sums) smem = sums;
+cudaError_t run_ring(K kernel, const P& p, int tpr, int blocks, cudaStream_t s) {
+    // All of a block's share of the shared memory, used or not: no SM takes a third block of the
+    // next launch while this one's are leaving, which would leave another SM with one (32768 x
+    // 2816 bf16 forward 91 us instead of 71).  The column sums reuse the ring.
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(tpr));
     if (e) return e;
-    return launch_pdl(kernel, dim3(blocks), dim3(ring_threads(tpr)), smem, s, p);
+    return launch_pdl(kernel, dim3(blocks), dim3(ring_threads(tpr)), ring_bytes(tpr), s, p);
 }
 
 template <typename T, typename W>
@@ -1020,12 +1027,12 @@ cudaError_t pick_fwd_ring(const NormFwdParams& p, int blocks, cudaStream_t s) {
     constexpr int NV = 16 / Elem<T>::VEC;
     const int tpr = ring_tpr(p.width, 1, true);
     switch (tpr) {
-        case 32: return run_ring(norm_fwd_ring_kernel<T, W, 32, NV>, p, true, tpr, 1, blocks, s);
-        case 64: return run_ring(norm_fwd_ring_kernel<T, W, 64, NV>, p, true, tpr, 1, blocks, s);
-        case 128: return run_ring(norm_fwd_ring_kernel<T, W, 128, NV>, p, true, tpr, 1, blocks, s);
-        case 192: return run_ring(norm_fwd_ring_kernel<T, W, 192, NV>, p, true, tpr, 1, blocks, s);
-        case 256: return run_ring(norm_fwd_ring_kernel<T, W, 256, NV>, p, true, tpr, 1, blocks, s);
-        default: return run_ring(norm_fwd_ring_kernel<T, W, 512, NV>, p, true, tpr, 1, blocks, s);
+        case 32: return run_ring(norm_fwd_ring_kernel<T, W, 32, NV>, p, tpr, blocks, s);
+        case 64: return run_ring(norm_fwd_ring_kernel<T, W, 64, NV>, p, tpr, blocks, s);
+        case 128: return run_ring(norm_fwd_ring_kernel<T, W, 128, NV>, p, tpr, blocks, s);
+        case 192: return run_ring(norm_fwd_ring_kernel<T, W, 192, NV>, p, tpr, blocks, s);
+        case 256: return run_ring(norm_fwd_ring_kernel<T, W, 256, NV>, p, tpr, blocks, s);
+        default: return run_ring(norm_fwd_ring_kernel<T, W, 512, NV>, p, tpr, blocks, s);
     }
 }
 template <typename T, typename W>
@@ -1034,20 +1041,20 @@ cudaError_t pick_bwd_ring(const NormBwdParams& p, cudaStream_t s) {
     const int arrays = p.res ? 3 : 2, tpr = ring_tpr(p.width, arrays, p.vec != 0);
     if (!p.vec) {
         switch (tpr) {
-            case 64: return run_ring(norm_bwd_ring_kernel<T, W, false, 64, 8>, p, false, tpr, arrays, p.blocks, s);
-            case 128: return run_ring(norm_bwd_ring_kernel<T, W, false, 128, 8>, p, false, tpr, arrays, p.blocks, s);
+            case 64: return run_ring(norm_bwd_ring_kernel<T, W, false, 64, 8>, p, tpr, p.blocks, s);
+            case 128: return run_ring(norm_bwd_ring_kernel<T, W, false, 128, 8>, p, tpr, p.blocks, s);
             case 256:
-                return p.width <= 2048 ? run_ring(norm_bwd_ring_kernel<T, W, false, 256, 8>, p, false, tpr, arrays, p.blocks, s)
-                                       : run_ring(norm_bwd_ring_kernel<T, W, false, 256, 16>, p, false, tpr, arrays, p.blocks, s);
-            default: return run_ring(norm_bwd_ring_kernel<T, W, false, 512, 16>, p, false, tpr, arrays, p.blocks, s);
+                return p.width <= 2048 ? run_ring(norm_bwd_ring_kernel<T, W, false, 256, 8>, p, tpr, p.blocks, s)
+                                       : run_ring(norm_bwd_ring_kernel<T, W, false, 256, 16>, p, tpr, p.blocks, s);
+            default: return run_ring(norm_bwd_ring_kernel<T, W, false, 512, 16>, p, tpr, p.blocks, s);
         }
     }
     switch (tpr) {
-        case 32: return run_ring(norm_bwd_ring_kernel<T, W, true, 32, NV>, p, true, tpr, arrays, p.blocks, s);
-        case 64: return run_ring(norm_bwd_ring_kernel<T, W, true, 64, NV>, p, true, tpr, arrays, p.blocks, s);
-        case 128: return run_ring(norm_bwd_ring_kernel<T, W, true, 128, NV>, p, true, tpr, arrays, p.blocks, s);
-        case 256: return run_ring(norm_bwd_ring_kernel<T, W, true, 256, NV>, p, true, tpr, arrays, p.blocks, s);
-        default: return run_ring(norm_bwd_ring_kernel<T, W, true, 512, NV>, p, true, tpr, arrays, p.blocks, s);
+        case 32: return run_ring(norm_bwd_ring_kernel<T, W, true, 32, NV>, p, tpr, p.blocks, s);
+        case 64: return run_ring(norm_bwd_ring_kernel<T, W, true, 64, NV>, p, tpr, p.blocks, s);
+        case 128: return run_ring(norm_bwd_ring_kernel<T, W, true, 128, NV>, p, tpr, p.blocks, s);
+        case 256: return run_ring(norm_bwd_ring_kernel<T, W, true, 256, NV>, p, tpr, p.blocks, s);
+        default: return run_ring(norm_bwd_ring_kernel<T, W, true, 512, NV>, p, tpr, p.blocks, s);
     }
 }
 
