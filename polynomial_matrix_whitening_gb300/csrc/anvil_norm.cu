@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, fwd_blocks_pe
 
 // The column sums of a thread: in registers, or (SUMS_SMEM, rows over 8192 wide, whose
 // sums would take more registers than the SM has) in shared memory, which no other thread
-// of the block touches; such a block reads its weights for every row.
+// of the block touches; such a block reads its weights for every row.  4096 x 16384 bf16: 146
+// us (sums laid out by column, a lane's eight neighbours: 319, the banks' conflicts).
 template <typename T, typename W, bool VEC, int TPR, int NV, bool SUMS_SMEM>
 __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_per_sm(TPR)) norm_bwd_kernel(const NormBwdParams p) {
     using S = Shape<T, VEC, TPR, NV>;
@@ -252,14 +253,15 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
     F aw[NA][P], ab[NA][P], wv[NA][P];
     pdl_allow_next();
     pdl_wait_previous();
+    // SUMS_SMEM: the thread's sums of unit u, pair i at own[(u * P + i) * TPR]: neighbouring lanes
+    // at neighbouring addresses
+    struct alignas(2 * sizeof(F)) Sums {
+        F w, b;
+    };
+    Sums* own = reinterpret_cast<Sums*>(cols) + t;
     if constexpr (SUMS_SMEM) {
 #pragma unroll
-        for (int u = 0; u < NV; ++u)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int c = (t + u * TPR) * E + e;
-                if (c < p.width) cols[c] = cols[p.width + c] = 0.f;
-            }
+        for (int i = 0; i < NV * P; ++i) own[i * TPR] = {p_all<F>(0.f), p_all<F>(0.f)};
     } else {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
@@ -325,7 +327,6 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             if (!in[u]) break;
-            const int c = (t + u * TPR) * E;
             F f[P], h[P], g[P];
             xr[u].get(h);
             gr[u].get(g);
@@ -334,14 +335,10 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
             for (int i = 0; i < P; ++i) {
                 h[i] = p_mul(p_add(h[i], nm), rs);
                 if constexpr (SUMS_SMEM) {
-                    float hv[2], gv[2];
-                    p_split(h[i], hv);
-                    p_split(g[i], gv);
-#pragma unroll
-                    for (int k = 0; k < E / P; ++k) {
-                        cols[c + i * (E / P) + k] += gv[k] * hv[k];
-                        cols[p.width + c + i * (E / P) + k] += gv[k];
-                    }
+                    Sums q = own[(u * P + i) * TPR];
+                    q.w = p_fma(g[i], h[i], q.w);
+                    q.b = p_add(q.b, g[i]);
+                    own[(u * P + i) * TPR] = q;
                 } else {
                     aw[u][i] = p_fma(g[i], h[i], aw[u][i]);
                     ab[u][i] = p_add(ab[u][i], g[i]);
@@ -386,16 +383,14 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
     }
     if (!p.dweight && !p.dbias) return;
     // the block's column sums: team 0's registers, then every other team's in turn
-    float cw[SUMS_SMEM ? 1 : NV][E], cb[SUMS_SMEM ? 1 : NV][E];
-    if constexpr (!SUMS_SMEM) {
+    float cw[NV][E], cb[NV][E];
 #pragma unroll
-        for (int u = 0; u < NV; ++u)
+    for (int u = 0; u < NV; ++u)
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                p_split(aw[u][i], &cw[u][i * (E / P)]);
-                p_split(ab[u][i], &cb[u][i * (E / P)]);
-            }
-    }
+        for (int i = 0; i < P; ++i) {
+            p_split(SUMS_SMEM ? own[(u * P + i) * TPR].w : aw[SUMS_SMEM ? 0 : u][i], &cw[u][i * (E / P)]);
+            p_split(SUMS_SMEM ? own[(u * P + i) * TPR].b : ab[SUMS_SMEM ? 0 : u][i], &cb[u][i * (E / P)]);
+        }
     if constexpr (S::TEAMS > 1) {
         for (int k = 1; k < S::TEAMS; ++k) {
             __syncthreads();
@@ -435,8 +430,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
         for (int e = 0; e < E; ++e) {
             const int c = (t + u * TPR) * E + e;
             if (c < p.width) {
-                if (p.dweight) pw[c] = SUMS_SMEM ? cols[c] : cw[SUMS_SMEM ? 0 : u][e];
-                if (p.dbias) pb[c] = SUMS_SMEM ? cols[p.width + c] : cb[SUMS_SMEM ? 0 : u][e];
+                if (p.dweight) pw[c] = cw[u][e];
+                if (p.dbias) pb[c] = cb[u][e];
             }
         }
 }
@@ -923,7 +918,7 @@ template <typename T, typename W, bool VEC, int TPR, int NV, bool SUMS_SMEM = fa
 cudaError_t run_bwd(const NormBwdParams& p, cudaStream_t s) {
     using S = Shape<T, VEC, TPR, NV>;
     auto kernel = norm_bwd_kernel<T, W, VEC, TPR, NV, SUMS_SMEM>;
-    const size_t smem = S::TEAMS > 1 || SUMS_SMEM ? 2 * sizeof(float) * p.width : 0;
+    const size_t smem = SUMS_SMEM ? 2 * sizeof(float) * S::CAP : S::TEAMS > 1 ? 2 * sizeof(float) * p.width : 0;
     if (SUMS_SMEM) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    2 * sizeof(float) * S::CAP);
