@@ -209,7 +209,9 @@ void plan_few(int64_t rows, int cols, int64_t kb, double epilogue, Plan* p) {
             if (s > 1 && (per * (s - 1) >= kb || tiles * s > PLAN_SMS)) break;  // every split has work
             const double turns = static_cast<double>(ceil_div(tiles * s, PLAN_SMS));
             const double finish = s == 1 ? 28.0 * columns : 2500.0 + 10.0 * bn + 60.0 * columns / s;
-            const double cost = turns * (per * 545.0 + 1700.0 + finish);
+            // (two blocks of up to 32 tokens share an SM: one's start and end beside the other's products)
+            const double ends = turns > 1 && bn <= ROW_TWO_TOKENS ? 0.5 * turns : turns;
+            const double cost = turns * per * 545.0 + ends * (1700.0 + finish);
             if (p->cost == 0 || cost < p->cost) {
                 p->cost = cost;
                 p->few = true;
@@ -359,7 +361,7 @@ anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, c
         g.splits = plan.splits;
         g.kb_per_split = plan.kb;
         g.err = dev->err;
-        e = profiled(ANVIL_KERNEL_LINEAR_PRODUCT, s, [&] { return launch_row_gemm(g, plan.bn, s); });
+        e = profiled(ANVIL_KERNEL_LINEAR_PRODUCT, s, [&] { return launch_row_gemm(g, plan.bn, dev->sm_count, s); });
         return e ? cuda_fail(e, "linear product launch") : ANVIL_OK;
     }
     PairGemmParams g;

@@ -790,9 +790,13 @@ template <int BN>
 struct RowShape {
     static constexpr int STAGE = A_STAGE + BN * 128;
     static constexpr int STAGES = BN <= 64 ? 8 : 6;
-    static constexpr int SMEM = STAGES * STAGE + 1024;
+    // Two blocks per SM where there are more blocks than SMs: one's first loads and last stores
+    // run beside the other's products (1 x 50304 x 768: 17.3 us, 20.6 with one; from 64 tokens
+    // on the fewer stages cost more than that gives, 24 against 21).
+    static constexpr int STAGES_OF_TWO = 110 * 1024 / STAGE;
+    static constexpr int smem(int stages) { return stages * STAGE + 1024; }
     static constexpr uint32_t TMEM_COLS = BN < 32 ? 32 : BN;
-    static_assert(BN * ROW_TILE_A * 4 <= STAGES * STAGE, "the partial accumulator reuses the stages");
+    static_assert(BN * ROW_TILE_A * 4 <= STAGES * STAGE && STAGES_OF_TWO < STAGES, "the partial accumulator reuses the stages");
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
@@ -829,7 +833,7 @@ __device__ __forceinline__ void finish_rows(const GemmEpilogue& e, float (&v)[N]
 }
 
 template <typename T, int BN>
-__global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_constant__ RowGemmParams p) {
+__global__ void __launch_bounds__(ROW_THREADS, 2) row_gemm_kernel(const __grid_constant__ RowGemmParams p) {
     using S = RowShape<BN>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[S::STAGES];
@@ -847,6 +851,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
     const int all = (p.k + GEMM_BK - 1) / GEMM_BK;
     const int kb0 = split * p.kb_per_split;
     const int nkb = max(0, min(p.kb_per_split, all - kb0));
+    const int stages = p.stages;
     uint8_t* smem =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     if (threadIdx.x == 0) {
@@ -872,8 +877,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
         if (lane == 0) {
             const int mine = warp == 0 ? 0 : warp - 5;
             for (int it = mine; it < nkb; it += ROW_PRODUCERS) {
-                const int s = it % S::STAGES;
-                if (!mbar_wait(&empty_bar[s], ((it / S::STAGES) & 1) ^ 1, p.err)) {
+                const int s = it % stages;
+                if (!mbar_wait(&empty_bar[s], ((it / stages) & 1) ^ 1, p.err)) {
                     aborted = 1;
                     break;
                 }
@@ -910,7 +915,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
                 for (int kk = 0; kk < GEMM_BK / 16; ++kk)
                     umma_bf16(tmem, sw128_desc(a_lo + kk * a_step), sw128_desc(b_lo + kk * (32 >> 4)), idesc,
                               (it | kk) != 0 ? 1u : 0u);
-                const int s_next = s + 1 == S::STAGES ? 0 : s + 1;
+                const int s_next = s + 1 == stages ? 0 : s + 1;
                 const uint32_t ph_next = s_next == 0 ? ph ^ 1u : ph;
                 ready = mbar_test_wait(smem_u32(&full_bar[s_next]), ph_next);
                 umma_commit(&empty_bar[s]);
@@ -995,8 +1000,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 1) row_gemm_kernel(const __grid_c
     __syncthreads();
     if (aborted && threadIdx.x == 0) {
         // the loads in flight land before the shared memory goes away
-        for (int s = 0; s < S::STAGES; ++s)
-            if (armed[s]) mbar_wait(&full_bar[s], ((armed[s] - 1) / S::STAGES) & 1, p.err);
+        for (int s = 0; s < stages; ++s)
+            if (armed[s]) mbar_wait(&full_bar[s], ((armed[s] - 1) / stages) & 1, p.err);
     }
     __syncthreads();
     tc_fence_after();
@@ -1108,7 +1113,7 @@ cudaError_t run_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
 }
 
 template <typename T, int BN>
-cudaError_t run_row(const RowGemmParams& p, cudaStream_t s) {
+cudaError_t run_row(RowGemmParams p, int sm_count, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1119,7 +1124,9 @@ cudaError_t run_row(const RowGemmParams& p, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((p.na + ROW_TILE_A - 1) / ROW_TILE_A * p.splits, (p.nb + BN - 1) / BN);
     cfg.blockDim = dim3(ROW_THREADS);
-    cfg.dynamicSmemBytes = RowShape<BN>::SMEM;
+    const bool more = BN <= ROW_TWO_TOKENS && static_cast<long long>(cfg.gridDim.x) * cfg.gridDim.y > sm_count;
+    p.stages = more ? RowShape<BN>::STAGES_OF_TWO : RowShape<BN>::STAGES;
+    cfg.dynamicSmemBytes = RowShape<BN>::smem(p.stages);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = p.splits > 1 ? 2 : 1;
@@ -1140,14 +1147,14 @@ cudaError_t linear_prepare() {
     ANVIL_SMEM(pair_gemm_kernel<__nv_bfloat16>, PAIR_SMEM);
     ANVIL_SMEM(pair_gemm_kernel<__half>, PAIR_SMEM);
     ANVIL_SMEM(pair_gemm_kernel<float>, PAIR_SMEM);
-    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 16>), RowShape<16>::SMEM);
-    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 32>), RowShape<32>::SMEM);
-    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 64>), RowShape<64>::SMEM);
-    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 128>), RowShape<128>::SMEM);
-    ANVIL_SMEM((row_gemm_kernel<__half, 16>), RowShape<16>::SMEM);
-    ANVIL_SMEM((row_gemm_kernel<__half, 32>), RowShape<32>::SMEM);
-    ANVIL_SMEM((row_gemm_kernel<__half, 64>), RowShape<64>::SMEM);
-    ANVIL_SMEM((row_gemm_kernel<__half, 128>), RowShape<128>::SMEM);
+    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 16>), RowShape<16>::smem(RowShape<16>::STAGES));
+    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 32>), RowShape<32>::smem(RowShape<32>::STAGES));
+    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 64>), RowShape<64>::smem(RowShape<64>::STAGES));
+    ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 128>), RowShape<128>::smem(RowShape<128>::STAGES));
+    ANVIL_SMEM((row_gemm_kernel<__half, 16>), RowShape<16>::smem(RowShape<16>::STAGES));
+    ANVIL_SMEM((row_gemm_kernel<__half, 32>), RowShape<32>::smem(RowShape<32>::STAGES));
+    ANVIL_SMEM((row_gemm_kernel<__half, 64>), RowShape<64>::smem(RowShape<64>::STAGES));
+    ANVIL_SMEM((row_gemm_kernel<__half, 128>), RowShape<128>::smem(RowShape<128>::STAGES));
 #undef ANVIL_SMEM
     return cudaSuccess;
 }
@@ -1164,12 +1171,12 @@ cudaError_t launch_finish(const FinishParams& p, cudaStream_t s) {
     return launch_pdl(finish_kernel<__nv_bfloat16>, grid, dim3(FINISH_THREADS), 0, s, p);
 }
 
-cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t s) {
+cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, int sm_count, cudaStream_t s) {
     switch (bn) {
-        case 16: return p.f16 ? run_row<__half, 16>(p, s) : run_row<__nv_bfloat16, 16>(p, s);
-        case 32: return p.f16 ? run_row<__half, 32>(p, s) : run_row<__nv_bfloat16, 32>(p, s);
-        case 64: return p.f16 ? run_row<__half, 64>(p, s) : run_row<__nv_bfloat16, 64>(p, s);
-        default: return p.f16 ? run_row<__half, 128>(p, s) : run_row<__nv_bfloat16, 128>(p, s);
+        case 16: return p.f16 ? run_row<__half, 16>(p, sm_count, s) : run_row<__nv_bfloat16, 16>(p, sm_count, s);
+        case 32: return p.f16 ? run_row<__half, 32>(p, sm_count, s) : run_row<__nv_bfloat16, 32>(p, sm_count, s);
+        case 64: return p.f16 ? run_row<__half, 64>(p, sm_count, s) : run_row<__nv_bfloat16, 64>(p, sm_count, s);
+        default: return p.f16 ? run_row<__half, 128>(p, sm_count, s) : run_row<__nv_bfloat16, 128>(p, sm_count, s);
     }
 }
 

@@ -76,6 +76,7 @@ struct RowGemmParams {
     int a_mn;                       // A MN-major (B is always K-major)
     int f16;
     int splits;                     // cluster size along k
+    int stages;                     // of the ring (set by the launcher)
     int kb_per_split;
     unsigned* err;
 };
@@ -83,13 +84,14 @@ struct RowGemmParams {
 constexpr int GEMM_BK = 64;    // k-block: one 128-byte swizzle row of 16-bit elements
 constexpr int PAIR_ROWS = 256; // output rows and columns of a CTA pair's tile
 constexpr int PAIR_COLS = 256;
-constexpr int ROW_TILE_A = 128;
+constexpr int ROW_TILE_A = 128;    // weight rows of a row kernel's block
+constexpr int ROW_TWO_TOKENS = 32; // tokens of a block up to which two share an SM
 
 cudaError_t linear_prepare();
 cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream);
 // bn: B's rows per block (16, 32, 64 or 128)
-cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, cudaStream_t stream);
+cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, int sm_count, cudaStream_t stream);
 
 // dst [rows, ldd] <- src [rows, cols] (row stride lds), 16-bit elements, ldd % 8 == 0, for
 // one or two arrays.
