@@ -226,13 +226,14 @@ anvil_status anvil_adam_step(float* param, const float* grad, float* exp_avg, fl
  * contiguous rows and a row stride ld* in elements (at least the row's length; not read
  * when there is at most one row), so a view of wider rows is fine.  Pointers are aligned
  * to their element size; rows on 16-byte boundaries are faster.  Sums, statistics and
- * accumulators are fp32; a result is rounded to its type once, to nearest even.  rows may
- * be 0: forward calls then do nothing, gradients of parameters become 0.  Results are the
- * same bits on every call with the same arguments (no atomics).  Written buffers must not
- * overlap any other buffer of the call except where said; views that interleave in one
- * buffer without sharing an element are fine if their row strides are the same.  Calls
- * allocate nothing and never synchronise, so they may be captured in a CUDA graph; where
- * a call needs scratch, its workspace is as for anvil_multi_bank_step. */
+ * accumulators are fp32; a result is rounded to its type once, to nearest even.  rows
+ * may be 0: forward calls then do nothing, gradients of parameters become 0.  Results
+ * are the same bits on every call with the same arguments (no sum's order depends on
+ * timing).  Written buffers must not overlap any other buffer of the call except where
+ * said; views that interleave in one buffer without sharing an element are fine if their
+ * row strides are the same.  Calls allocate nothing and never synchronise, so they may
+ * be captured in a CUDA graph; where a call needs scratch, its workspace is as for
+ * anvil_multi_bank_step. */
 typedef enum { ANVIL_F32 = 0, ANVIL_BF16 = 1, ANVIL_F16 = 2 } anvil_dtype;
 
 #define ANVIL_MAX_ROWS (1 << 30)     /* largest rows of these operators */
@@ -319,7 +320,8 @@ typedef struct {
     int weight_transposed;
 } anvil_linear_desc;
 /* Scratch of a call (0 for invalid descriptors and where none is needed): copies of
- * operands whose rows are not on 16-byte boundaries.  Depends on the pointers' alignment. */
+ * operands whose rows are not on 16-byte boundaries, and fp32 parts of products split along
+ * the contraction.  Depends on the pointers' alignment. */
 size_t anvil_linear_workspace_bytes(const anvil_linear_desc* desc);
 anvil_status anvil_linear_forward(const anvil_linear_desc* desc, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -24,7 +24,9 @@
 // stages per team, several rows ahead.  With one row ahead in registers a block waited out
 // the memory's latency on every row (32768 x 2816 bf16: 150-168 us backward, 78 forward;
 // with the ring 121-125 and 71, 5.2-6.1 TB/s; 32768 x 2815, off the 16-byte boundaries,
-// backward: 522, with the ring 199).
+// backward: 522, with the ring 199; forward, without it, 152: bound by the instructions of
+// element-by-element accesses, 2.4 TB/s; results staged in shared memory and stored by bulk
+// copies were slower, 227 backward).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -442,10 +444,10 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
 // team's first thread issues the copies of a stage once the team has read what was in it.
 //
 // Rows off the 16-byte boundaries (VEC false, backward only; forward the plain kernels are as
-// fast): a bulk copy takes the 16-byte pieces that
-// cover the row, so it brings up to 14 bytes of the rows (or padding) before and after,
-// which nothing reads; the array's first and last row, which have no such neighbour on one
-// side, are copied element by element.  A thread then has every TPR-th element.
+// fast): a bulk copy takes the 16-byte pieces that cover the row, so it brings up to 14
+// bytes of the rows (or padding) before and after, which nothing reads; the array's first and
+// last row, which have no such neighbour on one side, are copied element by element.  A
+// thread then has every TPR-th element.
 constexpr int RING_MAX = 8;
 constexpr int RING_BLOCK = 256;                  // threads per block, about (512 where a team is that wide)
 constexpr int RING_BYTES = 100 * 1024;           // shared memory of such a block: two per SM
