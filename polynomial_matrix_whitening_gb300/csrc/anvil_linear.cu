@@ -525,8 +525,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
             // thread about 500 cycles, as long as its products, so two take turns
             int it = 0;
             const int mine = warp / 2;
+            Unit next = unit_of(p, pair < units ? pair : 0);
             for (int u = pair; u < units; u += npairs) {
-                const Unit t = unit_of(p, u);
+                const Unit t = next;
+                bool looked = u + npairs >= units;  // the next unit's place: its divisions run while this one's loads do
                 const int arow = t.tr * PAIR_ROWS + CTA_ROWS * static_cast<int>(rank);
                 const int brow = t.tc * BN + BN / 2 * static_cast<int>(rank);
                 bool ok = true;
@@ -555,7 +557,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                     } else {
                         tma_load_3d_pair(sb, &p.tm_b, fb, kc, brow, 0);
                     }
+                    if (!looked) {
+                        looked = true;
+                        next = unit_of(p, u + npairs);
+                    }
                 }
+                if (!looked) next = unit_of(p, u + npairs);
                 if (!ok) {
                     aborted = 1;
                     break;
@@ -570,11 +577,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
             const uint32_t idesc = idesc_16(PAIR_ROWS, BN, p.a_mn, p.b_mn, p.f16);
             const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
             const uint32_t a_lbo = p.a_mn ? 8192 : 16, b_lbo = p.b_mn ? 8192 : 16;
+            const int whole_kb = (p.k + GEMM_BK - 1) / GEMM_BK;
             int s = 0, acc = 0;
             uint32_t ph = 0;
             bool ready = false, ok = true;
             for (int u = pair; u < units && ok; u += npairs) {
-                const int nkb = unit_of(p, u).nkb;
+                const int nkb = u < p.split.whole ? whole_kb : unit_of(p, u).nkb;
                 for (int c0 = 0; c0 < nkb && ok; c0 += F32 ? CHAIN_KB : nkb, ++acc) {
                     const int cn = F32 ? min(CHAIN_KB, nkb - c0) : nkb;
                     const int ab = acc & 1;
