@@ -113,6 +113,44 @@ def test_norm_backward(A, shape, dtype):
     assert A.device_error() == A.OK
 
 
+# Enough rows for the kernels that keep several rows on their way, with rows left over that do
+# not fill every team's share, for each width of a team; and rows off the 16-byte boundaries.
+NORM_MANY = [(117003, 512), (58501, 1000), (29301, 2000), (14701, 2816), (14651, 4000), (7403, 8000),
+             (29501, 300), (14801, 1023), (3701, 1500), (1901, 2815), (1003, 5001)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("shape", NORM_MANY, ids=lambda s: "x".join(map(str, s)))
+def test_norm_many_rows(A, shape, pad, dtype):
+    rows, n = shape
+    with_res = (rows + pad) % 2 == 0
+    x = randn(110, rows, n, scale=2.0, dtype=dtype, pad=pad)
+    dy = randn(111, rows, n, dtype=dtype, pad=pad)
+    res = randn(112, rows, n, dtype=dtype, pad=pad) if with_res else None
+    w, b = 1 + randn(113, n, scale=0.2), randn(114, n, scale=0.2)
+    y, mean, rstd = A.layernorm_forward(x, w, b, 1e-5)
+    ry, rm, rr = norm_ref(x, w, b, 1e-5)
+    size = x.double().abs().amax(-1)
+    close(mean, rm, "f32", size, 48, "mean")
+    close(rstd, rr, "f32", rr * (1 + (size * rr).square()), 128, "rstd")
+    close(y, ry, dtype, ((ry - b.double()).abs() + b.double().abs()) * (1 + (size * rr).square())[:, None]
+          + (size * rr)[:, None] * w.double().abs(), 192, "y")
+    del y, ry
+    dx, dw, db = A.layernorm_backward(dy, x, mean, rstd, w, residual_grad=res)
+    rx, rw, rb, mx, mw, mb = norm_grad_ref(dy, x, mean, rstd, w, res)
+    h_err = (x.double().abs().amax(1) * rstd.double())[:, None]
+    close(dx, rx, dtype, mx * (1 + h_err), 128, "dx")
+    # a column's chain: at most 117003 / (152 * 2 * 8) rows a team, 8 teams, 304 blocks by 16, 16
+    c = 2 * (rows // 152 // 2 + 1 if n > 512 else 49) + 8 + 19 + 16 + 16
+    close(dw, rw, "f32", mw * (1 + float(h_err.max())) + 1e-30, c, "dweight")
+    close(db, rb, "f32", mb, c, "dbias")
+    # in place, and without what was not asked for: the same bits
+    again = A.layernorm_backward(dy, x, mean, rstd, w, residual_grad=res, weight_grads=False, out=dy)
+    assert torch.equal(again[0], dx) and again[1] is None
+    assert A.device_error() == A.OK
+
+
 def test_norm_in_place_and_no_affine(A):
     x = randn(1, 130, 768, dtype="bf16")
     y, mean, rstd = A.layernorm_forward(x)
@@ -270,6 +308,41 @@ def test_linear_backward(A, shape, transposed, dtype):
         got = A.linear_backward(dy, x, w, preact=z, activation=act, dweight_dtype=DT[dw_type])
         assert got[1].stride() == ((1, n) if transposed and n > 1 and k > 1 else got[1].stride())
         linear_grad_check(A, dy, x, w, z, act, dtype, dw_type, got)
+    assert A.device_error() == A.OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("shape", [(8192, 2816, 768), (4096, 1024, 3000), (4099, 1027, 3001), (2500, 2304, 4200)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_linear_backward_both_products(A, shape, transposed, dtype):
+    """Sizes whose products share the device: a last turn of the first that is not full, the second in parts."""
+    rows, n, k = shape
+    for i, (act, dw_type) in enumerate([("relu2", "f32"), (None, dtype)]):
+        dy, x = randn(1210 + i, rows, n, dtype=dtype), randn(1310 + i, rows, k, dtype=dtype)
+        w = make_weight(1410 + i, n, k, dtype, transposed)
+        z = randn(1510 + i, rows, n, dtype=dtype) if act else None
+        got = A.linear_backward(dy, x, w, preact=z, activation=act, dweight_dtype=DT[dw_type])
+        linear_grad_check(A, dy, x, w, z, act, dtype, dw_type, got)
+        # which pairs start first does not show
+        for _ in range(3):
+            again = A.linear_backward(dy, x, w, preact=z, activation=act, dweight_dtype=DT[dw_type])
+            assert all(torch.equal(p, q) for p, q in zip(got, again))
+    assert A.device_error() == A.OK
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("rows", [1, 17, 32, 70])
+def test_linear_few_rows_of_wide_layers(A, rows, transposed):
+    """More blocks of weight rows than SMs."""
+    n, k = 20011, 200
+    x = randn(1220, rows, k, dtype="bf16")
+    w = make_weight(1221, n, k, "bf16", transposed, pad=5)
+    b = randn(1222, n)
+    y = A.linear_forward(x, w, b, activation="relu")
+    ref = (x.double() @ w.double().t() + b.double()).clamp_min(0)
+    mag = x.double().abs() @ w.double().abs().t() + b.double().abs()
+    close(y, ref, "bf16", mag, 2 * (k / 16 + 4), "y")
     assert A.device_error() == A.OK
 
 
