@@ -173,6 +173,7 @@ struct Product {
 
 // How a product runs.
 struct Plan {
+    bool tokens;      // token_kernel
     bool few;         // row_gemm_kernel
     int bn;           // few: B rows of a block,
     int splits, kb;   //      parts of the contraction and the k-blocks of each
@@ -273,10 +274,18 @@ void plan_parts(int64_t tiles, int64_t tail, int64_t kb, double turn, Start at, 
     p->part = static_cast<size_t>(parts) * 4 * PAIR_ROWS * PAIR_COLS;
 }
 
+// few: the kernels for few rows may run (A K-major, a 16-bit result); k_major: B is;
 // epilogue: SM cycles that the epilogue of a whole tile of the pair kernel takes.
-Plan plan_product(int64_t rows, int cols, int64_t k, bool few, double epilogue, Start at) {
+Plan plan_product(int64_t rows, int cols, int64_t k, bool few, bool k_major, double epilogue, Start at) {
     Plan p = {};
     const int64_t kb = ceil_div(k, GEMM_BK), tiles = tiles_of(rows, cols);
+    // One or two tokens and a small weight: no tensor core, no join, half the latency.  Against
+    // row_gemm_kernel, us: 2816 x 768 one token 2.7/4.4, two 3.4/4.5; 4096 x 4096 9.7/9.9 and 12.3/10;
+    // 16384 x 4096 27/23.3.
+    if (few && k_major && rows <= TOKEN_ROWS && rows * k <= TOKEN_CHUNKS * 8 && rows * rows * cols * k <= 1 << 24) {
+        p.tokens = p.few = true;
+        return p;
+    }
     if (few && rows <= FEW_ROWS) plan_few(rows, cols, kb, epilogue, &p);
     plan_whole(tiles, kb, epilogue, at, &p);
     const double turn = turn_cycles(kb, epilogue);
@@ -313,16 +322,16 @@ Plan plan_product(int64_t rows, int cols, int64_t k, bool few, double epilogue, 
 // The two products of a backward pass.  The second kernel's pairs start where the first
 // leaves SMs idle, so a last turn of the first that is not full costs nothing when the
 // second's parts are cut to fill it; or both run as they would alone.
-void plan_both(int64_t rows1, int cols1, int64_t k1, double epilogue1, int64_t rows2, int cols2, int64_t k2, double epilogue2,
+void plan_both(int64_t rows1, int cols1, int64_t k1, bool k_major1, double epilogue1, int64_t rows2, int cols2, int64_t k2, double epilogue2,
                Plan* first, Plan* second) {
-    *first = plan_product(rows1, cols1, k1, true, epilogue1, ALL_FREE);
-    *second = plan_product(rows2, cols2, k2, false, epilogue2, ALL_FREE);
+    *first = plan_product(rows1, cols1, k1, true, k_major1, epilogue1, ALL_FREE);
+    *second = plan_product(rows2, cols2, k2, false, false, epilogue2, ALL_FREE);
     if (first->few) return;
     const int64_t kb = ceil_div(k1, GEMM_BK), tiles = tiles_of(rows1, cols1);
     const int64_t full = tiles / PLAN_PAIRS, rest = tiles % PLAN_PAIRS;
     const double turn = turn_cycles(kb, epilogue1);
     const Start at = {rest ? static_cast<int>(PLAN_PAIRS - rest) : PLAN_PAIRS, rest ? turn : 0.0};
-    const Plan p = plan_product(rows2, cols2, k2, false, epilogue2, at);
+    const Plan p = plan_product(rows2, cols2, k2, false, false, epilogue2, at);
     const double cost = full * turn + LEAVE_CYCLES + p.cost;
     if (cost >= first->cost + second->cost) return;
     set_whole(tiles, full * turn + LEAVE_CYCLES, first);
@@ -346,6 +355,21 @@ double epilogue_cycles(const GemmEpilogue& e, int64_t rows) {
 anvil_status run_product(const Product& q, const Plan& plan, DeviceState* dev, cudaStream_t s, TailSumParams* rest) {
     anvil_status st;
     cudaError_t e;
+    if (plan.tokens) {
+        TokenParams g;
+        memset(&g, 0, sizeof(g));
+        g.x = q.a.p;
+        g.w = q.b.p;
+        g.epi = q.epi;
+        g.ldx = q.a.ld;
+        g.ldw = q.b.ld;
+        g.rows = static_cast<int>(q.rows);
+        g.cols = q.cols;
+        g.k = static_cast<int>(q.k);
+        g.f16 = q.f16;
+        e = profiled(ANVIL_KERNEL_LINEAR_PRODUCT, s, [&] { return launch_tokens(g, s); });
+        return e ? cuda_fail(e, "linear product launch") : ANVIL_OK;
+    }
     if (plan.few) {
         RowGemmParams g;
         memset(&g, 0, sizeof(g));
@@ -484,7 +508,7 @@ LinearLayout linear_layout(const anvil_linear_desc* d) {
     L.off_x = 0;
     L.off_w = L.off_x + copy_bytes(L.x);
     L.off_part = L.off_w + copy_bytes(L.w);
-    L.plan = plan_product(d->rows, d->n, d->k, true, epilogue_cycles(forward_epilogue(d), d->rows), ALL_FREE);
+    L.plan = plan_product(d->rows, d->n, d->k, true, !d->weight_transposed, epilogue_cycles(forward_epilogue(d), d->rows), ALL_FREE);
     L.total = L.off_part + L.plan.part;
     return L;
 }
@@ -547,9 +571,9 @@ LinearGradLayout linear_grad_layout(const anvil_linear_grad_desc* d) {
     const int64_t wr = tr ? d->k : d->n;
     const int wc = tr ? d->n : d->k;
     const double ex = epilogue_cycles(dx_epilogue(d), d->rows), ew = epilogue_cycles(dweight_epilogue(d), wr);
-    if (d->dx && d->dweight) plan_both(d->rows, d->k, d->n, ex, wr, wc, d->rows, ew, &L.pdx, &L.pdw);
-    else if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, true, ex, ALL_FREE);
-    else if (d->dweight) L.pdw = plan_product(wr, wc, d->rows, false, ew, ALL_FREE);
+    if (d->dx && d->dweight) plan_both(d->rows, d->k, d->n, tr, ex, wr, wc, d->rows, ew, &L.pdx, &L.pdw);
+    else if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, true, tr, ex, ALL_FREE);
+    else if (d->dweight) L.pdw = plan_product(wr, wc, d->rows, false, false, ew, ALL_FREE);
     L.total = at + L.pdx.part + L.pdw.part;  // the second product may start before the first's parts are added up
     return L;
 }

@@ -6,7 +6,7 @@
 //   input's grad   dx = dz W
 //   weight's grad  dW = dz^T x  (16 bit, or fp32, optionally added to what is there)
 //
-// Two kernels share the work.
+// Three kernels share the work.
 //
 // pair_gemm_kernel: clusters of two CTAs compute 256 x 256 output tiles with
 // tcgen05.mma.cta_group::2; CTA rank r loads rows 128r.. of the tile's A operand and
@@ -35,8 +35,10 @@
 // the tokens its N side (16 to 128), so a weight is read once, and a cluster of up to eight
 // CTAs splits the contraction, so that enough SMs read it; the partial accumulators are
 // joined through distributed shared memory in rank order.  HBM bounds it where the weight
-// is large (1 x 16384 x 4096: 23.3 us, 5.8 TB/s; 64 tokens 27), latency where it is small (1
-// x 2816 x 768: 4.4 us), and from 128 tokens on the MMA's reads of its 128-row operand.
+// is large (1 x 16384 x 4096: 23.3 us, 5.8 TB/s; 64 tokens 27), latency where it is small (16
+// x 2816 x 768: 4.7 us), and from 128 tokens on the MMA's reads of its 128-row operand.
+//
+// token_kernel: one or two tokens and a small weight, without tensor cores.
 //
 // Every wait is bounded (anvil_device.cuh): one that gives up sets the device error word
 // and an abort flag; loads in flight are waited for (bounded), the TMEM is freed and the
@@ -1023,6 +1025,114 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) row_gemm_kernel(const __grid_c
     if (warp == 1) tmem_dealloc(tmem, S::TMEM_COLS);
 }
 
+// ---------------------------------------------------------------- one or two tokens
+// For small weights, where the latency of one load after another is what a call costs (1 x 2816
+// x 768: 2.7 us; the row kernel, with its barriers, tensor memory and join: 4.4).  A warp takes
+// WR weight rows (or a ks-th of the chunks of each) with eight loads of 16 bytes in flight per
+// lane, the tokens wait in shared memory; fp32 FMAs on packed pairs, the lanes' sums joined by
+// shuffles, the parts of a row through shared memory in order.
+constexpr int TOKEN_THREADS = 256, TOKEN_WARPS = TOKEN_THREADS / 32;
+template <typename T, int R, int WR>
+__global__ void __launch_bounds__(TOKEN_THREADS) token_kernel(const TokenParams p, int ks) {
+    constexpr int E = Elem<T>::VEC, U = 8 / WR;
+    extern __shared__ __align__(16) uint8_t xs[];  // the tokens' whole chunks
+    __shared__ float parts[TOKEN_WARPS][WR * R];
+    pdl_allow_next();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp % ks;
+    const int col0 = (blockIdx.x * (TOKEN_WARPS / ks) + warp / ks) * WR;
+    const T* w[WR];
+#pragma unroll
+    for (int i = 0; i < WR; ++i) w[i] = static_cast<const T*>(p.w) + static_cast<long long>(min(col0 + i, p.cols - 1)) * p.ldw;
+    const int chunks = p.k / E;
+    uint64_t acc[WR][R];
+#pragma unroll
+    for (int i = 0; i < WR; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[i][r] = 0;
+    pdl_wait_previous();
+    const uint32_t xa = smem_u32(xs);
+    bool staged = false;
+    for (int c0 = part * 32 + lane; c0 - lane < chunks; c0 += 32 * ks * U) {
+        uint4 wr[U][WR];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 32 * ks;
+#pragma unroll
+            for (int i = 0; i < WR; ++i) wr[u][i] = c < chunks ? ldg_stream(w[i] + c * E) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (!staged) {  // the tokens, while the first weights are on their way
+            staged = true;
+            for (int i = threadIdx.x; i < chunks * R; i += TOKEN_THREADS) {
+                const int r = i / chunks, c = i - r * chunks;
+                sts128(xa + i * 16, __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + min(r, p.rows - 1) * p.ldx) + c));
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 32 * ks;
+            if (c >= chunks) break;
+            uint64_t xv[R][E / 2];
+#pragma unroll
+            for (int r = 0; r < R; ++r) Elem<T>::unpack_pairs(lds128(xa + (r * chunks + c) * 16), xv[r]);
+#pragma unroll
+            for (int i = 0; i < WR; ++i) {
+                uint64_t wv[E / 2];
+                Elem<T>::unpack_pairs(wr[u][i], wv);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) acc[i][r] = f2_fma(wv[e], xv[r][e], acc[i][r]);
+            }
+        }
+    }
+    const bool tail = part == 0 && lane < p.k - chunks * E;  // the elements after the last whole chunk
+    float v[WR][R];
+#pragma unroll
+    for (int i = 0; i < WR; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float lo, hi;
+            f2_split(acc[i][r], &lo, &hi);
+            v[i][r] = lo + hi;
+            if (tail) v[i][r] = fmaf(Elem<T>::load(w[i][chunks * E + lane]), 
+                                      Elem<T>::load(static_cast<const T*>(p.x)[min(r, p.rows - 1) * p.ldx + chunks * E + lane]), v[i][r]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v[i][r] += __shfl_xor_sync(0xffffffffu, v[i][r], o);
+        }
+    if (ks > 1) {
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < WR; ++i)
+#pragma unroll
+                for (int r = 0; r < R; ++r) parts[warp][i * R + r] = v[i][r];
+        }
+        __syncthreads();
+        if (part != 0) return;
+#pragma unroll
+        for (int i = 0; i < WR; ++i)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                for (int q = 1; q < ks; ++q) v[i][r] += parts[warp + q][i * R + r];
+    }
+    // lane i * R + r finishes weight row i's value of token r
+    float mine[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < WR; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (lane == i * R + r) mine[0] = v[i][r];
+    const int col = col0 + lane / R, row = lane % R;
+    if (lane >= WR * R || col >= p.cols || row >= p.rows) return;
+    const GemmEpilogue& e = p.epi;
+    if (e.bias) mine[0] += e.bias_f32 ? static_cast<const float*>(e.bias)[col] : Elem<T>::load(static_cast<const T*>(e.bias)[col]);
+    if (e.z) static_cast<T*>(e.z)[row * e.ldz + col] = Elem<T>::store(mine[0]);
+    act_values<1>(e.act, mine);
+    if (e.in) mine[0] += Elem<T>::load(static_cast<const T*>(e.in)[row * e.ldin + col]);
+    static_cast<T*>(e.out)[row * e.ldout + col] = Elem<T>::store(mine[0]);
+}
+
 // ---------------------------------------------------------------- around the products
 // Eight columns per thread; the last chunk of a row may be partial.
 __global__ void __launch_bounds__(256) repack_kernel(const RepackParams q) {
@@ -1148,6 +1258,26 @@ cudaError_t run_row(RowGemmParams p, int sm_count, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, row_gemm_kernel<T, BN>, p);
 }
 
+// Weight rows per warp: four where that still gives every SM sixteen warps, else fewer, then
+// several warps per row, as long as every lane has a chunk.
+template <typename T, int R>
+cudaError_t run_tokens(const TokenParams& p, cudaStream_t s) {
+    const int full = 152 * 2 * TOKEN_WARPS, chunks = p.k / Elem<T>::VEC;
+    const int wr = p.cols >= 4 * full ? 4 : p.cols >= 2 * full ? 2 : 1;
+    int ks = 1;
+    while (ks < TOKEN_WARPS && static_cast<long long>(p.cols) * ks < full && chunks >= 64 * ks) ks *= 2;
+    const int per = TOKEN_WARPS / ks * wr;
+    const dim3 grid((p.cols + per - 1) / per), block(TOKEN_THREADS);
+    const size_t smem = static_cast<size_t>(chunks) * 16 * R;
+    if (wr == 4) return launch_pdl(token_kernel<T, R, 4>, grid, block, smem, s, p, ks);
+    if (wr == 2) return launch_pdl(token_kernel<T, R, 2>, grid, block, smem, s, p, ks);
+    return launch_pdl(token_kernel<T, R, 1>, grid, block, smem, s, p, ks);
+}
+template <typename T>
+cudaError_t pick_tokens(const TokenParams& p, cudaStream_t s) {
+    return p.rows == 1 ? run_tokens<T, 1>(p, s) : run_tokens<T, 2>(p, s);
+}
+
 int blocks_for(long long items) {
     const long long b = (items + 255) / 256;
     return static_cast<int>(b < 1 ? 1 : b < 152 * 16 ? b : 152 * 16);
@@ -1184,6 +1314,10 @@ cudaError_t launch_finish(const FinishParams& p, cudaStream_t s) {
     const dim3 grid((p.tail[0].tiles + p.tail[1].tiles) * TAIL_BLOCKS + bias);
     if (p.f16) return launch_pdl(finish_kernel<__half>, grid, dim3(FINISH_THREADS), 0, s, p);
     return launch_pdl(finish_kernel<__nv_bfloat16>, grid, dim3(FINISH_THREADS), 0, s, p);
+}
+
+cudaError_t launch_tokens(const TokenParams& p, cudaStream_t s) {
+    return p.f16 ? pick_tokens<__half>(p, s) : pick_tokens<__nv_bfloat16>(p, s);
 }
 
 cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, int sm_count, cudaStream_t s) {

@@ -81,6 +81,18 @@ struct RowGemmParams {
     unsigned* err;
 };
 
+// One or two rows (tokens) and a weight stored [cols][k], both on 16-byte rows.
+struct TokenParams {
+    const void* x;
+    const void* w;
+    GemmEpilogue epi;
+    long long ldx, ldw;
+    int rows, cols, k;
+    int f16;
+};
+constexpr int TOKEN_ROWS = 2;
+constexpr int TOKEN_CHUNKS = 3008;  // 16-byte chunks of the tokens that shared memory takes (47 KB, 48 with what is static)
+
 constexpr int GEMM_BK = 64;    // k-block: one 128-byte swizzle row of 16-bit elements
 constexpr int PAIR_ROWS = 256; // output rows and columns of a CTA pair's tile
 constexpr int PAIR_COLS = 256;
@@ -90,6 +102,7 @@ constexpr int ROW_TWO_TOKENS = 32; // tokens of a block up to which two share an
 cudaError_t linear_prepare();
 cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream);
+cudaError_t launch_tokens(const TokenParams& p, cudaStream_t stream);
 // bn: B's rows per block (16, 32, 64 or 128)
 cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, int sm_count, cudaStream_t stream);
 

@@ -331,6 +331,30 @@ def test_linear_backward_both_products(A, shape, transposed, dtype):
     assert A.device_error() == A.OK
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows", [1, 2, 3])
+@pytest.mark.parametrize("shape", [(1, 7), (5, 8), (3, 24570), (3, 24060), (100, 12301), (70, 12030), (2816, 768), (768, 2816), (5001, 520), (12007, 1030),
+                                   (9800, 264), (4096, 4096), (4100, 4100)], ids=lambda s: "x".join(map(str, s)))
+def test_linear_tokens(A, shape, rows, dtype):
+    n, k = shape
+    x, w = randn(1230, rows, k, dtype=dtype), randn(1231, n, k, scale=k ** -0.5, dtype=dtype, pad=(-k) % 8)
+    b, r = randn(1232, n, scale=0.3), randn(1233, rows, n, dtype=dtype)
+    y, z = A.linear_forward(x, w, b, activation="silu", residual=r, save_preact=True)
+    zr = x.double() @ w.double().t() + b.double()
+    mag = x.double().abs() @ w.double().abs().t() + b.double().abs()
+    c = 2 * (k / 16 + 4)
+    close(z, zr, dtype, mag, c, "z")
+    close(y, act_ref(zr, "silu") + r.double(), dtype, 1.2 * mag + 8 * (zr.abs() + zr.square()) + r.double().abs(), c, "y")
+    plain = A.linear_forward(x, w)
+    close(plain, zr - b.double(), dtype, mag, c, "plain")
+    # a transposed bank's input gradient takes the same path
+    dy = randn(1234, rows, n, dtype=dtype)
+    wt = randn(1235, k, n, scale=k ** -0.5, dtype=dtype, pad=(-n) % 8).t()
+    dx = A.linear_backward(dy, x, wt, need_dweight=False, bias_grad=False)[0]
+    close(dx, dy.double() @ wt.double(), dtype, dy.double().abs() @ wt.double().abs(), 2 * (n / 16 + 4), "dx")
+    assert A.device_error() == A.OK
+
+
 @pytest.mark.parametrize("transposed", [False, True])
 @pytest.mark.parametrize("rows", [1, 17, 32, 70])
 def test_linear_few_rows_of_wide_layers(A, rows, transposed):
