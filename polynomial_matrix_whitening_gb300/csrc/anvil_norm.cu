@@ -23,7 +23,7 @@
 // Many rows (the ring kernels): the rows come by bulk copies into a ring of shared-memory
 // stages per team, several rows ahead.  With one row ahead in registers a block waited out
 // the memory's latency on every row (32768 x 2816 bf16: 150-168 us backward, 78 forward;
-// with the ring 121-125 and 71, 5.2-6.1 TB/s; 32768 x 2815, off the 16-byte boundaries,
+// with the ring 121-125 and 65, 5.7-6.1 TB/s; 32768 x 2815, off the 16-byte boundaries,
 // backward: 522, with the ring 199; forward, without it, 152: bound by the instructions of
 // element-by-element accesses, 2.4 TB/s; results staged in shared memory and stored by bulk
 // copies were slower, 227 backward).
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
 }
 
 // ---------------------------------------------------------------- the ring kernels
-// A team of TPR threads (32 to 512) takes a run of consecutive rows; up to RING_MAX stages
+// A team of TPR threads (64 to 512) takes a run of consecutive rows; up to RING_MAX stages
 // of `arrays` rows each (x, or x, dy and the residual's gradient) are on their way.  The
 // team's first thread issues the copies of a stage once the team has read what was in it.
 //
@@ -450,10 +450,13 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_pe
 // thread then has every TPR-th element.
 constexpr int RING_MAX = 8;
 constexpr int RING_BLOCK = 256;                  // threads per block, about (512 where a team is that wide)
-constexpr int RING_BYTES = 100 * 1024;           // shared memory of such a block: two per SM
+constexpr int RING_BYTES = 200 * 1024;           // shared memory of an SM's blocks
+// Blocks per SM: two of 256 threads, three of 192 (32768 x 2816 bf16 forward: 65 us, 70 with
+// two; three of 256 threads were slower, 48 against 45 at 65536 x 1024).
+constexpr int ring_blocks(int tpr) { return tpr > RING_BLOCK ? 1 : tpr == 192 ? 3 : 2; }
 constexpr int ring_teams(int tpr) { return tpr > RING_BLOCK ? 1 : RING_BLOCK / tpr; }
 constexpr int ring_threads(int tpr) { return ring_teams(tpr) * tpr; }
-constexpr int ring_bytes(int tpr) { return tpr > RING_BLOCK ? 2 * RING_BYTES : RING_BYTES; }
+constexpr int ring_bytes(int tpr) { return RING_BYTES / ring_blocks(tpr) / 1024 * 1024; }
 // Bytes of a row's place in a stage.
 __host__ __device__ constexpr int ring_slot(bool vec, int row_bytes) { return vec ? row_bytes : (row_bytes + 31) / 16 * 16; }
 // Stages per team of a ring of `arrays` rows of `row_bytes` (their slots) each.
@@ -468,8 +471,7 @@ struct Team {
     float4* red;  // [2][TPR / 64] pairs of two warps' sums
     int flip;
     __device__ __forceinline__ void sync() const {
-        if constexpr (TPR == 32) __syncwarp();
-        else named_barrier_sync(1 + id, TPR);
+        named_barrier_sync(1 + id, TPR);
     }
     // Sums of a and b over the team, the same in every thread; a barrier of the team.
     __device__ __forceinline__ void sum(float& a, float& b) {
@@ -478,23 +480,19 @@ struct Team {
             a += __shfl_xor_sync(0xffffffffu, a, o);
             b += __shfl_xor_sync(0xffffffffu, b, o);
         }
-        if constexpr (TPR > 32) {
-            // two arrays in turn: one is written again only after the next sum's barrier
-            float4* r = red + flip * (TPR / 64);
-            flip ^= 1;
-            if ((t & 31) == 0) reinterpret_cast<float2*>(r)[t >> 5] = make_float2(a, b);
-            sync();
-            a = b = 0.f;
+        // two arrays in turn: one is written again only after the next sum's barrier
+        float4* r = red + flip * (TPR / 64);
+        flip ^= 1;
+        if ((t & 31) == 0) reinterpret_cast<float2*>(r)[t >> 5] = make_float2(a, b);
+        sync();
+        a = b = 0.f;
 #pragma unroll
-            for (int w = 0; w < TPR / 64; ++w) {
-                const float4 f = r[w];
-                a += f.x;
-                b += f.y;
-                a += f.z;
-                b += f.w;
-            }
-        } else {
-            __syncwarp();
+        for (int w = 0; w < TPR / 64; ++w) {
+            const float4 f = r[w];
+            a += f.x;
+            b += f.y;
+            a += f.z;
+            b += f.w;
         }
     }
 };
@@ -552,13 +550,13 @@ struct RowStats {
 };
 
 template <typename T, typename W, bool VEC, int TPR, int NV>
-__global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) norm_bwd_ring_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(ring_threads(TPR), ring_blocks(TPR)) norm_bwd_ring_kernel(const NormBwdParams p) {
     using Raw = RawUnit<T, VEC>;
     using F = typename Raw::F;
     constexpr int E = VEC ? Elem<T>::VEC : 1, P = Raw::P, TEAMS = ring_teams(TPR);
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[TEAMS][RING_MAX];
-    __shared__ float4 red[TEAMS][2][TPR > 32 ? TPR / 64 : 1];
+    __shared__ float4 red[TEAMS][2][TPR / 64];
     const int lane = threadIdx.x & 31;
     Team<TPR> team;
     team.id = threadIdx.x / TPR;
@@ -745,13 +743,13 @@ __global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) n
 }
 
 template <typename T, typename W, int TPR, int NV>
-__global__ void __launch_bounds__(ring_threads(TPR), TPR > RING_BLOCK ? 1 : 2) norm_fwd_ring_kernel(const NormFwdParams p) {
+__global__ void __launch_bounds__(ring_threads(TPR), ring_blocks(TPR)) norm_fwd_ring_kernel(const NormFwdParams p) {
     using Raw = RawUnit<T, true>;
     constexpr int E = Elem<T>::VEC, P = E / 2, TEAMS = ring_teams(TPR);
     using F = uint64_t;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[TEAMS][RING_MAX];
-    __shared__ float4 red[TEAMS][2][TPR > 32 ? TPR / 64 : 1];
+    __shared__ float4 red[TEAMS][2][TPR / 64];
     Team<TPR> team;
     team.id = threadIdx.x / TPR;
     team.t = threadIdx.x % TPR;
@@ -939,6 +937,7 @@ cudaError_t pick_fwd(const NormFwdParams& p, bool vec, cudaStream_t s) {
     if (vec) {
         if (w <= 8 * E) return run_fwd<T, W, true, 8, 1>(p, s);
         if (w <= 32 * E) return run_fwd<T, W, true, 32, 1>(p, s);
+        if (w <= 512) return run_fwd<T, W, true, 32, 16 / E>(p, s);
         if (w <= 1024) return run_fwd<T, W, true, 128, 8 / E>(p, s);
         if (w <= 2048) return run_fwd<T, W, true, 128, 16 / E>(p, s);
         if (w <= 4096) return run_fwd<T, W, true, 256, 16 / E>(p, s);
@@ -947,6 +946,7 @@ cudaError_t pick_fwd(const NormFwdParams& p, bool vec, cudaStream_t s) {
     }
     if (w <= 64) return run_fwd<T, W, false, 8, 8>(p, s);
     if (w <= 256) return run_fwd<T, W, false, 32, 8>(p, s);
+    if (w <= 512) return run_fwd<T, W, false, 32, 16>(p, s);
     if (w <= 1024) return run_fwd<T, W, false, 128, 8>(p, s);
     if (w <= 2048) return run_fwd<T, W, false, 256, 8>(p, s);
     if (w <= 4096) return run_fwd<T, W, false, 512, 8>(p, s);
@@ -961,6 +961,7 @@ cudaError_t pick_bwd(const NormBwdParams& p, bool vec, cudaStream_t s) {
     if (vec) {
         if (w <= 8 * E) return run_bwd<T, W, true, 8, 1>(p, s);
         if (w <= 32 * E) return run_bwd<T, W, true, 32, 1>(p, s);
+        if (w <= 512) return run_bwd<T, W, true, 32, 16 / E>(p, s);
         if (w <= 1024) return run_bwd<T, W, true, 128, 8 / E>(p, s);
         if (w <= 2048) return run_bwd<T, W, true, 128, 16 / E>(p, s);
         if (w <= 4096) return run_bwd<T, W, true, 256, 16 / E>(p, s);
@@ -969,6 +970,7 @@ cudaError_t pick_bwd(const NormBwdParams& p, bool vec, cudaStream_t s) {
     }
     if (w <= 64) return run_bwd<T, W, false, 8, 8>(p, s);
     if (w <= 256) return run_bwd<T, W, false, 32, 8>(p, s);
+    if (w <= 512) return run_bwd<T, W, false, 32, 16>(p, s);
     if (w <= 1024) return run_bwd<T, W, false, 128, 8>(p, s);
     if (w <= 2048) return run_bwd<T, W, false, 128, 16>(p, s);
     if (w <= 4096) return run_bwd<T, W, false, 256, 16>(p, s);
@@ -982,26 +984,27 @@ namespace {
 
 // Threads of a team of the ring kernels: up to 16 columns each, off the 16-byte boundaries
 // 8 where a block can hold that many threads twice.
-// (2049 to 3072 columns: 192 threads run 32768 x 2816 bf16 forward in 71 us, 256 in 78;
+// (2049 to 3072 columns: 192 threads run 32768 x 2816 bf16 forward in 65 us, 256 in 78;
 // backward 256 are faster, 121 against 125.)
 int ring_tpr(int width, int arrays, bool vec) {
     if (!vec && width <= 2048) return width <= 512 ? 64 : width <= 1024 ? 128 : 256;
-    return width <= 512 ? 32 : width <= 1024 ? 64 : width <= 2048 ? 128 : width <= 3072 && arrays == 1 ? 192 : width <= 4096 ? 256 : 512;
+    return width <= 1024 ? 64 : width <= 2048 ? 128 : width <= 3072 && arrays == 1 ? 192 : width <= 4096 ? 256 : 512;
 }
 
 // Teams of the ring kernels on the whole device, and whether they run: two stages fit, rows
-// of 1 KB (off the 16-byte boundaries, backward only, 512 bytes; the plain kernels' narrow
-// teams are faster below), and enough rows per team to make up for a slower start.
-// Measured with bf16, ring against plain, us: forward 1024 columns 42.9/47.2 at 48 rows a
-// team and 22.8/21.4 at 24, 2816 64.9/65.9 at 96 and 35.9/34.0 at 48; backward 2816
-// 19.9/20.4 at 8 and 38/43 at 24; off the boundaries 1023 columns 38.3/39.0 at 24 and
-// 21.6/19.7 at 12, 2815 20.2/26.1 at 6.
+// too wide for a warp alone (off the 16-byte boundaries, backward only, 512 bytes), and enough
+// rows per team to make up for a slower start.
+// Measured with bf16, ring against plain, us: forward 768 columns 38.2/42.8 at 48 rows a team
+// and 11.3/11.8 at 12, 1024 22.8/21.4 at 24, 2816 46.0/50.1 at 48 and 24.4/23.0 at 24; backward
+// 2816 25.1/27.5 at 8 and 19.1/19.0 at 4; off the boundaries 500 columns 12.6/19.9 at 4, 1023
+// 38.3/39.0 at 24 and 21.6/19.7 at 12, 2815 20.2/26.1 at 6; a warp for 512 columns against a ring
+// of 32-thread teams 39.4/41.4 forward, 82/92 backward at 48.
 bool ring_plan(long long rows, int width, int dtype, bool vec, int arrays, int* blocks, int* team_rows) {
     const int es = dtype_size(dtype), tpr = ring_tpr(width, arrays, vec);
-    const int least = arrays == 1 ? 48 : vec ? 8 : width <= 1024 ? 24 : 6;
-    if (width * es < (vec ? 1024 : 512) || width > 8192 || ring_stages(tpr, arrays, ring_slot(vec, width * es)) < 2) return false;
+    const int least = arrays == 1 ? 32 : vec ? 8 : width <= 512 ? 4 : width <= 1024 ? 24 : 6;
+    if ((vec ? width <= 512 : width * es < 512) || width > 8192 || ring_stages(tpr, arrays, ring_slot(vec, width * es)) < 2) return false;
     const int per_block = ring_teams(tpr);
-    const long long teams = 152ll * (tpr > RING_BLOCK ? 1 : 2) * per_block;
+    const long long teams = 152ll * ring_blocks(tpr) * per_block;
     if (rows < least * teams) return false;
     const long long each = (rows + teams - 1) / teams;
     *team_rows = static_cast<int>(each);
@@ -1011,9 +1014,9 @@ bool ring_plan(long long rows, int width, int dtype, bool vec, int arrays, int* 
 
 template <typename K, typename P>
 cudaError_t run_ring(K kernel, const P& p, int tpr, int blocks, cudaStream_t s) {
-    // All of a block's share of the shared memory, used or not: no SM takes a third block of the
+    // All of a block's share of the shared memory, used or not: no SM takes one more block of the
     // next launch while this one's are leaving, which would leave another SM with one (32768 x
-    // 2816 bf16 forward 91 us instead of 71).  The column sums reuse the ring.
+    // 2816 bf16 forward 91 us instead of 70).  The column sums reuse the ring.
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(tpr));
     if (e) return e;
     return launch_pdl(kernel, dim3(blocks), dim3(ring_threads(tpr)), ring_bytes(tpr), s, p);
@@ -1024,7 +1027,6 @@ cudaError_t pick_fwd_ring(const NormFwdParams& p, int blocks, cudaStream_t s) {
     constexpr int NV = 16 / Elem<T>::VEC;
     const int tpr = ring_tpr(p.width, 1, true);
     switch (tpr) {
-        case 32: return run_ring(norm_fwd_ring_kernel<T, W, 32, NV>, p, tpr, blocks, s);
         case 64: return run_ring(norm_fwd_ring_kernel<T, W, 64, NV>, p, tpr, blocks, s);
         case 128: return run_ring(norm_fwd_ring_kernel<T, W, 128, NV>, p, tpr, blocks, s);
         case 192: return run_ring(norm_fwd_ring_kernel<T, W, 192, NV>, p, tpr, blocks, s);
@@ -1047,7 +1049,6 @@ cudaError_t pick_bwd_ring(const NormBwdParams& p, cudaStream_t s) {
         }
     }
     switch (tpr) {
-        case 32: return run_ring(norm_bwd_ring_kernel<T, W, true, 32, NV>, p, tpr, p.blocks, s);
         case 64: return run_ring(norm_bwd_ring_kernel<T, W, true, 64, NV>, p, tpr, p.blocks, s);
         case 128: return run_ring(norm_bwd_ring_kernel<T, W, true, 128, NV>, p, tpr, p.blocks, s);
         case 256: return run_ring(norm_bwd_ring_kernel<T, W, true, 256, NV>, p, tpr, p.blocks, s);
@@ -1083,19 +1084,18 @@ cudaError_t launch_norm_fwd(const NormFwdParams& p, cudaStream_t s) {
     }
 }
 
-static int plain_bwd_blocks(long long rows, int width, int dtype) {
+static int plain_bwd_blocks(long long rows, int width) {
     // narrow rows: teams of 8 or 32 threads, 32 or 8 rows per block and turn; else one row
     // and a team of 128 threads or more, 16 columns of a row per thread
-    const int unit = 16 / dtype_size(dtype);
-    const int per_block = width <= 64 ? 32 : width <= 32 * unit ? 8 : 1;
-    const int tpr = width <= 32 * unit ? 32 : width <= 2048 ? 128 : width <= 4096 ? 256 : 512;
+    const int per_block = width <= 64 ? 32 : width <= 512 ? 8 : 1;
+    const int tpr = width <= 512 ? 32 : width <= 2048 ? 128 : width <= 4096 ? 256 : 512;
     const long long want = (rows + per_block - 1) / per_block;
     const long long cap = 152ll * bwd_blocks_per_sm(tpr);
     return static_cast<int>(want < 1 ? 1 : want < cap ? want : cap);
 }
 
 int norm_bwd_max_blocks(long long rows, int width, int dtype) {
-    int most = plain_bwd_blocks(rows, width, dtype), blocks = 0, each = 0;
+    int most = plain_bwd_blocks(rows, width), blocks = 0, each = 0;
     for (int arrays = 2; arrays <= 3; ++arrays)
         for (int vec = 0; vec < 2; ++vec)
             if (ring_plan(rows, width, dtype, vec != 0, arrays, &blocks, &each) && blocks > most) most = blocks;
@@ -1110,7 +1110,7 @@ void norm_bwd_plan(NormBwdParams* p) {
              aligned16(p->weight, 0, ws, 1);
     p->team_rows = 0;
     if (!ring_plan(p->rows, p->width, p->dtype, p->vec != 0, p->res ? 3 : 2, &p->blocks, &p->team_rows))
-        p->blocks = plain_bwd_blocks(p->rows, p->width, p->dtype);
+        p->blocks = plain_bwd_blocks(p->rows, p->width);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdParams& p, cudaStream_t s) {
