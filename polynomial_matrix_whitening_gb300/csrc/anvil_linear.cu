@@ -10,7 +10,7 @@
 //
 // pair_gemm_kernel: clusters of two CTAs compute 256 x 256 output tiles with
 // tcgen05.mma.cta_group::2; CTA rank r loads rows 128r.. of the tile's A operand and
-// columns 128r.. of its B operand by TMA into a ring of five stages, and holds output rows
+// columns 128r.. of its B operand by TMA into a ring of five or six stages, and holds output rows
 // 128r.. in its TMEM.  Two accumulators alternate, so a tile's epilogue overlaps the next
 // tile's products.  Operands are taken in the order they are stored: K-major, or MN-major
 // as 64 x 64 boxes, so no operand is ever transposed in memory.  The grid is persistent
@@ -56,7 +56,6 @@ namespace anvil {
 namespace {
 
 constexpr int CTA_ROWS = 128;
-constexpr int QBOX = 16384;             // one staging box: 128 rows of 128 bytes
 constexpr int A_STAGE = CTA_ROWS * 128; // 16 KB: this CTA's A rows of a k-block
 constexpr int EPI_GROUPS = 4;           // epilogue warp groups, one per quarter of the columns
 constexpr int EPI_WARP0 = 4;            // warps 4-19; warp 1: MMA issuer and TMEM owner; warps 0 and 2: TMA producers
@@ -208,10 +207,19 @@ __device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int co
 constexpr int BN = PAIR_COLS;
 constexpr int B_STAGE = BN / 2 * 128;  // 16 KB: this CTA's half of the B columns of a k-block
 constexpr int STAGE = A_STAGE + B_STAGE;
-constexpr int STAGES = 5;
-constexpr int BOXES = EPI_GROUPS;
-constexpr int EPI_COLS = BN / EPI_GROUPS;  // 64: one staging box of 16-bit results, two of fp32
-constexpr int PAIR_SMEM = STAGES * STAGE + BOXES * QBOX + 1024;  // + alignment slack
+constexpr int EPI_COLS = BN / EPI_GROUPS;  // 64
+// The epilogue's staging boxes, one per group: 128 rows of W bytes, 16-byte chunk j of row r at
+// the chunk the tensor maps' swizzle gives it.  W = 128 takes a group's 64 columns of 16-bit
+// results at once; W = 64 takes them by halves and leaves the room of one more stage.
+template <int W>
+struct Staging {
+    static constexpr int BOX = CTA_ROWS * W;
+    static constexpr int STAGES = W == 128 ? 5 : 6;
+    static constexpr int SMEM = STAGES * STAGE + EPI_GROUPS * BOX + 1024;  // + alignment slack
+    static __device__ __forceinline__ uint32_t addr(uint32_t box, int r, int j) {
+        return box + static_cast<uint32_t>(W == 128 ? r * 128 + ((j ^ (r & 7)) << 4) : r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+    }
+};
 constexpr uint32_t PAIR_TMEM = 2 * BN;
 
 // Tile t: groups of RASTER_ROWS rows of tiles, column by column inside a group, so that the
@@ -255,12 +263,7 @@ __device__ __forceinline__ Unit unit_of(const PairGemmParams& p, int u) {
     return r;
 }
 
-// A staging box: 128 rows of 128 bytes, 16-byte chunk j of row r at chunk j ^ (r % 8).
-__device__ __forceinline__ uint32_t box_addr(uint32_t box, int r, int j) {
-    return box + static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4));
-}
-
-// Rows that TMA cannot take (not 16-byte aligned): the 32 box rows of this warp to or from
+// Rows that TMA cannot take (not 16-byte aligned; W = 128 then): the 32 box rows of this warp to or from
 // global memory, neighbouring lanes on neighbouring elements, eight rows in flight.
 template <typename E>
 __device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, int row0, int col0, int rows, int cols,
@@ -274,7 +277,7 @@ __device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, 
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int c = h * 32 + lane;
-                const uint32_t a = box_addr(box, quad * 32 + i0 + i, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
+                const uint32_t a = Staging<128>::addr(box, quad * 32 + i0 + i, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
                 if constexpr (sizeof(E) == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[i][h]) : "r"(a) : "memory");
                 else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[i][h]) : "r"(a) : "memory");
             }
@@ -306,7 +309,7 @@ __device__ __forceinline__ void rows_to_box(uint32_t box, const E* src, long lon
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int c = h * 32 + lane;
-                const uint32_t a = box_addr(box, quad * 32 + i0 + i, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
+                const uint32_t a = Staging<128>::addr(box, quad * 32 + i0 + i, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
                 if constexpr (sizeof(E) == 2) sts16(a, v[i][h]);
                 else asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v[i][h]) : "memory");
             }
@@ -337,10 +340,10 @@ __device__ __forceinline__ void tma_store_box(const CUtensorMap* tm, uint32_t bo
 
 // Sends the box out: by TMA (the group's leader, after every thread's writes), or by the
 // warps themselves, each its own rows.
-template <typename E>
+template <typename E, int W>
 __device__ __forceinline__ void send_box(const EpiState& x, const CUtensorMap* tm, int by_tma, void* dst, long long ld,
                                          int row0, int col0, int rows, int cols) {
-    if (by_tma) {
+    if (W == 64 || by_tma) {
         fence_proxy_async_smem();
         named_barrier_sync(1 + x.grp, 128);
         if (x.leader) {
@@ -355,9 +358,10 @@ __device__ __forceinline__ void send_box(const EpiState& x, const CUtensorMap* t
     }
 }
 
+template <int W>
 __device__ __forceinline__ void arm_input(EpiState& x, const CUtensorMap* tm, int col0, int row0) {
     if (x.leader) {
-        mbar_arrive_expect_tx(x.in_bar, QBOX);
+        mbar_arrive_expect_tx(x.in_bar, Staging<W>::BOX);
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
             " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(x.box),
@@ -385,35 +389,38 @@ __device__ __forceinline__ bool early_input(const PairGemmParams& p) { return p.
 
 // The 16-bit epilogue of this group's quarter of a tile: z first where it is stored, then y
 // (the accumulator is read again: TMEM is not what bounds it).
-template <typename T>
+template <typename T, int W>
 __device__ __forceinline__ void epilogue_16(const PairGemmParams& p, EpiState& x, uint32_t tacc, uint32_t tempty, int row0,
                                             int col0) {
     const GemmEpilogue& e = p.epi;
     const bool early = early_input(p);
+    constexpr int COLS = W / 2, N = EPI_COLS / COLS;  // columns of a box, boxes
 #pragma unroll 1
-    for (int pass = e.z ? 0 : 1; pass < 2; ++pass) {
-        const bool final = pass == 1;
-        if (final && early) wait_input(x, p.err);
+    for (int step = e.z ? 0 : N; step < 2 * N; ++step) {  // z's boxes, y's boxes
+        const bool final = step >= N;
+        const int from = step % N * COLS, col = col0 + from;
+        const bool armed = early && step == N;
+        if (armed) wait_input(x, p.err);
         else box_free(x);
-        if (final && e.in && !early) {
-            if (p.in_tma) {
-                arm_input(x, &p.tm_in, col0, row0);
+        if (final && e.in && !armed) {
+            if (W == 64 || p.in_tma) {
+                arm_input<W>(x, &p.tm_in, col, row0);
                 wait_input(x, p.err);
             } else {
-                rows_to_box<uint16_t>(x.box, static_cast<const uint16_t*>(e.in), e.ldin, row0, col0, p.rows, p.cols, x.quad,
+                rows_to_box<uint16_t>(x.box, static_cast<const uint16_t*>(e.in), e.ldin, row0, col, p.rows, p.cols, x.quad,
                                       x.lane);
                 __syncwarp();
             }
         }
 #pragma unroll 1
-        for (int c = 0; c < EPI_COLS / 16; ++c) {
+        for (int c = 0; c < COLS / 16; ++c) {
             float v[16];
-            tmem_ld_16(tacc + c * 16, v);
-            if (e.bias) add_bias<T, 16>(e, col0 + c * 16, p.cols, v);
+            tmem_ld_16(tacc + from + c * 16, v);
+            if (e.bias) add_bias<T, 16>(e, col + c * 16, p.cols, v);
             if (final) act_values<16>(e.act, v);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint32_t a = box_addr(x.box, x.r, c * 2 + j);
+                const uint32_t a = Staging<W>::addr(x.box, x.r, c * 2 + j);
                 if (final && e.in) {
                     float f[8];
                     Elem<T>::unpack(lds128(a), f);
@@ -423,22 +430,23 @@ __device__ __forceinline__ void epilogue_16(const PairGemmParams& p, EpiState& x
                 sts128(a, Elem<T>::pack(v + 8 * j));
             }
         }
-        if (final) release_acc(x, tempty);
-        if (final) send_box<uint16_t>(x, &p.tm_out, p.out_tma, e.out, e.ldout, row0, col0, p.rows, p.cols);
-        else send_box<uint16_t>(x, &p.tm_z, p.z_tma, e.z, e.ldz, row0, col0, p.rows, p.cols);
+        if (step == 2 * N - 1) release_acc(x, tempty);
+        if (final) send_box<uint16_t, W>(x, &p.tm_out, p.out_tma, e.out, e.ldout, row0, col, p.rows, p.cols);
+        else send_box<uint16_t, W>(x, &p.tm_z, p.z_tma, e.z, e.ldz, row0, col, p.rows, p.cols);
     }
 }
 
-// 32 fp32 columns of this thread's row through the box: to the scratch of split `part`, or
+// A box of fp32 columns of this thread's row: to the scratch of split `part`, or
 // to the fp32 result (with what it held).
+template <int W>
 __device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, const float* v, int part, int lrow, int lcol,
                                           int row0, int col0) {
     const GemmEpilogue& e = p.epi;
     const bool in = e.in && part < 0;
     box_free(x);
     if (in) {
-        if (p.in_tma) {
-            arm_input(x, &p.tm_in, col0, row0);
+        if (W == 64 || p.in_tma) {
+            arm_input<W>(x, &p.tm_in, col0, row0);
             wait_input(x, p.err);
         } else {
             rows_to_box<uint32_t>(x.box, static_cast<const uint32_t*>(e.in), e.ldin, row0, col0, p.rows, p.cols, x.quad, x.lane);
@@ -446,8 +454,8 @@ __device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, 
         }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t a = box_addr(x.box, x.r, j);
+    for (int j = 0; j < W / 16; ++j) {
+        const uint32_t a = Staging<W>::addr(x.box, x.r, j);
         float f[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
         if (in) {
             float o[4];
@@ -465,14 +473,15 @@ __device__ __forceinline__ void store_f32(const PairGemmParams& p, EpiState& x, 
             bulk_commit_group();
         }
     } else {
-        send_box<uint32_t>(x, &p.tm_out, p.out_tma, e.out, e.ldout, row0, col0, p.rows, p.cols);
+        send_box<uint32_t, W>(x, &p.tm_out, p.out_tma, e.out, e.ldout, row0, col0, p.rows, p.cols);
     }
 }
 
 // T: type of 16-bit results (float: fp32 results, taken in chains of CHAIN_KB k-blocks)
-template <typename T>
+template <typename T, int W>
 __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid_constant__ PairGemmParams p) {
     constexpr bool F32 = sizeof(T) == 4;
+    constexpr int STAGES = Staging<W>::STAGES, COLS4 = W / 4;  // fp32 columns of a box
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[STAGES];
     __shared__ __align__(8) uint64_t empty_bar[STAGES];
@@ -630,7 +639,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
         x.lane = lane;
         x.r = x.quad * 32 + lane;
         x.leader = x.quad == 0 && lane == 0;
-        x.box = smem_u32(smem + STAGES * STAGE + x.grp * QBOX);
+        x.box = smem_u32(smem + STAGES * STAGE + x.grp * Staging<W>::BOX);
         x.in_bar = &in_bar[x.grp];
         x.fail = false;
         x.loads = 0;
@@ -666,26 +675,27 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                     release_acc(x, te[ab]);
                 }
 #pragma unroll
-                for (int q = 0; q < EPI_COLS / 32; ++q)
-                    store_f32(p, x, sum + 32 * q, t.part, lrow, lcol + 32 * q, row0, col0 + 32 * q);
+                for (int q = 0; q < EPI_COLS / COLS4; ++q)
+                    store_f32<W>(p, x, sum + COLS4 * q, t.part, lrow, lcol + COLS4 * q, row0, col0 + COLS4 * q);
             } else {
                 const int ab = acc & 1;
                 if (t.part < 0 && early_input(p)) {
                     // the residual, once the box's earlier store has been read
                     if (x.leader) bulk_wait_read_all();
-                    arm_input(x, &p.tm_in, col0, row0);
+                    arm_input<W>(x, &p.tm_in, col0, row0);
                 }
                 if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
                 tc_fence_after();
                 if (t.part < 0) {
-                    epilogue_16<T>(p, x, tlane + ab * BN, te[ab], row0, col0);
+                    epilogue_16<T, W>(p, x, tlane + ab * BN, te[ab], row0, col0);
                 } else {
 #pragma unroll 1
-                    for (int q = 0; q < EPI_COLS / 32; ++q) {
-                        float v[32];
-                        tmem_ld_32x32b_x32(tlane + ab * BN + q * 32, v);
-                        if (q == EPI_COLS / 32 - 1) release_acc(x, te[ab]);
-                        store_f32(p, x, v, t.part, lrow, lcol + 32 * q, row0, col0 + 32 * q);
+                    for (int q = 0; q < EPI_COLS / COLS4; ++q) {
+                        float v[COLS4];
+                        if constexpr (COLS4 == 32) tmem_ld_32x32b_x32(tlane + ab * BN + q * COLS4, v);
+                        else tmem_ld_16(tlane + ab * BN + q * COLS4, v);
+                        if (q == EPI_COLS / COLS4 - 1) release_acc(x, te[ab]);
+                        store_f32<W>(p, x, v, t.part, lrow, lcol + COLS4 * q, row0, col0 + COLS4 * q);
                     }
                 }
                 ++acc;
@@ -1217,7 +1227,7 @@ __global__ void __launch_bounds__(32 * AG_LANES, ACT_GRAD_BLOCKS) act_grad_kerne
     }
 }
 
-template <typename T>
+template <typename T, int W>
 cudaError_t run_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -1228,13 +1238,13 @@ cudaError_t run_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.blockDim = dim3(PAIR_THREADS);
-    cfg.dynamicSmemBytes = PAIR_SMEM;
+    cfg.dynamicSmemBytes = Staging<W>::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     const int most = sm_count / 2;
     cfg.gridDim = dim3(2 * (p.units < most ? p.units : most));
-    return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<T>, p);
+    return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<T, W>, p);
 }
 
 template <typename T, int BN>
@@ -1289,9 +1299,12 @@ cudaError_t linear_prepare() {
     cudaError_t e;
 #define ANVIL_SMEM(kernel, bytes) \
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return e
-    ANVIL_SMEM(pair_gemm_kernel<__nv_bfloat16>, PAIR_SMEM);
-    ANVIL_SMEM(pair_gemm_kernel<__half>, PAIR_SMEM);
-    ANVIL_SMEM(pair_gemm_kernel<float>, PAIR_SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<__nv_bfloat16, 64>), Staging<64>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<__nv_bfloat16, 128>), Staging<128>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<__half, 64>), Staging<64>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<__half, 128>), Staging<128>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<float, 64>), Staging<64>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<float, 128>), Staging<128>::SMEM);
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 16>), RowShape<16>::smem(RowShape<16>::STAGES));
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 32>), RowShape<32>::smem(RowShape<32>::STAGES));
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 64>), RowShape<64>::smem(RowShape<64>::STAGES));
@@ -1304,9 +1317,16 @@ cudaError_t linear_prepare() {
     return cudaSuccess;
 }
 
+namespace {
+template <typename T>
+cudaError_t pick_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
+    return p.box_bytes == 64 ? run_pair<T, 64>(p, sm_count, s) : run_pair<T, 128>(p, sm_count, s);
+}
+}  // namespace
+
 cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t s) {
-    if (p.epi.out_f32) return run_pair<float>(p, sm_count, s);
-    return p.f16 ? run_pair<__half>(p, sm_count, s) : run_pair<__nv_bfloat16>(p, sm_count, s);
+    if (p.epi.out_f32) return pick_pair<float>(p, sm_count, s);
+    return p.f16 ? pick_pair<__half>(p, sm_count, s) : pick_pair<__nv_bfloat16>(p, sm_count, s);
 }
 
 cudaError_t launch_finish(const FinishParams& p, cudaStream_t s) {

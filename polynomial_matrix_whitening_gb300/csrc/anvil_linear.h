@@ -42,6 +42,7 @@ struct PairGemmParams {
     int a_mn, b_mn;
     int f16;                        // operands are fp16 (else bf16)
     int in_tma, out_tma, z_tma;     // through tensor maps (16-byte aligned rows)
+    int box_bytes;                  // row of a staging box: 64 (six stages) or 128 (five)
     int tiles_r, tiles_c;           // 256 x 256 output tiles
     TileSplit split;
     int units;                      // of work: whole tiles and the turns of the tail (unit_of)
