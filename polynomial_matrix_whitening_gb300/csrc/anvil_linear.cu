@@ -20,7 +20,7 @@
 // finish_kernel adds them up, in order, and finishes the elements.  A backward pass's second
 // product starts on the SMs that the first leaves idle in its last turn, its parts cut so
 // that early and late pairs end together (8192 x 2816 x 768, squared-ReLU gradient and bias
-// gradient included: 91 us one after the other, 79 so).
+// gradient included: 91 us one after the other, 77 so).
 // What bounds it: at 16384 x 4096 x 4096 the products, within a few percent of the
 // library's own rate; a tile narrower than 256 columns gains nothing (128 columns measured
 // 660 SM cycles per 64-deep k-block against 560: a k-block's time is the L2 round trip of
