@@ -323,8 +323,8 @@ Plan plan_product(int64_t rows, int cols, int64_t k, bool few, bool k_major, dou
 // The two products of a backward pass.  The second kernel's pairs start where the first
 // leaves SMs idle, so a last turn of the first that is not full costs nothing when the
 // second's parts are cut to fill it; or both run as they would alone.
-void plan_both(int64_t rows1, int cols1, int64_t k1, bool k_major1, double epilogue1, int64_t rows2, int cols2, int64_t k2, double epilogue2,
-               Plan* first, Plan* second) {
+void plan_both(int64_t rows1, int cols1, int64_t k1, bool k_major1, double epilogue1, int64_t rows2, int cols2, int64_t k2,
+               double epilogue2, Plan* first, Plan* second) {
     *first = plan_product(rows1, cols1, k1, true, k_major1, epilogue1, ALL_FREE);
     *second = plan_product(rows2, cols2, k2, false, false, epilogue2, ALL_FREE);
     if (first->few) return;
@@ -515,7 +515,8 @@ LinearLayout linear_layout(const anvil_linear_desc* d) {
     L.off_x = 0;
     L.off_w = L.off_x + copy_bytes(L.x);
     L.off_part = L.off_w + copy_bytes(L.w);
-    L.plan = plan_product(d->rows, d->n, d->k, true, !d->weight_transposed, epilogue_cycles(forward_epilogue(d), d->rows), ALL_FREE);
+    const double cycles = epilogue_cycles(forward_epilogue(d), d->rows);
+    L.plan = plan_product(d->rows, d->n, d->k, true, !d->weight_transposed, cycles, ALL_FREE);
     L.total = L.off_part + L.plan.part;
     return L;
 }

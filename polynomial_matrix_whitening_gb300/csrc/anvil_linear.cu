@@ -277,7 +277,8 @@ __device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, 
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int c = h * 32 + lane;
-                const uint32_t a = Staging<128>::addr(box, quad * 32 + i0 + i, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
+                const int b = c * static_cast<int>(sizeof(E));
+                const uint32_t a = Staging<128>::addr(box, quad * 32 + i0 + i, b / 16) + b % 16;
                 if constexpr (sizeof(E) == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[i][h]) : "r"(a) : "memory");
                 else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[i][h]) : "r"(a) : "memory");
             }
@@ -309,7 +310,8 @@ __device__ __forceinline__ void rows_to_box(uint32_t box, const E* src, long lon
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int c = h * 32 + lane;
-                const uint32_t a = Staging<128>::addr(box, quad * 32 + i0 + i, c * static_cast<int>(sizeof(E)) / 16) + (c * sizeof(E)) % 16;
+                const int b = c * static_cast<int>(sizeof(E));
+                const uint32_t a = Staging<128>::addr(box, quad * 32 + i0 + i, b / 16) + b % 16;
                 if constexpr (sizeof(E) == 2) sts16(a, v[i][h]);
                 else asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v[i][h]) : "memory");
             }
@@ -1075,7 +1077,8 @@ __global__ void __launch_bounds__(TOKEN_THREADS) token_kernel(const TokenParams 
             staged = true;
             for (int i = threadIdx.x; i < chunks * R; i += TOKEN_THREADS) {
                 const int r = i / chunks, c = i - r * chunks;
-                sts128(xa + i * 16, __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + min(r, p.rows - 1) * p.ldx) + c));
+                const T* x = static_cast<const T*>(p.x) + min(r, p.rows - 1) * p.ldx;
+                sts128(xa + i * 16, __ldg(reinterpret_cast<const uint4*>(x) + c));
             }
             __syncthreads();
         }

@@ -52,8 +52,9 @@ struct Shape {
 // Resident blocks per SM: the backward row pass 512 threads, at up to 128 registers each;
 // the forward one 1024 threads at 64 where a thread has at most 8 columns, else 512.
 constexpr int bwd_blocks_per_sm(int tpr) { return tpr <= 32 ? 2 : 512 / tpr; }
+constexpr int fwd_threads_per_sm(int columns) { return columns <= 8 ? 1024 : columns <= 16 ? 768 : 512; }
 constexpr int fwd_blocks_per_sm(int tpr, int columns) {
-    return tpr <= 32 ? 3 : (columns <= 8 ? 1024 : columns <= 16 ? 768 : 512) / tpr > 0 ? (columns <= 8 ? 1024 : columns <= 16 ? 768 : 512) / tpr : 1;
+    return tpr <= 32 ? 3 : tpr < fwd_threads_per_sm(columns) ? fwd_threads_per_sm(columns) / tpr : 1;
 }
 
 // A unit as it was loaded, unpacked where it is used (half the registers of fp32 values of
@@ -238,7 +239,8 @@ __global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, fwd_blocks_pe
 // of the block touches; such a block reads its weights for every row.  4096 x 16384 bf16: 146
 // us (sums laid out by column, a lane's eight neighbours: 319, the banks' conflicts).
 template <typename T, typename W, bool VEC, int TPR, int NV, bool SUMS_SMEM>
-__global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_per_sm(TPR)) norm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(Shape<T, VEC, TPR, NV>::THREADS, bwd_blocks_per_sm(TPR))
+    norm_bwd_kernel(const NormBwdParams p) {
     using S = Shape<T, VEC, TPR, NV>;
     using Raw = RawUnit<T, VEC>;
     constexpr int E = S::E;
@@ -509,7 +511,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ uint32_t slot_offset(const void* row) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15);
 }
-__device__ __forceinline__ uint32_t cover_bytes(const void* row, uint32_t bytes) { return (slot_offset(row) + bytes + 15u) & ~15u; }
+__device__ __forceinline__ uint32_t cover_bytes(const void* row, uint32_t bytes) {
+    return (slot_offset(row) + bytes + 15u) & ~15u;
+}
 __device__ __forceinline__ void cover_load(uint32_t dst, const void* row, uint32_t bytes, uint64_t* bar) {
     bulk_load(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(row) & ~static_cast<uintptr_t>(15)),
               cover_bytes(row, bytes), bar);
@@ -911,7 +915,8 @@ cudaError_t run_fwd(const NormFwdParams& p, cudaStream_t s) {
     using S = Shape<T, VEC, TPR, NV>;
     const long long want = (p.rows + S::TEAMS - 1) / S::TEAMS;
     const long long cap = 152ll * fwd_blocks_per_sm(TPR, NV * S::E);  // one wave of resident blocks
-    return launch_pdl(norm_fwd_kernel<T, W, VEC, TPR, NV>, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(S::THREADS), 0, s, p);
+    const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
+    return launch_pdl(norm_fwd_kernel<T, W, VEC, TPR, NV>, grid, dim3(S::THREADS), 0, s, p);
 }
 
 template <typename T, typename W, bool VEC, int TPR, int NV, bool SUMS_SMEM = false>
@@ -984,11 +989,12 @@ namespace {
 
 // Threads of a team of the ring kernels: up to 16 columns each, off the 16-byte boundaries
 // 8 where a block can hold that many threads twice.
-// (2049 to 3072 columns: 192 threads run 32768 x 2816 bf16 forward in 65 us, 256 in 78;
+// (2049 to 192 * 16 columns: 192 threads run 32768 x 2816 bf16 forward in 65 us, 256 in 78;
 // backward 256 are faster, 121 against 125.)
 int ring_tpr(int width, int arrays, bool vec) {
     if (!vec && width <= 2048) return width <= 512 ? 64 : width <= 1024 ? 128 : 256;
-    return width <= 1024 ? 64 : width <= 2048 ? 128 : width <= 3072 && arrays == 1 ? 192 : width <= 4096 ? 256 : 512;
+    if (width <= 2048) return width <= 1024 ? 64 : 128;
+    return width <= 192 * 16 && arrays == 1 ? 192 : width <= 4096 ? 256 : 512;
 }
 
 // Teams of the ring kernels on the whole device, and whether they run: two stages fit, rows
@@ -1002,7 +1008,8 @@ int ring_tpr(int width, int arrays, bool vec) {
 bool ring_plan(long long rows, int width, int dtype, bool vec, int arrays, int* blocks, int* team_rows) {
     const int es = dtype_size(dtype), tpr = ring_tpr(width, arrays, vec);
     const int least = arrays == 1 ? 32 : vec ? 8 : width <= 512 ? 4 : width <= 1024 ? 24 : 6;
-    if ((vec ? width <= 512 : width * es < 512) || width > 8192 || ring_stages(tpr, arrays, ring_slot(vec, width * es)) < 2) return false;
+    if ((vec ? width <= 512 : width * es < 512) || width > 8192) return false;
+    if (ring_stages(tpr, arrays, ring_slot(vec, width * es)) < 2) return false;
     const int per_block = ring_teams(tpr);
     const long long teams = 152ll * ring_blocks(tpr) * per_block;
     if (rows < least * teams) return false;
