@@ -263,12 +263,13 @@ __device__ __forceinline__ Unit unit_of(const PairGemmParams& p, int u) {
     return r;
 }
 
-// Rows that TMA cannot take (not 16-byte aligned; W = 128 then): the 32 box rows of this warp to or from
-// global memory, neighbouring lanes on neighbouring elements, eight rows in flight.
-template <typename E>
+// Results that TMA cannot store: the 32 box rows of this warp to global memory, neighbouring lanes
+// on neighbouring elements, eight rows in flight.
+template <typename E, int W>
 __device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, int row0, int col0, int rows, int cols,
                                             int quad, int lane) {
-    constexpr int H = 128 / sizeof(E) / 32;  // elements per lane of a box row
+    constexpr int C = W / sizeof(E);           // columns of a box
+    constexpr int H = C > 32 ? C / 32 : 1;     // elements per lane of a box row
 #pragma unroll 1
     for (int i0 = 0; i0 < 32; i0 += 8) {
         E v[8][H];
@@ -276,9 +277,9 @@ __device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, 
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const int c = h * 32 + lane;
+                const int c = C < 32 ? lane % C : h * 32 + lane;
                 const int b = c * static_cast<int>(sizeof(E));
-                const uint32_t a = Staging<128>::addr(box, quad * 32 + i0 + i, b / 16) + b % 16;
+                const uint32_t a = Staging<W>::addr(box, quad * 32 + i0 + i, b / 16) + b % 16;
                 if constexpr (sizeof(E) == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[i][h]) : "r"(a) : "memory");
                 else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[i][h]) : "r"(a) : "memory");
             }
@@ -286,11 +287,12 @@ __device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, 
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const int r = row0 + quad * 32 + i0 + i, c = col0 + h * 32 + lane;
-                if (r < rows && c < cols) dst[static_cast<size_t>(r) * ld + c] = v[i][h];
+                const int r = row0 + quad * 32 + i0 + i, c = h * 32 + lane;
+                if (r < rows && c < C && col0 + c < cols) dst[static_cast<size_t>(r) * ld + col0 + c] = v[i][h];
             }
     }
 }
+// A residual or gradient whose rows are not 16-byte aligned (W = 128 then), the same way back.
 template <typename E>
 __device__ __forceinline__ void rows_to_box(uint32_t box, const E* src, long long ld, int row0, int col0, int rows,
                                             int cols, int quad, int lane) {
@@ -341,11 +343,15 @@ __device__ __forceinline__ void tma_store_box(const CUtensorMap* tm, uint32_t bo
 }
 
 // Sends the box out: by TMA (the group's leader, after every thread's writes), or by the
-// warps themselves, each its own rows.
+// warps themselves, each its own rows.  A tensor-map store is clipped to the map's width by 16-byte
+// pieces (measured: a row of 97 16-bit elements has 104 written), so a box with a row end inside a
+// piece is the warps' too: the bytes after it are not the result's.
 template <typename E, int W>
 __device__ __forceinline__ void send_box(const EpiState& x, const CUtensorMap* tm, int by_tma, void* dst, long long ld,
                                          int row0, int col0, int rows, int cols) {
-    if (W == 64 || by_tma) {
+    constexpr int C = W / sizeof(E), PIECE = 16 / sizeof(E);
+    const bool cut = cols % PIECE != 0 && col0 < cols && col0 + C > cols;
+    if ((W == 64 || by_tma) && !cut) {
         fence_proxy_async_smem();
         named_barrier_sync(1 + x.grp, 128);
         if (x.leader) {
@@ -354,7 +360,7 @@ __device__ __forceinline__ void send_box(const EpiState& x, const CUtensorMap* t
         }
     } else {
         __syncwarp();
-        box_to_rows<E>(x.box, static_cast<E*>(dst), ld, row0, col0, rows, cols, x.quad, x.lane);
+        box_to_rows<E, W>(x.box, static_cast<E*>(dst), ld, row0, col0, rows, cols, x.quad, x.lane);
         fence_proxy_async_smem();  // before an input load into the box
         __syncwarp();
     }
