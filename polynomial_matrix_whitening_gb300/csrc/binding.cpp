@@ -294,11 +294,20 @@ struct Weight {
     int64_t n, k, ld;
     int transposed;
 };
+// The leading dimension of w [n, k] stored by rows (by columns: as [k, n]); -1: it is not stored
+// so.  A single row or column is stored in both orders, each with its own leading dimension.
+int64_t ld_in_order(const at::Tensor& w, int by_columns) {
+    const int64_t inner = w.size(by_columns ? 0 : 1), outer = w.size(by_columns ? 1 : 0);
+    const int64_t step = w.stride(by_columns ? 0 : 1), ld = w.stride(by_columns ? 1 : 0);
+    if ((step != 1 && inner > 1) || (ld < inner && outer > 1)) return -1;
+    return ld > inner ? ld : inner;
+}
 Weight weight_of(const at::Tensor& w, at::ScalarType type, const char* what) {
     if (w.dim() != 2 || w.scalar_type() != type) refuse("%s must be [n, k] of %s", what, c10::toString(type));
-    const int64_t n = w.size(0), k = w.size(1), s0 = w.stride(0), s1 = w.stride(1);
-    if ((s1 == 1 || k == 1) && (s0 >= k || n == 1)) return {n, k, s0 > k ? s0 : k, 0};
-    if ((s0 == 1 || n == 1) && (s1 >= n || k == 1)) return {n, k, s1 > n ? s1 : n, 1};
+    for (int by_columns = 0; by_columns < 2; ++by_columns) {
+        const int64_t ld = ld_in_order(w, by_columns);
+        if (ld >= 0) return {w.size(0), w.size(1), ld, by_columns};
+    }
     refuse("%s must be stored by rows or by columns; use .contiguous()", what);
 }
 
@@ -358,7 +367,7 @@ PyObject* linear_backward(PyObject* const* a) {
     if (d.dtype == ANVIL_F32) refuse("x must be bf16 or fp16");
     const at::ScalarType type = x.scalar_type();
     const Rows r = rows_of(x, "x");
-    const Weight m = weight_of(w, type, "weight");
+    Weight m = weight_of(w, type, "weight");
     if (m.k != r.width) refuse("weight must be [n, %lld]", static_cast<long long>(r.width));
     c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
     shape.back() = m.n;
@@ -389,10 +398,14 @@ PyObject* linear_backward(PyObject* const* a) {
     if (need_dw) {
         if (dw_in) {
             const Weight g = weight_of(*dw_in, wt, "dweight");
-            if (g.n != m.n || g.k != m.k || (g.transposed != m.transposed && m.n > 1 && m.k > 1))
-                refuse("dweight must have weight's shape and order");
+            // both in weight's order, or in the other one where both are stored so too (single rows)
+            if (ld_in_order(*dw_in, m.transposed) < 0 && ld_in_order(w, !m.transposed) >= 0) {
+                m.transposed = !m.transposed;
+                m.ld = ld_in_order(w, m.transposed);
+            }
+            d.lddw = ld_in_order(*dw_in, m.transposed);
+            if (g.n != m.n || g.k != m.k || d.lddw < 0) refuse("dweight must have weight's shape and order");
             dw = *dw_in;
-            d.lddw = g.ld;
         } else {
             dw = m.transposed ? here.empty({m.k, m.n}, wt).t() : here.empty({m.n, m.k}, wt);
             d.lddw = m.transposed ? m.n : m.k;

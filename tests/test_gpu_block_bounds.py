@@ -111,3 +111,70 @@ def test_linear_dweight_by_columns_writes_its_view(A, rows, dw_type):  # noqa: F
             linear_grad_check(A, dy, x, w, None, None, "bf16", dw_type, got)
             assert dw.untouched_around(), (n, pitch, offset)
     assert A.device_error() == A.OK
+
+
+def stored(kind, n, k, dtype, fill):
+    """A view [n, k] of a larger buffer, both filled with `fill` (a value, or a function of a shape):
+    (buffer, view)."""
+    if kind == "rows":            # contiguous rows, guard rows before and after
+        buf = fill((n + 4, k)).to(DT[dtype])
+        return buf, buf[2:2 + n]
+    if kind == "wide rows":       # rows of a wider buffer
+        buf = fill((n + 4, k + 9)).to(DT[dtype])
+        return buf, buf[2:2 + n, 8:8 + k]
+    if kind == "columns":         # the transpose of contiguous rows
+        buf = fill((k + 4, n)).to(DT[dtype])
+        return buf, buf[2:2 + k].t()
+    buf = fill((k + 4, n + 9)).to(DT[dtype])  # "wide columns"
+    return buf, buf[2:2 + k, 8:8 + n].t()
+
+
+KINDS = ("rows", "wide rows", "columns", "wide columns")
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("rows", [3, 300])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 96), (1, 515), (96, 1), (515, 1), (72, 96), (33, 65)], ids=lambda s: "x".join(map(str, s)))
+def test_dweight_in_its_own_place(A, shape, rows, accumulate):  # noqa: F811
+    """Every storage of weight with every storage of the caller's dweight: the gradient lands in the
+    view and nowhere else, or (orders that differ, more than one row and column) is refused."""
+    n, k = shape
+    dy, x = randn(1, rows, n, dtype="bf16"), randn(2, rows, k, dtype="bf16")
+    dense = randn(3, n, k, dtype="bf16", scale=k ** -0.5)
+    for wk in KINDS:
+        _, w = stored(wk, n, k, "bf16", lambda s: torch.zeros(s, device="cuda"))
+        w.copy_(dense)
+        for gk in KINDS:
+            for dw_type in ("f32", "bf16"):
+                buf, view = stored(gk, n, k, dw_type, lambda s: torch.full(s, 7.0, device="cuda"))
+                before = buf.clone()
+                db = torch.full((n,), 5.0, device="cuda")
+                if n > 1 and k > 1 and wk.split()[-1] != gk.split()[-1]:
+                    with pytest.raises(ValueError, match="shape and order"):
+                        A.linear_backward(dy, x, w, dweight=view, dbias=db, accumulate=accumulate)
+                    assert torch.equal(buf, before)
+                    continue
+                dx, dw, db = A.linear_backward(dy, x, w, dweight=view, dbias=db, accumulate=accumulate)
+                assert dw.data_ptr() == view.data_ptr() and dw.stride() == view.stride()
+                want = A.linear_backward(dy, x, dense, dweight_dtype=DT[dw_type])
+                if accumulate:
+                    full = torch.full((n, k), 7.0, device="cuda").to(DT[dw_type])
+                    want = A.linear_backward(dy, x, dense, dweight=full, dbias=torch.full((n,), 5.0, device="cuda"),
+                                             accumulate=True)
+                    p, mag = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
+                    u = {"f32": 2.0 ** -23, "bf16": 2.0 ** -8}[dw_type]
+                    # as for the products without it: 2 E per 16 rows, one rounding of the sum
+                    bar = u * (p + 7).abs() + (2 * (rows / 16 + 4) + 8) * 2.0 ** -24 * (mag + 7)
+                    assert ((want[1].double() - p - 7).abs() <= bar).all()
+                else:
+                    linear_grad_check(A, dy, x, dense, None, None, "bf16", dw_type, want)
+                # another order of the operands may add up in another order: one rounding each
+                tol = {"f32": 2.0 ** -20, "bf16": 2.0 ** -7}[dw_type]
+                scale = dy.double().abs().t() @ x.double().abs() + (7 if accumulate else 0)
+                assert ((dw.double() - want[1].double()).abs() <= tol * scale).all(), (wk, gk)
+                dxs = dy.double().abs() @ dense.double().abs()
+                assert ((dx.double() - want[0].double()).abs() <= 2.0 ** -7 * dxs).all()
+                assert torch.equal(db, want[2])
+                view.fill_(7.0)
+                assert torch.equal(buf, before), (wk, gk, dw_type)
+    assert A.device_error() == A.OK
