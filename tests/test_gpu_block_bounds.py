@@ -178,3 +178,103 @@ def test_dweight_in_its_own_place(A, shape, rows, accumulate):  # noqa: F811
                 view.fill_(7.0)
                 assert torch.equal(buf, before), (wk, gk, dw_type)
     assert A.device_error() == A.OK
+
+
+def padded(seed, rows, width, dtype, pitch, offset):
+    """Normal values in a view of wider rows whose other elements are NaN."""
+    buf = torch.full((rows, pitch), float("nan"), device="cuda", dtype=DT[dtype])
+    view = buf[:, offset:offset + width]
+    view.copy_(randn(seed, rows, width, dtype=dtype))
+    return view
+
+
+# narrow and wide teams, and rows enough for the kernels that keep several rows on their way
+NORM_VIEWS = [(1, 7), (37, 63), (300, 255), (9, 1023), (300, 1024), (41, 2815), (3, 5001), (2, 9999), (2, 16384),
+              (20001, 300), (14801, 1023), (29301, 1024), (14701, 2815), (14701, 2816)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", NORM_VIEWS, ids=lambda s: "x".join(map(str, s)))
+def test_norm_writes_its_views(A, shape, dtype):  # noqa: F811
+    """The same results as from contiguous copies, to the last rounding, and nothing beside them."""
+    rows, n = shape
+    w, b = 1 + randn(3, n, scale=0.2), randn(4, n, scale=0.2)
+    u = {"f32": 2.0 ** -18, "bf16": 2.0 ** -7, "f16": 2.0 ** -10}[dtype]  # sums of another order, one rounding each
+    for j, (pitch, offset) in enumerate(pitches(n, dtype)):
+        other = pitches(n, dtype)[(j + 2) % 4]
+        x, dy, res = padded(5, rows, n, dtype, pitch, offset), padded(6, rows, n, dtype, *other), padded(7, rows, n, dtype, pitch, offset)
+        y, dx = Guarded(rows, n, dtype, pitch, offset), Guarded(rows, n, dtype, *other)
+        _, mean, rstd = A.layernorm_forward(x, w, b, out=y.view)
+        wy, wm, wr = A.layernorm_forward(x.contiguous(), w, b)
+        with_res = res if j % 2 else None
+        _, dw, db = A.layernorm_backward(dy, x, wm, wr, w, residual_grad=with_res, out=dx.view)
+        want = A.layernorm_backward(dy.contiguous(), x.contiguous(), wm, wr, w,
+                                    residual_grad=with_res.contiguous() if j % 2 else None)
+        # y: the mean's and the variance's order of addition; a value of 0 has that of its terms
+        assert ((y.view.double() - wy.double()).abs() <= u * (wy.double().abs() + 1)).all()
+        assert torch.allclose(mean, wm, atol=1e-5, rtol=0) and torch.allclose(rstd, wr, rtol=1e-5, atol=0)
+        assert ((dx.view.double() - want[0].double()).abs() <= u * (want[0].double().abs() + wr.double()[:, None] * 4 + 1)).all()
+        # sqrt(rows) of the terms' size, and the rounding of their sums
+        assert torch.allclose(dw, want[1], rtol=1e-4, atol=2e-5 * rows ** 0.5 + 1e-5)
+        assert torch.allclose(db, want[2], rtol=1e-4, atol=2e-5 * rows ** 0.5 + 1e-5)
+        assert y.untouched_around() and dx.untouched_around(), (pitch, offset)
+    assert A.device_error() == A.OK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", [(1, 1), (3, 7), (2, 129), (5, 5003), (160, 4099), (1, 50257)], ids=lambda s: "x".join(map(str, s)))
+def test_logprob_writes_its_view(A, shape, dtype):  # noqa: F811
+    rows, vocab = shape
+    t = torch.arange(rows, device="cuda") * 37 % vocab
+    gl, gh = randn(1, rows), randn(2, rows)
+    for j, (pitch, offset) in enumerate(pitches(vocab, dtype)):
+        x = padded(3, rows, vocab, dtype, pitch, offset)
+        top = min(vocab, 9)
+        got, want = A.token_logprobs(x, t, top=top), A.token_logprobs(x.contiguous(), t, top=top)
+        assert torch.equal(got[4], want[4])
+        for p, q in zip(got[:4], want[:4]):  # sums of another order: at most 30 in magnitude, 192 roundings
+            assert torch.allclose(p, q, rtol=0, atol=30 * 192 * 2.0 ** -24)
+        d = Guarded(rows, vocab, dtype, *pitches(vocab, dtype)[(j + j // 2) % 4])
+        A.token_logprobs_backward(x, t, want[2], gl, entropy=want[1], grad_entropy=gh, out=d.view)
+        ref = A.token_logprobs_backward(x.contiguous(), t, want[2], gl, entropy=want[1], grad_entropy=gh)
+        u = {"f32": 2.0 ** -18, "bf16": 2.0 ** -7, "f16": 2.0 ** -10}[dtype]
+        assert ((d.view.double() - ref.double()).abs() <= u * ref.double().abs() + 2.0 ** -23).all()
+        assert d.untouched_around(), (pitch, offset)
+    assert A.device_error() == A.OK
+
+
+def test_offsets_past_32_bits_backward_and_results(A):  # noqa: F811
+    """Every array of the backward passes, and the results, as rows 2^28 elements apart."""
+    ld, rows, n = 1 << 28, 10, 768
+
+    def far(seed, width, dtype=torch.bfloat16, scale=1.0):
+        buf = torch.empty(ld * (rows - 1) + width, dtype=dtype, device="cuda")
+        view = torch.as_strided(buf, (rows, width), (ld, 1))
+        if seed is not None:
+            view.copy_(randn(seed, rows, width, scale=scale))
+        return view
+    x, dy, out = far(1, n), far(2, n), far(None, n)
+    y, mean, rstd = A.layernorm_forward(x, out=out)
+    assert torch.equal(y, A.layernorm_forward(x.contiguous())[0])
+    got = A.layernorm_backward(dy, x, mean, rstd, residual_grad=dy, out=out)
+    want = A.layernorm_backward(dy.contiguous(), x.contiguous(), mean, rstd, residual_grad=dy.contiguous())
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    w = randn(3, n, n, dtype="bf16", scale=n ** -0.5)
+    assert torch.equal(A.linear_forward(x, w, residual=dy, out=out),
+                       A.linear_forward(x.contiguous(), w, residual=dy.contiguous()))
+    dw = torch.empty((n, n), device="cuda")
+    native_linear_backward(A, dy, x, w, out, dw)
+    rdx, rdw, _ = A.linear_backward(dy.contiguous(), x.contiguous(), w, bias_grad=False, dweight_dtype=torch.float32)
+    assert torch.equal(out, rdx) and torch.equal(dw, rdw)
+    del x, dy, out, got, y
+    # a weight and its gradient whose rows are that far apart
+    w, dw = far(4, 264, scale=0.1), far(None, 264, torch.float32)
+    x, dy = randn(5, 300, 264, dtype="bf16"), randn(6, 300, rows, dtype="bf16")
+    dx, _, _ = A.linear_backward(dy, x, w, dweight=dw, bias_grad=False)
+    rdx, rdw, _ = A.linear_backward(dy, x, w.contiguous(), bias_grad=False, dweight_dtype=torch.float32)
+    assert torch.equal(dx, rdx) and torch.equal(dw, rdw)
+    dlogits = A.token_logprobs_backward(w, torch.arange(rows, device="cuda"), randn(7, rows), randn(8, rows),
+                                        out=far(None, 264))
+    assert torch.equal(dlogits, A.token_logprobs_backward(w.contiguous(), torch.arange(rows, device="cuda"), randn(7, rows),
+                                                          randn(8, rows)))
+    assert A.device_error() == A.OK
