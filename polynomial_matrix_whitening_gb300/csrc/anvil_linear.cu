@@ -743,12 +743,12 @@ __device__ __forceinline__ void tail_sum(const TailSumParams& p, int block) {
     const int rows = min(TAIL_ROWS, p.rows - tr * PAIR_ROWS - r0);  // of this block that exist
     const long long row = static_cast<long long>(tr) * PAIR_ROWS + r0;
     if (rows <= 0 || col >= p.cols) return;  // (the block's other threads wait for the parts)
+    pdl_wait_previous();  // (the product may have let this kernel start before what came before it had ended)
     float bias = 0.f;
     if constexpr (sizeof(T) == 2) {
         if (e.bias)
             bias = e.bias_f32 ? static_cast<const float*>(e.bias)[col] : Elem<T>::load(static_cast<const T*>(e.bias)[col]);
     }
-    pdl_wait_previous();
     const bool first = tile < p.split.tiles_a;
     const int splits = first ? p.split.sa : p.split.sb;
     const int part0 = first ? tile * splits : p.split.tiles_a * p.split.sa + (tile - p.split.tiles_a) * splits;

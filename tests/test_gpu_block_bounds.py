@@ -278,3 +278,24 @@ def test_offsets_past_32_bits_backward_and_results(A):  # noqa: F811
     assert torch.equal(dlogits, A.token_logprobs_backward(w.contiguous(), torch.arange(rows, device="cuda"), randn(7, rows),
                                                           randn(8, rows)))
     assert A.device_error() == A.OK
+
+
+def test_linear_bias_of_the_call_before(A):  # noqa: F811
+    """A bias (and residual) that the preceding call made, for products in one piece and in parts."""
+    for rows, n, k in ((1000, 2815, 771), (300, 768, 4096), (513, 1000, 2048), (8192, 2816, 768), (3, 2816, 768)):
+        x, w = randn(1, rows, k, dtype="bf16"), randn(2, n, k, dtype="bf16", scale=k ** -0.5)
+        to_bias = randn(3, n, 4096, dtype="bf16", scale=4096 ** -0.5)
+        to_res = randn(4, n, 64, dtype="bf16", scale=0.125)
+        plain = A.linear_forward(x, w).double()
+        mag = x.double().abs() @ w.double().abs().t()
+        bias = torch.empty((1, n), device="cuda", dtype=torch.bfloat16)
+        res = torch.empty((rows, n), device="cuda", dtype=torch.bfloat16)
+        for step in range(6):
+            c, r = randn(10 + step, 1, 4096, dtype="bf16", scale=3.0), randn(20 + step, rows, 64, dtype="bf16")
+            A.linear_forward(r, to_res, out=res)
+            A.linear_forward(c, to_bias, out=bias)
+            y = A.linear_forward(x, w, bias[0], residual=res)
+            want = plain + bias.double() + res.double()
+            # plain is rounded once itself; the products of the two calls may be split differently
+            close(y, want, "bf16", 2.0 ** 16 * plain.abs() + mag + bias.double().abs() + res.double().abs(), 4 * (k / 16 + 4), step)
+    assert A.device_error() == A.OK
