@@ -4,7 +4,8 @@ Each .cu under csrc/ compiles to its own object in parallel; the objects link in
 ``polynomial_matrix_whitening_gb300/libanvil.so`` with the CUDA runtime linked
 statically, so the library loads (and exports its symbols) on a machine without a
 GPU driver as well.  csrc/binding.cpp, the native part of the Python binding, compiles with
-g++ against the installed PyTorch's headers into ``_anvil_binding.so`` beside it.
+g++ against the installed PyTorch's headers into ``_anvil_binding.so`` beside it; without a CUDA
+build of PyTorch it is left out, and with it the Python calls of the operators around the banks.
 """
 from __future__ import annotations
 
@@ -52,12 +53,15 @@ def _stale(target, deps):
 
 
 def binding_command():
-    """The g++ call that compiles csrc/binding.cpp into a file named last."""
+    """The g++ call that compiles csrc/binding.cpp into a file named last; None without PyTorch,
+    or with one that has no CUDA."""
     import sysconfig
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch not found: its headers are required to build the binding")
+        return None
     torch = spec.submodule_search_locations[0]
+    if not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
+        return None
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
@@ -88,11 +92,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), timeline: 
     binding_tmp = BINDING + f".tmp{os.getpid()}"
     # named by the interpreter's torch too: a module built against another one is stale
     stamp = os.path.join(BUILD, "binding.torch")
-    flags = " ".join(binding_command())
-    make_binding = force or _stale(BINDING, [binding] + headers) or not os.path.exists(stamp) \
-        or open(stamp).read() != flags
+    compile_binding = binding_command()
+    make_binding = compile_binding is not None and (
+        force or _stale(BINDING, [binding] + headers) or not os.path.exists(stamp)
+        or open(stamp).read() != " ".join(compile_binding))
     if make_binding:
-        jobs.append(binding_command() + [binding_tmp])
+        jobs.append(compile_binding + [binding_tmp])
+    failed = []  # the binding's failure is raised once the library, which needs nvcc alone, is there
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
             results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -100,13 +106,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), timeline: 
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"{os.path.basename(cmd[0])} failed on "
-                                   + next(a for a in cmd if a.endswith((".cu", ".cpp"))))
-    if make_binding:
-        os.replace(binding_tmp, BINDING)
-        os.makedirs(BUILD, exist_ok=True)
-        with open(stamp, "w") as f:
-            f.write(flags)
+                failed.append(f"{os.path.basename(cmd[0])} failed on "
+                              + next(a for a in cmd if a.endswith((".cu", ".cpp"))))
+    binding_failed = make_binding and results[-1].returncode != 0
+    if len(failed) > binding_failed:
+        raise RuntimeError("; ".join(failed))
     objs = [os.path.join(build_dir, os.path.basename(s)[:-3] + ".o") for s in sources]
     if force or linked or _stale(lib, objs):
         tmp = lib + f".tmp{os.getpid()}"
@@ -116,6 +120,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), timeline: 
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError(f"nvcc link of {os.path.basename(lib)} failed")
         os.replace(tmp, lib)
+    if binding_failed:
+        raise RuntimeError(failed[-1])
+    if make_binding:
+        os.replace(binding_tmp, BINDING)
+        os.makedirs(BUILD, exist_ok=True)
+        with open(stamp, "w") as f:
+            f.write(" ".join(compile_binding))
     return lib
 
 
