@@ -98,18 +98,22 @@ __host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool a_mn, bool b_
            ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
-// Phi(z), the normal distribution, and e = exp(-z^2/2): the complementary error function by
-// Hastings' rational approximation (Abramowitz and Stegun 7.1.26, |error| <= 1.5e-7 in
-// erf), the tail taken directly so that Phi keeps its relative accuracy far below zero.
+// Phi(z), the normal distribution, and e = exp(-z^2/2).  Phi(-|z|) = e m(|z|) with m(a) =
+// exp(a^2/2) erfc(a / sqrt 2) / 2, which falls slowly: m = t P(t), t = 1 / (1 + 0.305 a), P the
+// polynomial of degree 7 of the least largest relative error over 0 <= a <= 16 (1.4e-7; fitted
+// by iterated weighted least squares).  So the tail has a relative error of (48 + 2 z^2) 2^-24 at
+// most, the exponential's own growth with its argument included, as far down as e reaches.
 __device__ __forceinline__ float normal_cdf(float z, float* e) {
-    const float a = fabsf(z) * 0.70710678118654752f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, a, 1.f));
-    float q = fmaf(t, 1.061405429f, -1.453152027f);
-    q = fmaf(t, q, 1.421413741f);
-    q = fmaf(t, q, -0.284496736f);
-    q = fmaf(t, q, 0.254829592f);
-    *e = __expf(-a * a);
-    const float tail = 0.5f * t * q * *e;
+    const float t = __fdividef(1.f, fmaf(0.305f, fabsf(z), 1.f));
+    float q = fmaf(t, 0.036033929f, -0.150315657f);
+    q = fmaf(t, q, 0.181285652f);
+    q = fmaf(t, q, -0.0340613788f);
+    q = fmaf(t, q, 0.119038255f);
+    q = fmaf(t, q, 0.103994657f);
+    q = fmaf(t, q, 0.122379342f);
+    q = fmaf(t, q, 0.121645144f);
+    *e = __expf(-0.5f * (z * z));
+    const float tail = t * q * *e;
     return z < 0.f ? tail : 1.f - tail;
 }
 

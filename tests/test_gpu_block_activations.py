@@ -1,0 +1,65 @@
+"""GPU tests of the linear layer's activations and their slopes over the whole range of z, with bars
+relative to the value itself, so that a tail counts as much as the middle."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_block_ops import A, DT, E, U  # noqa: E402,F401  (A: fixture)
+
+TINY = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}  # half the spacing of the type's subnormals
+
+
+def every_value(dtype, most):
+    """Every finite value of the type with |z| <= most, in rows of 64 (the last one filled up with zeros)."""
+    z = torch.arange(-(1 << 15), 1 << 15, device="cuda").to(torch.int16).view(DT[dtype])
+    z = z[z.abs() <= most]
+    return torch.nn.functional.pad(z, (0, -z.numel() % 64)).reshape(-1, 64)
+
+
+def reference(z, act):
+    """(value, slope, the size of the slope's terms) in 64 bits."""
+    z = z.double()
+    phi, cdf = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi), 0.5 * torch.special.erfc(-z / math.sqrt(2))
+    return z * cdf, cdf + z * phi, cdf + z.abs() * phi
+
+
+def outputs(A, x, act):  # noqa: F811
+    """act(x) through a product with the identity, by each of the layer's kernels."""
+    w = torch.eye(64, device="cuda").to(x.dtype)
+    some = x[::max(1, x.shape[0] // 9)]
+    yield x, A.linear_forward(x, w, activation=act)                                          # tiles
+    yield some, torch.cat([A.linear_forward(r[None], w, activation=act) for r in some])      # one token
+    for i in range(0, x.shape[0], 17 * 16):
+        yield x[i:i + 17], A.linear_forward(x[i:i + 17], w, activation=act)                  # few rows
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("act,most", [("gelu", 13.0)])
+def test_activation_tails(A, act, most, dtype):  # noqa: F811
+    """Every value within its own rounding and a relative error of the fp32 arithmetic: 48 E for the
+    reciprocal, the polynomial and the products, 2 z^2 E for the exponential of z^2 / 2."""
+    x = every_value(dtype, most)
+    for z, y in outputs(A, x, act):
+        ref = reference(z, act)[0]
+        bar = (U[dtype] + E * (48 + 2 * z.double().square())) * ref.abs() + TINY[dtype]
+        err = (y.double() - ref).abs()
+        assert (err <= bar).all(), (float((err / bar.clamp_min(1e-300)).max()), z[err > bar][:5].tolist())
+    assert A.device_error() == A.OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("act,most", [("gelu", 13.0)])
+def test_slope_tails(A, act, most, dtype):  # noqa: F811
+    """The bias's gradient of one row with dy = 1 is the slope itself in fp32."""
+    z = every_value(dtype, most).reshape(1, -1)
+    n = z.shape[1]
+    x, w = torch.zeros((1, 8), device="cuda", dtype=z.dtype), torch.zeros((n, 8), device="cuda", dtype=z.dtype)
+    _, _, db = A.linear_backward(torch.ones_like(z), x, w, preact=z, activation=act, need_dx=False, need_dweight=False)
+    _, ref, size = reference(z[0], act)
+    bar = E * (48 + 2 * z[0].double().square()) * size + 2.0 ** -148
+    err = (db.double() - ref).abs()
+    assert (err <= bar).all(), (float((err / bar).max()), z[0][err > bar][:5].tolist())
+    assert A.device_error() == A.OK
