@@ -144,8 +144,8 @@ __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == ACT_GELU_TANH) {
         const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
         const float du2 = 1.5957691216057308f * (1.f + 0.134145f * z * z);
-        const float s = __fdividef(1.f, 1.f + __expf(-u2));
-        return s + z * s * (1.f - s) * du2;
+        const float s = __fdividef(1.f, 1.f + __expf(-u2)), sc = s * (1.f - s);
+        return sc == 0.f ? s : s + z * sc * du2;  // far out du2 overflows, and its factor is 0 long before
     }
     if constexpr (ACT == ACT_SILU) {
         const float s = __fdividef(1.f, 1.f + __expf(-z));

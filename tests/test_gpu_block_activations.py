@@ -63,3 +63,24 @@ def test_slope_tails(A, act, most, dtype):  # noqa: F811
     err = (db.double() - ref).abs()
     assert (err <= bar).all(), (float((err / bar).max()), z[0][err > bar][:5].tolist())
     assert A.device_error() == A.OK
+
+
+def sigmoid_parts(z, act):
+    """(u, du/dz, e^-|u| / (1 + e^-|u|) on either side) of z sigmoid(u(z)) in 64 bits."""
+    z = z.double()
+    u, du = z, torch.ones_like(z)
+    if act == "gelu_tanh":
+        k = 2 * math.sqrt(2 / math.pi)
+        u, du = k * (z + 0.044715 * z ** 3), k * (1 + 3 * 0.044715 * z * z)
+    return u, du, 1 / (1 + torch.exp(-u)), 1 / (1 + torch.exp(u))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gelu_tanh_slope_far_out(A, dtype):  # noqa: F811
+    """Every finite value of the type from |z| = 12 on, where the slope is 0 or 1 to the last bit."""
+    z = every_value(dtype, math.inf).reshape(1, -1)
+    z = z[(z.abs() >= 12) & torch.isfinite(z)][None]
+    n = z.shape[1]
+    x, w = torch.zeros((1, 8), device="cuda", dtype=z.dtype), torch.zeros((n, 8), device="cuda", dtype=z.dtype)
+    _, _, db = A.linear_backward(torch.ones_like(z), x, w, preact=z, activation="gelu_tanh", need_dx=False, need_dweight=False)
+    assert torch.equal(db, (z[0] > 0).float()), db[db != (z[0] > 0)][:5]
