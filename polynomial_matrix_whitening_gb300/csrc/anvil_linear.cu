@@ -117,6 +117,14 @@ __device__ __forceinline__ float normal_cdf(float z, float* e) {
     return z < 0.f ? tail : 1.f - tail;
 }
 
+// s = 1 / (1 + e^-u) and c = 1 - s, both to their relative accuracy: from e^-|u|, so that the
+// divisor stays between 1 and 2 (the fast division gives 0 for divisors over 2^126).
+__device__ __forceinline__ void sigmoid(float u, float* s, float* c) {
+    const float e = __expf(-fabsf(u)), r = __fdividef(1.f, 1.f + e);
+    *s = u < 0.f ? e * r : r;
+    *c = u < 0.f ? r : e * r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == ACT_RELU) return z < 0.f ? 0.f : z;
@@ -126,10 +134,15 @@ __device__ __forceinline__ float act_value(float z) {
         return z * normal_cdf(z, &e);
     }
     if constexpr (ACT == ACT_GELU_TANH) {
-        const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);  // 2 sqrt(2/pi) (...)
-        return __fdividef(z, 1.f + __expf(-u2));                              // z (1 + tanh(u2 / 2)) / 2
+        float s, c;
+        sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z), &s, &c);  // 2 sqrt(2/pi) (...)
+        return z * s;                                                         // z (1 + tanh(u / 2)) / 2
     }
-    if constexpr (ACT == ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if constexpr (ACT == ACT_SILU) {
+        float s, c;
+        sigmoid(z, &s, &c);
+        return z * s;
+    }
     return z;
 }
 template <int ACT>
@@ -142,14 +155,16 @@ __device__ __forceinline__ float act_slope(float z) {
         return fmaf(z * 0.3989422804014327f, e, c);
     }
     if constexpr (ACT == ACT_GELU_TANH) {
-        const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
-        const float du2 = 1.5957691216057308f * (1.f + 0.134145f * z * z);
-        const float s = __fdividef(1.f, 1.f + __expf(-u2)), sc = s * (1.f - s);
-        return sc == 0.f ? s : s + z * sc * du2;  // far out du2 overflows, and its factor is 0 long before
+        const float du = 1.5957691216057308f * (1.f + 0.134145f * z * z);
+        float s, c;
+        sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z), &s, &c);
+        const float sc = s * c;
+        return sc == 0.f ? s : s + z * sc * du;  // far out du overflows, and its factor is 0 long before
     }
     if constexpr (ACT == ACT_SILU) {
-        const float s = __fdividef(1.f, 1.f + __expf(-z));
-        return s * (1.f + z * (1.f - s));
+        float s, c;
+        sigmoid(z, &s, &c);
+        return s * (1.f + z * c);
     }
     return 1.f;
 }

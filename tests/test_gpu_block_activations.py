@@ -84,3 +84,39 @@ def test_gelu_tanh_slope_far_out(A, dtype):  # noqa: F811
     x, w = torch.zeros((1, 8), device="cuda", dtype=z.dtype), torch.zeros((n, 8), device="cuda", dtype=z.dtype)
     _, _, db = A.linear_backward(torch.ones_like(z), x, w, preact=z, activation="gelu_tanh", need_dx=False, need_dweight=False)
     assert torch.equal(db, (z[0] > 0).float()), db[db != (z[0] > 0)][:5]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_sigmoid_tails(A, act, dtype):  # noqa: F811
+    """Value and slope of every finite value of the type.
+
+    u(z) takes at most 6 roundings (E |u| each, as an exponent), the exponential 2 (2 + 1.173 |u|) E,
+    the reciprocal, the products and the sum 12 E; beyond |u| = 110 it is 0.  Below 2^-126 the
+    exponential is off by up to 2^-149, times what it is multiplied with."""
+    every = every_value(dtype, math.inf)
+    every = torch.where(torch.isfinite(every), every, torch.zeros_like(every))
+
+    def terms(z):
+        u, du, s, c = sigmoid_parts(z, act)
+        z, far = z.double(), u.abs().clamp_max(110.0)
+        # (far out, where s c is 0, its factor z du is not taken into account)
+        return z, du, s, c, E * (16 + 9 * far), torch.where(u.abs() < 110, 1 + z.abs() * du, torch.ones_like(z))
+    for x, y in outputs(A, every, act):
+        z, du, s, c, rel, lost = terms(x)
+        ref = z * s
+        bar = (U[dtype] + rel) * ref.abs() + TINY[dtype] + 2.0 ** -148 * (1 + z.abs().clamp_max(110.0))
+        err = (y.double() - ref).abs()
+        assert (err <= bar).all(), (float((err / bar).max()), x[err > bar][:5].tolist())
+    x = every.reshape(1, -1)
+    n = x.shape[1]
+    _, _, db = A.linear_backward(torch.ones_like(x), torch.zeros((1, 8), device="cuda", dtype=x.dtype),
+                                 torch.zeros((n, 8), device="cuda", dtype=x.dtype), preact=x, activation=act,
+                                 need_dx=False, need_dweight=False)
+    z, du, s, c, rel, lost = terms(x[0])
+    inner = torch.where(s * c == 0, torch.zeros_like(z), z * c * du)
+    ref = s + s * inner
+    bar = 2 * rel * (s + s * inner.abs()) + 2.0 ** -147 * lost
+    err = (db.double() - ref).abs()
+    assert (err <= bar).all(), (float((err / bar).max()), x[0][err > bar][:5].tolist())
+    assert A.device_error() == A.OK
