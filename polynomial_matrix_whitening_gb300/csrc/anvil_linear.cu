@@ -147,7 +147,7 @@ __device__ __forceinline__ float act_value(float z) {
 }
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-    if constexpr (ACT == ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if constexpr (ACT == ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;  // (NaN: NaN, as forward)
     if constexpr (ACT == ACT_RELU2) return z < 0.f ? 0.f : 2.f * z;
     if constexpr (ACT == ACT_GELU) {
         float e;

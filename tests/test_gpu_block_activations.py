@@ -120,3 +120,21 @@ def test_sigmoid_tails(A, act, dtype):  # noqa: F811
     err = (db.double() - ref).abs()
     assert (err <= bar).all(), (float((err / bar).max()), x[0][err > bar][:5].tolist())
     assert A.device_error() == A.OK
+
+
+@pytest.mark.parametrize("act", ["relu", "relu2", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("rows", [1, 300])
+def test_nan_in_z_stays_nan(A, rows, act):  # noqa: F811
+    """A NaN in z gives NaN in y, and in every gradient it takes part in."""
+    x = torch.ones((rows, 64), device="cuda", dtype=torch.bfloat16)
+    x[rows // 2, 5] = math.nan
+    w = torch.eye(64, device="cuda").bfloat16()
+    y = A.linear_forward(x, w, activation=act)
+    assert torch.isnan(y[rows // 2]).all() and int(torch.isnan(y).sum()) == 64  # (each sum takes 0 * NaN)
+    z = torch.ones((rows, 64), device="cuda", dtype=torch.bfloat16)
+    z[rows // 2, 5] = math.nan
+    ones = torch.ones_like(z)
+    dx, dw, db = A.linear_backward(ones, ones, w, preact=z, activation=act)
+    assert torch.isnan(dx[rows // 2]).all() and int(torch.isnan(dx).sum()) == 64
+    assert torch.isnan(dw[5]).all() and int(torch.isnan(dw).sum()) == 64
+    assert torch.isnan(db[5]) and int(torch.isnan(db).sum()) == 1
