@@ -98,13 +98,26 @@ __host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool a_mn, bool b_
            ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
+// 1 / v to 1 ulp for v from 1 on (0 from 2^126 on).
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// 2^v (a relative error of 2^-22; the subnormal results too).
+__device__ __forceinline__ float power2(float v) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Phi(z), the normal distribution, and e = exp(-z^2/2).  Phi(-|z|) = e m(|z|) with m(a) =
 // exp(a^2/2) erfc(a / sqrt 2) / 2, which falls slowly: m = t P(t), t = 1 / (1 + 0.305 a), P the
 // polynomial of degree 7 of the least largest relative error over 0 <= a <= 16 (1.4e-7; fitted
 // by iterated weighted least squares).  So the tail has a relative error of (48 + 2 z^2) 2^-24 at
 // most, the exponential's own growth with its argument included, as far down as e reaches.
 __device__ __forceinline__ float normal_cdf(float z, float* e) {
-    const float t = __fdividef(1.f, fmaf(0.305f, fabsf(z), 1.f));
+    const float t = reciprocal(fmaf(0.305f, fabsf(z), 1.f));
     float q = fmaf(t, 0.036033929f, -0.150315657f);
     q = fmaf(t, q, 0.181285652f);
     q = fmaf(t, q, -0.0340613788f);
@@ -112,17 +125,24 @@ __device__ __forceinline__ float normal_cdf(float z, float* e) {
     q = fmaf(t, q, 0.103994657f);
     q = fmaf(t, q, 0.122379342f);
     q = fmaf(t, q, 0.121645144f);
-    *e = __expf(-0.5f * (z * z));
+    *e = power2(z * (z * -0.72134752044448170f));  // log2(e) / 2
     const float tail = t * q * *e;
     return z < 0.f ? tail : 1.f - tail;
 }
 
-// s = 1 / (1 + e^-u) and c = 1 - s, both to their relative accuracy: from e^-|u|, so that the
-// divisor stays between 1 and 2 (the fast division gives 0 for divisors over 2^126).
-__device__ __forceinline__ void sigmoid(float u, float* s, float* c) {
-    const float e = __expf(-fabsf(u)), r = __fdividef(1.f, 1.f + e);
-    *s = u < 0.f ? e * r : r;
-    *c = u < 0.f ? r : e * r;
+// s = 1 / (1 + e^-u) and c = 1 - s for a u of z's sign, both to their relative accuracy: from
+// e = e^-|u|, so that the divisor stays between 1 and 2 (1 + e^-u passes 2^126, where the
+// reciprocal is 0).
+__device__ __forceinline__ void sigmoid(float z, float e, float* s, float* c) {
+    const float r = reciprocal(1.f + e);
+    *s = z < 0.f ? e * r : r;
+    *c = z < 0.f ? r : e * r;
+}
+// SiLU: u = z.  tanh-GELU is z sigmoid(u) with u = 2 sqrt(2/pi) (z + 0.044715 z^3).  Both e^-|u|
+// with log2(e) in the factors.
+__device__ __forceinline__ float silu_exp(float z) { return power2(fabsf(z) * -1.4426950408889634f); }
+__device__ __forceinline__ float gelu_tanh_exp(float z, float zz) {
+    return power2(fabsf(z) * fmaf(-0.10294324f, zz, -2.3022082f));
 }
 
 template <int ACT>
@@ -135,12 +155,12 @@ __device__ __forceinline__ float act_value(float z) {
     }
     if constexpr (ACT == ACT_GELU_TANH) {
         float s, c;
-        sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z), &s, &c);  // 2 sqrt(2/pi) (...)
-        return z * s;                                                         // z (1 + tanh(u / 2)) / 2
+        sigmoid(z, gelu_tanh_exp(z, z * z), &s, &c);
+        return z * s;  // z (1 + tanh(u / 2)) / 2
     }
     if constexpr (ACT == ACT_SILU) {
         float s, c;
-        sigmoid(z, &s, &c);
+        sigmoid(z, silu_exp(z), &s, &c);
         return z * s;
     }
     return z;
@@ -155,15 +175,15 @@ __device__ __forceinline__ float act_slope(float z) {
         return fmaf(z * 0.3989422804014327f, e, c);
     }
     if constexpr (ACT == ACT_GELU_TANH) {
-        const float du = 1.5957691216057308f * (1.f + 0.134145f * z * z);
+        const float zz = z * z, du = fmaf(0.21406451f, zz, 1.5957691f);  // du/dz
         float s, c;
-        sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z), &s, &c);
+        sigmoid(z, gelu_tanh_exp(z, zz), &s, &c);
         const float sc = s * c;
         return sc == 0.f ? s : s + z * sc * du;  // far out du overflows, and its factor is 0 long before
     }
     if constexpr (ACT == ACT_SILU) {
         float s, c;
-        sigmoid(z, &s, &c);
+        sigmoid(z, silu_exp(z), &s, &c);
         return s * (1.f + z * c);
     }
     return 1.f;
