@@ -13,7 +13,9 @@ fp32 [2, g, m, n], out bf16 [g, m, n], all contiguous.  Calls are enqueued on
 
 The operators around the banks (layer norm, the linear layer, token log probabilities)
 take matrices whose rows may be a view of wider ones and allocate the results they
-return, and their scratch, on the stream they run on.
+return, and their scratch, on the stream they run on.  Autograd records nothing of them: a
+gradient comes from the operator's own backward call, and where grad mode is on a tensor that
+requires grad is refused (inside a ``torch.autograd.Function`` grad mode is off).
 """
 from __future__ import annotations
 

@@ -10,6 +10,7 @@
 
 #include <ATen/core/TensorBody.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -119,11 +120,18 @@ void same_form(const at::Tensor& t, at::IntArrayRef sizes, at::ScalarType type, 
     if (t.scalar_type() != type || t.sizes() != sizes) refuse("%s must have %s", what, like);
 }
 
-// The current stream, after checking that every tensor is on the current GPU.
+// The current stream, after checking that every tensor is on the current GPU, and that none
+// asks for a gradient that autograd would not get: the calls record nothing.
 struct Here {
     void* stream;
     at::Device device;
     Here(const char* what, std::initializer_list<const at::Tensor*> tensors) : stream(nullptr), device(at::kCUDA, 0) {
+        if (c10::GradMode::is_enabled()) {
+            for (const at::Tensor* t : tensors)
+                if (t && t->requires_grad())
+                    refuse("%s: a tensor requires grad, but autograd records nothing of the call; use torch.no_grad() "
+                           "(an autograd.Function runs under it) and the backward call", what);
+        }
         const at::Tensor* first = *tensors.begin();
         if (!first->is_cuda()) refuse("%s: every tensor must be on the current CUDA device", what);
         device = at::Device(at::kCUDA, c10::cuda::current_device());
