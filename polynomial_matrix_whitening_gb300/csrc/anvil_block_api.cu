@@ -99,10 +99,6 @@ size_t norm_bwd_bytes(const anvil_layernorm_grad_desc* d) {
 }
 
 // ---------------------------------------------------------------- the linear layer
-bool aligned16(const void* p, int64_t ld, int es, int64_t rows) {
-    return !(reinterpret_cast<uintptr_t>(p) & 15) && (rows <= 1 || (ld * es) % 16 == 0);
-}
-
 anvil_status check_linear_sizes(int64_t rows, int n, int k, int dtype, int act) {
     if (rows < 0 || n < 1 || k < 1 || (dtype != ANVIL_BF16 && dtype != ANVIL_F16) || act < 0 || act >= ACT_COUNT)
         return ANVIL_ERR_INVALID_ARG;

@@ -39,6 +39,11 @@ struct Range {
 };
 inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
+// Whether every row of a matrix (ld elements of es bytes apart) starts on a 16-byte boundary.
+inline bool aligned16(const void* p, int64_t ld, int es, int64_t rows) {
+    return !(reinterpret_cast<uintptr_t>(p) & 15) && (rows <= 1 || (ld * es) % 16 == 0);
+}
+
 // ---------------------------------------------------------------- launch profiling
 struct Profiler {
     std::mutex mu;

@@ -421,9 +421,12 @@ __device__ __forceinline__ void wait_input(EpiState& x, unsigned* err) {
     if (!mbar_wait(x.in_bar, static_cast<uint32_t>(x.loads - 1) & 1u, err)) x.fail = true;
 }
 
-// The accumulator is read (the loads have completed): its next products may start.  The arrival
-// orders nothing else: with release semantics it waited about 2000 cycles for the warp's
-// shared-memory writes to be visible to the whole cluster, which nothing needs.
+// The accumulator is read: its next products may overwrite it.  That order rests on the loads'
+// completion, not on the arrival: every lane has passed tcgen05.wait::ld (tmem_ld_* end with it),
+// after which the values are in registers and no write can reach them, and __syncwarp joins the
+// lanes before one of them arrives.  So the arrival may be relaxed, and orders nothing else: with
+// release semantics it waited about 2000 cycles for the warp's shared-memory writes to be visible
+// to the whole cluster, which nothing needs.
 __device__ __forceinline__ void release_acc(const EpiState& x, uint32_t tempty) {
     tc_fence_before();
     __syncwarp();

@@ -728,7 +728,7 @@ cudaError_t run_bwd(const LogprobGradParams& p, int segs, cudaStream_t s) {
 
 cudaError_t launch_logprob_fwd(const LogprobParams& p, int sm_count, cudaStream_t s) {
     // blocks per row: more where the rows alone do not fill the SMs, as long as a block
-    // still has a full turn of loads (16 KB)
+    // still has half a turn of loads (8 KB)
     const long long bytes = static_cast<long long>(p.vocab) * dtype_size(p.dtype);
     int csize = 1;
     while (csize < 8 && p.rows * csize * 2 <= 2 * sm_count && bytes / (csize * 2) >= FWD_THREADS * UNROLL * 16 / 2) csize *= 2;

@@ -33,6 +33,7 @@
 #include <string.h>
 
 #include "anvil_device.cuh"
+#include "anvil_host.h"
 #include "anvil_norm.h"
 #include "anvil_types.cuh"
 
@@ -50,7 +51,8 @@ struct Shape {
 };
 
 // Resident blocks per SM: the backward row pass 512 threads, at up to 128 registers each;
-// the forward one 1024 threads at 64 where a thread has at most 8 columns, else 512.
+// the forward one 1024 threads at 64 where a thread has at most 8 columns, 768 at 85 up to 16,
+// else 512 (teams of up to a warp: three blocks of 256).
 constexpr int bwd_blocks_per_sm(int tpr) { return tpr <= 32 ? 2 : 512 / tpr; }
 constexpr int fwd_threads_per_sm(int columns) { return columns <= 8 ? 1024 : columns <= 16 ? 768 : 512; }
 constexpr int fwd_blocks_per_sm(int tpr, int columns) {
@@ -905,10 +907,6 @@ __global__ void __launch_bounds__(32 * GRAD_LANES) norm_grads_kernel(const NormB
 }
 
 namespace {
-
-bool aligned16(const void* p, long long ld, int es, long long rows) {
-    return !(reinterpret_cast<uintptr_t>(p) & 15) && (rows <= 1 || (ld * es) % 16 == 0);
-}
 
 template <typename T, typename W, bool VEC, int TPR, int NV>
 cudaError_t run_fwd(const NormFwdParams& p, cudaStream_t s) {
