@@ -330,8 +330,9 @@ anvil_status anvil_linear_forward(const anvil_linear_desc* desc, void* workspace
  * dx [rows, k] of type dtype; dweight in W's layout (weight_transposed), of type
  * dweight_dtype: dtype or ANVIL_F32 (what the bank step takes); dbias [n] fp32.  Each may be
  * NULL (not computed); x is read for dweight only, weight for dx only.  dz is rounded to
- * dtype as the products' operand; dbias sums the unrounded dz.  accumulate != 0: dweight
- * and dbias are added to what they hold.  The residual's gradient is dy itself. */
+ * dtype as the products' operand (in fp16 one beyond 65504 becomes infinite, as do dx and dweight
+ * where it takes part); dbias sums the unrounded dz.  accumulate != 0: dweight and dbias are
+ * added to what they hold.  The residual's gradient is dy itself. */
 typedef struct {
     const void* dy;
     const void* x;

@@ -562,7 +562,9 @@ def linear_backward(dy, x, weight, preact=None, activation=None, need_dx=True, n
 
     preact is the forward call's z (needed with an activation).  dweight has weight's shape
     and order and dweight_dtype: x's type (default) or fp32, what the bank step takes; dbias
-    is fp32.  dweight and dbias may be given (with accumulate they are added to).  The
+    is fp32.  dweight and dbias may be given (with accumulate they are added to).  dy times the
+    activation's slope is rounded to x's type before the products (2^-8 of each value at most in bf16,
+    2^-11 in fp16, where one beyond 65504 becomes infinite), whatever dweight's type.  The
     residual's gradient is dy itself.
     """
     if stream is not None:

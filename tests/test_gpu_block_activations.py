@@ -138,3 +138,16 @@ def test_nan_in_z_stays_nan(A, rows, act):  # noqa: F811
     assert torch.isnan(dx[rows // 2]).all() and int(torch.isnan(dx).sum()) == 64
     assert torch.isnan(dw[5]).all() and int(torch.isnan(dw).sum()) == 64
     assert torch.isnan(db[5]) and int(torch.isnan(db).sum()) == 1
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_dz_beyond_fp16(A, rows):  # noqa: F811
+    """A dz that fp16 does not hold is infinite in the products' operands, and stays in the gradients it
+    takes part in; the bias's gradient is a sum of the unrounded values."""
+    dy, z = torch.ones((rows, 64), device="cuda").half(), torch.ones((rows, 64), device="cuda").half()
+    dy[1, 7], z[1, 7] = 300.0, 200.0                       # dz = 300 * 2 * 200 = 120000
+    x, w = torch.ones((rows, 64), device="cuda").half(), torch.ones((64, 64), device="cuda").half()
+    dx, dw, db = A.linear_backward(dy, x, w, preact=z, activation="relu2", dweight_dtype=torch.float32)
+    assert torch.isinf(dx[1]).all() and int(torch.isinf(dx).sum()) == 64
+    assert torch.isinf(dw[7]).all() and int(torch.isinf(dw).sum()) == 64
+    assert float(db[7]) == 120000.0 + 2 * (rows - 1) and not torch.isnan(dx).any() and not torch.isnan(dw).any()
