@@ -215,7 +215,7 @@ __device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int co
         if (vec) {
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(b + i));
+                const float4 f = *reinterpret_cast<const float4*>(b + i);
                 v[i] += f.x;
                 v[i + 1] += f.y;
                 v[i + 2] += f.z;
@@ -223,7 +223,7 @@ __device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int co
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += col0 + i < cols ? __ldg(b + i) : 0.f;
+            for (int i = 0; i < N; ++i) v[i] += col0 + i < cols ? b[i] : 0.f;
         }
     } else {
         const T* b = static_cast<const T*>(e.bias) + col0;
@@ -231,7 +231,7 @@ __device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int co
 #pragma unroll
             for (int i = 0; i < N; i += 8) {
                 float f[8];
-                Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(b + i)), f);
+                Elem<T>::unpack(*reinterpret_cast<const uint4*>(b + i), f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[i + k] += f[k];
             }
@@ -1126,7 +1126,7 @@ __global__ void __launch_bounds__(TOKEN_THREADS) token_kernel(const TokenParams 
             for (int i = threadIdx.x; i < chunks * R; i += TOKEN_THREADS) {
                 const int r = i / chunks, c = i - r * chunks;
                 const T* x = static_cast<const T*>(p.x) + min(r, p.rows - 1) * p.ldx;
-                sts128(xa + i * 16, __ldg(reinterpret_cast<const uint4*>(x) + c));
+                sts128(xa + i * 16, reinterpret_cast<const uint4*>(x)[c]);
             }
             __syncthreads();
         }
@@ -1207,7 +1207,7 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackParams q) {
         const uint16_t* s = p.src + row * p.lds + c;
         uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols ? __ldg(s + e) : 0u;
+        for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols ? s[e] : 0u;
         *reinterpret_cast<uint4*>(p.dst + row * p.ldd + c) =
             make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }

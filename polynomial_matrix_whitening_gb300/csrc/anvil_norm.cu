@@ -126,7 +126,7 @@ __device__ __forceinline__ void load_weight(const W* w, int c, float* f) {
         f[0] = Elem<W>::load(w[c]);
     } else {
 #pragma unroll
-        for (int e = 0; e < E; e += Elem<W>::VEC) Elem<W>::unpack(__ldg(reinterpret_cast<const uint4*>(w + c + e)), f + e);
+        for (int e = 0; e < E; e += Elem<W>::VEC) Elem<W>::unpack(*reinterpret_cast<const uint4*>(w + c + e), f + e);
     }
 }
 // A unit's columns of an optional weight vector (null: every value is `none`).

@@ -187,6 +187,8 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+// Loads are the ordinary, coherent ones: a kernel that was launched early runs while the one ahead of
+// it still writes, so nothing here is read-only for as long as the kernel runs (what __ldg asks for).
 // Streaming 16-byte load (read once) and store (not read again soon).
 __device__ __forceinline__ uint4 ldg_stream(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ void stg_stream(void* p, uint4 v) { __stcs(reinterpret_cast<uint4*>(p), v); }
