@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(NX_THREADS) normalize_kernel(const __grid_cons
     uint4* dst = reinterpret_cast<uint4*>(B.y1) + c0;
     uint4 v[NX_CHUNKS];
 #pragma unroll
-    for (int i = 0; i < NX_CHUNKS; ++i) v[i] = __ldg(src + i * NX_THREADS);
+    for (int i = 0; i < NX_CHUNKS; ++i) v[i] = src[i * NX_THREADS];  // (coherent loads: this kernel may start while X_raw is written)
 #pragma unroll
     for (int i = 0; i < NX_CHUNKS; ++i)
         dst[i * NX_THREADS] = div4_to_bf2(bf2_to_f2(v[i].x), bf2_to_f2(v[i].y), bf2_to_f2(v[i].z),

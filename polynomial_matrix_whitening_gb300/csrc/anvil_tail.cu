@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(256, 5) tail_apply_rows_kernel(const __grid_co
                     vu[u] = *reinterpret_cast<const uint4*>(B.update + rbase + 8 * ci);
                     pu[u] = *reinterpret_cast<const uint4*>(B.param + rbase + 8 * ci);
                     mu[u] = *reinterpret_cast<const uint4*>(B.mantissa + rbase + 8 * ci);
-                    sx[u] = __ldg(reinterpret_cast<const ulonglong2*>(sgn + kstride * (ci >> 3)));
+                    sx[u] = *reinterpret_cast<const ulonglong2*>(sgn + kstride * (ci >> 3));
                 }
             }
 #pragma unroll
