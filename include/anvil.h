@@ -291,7 +291,7 @@ anvil_status anvil_layernorm_backward(const anvil_layernorm_grad_desc* desc, voi
 
 typedef enum {
     ANVIL_ACT_NONE = 0,
-    ANVIL_ACT_RELU = 1,
+    ANVIL_ACT_RELU = 1,      /* max(z, 0), the slope 0 at 0 */
     ANVIL_ACT_RELU2 = 2,     /* max(z, 0)^2 */
     ANVIL_ACT_GELU = 3,      /* z Phi(z) */
     ANVIL_ACT_GELU_TANH = 4, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
