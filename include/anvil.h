@@ -325,14 +325,20 @@ typedef struct {
 size_t anvil_linear_workspace_bytes(const anvil_linear_desc* desc);
 anvil_status anvil_linear_forward(const anvil_linear_desc* desc, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Added to the gradient's activation: dz in two parts, see below. */
+#define ANVIL_DZ_TWO_PARTS 256
+
 /* Its gradient, for dy = dL/dy and z = preact (not read for ANVIL_ACT_NONE):
  *   dz = dy act'(z),  dx = dz W,  dweight = dz^T x,  dbias = sum over rows of dz.
  * dx [rows, k] of type dtype; dweight in W's layout (weight_transposed), of type
  * dweight_dtype: dtype or ANVIL_F32 (what the bank step takes); dbias [n] fp32.  Each may be
  * NULL (not computed); x is read for dweight only, weight for dx only.  dz is rounded to
  * dtype as the products' operand (in fp16 one beyond 65504 becomes infinite, as do dx and dweight
- * where it takes part); dbias sums the unrounded dz.  accumulate != 0: dweight and dbias are
- * added to what they hold.  The residual's gradient is dy itself. */
+ * where it takes part); dbias sums the unrounded dz.  With activation + ANVIL_DZ_TWO_PARTS what
+ * the rounding drops is kept as a second operand, rounded itself: dz is off by 2^-16 of itself at
+ * most (fp16 2^-22) instead of 2^-8 (2^-11), the products take twice the time, and rows is at most
+ * ANVIL_MAX_ROWS / 2.  Without an activation dz is dy and nothing is rounded.  accumulate != 0:
+ * dweight and dbias are added to what they hold.  The residual's gradient is dy itself. */
 typedef struct {
     const void* dy;
     const void* x;

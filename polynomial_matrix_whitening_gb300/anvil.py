@@ -557,27 +557,30 @@ def linear_forward(x, weight, bias=None, activation=None, residual=None, save_pr
 
 
 def linear_backward(dy, x, weight, preact=None, activation=None, need_dx=True, need_dweight=True, bias_grad=True,
-                    dweight_dtype=None, dweight=None, dbias=None, accumulate=False, workspace=None, stream=None):
+                    dweight_dtype=None, dweight=None, dbias=None, accumulate=False, workspace=None, stream=None, dz_parts=1):
     """Gradient of linear_forward: returns (dx, dweight, dbias), None where not asked for.
 
     preact is the forward call's z (needed with an activation).  dweight has weight's shape
     and order and dweight_dtype: x's type (default) or fp32, what the bank step takes; dbias
     is fp32.  dweight and dbias may be given (with accumulate they are added to).  dy times the
     activation's slope is rounded to x's type before the products (2^-8 of each value at most in bf16,
-    2^-11 in fp16, where one beyond 65504 becomes infinite), whatever dweight's type.  The
+    2^-11 in fp16, where one beyond 65504 becomes infinite), whatever dweight's type; dz_parts=2 keeps
+    what that drops as a second operand (2^-16, 2^-22), for twice the products' time.  The
     residual's gradient is dy itself.
     """
     if stream is not None:
         return _on_stream(stream, lambda: linear_backward(dy, x, weight, preact, activation, need_dx, need_dweight,
                                                           bias_grad, dweight_dtype, dweight, dbias, accumulate,
-                                                          workspace),
+                                                          workspace, dz_parts=dz_parts),
                           (dy, x, weight, preact, dweight, dbias, workspace))
+    if dz_parts not in (1, 2):
+        raise ValueError("dz_parts must be 1 or 2")
     fp32 = dweight_dtype is not None and dweight_dtype != x.dtype
     if fp32 and str(dweight_dtype) != "torch.float32":
         raise ValueError("dweight must be fp32 or of x's type")
     return (_native or _load_native()).linear_backward(dy, x, weight, preact, _activation(activation), need_dx,
                                                        need_dweight, bias_grad, fp32, dweight, dbias, accumulate,
-                                                       workspace)
+                                                       workspace, dz_parts == 2)
 
 
 def token_logprobs(logits, targets=None, top=0, stream=None):

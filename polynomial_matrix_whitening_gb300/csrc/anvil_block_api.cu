@@ -18,6 +18,7 @@ using namespace anvil;
 
 static_assert(ANVIL_ACT_SILU == ACT_SILU && ANVIL_ACT_RELU2 == ACT_RELU2, "activation codes of include/anvil.h");
 static_assert(ANVIL_MAX_TOP == LOGPROB_MAX_TOP, "ANVIL_MAX_TOP");
+static_assert(ANVIL_DZ_TWO_PARTS >= ACT_COUNT, "a bit of its own beside the activation codes");
 
 namespace {
 
@@ -448,14 +449,20 @@ struct Copies {
     RepackParams p;
     void add(Stored* s, void* copy) {
         if (!copy_bytes(*s)) return;
+        const Stored to = with_copy(*s, copy);
+        put(*s, copy, s->rows, to.ld);
+        *s = to;
+    }
+    // s into `rows` rows at dst, ldd elements apart (rows and columns that s lacks: zeros)
+    void put(const Stored& s, void* dst, int64_t rows, int64_t ldd) {
         Repack& r = p.job[p.jobs++];
-        r.src = static_cast<const uint16_t*>(s->p);
-        r.dst = static_cast<uint16_t*>(copy);
-        r.rows = s->rows;
-        r.lds = s->ld;
-        r.cols = s->cols;
-        *s = with_copy(*s, copy);
-        r.ldd = s->ld;
+        r.src = static_cast<const uint16_t*>(s.p);
+        r.dst = static_cast<uint16_t*>(dst);
+        r.rows = rows;
+        r.src_rows = s.rows;
+        r.lds = s.ld;
+        r.cols = s.cols;
+        r.ldd = ldd;
     }
     anvil_status run(cudaStream_t s) const {
         if (!p.jobs) return ANVIL_OK;
@@ -534,10 +541,19 @@ anvil_status check_linear(const anvil_linear_desc* d) {
     return ANVIL_OK;
 }
 
+int grad_activation(const anvil_linear_grad_desc* d) { return d->activation & ~ANVIL_DZ_TWO_PARTS; }
+
+// dz in two parts (h, the rounded values, and l, what that drops, rounded itself), for products that
+// know one operand and one contraction: dz is stored as rows of h, then l, n8 = n rounded up to
+// eights each.  For dx = (h + l) W a row is one row of 2 n8 columns, beside W twice; for
+// dW = (h + l)^T x the same memory is 2 rows of n8 columns, beside every row of x twice.
 struct LinearGradLayout {
     Stored dz, x, w;
     bool prep;        // act_grad_kernel runs
     bool dz_made;     // and writes dz
+    bool two;         // in two parts
+    int64_t n8;
+    int64_t kdx, kdw; // contractions of the products
     Plan pdx, pdw;
     int rows_per_block, blocks_r;
     size_t off_dz, off_x, off_w, off_sum, off_part, total;
@@ -551,15 +567,21 @@ LinearGradLayout linear_grad_layout(const anvil_linear_grad_desc* d) {
     L.x = {d->x, d->rows, d->ldx, d->k};
     L.w = stored_weight(d->weight, d->n, d->k, d->ldw, tr);
     const bool products = d->dx || d->dweight;
-    L.dz_made = products && (d->activation != ANVIL_ACT_NONE || copy_bytes(L.dz) != 0);
+    const bool act = grad_activation(d) != ANVIL_ACT_NONE;
+    L.dz_made = products && (act || copy_bytes(L.dz) != 0);
     L.prep = L.dz_made || d->dbias;
+    L.two = products && act && (d->activation & ANVIL_DZ_TWO_PARTS);
+    L.n8 = (d->n + 7) & ~7;
+    L.kdx = L.two ? 2 * L.n8 : d->n;
+    L.kdw = L.two ? 2 * d->rows : d->rows;
+    const int64_t k8 = (d->k + 7) & ~7;
     size_t at = 0;
     L.off_dz = at;
-    if (L.dz_made) at += align256(2 * static_cast<size_t>(d->rows) * ((d->n + 7) & ~7));
+    if (L.dz_made) at += align256(2 * static_cast<size_t>(d->rows) * (L.two ? 2 : 1) * L.n8);
     L.off_x = at;
-    if (d->dweight) at += copy_bytes(L.x);
+    if (d->dweight) at += L.two ? align256(2 * static_cast<size_t>(2 * d->rows) * k8) : copy_bytes(L.x);
     L.off_w = at;
-    if (d->dx) at += copy_bytes(L.w);
+    if (d->dx) at += L.two ? align256(2 * static_cast<size_t>(2 * L.n8) * (tr ? d->k : k8)) : copy_bytes(L.w);
     L.off_sum = at;
     if (L.prep) {
         // one turn of the blocks that the device holds at once, at least 32 rows each
@@ -575,17 +597,18 @@ LinearGradLayout linear_grad_layout(const anvil_linear_grad_desc* d) {
     const int64_t wr = tr ? d->k : d->n;
     const int wc = tr ? d->n : d->k;
     const double ex = epilogue_cycles(dx_epilogue(d), d->rows), ew = epilogue_cycles(dweight_epilogue(d), wr);
-    if (d->dx && d->dweight) plan_both(d->rows, d->k, d->n, tr, ex, wr, wc, d->rows, ew, &L.pdx, &L.pdw);
-    else if (d->dx) L.pdx = plan_product(d->rows, d->k, d->n, true, tr, ex, ALL_FREE);
-    else if (d->dweight) L.pdw = plan_product(wr, wc, d->rows, false, false, ew, ALL_FREE);
+    if (d->dx && d->dweight) plan_both(d->rows, d->k, L.kdx, tr, ex, wr, wc, L.kdw, ew, &L.pdx, &L.pdw);
+    else if (d->dx) L.pdx = plan_product(d->rows, d->k, L.kdx, true, tr, ex, ALL_FREE);
+    else if (d->dweight) L.pdw = plan_product(wr, wc, L.kdw, false, false, ew, ALL_FREE);
     L.total = at + L.pdx.part + L.pdw.part;  // the second product may start before the first's parts are added up
     return L;
 }
 
 anvil_status check_linear_grad(const anvil_linear_grad_desc* d) {
     if (!d) return ANVIL_ERR_INVALID_ARG;
-    anvil_status st = check_linear_sizes(d->rows, d->n, d->k, d->dtype, d->activation);
+    anvil_status st = check_linear_sizes(d->rows, d->n, d->k, d->dtype, grad_activation(d));
     if (st != ANVIL_OK) return st;
+    if ((d->activation & ANVIL_DZ_TWO_PARTS) && d->rows > ANVIL_MAX_ROWS / 2) return ANVIL_ERR_UNSUPPORTED_SHAPE;
     if (d->dweight && d->dweight_dtype != ANVIL_F32 && d->dweight_dtype != d->dtype) return ANVIL_ERR_INVALID_ARG;
     const bool tr = d->weight_transposed != 0;
     if (d->dweight && bad_ld(tr ? d->k : d->n, tr ? d->n : d->k, d->lddw)) return ANVIL_ERR_INVALID_ARG;
@@ -593,7 +616,7 @@ anvil_status check_linear_grad(const anvil_linear_grad_desc* d) {
         return ANVIL_ERR_ALIGNMENT;
     if (d->rows == 0) return ANVIL_OK;
     if (!d->dx && !d->dweight && !d->dbias) return ANVIL_OK;
-    const bool act = d->activation != ANVIL_ACT_NONE;
+    const bool act = grad_activation(d) != ANVIL_ACT_NONE;
     if (!d->dy || (d->dweight && !d->x) || (d->dx && !d->weight) || (act && !d->preact)) return ANVIL_ERR_INVALID_ARG;
     if (bad_ld(d->rows, d->n, d->lddy) || (d->dweight && bad_ld(d->rows, d->k, d->ldx)) ||
         (d->dx && (bad_ld(tr ? d->k : d->n, tr ? d->n : d->k, d->ldw) || bad_ld(d->rows, d->k, d->lddx))) ||
@@ -789,7 +812,7 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
             return cuda_fail(e, "cudaMemsetAsync");
         return ANVIL_OK;
     }
-    const bool act = d->activation != ANVIL_ACT_NONE;
+    const bool act = grad_activation(d) != ANVIL_ACT_NONE;
     const Area a[7] = {area(d->dy, d->rows, d->n, d->lddy, 2, false),
                        area(d->dweight ? d->x : nullptr, d->rows, d->k, d->ldx, 2, false),
                        area(d->dx ? d->weight : nullptr, wr, wc, d->ldw, 2, false),
@@ -817,32 +840,53 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
         p.lddy = d->lddy;
         p.ldz = d->ldz;
         p.cols = d->n;
-        p.act = d->activation;
+        p.act = grad_activation(d);
+        p.two_parts = L.two;
         p.f16 = f16;
         p.rows_per_block = L.rows_per_block;
         p.blocks_r = L.blocks_r;
         if (L.dz_made) {
             L.dz = with_copy(L.dz, ws + L.off_dz);
-            p.ldd = L.dz.ld;
+            p.ldd = L.two ? 2 * L.n8 : L.dz.ld;
         }
         if ((e = profiled(ANVIL_KERNEL_LINEAR_PREPARE, s, [&] { return launch_act_grad(p, s); })))
             return cuda_fail(e, "activation gradient launch");
         f.bias = {p.part, d->dbias, p.blocks_r, d->n, d->accumulate};
     }
     Copies copies = {};
-    if (d->dx) copies.add(&L.w, ws + L.off_w);
-    if (d->dweight) copies.add(&L.x, ws + L.off_x);
+    Stored dz_dx = L.dz, dz_dw = L.dz;
+    if (L.two) {
+        dz_dx = {L.dz.p, d->rows, 2 * L.n8, static_cast<int>(2 * L.n8)};
+        dz_dw.rows = 2 * d->rows;
+        if (d->dx) {
+            uint16_t* w2 = reinterpret_cast<uint16_t*>(ws + L.off_w);
+            const Stored to = tr ? Stored{w2, d->k, 2 * L.n8, static_cast<int>(2 * L.n8)} : Stored{w2, 2 * L.n8, (d->k + 7) & ~7, d->k};
+            copies.put(L.w, w2, tr ? d->k : L.n8, to.ld);
+            copies.put(L.w, w2 + (tr ? L.n8 : L.n8 * to.ld), tr ? d->k : L.n8, to.ld);
+            L.w = to;
+        }
+        if (d->dweight) {
+            uint16_t* x2 = reinterpret_cast<uint16_t*>(ws + L.off_x);
+            const Stored to = {x2, 2 * d->rows, (d->k + 7) & ~7, d->k};
+            copies.put(L.x, x2, d->rows, 2 * to.ld);
+            copies.put(L.x, x2 + to.ld, d->rows, 2 * to.ld);
+            L.x = to;
+        }
+    } else {
+        if (d->dx) copies.add(&L.w, ws + L.off_w);
+        if (d->dweight) copies.add(&L.x, ws + L.off_x);
+    }
     if ((st = copies.run(s)) != ANVIL_OK) return st;
     const bool overlap = d->dx && d->dweight && !L.pdx.few;
     if (d->dx) {
         Product q;
         memset(&q, 0, sizeof(q));
-        q.a = L.dz;
+        q.a = dz_dx;
         q.b = L.w;
         q.b_mn = !tr;
         q.rows = d->rows;
         q.cols = d->k;
-        q.k = d->n;
+        q.k = L.kdx;
         q.f16 = f16;
         q.epi = dx_epilogue(d);
         q.part = reinterpret_cast<float*>(ws + L.off_part);
@@ -852,12 +896,12 @@ anvil_status anvil_linear_backward(const anvil_linear_grad_desc* d, void* worksp
     if (d->dweight) {
         Product q;
         memset(&q, 0, sizeof(q));
-        q.a = tr ? L.x : L.dz;
-        q.b = tr ? L.dz : L.x;
+        q.a = tr ? L.x : dz_dw;
+        q.b = tr ? dz_dw : L.x;
         q.a_mn = q.b_mn = true;
         q.rows = wr;
         q.cols = static_cast<int>(wc);
-        q.k = d->rows;
+        q.k = L.kdw;
         q.f16 = f16;
         q.epi = dweight_epilogue(d);
         q.part = reinterpret_cast<float*>(ws + L.off_part + L.pdx.part);

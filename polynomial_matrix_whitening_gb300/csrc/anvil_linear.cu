@@ -1196,10 +1196,10 @@ __global__ void __launch_bounds__(TOKEN_THREADS) token_kernel(const TokenParams 
 
 // ---------------------------------------------------------------- around the products
 // Eight columns per thread; the last chunk of a row may be partial.
-__global__ void __launch_bounds__(256) repack_kernel(const RepackParams q) {
-    const Repack p = blockIdx.y ? q.job[1] : q.job[0];
+__global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ RepackParams q) {
+    const Repack& p = q.job[blockIdx.y];
     pdl_wait_previous();  // (the product starts after this kernel: its shared memory would take the L1 that the loads need)
-    const long long chunks = p.ldd / 8;
+    const long long chunks = (p.cols + 7) / 8;
     const long long total = chunks * p.rows;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
         const long long row = i / chunks;
@@ -1207,7 +1207,7 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackParams q) {
         const uint16_t* s = p.src + row * p.lds + c;
         uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols ? s[e] : 0u;
+        for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols && row < p.src_rows ? s[e] : 0u;
         *reinterpret_cast<uint4*>(p.dst + row * p.ldd + c) =
             make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
@@ -1217,9 +1217,10 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackParams q) {
 // the operands' type, because it is an operand: the tensor cores multiply 16-bit values.  Each
 // element is off by 2^-8 of itself (fp16 2^-11) at most, which leaves a sum over many rows or
 // columns off by less, relative to the root of its terms' squares: at 8192 x 2816 x 768 bf16 the
-// gradients are 0.0023 off (norm) where fp32 dz and results rounded to bf16 give 0.0017.  Keeping
-// what the rounding drops as a second operand would double both products (57 -> 102 us there, of a
-// call of 77).  In fp16 a dz beyond 65504 becomes infinite, and with it what it is added to.
+// gradients are 0.0023 off (norm) where fp32 dz and results rounded to bf16 give 0.0017.  A caller
+// who needs more asks for two parts (what the rounding drops as a second operand, the products'
+// contraction twice as long, W and x laid out twice: the call takes 140 us there instead of 80).
+// In fp16 a dz beyond 65504 becomes infinite either way, and with it what it is added to.
 constexpr int AG_LANES = 8;   // rows at a time per block: 32 threads x 8 columns each
 constexpr int AG_UNROLL = 4;  // turns whose loads are in flight together
 template <typename T, int ACT, bool VEC>
@@ -1268,7 +1269,17 @@ __global__ void __launch_bounds__(32 * AG_LANES, ACT_GRAD_BLOCKS) act_grad_kerne
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] += g[e];
-                if (dz && r < r1) *reinterpret_cast<uint4*>(dz + r * p.ldd + c) = Elem<T>::pack(g);
+                if (dz && r < r1) {
+                    const uint4 w = Elem<T>::pack(g);
+                    *reinterpret_cast<uint4*>(dz + r * p.ldd + c) = w;
+                    if (Z && p.two_parts) {
+                        float h[8];
+                        Elem<T>::unpack(w, h);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[e] = isfinite(h[e]) ? g[e] - h[e] : 0.f;
+                        *reinterpret_cast<uint4*>(dz + r * p.ldd + p.ldd / 2 + c) = Elem<T>::pack(h);
+                    }
+                }
             }
         }
     }
@@ -1410,7 +1421,7 @@ cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, int sm_count, cudaSt
 cudaError_t launch_repack(const RepackParams& p, cudaStream_t s) {
     long long most = 0;
     for (int j = 0; j < p.jobs; ++j) {
-        const long long n = p.job[j].ldd / 8 * p.job[j].rows;
+        const long long n = (p.job[j].cols + 7) / 8 * p.job[j].rows;
         if (n > most) most = n;
     }
     return launch_pdl(repack_kernel, dim3(blocks_for(most), p.jobs), dim3(256), 0, s, p);

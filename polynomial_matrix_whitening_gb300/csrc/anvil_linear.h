@@ -107,26 +107,28 @@ cudaError_t launch_tokens(const TokenParams& p, cudaStream_t stream);
 // bn: B's rows per block (16, 32, 64 or 128)
 cudaError_t launch_row_gemm(const RowGemmParams& p, int bn, int sm_count, cudaStream_t stream);
 
-// dst [rows, ldd] <- src [rows, cols] (row stride lds), 16-bit elements, ldd % 8 == 0, for
-// one or two arrays.
+// dst (`rows` rows of `cols` elements, rounded up to eights, row stride ldd, ldd % 8 == 0) <- src
+// (src_rows rows, row stride lds), zeros beyond; 16-bit elements, for up to four arrays.
 struct Repack {
     const uint16_t* src;
     uint16_t* dst;
-    long long rows, lds, ldd;
+    long long rows, src_rows, lds, ldd;
     int cols;
 };
 struct RepackParams {
-    Repack job[2];
+    Repack job[4];
     int jobs;
 };
 cudaError_t launch_repack(const RepackParams& p, cudaStream_t stream);
 
 // dz = dy * act'(z) (rounded to the operands' type for the products; may be null) and the
-// column sums of the unrounded dz (partial rows; may be null).
+// column sums of the unrounded dz (partial rows; may be null).  Two parts: what the rounding
+// drops, rounded itself, in the second half of dz's rows.
 struct ActGradParams {
     const void* dy;
     const void* z;       // null: dz = dy
     void* dz;            // [rows, ldd] or null
+    int two_parts;
     float* part;         // [blocks_r][cols] or null
     long long rows, lddy, ldz, ldd;
     int cols, act, f16;

@@ -363,7 +363,7 @@ PyObject* linear_forward(PyObject* const* a) {
 }
 
 // (dy, x, weight, preact, activation, need_dx, need_dweight, bias_grad, dweight fp32 (None:
-// x's type), dweight, dbias, accumulate, workspace) -> (dx, dweight, dbias)
+// x's type), dweight, dbias, accumulate, workspace, dz in two parts) -> (dx, dweight, dbias)
 PyObject* linear_backward(PyObject* const* a) {
     const at::Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &w = tensor(a[2], "weight");
     const at::Tensor *z = maybe(a[3], "preact"), *dw_in = maybe(a[9], "dweight"), *db_in = maybe(a[10], "dbias"),
@@ -434,6 +434,7 @@ PyObject* linear_backward(PyObject* const* a) {
     d.k = as_int(m.k, "weight");
     d.dweight_dtype = wt == type ? d.dtype : ANVIL_F32;
     d.weight_transposed = m.transposed;
+    if (truth(a[13])) d.activation |= ANVIL_DZ_TWO_PARTS;
     const Scratch scratch(ws ? 0 : api.linear_backward_workspace_bytes(&d), ws, here);
     check(api.linear_backward(&d, scratch.p, scratch.bytes, here.stream), "anvil_linear_backward");
     return tuple_of(std::move(dx), std::move(dw), std::move(db));
@@ -557,7 +558,7 @@ PyMethodDef methods[] = {
     ANVIL_ENTRY(layernorm_forward, 5),
     ANVIL_ENTRY(layernorm_backward, 9),
     ANVIL_ENTRY(linear_forward, 8),
-    ANVIL_ENTRY(linear_backward, 13),
+    ANVIL_ENTRY(linear_backward, 14),
     ANVIL_ENTRY(token_logprobs, 3),
     ANVIL_ENTRY(token_logprobs_backward, 7),
     {nullptr, nullptr, 0, nullptr}};
