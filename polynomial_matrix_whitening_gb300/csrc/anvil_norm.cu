@@ -987,8 +987,9 @@ namespace {
 
 // Threads of a team of the ring kernels: up to 16 columns each, off the 16-byte boundaries
 // 8 where a block can hold that many threads twice.
-// (2049 to 192 * 16 columns: 192 threads run 32768 x 2816 bf16 forward in 65 us, 256 in 78;
-// backward 256 are faster, 121 against 125.)
+// (2049 to 192 * 16 columns, forward, 192 threads against 256, us at 32768 rows: bf16 2056 columns
+// 60/77, 2560 61/77, 2816 65/77, 3064 69/79; fp32 92/88, 110/120, 120/131, 131/140.  Backward 256 are
+// faster, 2816 bf16 121 against 125.)
 int ring_tpr(int width, int arrays, bool vec) {
     if (!vec && width <= 2048) return width <= 512 ? 64 : width <= 1024 ? 128 : 256;
     if (width <= 2048) return width <= 1024 ? 64 : 128;
@@ -1002,7 +1003,8 @@ int ring_tpr(int width, int arrays, bool vec) {
 // and 11.3/11.8 at 12, 1024 22.8/21.4 at 24, 2816 46.0/50.1 at 48 and 24.4/23.0 at 24; backward
 // 2816 25.1/27.5 at 8 and 19.1/19.0 at 4; off the boundaries 500 columns 12.6/19.9 at 4, 1023
 // 38.3/39.0 at 24 and 21.6/19.7 at 12, 2815 20.2/26.1 at 6; a warp for 512 columns against a ring
-// of 32-thread teams 39.4/41.4 forward, 82/92 backward at 48.
+// of 32-thread teams 39.4/41.4 forward, 82/92 backward at 48.  (Forward one start for every width:
+// 768 columns gain 4% at 12 rows already, 1024 and 2816 still lose 6% at 24.)
 bool ring_plan(long long rows, int width, int dtype, bool vec, int arrays, int* blocks, int* team_rows) {
     const int es = dtype_size(dtype), tpr = ring_tpr(width, arrays, vec);
     const int least = arrays == 1 ? 32 : vec ? 8 : width <= 512 ? 4 : width <= 1024 ? 24 : 6;
