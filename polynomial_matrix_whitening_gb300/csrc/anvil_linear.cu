@@ -327,7 +327,7 @@ __device__ __forceinline__ void box_to_rows(uint32_t box, E* dst, long long ld, 
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int r = row0 + quad * 32 + i0 + i, c = h * 32 + lane;
-                if (r < rows && c < C && col0 + c < cols) dst[static_cast<size_t>(r) * ld + col0 + c] = v[i][h];
+                if (r < rows && (C >= 32 || lane < C) && col0 + c < cols) dst[static_cast<size_t>(r) * ld + col0 + c] = v[i][h];
             }
     }
 }
