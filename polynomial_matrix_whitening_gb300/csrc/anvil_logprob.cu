@@ -32,6 +32,9 @@
 // value, is not far above that is taken again value by value.  The gradient, where a vector's
 // sum of e y comes out NaN, from 0 times infinity, takes the vector again with the exponents
 // held at -200 (in base 2), where e is 0.  A NaN or +inf makes its row NaN.
+//
+// The exponentials flush results below 2^-126 to 0 (keeping them takes three more instructions an
+// element): a sum does not see them, a gradient loses values of at most about 1e-36.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stddef.h>
