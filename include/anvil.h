@@ -387,8 +387,9 @@ anvil_status anvil_token_logprobs(const anvil_logprob_desc* desc, void* stream);
 /* Their gradient, for u = dL/dlogprob (NULL: 0) and v = dL/dentropy (NULL: 0) [rows] fp32
  * and the lse (and entropy, with v) of the forward pass, p_j = e^(x_j - lse):
  *   dlogits_j = u ([j = target] - p_j) - v p_j (x_j - lse + entropy),
- * of type dtype [rows, vocab]; a p_j below 2^-126 counts as 0.  u is taken as 0 where the target is negative; a row whose
- * lse is -inf has the gradient 0.  dlogits may be logits itself (same pointer and stride). */
+ * of type dtype [rows, vocab]; a p_j below 2^-126 counts as 0.  u is taken as 0 where the
+ * target is negative; a row whose lse is -inf has the gradient 0.  dlogits may be logits itself
+ * (same pointer and stride). */
 typedef struct {
     const void* logits;
     const void* targets;

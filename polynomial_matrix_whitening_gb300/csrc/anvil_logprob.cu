@@ -34,7 +34,7 @@
 // held at -200 (in base 2), where e is 0.  A NaN or +inf makes its row NaN.
 //
 // The exponentials flush results below 2^-126 to 0 (keeping them takes three more instructions an
-// element): a sum does not see them, a gradient loses values of at most about 1e-36.
+// element): a sum does not see them, a gradient loses what is under 1e-36 of u and v.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stddef.h>
