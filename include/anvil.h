@@ -218,6 +218,65 @@ anvil_status anvil_adam_step(float* param, const float* grad, float* exp_avg, fl
                              size_t count, float beta1, float beta2, float eps, float step_size,
                              float eff_wd, void* stream);
 
+/* AdamW over many tensors in one call, in place: for every tensor, elementwise, with t = step,
+ *   g = grad * grad_scale
+ *   exp_avg    = exp_avg * beta1 + g * (1 - beta1)
+ *   exp_avg_sq = exp_avg_sq * beta2 + (g * (1 - beta2)) * g
+ *   param = param * decay - (exp_avg / (sqrt(exp_avg_sq) * root + eps)) * step_size
+ * with step_size = lr / (1 - beta1^t), root = 1 / sqrt(1 - beta2^t), decay = 1 - lr * weight_decay
+ * (in double, rounded to fp32), in fp32 with one rounding per operation in the order written.
+ * param [count] is fp32, bf16 or fp16 (rounded once, to nearest even), or bf16 with mantissa: the
+ * two halves of an fp32 value, as anvil_tail_desc has them.  grad is fp32 or of param's type (for
+ * an fp32 param any type).
+ * scales NULL: exp_avg and exp_avg_sq are fp32.  Else they are 8-bit codes, one byte a value, and
+ * scales [2, ceil(count / ANVIL_ADAMW_BLOCK)] fp32 holds a factor per block of consecutive values,
+ * for exp_avg and then for the root of exp_avg_sq:
+ *   exp_avg = e4m3 code * factor;  exp_avg_sq = (c < 16 ? c : (16 + c % 16) 2^(c / 16 - 1))^2 * factor^2
+ * (the root's code is c, and at least 1 where the root is not 0).  The factor is the block's largest
+ * magnitude times 1 / 448 (1 / 507904 for the root, the largest codes; 0 for a magnitude below 2^-100), the
+ * code the nearest, ties to the even one, of the value times 448 (507904) / that magnitude.  All zeros are states of 0.  The
+ * parameter's step uses the unrounded moments.  An infinite or NaN moment makes its block NaN.
+ * count may be 0.  Pointers are aligned to their elements' size; arrays on boundaries of four
+ * elements are faster.  A written array must not overlap any other array of the call; gradients may
+ * overlap each other. */
+#define ANVIL_ADAMW_BLOCK 256
+#define ANVIL_MAX_TENSORS (1 << 20)
+#define ANVIL_MAX_COUNT (1ll << 40)
+typedef struct {
+    void* param;
+    uint16_t* mantissa;
+    const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    float* scales;
+    int64_t count;
+    int param_dtype, grad_dtype; /* anvil_dtype, below */
+} anvil_adamw_tensor;
+/* 0 <= beta < 1, eps >= 0, step >= 1, grad_scale what every gradient is multiplied by (1, or what a
+ * loss scale or a norm's bound asks for). */
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    int64_t step;
+} anvil_adamw_config;
+/* d_scalars: NULL, or a DEVICE array of four fp32 that is read when the step runs in place of
+ * config's lr, weight_decay, grad_scale and step: step_size, root, decay, grad_scale, as
+ * anvil_adamw_scalars (host only) gives them; a captured graph then follows the schedule.  One
+ * launch per kind of tensor (types, codes) and 448 tensors; allocates no device memory. */
+anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, const anvil_adamw_config* config,
+                              const float* d_scalars, void* stream);
+anvil_status anvil_adamw_scalars(const anvil_adamw_config* config, float* scalars);
+
+/* The values that 8-bit states stand for, as fp32: m = exp_avg, v = exp_avg_sq, [count] each. */
+typedef struct {
+    const void* exp_avg;
+    const void* exp_avg_sq;
+    const float* scales;
+    float* m;
+    float* v;
+    int64_t count;
+} anvil_adamw_state;
+anvil_status anvil_adamw_values(const anvil_adamw_state* states, int nstates, void* stream);
+
 /* ---- operators around the banks: the layers whose gradients a bank or Adam step takes,
  * and the loss.  Layer norm, the linear layer with its bias, activation and residual, and
  * the log probabilities of given tokens, each forward and backward.
@@ -480,7 +539,8 @@ typedef enum {
     ANVIL_KERNEL_LINEAR_PRODUCT = 17,    /* a product of the linear layer */
     ANVIL_KERNEL_LINEAR_SUM = 18,        /* sums of split products and of dbias */
     ANVIL_KERNEL_LOGPROB = 19,           /* token log probabilities */
-    ANVIL_KERNEL_LOGPROB_BACKWARD = 20   /* their gradient */
+    ANVIL_KERNEL_LOGPROB_BACKWARD = 20,  /* their gradient */
+    ANVIL_KERNEL_ADAMW = 21              /* AdamW over many tensors, and the values of its states */
 } anvil_kernel_kind;
 
 typedef struct { int kind; float ms; } anvil_profile_record;

@@ -43,7 +43,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, ERR_ALIGNMENT, ERR_ALIAS, ERR_WORKSP
 KERNEL_KINDS = ("momentum", "norm_d", "normalize", "gram_norm", "gram", "sqpoly", "xupdate",
                 "xupdate_out", "tail_power", "tail_scale", "tail_apply", "adam", "cascade",
                 "norm_forward", "norm_backward", "norm_grads", "linear_prepare", "linear_product",
-                "linear_sum", "logprob", "logprob_backward")
+                "linear_sum", "logprob", "logprob_backward", "adamw")
 MAX_MAPS, MAX_BANKS, MAX_TOP = 16, 8, 32
 
 
@@ -130,6 +130,20 @@ class LogprobGradDesc(ctypes.Structure):
                 ("vocab", _I), ("dtype", _I), ("targets_int64", _I)]
 
 
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", _P), ("mantissa", _P), ("grad", _P), ("exp_avg", _P), ("exp_avg_sq", _P),
+                ("scales", _P), ("count", _L), ("param_dtype", _I), ("grad_dtype", _I)]
+
+
+class AdamwConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] \
+        + [("step", _L)]
+
+
+class AdamwState(ctypes.Structure):
+    _fields_ = [("exp_avg", _P), ("exp_avg_sq", _P), ("scales", _P), ("m", _P), ("v", _P), ("count", _L)]
+
+
 class ProfileRecord(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int), ("ms", ctypes.c_float)]
 
@@ -158,6 +172,9 @@ _lib.anvil_update_tail.argtypes = [ctypes.POINTER(TailDesc), _i, _vp, _sz, _vp]
 _lib.anvil_update_tail.restype = _i
 _lib.anvil_adam_step.argtypes = [_vp, _vp, _vp, _vp, _sz, _f, _f, _f, _f, _f, _vp]
 _lib.anvil_adam_step.restype = _i
+_lib.anvil_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), _i, ctypes.POINTER(AdamwConfig), _vp, _vp]
+_lib.anvil_adamw_scalars.argtypes = [ctypes.POINTER(AdamwConfig), ctypes.POINTER(ctypes.c_float)]
+_lib.anvil_adamw_values.argtypes = [ctypes.POINTER(AdamwState), _i, _vp]
 _lib.anvil_layernorm_forward.argtypes = [ctypes.POINTER(LayernormDesc), _vp]
 _lib.anvil_layernorm_backward_workspace_bytes.argtypes = [ctypes.POINTER(LayernormGradDesc)]
 _lib.anvil_layernorm_backward_workspace_bytes.restype = _sz
@@ -171,7 +188,7 @@ _lib.anvil_linear_backward.argtypes = [ctypes.POINTER(LinearGradDesc), _vp, _sz,
 _lib.anvil_token_logprobs.argtypes = [ctypes.POINTER(LogprobDesc), _vp]
 _lib.anvil_token_logprobs_backward.argtypes = [ctypes.POINTER(LogprobGradDesc), _vp]
 for _f_name in ("layernorm_forward", "layernorm_backward", "linear_forward", "linear_backward",
-                "token_logprobs", "token_logprobs_backward"):
+                "token_logprobs", "token_logprobs_backward", "adamw_step", "adamw_scalars", "adamw_values"):
     getattr(_lib, "anvil_" + _f_name).restype = _i
 _lib.anvil_device_error.argtypes = [_i]
 _lib.anvil_device_error.restype = _i
@@ -469,12 +486,76 @@ def adam_step(param, grad, exp_avg, exp_avg_sq, beta1, beta2, eps, step_size, ef
     _check(st, "anvil_adam_step")
 
 
+ADAMW_BLOCK = 256  # values of an 8-bit state that share a scale
+
+
+def _adamw_config(lr, step, beta1, beta2, eps, weight_decay, grad_scale):
+    return AdamwConfig(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale), int(step))
+
+
+def adamw_scalars(lr, step, beta1=0.9, beta2=0.95, weight_decay=0.0, grad_scale=1.0):
+    """The four values that adamw_step reads from `scalars` on the device, where it is given:
+    [lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step), 1 - lr weight_decay, grad_scale]."""
+    out = (ctypes.c_float * 4)()
+    config = _adamw_config(lr, step, beta1, beta2, 0.0, weight_decay, grad_scale)
+    _check(_lib.anvil_adamw_scalars(ctypes.byref(config), out), "anvil_adamw_scalars")
+    return list(out)
+
+
+def adamw_state(param, bits=32):
+    """New states of 0 for one parameter: (exp_avg, exp_avg_sq, scales).
+
+    32 bits: fp32 of param's shape, scales None.  8 bits: codes of param's shape
+    (torch.float8_e4m3fn and uint8) and fp32 scales [2, ceil(param.numel() / ADAMW_BLOCK)].
+    """
+    import torch
+    _require(bits in (8, 32), "bits must be 8 or 32")
+    new = lambda shape, dtype: torch.zeros(shape, dtype=dtype, device=param.device)  # noqa: E731
+    if bits == 32:
+        return new(param.shape, torch.float32), new(param.shape, torch.float32), None
+    return (new(param.shape, torch.float8_e4m3fn), new(param.shape, torch.uint8),
+            new((2, -(-param.numel() // ADAMW_BLOCK)), torch.float32))
+
+
+def adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0,
+               grad_scale=1.0, mantissas=None, scales=None, scalars=None, stream=None):
+    """AdamW over lists of tensors at once, in place; step counts from 1.
+
+    params: contiguous fp32, bf16 or fp16; grads of their shapes, fp32 or of their types (for
+    an fp32 parameter any of the three), multiplied by grad_scale first.  exp_avgs and
+    exp_avg_sqs as adamw_state makes them, with scales (a list, its items None for fp32 states;
+    None: all are fp32).  mantissas: a list of int16 or uint16 tensors (or None), the low halves
+    of fp32 values whose high halves the bf16 parameters are.  scalars: None, or fp32 [4] on the
+    device, read when the step runs in place of lr, step, weight_decay and grad_scale
+    (adamw_scalars; for CUDA-graph replays).  Parameters may require grad.
+    """
+    native = _native or _load_native()
+    args = (params, grads, exp_avgs, exp_avg_sqs, mantissas, scales, scalars, float(lr), float(beta1), float(beta2),
+            float(eps), float(weight_decay), float(grad_scale), step)
+    if stream is not None:
+        tensors = [t for part in (params, grads, exp_avgs, exp_avg_sqs, mantissas or (), scales or (), (scalars,)) for t in part]
+        return _on_stream(stream, lambda: native.adamw_step(*args), tensors)
+    native.adamw_step(*args)
+
+
+def adamw_values(exp_avgs, exp_avg_sqs, scales, out=None, stream=None):
+    """What 8-bit states stand for: two lists of fp32 tensors (exp_avg, exp_avg_sq), new or `out`'s."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, lambda: adamw_values(exp_avgs, exp_avg_sqs, scales, out),
+                          [t for part in (exp_avgs, exp_avg_sqs, scales) + tuple(out or ()) for t in part])
+    if out is None:
+        out = tuple([torch.empty(t.shape, dtype=torch.float32, device=t.device) for t in exp_avgs] for _ in range(2))
+    (_native or _load_native()).adamw_values(exp_avgs, exp_avg_sqs, scales, *out)
+    return out
+
+
 # ---- the operators around the banks
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
 _native = None
 _ENTRY_POINTS = ("layernorm_forward", "layernorm_backward_workspace_bytes", "layernorm_backward",
                  "linear_workspace_bytes", "linear_forward", "linear_backward_workspace_bytes",
-                 "linear_backward", "token_logprobs", "token_logprobs_backward")
+                 "linear_backward", "token_logprobs", "token_logprobs_backward", "adamw_step", "adamw_values")
 
 
 def _load_native():

@@ -1,0 +1,258 @@
+// anvil_adamw_api.cu -- the C ABI of AdamW over many tensors (include/anvil.h): argument checks
+// (before any CUDA call), the scalars of a step, and the tensors sorted into launches.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <new>
+
+#include "../../include/anvil.h"
+#include "anvil_adamw.h"
+#include "anvil_host.h"
+#include "anvil_types.cuh"
+
+using namespace anvil;
+
+static_assert(ANVIL_ADAMW_BLOCK == ADAMW_BLOCK, "ANVIL_ADAMW_BLOCK");
+
+namespace {
+
+bool off(const void* p, int es) { return (reinterpret_cast<uintptr_t>(p) & (es - 1)) != 0; }
+int64_t blocks_of(int64_t count) { return (count + ADAMW_BLOCK - 1) / ADAMW_BLOCK; }
+int64_t chunks_of(int64_t count) { return (count + ADAMW_CHUNK - 1) / ADAMW_CHUNK; }
+
+// The ranges of one array of every tensor (its role), in order of their addresses.
+struct Role {
+    Range* r;
+    bool written;
+};
+// No written range shares a byte with any other: a sweep over the roles' ranges, merged.
+bool disjoint(Role* roles, int nroles, int n) {
+    for (int i = 0; i < nroles; ++i) {
+        const auto below = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+        if (!std::is_sorted(roles[i].r, roles[i].r + n, below)) std::sort(roles[i].r, roles[i].r + n, below);
+    }
+    int at[8] = {0};
+    uintptr_t written = 0, read = 0;  // ends of what has been passed
+    for (;;) {
+        int k = -1;
+        for (int i = 0; i < nroles; ++i) {
+            while (at[i] < n && roles[i].r[at[i]].lo == roles[i].r[at[i]].hi) ++at[i];  // (absent or empty)
+            if (at[i] < n && (k < 0 || roles[i].r[at[i]].lo < roles[k].r[at[k]].lo)) k = i;
+        }
+        if (k < 0) return true;
+        const Range& x = roles[k].r[at[k]++];
+        if (x.lo < written || (roles[k].written && x.lo < read)) return false;
+        uintptr_t& end = roles[k].written ? written : read;
+        if (x.hi > end) end = x.hi;
+    }
+}
+Range range(const void* p, int64_t bytes) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return p ? Range{lo, lo + static_cast<uintptr_t>(bytes)} : Range{0, 0};
+}
+
+constexpr int ROLES = 6;
+anvil_status check_ranges(const Range (*get)(const void*, int, int), const void* tensors, int n, const bool (&written)[ROLES]) {
+    Range* all = new (std::nothrow) Range[static_cast<size_t>(n) * ROLES];
+    if (!all) {
+        set_error_text("out of host memory");
+        return ANVIL_ERR_CUDA;
+    }
+    Role roles[ROLES];
+    for (int k = 0; k < ROLES; ++k) {
+        roles[k] = {all + static_cast<size_t>(k) * n, written[k]};
+        for (int i = 0; i < n; ++i) roles[k].r[i] = get(tensors, i, k);
+    }
+    const bool ok = disjoint(roles, ROLES, n);
+    delete[] all;
+    return ok ? ANVIL_OK : ANVIL_ERR_ALIAS;
+}
+
+// Tensors of one kind share a launch: how param is stored, grad's type, states in 8 bits.
+int kind_of(const anvil_adamw_tensor& t) {
+    const int param = t.mantissa ? ADAMW_SPLIT : t.param_dtype == ANVIL_F32 ? ADAMW_F32 : t.param_dtype == ANVIL_BF16 ? ADAMW_BF16 : ADAMW_F16;
+    return param << 3 | t.grad_dtype << 1 | (t.scales ? 1 : 0);
+}
+int size_of(int dtype) { return dtype == ANVIL_F32 ? 4 : 2; }
+bool dtype_ok(int d) { return d == ANVIL_F32 || d == ANVIL_BF16 || d == ANVIL_F16; }
+
+const Range step_range(const void* tensors, int i, int role) {
+    const anvil_adamw_tensor& t = static_cast<const anvil_adamw_tensor*>(tensors)[i];
+    const int es = t.scales ? 1 : 4;
+    switch (role) {
+        case 0: return range(t.param, t.count * size_of(t.param_dtype));
+        case 1: return range(t.mantissa, t.count * 2);
+        case 2: return range(t.grad, t.count * size_of(t.grad_dtype));
+        case 3: return range(t.exp_avg, t.count * es);
+        case 4: return range(t.exp_avg_sq, t.count * es);
+        default: return range(t.scales, blocks_of(t.count) * 8);
+    }
+}
+const Range values_range(const void* tensors, int i, int role) {
+    const anvil_adamw_state& t = static_cast<const anvil_adamw_state*>(tensors)[i];
+    switch (role) {
+        case 0: return range(t.exp_avg, t.count);
+        case 1: return range(t.exp_avg_sq, t.count);
+        case 2: return range(t.scales, blocks_of(t.count) * 8);
+        case 3: return range(t.m, t.count * 4);
+        case 4: return range(t.v, t.count * 4);
+        default: return {0, 0};
+    }
+}
+
+// Whether a warp may take four neighbours at once of an array of es bytes a value.
+bool vector(const void* p, int es) { return !(reinterpret_cast<uintptr_t>(p) & (4 * es - 1)); }
+
+// Collects tensors of one kind and launches them, ADAMW_MANY or so many chunks at a time.
+template <class Launch>
+struct Batches {
+    AdamwGroup g;
+    Launch launch;
+    explicit Batches(Launch f) : launch(f) { g.p.tensors = g.chunks = 0; }
+    cudaError_t flush() {
+        if (!g.p.tensors) return cudaSuccess;
+        const cudaError_t e = launch(g);
+        g.p.tensors = g.chunks = 0;
+        return e;
+    }
+    cudaError_t add(AdamwTensor t) {
+        const int64_t chunks = chunks_of(t.count);
+        if (g.p.tensors == ADAMW_MANY || g.chunks + chunks > INT32_MAX) {
+            const cudaError_t e = flush();
+            if (e) return e;
+        }
+        t.chunk0 = g.chunks;
+        g.chunks += static_cast<int>(chunks);
+        g.p.t[g.p.tensors++] = t;
+        return cudaSuccess;
+    }
+};
+
+anvil_status check_config(const anvil_adamw_config* c) {
+    // (a NaN fails every comparison)
+    if (!c || !(c->beta1 >= 0 && c->beta1 < 1) || !(c->beta2 >= 0 && c->beta2 < 1) || !(c->eps >= 0) || !(fabs(c->lr) < 1e30) ||
+        !(fabs(c->weight_decay) < 1e30) || !(fabs(c->grad_scale) < 1e30) || c->step < 1)
+        return ANVIL_ERR_INVALID_ARG;
+    return ANVIL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+anvil_status anvil_adamw_scalars(const anvil_adamw_config* c, float* scalars) {
+    const anvil_status st = check_config(c);
+    if (st != ANVIL_OK || !scalars) return st != ANVIL_OK ? st : ANVIL_ERR_INVALID_ARG;
+    const double t = static_cast<double>(c->step);
+    scalars[0] = static_cast<float>(c->lr / (1.0 - pow(c->beta1, t)));
+    scalars[1] = static_cast<float>(1.0 / sqrt(1.0 - pow(c->beta2, t)));
+    scalars[2] = static_cast<float>(1.0 - c->lr * c->weight_decay);
+    scalars[3] = static_cast<float>(c->grad_scale);
+    return ANVIL_OK;
+}
+
+anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, const anvil_adamw_config* config,
+                              const float* d_scalars, void* stream) {
+    float scalars[4];
+    anvil_status st = anvil_adamw_scalars(config, scalars);
+    if (st != ANVIL_OK) return st;
+    if (ntensors < 0 || (ntensors > 0 && !tensors)) return ANVIL_ERR_INVALID_ARG;
+    if (ntensors > ANVIL_MAX_TENSORS) return ANVIL_ERR_UNSUPPORTED_SHAPE;
+    if (off(d_scalars, 4)) return ANVIL_ERR_ALIGNMENT;
+    uint32_t kinds = 0;  // that there are
+    for (int i = 0; i < ntensors; ++i) {
+        const anvil_adamw_tensor& t = tensors[i];
+        if (t.count < 0 || !dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype) || (t.mantissa && t.param_dtype != ANVIL_BF16))
+            return ANVIL_ERR_INVALID_ARG;
+        if (t.param_dtype != ANVIL_F32 && t.grad_dtype != ANVIL_F32 && t.grad_dtype != t.param_dtype) return ANVIL_ERR_INVALID_ARG;
+        if (t.count == 0) continue;
+        if (t.count > ANVIL_MAX_COUNT) return ANVIL_ERR_UNSUPPORTED_SHAPE;
+        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return ANVIL_ERR_INVALID_ARG;
+        const int es = t.scales ? 1 : 4;
+        if (off(t.param, size_of(t.param_dtype)) || off(t.mantissa, 2) || off(t.grad, size_of(t.grad_dtype)) ||
+            off(t.exp_avg, es) || off(t.exp_avg_sq, es) || off(t.scales, 4))
+            return ANVIL_ERR_ALIGNMENT;
+        kinds |= 1u << kind_of(t);
+    }
+    if (!kinds) return ANVIL_OK;
+    const bool written[ROLES] = {true, true, false, true, true, true};
+    if ((st = check_ranges(step_range, tensors, ntensors, written)) != ANVIL_OK) return st;
+    if (d_scalars) {
+        const Range s = range(d_scalars, 16);
+        for (int i = 0; i < ntensors; ++i)
+            for (int k = 0; k < ROLES; ++k)
+                if (written[k] && tensors[i].count && overlap(s, step_range(tensors, i, k))) return ANVIL_ERR_ALIAS;
+    }
+    DeviceState* dev = nullptr;
+    if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    for (int kind = 0; kind < 32; ++kind) {
+        if (!(kinds >> kind & 1)) continue;
+        const int param = kind >> 3, grad = kind >> 1 & 3;
+        const bool codes = kind & 1;
+        auto launch = [&](const AdamwGroup& g) {
+            return profiled(ANVIL_KERNEL_ADAMW, s, [&] { return launch_adamw(g, param, grad, codes, s); });
+        };
+        Batches<decltype(launch)> batch(launch);
+        batch.g.p.beta1 = static_cast<float>(config->beta1);
+        batch.g.p.c1 = static_cast<float>(1.0 - config->beta1);
+        batch.g.p.beta2 = static_cast<float>(config->beta2);
+        batch.g.p.c2 = static_cast<float>(1.0 - config->beta2);
+        batch.g.p.eps = static_cast<float>(config->eps);
+        for (int k = 0; k < 4; ++k) batch.g.p.scalars[k] = scalars[k];
+        batch.g.p.d_scalars = d_scalars;
+        for (int i = 0; i < ntensors; ++i) {
+            const anvil_adamw_tensor& t = tensors[i];
+            if (t.count == 0 || kind_of(t) != kind) continue;
+            const int es = codes ? 1 : 4;
+            const bool vec = vector(t.param, size_of(t.param_dtype)) && vector(t.mantissa, 2) && vector(t.grad, size_of(t.grad_dtype)) &&
+                             vector(t.exp_avg, es) && vector(t.exp_avg_sq, es);
+            if ((e = batch.add({t.param, t.mantissa, t.grad, t.exp_avg, t.exp_avg_sq, t.scales, t.count, vec, 0})))
+                return cuda_fail(e, "AdamW launch");
+        }
+        if ((e = batch.flush())) return cuda_fail(e, "AdamW launch");
+    }
+    return ANVIL_OK;
+}
+
+anvil_status anvil_adamw_values(const anvil_adamw_state* states, int nstates, void* stream) {
+    if (nstates < 0 || (nstates > 0 && !states)) return ANVIL_ERR_INVALID_ARG;
+    if (nstates > ANVIL_MAX_TENSORS) return ANVIL_ERR_UNSUPPORTED_SHAPE;
+    bool any = false;
+    for (int i = 0; i < nstates; ++i) {
+        const anvil_adamw_state& t = states[i];
+        if (t.count < 0) return ANVIL_ERR_INVALID_ARG;
+        if (t.count == 0) continue;
+        if (t.count > ANVIL_MAX_COUNT) return ANVIL_ERR_UNSUPPORTED_SHAPE;
+        if (!t.exp_avg || !t.exp_avg_sq || !t.scales || !t.m || !t.v) return ANVIL_ERR_INVALID_ARG;
+        if (off(t.scales, 4) || off(t.m, 4) || off(t.v, 4)) return ANVIL_ERR_ALIGNMENT;
+        any = true;
+    }
+    if (!any) return ANVIL_OK;
+    const bool written[ROLES] = {false, false, false, true, true, false};
+    anvil_status st = check_ranges(values_range, states, nstates, written);
+    if (st != ANVIL_OK) return st;
+    DeviceState* dev = nullptr;
+    if ((st = device_setup(&dev)) != ANVIL_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto launch = [&](const AdamwGroup& g) {
+        return profiled(ANVIL_KERNEL_ADAMW, s, [&] { return launch_adamw_values(g, s); });
+    };
+    Batches<decltype(launch)> batch(launch);
+    cudaError_t e;
+    for (int i = 0; i < nstates; ++i) {
+        const anvil_adamw_state& t = states[i];
+        if (t.count == 0) continue;
+        const bool vec = vector(t.exp_avg, 1) && vector(t.exp_avg_sq, 1) && vector(t.m, 4) && vector(t.v, 4);
+        if ((e = batch.add({t.m, nullptr, t.v, const_cast<void*>(t.exp_avg), const_cast<void*>(t.exp_avg_sq),
+                            const_cast<float*>(t.scales), t.count, vec, 0})))
+            return cuda_fail(e, "AdamW launch");
+    }
+    if ((e = batch.flush())) return cuda_fail(e, "AdamW launch");
+    return ANVIL_OK;
+}
+
+}  // extern "C"

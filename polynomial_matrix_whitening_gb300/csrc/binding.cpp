@@ -18,6 +18,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <vector>
+
 #include "../../include/anvil.h"
 
 namespace {
@@ -32,6 +34,8 @@ struct Api {
     anvil_status (*linear_backward)(const anvil_linear_grad_desc*, void*, size_t, void*);
     anvil_status (*token_logprobs)(const anvil_logprob_desc*, void*);
     anvil_status (*token_logprobs_backward)(const anvil_logprob_grad_desc*, void*);
+    anvil_status (*adamw_step)(const anvil_adamw_tensor*, int, const anvil_adamw_config*, const float*, void*);
+    anvil_status (*adamw_values)(const anvil_adamw_state*, int, void*);
 };
 Api api;
 PyObject* g_check = nullptr;          // Python: raises AnvilError(status, where)
@@ -516,6 +520,134 @@ PyObject* token_logprobs_backward(PyObject* const* a) {
     return wrap(std::move(dl));
 }
 
+// ---------------------------------------------------------------- AdamW
+// A list or tuple of tensors (of `n`, or any number where n < 0); items may be None where `gaps`.
+struct Tensors {
+    PyObject* seq;
+    Py_ssize_t n;
+    bool gaps;
+    const char* what;
+    Tensors(PyObject* o, Py_ssize_t want, bool may_be_none, const char* name) : seq(nullptr), n(want), gaps(may_be_none), what(name) {
+        if (o == Py_None && gaps) return;
+        if (!PyList_Check(o) && !PyTuple_Check(o)) refuse("%s must be a list of tensors", what);
+        seq = o;
+        n = PySequence_Fast_GET_SIZE(o);
+        if (want >= 0 && n != want) refuse("%s must have one tensor for each of params", what);
+    }
+    const at::Tensor* at(Py_ssize_t i) const {
+        PyObject* o = seq ? PySequence_Fast_GET_ITEM(seq, i) : Py_None;
+        if (o == Py_None && gaps) return nullptr;
+        if (!THPVariable_Check(o)) refuse("%s must be a list of tensors", what);
+        return &THPVariable_Unpack(o);
+    }
+};
+void plain_tensor(const at::Tensor& t, at::Device device, int64_t count, const char* where, const char* what) {
+    if (t.device() != device) refuse("%s: every tensor must be on the current CUDA device", where);
+    if (!t.is_contiguous()) refuse("%s: %s must be contiguous", where, what);
+    if (t.numel() != count) refuse("%s: %s must have its parameter's size", where, what);
+}
+// The codes and their scales, checked against a count.
+void check_codes(const at::Tensor& m, const at::Tensor& v, const at::Tensor& scales, int64_t count, at::Device device, const char* where) {
+    if (m.scalar_type() != at::kFloat8_e4m3fn || v.scalar_type() != at::kByte)
+        refuse("%s: with scales exp_avg must be float8_e4m3fn and exp_avg_sq uint8", where);
+    const int64_t blocks = (count + ANVIL_ADAMW_BLOCK - 1) / ANVIL_ADAMW_BLOCK;
+    plain_tensor(scales, device, 2 * blocks, where, "scales, [2, blocks],");
+    if (scales.scalar_type() != at::kFloat) refuse("%s: scales must be fp32", where);
+}
+void overwritten(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();  // (a graph that saved it would use the new values)
+}
+at::Device current(const char* where, const at::Tensor* first) {
+    if (!first || !first->is_cuda()) refuse("%s: every tensor must be on the current CUDA device", where);
+    return at::Device(at::kCUDA, c10::cuda::current_device());
+}
+double number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw PyError();
+    return v;
+}
+
+// (params, grads, exp_avgs, exp_avg_sqs, mantissas, scales, scalars, lr, beta1, beta2, eps, weight_decay, grad_scale, step)
+PyObject* adamw_step(PyObject* const* a) {
+    static const char* const where = "adamw_step";
+    const Tensors params(a[0], -1, false, "params"), grads(a[1], params.n, false, "grads"), ms(a[2], params.n, false, "exp_avgs"),
+        vs(a[3], params.n, false, "exp_avg_sqs"), lows(a[4], params.n, true, "mantissas"), scales(a[5], params.n, true, "scales");
+    const at::Tensor* scalars = maybe(a[6], "scalars");
+    anvil_adamw_config c = {number(a[7]), number(a[8]), number(a[9]), number(a[10]), number(a[11]), number(a[12]), 0};
+    c.step = PyLong_AsLongLong(a[13]);
+    if (c.step == -1 && PyErr_Occurred()) throw PyError();
+    if (params.n > ANVIL_MAX_TENSORS) refuse("adamw_step: too many tensors");
+    if (!params.n) return Py_NewRef(Py_None);
+    const at::Device device = current(where, params.at(0));
+    std::vector<anvil_adamw_tensor> tensors(static_cast<size_t>(params.n));
+    for (Py_ssize_t i = 0; i < params.n; ++i) {
+        const at::Tensor &p = *params.at(i), &g = *grads.at(i), &m = *ms.at(i), &v = *vs.at(i);
+        const at::Tensor *low = lows.at(i), *sc = scales.at(i);
+        const int64_t count = p.numel();
+        anvil_adamw_tensor& t = tensors[static_cast<size_t>(i)];
+        t = {};
+        t.param_dtype = dtype_code(p, "params");
+        t.grad_dtype = dtype_code(g, "grads");
+        if (t.param_dtype != ANVIL_F32 && t.grad_dtype != ANVIL_F32 && t.grad_dtype != t.param_dtype)
+            refuse("adamw_step: grads must be fp32 or of their parameters' types");
+        plain_tensor(p, device, count, where, "params");
+        plain_tensor(g, device, count, where, "grads");
+        plain_tensor(m, device, count, where, "exp_avgs");
+        plain_tensor(v, device, count, where, "exp_avg_sqs");
+        if (sc) check_codes(m, v, *sc, count, device, where);
+        else if (m.scalar_type() != at::kFloat || v.scalar_type() != at::kFloat)
+            refuse("adamw_step: exp_avgs and exp_avg_sqs must be fp32, or 8-bit codes with scales");
+        if (low) {
+            plain_tensor(*low, device, count, where, "mantissas");
+            if (t.param_dtype != ANVIL_BF16 || (low->scalar_type() != at::kShort && low->scalar_type() != at::kUInt16))
+                refuse("adamw_step: mantissas must be 16-bit integers beside bf16 parameters");
+            t.mantissa = static_cast<uint16_t*>(low->data_ptr());
+        }
+        t.param = p.data_ptr();
+        t.grad = g.data_ptr();
+        t.exp_avg = m.data_ptr();
+        t.exp_avg_sq = v.data_ptr();
+        t.scales = sc ? static_cast<float*>(sc->data_ptr()) : nullptr;
+        t.count = count;
+    }
+    const float* ds = nullptr;
+    if (scalars) {
+        plain_tensor(*scalars, device, 4, where, "scalars, fp32 [4],");
+        if (scalars->scalar_type() != at::kFloat) refuse("adamw_step: scalars must be fp32 [4]");
+        ds = static_cast<const float*>(scalars->data_ptr());
+    }
+    void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    check(api.adamw_step(tensors.data(), static_cast<int>(params.n), &c, ds, stream), "anvil_adamw_step");
+    for (Py_ssize_t i = 0; i < params.n; ++i) overwritten(*params.at(i));
+    return Py_NewRef(Py_None);
+}
+
+// (exp_avgs, exp_avg_sqs, scales, m's, v's)
+PyObject* adamw_values(PyObject* const* a) {
+    static const char* const where = "adamw_values";
+    const Tensors ms(a[0], -1, false, "exp_avgs"), vs(a[1], ms.n, false, "exp_avg_sqs"), scales(a[2], ms.n, false, "scales"),
+        om(a[3], ms.n, false, "out[0]"), ov(a[4], ms.n, false, "out[1]");
+    if (ms.n > ANVIL_MAX_TENSORS) refuse("adamw_values: too many tensors");
+    if (!ms.n) return Py_NewRef(Py_None);
+    const at::Device device = current(where, ms.at(0));
+    std::vector<anvil_adamw_state> states(static_cast<size_t>(ms.n));
+    for (Py_ssize_t i = 0; i < ms.n; ++i) {
+        const at::Tensor &m = *ms.at(i), &v = *vs.at(i), &sc = *scales.at(i), &to_m = *om.at(i), &to_v = *ov.at(i);
+        const int64_t count = m.numel();
+        plain_tensor(m, device, count, where, "exp_avgs");
+        plain_tensor(v, device, count, where, "exp_avg_sqs");
+        check_codes(m, v, sc, count, device, where);
+        plain_tensor(to_m, device, count, where, "out");
+        plain_tensor(to_v, device, count, where, "out");
+        if (to_m.scalar_type() != at::kFloat || to_v.scalar_type() != at::kFloat) refuse("adamw_values: out must be fp32");
+        states[static_cast<size_t>(i)] = {m.data_ptr(), v.data_ptr(), static_cast<const float*>(sc.data_ptr()),
+                                          static_cast<float*>(to_m.data_ptr()), static_cast<float*>(to_v.data_ptr()), count};
+    }
+    void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    check(api.adamw_values(states.data(), static_cast<int>(ms.n), stream), "anvil_adamw_values");
+    return Py_NewRef(Py_None);
+}
+
 // Exceptions end here: a C++ one (out of memory, say) becomes the Python one torch gives it.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -561,6 +693,8 @@ PyMethodDef methods[] = {
     ANVIL_ENTRY(linear_backward, 14),
     ANVIL_ENTRY(token_logprobs, 3),
     ANVIL_ENTRY(token_logprobs_backward, 7),
+    ANVIL_ENTRY(adamw_step, 14),
+    ANVIL_ENTRY(adamw_values, 5),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_anvil_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
