@@ -418,6 +418,59 @@ size_t anvil_linear_backward_workspace_bytes(const anvil_linear_grad_desc* desc)
 anvil_status anvil_linear_backward(const anvil_linear_grad_desc* desc, void* workspace, size_t workspace_bytes,
                                    void* stream);
 
+/* The gated layer:  g = x G^T,  u = x U^T,  y = act(g) * u, elementwise.
+ * x [rows, k], y [rows, n], G and U: [n, k] each, or both stored as their transposes [k, n] when
+ * weight_transposed != 0, all of type dtype (ANVIL_BF16 or ANVIL_F16); views of one matrix that
+ * holds both are fine.  preact_gate and preact_up [rows, n], or NULL, receive g and u (rounded; y comes
+ * from the unrounded values) for the backward pass.  From one row to many: few rows read the
+ * weights once. */
+typedef struct {
+    const void* x;
+    const void* gate;
+    const void* up;
+    void* y;
+    void* preact_gate;
+    void* preact_up;
+    int64_t rows;
+    int64_t ldx, ldgate, ldup, ldy, ldzg, ldzu;
+    int n, k;
+    int dtype;
+    int activation;
+    int weight_transposed;
+} anvil_gated_desc;
+/* Scratch of a call, as anvil_linear_workspace_bytes. */
+size_t anvil_gated_linear_workspace_bytes(const anvil_gated_desc* desc);
+anvil_status anvil_gated_linear_forward(const anvil_gated_desc* desc, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient, for dy = dL/dy and the forward pass's g and u:
+ *   dg = dy u act'(g),  du = dy act(g),  dx = dg G + du U,  dgate = dg^T x,  dup = du^T x.
+ * dx [rows, k] of type dtype, or NULL; dgate and dup in the weights' layout, of type dweight_dtype: dtype
+ * or ANVIL_F32, both or neither NULL; x is read for them only, the weights for dx only.  dg and
+ * du are rounded to dtype as operands, or kept in two parts with activation + ANVIL_DZ_TWO_PARTS, as the
+ * linear layer's dz is.  accumulate != 0: dgate and dup are added to what they hold.  rows is at most
+ * ANVIL_MAX_ROWS / 4. */
+typedef struct {
+    const void* dy;
+    const void* x;
+    const void* gate;
+    const void* up;
+    const void* preact_gate;
+    const void* preact_up;
+    void* dx;
+    void* dgate;
+    void* dup;
+    int64_t rows;
+    int64_t lddy, ldx, ldgate, ldup, ldzg, ldzu, lddx, lddgate, lddup;
+    int n, k;
+    int dtype, dweight_dtype;
+    int activation;
+    int weight_transposed;
+    int accumulate;
+} anvil_gated_grad_desc;
+size_t anvil_gated_linear_backward_workspace_bytes(const anvil_gated_grad_desc* desc);
+anvil_status anvil_gated_linear_backward(const anvil_gated_grad_desc* desc, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
 /* Log probabilities of given tokens under logits [rows, vocab] of type dtype:
  *   lse = log sum_j e^x_j,  logprob = x_target - lse,  entropy = lse - sum_j p_j x_j,
  *   and the `top` (0..ANVIL_MAX_TOP, at most vocab) largest x_j - lse with their columns,
@@ -540,7 +593,10 @@ typedef enum {
     ANVIL_KERNEL_LINEAR_SUM = 18,        /* sums of split products and of dbias */
     ANVIL_KERNEL_LOGPROB = 19,           /* token log probabilities */
     ANVIL_KERNEL_LOGPROB_BACKWARD = 20,  /* their gradient */
-    ANVIL_KERNEL_ADAMW = 21              /* AdamW over many tensors, and the values of its states */
+    ANVIL_KERNEL_ADAMW = 21,             /* AdamW over many tensors, and the values of its states */
+    ANVIL_KERNEL_GATED_PREPARE = 22,     /* the gated layer: dg and du */
+    ANVIL_KERNEL_GATED_PRODUCT = 23,     /* both products, activation and product */
+    ANVIL_KERNEL_GATED_SUM = 24          /* sums of its split products */
 } anvil_kernel_kind;
 
 typedef struct { int kind; float ms; } anvil_profile_record;

@@ -43,7 +43,8 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, ERR_ALIGNMENT, ERR_ALIAS, ERR_WORKSP
 KERNEL_KINDS = ("momentum", "norm_d", "normalize", "gram_norm", "gram", "sqpoly", "xupdate",
                 "xupdate_out", "tail_power", "tail_scale", "tail_apply", "adam", "cascade",
                 "norm_forward", "norm_backward", "norm_grads", "linear_prepare", "linear_product",
-                "linear_sum", "logprob", "logprob_backward", "adamw")
+                "linear_sum", "logprob", "logprob_backward", "adamw",
+                "gated_prepare", "gated_product", "gated_sum")
 MAX_MAPS, MAX_BANKS, MAX_TOP = 16, 8, 32
 
 
@@ -118,6 +119,21 @@ class LinearGradDesc(ctypes.Structure):
                 ("accumulate", _I)]
 
 
+class GatedDesc(ctypes.Structure):
+    _fields_ = [("x", _P), ("gate", _P), ("up", _P), ("y", _P), ("preact_gate", _P), ("preact_up", _P),
+                ("rows", _L), ("ldx", _L), ("ldgate", _L), ("ldup", _L), ("ldy", _L), ("ldzg", _L),
+                ("ldzu", _L), ("n", _I), ("k", _I), ("dtype", _I), ("activation", _I),
+                ("weight_transposed", _I)]
+
+
+class GatedGradDesc(ctypes.Structure):
+    _fields_ = [("dy", _P), ("x", _P), ("gate", _P), ("up", _P), ("preact_gate", _P), ("preact_up", _P),
+                ("dx", _P), ("dgate", _P), ("dup", _P), ("rows", _L), ("lddy", _L), ("ldx", _L),
+                ("ldgate", _L), ("ldup", _L), ("ldzg", _L), ("ldzu", _L), ("lddx", _L), ("lddgate", _L),
+                ("lddup", _L), ("n", _I), ("k", _I), ("dtype", _I), ("dweight_dtype", _I),
+                ("activation", _I), ("weight_transposed", _I), ("accumulate", _I)]
+
+
 class LogprobDesc(ctypes.Structure):
     _fields_ = [("logits", _P), ("targets", _P), ("logprob", _P), ("entropy", _P), ("lse", _P),
                 ("top_logprob", _P), ("top_index", _P), ("rows", _L), ("ld", _L), ("vocab", _I),
@@ -185,10 +201,17 @@ _lib.anvil_linear_forward.argtypes = [ctypes.POINTER(LinearDesc), _vp, _sz, _vp]
 _lib.anvil_linear_backward_workspace_bytes.argtypes = [ctypes.POINTER(LinearGradDesc)]
 _lib.anvil_linear_backward_workspace_bytes.restype = _sz
 _lib.anvil_linear_backward.argtypes = [ctypes.POINTER(LinearGradDesc), _vp, _sz, _vp]
+_lib.anvil_gated_linear_workspace_bytes.argtypes = [ctypes.POINTER(GatedDesc)]
+_lib.anvil_gated_linear_workspace_bytes.restype = _sz
+_lib.anvil_gated_linear_forward.argtypes = [ctypes.POINTER(GatedDesc), _vp, _sz, _vp]
+_lib.anvil_gated_linear_backward_workspace_bytes.argtypes = [ctypes.POINTER(GatedGradDesc)]
+_lib.anvil_gated_linear_backward_workspace_bytes.restype = _sz
+_lib.anvil_gated_linear_backward.argtypes = [ctypes.POINTER(GatedGradDesc), _vp, _sz, _vp]
 _lib.anvil_token_logprobs.argtypes = [ctypes.POINTER(LogprobDesc), _vp]
 _lib.anvil_token_logprobs_backward.argtypes = [ctypes.POINTER(LogprobGradDesc), _vp]
 for _f_name in ("layernorm_forward", "layernorm_backward", "linear_forward", "linear_backward",
-                "token_logprobs", "token_logprobs_backward", "adamw_step", "adamw_scalars", "adamw_values"):
+                "token_logprobs", "token_logprobs_backward", "adamw_step", "adamw_scalars", "adamw_values",
+                "gated_linear_forward", "gated_linear_backward"):
     getattr(_lib, "anvil_" + _f_name).restype = _i
 _lib.anvil_device_error.argtypes = [_i]
 _lib.anvil_device_error.restype = _i
@@ -555,7 +578,9 @@ ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "sil
 _native = None
 _ENTRY_POINTS = ("layernorm_forward", "layernorm_backward_workspace_bytes", "layernorm_backward",
                  "linear_workspace_bytes", "linear_forward", "linear_backward_workspace_bytes",
-                 "linear_backward", "token_logprobs", "token_logprobs_backward", "adamw_step", "adamw_values")
+                 "linear_backward", "token_logprobs", "token_logprobs_backward", "adamw_step", "adamw_values",
+                 "gated_linear_workspace_bytes", "gated_linear_forward", "gated_linear_backward_workspace_bytes",
+                 "gated_linear_backward")
 
 
 def _load_native():
@@ -620,6 +645,13 @@ def _activation(name):
     return code
 
 
+def _fp32_dweight(dtype, x):
+    fp32 = dtype is not None and dtype != x.dtype
+    if fp32 and str(dtype) != "torch.float32":
+        raise ValueError("dweight must be fp32 or of x's type")
+    return fp32
+
+
 def linear_forward(x, weight, bias=None, activation=None, residual=None, save_preact=False, out=None,
                    workspace=None, stream=None):
     """y = act(x weight^T + bias) + residual, bf16 or fp16, for x [..., k] and weight [n, k].
@@ -656,12 +688,45 @@ def linear_backward(dy, x, weight, preact=None, activation=None, need_dx=True, n
                           (dy, x, weight, preact, dweight, dbias, workspace))
     if dz_parts not in (1, 2):
         raise ValueError("dz_parts must be 1 or 2")
-    fp32 = dweight_dtype is not None and dweight_dtype != x.dtype
-    if fp32 and str(dweight_dtype) != "torch.float32":
-        raise ValueError("dweight must be fp32 or of x's type")
     return (_native or _load_native()).linear_backward(dy, x, weight, preact, _activation(activation), need_dx,
-                                                       need_dweight, bias_grad, fp32, dweight, dbias, accumulate,
+                                                       need_dweight, bias_grad, _fp32_dweight(dweight_dtype, x), dweight, dbias, accumulate,
                                                        workspace, dz_parts == 2)
+
+
+def gated_linear_forward(x, gate, up, activation="silu", save_preact=False, out=None, workspace=None, stream=None):
+    """y = act(x gate^T) * (x up^T), bf16 or fp16, for x [..., k] and weights [n, k].
+
+    The weights may be stored by rows or both by columns, and be views of one matrix that holds
+    both.  Returns y, or (y, g, u) with save_preact: what gated_linear_backward takes.
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: gated_linear_forward(x, gate, up, activation, save_preact, out, workspace),
+                          (x, gate, up, out, workspace))
+    y, g, u = (_native or _load_native()).gated_linear_forward(x, gate, up, _activation(activation), save_preact, out,
+                                                               workspace)
+    return (y, g, u) if save_preact else y
+
+
+def gated_linear_backward(dy, x, gate, up, preact_gate, preact_up, activation="silu", need_dx=True, need_dweight=True,
+                          dweight_dtype=None, dgate=None, dup=None, accumulate=False, workspace=None, stream=None,
+                          dz_parts=1):
+    """Gradient of gated_linear_forward: returns (dx, dgate, dup), None where not asked for.
+
+    preact_gate and preact_up are the forward call's g and u.  dgate and dup have the weights'
+    shape and order and dweight_dtype: x's type (default) or fp32; they may be given (with
+    accumulate they are added to).  The gradients of g and u are rounded to x's type before the
+    products, or kept in two parts, as linear_backward's (dz_parts).
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: gated_linear_backward(dy, x, gate, up, preact_gate, preact_up, activation, need_dx,
+                                                                need_dweight, dweight_dtype, dgate, dup, accumulate, workspace,
+                                                                dz_parts=dz_parts),
+                          (dy, x, gate, up, preact_gate, preact_up, dgate, dup, workspace))
+    if dz_parts not in (1, 2):
+        raise ValueError("dz_parts must be 1 or 2")
+    return (_native or _load_native()).gated_linear_backward(dy, x, gate, up, preact_gate, preact_up, _activation(activation),
+                                                             need_dx, need_dweight, _fp32_dweight(dweight_dtype, x), dgate, dup,
+                                                             accumulate, workspace, dz_parts == 2)
 
 
 def token_logprobs(logits, targets=None, top=0, stream=None):

@@ -22,6 +22,7 @@ struct GemmEpilogue {
     int bias_f32;         // bias is fp32 (else the operands' type)
     int act;
     int out_f32;          // out (and in) are fp32
+    const float* scale;   // null, or what v is multiplied by first (PairMultiParams only)
 };
 
 // Which tiles are computed in one piece and which in parts.  The first `whole` tiles are
@@ -50,6 +51,16 @@ struct PairGemmParams {
     int overlap_previous;           // and this one before the previous one has (both products of a backward pass)
     unsigned* err;
 };
+// Several products in one launch.  A result's contraction may be in up to four segments, each with
+// operands of its own (a sum of products); and there may be two results of the same sizes, the second
+// one's rows of tiles after the first one's (tiles_r counts both, rows one).
+struct PairMultiParams : PairGemmParams {
+    CUtensorMap tm_a2[3], tm_b2[3];  // operands of number 1 to 3: result * segments + segment (0: tm_a, tm_b)
+    CUtensorMap tm_in2, tm_out2;     // the second result's
+    GemmEpilogue epi2;
+    int result_tiles;                // rows of tiles of one result
+    int segments, seg_kb;            // k-blocks of a segment
+};
 // What is added up after the products, in one launch: the tail tiles' parts of up to two
 // products, with what follows the accumulator, and the column sums of a bias gradient.
 struct TailSumParams {
@@ -57,6 +68,8 @@ struct TailSumParams {
     const float* part;
     int rows, cols, tiles_r, tiles_c, tiles;  // tiles: of the tail (0: nothing to do)
     TileSplit split;
+    GemmEpilogue epi2;      // of a second result,
+    int result_tiles;       // whose rows of tiles come after these (0: there is none)
 };
 struct ColumnSumParams {
     const float* part;  // [blocks][cols]
@@ -91,6 +104,36 @@ struct TokenParams {
     int rows, cols, k;
     int f16;
 };
+// The gated layer: y = act(g) u with g = x G^T, u = x U^T, n columns each.  A tile of the pair kernel
+// is 256 rows by 128 columns of both (p.cols is n; tm_b is G's map, tm_b2 U's; g goes to epi.z, u to z2
+// where they are kept); the row kernel's 128 weight rows are 64 of each.
+struct PairGatedParams : PairGemmParams {
+    CUtensorMap tm_b2, tm_z2;
+    void* z2;
+    long long ldz2;
+    int z2_tma;
+};
+struct RowGatedParams : RowGemmParams {
+    CUtensorMap tm_a2;
+    void* z2;
+    long long ldz2;
+};
+struct TokenGatedParams : TokenParams {
+    const void* w2;
+    long long ldw2;
+    void* z2;
+    long long ldz2;
+};
+// The tail tiles' parts of a gated product.
+struct GatedTailParams {
+    GemmEpilogue epi;
+    void* z2;
+    long long ldz2;
+    const float* part;
+    int rows, cols, tiles_r, tiles_c, tiles, f16;
+    TileSplit split;
+};
+constexpr int GATED_COLS = 128;  // of y in a tile
 constexpr int TOKEN_ROWS = 2;
 constexpr int TOKEN_CHUNKS = 3008;  // 16-byte chunks of the tokens that shared memory takes (47 KB, 48 with what is static)
 
@@ -102,6 +145,25 @@ constexpr int ROW_TWO_TOKENS = 32; // tokens of a block up to which two share an
 
 cudaError_t linear_prepare();
 cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t stream);
+cudaError_t gated_prepare();
+cudaError_t launch_pair_gated(const PairGatedParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_row_gated(const RowGatedParams& p, int bn, int sm_count, cudaStream_t stream);
+cudaError_t launch_tokens_gated(const TokenGatedParams& p, cudaStream_t stream);
+cudaError_t launch_gated_finish(const GatedTailParams& p, cudaStream_t stream);
+// dg = dy u act'(g) and du = dy act(g), rounded to the operands' type, [rows, ldd] each; two parts:
+// what the rounding drops, rounded itself, behind each (dg, its rest, du, its rest).
+struct GatedGradParams {
+    const void* dy;
+    const void* g;
+    const void* u;
+    void* dz;
+    int two_parts;
+    long long rows, lddy, ldg, ldu, ldd;
+    int cols, act, f16;
+};
+cudaError_t launch_gated_grad(const GatedGradParams& p, cudaStream_t stream);
+cudaError_t multi_prepare();
+cudaError_t launch_pair_multi(const PairMultiParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream);
 cudaError_t launch_tokens(const TokenParams& p, cudaStream_t stream);
 // bn: B's rows per block (16, 32, 64 or 128)

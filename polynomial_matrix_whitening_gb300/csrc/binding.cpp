@@ -36,6 +36,10 @@ struct Api {
     anvil_status (*token_logprobs_backward)(const anvil_logprob_grad_desc*, void*);
     anvil_status (*adamw_step)(const anvil_adamw_tensor*, int, const anvil_adamw_config*, const float*, void*);
     anvil_status (*adamw_values)(const anvil_adamw_state*, int, void*);
+    size_t (*gated_linear_workspace_bytes)(const anvil_gated_desc*);
+    anvil_status (*gated_linear_forward)(const anvil_gated_desc*, void*, size_t, void*);
+    size_t (*gated_linear_backward_workspace_bytes)(const anvil_gated_grad_desc*);
+    anvil_status (*gated_linear_backward)(const anvil_gated_grad_desc*, void*, size_t, void*);
 };
 Api api;
 PyObject* g_check = nullptr;          // Python: raises AnvilError(status, where)
@@ -444,6 +448,129 @@ PyObject* linear_backward(PyObject* const* a) {
     return tuple_of(std::move(dx), std::move(dw), std::move(db));
 }
 
+// ---------------------------------------------------------------- the gated layer
+// The order (0 by rows, 1 by columns) that every given matrix of gate's shape is stored in.
+int common_order(const at::Tensor& gate, at::ScalarType type, int64_t k, std::initializer_list<const at::Tensor*> others) {
+    if (gate.dim() != 2 || gate.scalar_type() != type || gate.size(1) != k)
+        refuse("gate and up must be [n, %lld] of %s", static_cast<long long>(k), c10::toString(type));
+    for (const at::Tensor* t : others)
+        if (t && t->sizes() != gate.sizes()) refuse("up, dgate and dup must have gate's shape");
+    for (int by_columns = 0; by_columns < 2; ++by_columns) {
+        bool all = ld_in_order(gate, by_columns) >= 0;
+        for (const at::Tensor* t : others) all = all && (!t || ld_in_order(*t, by_columns) >= 0);
+        if (all) return by_columns;
+    }
+    refuse("gate, up, dgate and dup must be stored all by rows or all by columns");
+}
+
+// (x, gate, up, activation, save_preact, out, workspace) -> (y, g or None, u or None)
+PyObject* gated_linear_forward(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0], "x"), &gate = tensor(a[1], "gate"), &up = tensor(a[2], "up");
+    const at::Tensor *out = maybe(a[5], "out"), *ws = maybe(a[6], "workspace");
+    anvil_gated_desc d = {};
+    d.activation = static_cast<int>(PyLong_AsLong(a[3]));
+    d.dtype = dtype_code(x, "x");
+    if (d.dtype == ANVIL_F32) refuse("x must be bf16 or fp16");
+    const at::ScalarType type = x.scalar_type();
+    const Rows r = rows_of(x, "x");
+    if (up.scalar_type() != type) refuse("gate and up must be of x's type");
+    d.weight_transposed = common_order(gate, type, r.width, {&up});
+    const int64_t n = gate.size(0);
+    c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
+    shape.back() = n;
+    const Here here("gated_linear_forward", {&x, &gate, &up, out, ws});
+    at::Tensor y = result(out, shape, type, "the result's shape and type", &d.ldy, here), g, u;
+    if (truth(a[4])) {
+        g = here.empty(shape, type);
+        u = here.empty(shape, type);
+        d.preact_gate = g.data_ptr();
+        d.preact_up = u.data_ptr();
+        d.ldzg = d.ldzu = n;
+    }
+    d.x = x.data_ptr();
+    d.gate = gate.data_ptr();
+    d.up = up.data_ptr();
+    d.y = y.data_ptr();
+    d.rows = r.rows;
+    d.ldx = r.ld;
+    d.ldgate = ld_in_order(gate, d.weight_transposed);
+    d.ldup = ld_in_order(up, d.weight_transposed);
+    d.n = as_int(n, "gate");
+    d.k = as_int(r.width, "gate");
+    const Scratch scratch(ws ? 0 : api.gated_linear_workspace_bytes(&d), ws, here);
+    check(api.gated_linear_forward(&d, scratch.p, scratch.bytes, here.stream), "anvil_gated_linear_forward");
+    return tuple_of(std::move(y), std::move(g), std::move(u));
+}
+
+// (dy, x, gate, up, g, u, activation, need_dx, need_dweight, dweight fp32 (None: x's type), dgate, dup, accumulate,
+// workspace, dz in two parts) -> (dx, dgate, dup)
+PyObject* gated_linear_backward(PyObject* const* a) {
+    const at::Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &gate = tensor(a[2], "gate"), &up = tensor(a[3], "up"),
+                     &zg = tensor(a[4], "preact_gate"), &zu = tensor(a[5], "preact_up");
+    const at::Tensor *dg_in = maybe(a[10], "dgate"), *du_in = maybe(a[11], "dup"), *ws = maybe(a[13], "workspace");
+    const bool need_dx = truth(a[7]), need_dw = truth(a[8]);
+    anvil_gated_grad_desc d = {};
+    d.activation = static_cast<int>(PyLong_AsLong(a[6]));
+    d.dtype = dtype_code(x, "x");
+    if (d.dtype == ANVIL_F32) refuse("x must be bf16 or fp16");
+    const at::ScalarType type = x.scalar_type();
+    const Rows r = rows_of(x, "x");
+    if (up.scalar_type() != type) refuse("gate and up must be of x's type");
+    if ((dg_in != nullptr) != (du_in != nullptr)) refuse("dgate and dup must be given together");
+    d.weight_transposed = common_order(gate, type, r.width, {&up, need_dw ? dg_in : nullptr, need_dw ? du_in : nullptr});
+    const int64_t n = gate.size(0);
+    c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
+    shape.back() = n;
+    same_form(dy, shape, type, "dy", "the forward result's shape and type");
+    same_form(zg, shape, type, "preact_gate", "the forward result's shape and type");
+    same_form(zu, shape, type, "preact_up", "the forward result's shape and type");
+    d.lddy = rows_of(dy, "dy").ld;
+    d.ldzg = rows_of(zg, "preact_gate").ld;
+    d.ldzu = rows_of(zu, "preact_up").ld;
+    d.accumulate = truth(a[12]);
+    if (d.accumulate && need_dw && !dg_in) refuse("accumulate needs dgate and dup to add to");
+    at::ScalarType wt = type;
+    if (dg_in) {
+        wt = dg_in->scalar_type();
+        if ((wt != type && wt != at::kFloat) || du_in->scalar_type() != wt) refuse("dgate and dup must be both fp32 or both of x's type");
+    } else if (truth(a[9])) {
+        wt = at::kFloat;
+    }
+    const Here here("gated_linear_backward", {&x, &dy, &gate, &up, &zg, &zu, dg_in, du_in, ws});
+    at::Tensor dx, dg, du;
+    if (need_dx) {
+        dx = here.empty(x.sizes(), type);
+        d.dx = dx.data_ptr();
+        d.lddx = r.width;
+    }
+    if (need_dw) {
+        const auto make = [&] { return d.weight_transposed ? here.empty({r.width, n}, wt).t() : here.empty({n, r.width}, wt); };
+        dg = dg_in ? *dg_in : make();
+        du = du_in ? *du_in : make();
+        d.dgate = dg.data_ptr();
+        d.dup = du.data_ptr();
+        d.lddgate = ld_in_order(dg, d.weight_transposed);
+        d.lddup = ld_in_order(du, d.weight_transposed);
+    }
+    d.dy = dy.data_ptr();
+    d.x = x.data_ptr();
+    d.gate = gate.data_ptr();
+    d.up = up.data_ptr();
+    d.preact_gate = zg.data_ptr();
+    d.preact_up = zu.data_ptr();
+    d.rows = r.rows;
+    d.ldx = r.ld;
+    d.ldgate = ld_in_order(gate, d.weight_transposed);
+    d.ldup = ld_in_order(up, d.weight_transposed);
+    d.n = as_int(n, "gate");
+    d.k = as_int(r.width, "gate");
+    d.dweight_dtype = wt == type ? d.dtype : ANVIL_F32;
+    if (truth(a[14])) d.activation |= ANVIL_DZ_TWO_PARTS;
+    const Scratch scratch(ws ? 0 : api.gated_linear_backward_workspace_bytes(&d), ws, here);
+    check(api.gated_linear_backward(&d, scratch.p, scratch.bytes, here.stream), "anvil_gated_linear_backward");
+    return tuple_of(std::move(dx), std::move(dg), std::move(du));
+}
+
 // ---------------------------------------------------------------- token log probabilities
 const void* targets_of(const at::Tensor* t, int64_t rows, int* wide) {
     if (!t) return nullptr;
@@ -695,6 +822,8 @@ PyMethodDef methods[] = {
     ANVIL_ENTRY(token_logprobs_backward, 7),
     ANVIL_ENTRY(adamw_step, 14),
     ANVIL_ENTRY(adamw_values, 5),
+    ANVIL_ENTRY(gated_linear_forward, 7),
+    ANVIL_ENTRY(gated_linear_backward, 15),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_anvil_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
