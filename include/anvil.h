@@ -517,6 +517,59 @@ typedef struct {
 } anvil_logprob_grad_desc;
 anvil_status anvil_token_logprobs_backward(const anvil_logprob_grad_desc* desc, void* stream);
 
+/* Softmax cross entropy of a head, without its logits in memory:  z = x W^T,
+ *   lse = log sum_j e^z_j,  loss = lse - z_target.
+ * x [rows, k], W: [vocab, k], or its transpose [k, vocab] when weight_transposed != 0, both of type
+ * dtype (ANVIL_BF16 or ANVIL_F16); loss and lse [rows] fp32, or NULL.  targets [rows] int32 (int64 when
+ * targets_int64 != 0), or NULL with loss NULL.  A negative target marks a position that does not
+ * count: its loss is 0 (its lse is computed); one of vocab or more gives NaN.  A logit of -inf is a
+ * token that cannot be; a row of nothing else has lse -inf and loss inf.  A row with a NaN or +inf
+ * logit comes out NaN. */
+typedef struct {
+    const void* x;
+    const void* weight;
+    const void* targets;
+    float* loss;
+    float* lse;
+    int64_t rows;
+    int64_t ldx, ldw;
+    int vocab, k;
+    int dtype, targets_int64;
+    int weight_transposed;
+} anvil_head_desc;
+/* Scratch: 8 bytes per row and 64 columns of the vocabulary, 4 per row, and copies of operands off the
+ * 16-byte boundaries. */
+size_t anvil_linear_cross_entropy_workspace_bytes(const anvil_head_desc* desc);
+anvil_status anvil_linear_cross_entropy(const anvil_head_desc* desc, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient, for grad_loss = dL/dloss [rows] and the forward pass's lse [rows], both fp32:
+ *   d_j = grad_loss (e^(z_j - lse) - [j = target]),  dx = d W,  dweight = d^T x.
+ * The logits are computed again, a piece of the vocabulary at a time; d is rounded to dtype as the
+ * products' operand (in fp16 scaled by a power of two, so that small values are held), sums are fp32.  dx
+ * [rows, k] of type dtype; dweight in W's layout, of type dweight_dtype: dtype or ANVIL_F32.  Each may be
+ * NULL.  grad_loss is taken as 0 where the target is negative; a row whose lse is -inf has the gradient
+ * 0.  accumulate != 0: dweight is added to what it holds. */
+typedef struct {
+    const void* x;
+    const void* weight;
+    const void* targets;
+    const float* lse;
+    const float* grad_loss;
+    void* dx;
+    void* dweight;
+    int64_t rows;
+    int64_t ldx, ldw, lddx, lddw;
+    int vocab, k;
+    int dtype, targets_int64, dweight_dtype;
+    int weight_transposed;
+    int accumulate;
+} anvil_head_grad_desc;
+/* Scratch: d for a piece (256 MB, or 512 bytes a row where that is more), dx's fp32 sum where there are
+ * several pieces, copies as above, and parts of products split along the contraction. */
+size_t anvil_linear_cross_entropy_backward_workspace_bytes(const anvil_head_grad_desc* desc);
+anvil_status anvil_linear_cross_entropy_backward(const anvil_head_grad_desc* desc, void* workspace, size_t workspace_bytes,
+                                                 void* stream);
+
 /* Per-stage dumps of one bank step, for parity testing (not the hot path).
  * DEVICE pointers, each optional (NULL = skip), in the page's layout:
  *   X_raw [g, m, n] bf16            bf16 cast of the momentum lookahead
@@ -596,7 +649,10 @@ typedef enum {
     ANVIL_KERNEL_ADAMW = 21,             /* AdamW over many tensors, and the values of its states */
     ANVIL_KERNEL_GATED_PREPARE = 22,     /* the gated layer: dg and du */
     ANVIL_KERNEL_GATED_PRODUCT = 23,     /* both products, activation and product */
-    ANVIL_KERNEL_GATED_SUM = 24          /* sums of its split products */
+    ANVIL_KERNEL_GATED_SUM = 24,         /* sums of its split products */
+    ANVIL_KERNEL_HEAD_PREPARE = 25,      /* the head's cross entropy: the scale of fp16 gradients */
+    ANVIL_KERNEL_HEAD_PRODUCT = 26,      /* its logits, and what becomes of them */
+    ANVIL_KERNEL_HEAD_SUM = 27           /* rows' statistics joined; dx rounded */
 } anvil_kernel_kind;
 
 typedef struct { int kind; float ms; } anvil_profile_record;

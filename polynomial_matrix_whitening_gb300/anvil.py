@@ -44,7 +44,7 @@ KERNEL_KINDS = ("momentum", "norm_d", "normalize", "gram_norm", "gram", "sqpoly"
                 "xupdate_out", "tail_power", "tail_scale", "tail_apply", "adam", "cascade",
                 "norm_forward", "norm_backward", "norm_grads", "linear_prepare", "linear_product",
                 "linear_sum", "logprob", "logprob_backward", "adamw",
-                "gated_prepare", "gated_product", "gated_sum")
+                "gated_prepare", "gated_product", "gated_sum", "head_prepare", "head_product", "head_sum")
 MAX_MAPS, MAX_BANKS, MAX_TOP = 16, 8, 32
 
 
@@ -146,6 +146,19 @@ class LogprobGradDesc(ctypes.Structure):
                 ("vocab", _I), ("dtype", _I), ("targets_int64", _I)]
 
 
+class HeadDesc(ctypes.Structure):
+    _fields_ = [("x", _P), ("weight", _P), ("targets", _P), ("loss", _P), ("lse", _P), ("rows", _L),
+                ("ldx", _L), ("ldw", _L), ("vocab", _I), ("k", _I), ("dtype", _I), ("targets_int64", _I),
+                ("weight_transposed", _I)]
+
+
+class HeadGradDesc(ctypes.Structure):
+    _fields_ = [("x", _P), ("weight", _P), ("targets", _P), ("lse", _P), ("grad_loss", _P), ("dx", _P),
+                ("dweight", _P), ("rows", _L), ("ldx", _L), ("ldw", _L), ("lddx", _L), ("lddw", _L),
+                ("vocab", _I), ("k", _I), ("dtype", _I), ("targets_int64", _I), ("dweight_dtype", _I),
+                ("weight_transposed", _I), ("accumulate", _I)]
+
+
 class AdamwTensor(ctypes.Structure):
     _fields_ = [("param", _P), ("mantissa", _P), ("grad", _P), ("exp_avg", _P), ("exp_avg_sq", _P),
                 ("scales", _P), ("count", _L), ("param_dtype", _I), ("grad_dtype", _I)]
@@ -207,11 +220,18 @@ _lib.anvil_gated_linear_forward.argtypes = [ctypes.POINTER(GatedDesc), _vp, _sz,
 _lib.anvil_gated_linear_backward_workspace_bytes.argtypes = [ctypes.POINTER(GatedGradDesc)]
 _lib.anvil_gated_linear_backward_workspace_bytes.restype = _sz
 _lib.anvil_gated_linear_backward.argtypes = [ctypes.POINTER(GatedGradDesc), _vp, _sz, _vp]
+_lib.anvil_linear_cross_entropy_workspace_bytes.argtypes = [ctypes.POINTER(HeadDesc)]
+_lib.anvil_linear_cross_entropy_workspace_bytes.restype = _sz
+_lib.anvil_linear_cross_entropy.argtypes = [ctypes.POINTER(HeadDesc), _vp, _sz, _vp]
+_lib.anvil_linear_cross_entropy_backward_workspace_bytes.argtypes = [ctypes.POINTER(HeadGradDesc)]
+_lib.anvil_linear_cross_entropy_backward_workspace_bytes.restype = _sz
+_lib.anvil_linear_cross_entropy_backward.argtypes = [ctypes.POINTER(HeadGradDesc), _vp, _sz, _vp]
 _lib.anvil_token_logprobs.argtypes = [ctypes.POINTER(LogprobDesc), _vp]
 _lib.anvil_token_logprobs_backward.argtypes = [ctypes.POINTER(LogprobGradDesc), _vp]
 for _f_name in ("layernorm_forward", "layernorm_backward", "linear_forward", "linear_backward",
                 "token_logprobs", "token_logprobs_backward", "adamw_step", "adamw_scalars", "adamw_values",
-                "gated_linear_forward", "gated_linear_backward"):
+                "gated_linear_forward", "gated_linear_backward", "linear_cross_entropy",
+                "linear_cross_entropy_backward"):
     getattr(_lib, "anvil_" + _f_name).restype = _i
 _lib.anvil_device_error.argtypes = [_i]
 _lib.anvil_device_error.restype = _i
@@ -580,7 +600,8 @@ _ENTRY_POINTS = ("layernorm_forward", "layernorm_backward_workspace_bytes", "lay
                  "linear_workspace_bytes", "linear_forward", "linear_backward_workspace_bytes",
                  "linear_backward", "token_logprobs", "token_logprobs_backward", "adamw_step", "adamw_values",
                  "gated_linear_workspace_bytes", "gated_linear_forward", "gated_linear_backward_workspace_bytes",
-                 "gated_linear_backward")
+                 "gated_linear_backward", "linear_cross_entropy_workspace_bytes", "linear_cross_entropy",
+                 "linear_cross_entropy_backward_workspace_bytes", "linear_cross_entropy_backward")
 
 
 def _load_native():
@@ -751,6 +772,38 @@ def token_logprobs_backward(logits, targets, lse, grad_logprob=None, entropy=Non
                           (logits, targets, lse, grad_logprob, entropy, grad_entropy, out))
     return (_native or _load_native()).token_logprobs_backward(logits, targets, lse, grad_logprob, entropy,
                                                                grad_entropy, out)
+
+
+def linear_cross_entropy(x, weight, targets=None, workspace=None, stream=None):
+    """Softmax cross entropy of the logits x weight^T, bf16 or fp16, which never reach memory.
+
+    x [..., k], weight [vocab, k] (stored by rows or by columns), targets int64 or int32 of the
+    leading shape.  Returns (loss, lse), fp32 of the leading shape: loss = lse - logit[target], not
+    summed; 0 where the target is negative (a position that does not count), NaN from vocab on.
+    loss is None without targets.
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: linear_cross_entropy(x, weight, targets, workspace), (x, weight, targets, workspace))
+    return (_native or _load_native()).linear_cross_entropy(x, weight, targets, workspace)
+
+
+def linear_cross_entropy_backward(x, weight, targets, lse, grad_loss, need_dx=True, need_dweight=True, dweight_dtype=None,
+                                  dweight=None, accumulate=False, workspace=None, stream=None):
+    """Gradient of linear_cross_entropy's loss for grad_loss (fp32, one per row): returns (dx,
+    dweight), None where not asked for.
+
+    lse is the forward call's.  The logits are computed again, in pieces of the vocabulary.  dweight
+    has weight's shape and order and dweight_dtype: x's type (default) or fp32; it may be given
+    (with accumulate it is added to).  The logits' gradient is rounded to x's type before the
+    products (2^-8 of each value at most in bf16, 2^-11 in fp16).
+    """
+    if stream is not None:
+        return _on_stream(stream, lambda: linear_cross_entropy_backward(x, weight, targets, lse, grad_loss, need_dx, need_dweight,
+                                                                        dweight_dtype, dweight, accumulate, workspace),
+                          (x, weight, targets, lse, grad_loss, dweight, workspace))
+    return (_native or _load_native()).linear_cross_entropy_backward(x, weight, targets, lse, grad_loss, need_dx, need_dweight,
+                                                                     _fp32_dweight(dweight_dtype, x), dweight, accumulate,
+                                                                     workspace)
 
 
 def schedule_runs(shapes, nmaps=6):

@@ -104,7 +104,7 @@ anvil_status device_setup(DeviceState** out) {
                                  "cuTensorMapEncodeTiled lookup");
             g_encode = reinterpret_cast<EncodeTiledFn>(fn);
         }
-        if ((e = gemm_prepare()) || (e = linear_prepare()) || (e = multi_prepare()) || (e = gated_prepare())) return cuda_fail(e, "cudaFuncSetAttribute");
+        if ((e = gemm_prepare()) || (e = linear_prepare()) || (e = multi_prepare()) || (e = gated_prepare()) || (e = head_prepare())) return cuda_fail(e, "cudaFuncSetAttribute");
         if ((e = cudaDeviceGetAttribute(&st.sm_count, cudaDevAttrMultiProcessorCount, dev)))
             return cuda_fail(e, "cudaDeviceGetAttribute");
         st.err = device_error_word();

@@ -1,0 +1,282 @@
+// anvil_head.cu -- softmax cross entropy of a head z = x W^T over a large vocabulary, without the logits
+// in memory.
+//
+//   forward   lse = log sum_j e^z_j, loss = lse - z_t
+//   gradient  d_j = g (e^(z_j - lse) - [j = t]),  dx = d W,  dW = d^T x
+//
+// Forward: the pair kernel (anvil_linear.cuh), whose epilogue takes each tile's logits out of tensor
+// memory once and leaves, per row and 64 columns, their maximum and the sum of their exponentials
+// over it (8 bytes for 64 logits), and the target's logit where it is among them.  A second kernel joins a
+// row's pairs.  The products bound it (8192 x 50304 x 768: see anvil_head_api.cu for the figures); the
+// exponentials, 16 per SM and cycle, take a third of the time of a tile's products at k = 768.
+//
+// Gradient: the logits again, a piece of the vocabulary at a time.  The epilogue turns them into d, 16
+// bits, the operand of both products that follow: dW's rows of the piece are complete, dx is added up
+// in fp32 over the pieces.  So the workspace is bounded whatever the vocabulary, and the flops are the
+// three products' 6 rows vocab k.
+//
+// In powers of two: e^(z - m) = 2^(z log2(e) - M) with M = m log2(e) rounded, the same M in every
+// term, so that its rounding cancels in M + log2(S).
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "anvil_linear.cuh"
+
+namespace anvil {
+
+namespace {
+
+constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
+
+__device__ __forceinline__ long long target_of(const void* targets, int wide, long long row) {
+    return wide ? static_cast<const long long*>(targets)[row] : static_cast<const int*>(targets)[row];
+}
+// Column of the target relative to `first` as an int; -1 where it is before it or beyond any column.
+__device__ __forceinline__ int relative_target(const PairHeadParams& p, long long row) {
+    const long long t = target_of(p.targets, p.target64, row) - p.first;
+    return t >= 0 && t < p.cols ? static_cast<int>(t) : -1;
+}
+
+struct StatsPair {
+    using Params = PairHeadParams;
+    static constexpr bool MULTI = false, OWN = true, RANK_B = false;
+    struct Row {
+        long long row;
+        int target;
+    };
+    static __device__ __forceinline__ Row load(const Params& p, const Unit& t, int r) {
+        const long long row = static_cast<long long>(t.tr) * PAIR_ROWS + r;
+        return {row, row < p.rows && p.hit ? relative_target(p, row) : -1};
+    }
+    template <typename T, int W>
+    static __device__ __forceinline__ void tile(const Params& p, EpiState& x, uint32_t tacc, uint32_t tempty, const Unit& t,
+                                                int, const Row& row) {
+        static_assert(EPI_COLS == HEAD_STATS_COLS, "one pair of statistics per group and row");
+        const int col0 = t.tc * BN + x.grp * EPI_COLS;
+        const uint32_t ta = tacc + x.grp * EPI_COLS;
+        const int live = p.cols - col0;  // columns of this group that exist
+        float most = -INFINITY, ref = 0.f, sum = 0.f;
+#pragma unroll 1
+        for (int h = 0; h < EPI_COLS; h += 32) {
+            float v[32];
+            tmem_ld_32x32b_x32(ta + h, v);
+            if (live < h + 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (h + i >= live) v[i] = -INFINITY;
+            }
+            float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int i = 4; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], v[i]);
+            const float now = fmaxf(most, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+            const float base = now == -INFINITY ? 0.f : now * LOG2E;
+            float s[4] = {sum * power2(ref - base), 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i & 3] += power2(fmaf(v[i], LOG2E, -base));
+            sum = (s[0] + s[1]) + (s[2] + s[3]);
+            most = now;
+            ref = base;
+        }
+        const int at = row.target - col0;
+        const bool mine = row.target >= 0 && at >= 0 && at < EPI_COLS;
+        if (__any_sync(0xffffffffu, mine)) {  // one warp and tile in twenty at a vocabulary of 50,000
+            float hit = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < EPI_COLS; c += 16) {
+                float v[16];
+                tmem_ld_16(ta + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (at == c + i) hit = v[i];
+            }
+            if (mine) p.hit[row.row] = hit;
+        }
+        release_acc(x, tempty);
+        if (row.row < p.rows) p.stats[static_cast<long long>(t.tc * EPI_GROUPS + x.grp) * p.rows + row.row] = make_float2(ref, sum);
+    }
+};
+
+struct DlogitsPair {
+    using Params = PairHeadParams;
+    static constexpr bool MULTI = false, OWN = true, RANK_B = false;
+    struct Row {
+        float lse2, g;
+        int target;
+    };
+    static __device__ __forceinline__ Row load(const Params& p, const Unit& t, int r) {
+        const long long row = static_cast<long long>(t.tr) * PAIR_ROWS + r;
+        Row x = {0.f, 0.f, -1};
+        if (row < p.rows && target_of(p.targets, p.target64, row) >= 0) {
+            const float lse = p.lse[row];
+            if (lse != -INFINITY) {  // (no token of that row can be: its gradient is 0)
+                x.lse2 = lse * LOG2E;
+                x.g = p.scale ? p.grad[row] * *p.scale : p.grad[row];
+                x.target = relative_target(p, row);
+            }
+        }
+        return x;
+    }
+    template <typename T, int W>
+    static __device__ __forceinline__ void tile(const Params& p, EpiState& x, uint32_t tacc, uint32_t tempty, const Unit& t,
+                                                int row0, const Row& row) {
+        constexpr int COLS = W / 2, N = EPI_COLS / COLS;
+        const int col0 = t.tc * BN + x.grp * EPI_COLS;
+        const uint32_t ta = tacc + x.grp * EPI_COLS;
+        const int at = row.target - col0;
+#pragma unroll 1
+        for (int b = 0; b < N; ++b) {
+            box_free(x);
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += 16) {
+                float v[16];
+                tmem_ld_16(ta + b * COLS + c, v);
+                const int hot = at - (b * COLS + c);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[i] = power2(fmaf(v[i], LOG2E, -row.lse2));
+                    if (row.target >= 0 && hot == i) v[i] -= 1.f;
+                    v[i] = row.g == 0.f ? 0.f : v[i] * row.g;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) sts128(Staging<W>::addr(x.box, x.r, c / 8 + j), Elem<T>::pack(v + 8 * j));
+            }
+            if (b == N - 1) release_acc(x, tempty);
+            // (the buffer's rows go on in eights: no box ends inside 16 bytes)
+            send_box<uint16_t, W, true>(x, &p.tm_out, 1, p.epi.out, p.epi.ldout, row0, col0 + b * COLS, p.rows, (p.cols + 7) & ~7);
+        }
+    }
+};
+
+// A row's statistics joined, in order within each of eight shares and then over them: 32 rows a block,
+// a warp per share.
+constexpr int HJ_ROWS = 32, HJ_SHARES = 8;
+__global__ void __launch_bounds__(HJ_ROWS* HJ_SHARES) head_join_kernel(const HeadJoinParams p) {
+    __shared__ float2 share[HJ_SHARES][HJ_ROWS];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const long long row = static_cast<long long>(blockIdx.x) * HJ_ROWS + x;
+    pdl_allow_next();
+    pdl_wait_previous();
+    // (a part with a sum of 0 has no logit above -inf; a NaN goes through the sums)
+    float ref = -INFINITY, sum = 0.f;
+    if (row < p.rows) {
+#pragma unroll 8
+        for (int i = y; i < p.parts; i += HJ_SHARES) {
+            const float2 s = __ldcs(&p.stats[static_cast<long long>(i) * p.rows + row]);
+            if (s.y != 0.f) {
+                const float now = fmaxf(ref, s.x);
+                sum = sum * power2(ref - now) + s.y * power2(s.x - now);
+                ref = now;
+            }
+        }
+    }
+    share[y][x] = make_float2(ref, sum);
+    __syncthreads();
+    if (y != 0 || row >= p.rows) return;
+    for (int k = 1; k < HJ_SHARES; ++k) {
+        const float2 s = share[k][x];
+        if (s.y != 0.f) {
+            const float now = fmaxf(ref, s.x);
+            sum = sum * power2(ref - now) + s.y * power2(s.x - now);
+            ref = now;
+        }
+    }
+    const float lse = sum == 0.f ? -INFINITY : fmaf(ref, LN2, logf(sum));
+    if (p.lse) p.lse[row] = lse;
+    if (p.loss) {
+        const long long t = target_of(p.targets, p.target64, row);
+        p.loss[row] = t < 0 ? 0.f : t >= p.vocab ? NAN : lse == -INFINITY ? INFINITY : lse - p.hit[row];
+    }
+}
+
+// fp16 holds nothing below 2^-25, where most of d lies for a mean over thousands of rows: there d is
+// taken times a power of two, which the products' results are divided by (both exact).
+__global__ void __launch_bounds__(1024) head_scale_kernel(const HeadScaleParams p) {
+    __shared__ uint32_t warps[32];
+    pdl_allow_next();
+    pdl_wait_previous();
+    uint32_t most = 0;
+    for (long long i = threadIdx.x; i < p.rows; i += 1024)
+        if (target_of(p.targets, p.target64, i) >= 0) most = max(most, __float_as_uint(p.grad[i]) & 0x7fffffffu);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = most;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    most = __reduce_max_sync(0xffffffffu, warps[threadIdx.x]);
+    if (threadIdx.x == 0) {
+        int e = 0;  // 0, an infinity or a NaN: as they are
+        if (most != 0 && most < 0x7f800000u) e = min(max(13 - (static_cast<int>(most >> 23) - 127), -120), 120);
+        p.scale[0] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        p.scale[1] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) head_round_kernel(const HeadRoundParams p) {
+    pdl_allow_next();
+    pdl_wait_previous();
+    const float scale = p.scale ? *p.scale : 1.f;
+    const int chunks = (p.cols + 7) / 8;
+    const long long total = chunks * p.rows, ld = chunks * 8ll;  // (src's rows go on in eights)
+    const bool vec = p.cols % 8 == 0 && p.ldd % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.dst) & 15);
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long row = i / chunks;
+        const int c = static_cast<int>(i - row * chunks) * 8;
+        float v[8];
+        Elem<float>::unpack(ldg_stream(p.src + row * ld + c), v);
+        Elem<float>::unpack(ldg_stream(p.src + row * ld + c + 4), v + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= scale;
+        T* to = static_cast<T*>(p.dst) + row * p.ldd + c;
+        if (vec) {
+            *reinterpret_cast<uint4*>(to) = Elem<T>::pack(v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < p.cols) to[e] = Elem<T>::store(v[e]);
+        }
+    }
+}
+
+constexpr int HEAD_BOX = 64;  // six stages: the products bound both kernels
+
+}  // namespace
+
+cudaError_t head_prepare() {
+    cudaError_t e;
+#define ANVIL_SMEM(T, M)                                                                                                    \
+    if ((e = cudaFuncSetAttribute(pair_gemm_kernel<T, HEAD_BOX, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,            \
+                                  Staging<HEAD_BOX>::SMEM)))                                                                \
+    return e
+    ANVIL_SMEM(__nv_bfloat16, StatsPair);
+    ANVIL_SMEM(__half, StatsPair);
+    ANVIL_SMEM(__nv_bfloat16, DlogitsPair);
+    ANVIL_SMEM(__half, DlogitsPair);
+#undef ANVIL_SMEM
+    return cudaSuccess;
+}
+
+cudaError_t launch_head_stats(const PairHeadParams& p, int sm_count, cudaStream_t s) {
+    return p.f16 ? run_pair<__half, HEAD_BOX, StatsPair>(p, sm_count, s) : run_pair<__nv_bfloat16, HEAD_BOX, StatsPair>(p, sm_count, s);
+}
+
+cudaError_t launch_head_dlogits(const PairHeadParams& p, int sm_count, cudaStream_t s) {
+    return p.f16 ? run_pair<__half, HEAD_BOX, DlogitsPair>(p, sm_count, s)
+                 : run_pair<__nv_bfloat16, HEAD_BOX, DlogitsPair>(p, sm_count, s);
+}
+
+cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t s) {
+    return launch_pdl(head_join_kernel, dim3(static_cast<unsigned>((p.rows + HJ_ROWS - 1) / HJ_ROWS)), dim3(HJ_ROWS * HJ_SHARES), 0, s, p);
+}
+
+cudaError_t launch_head_scale(const HeadScaleParams& p, cudaStream_t s) {
+    return launch_pdl(head_scale_kernel, dim3(1), dim3(1024), 0, s, p);
+}
+
+cudaError_t launch_head_round(const HeadRoundParams& p, cudaStream_t s) {
+    const long long items = (p.cols + 7) / 8 * p.rows, blocks = (items + 255) / 256;
+    const dim3 grid(static_cast<unsigned>(blocks < 152 * 16 ? blocks : 152 * 16));
+    return p.f16 ? launch_pdl(head_round_kernel<__half>, grid, dim3(256), 0, s, p)
+                 : launch_pdl(head_round_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p);
+}
+
+}  // namespace anvil

@@ -162,6 +162,51 @@ struct GatedGradParams {
     int cols, act, f16;
 };
 cudaError_t launch_gated_grad(const GatedGradParams& p, cudaStream_t stream);
+// The head: z = x W^T by tiles that are used and dropped (p.cols columns from column `first` of the vocabulary).
+// Statistics: of each row's 64 columns (M, S) with S = sum_j 2^(z_j log2(e) - M), and the target's z.
+// Gradient: out = g (e^(z - lse) - [j = target]) (times *scale), 16 bit.
+struct PairHeadParams : PairGemmParams {
+    const void* targets;
+    int target64;
+    int first;
+    float2* stats;        // [4 tiles_c][rows]
+    float* hit;           // [rows]
+    const float* lse;     // [rows]
+    const float* grad;    // [rows]
+    const float* scale;   // or null
+};
+constexpr int HEAD_STATS_COLS = 64;  // columns behind one pair of statistics
+struct HeadJoinParams {
+    const float2* stats;
+    const float* hit;
+    const void* targets;
+    float* loss;          // or null
+    float* lse;           // or null
+    long long rows;
+    int parts, vocab, target64;
+};
+// scale[0] = a power of two that brings the largest |grad| (of rows that count) to 2^13 or above it, scale[1] = 1 / scale[0]
+struct HeadScaleParams {
+    const float* grad;
+    const void* targets;
+    float* scale;
+    long long rows;
+    int target64;
+};
+// dst [rows, cols] 16 bit = src fp32 [rows, cols] (times *scale)
+struct HeadRoundParams {
+    const float* src;
+    void* dst;
+    const float* scale;   // or null
+    long long rows, ldd;
+    int cols, f16;
+};
+cudaError_t head_prepare();
+cudaError_t launch_head_stats(const PairHeadParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t stream);
+cudaError_t launch_head_dlogits(const PairHeadParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_head_scale(const HeadScaleParams& p, cudaStream_t stream);
+cudaError_t launch_head_round(const HeadRoundParams& p, cudaStream_t stream);
 cudaError_t multi_prepare();
 cudaError_t launch_pair_multi(const PairMultiParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream);

@@ -40,6 +40,10 @@ struct Api {
     anvil_status (*gated_linear_forward)(const anvil_gated_desc*, void*, size_t, void*);
     size_t (*gated_linear_backward_workspace_bytes)(const anvil_gated_grad_desc*);
     anvil_status (*gated_linear_backward)(const anvil_gated_grad_desc*, void*, size_t, void*);
+    size_t (*linear_cross_entropy_workspace_bytes)(const anvil_head_desc*);
+    anvil_status (*linear_cross_entropy)(const anvil_head_desc*, void*, size_t, void*);
+    size_t (*linear_cross_entropy_backward_workspace_bytes)(const anvil_head_grad_desc*);
+    anvil_status (*linear_cross_entropy_backward)(const anvil_head_grad_desc*, void*, size_t, void*);
 };
 Api api;
 PyObject* g_check = nullptr;          // Python: raises AnvilError(status, where)
@@ -327,6 +331,23 @@ Weight weight_of(const at::Tensor& w, at::ScalarType type, const char* what) {
     refuse("%s must be stored by rows or by columns; use .contiguous()", what);
 }
 
+// The weight's gradient: the caller's, in weight's order (m changes to the other one where both are
+// stored so too: single rows), or a new one.
+at::Tensor dweight_like(const at::Tensor& w, Weight* m, const at::Tensor* given, at::ScalarType type, const Here& here, int64_t* ld) {
+    if (!given) {
+        *ld = m->transposed ? m->n : m->k;
+        return m->transposed ? here.empty({m->k, m->n}, type).t() : here.empty({m->n, m->k}, type);
+    }
+    const Weight g = weight_of(*given, type, "dweight");
+    if (ld_in_order(*given, m->transposed) < 0 && ld_in_order(w, !m->transposed) >= 0) {
+        m->transposed = !m->transposed;
+        m->ld = ld_in_order(w, m->transposed);
+    }
+    *ld = ld_in_order(*given, m->transposed);
+    if (g.n != m->n || g.k != m->k || *ld < 0) refuse("dweight must have weight's shape and order");
+    return *given;
+}
+
 // (x, weight, bias, activation, residual, save_preact, out, workspace) -> (y, z or None)
 PyObject* linear_forward(PyObject* const* a) {
     const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight");
@@ -412,20 +433,7 @@ PyObject* linear_backward(PyObject* const* a) {
         d.lddx = m.k;
     }
     if (need_dw) {
-        if (dw_in) {
-            const Weight g = weight_of(*dw_in, wt, "dweight");
-            // both in weight's order, or in the other one where both are stored so too (single rows)
-            if (ld_in_order(*dw_in, m.transposed) < 0 && ld_in_order(w, !m.transposed) >= 0) {
-                m.transposed = !m.transposed;
-                m.ld = ld_in_order(w, m.transposed);
-            }
-            d.lddw = ld_in_order(*dw_in, m.transposed);
-            if (g.n != m.n || g.k != m.k || d.lddw < 0) refuse("dweight must have weight's shape and order");
-            dw = *dw_in;
-        } else {
-            dw = m.transposed ? here.empty({m.k, m.n}, wt).t() : here.empty({m.n, m.k}, wt);
-            d.lddw = m.transposed ? m.n : m.k;
-        }
+        dw = dweight_like(w, &m, dw_in, wt, here, &d.lddw);
         d.dweight = dw.data_ptr();
     }
     if (need_db) {
@@ -647,6 +655,91 @@ PyObject* token_logprobs_backward(PyObject* const* a) {
     return wrap(std::move(dl));
 }
 
+// ---------------------------------------------------------------- the head's cross entropy
+// (x, weight, targets, workspace) -> (loss or None, lse)
+PyObject* linear_cross_entropy(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight");
+    const at::Tensor *t = maybe(a[2], "targets"), *ws = maybe(a[3], "workspace");
+    anvil_head_desc d = {};
+    d.dtype = dtype_code(x, "x");
+    if (d.dtype == ANVIL_F32) refuse("x must be bf16 or fp16");
+    const Rows r = rows_of(x, "x");
+    const Weight m = weight_of(w, x.scalar_type(), "weight");
+    if (m.k != r.width) refuse("weight must be [vocab, %lld]", static_cast<long long>(r.width));
+    d.targets = targets_of(t, r.rows, &d.targets_int64);
+    const Here here("linear_cross_entropy", {&x, &w, t, ws});
+    const auto lead = x.sizes().slice(0, x.dim() - 1);
+    Together results((t ? 2 : 1) * r.rows, here);
+    at::Tensor lse = results.next(lead, at::kFloat, r.rows), loss;
+    if (t) {
+        loss = results.next(lead, at::kFloat, r.rows);
+        d.loss = static_cast<float*>(loss.data_ptr());
+    }
+    d.x = x.data_ptr();
+    d.weight = w.data_ptr();
+    d.lse = static_cast<float*>(lse.data_ptr());
+    d.rows = r.rows;
+    d.ldx = r.ld;
+    d.ldw = m.ld;
+    d.vocab = as_int(m.n, "weight");
+    d.k = as_int(m.k, "weight");
+    d.weight_transposed = m.transposed;
+    const Scratch scratch(ws ? 0 : api.linear_cross_entropy_workspace_bytes(&d), ws, here);
+    check(api.linear_cross_entropy(&d, scratch.p, scratch.bytes, here.stream), "anvil_linear_cross_entropy");
+    return tuple_of(std::move(loss), std::move(lse));
+}
+
+// (x, weight, targets, lse, grad_loss, need_dx, need_dweight, dweight fp32 (None: x's type), dweight, accumulate, workspace)
+// -> (dx, dweight)
+PyObject* linear_cross_entropy_backward(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight"), &t = tensor(a[2], "targets"), &lse = tensor(a[3], "lse"),
+                     &gl = tensor(a[4], "grad_loss");
+    const at::Tensor *dw_in = maybe(a[8], "dweight"), *ws = maybe(a[10], "workspace");
+    const bool need_dx = truth(a[5]), need_dw = truth(a[6]);
+    anvil_head_grad_desc d = {};
+    d.dtype = dtype_code(x, "x");
+    if (d.dtype == ANVIL_F32) refuse("x must be bf16 or fp16");
+    const at::ScalarType type = x.scalar_type();
+    const Rows r = rows_of(x, "x");
+    Weight m = weight_of(w, type, "weight");
+    if (m.k != r.width) refuse("weight must be [vocab, %lld]", static_cast<long long>(r.width));
+    d.targets = targets_of(&t, r.rows, &d.targets_int64);
+    d.lse = per_row(&lse, r.rows, "lse");
+    d.grad_loss = per_row(&gl, r.rows, "grad_loss");
+    d.accumulate = truth(a[9]);
+    if (d.accumulate && need_dw && !dw_in) refuse("accumulate needs dweight to add to");
+    at::ScalarType wt = type;
+    if (dw_in) {
+        wt = dw_in->scalar_type();
+        if (wt != type && wt != at::kFloat) refuse("dweight must be fp32 or of x's type");
+    } else if (truth(a[7])) {
+        wt = at::kFloat;
+    }
+    const Here here("linear_cross_entropy_backward", {&x, &w, &t, &lse, &gl, dw_in, ws});
+    at::Tensor dx, dw;
+    if (need_dx) {
+        dx = here.empty(x.sizes(), type);
+        d.dx = dx.data_ptr();
+        d.lddx = m.k;
+    }
+    if (need_dw) {
+        dw = dweight_like(w, &m, dw_in, wt, here, &d.lddw);
+        d.dweight = dw.data_ptr();
+    }
+    d.x = x.data_ptr();
+    d.weight = w.data_ptr();
+    d.rows = r.rows;
+    d.ldx = r.ld;
+    d.ldw = m.ld;
+    d.vocab = as_int(m.n, "weight");
+    d.k = as_int(m.k, "weight");
+    d.weight_transposed = m.transposed;
+    d.dweight_dtype = wt == type ? d.dtype : ANVIL_F32;
+    const Scratch scratch(ws ? 0 : api.linear_cross_entropy_backward_workspace_bytes(&d), ws, here);
+    check(api.linear_cross_entropy_backward(&d, scratch.p, scratch.bytes, here.stream), "anvil_linear_cross_entropy_backward");
+    return tuple_of(std::move(dx), std::move(dw));
+}
+
 // ---------------------------------------------------------------- AdamW
 // A list or tuple of tensors (of `n`, or any number where n < 0); items may be None where `gaps`.
 struct Tensors {
@@ -824,6 +917,8 @@ PyMethodDef methods[] = {
     ANVIL_ENTRY(adamw_values, 5),
     ANVIL_ENTRY(gated_linear_forward, 7),
     ANVIL_ENTRY(gated_linear_backward, 15),
+    ANVIL_ENTRY(linear_cross_entropy, 4),
+    ANVIL_ENTRY(linear_cross_entropy_backward, 11),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_anvil_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
