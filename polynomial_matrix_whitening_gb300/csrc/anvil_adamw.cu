@@ -23,46 +23,65 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "anvil_adamw.h"
 #include "anvil_device.cuh"
+#include "anvil_round.cuh"
 #include "anvil_types.cuh"
 
 namespace anvil {
 
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32, TURNS = ADAMW_CHUNK / (WARPS * ADAMW_BLOCK);
+constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr float TOP_M = 448.f, TOP_R = 507904.f;  // 31 2^14
 constexpr float SMALLEST = 7.8886090522101181e-31f;  // 2^-100
 
-// Eight values of a lane from an array of 4-, 2- or 1-byte elements, as their bits: four neighbours
-// at a time, or one (what is at `left` and beyond reads as 0).
-template <typename E>
-__device__ __forceinline__ void load8(const E* p, bool vec, int lane, int left, E (&v)[8]) {
-    if (vec) {
+// Eight values of a lane from an array of 4-, 2- or 1-byte elements, as they were loaded: nothing
+// uses them before they are needed, so a block's loads are on their way while the one before it is
+// computed.  VEC: every whole block is on vector boundaries, four neighbours at a time.  Otherwise,
+// and in a tensor's last block, one by one (what is at `left` and beyond reads as 0).
+template <typename E, bool VEC>
+struct Eight {
+    static constexpr int W = VEC ? 2 * sizeof(E) : 8;  // words
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const E* p, int lane, int left) {
+        if (VEC && left == ADAMW_BLOCK) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const E* q = p + h * 128 + lane * 4;
-            if constexpr (sizeof(E) == 4) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(q));
-                v[4 * h] = w.x, v[4 * h + 1] = w.y, v[4 * h + 2] = w.z, v[4 * h + 3] = w.w;
-            } else if constexpr (sizeof(E) == 2) {
-                const uint2 w = __ldcs(reinterpret_cast<const uint2*>(q));
-                v[4 * h] = w.x & 0xffffu, v[4 * h + 1] = w.x >> 16, v[4 * h + 2] = w.y & 0xffffu, v[4 * h + 3] = w.y >> 16;
-            } else {
-                const uint32_t w = __ldcs(reinterpret_cast<const uint32_t*>(q));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[4 * h + i] = (w >> 8 * i) & 0xffu;
+            for (int h = 0; h < 2; ++h) {
+                const E* q = p + h * 128 + lane * 4;
+                if constexpr (sizeof(E) == 4) {
+                    const uint4 x = __ldcs(reinterpret_cast<const uint4*>(q));
+                    w[4 * h] = x.x, w[4 * h + 1] = x.y, w[4 * h + 2] = x.z, w[4 * h + 3] = x.w;
+                } else if constexpr (sizeof(E) == 2) {
+                    const uint2 x = __ldcs(reinterpret_cast<const uint2*>(q));
+                    w[2 * h] = x.x, w[2 * h + 1] = x.y;
+                } else {
+                    w[h] = __ldcs(reinterpret_cast<const uint32_t*>(q));
+                }
             }
+            return;
         }
-    } else {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i * 32 + lane < left ? __ldcs(p + i * 32 + lane) : E(0);
+            for (int k = 0; k < W; ++k) w[k] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t x = i * 32 + lane < left ? static_cast<uint32_t>(__ldcs(p + i * 32 + lane)) : 0u;
+            if constexpr (VEC) w[i * sizeof(E) / 4] |= x << (i * sizeof(E) % 4 * 8);
+            else w[i] = x;
+        }
     }
-}
-template <typename E>
-__device__ __forceinline__ void store8(E* p, bool vec, int lane, int left, const E (&v)[8]) {
-    if (vec) {
+    __device__ __forceinline__ E operator[](int i) const {
+        if constexpr (VEC) return static_cast<E>(w[i * sizeof(E) / 4] >> (i * sizeof(E) % 4 * 8));
+        else return static_cast<E>(w[i]);
+    }
+};
+template <bool VEC, typename E>
+__device__ __forceinline__ void store8(E* p, int lane, int left, const E (&v)[8]) {
+    if (VEC && left == ADAMW_BLOCK) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             E* q = p + h * 128 + lane * 4;
@@ -106,7 +125,8 @@ struct Word<DT_F16> {
     static __device__ __forceinline__ uint16_t word(float v) { return __half_as_ushort(__float2half_rn(v)); }
 };
 
-__device__ __forceinline__ void e4m3_values(const uint8_t (&c)[8], float (&v)[8]) {
+template <bool VEC>
+__device__ __forceinline__ void e4m3_values(const Eight<uint8_t, VEC>& c, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         const uint16_t two = static_cast<uint16_t>(c[i] | c[i + 1] << 8);
@@ -126,28 +146,46 @@ __device__ __forceinline__ void e4m3_codes(const float (&v)[8], uint8_t (&c)[8])
         c[i + 1] = two >> 8;
     }
 }
-// From 16 on the code's bits are the value's own: the exponent (less 130) and four fraction bits.
-__device__ __forceinline__ float root_value(uint8_t c) {
-    return c < 16 ? static_cast<float>(c) : __uint_as_float((static_cast<uint32_t>(c) << 19) + (130u << 23));
+// A root's code is an fp16 number's exponent (its lower four bits) and first four fraction bits, 0 to 15
+// its subnormal ones: shifted there it is the value over 2^18.
+template <bool VEC>
+__device__ __forceinline__ void root_values(const Eight<uint8_t, VEC>& c, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        uint32_t h;
+        if constexpr (VEC) h = __byte_perm(c.w[i / 4], 0, i % 4 ? 0x4342 : 0x4140) << 6;
+        else h = (c.w[i] | c.w[i + 1] << 16) << 6;
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[i] = f.x;
+        v[i + 1] = f.y;
+    }
 }
-__device__ __forceinline__ uint8_t root_code(float q) {
-    const uint32_t b = __float_as_uint(q);
-    const int large = static_cast<int>((b + 0x3ffffu + (b >> 19 & 1u)) >> 19) - (131 << 4) + 16;
-    const int c = q < 16.f ? __float2int_rn(q) : large;
-    return static_cast<uint8_t>(q > 0.f ? min(max(c, 1), 255) : 0);
+constexpr float ROOT_UNIT = 262144.f;  // 2^18
+// The nearest code of q (507904 at most, but for its rounding), ties to the even one: adding 2^19 times
+// the power of two below q (16 at least) leaves q's first five bits, rounded, at the end of the sum.  A q
+// above 0 has a code of 1 at least; NaN gives 0.  Only the low byte counts.
+__device__ __forceinline__ uint32_t root_code(float q) {
+    const uint32_t power = max(__float_as_uint(q) & 0x7f800000u, 131u << 23);
+    const uint32_t sum = __float_as_uint(__fadd_rn(q, __uint_as_float(power + (19u << 23))));
+    const uint32_t c = ((power >> 19) + sum - (131u << 4)) & 0xffu;
+    return q > 0.f ? max(c, 1u) : 0u;
 }
 
-// A block's scale, and what its values are multiplied by for their codes.
-struct Scale {
-    float scale, inverse;
-};
-__device__ __forceinline__ Scale block_scale(const float (&v)[8], float top) {
+// The largest of a warp's values (magnitudes: bits without the sign), as bits, which puts an infinity
+// above every number and a NaN above that.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t most_bits(const float (&v)[8]) {
     uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
-    float f = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
-    if (f < SMALLEST) f = 0.f;
-    return {__fmul_rn(f, 1.f / top), f > 0.f ? __fdiv_rn(top, f) : 0.f};
+    for (int i = 0; i < 8; ++i) most = max(most, SIGNED ? __float_as_uint(v[i]) & 0x7fffffffu : __float_as_uint(v[i]));
+    return most;
+}
+
+// The eight values times one factor, in pairs.
+__device__ __forceinline__ void times8(float (&v)[8], float f) {
+    const uint64_t ff = f2_make(f, f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) f2_split(f2_mul(f2_make(v[i], v[i + 1]), ff), &v[i], &v[i + 1]);
 }
 
 // The tensor whose chunks hold `chunk`.
@@ -162,15 +200,53 @@ __device__ __forceinline__ int tensor_of(const AdamwParams<N>& a, int chunk) {
     return lo;
 }
 
-template <int PARAM, int GRAD, bool CODES, int N>
-__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ AdamwParams<N> a) {
-    constexpr bool SPLIT = PARAM == ADAMW_SPLIT;
+// What a block's step reads.
+template <int PARAM, int GRAD, bool CODES, bool VEC>
+struct Inputs {
+    static constexpr bool SPLIT = PARAM == ADAMW_SPLIT;
     using P = Word<SPLIT ? DT_BF16 : PARAM>;
     using G = Word<GRAD>;
+    using S = std::conditional_t<CODES, uint8_t, uint32_t>;
+    Eight<typename P::type, VEC> p;
+    Eight<uint16_t, VEC> low;
+    Eight<typename G::type, VEC> g;
+    Eight<S, VEC> m, v;
+    float ms, rs;
+    // gradient and moments, and the parameter: apart, since they are used at different times
+    __device__ __forceinline__ void load_moments(const AdamwTensor& t, long long block, long long blocks, int lane) {
+        const long long at = block * ADAMW_BLOCK;
+        const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
+        g.load(static_cast<const typename G::type*>(t.g) + at, lane, left);
+        m.load(static_cast<const S*>(t.m) + at, lane, left);
+        v.load(static_cast<const S*>(t.v) + at, lane, left);
+        if constexpr (CODES) {
+            ms = t.scales[block];
+            rs = t.scales[blocks + block];
+        }
+    }
+    __device__ __forceinline__ void load_param(const AdamwTensor& t, long long block, int lane) {
+        const long long at = block * ADAMW_BLOCK;
+        const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
+        p.load(static_cast<const typename P::type*>(t.p) + at, lane, left);
+        if constexpr (SPLIT) low.load(t.low + at, lane, left);
+    }
+};
+
+// With fp32 states the kernel waits for memory (50M split bf16 values 190 us, 6.8 TB/s).  With codes it is
+// short of instructions (98 a value, at 80% of the issue slots, in its first form; 78 in this one): quotients
+// and roots there are pairs without the general ones' branches (where a lane's values are in the
+// middle of the range), and of the two scales each half of the warp divides for one.  134M fp32 values: 543 us
+// with the general operations, 400 now, 5.4 TB/s.
+template <int PARAM, int GRAD, bool CODES, bool VEC, int N>
+__global__ void __launch_bounds__(THREADS, CODES && VEC ? 4 : 3) adamw_kernel(const __grid_constant__ AdamwParams<N> a) {
+    using In = Inputs<PARAM, GRAD, CODES, VEC>;
+    using P = typename In::P;
+    using G = typename In::G;
+    constexpr bool SPLIT = In::SPLIT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const AdamwTensor& t = a.t[tensor_of(a, blockIdx.x)];
     const long long blocks = (t.count + ADAMW_BLOCK - 1) / ADAMW_BLOCK;
-    const long long first = static_cast<long long>(blockIdx.x - t.chunk0) * (ADAMW_CHUNK / ADAMW_BLOCK);
+    const long long first = static_cast<long long>(blockIdx.x - t.chunk0) * a.chunk, end = min(blocks, first + a.chunk);
     pdl_allow_next();
     pdl_wait_previous();
     float step_size = a.scalars[0], root = a.scalars[1], decay = a.scalars[2], grad_scale = a.scalars[3];
@@ -180,52 +256,76 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
         decay = a.d_scalars[2];
         grad_scale = a.d_scalars[3];
     }
+    // denominators from 2^-60 (eps) to 2^63 2^20 + eps
+    const bool middle = a.eps >= 8.67361738e-19f && a.eps <= 1.f && root >= 0.f && root <= 1048576.f;
+    In in;  // of this block, and as soon as they are used, of the warp's next
+    long long b = first + warp;
+    if (b < end) {
+        in.load_moments(t, b, blocks, lane);
+        in.load_param(t, b, lane);
+    }
 #pragma unroll 1
-    for (int turn = 0; turn < TURNS; ++turn) {
-        const long long b = first + turn * WARPS + warp;
-        if (b >= blocks) break;
+    for (; b < end; b += WARPS) {
         const long long at = b * ADAMW_BLOCK;
         const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
-        const bool vec = t.vec && left == ADAMW_BLOCK;
-        typename P::type pw[8];
-        typename G::type gw[8];
-        uint16_t low[8];
-        load8(static_cast<const typename P::type*>(t.p) + at, vec, lane, left, pw);
-        if constexpr (SPLIT) load8(static_cast<const uint16_t*>(t.low) + at, vec, lane, left, low);
-        load8(static_cast<const typename G::type*>(t.g) + at, vec, lane, left, gw);
-        float m[8], v[8], r[8];
+        float m[8], v[8], r[8], u[8];
         if constexpr (CODES) {
-            uint8_t mc[8], vc[8];
-            load8(static_cast<const uint8_t*>(t.m) + at, vec, lane, left, mc);
-            load8(static_cast<const uint8_t*>(t.v) + at, vec, lane, left, vc);
-            const float ms = t.scales[b], rs = t.scales[blocks + b];
-            e4m3_values(mc, m);
+            e4m3_values(in.m, m);
+            times8(m, in.ms);
+            root_values(in.v, v);
+            times8(v, __fmul_rn(in.rs, ROOT_UNIT));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m[i] = __fmul_rn(m[i], ms);
-                const float root0 = __fmul_rn(root_value(vc[i]), rs);
-                v[i] = __fmul_rn(root0, root0);
+            for (int i = 0; i < 8; i += 2) {
+                const uint64_t x = f2_make(v[i], v[i + 1]);
+                f2_split(f2_mul(x, x), &v[i], &v[i + 1]);
             }
         } else {
-            uint32_t w[8];
-            load8(static_cast<const uint32_t*>(t.m) + at, vec, lane, left, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = __uint_as_float(w[i]);
-            load8(static_cast<const uint32_t*>(t.v) + at, vec, lane, left, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+            for (int i = 0; i < 8; ++i) {
+                m[i] = __uint_as_float(in.m[i]);
+                v[i] = __uint_as_float(in.v[i]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float g = __fmul_rn(G::value(gw[i]), grad_scale);
+            const float g = __fmul_rn(G::value(in.g[i]), grad_scale);
             m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(g, a.c1));
             v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(g, a.c2), g));
-            r[i] = __fsqrt_rn(v[i]);
-            const float u = __fmul_rn(__fdiv_rn(m[i], __fadd_rn(__fmul_rn(r[i], root), a.eps)), step_size);
+        }
+        if (b + WARPS < end) in.load_moments(t, b + WARPS, blocks, lane);
+        if (CODES && left < ADAMW_BLOCK) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i * 32 + lane >= left) m[i] = v[i] = 0.f;  // behind the tensor's end
+        }
+        uint32_t most_m = 0, most_v = 0;
+        if constexpr (CODES) {
+            most_m = most_bits<true>(m);
+            most_v = most_bits<false>(v);
+        }
+        // |m| below 2^100 and v below 2^126, no infinity or NaN among them
+        if (CODES && middle && most_m < (227u << 23) && most_v < (253u << 23)) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                f2_split(f2_root(f2_make(v[i], v[i + 1])), &r[i], &r[i + 1]);
+                const uint64_t d = f2_make(__fadd_rn(__fmul_rn(r[i], root), a.eps), __fadd_rn(__fmul_rn(r[i + 1], root), a.eps));
+                f2_split(f2_divide(f2_make(m[i], m[i + 1]), d), &u[i], &u[i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                r[i] = __fsqrt_rn(v[i]);
+                u[i] = __fdiv_rn(m[i], __fadd_rn(__fmul_rn(r[i], root), a.eps));
+            }
+        }
+        typename P::type pw[8];
+        uint16_t low[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
             float p;
-            if constexpr (SPLIT) p = __uint_as_float(static_cast<uint32_t>(pw[i]) << 16 | low[i]);
-            else p = P::value(pw[i]);
-            p = __fsub_rn(__fmul_rn(p, decay), u);
+            if constexpr (SPLIT) p = __uint_as_float(static_cast<uint32_t>(in.p[i]) << 16 | in.low[i]);
+            else p = P::value(in.p[i]);
+            p = __fsub_rn(__fmul_rn(p, decay), __fmul_rn(u[i], step_size));
             if constexpr (SPLIT) {
                 const uint32_t bits = __float_as_uint(p);
                 pw[i] = bits >> 16;
@@ -234,70 +334,81 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
                 pw[i] = P::word(p);
             }
         }
-        store8(static_cast<typename P::type*>(t.p) + at, vec, lane, left, pw);
-        if constexpr (SPLIT) store8(t.low + at, vec, lane, left, low);
+        if (b + WARPS < end) in.load_param(t, b + WARPS, lane);
+        store8<VEC>(static_cast<typename P::type*>(t.p) + at, lane, left, pw);
+        if constexpr (SPLIT) store8<VEC>(t.low + at, lane, left, low);
         if constexpr (CODES) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!vec && i * 32 + lane >= left) m[i] = r[i] = 0.f;  // behind the tensor's end
-            const Scale sm = block_scale(m, TOP_M), sr = block_scale(r, TOP_R);
+            // each half of the warp finds one moment's scale (the largest root is the largest v's), and
+            // what its values are multiplied by for their codes
+            most_m = __reduce_max_sync(0xffffffffu, most_m);
+            most_v = __reduce_max_sync(0xffffffffu, most_v);
+            const bool second = lane >= 16;
+            float most = second ? __fsqrt_rn(__uint_as_float(most_v)) : __uint_as_float(most_m);
+            if (most < SMALLEST) most = 0.f;
+            const float top = second ? TOP_R : TOP_M;
+            const float inverse = most > 0.f ? __fdiv_rn(top, most) : 0.f;
+            if ((lane & 15) == 0) t.scales[second ? blocks + b : b] = __fmul_rn(most, second ? 1.f / TOP_R : 1.f / TOP_M);
             uint8_t c[8];
-            float q[8];
+            times8(m, __shfl_sync(0xffffffffu, inverse, 0));
+            e4m3_codes(m, c);
+            store8<VEC>(static_cast<uint8_t*>(t.m) + at, lane, left, c);
+            times8(r, __shfl_sync(0xffffffffu, inverse, 16));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(m[i], sm.inverse);
-            e4m3_codes(q, c);
-            store8(static_cast<uint8_t*>(t.m) + at, vec, lane, left, c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = root_code(__fmul_rn(r[i], sr.inverse));
-            store8(static_cast<uint8_t*>(t.v) + at, vec, lane, left, c);
-            if (lane == 0) {
-                t.scales[b] = sm.scale;
-                t.scales[blocks + b] = sr.scale;
-            }
+            for (int i = 0; i < 8; ++i) c[i] = static_cast<uint8_t>(root_code(r[i]));
+            store8<VEC>(static_cast<uint8_t*>(t.v) + at, lane, left, c);
         } else {
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(m[i]);
-            store8(static_cast<uint32_t*>(t.m) + at, vec, lane, left, w);
+            store8<VEC>(static_cast<uint32_t*>(t.m) + at, lane, left, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
-            store8(static_cast<uint32_t*>(t.v) + at, vec, lane, left, w);
+            store8<VEC>(static_cast<uint32_t*>(t.v) + at, lane, left, w);
         }
     }
 }
 
 // What the codes stand for (10 bytes a value: HBM).
-template <int N>
+template <bool VEC, int N>
 __global__ void __launch_bounds__(THREADS) adamw_values_kernel(const __grid_constant__ AdamwParams<N> a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const AdamwTensor& t = a.t[tensor_of(a, blockIdx.x)];
     const long long blocks = (t.count + ADAMW_BLOCK - 1) / ADAMW_BLOCK;
-    const long long first = static_cast<long long>(blockIdx.x - t.chunk0) * (ADAMW_CHUNK / ADAMW_BLOCK);
+    const long long first = static_cast<long long>(blockIdx.x - t.chunk0) * a.chunk, end = min(blocks, first + a.chunk);
     pdl_allow_next();
     pdl_wait_previous();
-#pragma unroll
-    for (int turn = 0; turn < TURNS; ++turn) {
-        const long long b = first + turn * WARPS + warp;
-        if (b >= blocks) break;
+    struct In {
+        Eight<uint8_t, VEC> m, v;
+        float ms, rs;
+    } now, next;
+    const auto load = [&](long long b, In& in) {
         const long long at = b * ADAMW_BLOCK;
         const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
-        const bool vec = t.vec && left == ADAMW_BLOCK;
-        uint8_t mc[8], vc[8];
-        load8(static_cast<const uint8_t*>(t.m) + at, vec, lane, left, mc);
-        load8(static_cast<const uint8_t*>(t.v) + at, vec, lane, left, vc);
-        const float ms = t.scales[b], rs = t.scales[blocks + b];
+        in.m.load(static_cast<const uint8_t*>(t.m) + at, lane, left);
+        in.v.load(static_cast<const uint8_t*>(t.v) + at, lane, left);
+        in.ms = t.scales[b];
+        in.rs = t.scales[blocks + b];
+    };
+    long long b = first + warp;
+    if (b < end) load(b, next);
+#pragma unroll 1
+    for (; b < end; b += WARPS) {
+        now = next;
+        if (b + WARPS < end) load(b + WARPS, next);
+        const long long at = b * ADAMW_BLOCK;
+        const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
         float m[8];
         uint32_t w[8];
-        e4m3_values(mc, m);
+        e4m3_values(now.m, m);
+        times8(m, now.ms);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__fmul_rn(m[i], ms));
-        store8(static_cast<uint32_t*>(t.p) + at, vec, lane, left, w);
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(m[i]);
+        store8<VEC>(static_cast<uint32_t*>(t.p) + at, lane, left, w);
+        root_values(now.v, m);
+        times8(m, __fmul_rn(now.rs, ROOT_UNIT));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float r = __fmul_rn(root_value(vc[i]), rs);
-            w[i] = __float_as_uint(__fmul_rn(r, r));
-        }
-        store8(static_cast<uint32_t*>(const_cast<void*>(t.g)) + at, vec, lane, left, w);
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__fmul_rn(m[i], m[i]));
+        store8<VEC>(static_cast<uint32_t*>(const_cast<void*>(t.g)) + at, lane, left, w);
     }
 }
 
@@ -307,6 +418,7 @@ AdamwParams<ADAMW_FEW> few_of(const AdamwGroup& g) {
     AdamwParams<ADAMW_FEW> p;
     for (int i = 0; i < g.p.tensors; ++i) p.t[i] = g.p.t[i];
     p.tensors = g.p.tensors;
+    p.chunk = g.p.chunk;
     p.beta1 = g.p.beta1;
     p.c1 = g.p.c1;
     p.beta2 = g.p.beta2;
@@ -317,38 +429,43 @@ AdamwParams<ADAMW_FEW> few_of(const AdamwGroup& g) {
     return p;
 }
 
-template <int PARAM, int GRAD, bool CODES>
+template <int PARAM, int GRAD, bool CODES, bool VEC>
 cudaError_t run(const AdamwGroup& g, cudaStream_t s) {
-    if (g.p.tensors <= ADAMW_FEW)
-        return launch_pdl(adamw_kernel<PARAM, GRAD, CODES, ADAMW_FEW>, dim3(g.chunks), dim3(THREADS), 0, s, few_of(g));
-    return launch_pdl(adamw_kernel<PARAM, GRAD, CODES, ADAMW_MANY>, dim3(g.chunks), dim3(THREADS), 0, s, g.p);
+    const dim3 grid(g.chunks), block(THREADS);
+    if (g.p.tensors <= ADAMW_FEW) return launch_pdl(adamw_kernel<PARAM, GRAD, CODES, VEC, ADAMW_FEW>, grid, block, 0, s, few_of(g));
+    return launch_pdl(adamw_kernel<PARAM, GRAD, CODES, VEC, ADAMW_MANY>, grid, block, 0, s, g.p);
 }
 template <int PARAM, int GRAD>
-cudaError_t pick(const AdamwGroup& g, bool codes, cudaStream_t s) {
-    return codes ? run<PARAM, GRAD, true>(g, s) : run<PARAM, GRAD, false>(g, s);
+cudaError_t pick(const AdamwGroup& g, bool codes, bool vec, cudaStream_t s) {
+    if (codes) return vec ? run<PARAM, GRAD, true, true>(g, s) : run<PARAM, GRAD, true, false>(g, s);
+    return vec ? run<PARAM, GRAD, false, true>(g, s) : run<PARAM, GRAD, false, false>(g, s);
+}
+template <bool VEC>
+cudaError_t run_values(const AdamwGroup& g, cudaStream_t s) {
+    const dim3 grid(g.chunks), block(THREADS);
+    if (g.p.tensors <= ADAMW_FEW) return launch_pdl(adamw_values_kernel<VEC, ADAMW_FEW>, grid, block, 0, s, few_of(g));
+    return launch_pdl(adamw_values_kernel<VEC, ADAMW_MANY>, grid, block, 0, s, g.p);
 }
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamwGroup& g, int param, int grad, bool codes, cudaStream_t s) {
+cudaError_t launch_adamw(const AdamwGroup& g, int param, int grad, bool codes, bool vec, cudaStream_t s) {
     switch (param * 4 + grad) {
-        case ADAMW_F32 * 4 + DT_F32: return pick<ADAMW_F32, DT_F32>(g, codes, s);
-        case ADAMW_F32 * 4 + DT_BF16: return pick<ADAMW_F32, DT_BF16>(g, codes, s);
-        case ADAMW_F32 * 4 + DT_F16: return pick<ADAMW_F32, DT_F16>(g, codes, s);
-        case ADAMW_BF16 * 4 + DT_F32: return pick<ADAMW_BF16, DT_F32>(g, codes, s);
-        case ADAMW_BF16 * 4 + DT_BF16: return pick<ADAMW_BF16, DT_BF16>(g, codes, s);
-        case ADAMW_F16 * 4 + DT_F32: return pick<ADAMW_F16, DT_F32>(g, codes, s);
-        case ADAMW_F16 * 4 + DT_F16: return pick<ADAMW_F16, DT_F16>(g, codes, s);
-        case ADAMW_SPLIT * 4 + DT_F32: return pick<ADAMW_SPLIT, DT_F32>(g, codes, s);
-        case ADAMW_SPLIT * 4 + DT_BF16: return pick<ADAMW_SPLIT, DT_BF16>(g, codes, s);
+        case ADAMW_F32 * 4 + DT_F32: return pick<ADAMW_F32, DT_F32>(g, codes, vec, s);
+        case ADAMW_F32 * 4 + DT_BF16: return pick<ADAMW_F32, DT_BF16>(g, codes, vec, s);
+        case ADAMW_F32 * 4 + DT_F16: return pick<ADAMW_F32, DT_F16>(g, codes, vec, s);
+        case ADAMW_BF16 * 4 + DT_F32: return pick<ADAMW_BF16, DT_F32>(g, codes, vec, s);
+        case ADAMW_BF16 * 4 + DT_BF16: return pick<ADAMW_BF16, DT_BF16>(g, codes, vec, s);
+        case ADAMW_F16 * 4 + DT_F32: return pick<ADAMW_F16, DT_F32>(g, codes, vec, s);
+        case ADAMW_F16 * 4 + DT_F16: return pick<ADAMW_F16, DT_F16>(g, codes, vec, s);
+        case ADAMW_SPLIT * 4 + DT_F32: return pick<ADAMW_SPLIT, DT_F32>(g, codes, vec, s);
+        case ADAMW_SPLIT * 4 + DT_BF16: return pick<ADAMW_SPLIT, DT_BF16>(g, codes, vec, s);
         default: return cudaErrorInvalidValue;
     }
 }
 
-cudaError_t launch_adamw_values(const AdamwGroup& g, cudaStream_t s) {
-    if (g.p.tensors <= ADAMW_FEW)
-        return launch_pdl(adamw_values_kernel<ADAMW_FEW>, dim3(g.chunks), dim3(THREADS), 0, s, few_of(g));
-    return launch_pdl(adamw_values_kernel<ADAMW_MANY>, dim3(g.chunks), dim3(THREADS), 0, s, g.p);
+cudaError_t launch_adamw_values(const AdamwGroup& g, bool vec, cudaStream_t s) {
+    return vec ? run_values<true>(g, s) : run_values<false>(g, s);
 }
 
 }  // namespace anvil

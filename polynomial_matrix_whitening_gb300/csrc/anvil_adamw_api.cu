@@ -20,7 +20,6 @@ namespace {
 
 bool off(const void* p, int es) { return (reinterpret_cast<uintptr_t>(p) & (es - 1)) != 0; }
 int64_t blocks_of(int64_t count) { return (count + ADAMW_BLOCK - 1) / ADAMW_BLOCK; }
-int64_t chunks_of(int64_t count) { return (count + ADAMW_CHUNK - 1) / ADAMW_CHUNK; }
 
 // The ranges of one array of every tensor (its role), in order of their addresses.
 struct Role {
@@ -70,12 +69,19 @@ anvil_status check_ranges(const Range (*get)(const void*, int, int), const void*
     return ok ? ANVIL_OK : ANVIL_ERR_ALIAS;
 }
 
-// Tensors of one kind share a launch: how param is stored, grad's type, states in 8 bits.
+int size_of(int dtype) { return dtype == ANVIL_F32 ? 4 : 2; }
+// Whether a warp may take four neighbours at once of an array of es bytes a value.
+bool vector(const void* p, int es) { return !(reinterpret_cast<uintptr_t>(p) & (4 * es - 1)); }
+
+// Tensors of one kind share a launch: how param is stored, grad's type, states in 8 bits, all on vector boundaries.
 int kind_of(const anvil_adamw_tensor& t) {
     const int param = t.mantissa ? ADAMW_SPLIT : t.param_dtype == ANVIL_F32 ? ADAMW_F32 : t.param_dtype == ANVIL_BF16 ? ADAMW_BF16 : ADAMW_F16;
-    return param << 3 | t.grad_dtype << 1 | (t.scales ? 1 : 0);
+    const int es = t.scales ? 1 : 4;
+    const bool vec = vector(t.param, size_of(t.param_dtype)) && vector(t.mantissa, 2) && vector(t.grad, size_of(t.grad_dtype)) &&
+                     vector(t.exp_avg, es) && vector(t.exp_avg_sq, es);
+    return param << 4 | t.grad_dtype << 2 | (t.scales ? 2 : 0) | (vec ? 1 : 0);
 }
-int size_of(int dtype) { return dtype == ANVIL_F32 ? 4 : 2; }
+constexpr int KINDS = 64;
 bool dtype_ok(int d) { return d == ANVIL_F32 || d == ANVIL_BF16 || d == ANVIL_F16; }
 
 const Range step_range(const void* tensors, int i, int role) {
@@ -102,15 +108,16 @@ const Range values_range(const void* tensors, int i, int role) {
     }
 }
 
-// Whether a warp may take four neighbours at once of an array of es bytes a value.
-bool vector(const void* p, int es) { return !(reinterpret_cast<uintptr_t>(p) & (4 * es - 1)); }
-
 // Collects tensors of one kind and launches them, ADAMW_MANY or so many chunks at a time.
 template <class Launch>
 struct Batches {
     AdamwGroup g;
     Launch launch;
-    explicit Batches(Launch f) : launch(f) { g.p.tensors = g.chunks = 0; }
+    // blocks: of all the tensors together
+    Batches(Launch f, int64_t blocks) : launch(f) {
+        g.p.tensors = g.chunks = 0;
+        g.p.chunk = adamw_chunk(blocks);
+    }
     cudaError_t flush() {
         if (!g.p.tensors) return cudaSuccess;
         const cudaError_t e = launch(g);
@@ -118,7 +125,7 @@ struct Batches {
         return e;
     }
     cudaError_t add(AdamwTensor t) {
-        const int64_t chunks = chunks_of(t.count);
+        const int64_t chunks = (blocks_of(t.count) + g.p.chunk - 1) / g.p.chunk;
         if (g.p.tensors == ADAMW_MANY || g.chunks + chunks > INT32_MAX) {
             const cudaError_t e = flush();
             if (e) return e;
@@ -161,7 +168,7 @@ anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, c
     if (ntensors < 0 || (ntensors > 0 && !tensors)) return ANVIL_ERR_INVALID_ARG;
     if (ntensors > ANVIL_MAX_TENSORS) return ANVIL_ERR_UNSUPPORTED_SHAPE;
     if (off(d_scalars, 4)) return ANVIL_ERR_ALIGNMENT;
-    uint32_t kinds = 0;  // that there are
+    uint64_t kinds = 0;  // that there are
     for (int i = 0; i < ntensors; ++i) {
         const anvil_adamw_tensor& t = tensors[i];
         if (t.count < 0 || !dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype) || (t.mantissa && t.param_dtype != ANVIL_BF16))
@@ -174,7 +181,7 @@ anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, c
         if (off(t.param, size_of(t.param_dtype)) || off(t.mantissa, 2) || off(t.grad, size_of(t.grad_dtype)) ||
             off(t.exp_avg, es) || off(t.exp_avg_sq, es) || off(t.scales, 4))
             return ANVIL_ERR_ALIGNMENT;
-        kinds |= 1u << kind_of(t);
+        kinds |= 1ull << kind_of(t);
     }
     if (!kinds) return ANVIL_OK;
     const bool written[ROLES] = {true, true, false, true, true, true};
@@ -189,14 +196,16 @@ anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, c
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    for (int kind = 0; kind < 32; ++kind) {
+    for (int kind = 0; kind < KINDS; ++kind) {
         if (!(kinds >> kind & 1)) continue;
-        const int param = kind >> 3, grad = kind >> 1 & 3;
-        const bool codes = kind & 1;
+        const int param = kind >> 4, grad = kind >> 2 & 3;
+        const bool codes = kind >> 1 & 1, vec = kind & 1;
         auto launch = [&](const AdamwGroup& g) {
-            return profiled(ANVIL_KERNEL_ADAMW, s, [&] { return launch_adamw(g, param, grad, codes, s); });
+            return profiled(ANVIL_KERNEL_ADAMW, s, [&] { return launch_adamw(g, param, grad, codes, vec, s); });
         };
-        Batches<decltype(launch)> batch(launch);
+        int64_t blocks = 0;
+        for (int i = 0; i < ntensors; ++i) blocks += tensors[i].count && kind_of(tensors[i]) == kind ? blocks_of(tensors[i].count) : 0;
+        Batches<decltype(launch)> batch(launch, blocks);
         batch.g.p.beta1 = static_cast<float>(config->beta1);
         batch.g.p.c1 = static_cast<float>(1.0 - config->beta1);
         batch.g.p.beta2 = static_cast<float>(config->beta2);
@@ -207,10 +216,7 @@ anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, c
         for (int i = 0; i < ntensors; ++i) {
             const anvil_adamw_tensor& t = tensors[i];
             if (t.count == 0 || kind_of(t) != kind) continue;
-            const int es = codes ? 1 : 4;
-            const bool vec = vector(t.param, size_of(t.param_dtype)) && vector(t.mantissa, 2) && vector(t.grad, size_of(t.grad_dtype)) &&
-                             vector(t.exp_avg, es) && vector(t.exp_avg_sq, es);
-            if ((e = batch.add({t.param, t.mantissa, t.grad, t.exp_avg, t.exp_avg_sq, t.scales, t.count, vec, 0})))
+            if ((e = batch.add({t.param, t.mantissa, t.grad, t.exp_avg, t.exp_avg_sq, t.scales, t.count, 0})))
                 return cuda_fail(e, "AdamW launch");
         }
         if ((e = batch.flush())) return cuda_fail(e, "AdamW launch");
@@ -238,20 +244,26 @@ anvil_status anvil_adamw_values(const anvil_adamw_state* states, int nstates, vo
     DeviceState* dev = nullptr;
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto launch = [&](const AdamwGroup& g) {
-        return profiled(ANVIL_KERNEL_ADAMW, s, [&] { return launch_adamw_values(g, s); });
-    };
-    Batches<decltype(launch)> batch(launch);
     cudaError_t e;
-    for (int i = 0; i < nstates; ++i) {
-        const anvil_adamw_state& t = states[i];
-        if (t.count == 0) continue;
-        const bool vec = vector(t.exp_avg, 1) && vector(t.exp_avg_sq, 1) && vector(t.m, 4) && vector(t.v, 4);
-        if ((e = batch.add({t.m, nullptr, t.v, const_cast<void*>(t.exp_avg), const_cast<void*>(t.exp_avg_sq),
-                            const_cast<float*>(t.scales), t.count, vec, 0})))
-            return cuda_fail(e, "AdamW launch");
+    for (int vec = 0; vec < 2; ++vec) {
+        const auto of_kind = [vec](const anvil_adamw_state& t) {
+            return t.count && (vector(t.exp_avg, 1) && vector(t.exp_avg_sq, 1) && vector(t.m, 4) && vector(t.v, 4)) == (vec != 0);
+        };
+        auto launch = [&](const AdamwGroup& g) {
+            return profiled(ANVIL_KERNEL_ADAMW, s, [&] { return launch_adamw_values(g, vec != 0, s); });
+        };
+        int64_t blocks = 0;
+        for (int i = 0; i < nstates; ++i) blocks += of_kind(states[i]) ? blocks_of(states[i].count) : 0;
+        Batches<decltype(launch)> batch(launch, blocks);
+        for (int i = 0; i < nstates; ++i) {
+            const anvil_adamw_state& t = states[i];
+            if (!of_kind(t)) continue;
+            if ((e = batch.add({t.m, nullptr, t.v, const_cast<void*>(t.exp_avg), const_cast<void*>(t.exp_avg_sq),
+                                const_cast<float*>(t.scales), t.count, 0})))
+                return cuda_fail(e, "AdamW launch");
+        }
+        if ((e = batch.flush())) return cuda_fail(e, "AdamW launch");
     }
-    if ((e = batch.flush())) return cuda_fail(e, "AdamW launch");
     return ANVIL_OK;
 }
 
