@@ -145,7 +145,7 @@ struct Product {
     bool f16;
     GemmEpilogue epi;
     float* part;  // scratch of the tail tiles' parts
-    bool overlap_next, overlap_previous;  // pair_gemm_kernel's flags
+    bool one_chain, overlap_next, overlap_previous;  // pair_gemm_kernel's flags
 };
 
 // How a product runs.
@@ -347,6 +347,7 @@ inline anvil_status fill_pair(const Product& q, const Plan& plan, DeviceState* d
     g.tiles_c = (q.cols + PAIR_COLS - 1) / PAIR_COLS;
     g.split = plan.split;
     g.units = plan.units;
+    g.one_chain = q.one_chain;
     g.overlap_next = q.overlap_next;
     g.overlap_previous = q.overlap_previous;
     g.err = dev->err;

@@ -39,7 +39,7 @@ __device__ __forceinline__ int relative_target(const PairHeadParams& p, long lon
 
 struct StatsPair {
     using Params = PairHeadParams;
-    static constexpr bool MULTI = false, OWN = true, RANK_B = false;
+    static constexpr bool MULTI = false, OWN = true, RANK_B = false, ONE_CHAIN = false;
     struct Row {
         long long row;
         int target;
@@ -98,7 +98,7 @@ struct StatsPair {
 
 struct DlogitsPair {
     using Params = PairHeadParams;
-    static constexpr bool MULTI = false, OWN = true, RANK_B = false;
+    static constexpr bool MULTI = false, OWN = true, RANK_B = false, ONE_CHAIN = false;
     struct Row {
         float lse2, g;
         int target;
@@ -110,7 +110,7 @@ struct DlogitsPair {
             const float lse = p.lse[row];
             if (lse != -INFINITY) {  // (no token of that row can be: its gradient is 0)
                 x.lse2 = lse * LOG2E;
-                x.g = p.scale ? p.grad[row] * *p.scale : p.grad[row];
+                x.g = p.grad[row] * *p.scale;
                 x.target = relative_target(p, row);
             }
         }
@@ -147,39 +147,80 @@ struct DlogitsPair {
     }
 };
 
-// A row's statistics joined, in order within each of eight shares and then over them: 32 rows a block,
-// a warp per share.
-constexpr int HJ_ROWS = 32, HJ_SHARES = 8;
-__global__ void __launch_bounds__(HJ_ROWS* HJ_SHARES) head_join_kernel(const HeadJoinParams p) {
-    __shared__ float2 share[HJ_SHARES][HJ_ROWS];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+// Two sums over different bases as one.  (A part with a sum of 0 has no logit above -inf; a NaN goes
+// through the sums.)
+__device__ __forceinline__ void join(float& ref, float& sum, float ref2, float sum2) {
+    const float now = sum2 == 0.f ? ref : sum == 0.f ? ref2 : fmaxf(ref, ref2);
+    sum = (sum == 0.f ? 0.f : sum * power2(ref - now)) + (sum2 == 0.f ? 0.f : sum2 * power2(ref2 - now));
+    ref = now;
+}
+
+// Few rows: a thread has one column's logits of eight rows, a warp 32 columns, a block 128.
+struct HeadRows {
+    using Params = RowHeadParams;
+    static constexpr bool GATED = false, HEAD = true;
+    static __device__ __forceinline__ void finish(const Params& p, const float (&v)[8], int col, bool live, int row, int rows, float2* to) {
+        float m[8], s[8], ref[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = live ? v[i] : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            ref[i] = m[i] == -INFINITY ? 0.f : m[i] * LOG2E;
+            s[i] = live ? power2(fmaf(v[i], LOG2E, -ref[i])) : 0.f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if ((threadIdx.x & 31) == i) to[i] = make_float2(ref[i], s[i]);
+            if (p.hit && live && i < rows && target_of(p.targets, p.target64, row + i) == col) p.hit[row + i] = v[i];
+        }
+    }
+    static __device__ __forceinline__ void end(const Params& p, int block, int row, float2 a, float2 b, float2 c, float2 d) {
+        join(a.x, a.y, b.x, b.y);
+        join(c.x, c.y, d.x, d.y);
+        join(a.x, a.y, c.x, c.y);
+        p.stats[static_cast<long long>(block) * p.nb + row] = a;
+    }
+};
+
+// A row's statistics joined, in a fixed order.  A block takes four rows, neighbours in the statistics (32
+// bytes), and 64 shares of the parts: 8 in a warp, joined by shuffles, and 8 warps.
+constexpr int HJ_ROWS = 4, HJ_THREADS = 256, HJ_SHARES = HJ_THREADS / HJ_ROWS, HJ_UNROLL = 4;
+__global__ void __launch_bounds__(HJ_THREADS) head_join_kernel(const HeadJoinParams p) {
+    __shared__ float2 share[HJ_THREADS / 32][HJ_ROWS];
+    const int x = threadIdx.x % HJ_ROWS, y = threadIdx.x / HJ_ROWS;
     const long long row = static_cast<long long>(blockIdx.x) * HJ_ROWS + x;
     pdl_allow_next();
     pdl_wait_previous();
-    // (a part with a sum of 0 has no logit above -inf; a NaN goes through the sums)
-    float ref = -INFINITY, sum = 0.f;
+    float ref = 0.f, sum = 0.f;
     if (row < p.rows) {
-#pragma unroll 8
-        for (int i = y; i < p.parts; i += HJ_SHARES) {
-            const float2 s = __ldcs(&p.stats[static_cast<long long>(i) * p.rows + row]);
-            if (s.y != 0.f) {
-                const float now = fmaxf(ref, s.x);
-                sum = sum * power2(ref - now) + s.y * power2(s.x - now);
-                ref = now;
+        for (int i0 = y; i0 < p.parts; i0 += HJ_SHARES * HJ_UNROLL) {
+            float2 s[HJ_UNROLL];
+#pragma unroll
+            for (int k = 0; k < HJ_UNROLL; ++k) {
+                const int i = i0 + k * HJ_SHARES;
+                s[k] = i < p.parts ? __ldcs(&p.stats[static_cast<long long>(i) * p.rows + row]) : make_float2(0.f, 0.f);
             }
+#pragma unroll
+            for (int k = 0; k < HJ_UNROLL; ++k) join(ref, sum, s[k].x, s[k].y);
         }
     }
-    share[y][x] = make_float2(ref, sum);
+#pragma unroll
+    for (int o = HJ_ROWS; o < 32; o *= 2) {
+        const float r2 = __shfl_xor_sync(0xffffffffu, ref, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
+        join(ref, sum, r2, s2);
+    }
+    if ((threadIdx.x & 31) < HJ_ROWS) share[threadIdx.x >> 5][x] = make_float2(ref, sum);
     __syncthreads();
-    if (y != 0 || row >= p.rows) return;
-    for (int k = 1; k < HJ_SHARES; ++k) {
-        const float2 s = share[k][x];
-        if (s.y != 0.f) {
-            const float now = fmaxf(ref, s.x);
-            sum = sum * power2(ref - now) + s.y * power2(s.x - now);
-            ref = now;
-        }
-    }
+    if (threadIdx.x >= HJ_ROWS || row >= p.rows) return;
+    for (int k = 1; k < HJ_THREADS / 32; ++k) join(ref, sum, share[k][x].x, share[k][x].y);
     const float lse = sum == 0.f ? -INFINITY : fmaf(ref, LN2, logf(sum));
     if (p.lse) p.lse[row] = lse;
     if (p.loss) {
@@ -188,8 +229,9 @@ __global__ void __launch_bounds__(HJ_ROWS* HJ_SHARES) head_join_kernel(const Hea
     }
 }
 
-// fp16 holds nothing below 2^-25, where most of d lies for a mean over thousands of rows: there d is
-// taken times a power of two, which the products' results are divided by (both exact).
+// d is taken over the largest |g|, which the products' results are multiplied by: a mean's g, the same
+// in every row, would be rounded to 16 bits the same way in each, 2^-9 of every gradient, and in fp16
+// most of d would be below the smallest value (2^-25; there 2^13 more).
 __global__ void __launch_bounds__(1024) head_scale_kernel(const HeadScaleParams p) {
     __shared__ uint32_t warps[32];
     pdl_allow_next();
@@ -203,10 +245,11 @@ __global__ void __launch_bounds__(1024) head_scale_kernel(const HeadScaleParams 
     if (threadIdx.x >= 32) return;
     most = __reduce_max_sync(0xffffffffu, warps[threadIdx.x]);
     if (threadIdx.x == 0) {
-        int e = 0;  // 0, an infinity or a NaN: as they are
-        if (most != 0 && most < 0x7f800000u) e = min(max(13 - (static_cast<int>(most >> 23) - 127), -120), 120);
-        p.scale[0] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        p.scale[1] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        float unit = __uint_as_float(most);
+        // 0, and beyond 2^100 either way (infinities and NaN among them): as they are
+        unit = unit >= 7.8886090522101181e-31f && unit <= 1.2676506002282294e30f ? (p.f16 ? unit * 0x1p-13f : unit) : 1.f;
+        p.scale[0] = __fdiv_rn(1.f, unit);
+        p.scale[1] = unit;
     }
 }
 
@@ -214,7 +257,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) head_round_kernel(const HeadRoundParams p) {
     pdl_allow_next();
     pdl_wait_previous();
-    const float scale = p.scale ? *p.scale : 1.f;
+    const float scale = *p.scale;
     const int chunks = (p.cols + 7) / 8;
     const long long total = chunks * p.rows, ld = chunks * 8ll;  // (src's rows go on in eights)
     const bool vec = p.cols % 8 == 0 && p.ldd % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.dst) & 15);
@@ -237,35 +280,55 @@ __global__ void __launch_bounds__(256) head_round_kernel(const HeadRoundParams p
     }
 }
 
-constexpr int HEAD_BOX = 64;  // six stages: the products bound both kernels
+constexpr int STATS_BOX = 0, DLOGITS_BOX = 64;  // seven and six stages: the products bound both kernels
 
 }  // namespace
 
 cudaError_t head_prepare() {
     cudaError_t e;
-#define ANVIL_SMEM(T, M)                                                                                                    \
-    if ((e = cudaFuncSetAttribute(pair_gemm_kernel<T, HEAD_BOX, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,            \
-                                  Staging<HEAD_BOX>::SMEM)))                                                                \
-    return e
-    ANVIL_SMEM(__nv_bfloat16, StatsPair);
-    ANVIL_SMEM(__half, StatsPair);
-    ANVIL_SMEM(__nv_bfloat16, DlogitsPair);
-    ANVIL_SMEM(__half, DlogitsPair);
+#define ANVIL_SMEM(kernel, bytes) \
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return e
+#define ANVIL_HEAD(T)                                                                                    \
+    ANVIL_SMEM((pair_gemm_kernel<T, STATS_BOX, StatsPair>), Staging<STATS_BOX>::SMEM);                   \
+    ANVIL_SMEM((pair_gemm_kernel<T, DLOGITS_BOX, DlogitsPair>), Staging<DLOGITS_BOX>::SMEM);             \
+    ANVIL_SMEM((row_gemm_kernel<T, 16, HeadRows>), RowShape<16>::smem(RowShape<16>::STAGES));            \
+    ANVIL_SMEM((row_gemm_kernel<T, 32, HeadRows>), RowShape<32>::smem(RowShape<32>::STAGES));            \
+    ANVIL_SMEM((row_gemm_kernel<T, 64, HeadRows>), RowShape<64>::smem(RowShape<64>::STAGES));            \
+    ANVIL_SMEM((row_gemm_kernel<T, 128, HeadRows>), RowShape<128>::smem(RowShape<128>::STAGES))
+    ANVIL_HEAD(__nv_bfloat16);
+    ANVIL_HEAD(__half);
+#undef ANVIL_HEAD
 #undef ANVIL_SMEM
     return cudaSuccess;
 }
 
 cudaError_t launch_head_stats(const PairHeadParams& p, int sm_count, cudaStream_t s) {
-    return p.f16 ? run_pair<__half, HEAD_BOX, StatsPair>(p, sm_count, s) : run_pair<__nv_bfloat16, HEAD_BOX, StatsPair>(p, sm_count, s);
+    return p.f16 ? run_pair<__half, STATS_BOX, StatsPair>(p, sm_count, s) : run_pair<__nv_bfloat16, STATS_BOX, StatsPair>(p, sm_count, s);
 }
 
 cudaError_t launch_head_dlogits(const PairHeadParams& p, int sm_count, cudaStream_t s) {
-    return p.f16 ? run_pair<__half, HEAD_BOX, DlogitsPair>(p, sm_count, s)
-                 : run_pair<__nv_bfloat16, HEAD_BOX, DlogitsPair>(p, sm_count, s);
+    return p.f16 ? run_pair<__half, DLOGITS_BOX, DlogitsPair>(p, sm_count, s)
+                 : run_pair<__nv_bfloat16, DLOGITS_BOX, DlogitsPair>(p, sm_count, s);
+}
+
+namespace {
+template <typename T>
+cudaError_t pick_rows(const RowHeadParams& p, int bn, int sm_count, cudaStream_t s) {
+    switch (bn) {
+        case 16: return run_row<T, 16, HeadRows>(p, sm_count, s);
+        case 32: return run_row<T, 32, HeadRows>(p, sm_count, s);
+        case 64: return run_row<T, 64, HeadRows>(p, sm_count, s);
+        default: return run_row<T, 128, HeadRows>(p, sm_count, s);
+    }
+}
+}  // namespace
+
+cudaError_t launch_head_rows(const RowHeadParams& p, int bn, int sm_count, cudaStream_t s) {
+    return p.f16 ? pick_rows<__half>(p, bn, sm_count, s) : pick_rows<__nv_bfloat16>(p, bn, sm_count, s);
 }
 
 cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t s) {
-    return launch_pdl(head_join_kernel, dim3(static_cast<unsigned>((p.rows + HJ_ROWS - 1) / HJ_ROWS)), dim3(HJ_ROWS * HJ_SHARES), 0, s, p);
+    return launch_pdl(head_join_kernel, dim3(static_cast<unsigned>((p.rows + HJ_ROWS - 1) / HJ_ROWS)), dim3(HJ_THREADS), 0, s, p);
 }
 
 cudaError_t launch_head_scale(const HeadScaleParams& p, cudaStream_t s) {

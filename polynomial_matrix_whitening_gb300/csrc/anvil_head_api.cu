@@ -19,9 +19,10 @@ anvil_status check_sizes(int64_t rows, int vocab, int k, int dtype) {
     return ANVIL_OK;
 }
 
-// Forward: copies of unaligned operands, the statistics [4 tiles][rows], the targets' logits [rows].
+// Forward: copies of unaligned operands, the statistics [parts][rows], the targets' logits [rows].
 struct HeadLayout {
     Stored x, w;
+    Plan plan;
     int parts;
     size_t off_x, off_w, off_stats, off_hit, total;
 };
@@ -29,7 +30,14 @@ HeadLayout head_layout(const anvil_head_desc* d) {
     HeadLayout L;
     L.x = {d->x, d->rows, d->ldx, d->k};
     L.w = stored_weight(d->weight, d->vocab, d->k, d->ldw, d->weight_transposed != 0);
-    L.parts = static_cast<int>(ceil_div(d->vocab, PAIR_COLS)) * (PAIR_COLS / HEAD_STATS_COLS);
+    // (an epilogue's cycles: a tile's exponentials, 2048 for the special function units of either CTA,
+    // and what is around them)
+    const double epilogue = 4000.0;
+    const int64_t kb = ceil_div(d->k, GEMM_BK);
+    memset(&L.plan, 0, sizeof(L.plan));
+    if (d->rows <= FEW_ROWS) plan_few(d->rows, d->vocab, kb, epilogue, &L.plan);
+    plan_whole(tiles_of(d->rows, d->vocab), kb, epilogue, ALL_FREE, &L.plan);
+    L.parts = static_cast<int>(L.plan.few ? ceil_div(d->vocab, ROW_TILE_A) : ceil_div(d->vocab, PAIR_COLS) * (PAIR_COLS / HEAD_STATS_COLS));
     L.off_x = 0;
     L.off_w = L.off_x + copy_bytes(L.x);
     L.off_stats = L.off_w + copy_bytes(L.w);
@@ -107,7 +115,7 @@ HeadGradLayout head_grad_layout(const anvil_head_grad_desc* d) {
     L.k8 = (d->k + 7) & ~7;
     size_t at = 0;
     L.off_scale = at;
-    if (d->dtype == ANVIL_F16) at += 256;
+    at += 256;
     L.off_x = at;
     at += copy_bytes(L.x);
     L.off_w = at;
@@ -125,10 +133,8 @@ HeadGradLayout head_grad_layout(const anvil_head_grad_desc* d) {
         const int wc = tr ? cols : d->k;
         const double ex = epilogue_cycles(dx_epilogue(d, L, aligned, false), d->rows);
         const double ew = d->dweight ? epilogue_cycles(dweight_epilogue(d, 0), wr) : 0.0;
-        // (few rows: only into the 16-bit result, which the kernels for them know)
-        const bool few = L.pieces == 1 && d->dtype == ANVIL_BF16;
-        if (d->dx && d->dweight) plan_both(d->rows, d->k, cols, few, tr, ex, wr, wc, d->rows, ew, &L.pdx[i], &L.pdw[i]);
-        else if (d->dx) L.pdx[i] = plan_product(d->rows, d->k, cols, few, tr, ex, ALL_FREE);
+        if (d->dx && d->dweight) plan_both(d->rows, d->k, cols, false, tr, ex, wr, wc, d->rows, ew, &L.pdx[i], &L.pdw[i]);
+        else if (d->dx) L.pdx[i] = plan_product(d->rows, d->k, cols, false, tr, ex, ALL_FREE);
         else L.pdw[i] = plan_product(wr, wc, d->rows, false, false, ew, ALL_FREE);
         if (L.pdx[i].part > L.part_dx) L.part_dx = L.pdx[i].part;
         if (L.pdw[i].part > part_dw) part_dw = L.pdw[i].part;
@@ -215,16 +221,40 @@ anvil_status anvil_linear_cross_entropy(const anvil_head_desc* d, void* workspac
     copies.add(&L.x, ws + L.off_x);
     copies.add(&L.w, ws + L.off_w);
     if ((st = copies.run(s)) != ANVIL_OK) return st;
-    PairHeadParams g;
-    memset(&g, 0, sizeof(g));
-    if ((st = fill_logits(L.x, L.w, tr, 0, d->vocab, f16, dev, &g)) != ANVIL_OK) return st;
-    g.targets = d->targets;
-    g.target64 = d->targets_int64 != 0;
-    g.stats = reinterpret_cast<float2*>(ws + L.off_stats);
-    g.hit = d->loss ? reinterpret_cast<float*>(ws + L.off_hit) : nullptr;
-    if ((e = profiled(ANVIL_KERNEL_HEAD_PRODUCT, s, [&] { return launch_head_stats(g, dev->sm_count, s); })))
-        return cuda_fail(e, "cross entropy launch");
-    const HeadJoinParams j = {g.stats, g.hit, d->targets, d->loss, d->lse, d->rows, L.parts, d->vocab, g.target64};
+    const int target64 = d->targets_int64 != 0;
+    float2* stats = reinterpret_cast<float2*>(ws + L.off_stats);
+    float* hit = d->loss ? reinterpret_cast<float*>(ws + L.off_hit) : nullptr;
+    if (L.plan.few) {
+        RowHeadParams g;
+        memset(&g, 0, sizeof(g));
+        if ((st = encode(&g.tm_a, 2, f16, L.w.p, L.w.cols, L.w.rows, L.w.ld, 64, tr ? 64 : ROW_TILE_A)) ||
+            (st = encode(&g.tm_b, 2, f16, L.x.p, L.x.cols, L.x.rows, L.x.ld, 64, L.plan.bn)))
+            return st;
+        g.na = d->vocab;
+        g.nb = static_cast<int>(d->rows);
+        g.k = d->k;
+        g.a_mn = tr;
+        g.f16 = f16;
+        g.splits = L.plan.splits;
+        g.kb_per_split = L.plan.kb;
+        g.err = dev->err;
+        g.targets = d->targets;
+        g.target64 = target64;
+        g.stats = stats;
+        g.hit = hit;
+        e = profiled(ANVIL_KERNEL_HEAD_PRODUCT, s, [&] { return launch_head_rows(g, L.plan.bn, dev->sm_count, s); });
+    } else {
+        PairHeadParams g;
+        memset(&g, 0, sizeof(g));
+        if ((st = fill_logits(L.x, L.w, tr, 0, d->vocab, f16, dev, &g)) != ANVIL_OK) return st;
+        g.targets = d->targets;
+        g.target64 = target64;
+        g.stats = stats;
+        g.hit = hit;
+        e = profiled(ANVIL_KERNEL_HEAD_PRODUCT, s, [&] { return launch_head_stats(g, dev->sm_count, s); });
+    }
+    if (e) return cuda_fail(e, "cross entropy launch");
+    const HeadJoinParams j = {stats, hit, d->targets, d->loss, d->lse, d->rows, L.parts, d->vocab, target64};
     e = profiled(ANVIL_KERNEL_HEAD_SUM, s, [&] { return launch_head_join(j, s); });
     return e ? cuda_fail(e, "cross entropy launch") : ANVIL_OK;
 }
@@ -261,13 +291,11 @@ anvil_status anvil_linear_cross_entropy_backward(const anvil_head_grad_desc* d, 
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int target64 = d->targets_int64 != 0;
-    float* scale = f16 ? reinterpret_cast<float*>(ws + L.off_scale) : nullptr;
+    float* scale = reinterpret_cast<float*>(ws + L.off_scale);
     float* sum = reinterpret_cast<float*>(ws + L.off_sum);
-    if (scale) {
-        const HeadScaleParams p = {d->grad_loss, d->targets, scale, d->rows, target64};
-        if ((e = profiled(ANVIL_KERNEL_HEAD_PREPARE, s, [&] { return launch_head_scale(p, s); })))
-            return cuda_fail(e, "cross entropy gradient launch");
-    }
+    const HeadScaleParams unit = {d->grad_loss, d->targets, scale, d->rows, target64, f16};
+    if ((e = profiled(ANVIL_KERNEL_HEAD_PREPARE, s, [&] { return launch_head_scale(unit, s); })))
+        return cuda_fail(e, "cross entropy gradient launch");
     Copies copies = {};
     copies.add(&L.x, ws + L.off_x);
     copies.add(&L.w, ws + L.off_w);
@@ -294,7 +322,7 @@ anvil_status anvil_linear_cross_entropy_backward(const anvil_head_grad_desc* d, 
         memset(&f, 0, sizeof(f));
         f.f16 = f16;
         const Plan &pdx = L.pdx[last], &pdw = L.pdw[last];
-        const bool overlap = d->dx && d->dweight && !pdx.few;
+        const bool overlap = d->dx && d->dweight;
         MultiProduct m;
         if (d->dx) {
             memset(&m, 0, sizeof(m));
@@ -312,10 +340,11 @@ anvil_status anvil_linear_cross_entropy_backward(const anvil_head_grad_desc* d, 
             m.q.epi = dx_epilogue(d, L, sum, i == 0);
             m.q.part = reinterpret_cast<float*>(ws + L.off_part);
             m.q.overlap_next = overlap;
-            if (scale && L.pieces == 1) {
+            if (L.pieces == 1) {
                 m.q.epi.scale = scale + 1;
                 st = run_multi(m, pdx, dev, s, &f.tail[0]);
             } else {
+                m.q.one_chain = true;
                 st = run_product(m.q, pdx, dev, s, &f.tail[0]);
             }
             if (st != ANVIL_OK) return st;
@@ -333,18 +362,13 @@ anvil_status anvil_linear_cross_entropy_backward(const anvil_head_grad_desc* d, 
             m.q.epi = dweight_epilogue(d, first);
             m.q.part = reinterpret_cast<float*>(ws + L.off_part + L.part_dx);
             m.q.overlap_previous = overlap;
-            if (scale) {
-                m.q.epi.scale = scale + 1;
-                st = run_multi(m, pdw, dev, s, &f.tail[1]);
-            } else {
-                st = run_product(m.q, pdw, dev, s, &f.tail[1]);
-            }
-            if (st != ANVIL_OK) return st;
+            m.q.epi.scale = scale + 1;
+            if ((st = run_multi(m, pdw, dev, s, &f.tail[1])) != ANVIL_OK) return st;
         }
         if ((st = run_finish(f, s)) != ANVIL_OK) return st;
     }
     if (!d->dx || L.pieces == 1) return ANVIL_OK;
-    const HeadRoundParams p = {sum, d->dx, scale ? scale + 1 : nullptr, d->rows, d->rows > 1 ? d->lddx : d->k, d->k, f16};
+    const HeadRoundParams p = {sum, d->dx, scale + 1, d->rows, d->rows > 1 ? d->lddx : d->k, d->k, f16};
     e = profiled(ANVIL_KERNEL_HEAD_SUM, s, [&] { return launch_head_round(p, s); });
     return e ? cuda_fail(e, "cross entropy gradient launch") : ANVIL_OK;
 }

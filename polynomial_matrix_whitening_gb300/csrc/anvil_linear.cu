@@ -268,6 +268,8 @@ cudaError_t linear_prepare() {
     ANVIL_SMEM((pair_gemm_kernel<__half, 128, PlainPair>), Staging<128>::SMEM);
     ANVIL_SMEM((pair_gemm_kernel<float, 64, PlainPair>), Staging<64>::SMEM);
     ANVIL_SMEM((pair_gemm_kernel<float, 128, PlainPair>), Staging<128>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<float, 64, SumPair>), Staging<64>::SMEM);
+    ANVIL_SMEM((pair_gemm_kernel<float, 128, SumPair>), Staging<128>::SMEM);
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 16, PlainRows>), RowShape<16>::smem(RowShape<16>::STAGES));
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 32, PlainRows>), RowShape<32>::smem(RowShape<32>::STAGES));
     ANVIL_SMEM((row_gemm_kernel<__nv_bfloat16, 64, PlainRows>), RowShape<64>::smem(RowShape<64>::STAGES));
@@ -288,6 +290,7 @@ cudaError_t pick_pair(const PairGemmParams& p, int sm_count, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t s) {
+    if (p.one_chain) return p.box_bytes == 64 ? run_pair<float, 64, SumPair>(p, sm_count, s) : run_pair<float, 128, SumPair>(p, sm_count, s);
     if (p.epi.out_f32) return pick_pair<float>(p, sm_count, s);
     return p.f16 ? pick_pair<__half>(p, sm_count, s) : pick_pair<__nv_bfloat16>(p, sm_count, s);
 }

@@ -205,14 +205,19 @@ __device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int co
 // ---------------------------------------------------------------- the pair kernel
 // What a variant of it computes.  OWN: its tiles' epilogue is its own (Row load(p, unit, row of the
 // CTA's 128), ahead of the accumulator, and tile()).  RANK_B: the pair's CTAs load operand B through a
-// map each, both from the same rows (the tile is as wide as one CTA's share).
+// map each, both from the same rows (the tile is as wide as one CTA's share).  ONE_CHAIN: an fp32 result
+// is one chain of products, as a 16-bit one is (it is on its way to 16 bits).
 struct PlainPair {
     using Params = PairGemmParams;
-    static constexpr bool MULTI = false, OWN = false, RANK_B = false;
+    static constexpr bool MULTI = false, OWN = false, RANK_B = false, ONE_CHAIN = false;
+};
+struct SumPair {
+    using Params = PairGemmParams;
+    static constexpr bool MULTI = false, OWN = false, RANK_B = false, ONE_CHAIN = true;
 };
 struct MultiPair {
     using Params = PairMultiParams;
-    static constexpr bool MULTI = true, OWN = false, RANK_B = false;
+    static constexpr bool MULTI = true, OWN = false, RANK_B = false, ONE_CHAIN = false;
 };
 // The parameters of result `res` (0 or 1).
 __device__ __forceinline__ const GemmEpilogue& epi_of(const PairGemmParams& p, int) { return p.epi; }
@@ -230,11 +235,12 @@ constexpr int STAGE = A_STAGE + B_STAGE;
 constexpr int EPI_COLS = BN / EPI_GROUPS;  // 64
 // The epilogue's staging boxes, one per group: 128 rows of W bytes, 16-byte chunk j of row r at
 // the chunk the tensor maps' swizzle gives it.  W = 128 takes a group's 64 columns of 16-bit
-// results at once; W = 64 takes them by halves and leaves the room of one more stage.
+// results at once; W = 64 takes them by halves and leaves the room of one more stage, W = 0 (nothing
+// is stored by boxes) that of two.
 template <int W>
 struct Staging {
     static constexpr int BOX = CTA_ROWS * W;
-    static constexpr int STAGES = W == 128 ? 5 : 6;
+    static constexpr int STAGES = W == 128 ? 5 : W == 64 ? 6 : 7;
     static constexpr int SMEM = STAGES * STAGE + EPI_GROUPS * BOX + 1024;  // + alignment slack
     static __device__ __forceinline__ uint32_t addr(uint32_t box, int r, int j) {
         return box + static_cast<uint32_t>(W == 128 ? r * 128 + ((j ^ (r & 7)) << 4) : r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
@@ -526,7 +532,7 @@ __device__ __forceinline__ void store_f32(const P& p, EpiState& x, const float* 
 // T: type of 16-bit results (float: fp32 results, taken in chains of CHAIN_KB k-blocks)
 template <typename T, int W, typename M>
 __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid_constant__ typename M::Params p) {
-    constexpr bool F32 = sizeof(T) == 4;
+    constexpr bool F32 = sizeof(T) == 4 && !M::ONE_CHAIN;
     constexpr int STAGES = Staging<W>::STAGES, COLS4 = W / 4;  // fp32 columns of a box
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[STAGES];
@@ -756,6 +762,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                     if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
                     tc_fence_after();
                     if (t.part < 0) M::template tile<T, W>(p, x, tlane - lcol + ab * BN, te[ab], t, row0, row);
+                } else if constexpr (M::ONE_CHAIN) {
+                    if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
+                    tc_fence_after();
                 } else {
                     if (t.part < 0 && early_input(p, res)) {
                         // the residual, once the box's earlier store has been read
@@ -766,14 +775,16 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                     tc_fence_after();
                     if (t.part < 0) epilogue_16<T, W, M::MULTI>(p, x, tlane + ab * BN, te[ab], row0, col0, res);
                 }
-                if (t.part >= 0) {
+                if constexpr (W > 0) {
+                    if (t.part >= 0 || M::ONE_CHAIN) {
 #pragma unroll 1
-                    for (int q = 0; q < EPI_COLS / COLS4; ++q) {
-                        float v[COLS4];
-                        if constexpr (COLS4 == 32) tmem_ld_32x32b_x32(tlane + ab * BN + q * COLS4, v);
-                        else tmem_ld_16(tlane + ab * BN + q * COLS4, v);
-                        if (q == EPI_COLS / COLS4 - 1) release_acc(x, te[ab]);
-                        store_f32<W, M::MULTI>(p, x, v, t.part, lrow, lcol + COLS4 * q, row0, col0 + COLS4 * q, res);
+                        for (int q = 0; q < EPI_COLS / COLS4; ++q) {
+                            float v[COLS4];
+                            if constexpr (COLS4 == 32) tmem_ld_32x32b_x32(tlane + ab * BN + q * COLS4, v);
+                            else tmem_ld_16(tlane + ab * BN + q * COLS4, v);
+                            if (q == EPI_COLS / COLS4 - 1) release_acc(x, te[ab]);
+                            store_f32<W, M::MULTI>(p, x, v, t.part, lrow, lcol + COLS4 * q, row0, col0 + COLS4 * q, res);
+                        }
                     }
                 }
                 ++acc;
@@ -867,15 +878,16 @@ __device__ __forceinline__ void finish_rows(const GemmEpilogue& e, float (&v)[N]
         if (i < rows) static_cast<T*>(e.out)[(row + i) * e.ldout + col] = Elem<T>::store(v[i]);
 }
 
-// What a variant of the row kernel computes.  GATED: its 128 weight rows are 64 of one weight (TMEM
+// What a variant of the row kernel computes.  HEAD: its eight results of a thread at a time go to
+// finish(p, v, column, exists, first row, rows, this block's shared memory), and the block's to end().  GATED: its 128 weight rows are 64 of one weight (TMEM
 // lanes 0 to 63) and the same 64 of another, whose results finish one element together.
 struct PlainRows {
     using Params = RowGemmParams;
-    static constexpr bool GATED = false;
+    static constexpr bool GATED = false, HEAD = false;
 };
 struct GatedRows {
     using Params = RowGatedParams;
-    static constexpr bool GATED = true;
+    static constexpr bool GATED = true, HEAD = false;
 };
 // act(g) u of up to N rows (B's) of one column, g and u kept where they are asked for.
 template <typename T, int N, typename P>
@@ -933,6 +945,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) row_gemm_kernel(const __grid_c
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int aborted;
     __shared__ volatile int armed[S::STAGES];  // 1 + the k-block last loaded into each stage (0: none)
+    __shared__ float2 stats[M::HEAD ? 4 : 1][M::HEAD ? BN : 1];
 
     pdl_allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1037,7 +1050,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) row_gemm_kernel(const __grid_c
             for (int q = 0; q < nb; q += 8) {
                 float v[8];
                 tmem_ld_8(tlane + q, v);
-                if (live) finish_rows<T, 8>(p.epi, v, bias, b0 + q, nb - q, col);
+                if constexpr (M::HEAD) M::finish(p, v, col, live, b0 + q, nb - q, &stats[quad][q]);
+                else if (live) finish_rows<T, 8>(p.epi, v, bias, b0 + q, nb - q, col);
             }
         } else {
             // the partial accumulator, in place of the stages (which are done): four B rows of one
@@ -1069,10 +1083,16 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) row_gemm_kernel(const __grid_c
                 for (int j = 2 * split; j < quads; j += 2 * p.splits) {
                     float v[8];
                     join_parts(smem_u32(&own[j * ROW_TILE_A + r]), p.splits, v);
-                    if (live) finish_rows<T, 8>(p.epi, v, bias, b0 + 4 * j, nb - 4 * j, col);
+                    if constexpr (M::HEAD) M::finish(p, v, col, live, b0 + 4 * j, nb - 4 * j, &stats[quad][4 * j]);
+                    else if (live) finish_rows<T, 8>(p.epi, v, bias, b0 + 4 * j, nb - 4 * j, col);
                 }
             }
             __syncwarp();
+        }
+        if constexpr (M::HEAD) {
+            named_barrier_sync(1, 128);
+            // (a split has finished every splits-th eight of the rows)
+            if (r < nb && r / 8 % p.splits == split) M::end(p, blockIdx.x / p.splits, b0 + r, stats[0][r], stats[1][r], stats[2][r], stats[3][r]);
         }
         tc_fence_before();
     }

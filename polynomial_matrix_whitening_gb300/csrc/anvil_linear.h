@@ -47,6 +47,7 @@ struct PairGemmParams {
     int tiles_r, tiles_c;           // 256 x 256 output tiles
     TileSplit split;
     int units;                      // of work: whole tiles and the turns of the tail (unit_of)
+    int one_chain;                  // the fp32 result is one chain of products
     int overlap_next;               // the next kernel may start before this one has ended
     int overlap_previous;           // and this one before the previous one has (both products of a backward pass)
     unsigned* err;
@@ -173,9 +174,16 @@ struct PairHeadParams : PairGemmParams {
     float* hit;           // [rows]
     const float* lse;     // [rows]
     const float* grad;    // [rows]
-    const float* scale;   // or null
+    const float* scale;
 };
 constexpr int HEAD_STATS_COLS = 64;  // columns behind one pair of statistics
+// The same for few rows: statistics [blocks of 128 columns][rows].
+struct RowHeadParams : RowGemmParams {
+    const void* targets;
+    int target64;
+    float2* stats;
+    float* hit;
+};
 struct HeadJoinParams {
     const float2* stats;
     const float* hit;
@@ -185,24 +193,26 @@ struct HeadJoinParams {
     long long rows;
     int parts, vocab, target64;
 };
-// scale[0] = a power of two that brings the largest |grad| (of rows that count) to 2^13 or above it, scale[1] = 1 / scale[0]
+// scale[1] = the largest |grad| of rows that count (fp16: over 2^13), scale[0] = 1 / scale[1]
 struct HeadScaleParams {
     const float* grad;
     const void* targets;
     float* scale;
     long long rows;
-    int target64;
+    int target64, f16;
 };
 // dst [rows, cols] 16 bit = src fp32 [rows, cols] (times *scale)
 struct HeadRoundParams {
     const float* src;
     void* dst;
-    const float* scale;   // or null
+    const float* scale;
     long long rows, ldd;
     int cols, f16;
 };
 cudaError_t head_prepare();
 cudaError_t launch_head_stats(const PairHeadParams& p, int sm_count, cudaStream_t stream);
+// bn: rows of x per block (16, 32, 64 or 128)
+cudaError_t launch_head_rows(const RowHeadParams& p, int bn, int sm_count, cudaStream_t stream);
 cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t stream);
 cudaError_t launch_head_dlogits(const PairHeadParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_head_scale(const HeadScaleParams& p, cudaStream_t stream);
