@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(GG_THREADS) gated_grad_kernel(const GatedGradP
     T* dz = static_cast<T*>(p.dz);
     const long long part = p.rows * p.ldd;
     const int chunks = (p.cols + 7) / 8;
-    const long long total = chunks * p.rows, step = static_cast<long long>(gridDim.x) * GG_THREADS;
     pdl_allow_next();
     pdl_wait_previous();
     auto fetch = [&](const T* q, int c) {
@@ -133,23 +132,24 @@ __global__ void __launch_bounds__(GG_THREADS) gated_grad_kernel(const GatedGradP
             *reinterpret_cast<uint4*>(to + part) = Elem<T>::pack(h);
         }
     };
-    for (long long i0 = blockIdx.x * static_cast<long long>(GG_THREADS) + threadIdx.x; i0 < total; i0 += step * GG_UNROLL) {
+    Walk w(chunks, blockIdx.x * static_cast<long long>(GG_THREADS) + threadIdx.x, static_cast<long long>(gridDim.x) * GG_THREADS);
+    while (w.row < p.rows) {
         uint4 wd[GG_UNROLL], wg[GG_UNROLL], wu[GG_UNROLL];
         long long row[GG_UNROLL];
         int c[GG_UNROLL];
 #pragma unroll
         for (int k = 0; k < GG_UNROLL; ++k) {
-            const long long i = i0 + k * step;
-            if (i >= total) break;
-            row[k] = i / chunks;
-            c[k] = static_cast<int>(i - row[k] * chunks) * 8;
+            row[k] = w.row;
+            c[k] = w.chunk * 8;
+            w.next(chunks);
+            if (row[k] >= p.rows) continue;
             wd[k] = fetch(dy + row[k] * p.lddy, c[k]);
             wg[k] = fetch(g + row[k] * p.ldg, c[k]);
             wu[k] = fetch(u + row[k] * p.ldu, c[k]);
         }
 #pragma unroll
         for (int k = 0; k < GG_UNROLL; ++k) {
-            if (i0 + k * step >= total) break;
+            if (row[k] >= p.rows) break;
             float d[8], a[8], b[8], dg[8];
             Elem<T>::unpack(wd[k], d);
             Elem<T>::unpack(wg[k], a);

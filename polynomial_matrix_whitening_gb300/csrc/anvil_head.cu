@@ -190,6 +190,112 @@ struct HeadRows {
     }
 };
 
+// One to four rows: the weight is read once, by warps that take four of its rows at a time and keep
+// each token's running statistics; no tensor cores, no tiles to fill.  A lane takes every 32nd 16-byte chunk,
+// the tokens wait in shared memory as fp32.
+template <typename T, int R>
+__global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 3) head_token_kernel(const TokenHeadParams p) {
+    constexpr int G = HEAD_TOKEN_GROUP, E = Elem<T>::VEC;
+    extern __shared__ __align__(16) float token_values[];  // [R][chunks * E]
+    float* const xs = token_values;
+    __shared__ float2 shares[HEAD_TOKEN_WARPS][R];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int chunks = (p.k + E - 1) / E, whole = p.k / E;
+    const long long step = static_cast<long long>(gridDim.x) * HEAD_TOKEN_WARPS * G;
+    pdl_allow_next();
+    pdl_wait_previous();
+    for (int i = threadIdx.x; i < R * chunks * E; i += 32 * HEAD_TOKEN_WARPS) {
+        const int r = i / (chunks * E), c = i - r * chunks * E;
+        xs[i] = c < p.k && r < p.rows ? Elem<T>::load(static_cast<const T*>(p.x)[r * p.ldx + c]) : 0.f;
+    }
+    __syncthreads();
+    float ref = 0.f, sum = 0.f;  // lane r's: token r
+    const long long target = p.hit && lane < p.rows ? target_of(p.targets, p.target64, lane) : -1;
+    for (long long row0 = (static_cast<long long>(blockIdx.x) * HEAD_TOKEN_WARPS + warp) * G; row0 < p.cols; row0 += step) {
+        const T* w[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) w[g] = static_cast<const T*>(p.w) + min(row0 + g, static_cast<long long>(p.cols) - 1) * p.ldw;
+        uint64_t acc[G][R];
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[g][r] = 0;
+        constexpr int U = 3;  // chunks of a lane on their way at a time
+        for (int c0 = lane; c0 - lane < chunks; c0 += 32 * U) {
+            uint4 in[U][G];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    in[u][g] = c0 + 32 * u < whole ? ldg_stream(w[g] + (c0 + 32 * u) * E) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + 32 * u;
+                if (c == whole && whole < chunks) {  // the row's last values
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        float f[E];
+#pragma unroll
+                        for (int e = 0; e < E; ++e) f[e] = c * E + e < p.k ? Elem<T>::load(w[g][c * E + e]) : 0.f;
+                        in[u][g] = Elem<T>::pack(f);
+                    }
+                }
+                if (c >= chunks) break;
+                uint64_t wv[G][E / 2];
+#pragma unroll
+                for (int g = 0; g < G; ++g) Elem<T>::unpack_pairs(in[u][g], wv[g]);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float4* q = reinterpret_cast<const float4*>(xs + (r * chunks + c) * E);
+                    const float4 a = q[0], b = q[1];
+                    const uint64_t xv[4] = {f2_make(a.x, a.y), f2_make(a.z, a.w), f2_make(b.x, b.y), f2_make(b.z, b.w)};
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int e = 0; e < E / 2; ++e) acc[g][r] = f2_fma(wv[g][e], xv[e], acc[g][r]);
+                }
+            }
+        }
+        float z[G];  // of token `lane`
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            z[g] = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float lo, hi;
+                f2_split(acc[g][r], &lo, &hi);
+                float v = lo + hi;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == r) z[g] = v;
+            }
+        }
+        if (lane < R) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if (row0 + g >= p.cols) z[g] = -INFINITY;
+                else if (row0 + g == target) p.hit[lane] = z[g];
+                most = fmaxf(most, z[g]);
+            }
+            const float base = most == -INFINITY ? 0.f : most * LOG2E;
+            float s = 0.f;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (row0 + g < p.cols) s += power2(fmaf(z[g], LOG2E, -base));
+            join(ref, sum, base, s);
+        }
+    }
+    if (lane < R) shares[warp][lane] = make_float2(ref, sum);
+    __syncthreads();
+    if (threadIdx.x < p.rows) {
+        ref = shares[0][threadIdx.x].x;
+        sum = shares[0][threadIdx.x].y;
+        for (int k = 1; k < HEAD_TOKEN_WARPS; ++k) join(ref, sum, shares[k][threadIdx.x].x, shares[k][threadIdx.x].y);
+        p.stats[static_cast<long long>(blockIdx.x) * p.rows + threadIdx.x] = make_float2(ref, sum);
+    }
+}
+
 // A row's statistics joined, in a fixed order.  A block takes four rows, neighbours in the statistics (32
 // bytes), and 64 shares of the parts: 8 in a warp, joined by shuffles, and 8 warps.
 constexpr int HJ_ROWS = 4, HJ_THREADS = 256, HJ_SHARES = HJ_THREADS / HJ_ROWS, HJ_UNROLL = 4;
@@ -259,11 +365,11 @@ __global__ void __launch_bounds__(256) head_round_kernel(const HeadRoundParams p
     pdl_wait_previous();
     const float scale = *p.scale;
     const int chunks = (p.cols + 7) / 8;
-    const long long total = chunks * p.rows, ld = chunks * 8ll;  // (src's rows go on in eights)
+    const long long ld = chunks * 8ll;  // (src's rows go on in eights)
     const bool vec = p.cols % 8 == 0 && p.ldd % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.dst) & 15);
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long row = i / chunks;
-        const int c = static_cast<int>(i - row * chunks) * 8;
+    for (Walk at(chunks, blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll); at.row < p.rows; at.next(chunks)) {
+        const long long row = at.row;
+        const int c = at.chunk * 8;
         float v[8];
         Elem<float>::unpack(ldg_stream(p.src + row * ld + c), v);
         Elem<float>::unpack(ldg_stream(p.src + row * ld + c + 4), v + 4);
@@ -291,6 +397,9 @@ cudaError_t head_prepare() {
 #define ANVIL_HEAD(T)                                                                                    \
     ANVIL_SMEM((pair_gemm_kernel<T, STATS_BOX, StatsPair>), Staging<STATS_BOX>::SMEM);                   \
     ANVIL_SMEM((pair_gemm_kernel<T, DLOGITS_BOX, DlogitsPair>), Staging<DLOGITS_BOX>::SMEM);             \
+    ANVIL_SMEM((head_token_kernel<T, 1>), 4 * (HEAD_TOKEN_VALUES + 8));                                  \
+    ANVIL_SMEM((head_token_kernel<T, 2>), 4 * (HEAD_TOKEN_VALUES + 16));                                 \
+    ANVIL_SMEM((head_token_kernel<T, 4>), 4 * (HEAD_TOKEN_VALUES / 3 * 4 + 32));                         \
     ANVIL_SMEM((row_gemm_kernel<T, 16, HeadRows>), RowShape<16>::smem(RowShape<16>::STAGES));            \
     ANVIL_SMEM((row_gemm_kernel<T, 32, HeadRows>), RowShape<32>::smem(RowShape<32>::STAGES));            \
     ANVIL_SMEM((row_gemm_kernel<T, 64, HeadRows>), RowShape<64>::smem(RowShape<64>::STAGES));            \
@@ -325,6 +434,22 @@ cudaError_t pick_rows(const RowHeadParams& p, int bn, int sm_count, cudaStream_t
 
 cudaError_t launch_head_rows(const RowHeadParams& p, int bn, int sm_count, cudaStream_t s) {
     return p.f16 ? pick_rows<__half>(p, bn, sm_count, s) : pick_rows<__nv_bfloat16>(p, bn, sm_count, s);
+}
+
+namespace {
+template <typename T, int R>
+cudaError_t run_tokens_of(const TokenHeadParams& p, cudaStream_t s) {
+    const size_t smem = sizeof(float) * R * ((p.k + 7) / 8 * 8);
+    return launch_pdl(head_token_kernel<T, R>, dim3(head_token_blocks(p.cols)), dim3(32 * HEAD_TOKEN_WARPS), smem, s, p);
+}
+template <typename T>
+cudaError_t pick_tokens_of(const TokenHeadParams& p, cudaStream_t s) {
+    return p.rows == 1 ? run_tokens_of<T, 1>(p, s) : p.rows == 2 ? run_tokens_of<T, 2>(p, s) : run_tokens_of<T, 4>(p, s);
+}
+}  // namespace
+
+cudaError_t launch_head_tokens(const TokenHeadParams& p, cudaStream_t s) {
+    return p.f16 ? pick_tokens_of<__half>(p, s) : pick_tokens_of<__nv_bfloat16>(p, s);
 }
 
 cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t s) {

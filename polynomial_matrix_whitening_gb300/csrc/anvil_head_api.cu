@@ -35,9 +35,14 @@ HeadLayout head_layout(const anvil_head_desc* d) {
     const double epilogue = 4000.0;
     const int64_t kb = ceil_div(d->k, GEMM_BK);
     memset(&L.plan, 0, sizeof(L.plan));
+    // one to four rows and a weight stored by rows: read without tensor cores
+    L.plan.tokens = d->rows <= HEAD_TOKENS && !d->weight_transposed && d->rows * d->k <= HEAD_TOKEN_VALUES;
     if (d->rows <= FEW_ROWS) plan_few(d->rows, d->vocab, kb, epilogue, &L.plan);
+    const bool tokens = L.plan.tokens;
     plan_whole(tiles_of(d->rows, d->vocab), kb, epilogue, ALL_FREE, &L.plan);
-    L.parts = static_cast<int>(L.plan.few ? ceil_div(d->vocab, ROW_TILE_A) : ceil_div(d->vocab, PAIR_COLS) * (PAIR_COLS / HEAD_STATS_COLS));
+    L.plan.tokens = tokens;
+    if (L.plan.tokens) L.parts = head_token_blocks(d->vocab);
+    else L.parts = static_cast<int>(L.plan.few ? ceil_div(d->vocab, ROW_TILE_A) : ceil_div(d->vocab, PAIR_COLS) * (PAIR_COLS / HEAD_STATS_COLS));
     L.off_x = 0;
     L.off_w = L.off_x + copy_bytes(L.x);
     L.off_stats = L.off_w + copy_bytes(L.w);
@@ -60,9 +65,10 @@ anvil_status check_head(const anvil_head_desc* d) {
     return ANVIL_OK;
 }
 
-// The gradient's pieces: as many columns of the vocabulary as d takes 256 MB for, whole tiles, all but the
-// last of one size.
-constexpr int64_t PIECE_BYTES = 256ll << 20;
+// The gradient's pieces: as many columns of the vocabulary as d takes 512 MB for, whole tiles, all but the
+// last of one size.  (8192 x 50304 x 768, us: pieces of 64 MB 1407, 128 MB 1304, 256 MB 1166, 512 MB 1121, the
+// whole of it 1125.)
+constexpr int64_t PIECE_BYTES = 512ll << 20;
 struct HeadGradLayout {
     Stored x, w;
     int pieces, piece, last;    // columns of a piece, of the last one
@@ -224,7 +230,10 @@ anvil_status anvil_linear_cross_entropy(const anvil_head_desc* d, void* workspac
     const int target64 = d->targets_int64 != 0;
     float2* stats = reinterpret_cast<float2*>(ws + L.off_stats);
     float* hit = d->loss ? reinterpret_cast<float*>(ws + L.off_hit) : nullptr;
-    if (L.plan.few) {
+    if (L.plan.tokens) {
+        const TokenHeadParams g = {L.x.p, L.w.p, L.x.ld, L.w.ld, static_cast<int>(d->rows), d->vocab, d->k, f16, d->targets, target64, stats, hit};
+        e = profiled(ANVIL_KERNEL_HEAD_PRODUCT, s, [&] { return launch_head_tokens(g, s); });
+    } else if (L.plan.few) {
         RowHeadParams g;
         memset(&g, 0, sizeof(g));
         if ((st = encode(&g.tm_a, 2, f16, L.w.p, L.w.cols, L.w.rows, L.w.ld, 64, tr ? 64 : ROW_TILE_A)) ||

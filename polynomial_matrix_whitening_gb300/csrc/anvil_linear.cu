@@ -154,17 +154,30 @@ __global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const __grid_con
 __global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ RepackParams q) {
     const Repack& p = q.job[blockIdx.y];
     pdl_wait_previous();  // (the product starts after this kernel: its shared memory would take the L1 that the loads need)
-    const long long chunks = (p.cols + 7) / 8;
-    const long long total = chunks * p.rows;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long row = i / chunks;
-        const int c = static_cast<int>(i - row * chunks) * 8;
+    const int chunks = (p.cols + 7) / 8;
+    for (Walk at(chunks, blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll); at.row < p.rows; at.next(chunks)) {
+        const long long row = at.row;
+        const int c = at.chunk * 8;
         const uint16_t* s = p.src + row * p.lds + c;
-        uint32_t w[8];
+        uint4 to;
+        if (row < p.src_rows && c + 8 <= p.cols) {
+            // words, of which an odd start is half a word off
+            uint32_t w[5];
+            const bool odd = (reinterpret_cast<uintptr_t>(s) & 2) != 0;
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(s + odd);
+            w[0] = odd ? *s : 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols && row < p.src_rows ? s[e] : 0u;
-        *reinterpret_cast<uint4*>(p.dst + row * p.ldd + c) =
-            make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+            for (int e = 0; e < 3; ++e) w[e + 1] = q[e];
+            w[4] = odd ? s[7] : q[3];
+            to = odd ? make_uint4(w[0] | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, w[3] >> 16 | w[4] << 16)
+                     : make_uint4(w[1], w[2], w[3], w[4]);
+        } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols && row < p.src_rows ? s[e] : 0u;
+            to = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        }
+        *reinterpret_cast<uint4*>(p.dst + row * p.ldd + c) = to;
     }
 }
 

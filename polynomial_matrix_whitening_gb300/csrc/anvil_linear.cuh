@@ -24,6 +24,23 @@ constexpr int PAIR_THREADS = 32 * (EPI_WARP0 + 4 * EPI_GROUPS);
 constexpr int CHAIN_KB = 8;             // k-blocks of one chain of an fp32 result (512 deep)
 constexpr int RASTER_ROWS = 8;          // rows of tiles per raster group
 
+// A thread's way over the chunks of a matrix's rows, `step` chunks at a time, without a division a step.
+struct Walk {
+    long long row, rows_a_step;
+    int chunk, chunks_a_step;
+    __device__ __forceinline__ Walk(int chunks, long long first, long long step)
+        : row(first / chunks), rows_a_step(step / chunks), chunk(static_cast<int>(first - row * chunks)),
+          chunks_a_step(static_cast<int>(step - rows_a_step * chunks)) {}
+    __device__ __forceinline__ void next(int chunks) {
+        row += rows_a_step;
+        chunk += chunks_a_step;
+        if (chunk >= chunks) {
+            chunk -= chunks;
+            ++row;
+        }
+    }
+};
+
 // 32 lanes x 16 or 8 consecutive fp32 columns of TMEM (as tmem_ld_32x32b_x32).
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];

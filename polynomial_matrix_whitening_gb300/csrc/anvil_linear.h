@@ -184,6 +184,24 @@ struct RowHeadParams : RowGemmParams {
     float2* stats;
     float* hit;
 };
+// One to four rows, the weight [cols][k] on 16-byte rows: statistics [blocks][rows].
+struct TokenHeadParams {
+    const void* x;
+    const void* w;
+    long long ldx, ldw;
+    int rows, cols, k, f16;
+    const void* targets;
+    int target64;
+    float2* stats;
+    float* hit;
+};
+constexpr int HEAD_TOKENS = 4, HEAD_TOKEN_VALUES = 16384;  // rows; values of x, fp32 in shared memory
+constexpr int HEAD_TOKEN_GROUP = 4, HEAD_TOKEN_WARPS = 8;  // weight rows of a warp at a time, warps of a block
+// Blocks: three for each of a GB300's SMs, as far as there are groups of weight rows for their warps.
+inline int head_token_blocks(int cols) {
+    const int per = HEAD_TOKEN_GROUP * HEAD_TOKEN_WARPS, all = (cols + per - 1) / per;
+    return all < 152 * 3 ? all : 152 * 3;
+}
 struct HeadJoinParams {
     const float2* stats;
     const float* hit;
@@ -211,6 +229,7 @@ struct HeadRoundParams {
 };
 cudaError_t head_prepare();
 cudaError_t launch_head_stats(const PairHeadParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_head_tokens(const TokenHeadParams& p, cudaStream_t stream);
 // bn: rows of x per block (16, 32, 64 or 128)
 cudaError_t launch_head_rows(const RowHeadParams& p, int bn, int sm_count, cudaStream_t stream);
 cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t stream);

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 from test_gpu_block_ops import A, DT, E, U, close, make_weight, randn  # noqa: E402,F401
 
-SHAPES = [(1, 1, 1), (1, 50304, 768), (7, 700, 5000), (30, 16384, 1024), (100, 50304, 200), (250, 257, 300), (2, 7, 5), (3, 65, 64), (5, 1000, 100), (17, 50257, 130), (64, 4096, 768), (129, 300, 771),
+SHAPES = [(1, 1, 1), (1, 50304, 768), (7, 700, 5000), (1, 1001, 5001), (4, 50257, 771), (3, 33, 4000), (2, 131072, 64), (4, 16, 4096), (30, 16384, 1024), (100, 50304, 200), (250, 257, 300), (2, 7, 5), (3, 65, 64), (5, 1000, 100), (17, 50257, 130), (64, 4096, 768), (129, 300, 771),
           (257, 511, 256), (300, 50304, 64), (777, 5003, 771), (1500, 256, 96), (2048, 8192, 520)]
 
 
