@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(GG_THREADS) gated_grad_kernel(const GatedGradP
             *reinterpret_cast<uint4*>(to + part) = Elem<T>::pack(h);
         }
     };
-    Walk w(chunks, blockIdx.x * static_cast<long long>(GG_THREADS) + threadIdx.x, static_cast<long long>(gridDim.x) * GG_THREADS);
+    Walk w(chunks, blockIdx.x * GG_THREADS + threadIdx.x, gridDim.x * GG_THREADS);
     while (w.row < p.rows) {
         uint4 wd[GG_UNROLL], wg[GG_UNROLL], wu[GG_UNROLL];
         long long row[GG_UNROLL];

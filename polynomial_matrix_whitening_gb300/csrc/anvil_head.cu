@@ -190,11 +190,13 @@ struct HeadRows {
     }
 };
 
-// One to four rows: the weight is read once, by warps that take four of its rows at a time and keep
+// One or two rows: the weight is read once, by warps that take four of its rows at a time and keep
 // each token's running statistics; no tensor cores, no tiles to fill.  A lane takes every 32nd 16-byte chunk,
-// the tokens wait in shared memory as fp32.
+// twelve of them on their way, the tokens wait in shared memory as fp32.  HBM bounds it where the weight is
+// large (1 x 131072 x 4096: 157 us, 6.8 TB/s; 1 x 50304 x 768 with the join 18.7, the row kernel 24); three
+// blocks an SM, with fewer registers each, were slower (187, 20.1), and for four rows the row kernel is faster.
 template <typename T, int R>
-__global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 3) head_token_kernel(const TokenHeadParams p) {
+__global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(const TokenHeadParams p) {
     constexpr int G = HEAD_TOKEN_GROUP, E = Elem<T>::VEC;
     extern __shared__ __align__(16) float token_values[];  // [R][chunks * E]
     float* const xs = token_values;
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(256) head_round_kernel(const HeadRoundParams p
     const int chunks = (p.cols + 7) / 8;
     const long long ld = chunks * 8ll;  // (src's rows go on in eights)
     const bool vec = p.cols % 8 == 0 && p.ldd % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.dst) & 15);
-    for (Walk at(chunks, blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll); at.row < p.rows; at.next(chunks)) {
+    for (Walk at(chunks, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256); at.row < p.rows; at.next(chunks)) {
         const long long row = at.row;
         const int c = at.chunk * 8;
         float v[8];
@@ -399,7 +401,6 @@ cudaError_t head_prepare() {
     ANVIL_SMEM((pair_gemm_kernel<T, DLOGITS_BOX, DlogitsPair>), Staging<DLOGITS_BOX>::SMEM);             \
     ANVIL_SMEM((head_token_kernel<T, 1>), 4 * (HEAD_TOKEN_VALUES + 8));                                  \
     ANVIL_SMEM((head_token_kernel<T, 2>), 4 * (HEAD_TOKEN_VALUES + 16));                                 \
-    ANVIL_SMEM((head_token_kernel<T, 4>), 4 * (HEAD_TOKEN_VALUES / 3 * 4 + 32));                         \
     ANVIL_SMEM((row_gemm_kernel<T, 16, HeadRows>), RowShape<16>::smem(RowShape<16>::STAGES));            \
     ANVIL_SMEM((row_gemm_kernel<T, 32, HeadRows>), RowShape<32>::smem(RowShape<32>::STAGES));            \
     ANVIL_SMEM((row_gemm_kernel<T, 64, HeadRows>), RowShape<64>::smem(RowShape<64>::STAGES));            \
@@ -444,7 +445,7 @@ cudaError_t run_tokens_of(const TokenHeadParams& p, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t pick_tokens_of(const TokenHeadParams& p, cudaStream_t s) {
-    return p.rows == 1 ? run_tokens_of<T, 1>(p, s) : p.rows == 2 ? run_tokens_of<T, 2>(p, s) : run_tokens_of<T, 4>(p, s);
+    return p.rows == 1 ? run_tokens_of<T, 1>(p, s) : run_tokens_of<T, 2>(p, s);
 }
 }  // namespace
 

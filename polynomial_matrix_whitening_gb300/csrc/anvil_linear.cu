@@ -57,12 +57,15 @@ namespace {
 // neighbouring lanes are neighbouring elements whatever the arrays' alignment.
 constexpr int FINISH_THREADS = PAIR_COLS;
 constexpr int TAIL_ROWS = 16, TAIL_BLOCKS = PAIR_ROWS / TAIL_ROWS;
-template <typename T>
+// MULTI: of a launch of several products (a second result, scaled results); apart, since a choice of
+// parameters by a value costs the others 2 us (1000 x 2815 x 771).
+template <typename T, bool MULTI>
 __device__ __forceinline__ void tail_sum(const TailSumParams& p, int block) {
     const int tile = block / TAIL_BLOCKS, r0 = block % TAIL_BLOCKS * TAIL_ROWS;
     int tr, tc;
     tile_at(p.split.whole + tile, p.tiles_r, p.tiles_c, &tr, &tc);
-    const bool second = p.result_tiles && tr >= p.result_tiles;
+    bool second = false;
+    if constexpr (MULTI) second = p.result_tiles && tr >= p.result_tiles;
     if (second) tr -= p.result_tiles;
     const GemmEpilogue& e = second ? p.epi2 : p.epi;
     const int col = tc * PAIR_COLS + threadIdx.x;
@@ -90,7 +93,7 @@ __device__ __forceinline__ void tail_sum(const TailSumParams& p, int block) {
 #pragma unroll
         for (int i = 0; i < TAIL_ROWS; ++i) v[i] += __ldcs(part + i * PAIR_COLS);
     }
-    if (e.scale) {
+    if (MULTI && e.scale) {
         const float scale = *e.scale;
 #pragma unroll
         for (int i = 0; i < TAIL_ROWS; ++i) v[i] *= scale;
@@ -131,7 +134,7 @@ __device__ __forceinline__ void column_sum(const ColumnSumParams& p, int block) 
 }
 
 // Everything that is added up after the products: one launch (T: type of 16-bit results).
-template <typename T>
+template <typename T, bool MULTI>
 __global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const __grid_constant__ FinishParams p) {
     pdl_allow_next();
     int b = blockIdx.x;
@@ -140,8 +143,8 @@ __global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const __grid_con
         const TailSumParams& t = p.tail[j];
         const int blocks = t.tiles * TAIL_BLOCKS;
         if (b < blocks) {
-            if (t.epi.out_f32) tail_sum<float>(t, b);
-            else tail_sum<T>(t, b);
+            if (t.epi.out_f32) tail_sum<float, MULTI>(t, b);
+            else tail_sum<T, MULTI>(t, b);
             return;
         }
         b -= blocks;
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(256) repack_kernel(const __grid_constant__ Rep
     const Repack& p = q.job[blockIdx.y];
     pdl_wait_previous();  // (the product starts after this kernel: its shared memory would take the L1 that the loads need)
     const int chunks = (p.cols + 7) / 8;
-    for (Walk at(chunks, blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll); at.row < p.rows; at.next(chunks)) {
+    for (Walk at(chunks, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256); at.row < p.rows; at.next(chunks)) {
         const long long row = at.row;
         const int c = at.chunk * 8;
         const uint16_t* s = p.src + row * p.lds + c;
@@ -311,8 +314,12 @@ cudaError_t launch_pair_gemm(const PairGemmParams& p, int sm_count, cudaStream_t
 cudaError_t launch_finish(const FinishParams& p, cudaStream_t s) {
     const int bias = p.bias.out ? (p.bias.cols + CS_COLS - 1) / CS_COLS : 0;
     const dim3 grid((p.tail[0].tiles + p.tail[1].tiles) * TAIL_BLOCKS + bias);
-    if (p.f16) return launch_pdl(finish_kernel<__half>, grid, dim3(FINISH_THREADS), 0, s, p);
-    return launch_pdl(finish_kernel<__nv_bfloat16>, grid, dim3(FINISH_THREADS), 0, s, p);
+    const dim3 block(FINISH_THREADS);
+    bool multi = false;
+    for (const TailSumParams& t : p.tail) multi = multi || (t.tiles && (t.result_tiles || t.epi.scale));
+    if (p.f16) return multi ? launch_pdl(finish_kernel<__half, true>, grid, block, 0, s, p) : launch_pdl(finish_kernel<__half, false>, grid, block, 0, s, p);
+    return multi ? launch_pdl(finish_kernel<__nv_bfloat16, true>, grid, block, 0, s, p)
+                 : launch_pdl(finish_kernel<__nv_bfloat16, false>, grid, block, 0, s, p);
 }
 
 cudaError_t launch_tokens(const TokenParams& p, cudaStream_t s) {

@@ -24,13 +24,18 @@ constexpr int PAIR_THREADS = 32 * (EPI_WARP0 + 4 * EPI_GROUPS);
 constexpr int CHAIN_KB = 8;             // k-blocks of one chain of an fp32 result (512 deep)
 constexpr int RASTER_ROWS = 8;          // rows of tiles per raster group
 
-// A thread's way over the chunks of a matrix's rows, `step` chunks at a time, without a division a step.
+// A thread's way over the chunks of a matrix's rows: from number `first` (its own in the grid), `step`
+// (the grid's threads) at a time, with 32-bit divisions at its start and none on the way.
 struct Walk {
-    long long row, rows_a_step;
-    int chunk, chunks_a_step;
-    __device__ __forceinline__ Walk(int chunks, long long first, long long step)
-        : row(first / chunks), rows_a_step(step / chunks), chunk(static_cast<int>(first - row * chunks)),
-          chunks_a_step(static_cast<int>(step - rows_a_step * chunks)) {}
+    long long row;
+    int chunk, rows_a_step, chunks_a_step;
+    __device__ __forceinline__ Walk(int chunks, unsigned first, unsigned step) {
+        const unsigned n = static_cast<unsigned>(chunks);
+        row = first / n;
+        chunk = static_cast<int>(first % n);
+        rows_a_step = static_cast<int>(step / n);
+        chunks_a_step = static_cast<int>(step % n);
+    }
     __device__ __forceinline__ void next(int chunks) {
         row += rows_a_step;
         chunk += chunks_a_step;

@@ -184,7 +184,7 @@ struct RowHeadParams : RowGemmParams {
     float2* stats;
     float* hit;
 };
-// One to four rows, the weight [cols][k] on 16-byte rows: statistics [blocks][rows].
+// One or two rows, the weight [cols][k] on 16-byte rows: statistics [blocks][rows].
 struct TokenHeadParams {
     const void* x;
     const void* w;
@@ -195,12 +195,12 @@ struct TokenHeadParams {
     float2* stats;
     float* hit;
 };
-constexpr int HEAD_TOKENS = 4, HEAD_TOKEN_VALUES = 16384;  // rows; values of x, fp32 in shared memory
+constexpr int HEAD_TOKENS = 2, HEAD_TOKEN_VALUES = 16384;  // rows; values of x, fp32 in shared memory
 constexpr int HEAD_TOKEN_GROUP = 4, HEAD_TOKEN_WARPS = 8;  // weight rows of a warp at a time, warps of a block
-// Blocks: three for each of a GB300's SMs, as far as there are groups of weight rows for their warps.
+// Blocks: two for each of a GB300's SMs, as far as there are groups of weight rows for their warps.
 inline int head_token_blocks(int cols) {
     const int per = HEAD_TOKEN_GROUP * HEAD_TOKEN_WARPS, all = (cols + per - 1) / per;
-    return all < 152 * 3 ? all : 152 * 3;
+    return all < 152 * 2 ? all : 152 * 2;
 }
 struct HeadJoinParams {
     const float2* stats;
