@@ -11,6 +11,14 @@ The operators around the banks as a training program uses them, next to the bank
                tail; the head and the norms take the Adam step
     serving    one token at a time, with the likeliest alternatives
 
+Three options exchange a part each for the operator that does it in fewer launches and less memory:
+
+    --gated       a block is x += W_down (silu(W_gate h) * (W_up h)), h = norm(x): both projections in
+                  one kernel, three matrices of a block in the bank
+    --fused-loss  head and loss as one operator: no logits in training (and no entropy)
+    --adamw BITS  the head (bf16 beside the low half of its fp32 value) and the norms in one AdamW
+                  step, its moments in 32 or 8 bits
+
 The data is synthetic: the next token follows from the current one by a fixed random map
 nine times in ten, and is any token else.  The embedding is fixed.
 
@@ -44,19 +52,41 @@ class Adam:
             self.value.copy_(self.master)
 
 
+class Parameter:
+    """A parameter of the AdamW step: `value` in fp32, or in bf16 with the fp32 value's low half beside it."""
+
+    def __init__(self, init, compute=F32, bits=32):
+        init, self.mantissa = init.to(F32).contiguous(), None
+        self.value = init
+        if compute == BF16:
+            halves = init.view(torch.int32)
+            self.value = (halves >> 16).to(torch.int16).view(BF16)
+            self.mantissa = (halves << 16 >> 16).to(torch.int16)
+        self.state = anvil.adamw_state(self.value, bits)
+
+
+def adamw(parameters, grads, step, lr, weight_decay=0.0):
+    """One AdamW step of all of them."""
+    exp_avgs, exp_avg_sqs, scales = zip(*(p.state for p in parameters))
+    anvil.adamw_step([p.value for p in parameters], grads, exp_avgs, exp_avg_sqs, lr, step, weight_decay=weight_decay,
+                     mantissas=[p.mantissa for p in parameters], scales=scales)
+
+
 class Model:
-    def __init__(self, vocab=8192, dim=768, hidden=2816, blocks=2, seed=0):
+    def __init__(self, vocab=8192, dim=768, hidden=2816, blocks=2, seed=0, gated=False, fused_loss=False, adamw=None):
         gen = torch.Generator(device="cuda").manual_seed(seed)
 
         def normal(*shape, scale):
             return torch.randn(*shape, generator=gen, device="cuda") * scale
 
         self.vocab, self.dim, self.blocks = vocab, dim, blocks
+        self.gated, self.fused_loss, self.adamw, self.steps = gated, fused_loss, adamw, 0
         self.embedding = normal(vocab, dim, scale=1.0).to(BF16)
-        # the bank: W_up of block i is matrix 2i, W_down^T is matrix 2i + 1
-        g = 2 * blocks
+        # the bank: W_up of block i is matrix 2i, W_down^T is matrix 2i + 1; gated: W_gate, W_up, W_down^T
+        self.per_block = 3 if gated else 2
+        g = self.per_block * blocks
         self.bank = normal(g, hidden, dim, scale=dim ** -0.5).to(BF16)
-        self.bank[1::2] *= 0.1
+        self.bank[self.per_block - 1::self.per_block] *= 0.1
         self.mantissa = torch.zeros(g, hidden, dim, device="cuda", dtype=torch.int16)
         self.grad = torch.zeros(g, hidden, dim, device="cuda")
         self.velocity = torch.zeros(2, g, hidden, dim, device="cuda")
@@ -67,61 +97,91 @@ class Model:
         self.link = anvil.alloc_tail_link((g, hidden, dim))
         self.workspace = anvil.alloc_workspace(shape)
         self.tail_workspace = torch.empty(anvil.tail_workspace_bytes(shape), device="cuda", dtype=torch.uint8)
-        self.gains = [Adam(torch.ones(dim, device="cuda")) for _ in range(blocks + 1)]
-        self.shifts = [Adam(torch.zeros(dim, device="cuda")) for _ in range(blocks + 1)]
-        self.head = Adam(normal(vocab, dim, scale=dim ** -0.5), BF16)
+        vector, matrix = Adam, Adam
+        if adamw:  # a norm's moments are small: 32 bits
+            vector, matrix = Parameter, lambda init, compute: Parameter(init, compute, adamw)
+        self.gains = [vector(torch.ones(dim, device="cuda")) for _ in range(blocks + 1)]
+        self.shifts = [vector(torch.zeros(dim, device="cuda")) for _ in range(blocks + 1)]
+        self.head = matrix(normal(vocab, dim, scale=dim ** -0.5), BF16)
 
-    def up(self, i):
-        return self.bank[2 * i]
+    def gate(self, i, of=None):
+        return (self.bank if of is None else of)[self.per_block * i]
 
-    def down(self, i):
-        return self.bank[2 * i + 1].t()
+    def up(self, i, of=None):
+        return (self.bank if of is None else of)[self.per_block * (i + 1) - 2]
 
-    def forward(self, tokens, save=None):
-        """Logits of the next tokens; save: a list that takes what the backward pass needs."""
+    def down(self, i, of=None):
+        return (self.bank if of is None else of)[self.per_block * (i + 1) - 1].t()
+
+    def hidden(self, tokens, save=None):
+        """What the head multiplies; save: a list that takes what the backward pass needs."""
         x = self.embedding[tokens]
         for i in range(self.blocks):
             h, mean, rstd = anvil.layernorm_forward(x, self.gains[i].value, self.shifts[i].value)
-            if save is None:
-                a = anvil.linear_forward(h, self.up(i), activation="relu2")
+            if self.gated:
+                a = anvil.gated_linear_forward(h, self.gate(i), self.up(i), save_preact=save is not None)
             else:
-                a, z = anvil.linear_forward(h, self.up(i), activation="relu2", save_preact=True)
+                a = anvil.linear_forward(h, self.up(i), activation="relu2", save_preact=save is not None)
+            if save is not None:
+                a, *z = a
                 save.append((x, mean, rstd, h, z, a))
             x = anvil.linear_forward(a, self.down(i), residual=x)
         h, mean, rstd = anvil.layernorm_forward(x, self.gains[-1].value, self.shifts[-1].value)
         if save is not None:
             save.append((x, mean, rstd, h))
-        return anvil.linear_forward(h, self.head.value)
+        return h
+
+    def forward(self, tokens, save=None):
+        """Logits of the next tokens; save as hidden's."""
+        return anvil.linear_forward(self.hidden(tokens, save), self.head.value)
 
     def loss_and_gradients(self, tokens, targets):
         """(loss, entropy) and the gradients: the bank's in self.grad, the others returned as
         (head, [(gain, shift) per norm])."""
         save = []
-        logits = self.forward(tokens, save)
-        logprob, entropy, lse, _, _ = anvil.token_logprobs(logits, targets)
-        seed = torch.full_like(lse, -1.0 / targets.numel())
-        dlogits = anvil.token_logprobs_backward(logits, targets, lse, seed, out=logits)
+        if self.fused_loss:
+            h = self.hidden(tokens, save)
+            loss, lse = anvil.linear_cross_entropy(h, self.head.value, targets)
+            seed = torch.full_like(lse, 1.0 / targets.numel())
+            dh, dhead = anvil.linear_cross_entropy_backward(h, self.head.value, targets, lse, seed, dweight_dtype=F32)
+            stats = (loss.mean(), None)
+        else:
+            logits = self.forward(tokens, save)
+            h = save[-1][3]
+            logprob, entropy, lse, _, _ = anvil.token_logprobs(logits, targets)
+            seed = torch.full_like(lse, -1.0 / targets.numel())
+            dlogits = anvil.token_logprobs_backward(logits, targets, lse, seed, out=logits)
+            dh, dhead, _ = anvil.linear_backward(dlogits, h, self.head.value, bias_grad=False, dweight_dtype=F32)
+            stats = (-logprob.mean(), entropy.mean())
         x, mean, rstd, h = save.pop()
-        dh, dhead, _ = anvil.linear_backward(dlogits, h, self.head.value, bias_grad=False, dweight_dtype=F32)
         dx, *norm = anvil.layernorm_backward(dh, x, mean, rstd, self.gains[-1].value, out=dh)
         norms = [tuple(norm)]
         for i in reversed(range(self.blocks)):
             x, mean, rstd, h, z, a = save.pop()
             da, _, _ = anvil.linear_backward(dx, a, self.down(i), bias_grad=False, dweight_dtype=F32,
-                                             dweight=self.grad[2 * i + 1].t())
-            dh, _, _ = anvil.linear_backward(da, h, self.up(i), preact=z, activation="relu2", bias_grad=False,
-                                             dweight_dtype=F32, dweight=self.grad[2 * i])
+                                             dweight=self.down(i, self.grad))
+            if self.gated:
+                dh, _, _ = anvil.gated_linear_backward(da, h, self.gate(i), self.up(i), *z, dweight_dtype=F32,
+                                                       dgate=self.gate(i, self.grad), dup=self.up(i, self.grad))
+            else:
+                dh, _, _ = anvil.linear_backward(da, h, self.up(i), preact=z[0], activation="relu2", bias_grad=False,
+                                                 dweight_dtype=F32, dweight=self.up(i, self.grad))
             dx, *norm = anvil.layernorm_backward(dh, x, mean, rstd, self.gains[i].value, residual_grad=dx, out=dh)
             norms.append(tuple(norm))
-        return (-logprob.mean(), entropy.mean()), (dhead, norms[::-1])
+        return stats, (dhead, norms[::-1])
 
     def step(self, tokens, targets, bank_lr=0.01, lr=2e-3):
-        """One training step; returns (loss, entropy) as they were before it."""
+        """One training step; returns (loss, entropy) as they were before it (no entropy with the fused loss)."""
         stats, (dhead, norms) = self.loss_and_gradients(tokens, targets)
         anvil.multi_bank_step([anvil.Bank(self.grad, self.velocity, self.update, tail_link=self.link)], self.workspace)
         self.bank_lr.fill_(bank_lr)
         anvil.update_tail([anvil.Tail(self.update, self.velocity, self.energy, self.bank, self.mantissa, self.bank_lr,
                                       eff_wd=0.0, beta2=0.95, tail_link=self.link)], self.tail_workspace)
+        if self.adamw:
+            self.steps += 1
+            adamw([self.head] + self.gains + self.shifts, [dhead] + [g for g, _ in norms] + [g for _, g in norms],
+                  self.steps, lr)
+            return stats
         self.head.update(dhead, lr)
         for (gain, shift), dgain, dshift in zip(zip(self.gains, self.shifts), *zip(*norms)):
             gain.update(dgain, lr)
@@ -161,7 +221,7 @@ def train(model, data, steps, tokens, report=None):
         loss, entropy = model.step(*data.batch(tokens))
         losses.append(loss)
         if report and (i % 10 == 0 or i == steps - 1):
-            report(f"step {i:4d}  loss {float(loss):.4f}  entropy {float(entropy):.4f}")
+            report(f"step {i:4d}  loss {float(loss):.4f}" + ("" if entropy is None else f"  entropy {float(entropy):.4f}"))
     status = anvil.last_device_error()
     if status != anvil.OK:
         raise RuntimeError(f"device error {anvil.STATUS[status]}")
@@ -176,8 +236,12 @@ def main(argv=None):
     p.add_argument("--dim", type=int, default=768)
     p.add_argument("--hidden", type=int, default=2816)
     p.add_argument("--blocks", type=int, default=2)
+    p.add_argument("--gated", action="store_true", help="gated blocks")
+    p.add_argument("--fused-loss", action="store_true", help="head and loss as one operator")
+    p.add_argument("--adamw", type=int, choices=(8, 32), help="AdamW for head and norms, its moments in so many bits")
     a = p.parse_args(argv)
-    model, data = Model(a.vocab, a.dim, a.hidden, a.blocks), Data(a.vocab)
+    model = Model(a.vocab, a.dim, a.hidden, a.blocks, gated=a.gated, fused_loss=a.fused_loss, adamw=a.adamw)
+    data = Data(a.vocab)
     train(model, data, a.steps, a.tokens, report=print)
     token = 17 % a.vocab
     for following, best in model.generate(token, 4):
