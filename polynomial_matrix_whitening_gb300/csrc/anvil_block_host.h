@@ -310,7 +310,10 @@ inline void plan_both(int64_t rows1, int cols1, int64_t k1, bool few1, bool k_ma
     const double turn = turn_cycles(kb, epilogue1);
     const Start at = {rest ? static_cast<int>(PLAN_PAIRS - rest) : PLAN_PAIRS, rest ? turn : 0.0};
     const Plan p = plan_product(rows2, cols2, k2, false, false, epilogue2, at);
-    const double cost = full * turn + LEAVE_CYCLES + p.cost;
+    double cost = full * turn + LEAVE_CYCLES + p.cost;
+    // a last turn that is long beside the second product (a few tiles of a long contraction)
+    const double alone = (full + (rest ? 1 : 0)) * turn + LEAVE_CYCLES;
+    if (!few1 && alone > cost) cost = alone;
     if (cost >= first->cost + second->cost) return;
     set_whole(tiles, full * turn + LEAVE_CYCLES, first);
     *second = p;

@@ -84,16 +84,17 @@ __global__ void __launch_bounds__(GF_THREADS) gated_finish_kernel(const __grid_c
     float g[N], u[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        g[i] = __ldcs(part + i * PAIR_COLS);
-        u[i] = __ldcs(part + i * PAIR_COLS + GATED_COLS);
+        g[i] = i < rows ? __ldcs(part + i * PAIR_COLS) : 0.f;
+        u[i] = i < rows ? __ldcs(part + i * PAIR_COLS + GATED_COLS) : 0.f;
     }
     for (int s = 1; s < splits; ++s) {
         part += static_cast<size_t>(PAIR_ROWS) * PAIR_COLS;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            g[i] += __ldcs(part + i * PAIR_COLS);
-            u[i] += __ldcs(part + i * PAIR_COLS + GATED_COLS);
-        }
+        for (int i = 0; i < N; ++i)
+            if (i < rows) {
+                g[i] += __ldcs(part + i * PAIR_COLS);
+                u[i] += __ldcs(part + i * PAIR_COLS + GATED_COLS);
+            }
     }
     finish_gated<T, N>(p, g, u, static_cast<long long>(tr) * PAIR_ROWS + r0, rows, col);
 }

@@ -28,6 +28,18 @@ namespace {
 
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
 
+// 2^v, of results below 2^-126 0 (a relative error of 2^-22; the subnormal results would cost as much again).
+__device__ __forceinline__ float exp2_of(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t exp2_of(uint64_t v) {
+    float lo, hi;
+    f2_split(v, &lo, &hi);
+    return f2_make(exp2_of(lo), exp2_of(hi));
+}
+
 __device__ __forceinline__ long long target_of(const void* targets, int wide, long long row) {
     return wide ? static_cast<const long long*>(targets)[row] : static_cast<const int*>(targets)[row];
 }
@@ -70,10 +82,13 @@ struct StatsPair {
             for (int i = 4; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], v[i]);
             const float now = fmaxf(most, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
             const float base = now == -INFINITY ? 0.f : now * LOG2E;
-            float s[4] = {sum * power2(ref - base), 0.f, 0.f, 0.f};
+            const uint64_t by = f2_make(LOG2E, LOG2E), less = f2_make(-base, -base);
+            uint64_t s[2] = {f2_make(sum * exp2_of(ref - base), 0.f), 0};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i & 3] += power2(fmaf(v[i], LOG2E, -base));
-            sum = (s[0] + s[1]) + (s[2] + s[3]);
+            for (int i = 0; i < 32; i += 2) s[i / 2 & 1] = f2_add(s[i / 2 & 1], exp2_of(f2_fma(f2_make(v[i], v[i + 1]), by, less)));
+            float s0, s1;
+            f2_split(f2_add(s[0], s[1]), &s0, &s1);
+            sum = s0 + s1;
             most = now;
             ref = base;
         }
@@ -101,16 +116,18 @@ struct DlogitsPair {
     static constexpr bool MULTI = false, OWN = true, RANK_B = false, ONE_CHAIN = false;
     struct Row {
         float lse2, g;
+        uint32_t counts;  // all ones, or 0 where the gradient is 0 whatever the logits are
         int target;
     };
     static __device__ __forceinline__ Row load(const Params& p, const Unit& t, int r) {
         const long long row = static_cast<long long>(t.tr) * PAIR_ROWS + r;
-        Row x = {0.f, 0.f, -1};
+        Row x = {0.f, 0.f, 0u, -1};
         if (row < p.rows && target_of(p.targets, p.target64, row) >= 0) {
             const float lse = p.lse[row];
             if (lse != -INFINITY) {  // (no token of that row can be: its gradient is 0)
                 x.lse2 = lse * LOG2E;
                 x.g = p.grad[row] * *p.scale;
+                x.counts = x.g == 0.f ? 0u : 0xffffffffu;
                 x.target = relative_target(p, row);
             }
         }
@@ -130,15 +147,27 @@ struct DlogitsPair {
             for (int c = 0; c < COLS; c += 16) {
                 float v[16];
                 tmem_ld_16(ta + b * COLS + c, v);
-                const int hot = at - (b * COLS + c);
+                const uint64_t by = f2_make(LOG2E, LOG2E), less = f2_make(-row.lse2, -row.lse2), g = f2_make(row.g, row.g);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] = power2(fmaf(v[i], LOG2E, -row.lse2));
-                    if (row.target >= 0 && hot == i) v[i] -= 1.f;
-                    v[i] = row.g == 0.f ? 0.f : v[i] * row.g;
+                for (int i = 0; i < 16; i += 2) f2_split(exp2_of(f2_fma(f2_make(v[i], v[i + 1]), by, less)), &v[i], &v[i + 1]);
+                const int hot = at - (b * COLS + c);
+                if (row.target >= 0 && hot >= 0 && hot < 16) {  // one warp and sixteen columns in a hundred, of 50,000
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (hot == i) v[i] -= 1.f;
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) sts128(Staging<W>::addr(x.box, x.r, c / 8 + j), Elem<T>::pack(v + 8 * j));
+                for (int j = 0; j < 2; ++j) {
+                    uint64_t d[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = f2_mul(f2_make(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]), g);
+                    uint4 w = Elem<T>::pack_pairs(d);
+                    w.x &= row.counts;
+                    w.y &= row.counts;
+                    w.z &= row.counts;
+                    w.w &= row.counts;
+                    sts128(Staging<W>::addr(x.box, x.r, c / 8 + j), w);
+                }
             }
             if (b == N - 1) release_acc(x, tempty);
             // (the buffer's rows go on in eights: no box ends inside 16 bytes)
@@ -151,8 +180,24 @@ struct DlogitsPair {
 // through the sums.)
 __device__ __forceinline__ void join(float& ref, float& sum, float ref2, float sum2) {
     const float now = sum2 == 0.f ? ref : sum == 0.f ? ref2 : fmaxf(ref, ref2);
-    sum = (sum == 0.f ? 0.f : sum * power2(ref - now)) + (sum2 == 0.f ? 0.f : sum2 * power2(ref2 - now));
+    sum = (sum == 0.f ? 0.f : sum * exp2_of(ref - now)) + (sum2 == 0.f ? 0.f : sum2 * exp2_of(ref2 - now));
     ref = now;
+}
+
+// Eight values of every lane combined over the warp; lane l gets number l / 4's.
+template <class Op>
+__device__ __forceinline__ float gather8(float (&v)[8], int lane, Op op) {
+#pragma unroll
+    for (int half = 4, bit = 16; half > 0; half /= 2, bit /= 2) {
+        const bool upper = lane & bit;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float keep = upper ? v[i + half] : v[i], give = upper ? v[i] : v[i + half];
+            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+        }
+    }
+    v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 // Few rows: a thread has one column's logits of eight rows, a warp 32 columns, a block 128.
@@ -160,26 +205,25 @@ struct HeadRows {
     using Params = RowHeadParams;
     static constexpr bool GATED = false, HEAD = true;
     static __device__ __forceinline__ void finish(const Params& p, const float (&v)[8], int col, bool live, int row, int rows, float2* to) {
-        float m[8], s[8], ref[8];
+        // over the warp's columns: each exchange halves the rows that a lane goes on with, until lane l has
+        // row l / 4's, from where every lane gets all eight maxima
+        const int lane = threadIdx.x & 31;
+        float m[8], s[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) m[i] = live ? v[i] : -INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+        const float most = gather8(m, lane, [](float a, float b) { return fmaxf(a, b); });
+        const float mine = most == -INFINITY ? 0.f : most * LOG2E;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            ref[i] = m[i] == -INFINITY ? 0.f : m[i] * LOG2E;
-            s[i] = live ? power2(fmaf(v[i], LOG2E, -ref[i])) : 0.f;
+            const float ref = __shfl_sync(0xffffffffu, mine, 4 * i);
+            s[i] = live ? exp2_of(fmaf(v[i], LOG2E, -ref)) : 0.f;
         }
+        const float sum = gather8(s, lane, [](float a, float b) { return a + b; });
+        if (lane % 4 == 0) to[lane / 4] = make_float2(mine, sum);
+        if (p.hit) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if ((threadIdx.x & 31) == i) to[i] = make_float2(ref[i], s[i]);
-            if (p.hit && live && i < rows && target_of(p.targets, p.target64, row + i) == col) p.hit[row + i] = v[i];
+            for (int i = 0; i < 8; ++i)
+                if (live && i < rows && target_of(p.targets, p.target64, row + i) == col) p.hit[row + i] = v[i];
         }
     }
     static __device__ __forceinline__ void end(const Params& p, int block, int row, float2 a, float2 b, float2 c, float2 d) {
@@ -284,7 +328,7 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
             float s = 0.f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                if (row0 + g < p.cols) s += power2(fmaf(z[g], LOG2E, -base));
+                if (row0 + g < p.cols) s += exp2_of(fmaf(z[g], LOG2E, -base));
             join(ref, sum, base, s);
         }
     }

@@ -88,10 +88,28 @@ __device__ __forceinline__ void tail_sum(const TailSumParams& p, int block) {
         v[i] = __ldcs(part + i * PAIR_COLS);
         in[i] = e.in && i < rows ? Elem<T>::load(static_cast<const T*>(e.in)[(row + i) * e.ldin + col]) : 0.f;
     }
-    for (int s = 1; s < splits; ++s) {
-        part += static_cast<size_t>(PAIR_ROWS) * PAIR_COLS;
+    if constexpr (MULTI) {
+        // in order, four parts on their way at a time (one after the other, 64 parts of a few rows took 14 us)
+        constexpr size_t PART = static_cast<size_t>(PAIR_ROWS) * PAIR_COLS;
+        part += PART;
+        for (int s = 1; s < splits; s += 4, part += 4 * PART) {
+            float t[4][TAIL_ROWS];
 #pragma unroll
-        for (int i = 0; i < TAIL_ROWS; ++i) v[i] += __ldcs(part + i * PAIR_COLS);
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < TAIL_ROWS; ++i) t[k][i] = s + k < splits && i < rows ? __ldcs(part + k * PART + i * PAIR_COLS) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < TAIL_ROWS; ++i)
+                    if (s + k < splits) v[i] += t[k][i];
+        }
+    } else {
+        for (int s = 1; s < splits; ++s) {
+            part += static_cast<size_t>(PAIR_ROWS) * PAIR_COLS;
+#pragma unroll
+            for (int i = 0; i < TAIL_ROWS; ++i) v[i] += __ldcs(part + i * PAIR_COLS);
+        }
     }
     if (MULTI && e.scale) {
         const float scale = *e.scale;
