@@ -82,6 +82,7 @@ int kind_of(const anvil_adamw_tensor& t) {
     return param << 4 | t.grad_dtype << 2 | (t.scales ? 2 : 0) | (vec ? 1 : 0);
 }
 constexpr int KINDS = 64;
+constexpr int64_t FEW_BLOCKS = 152 * 8;  // a turn of the SMs' blocks
 bool dtype_ok(int d) { return d == ANVIL_F32 || d == ANVIL_BF16 || d == ANVIL_F16; }
 
 const Range step_range(const void* tensors, int i, int role) {
@@ -196,16 +197,20 @@ anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, c
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
+    int64_t blocks[KINDS] = {0};
+    for (int i = 0; i < ntensors; ++i)
+        if (tensors[i].count) blocks[kind_of(tensors[i])] += blocks_of(tensors[i].count);
     for (int kind = 0; kind < KINDS; ++kind) {
         if (!(kinds >> kind & 1)) continue;
+        // a few blocks on vector boundaries go with those that are not: a launch takes longer
+        const bool both = !(kind & 1) && blocks[kind | 1] <= FEW_BLOCKS;
+        if ((kind & 1) && blocks[kind & ~1] && blocks[kind] <= FEW_BLOCKS) continue;
         const int param = kind >> 4, grad = kind >> 2 & 3;
         const bool codes = kind >> 1 & 1, vec = kind & 1;
         auto launch = [&](const AdamwGroup& g) {
             return profiled(ANVIL_KERNEL_ADAMW, s, [&] { return launch_adamw(g, param, grad, codes, vec, s); });
         };
-        int64_t blocks = 0;
-        for (int i = 0; i < ntensors; ++i) blocks += tensors[i].count && kind_of(tensors[i]) == kind ? blocks_of(tensors[i].count) : 0;
-        Batches<decltype(launch)> batch(launch, blocks);
+        Batches<decltype(launch)> batch(launch, blocks[kind] + (both ? blocks[kind | 1] : 0));
         batch.g.p.beta1 = static_cast<float>(config->beta1);
         batch.g.p.c1 = static_cast<float>(1.0 - config->beta1);
         batch.g.p.beta2 = static_cast<float>(config->beta2);
@@ -215,7 +220,7 @@ anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, c
         batch.g.p.d_scalars = d_scalars;
         for (int i = 0; i < ntensors; ++i) {
             const anvil_adamw_tensor& t = tensors[i];
-            if (t.count == 0 || kind_of(t) != kind) continue;
+            if (t.count == 0 || (both ? kind_of(t) & ~1 : kind_of(t)) != kind) continue;
             if ((e = batch.add({t.param, t.mantissa, t.grad, t.exp_avg, t.exp_avg_sq, t.scales, t.count, 0})))
                 return cuda_fail(e, "AdamW launch");
         }
@@ -245,19 +250,21 @@ anvil_status anvil_adamw_values(const anvil_adamw_state* states, int nstates, vo
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    for (int vec = 0; vec < 2; ++vec) {
-        const auto of_kind = [vec](const anvil_adamw_state& t) {
-            return t.count && (vector(t.exp_avg, 1) && vector(t.exp_avg_sq, 1) && vector(t.m, 4) && vector(t.v, 4)) == (vec != 0);
-        };
+    const auto on_vectors = [](const anvil_adamw_state& t) {
+        return vector(t.exp_avg, 1) && vector(t.exp_avg_sq, 1) && vector(t.m, 4) && vector(t.v, 4);
+    };
+    int64_t blocks[2] = {0, 0};
+    for (int i = 0; i < nstates; ++i)
+        if (states[i].count) blocks[on_vectors(states[i])] += blocks_of(states[i].count);
+    const bool both = blocks[0] && blocks[1] <= FEW_BLOCKS;  // as above
+    for (int vec = 0; vec < (both ? 1 : 2); ++vec) {
         auto launch = [&](const AdamwGroup& g) {
             return profiled(ANVIL_KERNEL_ADAMW, s, [&] { return launch_adamw_values(g, vec != 0, s); });
         };
-        int64_t blocks = 0;
-        for (int i = 0; i < nstates; ++i) blocks += of_kind(states[i]) ? blocks_of(states[i].count) : 0;
-        Batches<decltype(launch)> batch(launch, blocks);
+        Batches<decltype(launch)> batch(launch, blocks[vec] + (both ? blocks[1] : 0));
         for (int i = 0; i < nstates; ++i) {
             const anvil_adamw_state& t = states[i];
-            if (!of_kind(t)) continue;
+            if (t.count == 0 || (!both && on_vectors(t) != (vec != 0))) continue;
             if ((e = batch.add({t.m, nullptr, t.v, const_cast<void*>(t.exp_avg), const_cast<void*>(t.exp_avg_sq),
                                 const_cast<float*>(t.scales), t.count, 0})))
                 return cuda_fail(e, "AdamW launch");
