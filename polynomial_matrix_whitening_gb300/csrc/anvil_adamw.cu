@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, CODES && VEC ? 4 : 3) adamw_kernel(co
         decay = a.d_scalars[2];
         grad_scale = a.d_scalars[3];
     }
-    // denominators from 2^-60 (eps) to 2^63 2^20 + eps
+    // denominators from 2^-60 (eps) to 2^13 2^20 + eps
     const bool middle = a.eps >= 8.67361738e-19f && a.eps <= 1.f && root >= 0.f && root <= 1048576.f;
     In in;  // of this block, and as soon as they are used, of the warp's next
     long long b = first + warp;
@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(THREADS, CODES && VEC ? 4 : 3) adamw_kernel(co
             most_m = most_bits<true>(m);
             most_v = most_bits<false>(v);
         }
-        // |m| below 2^100 and v below 2^126, no infinity or NaN among them
-        if (CODES && middle && most_m < (227u << 23) && most_v < (253u << 23)) {
+        // |m| below 2^60 (no quotient overflows) and v below 2^26, no infinity or NaN among them
+        if (CODES && middle && most_m < (187u << 23) && most_v < (153u << 23)) {
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 f2_split(f2_root(f2_make(v[i], v[i + 1])), &r[i], &r[i + 1]);

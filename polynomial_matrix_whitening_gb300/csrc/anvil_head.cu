@@ -389,8 +389,11 @@ __global__ void __launch_bounds__(1024) head_scale_kernel(const HeadScaleParams 
     pdl_allow_next();
     pdl_wait_previous();
     uint32_t most = 0;
-    for (long long i = threadIdx.x; i < p.rows; i += 1024)
-        if (target_of(p.targets, p.target64, i) >= 0) most = max(most, __float_as_uint(p.grad[i]) & 0x7fffffffu);
+#pragma unroll 8
+    for (long long i = threadIdx.x; i < p.rows; i += 1024) {
+        const uint32_t g = __float_as_uint(p.grad[i]) & 0x7fffffffu;
+        most = max(most, target_of(p.targets, p.target64, i) >= 0 ? g : 0u);
+    }
     most = __reduce_max_sync(0xffffffffu, most);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = most;
     __syncthreads();

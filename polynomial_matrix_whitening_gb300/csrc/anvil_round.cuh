@@ -7,8 +7,8 @@
 // rounded reciprocal y of b, q + (a - b q) y rounds to a / b, since the remainder a - b q is exact in
 // one fused operation; the square root's correction is g + (v - g g) h with h near 1 / (2 sqrt v).
 // Checked on the hardware: the reciprocal for every significand of b, the root for every significand
-// of v at either parity of the exponent (scaling by powers of four changes nothing else), the quotient for 2^36
-// pairs of significands: all the same as the correctly rounded operations.
+// of v at either parity of the exponent (scaling by powers of four changes nothing else) and every subnormal v,
+// the quotient for 2^36 pairs of significands: all the same as the correctly rounded operations.
 #pragma once
 
 #include <stdint.h>
@@ -29,8 +29,8 @@ __device__ __forceinline__ float approx_rsqrt(float v) {
     return r;
 }
 
-// (a.x / b.x, a.y / b.y) for b within 2^-60 to 2^90 and |a| within 2^-102 to 2^100, or a = 0.  (Below
-// 2^-102 the remainder is not exact: off by an ulp at most.)
+// (a.x / b.x, a.y / b.y) for b within 2^-60 to 2^90 and |a| within 2^-102 to 2^60, or a = 0.  (Below
+// 2^-102, and where the quotient is below 2^-126, the remainder is not exact: off by two ulps at most.)
 __device__ __forceinline__ uint64_t f2_divide(uint64_t a, uint64_t b) {
     const uint64_t one = f2_make(1.f, 1.f), nb = f2_neg(b);
     float b0, b1;
@@ -42,18 +42,20 @@ __device__ __forceinline__ uint64_t f2_divide(uint64_t a, uint64_t b) {
     return f2_fma(f2_fma(nb, q, a), y, q);
 }
 
-// (sqrt v.x, sqrt v.y) for v within 2^-101 to 2^126, or 0.  (Below 2^-101 off by an ulp at most.)
+// (sqrt v.x, sqrt v.y) for v from the smallest value to 2^26, or 0: of 2^100 v, which is exact and in the
+// middle of the range.
 __device__ __forceinline__ uint64_t f2_root(uint64_t v) {
+    v = f2_mul(v, f2_make(0x1p100f, 0x1p100f));
     float v0, v1;
     f2_split(v, &v0, &v1);
-    const float least = 1.17549435e-38f;  // of 0 the approximation is infinite: 0 times this one's is 0
+    const float least = 0x1p-60f;  // of 0 the approximation is infinite: 0 times this one's is 0
     const uint64_t half = f2_make(0.5f, 0.5f);
     const uint64_t y = f2_make(approx_rsqrt(fmaxf(v0, least)), approx_rsqrt(fmaxf(v1, least)));
     uint64_t g = f2_mul(v, y), h = f2_mul(y, half);
     const uint64_t r = f2_fma(f2_neg(g), h, half);
     g = f2_fma(g, r, g);
     h = f2_fma(h, r, h);
-    return f2_fma(f2_fma(f2_neg(g), g, v), h, g);
+    return f2_mul(f2_fma(f2_fma(f2_neg(g), g, v), h, g), f2_make(0x1p-50f, 0x1p-50f));
 }
 
 }  // namespace anvil

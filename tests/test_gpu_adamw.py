@@ -194,6 +194,35 @@ def test_step_against_64_bits(A, param, grad):
     assert (np.abs(c.master() - p) <= bar * (1 + 1e-6)).all()
 
 
+@pytest.mark.parametrize("eps", [1e-8, 0.0, 1e-20, 1e-30, 0.5, 100.0])
+def test_extremes_bit_for_bit(A, eps):
+    """Moments and gradients from 1e-30 to 1e30 and zeros, roots that belong to other moments, denominators of
+    eps alone: quotients from 0 to infinity, as numpy has them.  (Where 8-bit states leave the middle
+    of the range: |m| below 2^-102 is a last bit of nothing, so no value here is between 0 and 1e-30.)"""
+    for bits in (8, 32):
+        c = Case(A, 21, 256 * 40, "f32", "f32", bits)
+        rng = np.random.default_rng(22)
+        wide = lambda: (rng.choice([-1.0, 1.0], 256 * 40) * 10.0 ** np.repeat(rng.uniform(-30, 30, 40), 256)  # noqa: E731
+                        * 10.0 ** rng.uniform(-1, 0, 256 * 40) * (rng.random(256 * 40) < 0.9)).astype(F)
+        m, r, g = wide(), np.abs(wide()), wide()
+        g[:256 * 20] = 0.0
+        r = np.minimum(r, F(1e18))  # (squares stay finite)
+        g = np.clip(g, F(-1e18), F(1e18))
+        c.g.copy_(torch.from_numpy(g))
+        if bits == 32:
+            c.m.copy_(torch.from_numpy(m))
+            c.v.copy_(torch.from_numpy(np.square(r)))
+        else:
+            (mc, ms), (rc, rs) = encode(m, False), encode(r, True)
+            c.m.copy_(torch.from_numpy(mc).view(torch.float8_e4m3fn))
+            c.v.copy_(torch.from_numpy(rc))
+            c.scales.copy_(torch.from_numpy(np.stack([ms, rs])))
+        hp = dict(HP, eps=eps)
+        want = c.expect(A, hp)
+        run(A, [c], hp)
+        c.check(want, (bits, eps))
+
+
 def test_steps_in_a_row(A):
     """Ten steps of 8-bit states from zero, each from what the last one left."""
     c = Case(A, 7, 5000, "f32", "f32", 8)
