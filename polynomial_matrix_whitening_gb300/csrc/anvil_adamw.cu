@@ -40,14 +40,15 @@ constexpr float SMALLEST = 7.8886090522101181e-31f;  // 2^-100
 
 // Eight values of a lane from an array of 4-, 2- or 1-byte elements, as they were loaded: nothing
 // uses them before they are needed, so a block's loads are on their way while the one before it is
-// computed.  VEC: every whole block is on vector boundaries, four neighbours at a time.  Otherwise,
-// and in a tensor's last block, one by one (what is at `left` and beyond reads as 0).
+// computed.  VEC: whole blocks are on vector boundaries, four neighbours at a time.  Otherwise,
+// and in a tensor's last block (not WHOLE), one by one (what is at `left` and beyond reads as 0).
 template <typename E, bool VEC>
 struct Eight {
     static constexpr int W = VEC ? 2 * sizeof(E) : 8;  // words
     uint32_t w[W];
+    template <bool WHOLE>
     __device__ __forceinline__ void load(const E* p, int lane, int left) {
-        if (VEC && left == ADAMW_BLOCK) {
+        if constexpr (VEC && WHOLE) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const E* q = p + h * 128 + lane * 4;
@@ -69,7 +70,7 @@ struct Eight {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t x = i * 32 + lane < left ? static_cast<uint32_t>(__ldcs(p + i * 32 + lane)) : 0u;
+            const uint32_t x = WHOLE || i * 32 + lane < left ? static_cast<uint32_t>(__ldcs(p + i * 32 + lane)) : 0u;
             if constexpr (VEC) w[i * sizeof(E) / 4] |= x << (i * sizeof(E) % 4 * 8);
             else w[i] = x;
         }
@@ -79,9 +80,9 @@ struct Eight {
         else return static_cast<E>(w[i]);
     }
 };
-template <bool VEC, typename E>
+template <bool VEC, bool WHOLE, typename E>
 __device__ __forceinline__ void store8(E* p, int lane, int left, const E (&v)[8]) {
-    if (VEC && left == ADAMW_BLOCK) {
+    if constexpr (VEC && WHOLE) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             E* q = p + h * 128 + lane * 4;
@@ -99,7 +100,7 @@ __device__ __forceinline__ void store8(E* p, int lane, int left, const E (&v)[8]
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i * 32 + lane < left) __stcs(p + i * 32 + lane, v[i]);
+            if (WHOLE || i * 32 + lane < left) __stcs(p + i * 32 + lane, v[i]);
     }
 }
 
@@ -213,158 +214,182 @@ struct Inputs {
     Eight<S, VEC> m, v;
     float ms, rs;
     // gradient and moments, and the parameter: apart, since they are used at different times
+    template <bool WHOLE>
     __device__ __forceinline__ void load_moments(const AdamwTensor& t, long long block, long long blocks, int lane) {
         const long long at = block * ADAMW_BLOCK;
-        const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
-        g.load(static_cast<const typename G::type*>(t.g) + at, lane, left);
-        m.load(static_cast<const S*>(t.m) + at, lane, left);
-        v.load(static_cast<const S*>(t.v) + at, lane, left);
+        const int left = WHOLE ? ADAMW_BLOCK : static_cast<int>(t.count - at);
+        g.template load<WHOLE>(static_cast<const typename G::type*>(t.g) + at, lane, left);
+        m.template load<WHOLE>(static_cast<const S*>(t.m) + at, lane, left);
+        v.template load<WHOLE>(static_cast<const S*>(t.v) + at, lane, left);
         if constexpr (CODES) {
             ms = t.scales[block];
             rs = t.scales[blocks + block];
         }
     }
+    template <bool WHOLE>
     __device__ __forceinline__ void load_param(const AdamwTensor& t, long long block, int lane) {
         const long long at = block * ADAMW_BLOCK;
-        const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
-        p.load(static_cast<const typename P::type*>(t.p) + at, lane, left);
-        if constexpr (SPLIT) low.load(t.low + at, lane, left);
+        const int left = WHOLE ? ADAMW_BLOCK : static_cast<int>(t.count - at);
+        p.template load<WHOLE>(static_cast<const typename P::type*>(t.p) + at, lane, left);
+        if constexpr (SPLIT) low.template load<WHOLE>(t.low + at, lane, left);
     }
 };
+struct Constants {
+    float beta1, c1, beta2, c2, eps, step_size, root, decay, grad_scale;
+    bool middle;  // denominators from 2^-60 (eps) to 2^13 2^20 + eps
+};
 
-// With fp32 states the kernel waits for memory (50M split bf16 values 190 us, 6.8 TB/s).  With codes it is
-// short of instructions (98 a value, at 80% of the issue slots, in its first form; 78 in this one): quotients
-// and roots there are pairs without the general ones' branches (where a lane's values are in the
-// middle of the range), and of the two scales each half of the warp divides for one.  134M fp32 values: 543 us
-// with the general operations, 400 now, 5.4 TB/s.
-template <int PARAM, int GRAD, bool CODES, bool VEC, int N>
-__global__ void __launch_bounds__(THREADS, CODES && VEC ? 4 : 3) adamw_kernel(const __grid_constant__ AdamwParams<N> a) {
+// One block's step from what `in` holds; as soon as that is used, what block `next` (whole; -1: none) needs
+// takes its place.
+template <int PARAM, int GRAD, bool CODES, bool VEC, bool WHOLE>
+__device__ __forceinline__ void adamw_block(const AdamwTensor& t, const Constants& a, Inputs<PARAM, GRAD, CODES, VEC>& in, long long b,
+                                            long long next, long long blocks, int lane) {
     using In = Inputs<PARAM, GRAD, CODES, VEC>;
     using P = typename In::P;
     using G = typename In::G;
     constexpr bool SPLIT = In::SPLIT;
+    const long long at = b * ADAMW_BLOCK;
+    const int left = WHOLE ? ADAMW_BLOCK : static_cast<int>(t.count - at);
+    float m[8], v[8], r[8], u[8];
+    if constexpr (CODES) {
+        e4m3_values(in.m, m);
+        times8(m, in.ms);
+        root_values(in.v, v);
+        times8(v, __fmul_rn(in.rs, ROOT_UNIT));
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const uint64_t x = f2_make(v[i], v[i + 1]);
+            f2_split(f2_mul(x, x), &v[i], &v[i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i] = __uint_as_float(in.m[i]);
+            v[i] = __uint_as_float(in.v[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float g = __fmul_rn(G::value(in.g[i]), a.grad_scale);
+        m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(g, a.c1));
+        v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(g, a.c2), g));
+    }
+    if (next >= 0) in.template load_moments<true>(t, next, blocks, lane);
+    if constexpr (CODES && !WHOLE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i * 32 + lane >= left) m[i] = v[i] = 0.f;  // behind the tensor's end
+    }
+    uint32_t most_m = 0, most_v = 0;
+    if constexpr (CODES) {
+        most_m = most_bits<true>(m);
+        most_v = most_bits<false>(v);
+    }
+    // |m| below 2^60 (no quotient overflows) and v below 2^26, no infinity or NaN among them
+    if (CODES && a.middle && most_m < (187u << 23) && most_v < (153u << 23)) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            f2_split(f2_root(f2_make(v[i], v[i + 1])), &r[i], &r[i + 1]);
+            const uint64_t d = f2_make(__fadd_rn(__fmul_rn(r[i], a.root), a.eps), __fadd_rn(__fmul_rn(r[i + 1], a.root), a.eps));
+            f2_split(f2_divide(f2_make(m[i], m[i + 1]), d), &u[i], &u[i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r[i] = __fsqrt_rn(v[i]);
+            u[i] = __fdiv_rn(m[i], __fadd_rn(__fmul_rn(r[i], a.root), a.eps));
+        }
+    }
+    typename P::type pw[8];
+    uint16_t low[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float p;
+        if constexpr (SPLIT) p = __uint_as_float(static_cast<uint32_t>(in.p[i]) << 16 | in.low[i]);
+        else p = P::value(in.p[i]);
+        p = __fsub_rn(__fmul_rn(p, a.decay), __fmul_rn(u[i], a.step_size));
+        if constexpr (SPLIT) {
+            const uint32_t bits = __float_as_uint(p);
+            pw[i] = bits >> 16;
+            low[i] = bits & 0xffffu;
+        } else {
+            pw[i] = P::word(p);
+        }
+    }
+    if (next >= 0) in.template load_param<true>(t, next, lane);
+    store8<VEC, WHOLE>(static_cast<typename P::type*>(t.p) + at, lane, left, pw);
+    if constexpr (SPLIT) store8<VEC, WHOLE>(t.low + at, lane, left, low);
+    if constexpr (CODES) {
+        // the scales (the largest root is the largest v's), and what the values are multiplied by for their codes
+        most_m = __reduce_max_sync(0xffffffffu, most_m);
+        most_v = __reduce_max_sync(0xffffffffu, most_v);
+        float fm = __uint_as_float(most_m), fr, im, ir;
+        // |m| and v where the pair's root and quotients reach (the same for the whole warp)
+        if (most_m >= (67u << 23) && most_m < (187u << 23) && most_v >= (37u << 23) && most_v < (153u << 23)) {
+            float other;
+            f2_split(f2_root(f2_make(__uint_as_float(most_v), 0.f)), &fr, &other);
+            f2_split(f2_divide(f2_make(TOP_M, TOP_R), f2_make(fm, fr)), &im, &ir);
+        } else {
+            fr = __fsqrt_rn(__uint_as_float(most_v));
+            if (fm < SMALLEST) fm = 0.f;
+            if (fr < SMALLEST) fr = 0.f;
+            im = fm > 0.f ? __fdiv_rn(TOP_M, fm) : 0.f;
+            ir = fr > 0.f ? __fdiv_rn(TOP_R, fr) : 0.f;
+        }
+        if (lane < 2) t.scales[lane ? blocks + b : b] = lane ? __fmul_rn(fr, 1.f / TOP_R) : __fmul_rn(fm, 1.f / TOP_M);
+        uint8_t c[8];
+        times8(m, im);
+        e4m3_codes(m, c);
+        store8<VEC, WHOLE>(static_cast<uint8_t*>(t.m) + at, lane, left, c);
+        times8(r, ir);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = static_cast<uint8_t>(root_code(r[i]));
+        store8<VEC, WHOLE>(static_cast<uint8_t*>(t.v) + at, lane, left, c);
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(m[i]);
+        store8<VEC, WHOLE>(static_cast<uint32_t*>(t.m) + at, lane, left, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+        store8<VEC, WHOLE>(static_cast<uint32_t*>(t.v) + at, lane, left, w);
+    }
+}
+
+// With fp32 states the kernel waits for memory (50M split bf16 values 190 us, 6.8 TB/s).  With codes it is
+// short of instructions (98 a value, at 80% of the issue slots, in its first form): quotients and roots
+// there are pairs without the general ones' branches (where a lane's values are in the middle of the
+// range), and a tensor's last block, the only one with bounds, is apart.  134M fp32 values: 470 us in the
+// first form, 365 now (5.9 TB/s); four blocks an SM, three where their registers are needed (with codes 3 gives 405).
+template <int PARAM, int GRAD, bool CODES, bool VEC, int N>
+__global__ void __launch_bounds__(THREADS, CODES && VEC ? 4 : 3) adamw_kernel(const __grid_constant__ AdamwParams<N> p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const AdamwTensor& t = a.t[tensor_of(a, blockIdx.x)];
+    const AdamwTensor& t = p.t[tensor_of(p, blockIdx.x)];
     const long long blocks = (t.count + ADAMW_BLOCK - 1) / ADAMW_BLOCK;
-    const long long first = static_cast<long long>(blockIdx.x - t.chunk0) * a.chunk, end = min(blocks, first + a.chunk);
+    const long long first = static_cast<long long>(blockIdx.x - t.chunk0) * p.chunk, end = min(blocks, first + p.chunk);
+    const long long whole = min(t.count / ADAMW_BLOCK, end);
     pdl_allow_next();
     pdl_wait_previous();
-    float step_size = a.scalars[0], root = a.scalars[1], decay = a.scalars[2], grad_scale = a.scalars[3];
-    if (a.d_scalars) {
-        step_size = a.d_scalars[0];
-        root = a.d_scalars[1];
-        decay = a.d_scalars[2];
-        grad_scale = a.d_scalars[3];
+    Constants a = {p.beta1, p.c1, p.beta2, p.c2, p.eps, p.scalars[0], p.scalars[1], p.scalars[2], p.scalars[3], false};
+    if (p.d_scalars) {
+        a.step_size = p.d_scalars[0];
+        a.root = p.d_scalars[1];
+        a.decay = p.d_scalars[2];
+        a.grad_scale = p.d_scalars[3];
     }
-    // denominators from 2^-60 (eps) to 2^13 2^20 + eps
-    const bool middle = a.eps >= 8.67361738e-19f && a.eps <= 1.f && root >= 0.f && root <= 1048576.f;
-    In in;  // of this block, and as soon as they are used, of the warp's next
+    a.middle = a.eps >= 0x1p-60f && a.eps <= 1.f && a.root >= 0.f && a.root <= 0x1p20f;
+    Inputs<PARAM, GRAD, CODES, VEC> in;
     long long b = first + warp;
-    if (b < end) {
-        in.load_moments(t, b, blocks, lane);
-        in.load_param(t, b, lane);
+    if (b < whole) {
+        in.template load_moments<true>(t, b, blocks, lane);
+        in.template load_param<true>(t, b, lane);
     }
 #pragma unroll 1
-    for (; b < end; b += WARPS) {
-        const long long at = b * ADAMW_BLOCK;
-        const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
-        float m[8], v[8], r[8], u[8];
-        if constexpr (CODES) {
-            e4m3_values(in.m, m);
-            times8(m, in.ms);
-            root_values(in.v, v);
-            times8(v, __fmul_rn(in.rs, ROOT_UNIT));
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const uint64_t x = f2_make(v[i], v[i + 1]);
-                f2_split(f2_mul(x, x), &v[i], &v[i + 1]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m[i] = __uint_as_float(in.m[i]);
-                v[i] = __uint_as_float(in.v[i]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float g = __fmul_rn(G::value(in.g[i]), grad_scale);
-            m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(g, a.c1));
-            v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(g, a.c2), g));
-        }
-        if (b + WARPS < end) in.load_moments(t, b + WARPS, blocks, lane);
-        if (CODES && left < ADAMW_BLOCK) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i * 32 + lane >= left) m[i] = v[i] = 0.f;  // behind the tensor's end
-        }
-        uint32_t most_m = 0, most_v = 0;
-        if constexpr (CODES) {
-            most_m = most_bits<true>(m);
-            most_v = most_bits<false>(v);
-        }
-        // |m| below 2^60 (no quotient overflows) and v below 2^26, no infinity or NaN among them
-        if (CODES && middle && most_m < (187u << 23) && most_v < (153u << 23)) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                f2_split(f2_root(f2_make(v[i], v[i + 1])), &r[i], &r[i + 1]);
-                const uint64_t d = f2_make(__fadd_rn(__fmul_rn(r[i], root), a.eps), __fadd_rn(__fmul_rn(r[i + 1], root), a.eps));
-                f2_split(f2_divide(f2_make(m[i], m[i + 1]), d), &u[i], &u[i + 1]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                r[i] = __fsqrt_rn(v[i]);
-                u[i] = __fdiv_rn(m[i], __fadd_rn(__fmul_rn(r[i], root), a.eps));
-            }
-        }
-        typename P::type pw[8];
-        uint16_t low[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float p;
-            if constexpr (SPLIT) p = __uint_as_float(static_cast<uint32_t>(in.p[i]) << 16 | in.low[i]);
-            else p = P::value(in.p[i]);
-            p = __fsub_rn(__fmul_rn(p, decay), __fmul_rn(u[i], step_size));
-            if constexpr (SPLIT) {
-                const uint32_t bits = __float_as_uint(p);
-                pw[i] = bits >> 16;
-                low[i] = bits & 0xffffu;
-            } else {
-                pw[i] = P::word(p);
-            }
-        }
-        if (b + WARPS < end) in.load_param(t, b + WARPS, lane);
-        store8<VEC>(static_cast<typename P::type*>(t.p) + at, lane, left, pw);
-        if constexpr (SPLIT) store8<VEC>(t.low + at, lane, left, low);
-        if constexpr (CODES) {
-            // each half of the warp finds one moment's scale (the largest root is the largest v's), and
-            // what its values are multiplied by for their codes
-            most_m = __reduce_max_sync(0xffffffffu, most_m);
-            most_v = __reduce_max_sync(0xffffffffu, most_v);
-            const bool second = lane >= 16;
-            float most = second ? __fsqrt_rn(__uint_as_float(most_v)) : __uint_as_float(most_m);
-            if (most < SMALLEST) most = 0.f;
-            const float top = second ? TOP_R : TOP_M;
-            const float inverse = most > 0.f ? __fdiv_rn(top, most) : 0.f;
-            if ((lane & 15) == 0) t.scales[second ? blocks + b : b] = __fmul_rn(most, second ? 1.f / TOP_R : 1.f / TOP_M);
-            uint8_t c[8];
-            times8(m, __shfl_sync(0xffffffffu, inverse, 0));
-            e4m3_codes(m, c);
-            store8<VEC>(static_cast<uint8_t*>(t.m) + at, lane, left, c);
-            times8(r, __shfl_sync(0xffffffffu, inverse, 16));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = static_cast<uint8_t>(root_code(r[i]));
-            store8<VEC>(static_cast<uint8_t*>(t.v) + at, lane, left, c);
-        } else {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(m[i]);
-            store8<VEC>(static_cast<uint32_t*>(t.m) + at, lane, left, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
-            store8<VEC>(static_cast<uint32_t*>(t.v) + at, lane, left, w);
-        }
+    for (; b < whole; b += WARPS) adamw_block<PARAM, GRAD, CODES, VEC, true>(t, a, in, b, b + WARPS < whole ? b + WARPS : -1, blocks, lane);
+    if (b < end) {  // the block behind the whole ones
+        in.template load_moments<false>(t, b, blocks, lane);
+        in.template load_param<false>(t, b, lane);
+        adamw_block<PARAM, GRAD, CODES, VEC, false>(t, a, in, b, -1, blocks, lane);
     }
 }
 
@@ -377,38 +402,47 @@ __global__ void __launch_bounds__(THREADS) adamw_values_kernel(const __grid_cons
     const long long first = static_cast<long long>(blockIdx.x - t.chunk0) * a.chunk, end = min(blocks, first + a.chunk);
     pdl_allow_next();
     pdl_wait_previous();
+    const long long whole = min(t.count / ADAMW_BLOCK, end);
     struct In {
         Eight<uint8_t, VEC> m, v;
         float ms, rs;
     } now, next;
-    const auto load = [&](long long b, In& in) {
+    const auto load = [&](auto is_whole, long long b, In& in) {
+        constexpr bool WHOLE = decltype(is_whole)::value;
         const long long at = b * ADAMW_BLOCK;
-        const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
-        in.m.load(static_cast<const uint8_t*>(t.m) + at, lane, left);
-        in.v.load(static_cast<const uint8_t*>(t.v) + at, lane, left);
+        in.m.template load<WHOLE>(static_cast<const uint8_t*>(t.m) + at, lane, static_cast<int>(t.count - at));
+        in.v.template load<WHOLE>(static_cast<const uint8_t*>(t.v) + at, lane, static_cast<int>(t.count - at));
         in.ms = t.scales[b];
         in.rs = t.scales[blocks + b];
     };
-    long long b = first + warp;
-    if (b < end) load(b, next);
-#pragma unroll 1
-    for (; b < end; b += WARPS) {
-        now = next;
-        if (b + WARPS < end) load(b + WARPS, next);
+    const auto send = [&](auto is_whole, long long b, const In& in) {
+        constexpr bool WHOLE = decltype(is_whole)::value;
         const long long at = b * ADAMW_BLOCK;
-        const int left = static_cast<int>(min(t.count - at, static_cast<long long>(ADAMW_BLOCK)));
+        const int left = static_cast<int>(t.count - at);
         float m[8];
         uint32_t w[8];
-        e4m3_values(now.m, m);
-        times8(m, now.ms);
+        e4m3_values(in.m, m);
+        times8(m, in.ms);
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(m[i]);
-        store8<VEC>(static_cast<uint32_t*>(t.p) + at, lane, left, w);
-        root_values(now.v, m);
-        times8(m, __fmul_rn(now.rs, ROOT_UNIT));
+        store8<VEC, WHOLE>(static_cast<uint32_t*>(t.p) + at, lane, left, w);
+        root_values(in.v, m);
+        times8(m, __fmul_rn(in.rs, ROOT_UNIT));
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__fmul_rn(m[i], m[i]));
-        store8<VEC>(static_cast<uint32_t*>(const_cast<void*>(t.g)) + at, lane, left, w);
+        store8<VEC, WHOLE>(static_cast<uint32_t*>(const_cast<void*>(t.g)) + at, lane, left, w);
+    };
+    long long b = first + warp;
+    if (b < whole) load(std::true_type(), b, next);
+#pragma unroll 1
+    for (; b < whole; b += WARPS) {
+        now = next;
+        if (b + WARPS < whole) load(std::true_type(), b + WARPS, next);
+        send(std::true_type(), b, now);
+    }
+    if (b < end) {
+        load(std::false_type(), b, now);
+        send(std::false_type(), b, now);
     }
 }
 
