@@ -23,28 +23,41 @@ int64_t blocks_of(int64_t count) { return (count + ADAMW_BLOCK - 1) / ADAMW_BLOC
 
 // The ranges of one array of every tensor (its role), in order of their addresses.
 struct Role {
-    Range* r;
+    Range *r, *end;
     bool written;
 };
-// No written range shares a byte with any other: a sweep over the roles' ranges, merged.
-bool disjoint(Role* roles, int nroles, int n) {
+// No written range shares a byte with any other.  The arrays of a role are often neighbours in one
+// buffer; otherwise a sweep over all ranges, the roles merged.
+bool disjoint(Role* roles, int nroles) {
+    const auto below = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+    bool apart = true;
     for (int i = 0; i < nroles; ++i) {
-        const auto below = [](const Range& a, const Range& b) { return a.lo < b.lo; };
-        if (!std::is_sorted(roles[i].r, roles[i].r + n, below)) std::sort(roles[i].r, roles[i].r + n, below);
-    }
-    int at[8] = {0};
-    uintptr_t written = 0, read = 0;  // ends of what has been passed
-    for (;;) {
-        int k = -1;
-        for (int i = 0; i < nroles; ++i) {
-            while (at[i] < n && roles[i].r[at[i]].lo == roles[i].r[at[i]].hi) ++at[i];  // (absent or empty)
-            if (at[i] < n && (k < 0 || roles[i].r[at[i]].lo < roles[k].r[at[k]].lo)) k = i;
+        Role& x = roles[i];
+        if (!std::is_sorted(x.r, x.end, below)) std::sort(x.r, x.end, below);
+        if (x.r == x.end) continue;
+        uintptr_t hi = x.r->hi;
+        for (const Range* q = x.r + 1; q < x.end; ++q) {
+            if (x.written && q->lo < hi) return false;
+            if (q->hi > hi) hi = q->hi;
         }
-        if (k < 0) return true;
-        const Range& x = roles[k].r[at[k]++];
-        if (x.lo < written || (roles[k].written && x.lo < read)) return false;
-        uintptr_t& end = roles[k].written ? written : read;
-        if (x.hi > end) end = x.hi;
+        for (int k = 0; k < i; ++k)
+            if (roles[k].r != roles[k].end && overlap({x.r->lo, hi}, {roles[k].r->lo, (roles[k].end - 1)->hi})) apart = false;
+        (x.end - 1)->hi = hi;  // (a read range may end before an earlier one)
+    }
+    if (apart) return true;
+    uintptr_t written = 0, read = 0;  // ends of what has been passed
+    uintptr_t next[8];
+    for (int i = 0; i < nroles; ++i) next[i] = roles[i].r != roles[i].end ? roles[i].r->lo : UINTPTR_MAX;
+    for (;;) {
+        int k = 0;
+        for (int i = 1; i < nroles; ++i)
+            if (next[i] < next[k]) k = i;
+        if (next[k] == UINTPTR_MAX) return true;
+        Role& x = roles[k];
+        if (x.r->lo < written || (x.written && x.r->lo < read)) return false;
+        uintptr_t& end = x.written ? written : read;
+        if (x.r->hi > end) end = x.r->hi;
+        next[k] = ++x.r != x.end ? x.r->lo : UINTPTR_MAX;
     }
 }
 Range range(const void* p, int64_t bytes) {
@@ -53,7 +66,8 @@ Range range(const void* p, int64_t bytes) {
 }
 
 constexpr int ROLES = 6;
-anvil_status check_ranges(const Range (*get)(const void*, int, int), const void* tensors, int n, const bool (&written)[ROLES]) {
+template <class T, class Get>
+anvil_status check_ranges(const T* tensors, int n, const bool (&written)[ROLES], Get get) {
     Range* all = new (std::nothrow) Range[static_cast<size_t>(n) * ROLES];
     if (!all) {
         set_error_text("out of host memory");
@@ -61,10 +75,14 @@ anvil_status check_ranges(const Range (*get)(const void*, int, int), const void*
     }
     Role roles[ROLES];
     for (int k = 0; k < ROLES; ++k) {
-        roles[k] = {all + static_cast<size_t>(k) * n, written[k]};
-        for (int i = 0; i < n; ++i) roles[k].r[i] = get(tensors, i, k);
+        Range* to = all + static_cast<size_t>(k) * n;
+        roles[k] = {to, to, written[k]};
+        for (int i = 0; i < n; ++i) {
+            const Range r = get(tensors[i], k);
+            if (r.lo < r.hi) *roles[k].end++ = r;  // (others are absent or empty)
+        }
     }
-    const bool ok = disjoint(roles, ROLES, n);
+    const bool ok = disjoint(roles, ROLES);
     delete[] all;
     return ok ? ANVIL_OK : ANVIL_ERR_ALIAS;
 }
@@ -85,8 +103,7 @@ constexpr int KINDS = 64;
 constexpr int64_t FEW_BLOCKS = 152 * 8;  // a turn of the SMs' blocks
 bool dtype_ok(int d) { return d == ANVIL_F32 || d == ANVIL_BF16 || d == ANVIL_F16; }
 
-const Range step_range(const void* tensors, int i, int role) {
-    const anvil_adamw_tensor& t = static_cast<const anvil_adamw_tensor*>(tensors)[i];
+Range step_range(const anvil_adamw_tensor& t, int role) {
     const int es = t.scales ? 1 : 4;
     switch (role) {
         case 0: return range(t.param, t.count * size_of(t.param_dtype));
@@ -97,8 +114,7 @@ const Range step_range(const void* tensors, int i, int role) {
         default: return range(t.scales, blocks_of(t.count) * 8);
     }
 }
-const Range values_range(const void* tensors, int i, int role) {
-    const anvil_adamw_state& t = static_cast<const anvil_adamw_state*>(tensors)[i];
+Range values_range(const anvil_adamw_state& t, int role) {
     switch (role) {
         case 0: return range(t.exp_avg, t.count);
         case 1: return range(t.exp_avg_sq, t.count);
@@ -186,12 +202,12 @@ anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, c
     }
     if (!kinds) return ANVIL_OK;
     const bool written[ROLES] = {true, true, false, true, true, true};
-    if ((st = check_ranges(step_range, tensors, ntensors, written)) != ANVIL_OK) return st;
+    if ((st = check_ranges(tensors, ntensors, written, step_range)) != ANVIL_OK) return st;
     if (d_scalars) {
         const Range s = range(d_scalars, 16);
         for (int i = 0; i < ntensors; ++i)
             for (int k = 0; k < ROLES; ++k)
-                if (written[k] && tensors[i].count && overlap(s, step_range(tensors, i, k))) return ANVIL_ERR_ALIAS;
+                if (written[k] && tensors[i].count && overlap(s, step_range(tensors[i], k))) return ANVIL_ERR_ALIAS;
     }
     DeviceState* dev = nullptr;
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;
@@ -244,7 +260,7 @@ anvil_status anvil_adamw_values(const anvil_adamw_state* states, int nstates, vo
     }
     if (!any) return ANVIL_OK;
     const bool written[ROLES] = {false, false, false, true, true, false};
-    anvil_status st = check_ranges(values_range, states, nstates, written);
+    anvil_status st = check_ranges(states, nstates, written, values_range);
     if (st != ANVIL_OK) return st;
     DeviceState* dev = nullptr;
     if ((st = device_setup(&dev)) != ANVIL_OK) return st;

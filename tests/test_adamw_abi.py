@@ -123,3 +123,26 @@ def test_binding_refusals():
         anvil.adamw_step([p], [p], [p], [p], 1e-3, "first")
     anvil.adamw_step([], [], [], [], 1e-3, 1)
     assert anvil.adamw_values([], [], []) == ([], [])
+
+
+def test_refusals_among_many_tensors():
+    """Tensors in any order of addresses, arrays of all roles between each other: one overlap among them is found."""
+    import random
+    rng = random.Random(5)
+    slots = list(range(1, 4 * 40 + 1))
+    rng.shuffle(slots)
+
+    def tensors(**kw):
+        it = iter(slots)
+        at = [[next(it) << 20 for _ in range(4)] for _ in range(40)]
+        made = [tensor(param=a, grad=b, exp_avg=c, exp_avg_sq=d, count=1000) for a, b, c, d in at]
+        for k, v in kw.items():
+            setattr(made[17], k, v)
+        return made
+    for other in (3, 16, 18, 39):
+        for field in ("param", "grad", "exp_avg", "exp_avg_sq"):
+            lo = getattr(tensors()[other], field)
+            assert step(tensors(param=lo + 3996)) == anvil.ERR_ALIAS
+            assert step(tensors(exp_avg=lo - 3996)) == anvil.ERR_ALIAS
+            if field != "grad":
+                assert step(tensors(grad=lo + 8)) == anvil.ERR_ALIAS
