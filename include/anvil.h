@@ -564,7 +564,7 @@ typedef struct {
     int weight_transposed;
     int accumulate;
 } anvil_head_grad_desc;
-/* Scratch: d for a piece (256 MB, or 512 bytes a row where that is more), dx's fp32 sum where there are
+/* Scratch: d for a piece (512 MB, or 512 bytes a row where that is more), dx's fp32 sum where there are
  * several pieces, copies as above, and parts of products split along the contraction. */
 size_t anvil_linear_cross_entropy_backward_workspace_bytes(const anvil_head_grad_desc* desc);
 anvil_status anvil_linear_cross_entropy_backward(const anvil_head_grad_desc* desc, void* workspace, size_t workspace_bytes,

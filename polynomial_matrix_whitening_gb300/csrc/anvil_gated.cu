@@ -10,7 +10,8 @@
 // of operand B from different weights, rank 0 from G and rank 1 from U.  A tile's accumulator then
 // holds g in its columns 0 to 127 and u in 128 to 255, each CTA has both for its 128 rows, and the
 // epilogue multiplies registers with registers: g and u never leave the SM unless they are kept.  The
-// products bound it, as they do the linear layer; the epilogue reads two columns and stores one.
+// products bound it, as they do the linear layer; the epilogue reads two columns and stores one (16384 x
+// 8192 x 4096 bf16 1143 us, 1.92 PFLOP/s; 8192 x 2816 x 768 48 us, 54 with g and u kept; 1 x 2816 x 768 2.8).
 // Few rows: the row kernel with 64 rows of either weight as the MMA's 128, joined through shared
 // memory, where g and u of an element meet.  One or two tokens of small weights: the token kernel, a
 // warp taking the same row of both.

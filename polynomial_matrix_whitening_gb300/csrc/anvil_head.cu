@@ -7,13 +7,13 @@
 // Forward: the pair kernel (anvil_linear.cuh), whose epilogue takes each tile's logits out of tensor
 // memory once and leaves, per row and 64 columns, their maximum and the sum of their exponentials
 // over it (8 bytes for 64 logits), and the target's logit where it is among them.  A second kernel joins a
-// row's pairs.  The products bound it (8192 x 50304 x 768: see anvil_head_api.cu for the figures); the
-// exponentials, 16 per SM and cycle, take a third of the time of a tile's products at k = 768.
+// row's pairs.  8192 x 50304 x 768 bf16: 377 us, 1.68 PFLOP/s, the tensor pipe active 78% of the time; from
+// k = 256 down the epilogue bounds it (3205 x 98816 x 152: 135 us, about 4400 cycles a tile).
 //
 // Gradient: the logits again, a piece of the vocabulary at a time.  The epilogue turns them into d, 16
 // bits, the operand of both products that follow: dW's rows of the piece are complete, dx is added up
 // in fp32 over the pieces.  So the workspace is bounded whatever the vocabulary, and the flops are the
-// three products' 6 rows vocab k.
+// three products' 6 rows vocab k.  8192 x 50304 x 768 bf16: 1106 us, 1.72 PFLOP/s.
 //
 // In powers of two: e^(z - m) = 2^(z log2(e) - M) with M = m log2(e) rounded, the same M in every
 // term, so that its rounding cancels in M + log2(S).
@@ -247,7 +247,9 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
     __shared__ float2 shares[HEAD_TOKEN_WARPS][R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int chunks = (p.k + E - 1) / E, whole = p.k / E;
-    const long long step = static_cast<long long>(gridDim.x) * HEAD_TOKEN_WARPS * G;
+    // the warp's share of the weight's rows, to a row: its last group may be smaller
+    const long long number = static_cast<long long>(blockIdx.x) * HEAD_TOKEN_WARPS + warp, warps = gridDim.x * static_cast<long long>(HEAD_TOKEN_WARPS);
+    const long long begin = number * p.cols / warps, end = (number + 1) * p.cols / warps;
     pdl_allow_next();
     pdl_wait_previous();
     for (int i = threadIdx.x; i < R * chunks * E; i += 32 * HEAD_TOKEN_WARPS) {
@@ -257,10 +259,10 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
     __syncthreads();
     float ref = 0.f, sum = 0.f;  // lane r's: token r
     const long long target = p.hit && lane < p.rows ? target_of(p.targets, p.target64, lane) : -1;
-    for (long long row0 = (static_cast<long long>(blockIdx.x) * HEAD_TOKEN_WARPS + warp) * G; row0 < p.cols; row0 += step) {
+    for (long long row0 = begin; row0 < end; row0 += G) {
         const T* w[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) w[g] = static_cast<const T*>(p.w) + min(row0 + g, static_cast<long long>(p.cols) - 1) * p.ldw;
+        for (int g = 0; g < G; ++g) w[g] = static_cast<const T*>(p.w) + min(row0 + g, end - 1) * p.ldw;
         uint64_t acc[G][R];
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
             float most = -INFINITY;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                if (row0 + g >= p.cols) z[g] = -INFINITY;
+                if (row0 + g >= end) z[g] = -INFINITY;
                 else if (row0 + g == target) p.hit[lane] = z[g];
                 most = fmaxf(most, z[g]);
             }
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
             float s = 0.f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                if (row0 + g < p.cols) s += exp2_of(fmaf(z[g], LOG2E, -base));
+                if (row0 + g < end) s += exp2_of(fmaf(z[g], LOG2E, -base));
             join(ref, sum, base, s);
         }
     }
