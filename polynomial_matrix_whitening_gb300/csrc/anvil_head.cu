@@ -247,9 +247,7 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
     __shared__ float2 shares[HEAD_TOKEN_WARPS][R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int chunks = (p.k + E - 1) / E, whole = p.k / E;
-    // the warp's share of the weight's rows, to a row: its last group may be smaller
-    const long long number = static_cast<long long>(blockIdx.x) * HEAD_TOKEN_WARPS + warp, warps = gridDim.x * static_cast<long long>(HEAD_TOKEN_WARPS);
-    const long long begin = number * p.cols / warps, end = (number + 1) * p.cols / warps;
+    const long long step = static_cast<long long>(gridDim.x) * HEAD_TOKEN_WARPS * G;
     pdl_allow_next();
     pdl_wait_previous();
     for (int i = threadIdx.x; i < R * chunks * E; i += 32 * HEAD_TOKEN_WARPS) {
@@ -259,10 +257,10 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
     __syncthreads();
     float ref = 0.f, sum = 0.f;  // lane r's: token r
     const long long target = p.hit && lane < p.rows ? target_of(p.targets, p.target64, lane) : -1;
-    for (long long row0 = begin; row0 < end; row0 += G) {
+    for (long long row0 = (static_cast<long long>(blockIdx.x) * HEAD_TOKEN_WARPS + warp) * G; row0 < p.cols; row0 += step) {
         const T* w[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) w[g] = static_cast<const T*>(p.w) + min(row0 + g, end - 1) * p.ldw;
+        for (int g = 0; g < G; ++g) w[g] = static_cast<const T*>(p.w) + min(row0 + g, static_cast<long long>(p.cols) - 1) * p.ldw;
         uint64_t acc[G][R];
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -322,7 +320,7 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
             float most = -INFINITY;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                if (row0 + g >= end) z[g] = -INFINITY;
+                if (row0 + g >= p.cols) z[g] = -INFINITY;
                 else if (row0 + g == target) p.hit[lane] = z[g];
                 most = fmaxf(most, z[g]);
             }
@@ -330,7 +328,7 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
             float s = 0.f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                if (row0 + g < end) s += exp2_of(fmaf(z[g], LOG2E, -base));
+                if (row0 + g < p.cols) s += exp2_of(fmaf(z[g], LOG2E, -base));
             join(ref, sum, base, s);
         }
     }
