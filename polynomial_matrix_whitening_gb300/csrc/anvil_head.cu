@@ -83,7 +83,8 @@ struct StatsPair {
             const float now = fmaxf(most, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
             const float base = now == -INFINITY ? 0.f : now * LOG2E;
             const uint64_t by = f2_make(LOG2E, LOG2E), less = f2_make(-base, -base);
-            uint64_t s[2] = {f2_make(sum * exp2_of(ref - base), 0.f), 0};
+            // (the sum's own base is never above: but for the first, of an empty sum)
+            uint64_t s[2] = {f2_make(sum * exp2_of(fminf(ref - base, 0.f)), 0.f), 0};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) s[i / 2 & 1] = f2_add(s[i / 2 & 1], exp2_of(f2_fma(f2_make(v[i], v[i + 1]), by, less)));
             float s0, s1;

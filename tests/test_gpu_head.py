@@ -215,6 +215,34 @@ def test_large_logits(A):  # noqa: F811
     assert torch.equal(loss, lse - torch.where(t % 2 == 0, -4096.0, 4096.0))
 
 
+@pytest.mark.parametrize("rows", [1, 2, 5, 40, 200, 300, 900])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_low_logits(A, transposed, rows):  # noqa: F811
+    """Logits far below 0 only, where 2 to the power of their distance from 0 overflows; the same behind columns of -inf."""
+    vocab, k = 700, 64
+    x = torch.zeros(rows, k, device="cuda", dtype=torch.bfloat16)
+    w = make_weight(1, vocab, k, "bf16", transposed)
+    w.zero_()
+    x[:, 0], x[:, 1] = 64.0, 1.0
+    w[:, 0] = torch.where(torch.arange(vocab, device="cuda") % 256 < 128, -64.0, -4.0).bfloat16()
+    w[:, 1] = torch.arange(vocab, device="cuda").remainder(5).bfloat16()
+    t = make_targets(2, rows, vocab)
+    for least in (0, 40):
+        w[:least, 0] = -math.inf
+        loss, lse = A.linear_cross_entropy(x, w, t)
+        z = x.double() @ w.double().nan_to_num(neginf=0.0).t()  # (exact in fp32 as well)
+        z[:, :least] = -math.inf
+        want = torch.logsumexp(z, 1)
+        # forward_check's without the products' part
+        parts = math.ceil(vocab / 256) * 4
+        bar = E * (34 + 11 * (parts / 8 + 9) + 4 * want.abs())
+        assert ((lse.double() - want).abs() <= 1.01 * bar).all()
+        ref = want - z.gather(1, t.clamp_min(0)[:, None])[:, 0]
+        live = (t >= 0) & ~torch.isinf(ref)
+        assert ((loss.double() - ref).abs() <= 1.01 * (bar + 2 * E * ref.abs()))[live].all()
+        assert (loss[t < 0] == 0).all() and (loss[(t >= 0) & torch.isinf(ref)] == math.inf).all()
+
+
 def test_rows_past_the_last_and_workspace(A):  # noqa: F811
     """The caller's workspace, and nothing written beside a gradient given in wider rows."""
     rows, vocab, k = 130, 515, 77
