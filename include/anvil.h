@@ -547,8 +547,9 @@ anvil_status anvil_linear_cross_entropy(const anvil_head_desc* desc, void* works
  * The logits are computed again, a piece of the vocabulary at a time; d over the largest |grad_loss| is rounded to
  * dtype as the products' operand (in fp16 with 2^13 more, so that small values are held), sums are fp32.  dx
  * [rows, k] of type dtype; dweight in W's layout, of type dweight_dtype: dtype or ANVIL_F32.  Each may be
- * NULL.  grad_loss is taken as 0 where the target is negative; a row whose lse is -inf has the gradient
- * 0.  accumulate != 0: dweight is added to what it holds. */
+ * NULL.  grad_loss is taken as 0 where the target is negative; a target of vocab or more is no column's
+ * (d_j = grad_loss e^(z_j - lse)); a row whose lse is -inf has the gradient 0.  accumulate != 0: dweight
+ * is added to what it holds. */
 typedef struct {
     const void* x;
     const void* weight;
@@ -650,7 +651,7 @@ typedef enum {
     ANVIL_KERNEL_GATED_PREPARE = 22,     /* the gated layer: dg and du */
     ANVIL_KERNEL_GATED_PRODUCT = 23,     /* both products, activation and product */
     ANVIL_KERNEL_GATED_SUM = 24,         /* sums of its split products */
-    ANVIL_KERNEL_HEAD_PREPARE = 25,      /* the head's cross entropy: the scale of fp16 gradients */
+    ANVIL_KERNEL_HEAD_PREPARE = 25,      /* the head's cross entropy: the scale of its gradient */
     ANVIL_KERNEL_HEAD_PRODUCT = 26,      /* its logits, and what becomes of them */
     ANVIL_KERNEL_HEAD_SUM = 27           /* rows' statistics joined; dx rounded */
 } anvil_kernel_kind;
