@@ -901,8 +901,9 @@ __device__ __forceinline__ void finish_rows(const GemmEpilogue& e, float (&v)[N]
 }
 
 // What a variant of the row kernel computes.  HEAD: its eight results of a thread at a time go to
-// finish(p, v, column, exists, first row, rows, this block's shared memory), and the block's to end().  GATED: its 128 weight rows are 64 of one weight (TMEM
-// lanes 0 to 63) and the same 64 of another, whose results finish one element together.
+// finish(p, v, column, exists, first row, rows, this block's shared memory), and the block's to end().
+// GATED: its 128 weight rows are 64 of one weight (TMEM lanes 0 to 63) and the same 64 of another,
+// whose results finish one element together.
 struct PlainRows {
     using Params = RowGemmParams;
     static constexpr bool GATED = false, HEAD = false;
@@ -1293,8 +1294,8 @@ __global__ void __launch_bounds__(TOKEN_THREADS) token_kernel(const typename M::
     static_cast<T*>(e.out)[row * e.ldout + col] = Elem<T>::store(mine[0]);
 }
 
-// Weight rows per warp (of both weights together: two at least): four where that still gives every SM sixteen warps, else fewer, then
-// several warps per row, as long as every lane has a chunk.
+// Weight rows per warp (of both weights together: two at least): four where that still gives every SM
+// sixteen warps, else fewer, then several warps per row, as long as every lane has a chunk.
 template <typename T, int R, typename M>
 cudaError_t run_tokens(const typename M::Params& p, cudaStream_t s) {
     const int full = 152 * 2 * TOKEN_WARPS, chunks = p.k / Elem<T>::VEC;
