@@ -205,6 +205,7 @@ __device__ __forceinline__ float gather8(float (&v)[8], int lane, Op op) {
 struct HeadRows {
     using Params = RowHeadParams;
     static constexpr bool GATED = false, HEAD = true;
+    static constexpr int BLOCKS = 3;
     static __device__ __forceinline__ void finish(const Params& p, const float (&v)[8], int col, bool live, int row, int rows, float2* to) {
         // over the warp's columns: each exchange halves the rows that a lane goes on with, until lane l has
         // row l / 4's, from where every lane gets all eight maxima
@@ -235,11 +236,11 @@ struct HeadRows {
     }
 };
 
-// One or two rows: the weight is read once, by warps that take four of its rows at a time and keep
+// One or two rows and a small weight: read once, by warps that take four of its rows at a time and keep
 // each token's running statistics; no tensor cores, no tiles to fill.  A lane takes every 32nd 16-byte chunk,
-// twelve of them on their way, the tokens wait in shared memory as fp32.  HBM bounds it where the weight is
-// large (1 x 131072 x 4096: 157 us, 6.8 TB/s; 1 x 50304 x 768 with the join 18.7, the row kernel 24); three
-// blocks an SM, with fewer registers each, were slower (187, 20.1), and for four rows the row kernel is faster.
+// twelve of them on their way, the tokens wait in shared memory as fp32.  One row, us with the join, against the
+// row kernel: 5000 x 768 6.5/8.3, 8000 x 4096 15.4/17.8; 20000 x 768 10.8/9.4, 50304 x 768 18.3/17.4, 32000 x
+// 4096 47.2/44.6.  (Three blocks an SM, with fewer registers each, were slower.)
 template <typename T, int R>
 __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(const TokenHeadParams p) {
     constexpr int G = HEAD_TOKEN_GROUP, E = Elem<T>::VEC;

@@ -35,8 +35,10 @@ HeadLayout head_layout(const anvil_head_desc* d) {
     const double epilogue = 4000.0;
     const int64_t kb = ceil_div(d->k, GEMM_BK);
     memset(&L.plan, 0, sizeof(L.plan));
-    // one or two rows and a weight stored by rows: read without tensor cores
-    L.plan.tokens = d->rows <= HEAD_TOKENS && !d->weight_transposed && d->rows * d->k <= HEAD_TOKEN_VALUES;
+    // one or two rows and a weight stored by rows for which the row kernel would have a block an SM at
+    // most: read without tensor cores
+    L.plan.tokens = d->rows <= HEAD_TOKENS && !d->weight_transposed && d->rows * d->k <= HEAD_TOKEN_VALUES &&
+                    ceil_div(d->vocab, ROW_TILE_A) <= PLAN_SMS;
     if (d->rows <= FEW_ROWS) plan_few(d->rows, d->vocab, kb, epilogue, &L.plan);
     const bool tokens = L.plan.tokens;
     plan_whole(tiles_of(d->rows, d->vocab), kb, epilogue, ALL_FREE, &L.plan);

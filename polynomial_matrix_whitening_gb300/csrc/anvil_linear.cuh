@@ -862,9 +862,14 @@ struct RowShape {
     // run beside the other's products (1 x 50304 x 768: 17.3 us, 20.6 with one; from 64 tokens
     // on the fewer stages cost more than that gives, 24 against 21).
     static constexpr int STAGES_OF_TWO = 110 * 1024 / STAGE;
+    // Three where there are more than two for each SM and the variant's registers allow it (the head's
+    // 393 blocks in one turn: 50304 x 768, 4 rows 21.5 -> 17.8 us with what follows it, 16 rows 24.4 -> 19).
+    static constexpr int STAGES_OF_THREE = 73 * 1024 / STAGE;
     static constexpr int smem(int stages) { return stages * STAGE + 1024; }
     static constexpr uint32_t TMEM_COLS = BN < 32 ? 32 : BN;
     static_assert(BN * ROW_TILE_A * 4 <= STAGES * STAGE && STAGES_OF_TWO < STAGES, "the partial accumulator reuses the stages");
+    // a producer waits for its stage's last use by parity: it must not come to a stage two uses ahead of it
+    static_assert(BN > ROW_TWO_TOKENS || STAGES_OF_THREE >= ROW_PRODUCERS, "a stage for every producer");
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
@@ -907,10 +912,12 @@ __device__ __forceinline__ void finish_rows(const GemmEpilogue& e, float (&v)[N]
 struct PlainRows {
     using Params = RowGemmParams;
     static constexpr bool GATED = false, HEAD = false;
+    static constexpr int BLOCKS = 2;  // of an SM, for up to ROW_TWO_TOKENS tokens
 };
 struct GatedRows {
     using Params = RowGatedParams;
     static constexpr bool GATED = true, HEAD = false;
+    static constexpr int BLOCKS = 2;
 };
 // act(g) u of up to N rows (B's) of one column, g and u kept where they are asked for.
 template <typename T, int N, typename P>
@@ -959,7 +966,7 @@ __device__ __forceinline__ void join_parts(uint32_t mine, int splits, float (&v)
 }
 
 template <typename T, int BN, typename M>
-__global__ void __launch_bounds__(ROW_THREADS, 2) row_gemm_kernel(const __grid_constant__ typename M::Params p) {
+__global__ void __launch_bounds__(ROW_THREADS, BN <= ROW_TWO_TOKENS ? M::BLOCKS : 2) row_gemm_kernel(const __grid_constant__ typename M::Params p) {
     using S = RowShape<BN>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[S::STAGES];
@@ -1148,8 +1155,10 @@ cudaError_t run_row(typename M::Params p, int sm_count, cudaStream_t s) {
     constexpr int rows = M::GATED ? ROW_TILE_A / 2 : ROW_TILE_A;  // of the result's columns
     cfg.gridDim = dim3((p.na + rows - 1) / rows * p.splits, (p.nb + BN - 1) / BN);
     cfg.blockDim = dim3(ROW_THREADS);
-    const bool more = BN <= ROW_TWO_TOKENS && static_cast<long long>(cfg.gridDim.x) * cfg.gridDim.y > sm_count;
-    p.stages = more ? RowShape<BN>::STAGES_OF_TWO : RowShape<BN>::STAGES;
+    const long long blocks = BN <= ROW_TWO_TOKENS ? static_cast<long long>(cfg.gridDim.x) * cfg.gridDim.y : 0;
+    p.stages = M::BLOCKS > 2 && blocks > 2 * sm_count ? RowShape<BN>::STAGES_OF_THREE
+               : blocks > sm_count                    ? RowShape<BN>::STAGES_OF_TWO
+                                                      : RowShape<BN>::STAGES;
     cfg.dynamicSmemBytes = RowShape<BN>::smem(p.stages);
     cfg.stream = s;
     cfg.attrs = attr;
