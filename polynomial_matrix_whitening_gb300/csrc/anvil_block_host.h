@@ -251,15 +251,39 @@ inline void plan_parts(int64_t tiles, int64_t tail, int64_t kb, double turn, Sta
     p->part = static_cast<size_t>(parts) * 4 * PAIR_ROWS * PAIR_COLS;
 }
 
+// One or two tokens and a small weight: no tensor core, no join, half the latency.  Against
+// row_gemm_kernel, us: 2816 x 768 one token 2.7/4.4, two 3.4/4.5; 4096 x 4096 9.7/9.9 and 12.3/10;
+// 16384 x 4096 27/23.3.
+inline bool token_product(int64_t rows, int cols, int64_t k) {
+    return rows <= TOKEN_ROWS && rows * k <= TOKEN_CHUNKS * 8 && rows * rows * cols * k <= 1 << 24;
+}
+
+// The row kernel for `rows` tokens, up to 32 a tile, and so many tiles of the weight: split along k as long as
+// two of its blocks share an SM at most and every part has four k-blocks (us in one part/two/four: gated 32 x 8192
+// x 1024, 128 tiles, 9.7/8.5/14.6; 32 x 11008 x 4096, 172 tiles, 34.8/42; 16 x 5000 x 128, 79 tiles, 3.9/5.2; the
+// head's 16 x 8000 x 4096, 63 tiles, 25.7/19.1/17.9).  Clusters of eight find fewer places: 64 blocks at most.
+constexpr int ROW_TOKENS = 32;
+inline int64_t row_tiles(int64_t rows) { return ceil_div(rows, rows <= 16 ? 16 : ROW_TOKENS); }
+inline void set_rows(int64_t rows, int64_t weight_tiles, int64_t kb, Plan* p) {
+    const int64_t blocks = weight_tiles * row_tiles(rows);
+    memset(p, 0, sizeof(*p));
+    p->few = true;
+    p->bn = rows <= 16 ? 16 : ROW_TOKENS;
+    p->splits = 1;
+    for (int s = 2; s <= 8; s *= 2) {
+        const int64_t per = ceil_div(kb, s);
+        if (blocks * s > (s < 8 ? 2 * PLAN_SMS : 64) || per < 4 || per * (s - 1) >= kb) break;  // (every part has work)
+        p->splits = s;
+    }
+    p->kb = static_cast<int>(ceil_div(kb, p->splits));
+}
+
 // few: the kernels for few rows may run (A K-major, a 16-bit result); k_major: B is;
 // epilogue: SM cycles that the epilogue of a whole tile of the pair kernel takes.
 inline Plan plan_product(int64_t rows, int cols, int64_t k, bool few, bool k_major, double epilogue, Start at) {
     Plan p = {};
     const int64_t kb = ceil_div(k, GEMM_BK), tiles = tiles_of(rows, cols);
-    // One or two tokens and a small weight: no tensor core, no join, half the latency.  Against
-    // row_gemm_kernel, us: 2816 x 768 one token 2.7/4.4, two 3.4/4.5; 4096 x 4096 9.7/9.9 and 12.3/10;
-    // 16384 x 4096 27/23.3.
-    if (few && k_major && rows <= TOKEN_ROWS && rows * k <= TOKEN_CHUNKS * 8 && rows * rows * cols * k <= 1 << 24) {
+    if (few && k_major && token_product(rows, cols, k)) {
         p.tokens = p.few = true;
         return p;
     }

@@ -204,12 +204,8 @@ cudaError_t gated_prepare() {
     ANVIL_SMEM((pair_gemm_kernel<__half, 64, GatedPair>), Staging<64>::SMEM);
     ANVIL_ROWS(__nv_bfloat16, 16);
     ANVIL_ROWS(__nv_bfloat16, 32);
-    ANVIL_ROWS(__nv_bfloat16, 64);
-    ANVIL_ROWS(__nv_bfloat16, 128);
     ANVIL_ROWS(__half, 16);
     ANVIL_ROWS(__half, 32);
-    ANVIL_ROWS(__half, 64);
-    ANVIL_ROWS(__half, 128);
 #undef ANVIL_ROWS
 #undef ANVIL_SMEM
     return cudaSuccess;
@@ -222,12 +218,7 @@ cudaError_t launch_pair_gated(const PairGatedParams& p, int sm_count, cudaStream
 namespace {
 template <typename T>
 cudaError_t pick_row(const RowGatedParams& p, int bn, int sm_count, cudaStream_t s) {
-    switch (bn) {
-        case 16: return run_row<T, 16, GatedRows>(p, sm_count, s);
-        case 32: return run_row<T, 32, GatedRows>(p, sm_count, s);
-        case 64: return run_row<T, 64, GatedRows>(p, sm_count, s);
-        default: return run_row<T, 128, GatedRows>(p, sm_count, s);
-    }
+    return bn == 16 ? run_row<T, 16, GatedRows>(p, sm_count, s) : run_row<T, 32, GatedRows>(p, sm_count, s);
 }
 }  // namespace
 

@@ -11,9 +11,20 @@ using namespace anvil;
 
 namespace {
 
-// The columns that plan_product sees: a tile of the pair kernel holds GATED_COLS of y, a block of the
-// row kernel half as many weight rows of each kind as it has.
+// The columns that plan_product sees: a tile of the pair kernel holds GATED_COLS of y.
 int plan_cols(int n) { return static_cast<int>(2 * ceil_div(n, GATED_COLS) * GATED_COLS); }
+
+// The row kernel where one tile of up to 32 tokens takes them all, or its blocks are all on SMs of their own.  Row kernel/pair
+// kernel, us: 16 x 2816 x 768 6.5/8.8, 16 x 11008 x 4096 33/43, 32 x 12288 x 1024 11.7/17.4, 32 x 40000 x 2048 64.9/65.3;
+// 64 x 4096 x 1024 (128 blocks) 8.3/10.1, 64 x 8192 x 4096 (256) 33.3/29, 64 x 10000 x 768 (314) 16.5/13.8.
+Plan plan_forward(int64_t rows, int n, int k, bool k_major, double cycles) {
+    Plan p = {};
+    const int64_t tiles = ceil_div(n, ROW_TILE_A / 2);
+    if (k_major && token_product(rows, plan_cols(n), k)) p.tokens = p.few = true;
+    else if (rows <= ROW_TOKENS || (rows <= FEW_ROWS && tiles * row_tiles(rows) <= PLAN_SMS)) set_rows(rows, tiles, ceil_div(k, GEMM_BK), &p);
+    else p = plan_product(rows, plan_cols(n), k, false, k_major, cycles, ALL_FREE);
+    return p;
+}
 
 GemmEpilogue forward_epilogue(const anvil_gated_desc* d) {
     GemmEpilogue e = {};
@@ -43,7 +54,7 @@ GatedLayout gated_layout(const anvil_gated_desc* d) {
     GemmEpilogue e = forward_epilogue(d);
     double cycles = epilogue_cycles(e, d->rows);
     if (d->preact_up) cycles += aligned16(d->preact_up, d->ldzu, 2, d->rows) ? 2500.0 : 12000.0;
-    L.plan = plan_product(d->rows, plan_cols(d->n), d->k, true, !tr, cycles, ALL_FREE);
+    L.plan = plan_forward(d->rows, d->n, d->k, !tr, cycles);
     L.total = L.off_part + L.plan.part;
     return L;
 }

@@ -451,9 +451,7 @@ cudaError_t head_prepare() {
     ANVIL_SMEM((head_token_kernel<T, 1>), 4 * (HEAD_TOKEN_VALUES + 8));                                  \
     ANVIL_SMEM((head_token_kernel<T, 2>), 4 * (HEAD_TOKEN_VALUES + 16));                                 \
     ANVIL_SMEM((row_gemm_kernel<T, 16, HeadRows>), RowShape<16>::smem(RowShape<16>::STAGES));            \
-    ANVIL_SMEM((row_gemm_kernel<T, 32, HeadRows>), RowShape<32>::smem(RowShape<32>::STAGES));            \
-    ANVIL_SMEM((row_gemm_kernel<T, 64, HeadRows>), RowShape<64>::smem(RowShape<64>::STAGES));            \
-    ANVIL_SMEM((row_gemm_kernel<T, 128, HeadRows>), RowShape<128>::smem(RowShape<128>::STAGES))
+    ANVIL_SMEM((row_gemm_kernel<T, 32, HeadRows>), RowShape<32>::smem(RowShape<32>::STAGES))
     ANVIL_HEAD(__nv_bfloat16);
     ANVIL_HEAD(__half);
 #undef ANVIL_HEAD
@@ -473,12 +471,7 @@ cudaError_t launch_head_dlogits(const PairHeadParams& p, int sm_count, cudaStrea
 namespace {
 template <typename T>
 cudaError_t pick_rows(const RowHeadParams& p, int bn, int sm_count, cudaStream_t s) {
-    switch (bn) {
-        case 16: return run_row<T, 16, HeadRows>(p, sm_count, s);
-        case 32: return run_row<T, 32, HeadRows>(p, sm_count, s);
-        case 64: return run_row<T, 64, HeadRows>(p, sm_count, s);
-        default: return run_row<T, 128, HeadRows>(p, sm_count, s);
-    }
+    return bn == 16 ? run_row<T, 16, HeadRows>(p, sm_count, s) : run_row<T, 32, HeadRows>(p, sm_count, s);
 }
 }  // namespace
 

@@ -30,19 +30,14 @@ HeadLayout head_layout(const anvil_head_desc* d) {
     HeadLayout L;
     L.x = {d->x, d->rows, d->ldx, d->k};
     L.w = stored_weight(d->weight, d->vocab, d->k, d->ldw, d->weight_transposed != 0);
-    // (an epilogue's cycles: a tile's exponentials, 2048 for the special function units of either CTA,
-    // and what is around them)
-    const double epilogue = 4000.0;
-    const int64_t kb = ceil_div(d->k, GEMM_BK);
     memset(&L.plan, 0, sizeof(L.plan));
-    // one or two rows and a weight stored by rows for which the row kernel would have a block an SM at
-    // most: read without tensor cores
+    // One or two rows and a weight stored by rows for which the row kernel would have a block an SM at
+    // most: read without tensor cores.  The row kernel up to one tile of tokens (us, row kernel/pair kernel: 32 rows
+    // 50304 x 768 21.4/25.3, 8000 x 4096 18.2/24.9, 128000 x 4096 176/172; 64 rows 20000 x 768 14.5/15.7, 32000 x
+    // 4096 67/52, 5000 x 768 10.1/9.9).
     L.plan.tokens = d->rows <= HEAD_TOKENS && !d->weight_transposed && d->rows * d->k <= HEAD_TOKEN_VALUES &&
                     ceil_div(d->vocab, ROW_TILE_A) <= PLAN_SMS;
-    if (d->rows <= FEW_ROWS) plan_few(d->rows, d->vocab, kb, epilogue, &L.plan);
-    const bool tokens = L.plan.tokens;
-    plan_whole(tiles_of(d->rows, d->vocab), kb, epilogue, ALL_FREE, &L.plan);
-    L.plan.tokens = tokens;
+    if (!L.plan.tokens && d->rows <= ROW_TOKENS) set_rows(d->rows, ceil_div(d->vocab, ROW_TILE_A), ceil_div(d->k, GEMM_BK), &L.plan);
     if (L.plan.tokens) L.parts = head_token_blocks(d->vocab);
     else L.parts = static_cast<int>(L.plan.few ? ceil_div(d->vocab, ROW_TILE_A) : ceil_div(d->vocab, PAIR_COLS) * (PAIR_COLS / HEAD_STATS_COLS));
     L.off_x = 0;

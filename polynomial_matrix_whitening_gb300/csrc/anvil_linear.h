@@ -230,7 +230,7 @@ struct HeadRoundParams {
 cudaError_t head_prepare();
 cudaError_t launch_head_stats(const PairHeadParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_head_tokens(const TokenHeadParams& p, cudaStream_t stream);
-// bn: rows of x per block (16, 32, 64 or 128)
+// bn: rows of x per block (16 or 32)
 cudaError_t launch_head_rows(const RowHeadParams& p, int bn, int sm_count, cudaStream_t stream);
 cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t stream);
 cudaError_t launch_head_dlogits(const PairHeadParams& p, int sm_count, cudaStream_t stream);
