@@ -172,7 +172,7 @@ __device__ __forceinline__ uint32_t root_code(float q) {
     return q > 0.f ? max(c, 1u) : 0u;
 }
 
-// The largest of a warp's values (magnitudes: bits without the sign), as bits, which puts an infinity
+// The largest of a lane's values (magnitudes: bits without the sign), as bits, which puts an infinity
 // above every number and a NaN above that.
 template <bool SIGNED>
 __device__ __forceinline__ uint32_t most_bits(const float (&v)[8]) {
@@ -180,6 +180,14 @@ __device__ __forceinline__ uint32_t most_bits(const float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) most = max(most, SIGNED ? __float_as_uint(v[i]) & 0x7fffffffu : __float_as_uint(v[i]));
     return most;
+}
+
+// The least magnitude of a lane's values that are not 0, as bits less 1, which puts 0 above all.
+__device__ __forceinline__ uint32_t least_bits(const float (&v)[8]) {
+    uint32_t least = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) least = min(least, (__float_as_uint(v[i]) & 0x7fffffffu) - 1u);
+    return least;
 }
 
 // The eight values times one factor, in pairs.
@@ -236,7 +244,7 @@ struct Inputs {
 };
 struct Constants {
     float beta1, c1, beta2, c2, eps, step_size, root, decay, grad_scale;
-    bool middle;  // denominators from 2^-60 (eps) to 2^13 2^20 + eps
+    bool middle;  // denominators from 2^-60 (eps) to 2^24 (2^13 2^10 + eps)
 };
 
 // One block's step from what `in` holds; as soon as that is used, what block `next` (whole; -1: none) needs
@@ -285,8 +293,9 @@ __device__ __forceinline__ void adamw_block(const AdamwTensor& t, const Constant
         most_m = most_bits<true>(m);
         most_v = most_bits<false>(v);
     }
-    // |m| below 2^60 (no quotient overflows) and v below 2^26, no infinity or NaN among them
-    if (CODES && a.middle && most_m < (187u << 23) && most_v < (153u << 23)) {
+    // |m| 0 or from 2^-102 (no quotient below 2^-126, and every remainder exact) to 2^60 (none overflows) and v below
+    // 2^26, no infinity or NaN among them
+    if (CODES && a.middle && least_bits(m) >= (25u << 23) - 1u && most_m < (187u << 23) && most_v < (153u << 23)) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             f2_split(f2_root(f2_make(v[i], v[i + 1])), &r[i], &r[i + 1]);
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, CODES && VEC ? 4 : 3) adamw_kernel(co
         a.decay = p.d_scalars[2];
         a.grad_scale = p.d_scalars[3];
     }
-    a.middle = a.eps >= 0x1p-60f && a.eps <= 1.f && a.root >= 0.f && a.root <= 0x1p20f;
+    a.middle = a.eps >= 0x1p-60f && a.eps <= 1.f && a.root >= 0.f && a.root <= 0x1p10f;
     Inputs<PARAM, GRAD, CODES, VEC> in;
     long long b = first + warp;
     if (b < whole) {

@@ -6,9 +6,10 @@
 // System/6000 processor", IBM J. Res. Dev. 34, 1990): from a quotient q within an ulp and the correctly
 // rounded reciprocal y of b, q + (a - b q) y rounds to a / b, since the remainder a - b q is exact in
 // one fused operation; the square root's correction is g + (v - g g) h with h near 1 / (2 sqrt v).
-// Checked on the hardware: the reciprocal for every significand of b, the root for every significand
-// of v at either parity of the exponent (scaling by powers of four changes nothing else) and every subnormal v,
-// the quotient for 2^36 pairs of significands: all the same as the correctly rounded operations.
+// tests/test_gpu_adamw_rounding.py compares AdamW's steps, which are these operations, with the correctly rounded
+// ones: the root of every significand at either parity of the exponent (scaling by powers of four changes
+// nothing else), and with it every significand of the divisor; 2^26 quotients, a fourth of them as near to the
+// middle between two values as any.
 #pragma once
 
 #include <stdint.h>
@@ -29,8 +30,8 @@ __device__ __forceinline__ float approx_rsqrt(float v) {
     return r;
 }
 
-// (a.x / b.x, a.y / b.y) for b within 2^-60 to 2^90 and |a| within 2^-102 to 2^60, or a = 0.  (Below
-// 2^-102, and where the quotient is below 2^-126, the remainder is not exact: off by two ulps at most.)
+// (a.x / b.x, a.y / b.y) for b within 2^-60 to 2^90 and |a| within 2^-102 to 2^60 with a quotient from 2^-126 on,
+// or a = 0.  (Elsewhere the remainder is not exact, and the quotient off by two ulps at most.)
 __device__ __forceinline__ uint64_t f2_divide(uint64_t a, uint64_t b) {
     const uint64_t one = f2_make(1.f, 1.f), nb = f2_neg(b);
     float b0, b1;
