@@ -544,8 +544,8 @@ anvil_status anvil_linear_cross_entropy(const anvil_head_desc* desc, void* works
 
 /* Its gradient, for grad_loss = dL/dloss [rows] and the forward pass's lse [rows], both fp32:
  *   d_j = grad_loss (e^(z_j - lse) - [j = target]),  dx = d W,  dweight = d^T x.
- * The logits are computed again, a piece of the vocabulary at a time; d over the largest |grad_loss| is rounded to
- * dtype as the products' operand (in fp16 with 2^13 more, so that small values are held), sums are fp32.  dx
+ * The logits are computed again, a piece of the vocabulary at a time; d over the largest finite |grad_loss| is
+ * rounded to dtype as the products' operand (in fp16 with 2^13 more, so that small values are held), sums are fp32.  dx
  * [rows, k] of type dtype; dweight in W's layout, of type dweight_dtype: dtype or ANVIL_F32.  Each may be
  * NULL.  grad_loss is taken as 0 where the target is negative; a target of vocab or more is no column's
  * (d_j = grad_loss e^(z_j - lse)); a row whose lse is -inf has the gradient 0.  accumulate != 0: dweight

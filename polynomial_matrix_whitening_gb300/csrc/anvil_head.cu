@@ -394,7 +394,8 @@ __global__ void __launch_bounds__(1024) head_scale_kernel(const HeadScaleParams 
 #pragma unroll 8
     for (long long i = threadIdx.x; i < p.rows; i += 1024) {
         const uint32_t g = __float_as_uint(p.grad[i]) & 0x7fffffffu;
-        most = max(most, target_of(p.targets, p.target64, i) >= 0 ? g : 0u);
+        // (an infinity or a NaN makes its row what it is over any scale)
+        most = max(most, target_of(p.targets, p.target64, i) >= 0 && g < 0x7f800000u ? g : 0u);
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = most;
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(1024) head_scale_kernel(const HeadScaleParams 
     most = __reduce_max_sync(0xffffffffu, warps[threadIdx.x]);
     if (threadIdx.x == 0) {
         float unit = __uint_as_float(most);
-        // 0, and beyond 2^100 either way (infinities and NaN among them): as they are
+        // 0, and beyond 2^100 either way: as they are
         unit = unit >= 7.8886090522101181e-31f && unit <= 1.2676506002282294e30f ? (p.f16 ? unit * 0x1p-13f : unit) : 1.f;
         p.scale[0] = __fdiv_rn(1.f, unit);
         p.scale[1] = unit;

@@ -211,7 +211,7 @@ struct HeadJoinParams {
     long long rows;
     int parts, vocab, target64;
 };
-// scale[1] = the largest |grad| of rows that count (fp16: over 2^13), scale[0] = 1 / scale[1]
+// scale[1] = the largest finite |grad| of rows that count (fp16: over 2^13), scale[0] = 1 / scale[1]
 struct HeadScaleParams {
     const float* grad;
     const void* targets;
