@@ -15,8 +15,8 @@
 // in fp32 over the pieces.  So the workspace is bounded whatever the vocabulary, and the flops are the
 // three products' 6 rows vocab k.  8192 x 50304 x 768 bf16: 1106 us, 1.72 PFLOP/s.
 //
-// In powers of two: e^(z - m) = 2^(z log2(e) - M) with M = m log2(e) rounded, the same M in every
-// term, so that its rounding cancels in M + log2(S).
+// Exponentials in powers of two, one fused operation and one of the hardware's powers each (struct Base), over
+// the largest logit itself: lse = m + log S, so that a logit that stands alone is its row's lse to the bit.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -26,7 +26,7 @@ namespace anvil {
 
 namespace {
 
-constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
+constexpr float LOG2E = 1.44269504f;
 
 // 2^v, of results below 2^-126 0 (a relative error of 2^-22; the subnormal results would cost as much again).
 __device__ __forceinline__ float exp2_of(float v) {
@@ -39,6 +39,18 @@ __device__ __forceinline__ uint64_t exp2_of(uint64_t v) {
     f2_split(v, &lo, &hi);
     return f2_make(exp2_of(lo), exp2_of(hi));
 }
+
+// e^(z - m) = 2^(z by - base) undo, by = log2(e).  base = m by is rounded; what that drops is the same in every
+// z's power, 2^rest, and undo = 2^-rest takes it out again.  From |m| = 2^29 on rest passes 32 and would soon
+// overflow, but fp32 values are 64 apart there: by = 1 takes any other z than m to nothing as well, and base is m.
+struct Base {
+    float by, base;
+    __device__ __forceinline__ explicit Base(float m) {
+        by = fabsf(m) >= 0x1p29f ? 1.f : LOG2E;
+        base = __fmul_rn(m, by);
+    }
+    __device__ __forceinline__ float rest(float m) const { return by == 1.f ? 0.f : __fmaf_rn(m, by, -base); }
+};
 
 __device__ __forceinline__ long long target_of(const void* targets, int wide, long long row) {
     return wide ? static_cast<const long long*>(targets)[row] : static_cast<const int*>(targets)[row];
@@ -67,7 +79,7 @@ struct StatsPair {
         const int col0 = t.tc * BN + x.grp * EPI_COLS;
         const uint32_t ta = tacc + x.grp * EPI_COLS;
         const int live = p.cols - col0;  // columns of this group that exist
-        float most = -INFINITY, ref = 0.f, sum = 0.f;
+        float most = -INFINITY, sum = 0.f;
 #pragma unroll 1
         for (int h = 0; h < EPI_COLS; h += 32) {
             float v[32];
@@ -81,17 +93,17 @@ struct StatsPair {
 #pragma unroll
             for (int i = 4; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], v[i]);
             const float now = fmaxf(most, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
-            const float base = now == -INFINITY ? 0.f : now * LOG2E;
-            const uint64_t by = f2_make(LOG2E, LOG2E), less = f2_make(-base, -base);
-            // (the sum's own base is never above: but for the first, of an empty sum)
-            uint64_t s[2] = {f2_make(sum * exp2_of(fminf(ref - base, 0.f)), 0.f), 0};
+            const float ref = now == -INFINITY ? 0.f : now;
+            const Base e(ref);
+            const uint64_t by = f2_make(e.by, e.by), less = f2_make(-e.base, -e.base);
+            uint64_t s[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) s[i / 2 & 1] = f2_add(s[i / 2 & 1], exp2_of(f2_fma(f2_make(v[i], v[i + 1]), by, less)));
             float s0, s1;
             f2_split(f2_add(s[0], s[1]), &s0, &s1);
-            sum = s0 + s1;
+            // (of an empty sum the factor does not count, but for being a number)
+            sum = fmaf(s0 + s1, exp2_of(-e.rest(ref)), sum * exp2_of(fminf((most - now) * LOG2E, 0.f)));
             most = now;
-            ref = base;
         }
         const int at = row.target - col0;
         const bool mine = row.target >= 0 && at >= 0 && at < EPI_COLS;
@@ -108,7 +120,7 @@ struct StatsPair {
             if (mine) p.hit[row.row] = hit;
         }
         release_acc(x, tempty);
-        if (row.row < p.rows) p.stats[static_cast<long long>(t.tc * EPI_GROUPS + x.grp) * p.rows + row.row] = make_float2(ref, sum);
+        if (row.row < p.rows) p.stats[static_cast<long long>(t.tc * EPI_GROUPS + x.grp) * p.rows + row.row] = make_float2(most == -INFINITY ? 0.f : most, sum);
     }
 };
 
@@ -116,19 +128,24 @@ struct DlogitsPair {
     using Params = PairHeadParams;
     static constexpr bool MULTI = false, OWN = true, RANK_B = false, ONE_CHAIN = false;
     struct Row {
-        float lse2, g;
+        float by, less;   // e^(z - lse) = 2^(z by + less) / one
+        float one, g;     // d = (2^(z by + less) - [j = target] one) g
         uint32_t counts;  // all ones, or 0 where the gradient is 0 whatever the logits are
         int target;
     };
     static __device__ __forceinline__ Row load(const Params& p, const Unit& t, int r) {
         const long long row = static_cast<long long>(t.tr) * PAIR_ROWS + r;
-        Row x = {0.f, 0.f, 0u, -1};
+        Row x = {0.f, 0.f, 1.f, 0.f, 0u, -1};
         if (row < p.rows && target_of(p.targets, p.target64, row) >= 0) {
             const float lse = p.lse[row];
             if (lse != -INFINITY) {  // (no token of that row can be: its gradient is 0)
-                x.lse2 = lse * LOG2E;
-                x.g = p.grad[row] * *p.scale;
-                x.counts = x.g == 0.f ? 0u : 0xffffffffu;
+                const Base e(lse);
+                const float rest = e.rest(lse), g = p.grad[row] * *p.scale;
+                x.by = e.by;
+                x.less = -e.base;
+                x.one = exp2_of(rest);
+                x.g = g * exp2_of(-rest);
+                x.counts = g == 0.f ? 0u : 0xffffffffu;
                 x.target = relative_target(p, row);
             }
         }
@@ -148,14 +165,14 @@ struct DlogitsPair {
             for (int c = 0; c < COLS; c += 16) {
                 float v[16];
                 tmem_ld_16(ta + b * COLS + c, v);
-                const uint64_t by = f2_make(LOG2E, LOG2E), less = f2_make(-row.lse2, -row.lse2), g = f2_make(row.g, row.g);
+                const uint64_t by = f2_make(row.by, row.by), less = f2_make(row.less, row.less), g = f2_make(row.g, row.g);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) f2_split(exp2_of(f2_fma(f2_make(v[i], v[i + 1]), by, less)), &v[i], &v[i + 1]);
                 const int hot = at - (b * COLS + c);
                 if (row.target >= 0 && hot >= 0 && hot < 16) {  // one warp and sixteen columns in a hundred, of 50,000
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (hot == i) v[i] -= 1.f;
+                        if (hot == i) v[i] -= row.one;
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -177,11 +194,11 @@ struct DlogitsPair {
     }
 };
 
-// Two sums over different bases as one.  (A part with a sum of 0 has no logit above -inf; a NaN goes
+// Two sums over different logits as one.  (A part with a sum of 0 has no logit above -inf; a NaN goes
 // through the sums.)
 __device__ __forceinline__ void join(float& ref, float& sum, float ref2, float sum2) {
     const float now = sum2 == 0.f ? ref : sum == 0.f ? ref2 : fmaxf(ref, ref2);
-    sum = (sum == 0.f ? 0.f : sum * exp2_of(ref - now)) + (sum2 == 0.f ? 0.f : sum2 * exp2_of(ref2 - now));
+    sum = (sum == 0.f ? 0.f : sum * exp2_of((ref - now) * LOG2E)) + (sum2 == 0.f ? 0.f : sum2 * exp2_of((ref2 - now) * LOG2E));
     ref = now;
 }
 
@@ -214,14 +231,14 @@ struct HeadRows {
 #pragma unroll
         for (int i = 0; i < 8; ++i) m[i] = live ? v[i] : -INFINITY;
         const float most = gather8(m, lane, [](float a, float b) { return fmaxf(a, b); });
-        const float mine = most == -INFINITY ? 0.f : most * LOG2E;
+        const float mine = most == -INFINITY ? 0.f : most;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float ref = __shfl_sync(0xffffffffu, mine, 4 * i);
-            s[i] = live ? exp2_of(fmaf(v[i], LOG2E, -ref)) : 0.f;
+            const Base e(__shfl_sync(0xffffffffu, mine, 4 * i));
+            s[i] = live ? exp2_of(fmaf(v[i], e.by, -e.base)) : 0.f;
         }
         const float sum = gather8(s, lane, [](float a, float b) { return a + b; });
-        if (lane % 4 == 0) to[lane / 4] = make_float2(mine, sum);
+        if (lane % 4 == 0) to[lane / 4] = make_float2(mine, sum * exp2_of(-Base(mine).rest(mine)));
         if (p.hit) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -326,12 +343,13 @@ __global__ void __launch_bounds__(32 * HEAD_TOKEN_WARPS, 2) head_token_kernel(co
                 else if (row0 + g == target) p.hit[lane] = z[g];
                 most = fmaxf(most, z[g]);
             }
-            const float base = most == -INFINITY ? 0.f : most * LOG2E;
+            const float m = most == -INFINITY ? 0.f : most;
+            const Base e(m);
             float s = 0.f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                if (row0 + g < p.cols) s += exp2_of(fmaf(z[g], LOG2E, -base));
-            join(ref, sum, base, s);
+                if (row0 + g < p.cols) s += exp2_of(fmaf(z[g], e.by, -e.base));
+            join(ref, sum, m, s * exp2_of(-e.rest(m)));
         }
     }
     if (lane < R) shares[warp][lane] = make_float2(ref, sum);
@@ -375,7 +393,7 @@ __global__ void __launch_bounds__(HJ_THREADS) head_join_kernel(const HeadJoinPar
     __syncthreads();
     if (threadIdx.x >= HJ_ROWS || row >= p.rows) return;
     for (int k = 1; k < HJ_THREADS / 32; ++k) join(ref, sum, share[k][x].x, share[k][x].y);
-    const float lse = sum == 0.f ? -INFINITY : fmaf(ref, LN2, logf(sum));
+    const float lse = sum == 0.f ? -INFINITY : ref + logf(sum);
     if (p.lse) p.lse[row] = lse;
     if (p.loss) {
         const long long t = target_of(p.targets, p.target64, row);

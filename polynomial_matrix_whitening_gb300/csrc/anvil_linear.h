@@ -164,7 +164,7 @@ struct GatedGradParams {
 };
 cudaError_t launch_gated_grad(const GatedGradParams& p, cudaStream_t stream);
 // The head: z = x W^T by tiles that are used and dropped (p.cols columns from column `first` of the vocabulary).
-// Statistics: of each row's 64 columns (M, S) with S = sum_j 2^(z_j log2(e) - M), and the target's z.
+// Statistics: of each row's 64 columns (m, S), the largest z and S = sum_j e^(z_j - m), and the target's z.
 // Gradient: out = g (e^(z - lse) - [j = target]) (times *scale), 16 bit.
 struct PairHeadParams : PairGemmParams {
     const void* targets;

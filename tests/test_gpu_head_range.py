@@ -6,8 +6,68 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_block_ops import A, make_weight, randn  # noqa: E402,F401
+from test_gpu_block_ops import A, E, make_weight, randn  # noqa: E402,F401
 from test_gpu_head import backward_check, make_targets  # noqa: E402
+
+
+SIZES = [3e3, 1.1e5, 1.3e6, 2.7e7, 7e8, 3.3e9, 5e12, 1e25, 3e37]
+
+
+def one_above(rows, vocab, size, transposed, sign):
+    """Logits of `size` or so, one per row above the others by a part in 128 at least; exact in fp32."""
+    x = torch.zeros(rows, 64, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(vocab, 64, device="cuda", dtype=torch.bfloat16)
+    if transposed:
+        w = torch.zeros(64, vocab, device="cuda", dtype=torch.bfloat16).t()
+    x[:, 0] = 2.0 ** int(math.log2(size) / 2)
+    w[:, 0] = sign * size / float(x[0, 0]) * (0.75 if sign > 0 else 1.5)
+    w[vocab // 3, 0] = sign * size / float(x[0, 0])
+    return x, w
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5, 40, 300, 900])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_large_logits(A, size, sign, transposed, rows):  # noqa: F811
+    """The sum is of one exponential of 0 and nothing else, so lse is that logit, to the bit."""
+    vocab = 700
+    x, w = one_above(rows, vocab, size, transposed, sign)
+    t = make_targets(3, rows, vocab)
+    t[rows // 2] = vocab // 3
+    loss, lse = A.linear_cross_entropy(x, w, t)
+    z = x.float() @ w.float().t()
+    most = z.amax(1)
+    assert torch.equal(lse, most)
+    want = torch.where(t >= 0, most - z.gather(1, t.clamp_min(0)[:, None])[:, 0], 0.0)
+    assert torch.equal(loss, want)
+    # d is -g and g, or 0 where the target is the largest
+    gl = randn(4, rows).abs() + 0.5
+    dx, dw = A.linear_cross_entropy_backward(x, w, t, lse, gl, dweight_dtype=torch.float32)
+    d = torch.zeros(rows, vocab, device="cuda", dtype=torch.float64)
+    live = torch.where(t >= 0, gl.double(), 0.0)
+    d[:, vocab // 3] += live
+    d.scatter_add_(1, t.clamp_min(0)[:, None], -live[:, None])
+    # d: its rounding to bf16 and the factor's three; results: bf16's, or the sums'
+    bar = 2.0 ** -8 + 16 * E
+    ref, mag = d.t() @ x.double(), d.abs().t() @ x.double().abs()
+    assert ((dw.double() - ref).abs() <= bar * mag + 80 * E * mag).all()
+    ref, mag = d @ w.double(), d.abs() @ w.double().abs()
+    assert ((dx.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (bar + 200 * E) * mag).all()
+
+
+@pytest.mark.parametrize("rows", [1, 4, 40, 300])
+def test_equal_large_logits(A, rows):  # noqa: F811
+    """Half of the vocabulary at one large value: its logarithm is within lse's last places."""
+    vocab = 700
+    for size in SIZES:
+        x, w = one_above(rows, vocab, size, False, 1)
+        w[::2, 0] = w[vocab // 3, 0].clone()
+        w[vocab // 3, 0] = 0.0  # (odd)
+        z = float(x[0, 0]) * float(w[0, 0])
+        _, lse = A.linear_cross_entropy(x, w)
+        want = z + math.log(350.0)
+        assert ((lse.double() - want).abs() <= E * want + 200 * E).all(), size
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
