@@ -524,7 +524,8 @@ anvil_status anvil_token_logprobs_backward(const anvil_logprob_grad_desc* desc, 
  * targets_int64 != 0), or NULL with loss NULL.  A negative target marks a position that does not
  * count: its loss is 0 (its lse is computed); one of vocab or more gives NaN.  A logit of -inf is a
  * token that cannot be; a row of nothing else has lse -inf and loss inf.  A row with a NaN or +inf
- * logit comes out NaN. */
+ * logit comes out NaN.  Logits are fp32 sums: of up to 1024 terms as the tensor cores add them, which cuts off
+ * (1e-6 of a logit's magnitude, towards 0), and of those sums rounded to nearest. */
 typedef struct {
     const void* x;
     const void* weight;

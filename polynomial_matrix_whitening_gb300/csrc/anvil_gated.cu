@@ -29,6 +29,7 @@ constexpr int GROUP_COLS = GATED_COLS / EPI_GROUPS;  // 32 columns of y per epil
 struct GatedPair {
     using Params = PairGatedParams;
     static constexpr bool MULTI = false, OWN = true, RANK_B = true, ONE_CHAIN = false;
+    static constexpr int CHAIN = 0;
     struct Row {};
     static __device__ __forceinline__ Row load(const Params&, const Unit&, int) { return {}; }
     // tacc: this warp's lanes, column 0 of the accumulator

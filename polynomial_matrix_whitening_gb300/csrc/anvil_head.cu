@@ -64,6 +64,7 @@ __device__ __forceinline__ int relative_target(const PairHeadParams& p, long lon
 struct StatsPair {
     using Params = PairHeadParams;
     static constexpr bool MULTI = false, OWN = true, RANK_B = false, ONE_CHAIN = false;
+    static constexpr int CHAIN = 0;
     struct Row {
         long long row;
         int target;
@@ -124,9 +125,56 @@ struct StatsPair {
     }
 };
 
+// The same of logits that are added up in registers, 1024 terms by the tensor cores at a time, for longer
+// contractions.  The tensor cores' sums are cut off, which takes about 1.3e-8 of a logit at every 16 terms: at k = 65536
+// one chain left lse 2.6e-4 too low (logits of deviation 2), this 3.5e-6.  512 terms would halve that, and cost 10% of the time
+// at 2048 x 32000 x 4096 where 1024 cost 4% (about 297, 309 and 323 us); up to 1024 one chain is taken, in the kernel above,
+// since the 64 sums of a thread hold its epilogue up (8192 x 50304 x 256: 173 us above, 187 here).
+struct StatsChains {
+    using Params = PairHeadParams;
+    static constexpr bool MULTI = false, OWN = true, RANK_B = false, ONE_CHAIN = false;
+    static constexpr int CHAIN = HEAD_CHAIN_KB;
+    using Row = StatsPair::Row;
+    static __device__ __forceinline__ Row load(const Params& p, const Unit& t, int r) { return StatsPair::load(p, t, r); }
+    // v: this thread's row of the columns from col0 on
+    static __device__ __forceinline__ void tile(const Params& p, float (&v)[EPI_COLS], const Unit& t, int col0, const Row& row) {
+        static_assert(EPI_COLS == HEAD_STATS_COLS, "one pair of statistics per group and row");
+        const int at = row.target - col0;
+        const bool mine = row.target >= 0 && at >= 0 && at < EPI_COLS;
+        if (__any_sync(0xffffffffu, mine)) {  // one warp and tile in twenty at a vocabulary of 50,000
+            float hit = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPI_COLS; ++i)
+                if (at == i) hit = v[i];
+            if (mine) p.hit[row.row] = hit;
+        }
+        const int live = p.cols - col0;  // columns that exist
+        if (live < EPI_COLS) {
+#pragma unroll
+            for (int i = 0; i < EPI_COLS; ++i)
+                if (i >= live) v[i] = -INFINITY;
+        }
+        float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int i = 4; i < EPI_COLS; ++i) m[i & 3] = fmaxf(m[i & 3], v[i]);
+        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));  // (NaN where all are, and so is the sum)
+        const float ref = most == -INFINITY ? 0.f : most;
+        const Base e(ref);
+        const uint64_t by = f2_make(e.by, e.by), less = f2_make(-e.base, -e.base);
+        uint64_t s[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; i += 2) s[i / 2 & 3] = f2_add(s[i / 2 & 3], exp2_of(f2_fma(f2_make(v[i], v[i + 1]), by, less)));
+        float s0, s1;
+        f2_split(f2_add(f2_add(s[0], s[1]), f2_add(s[2], s[3])), &s0, &s1);
+        if (row.row < p.rows)
+            p.stats[static_cast<long long>(col0 / EPI_COLS) * p.rows + row.row] = make_float2(ref, (s0 + s1) * exp2_of(-e.rest(ref)));
+    }
+};
+
 struct DlogitsPair {
     using Params = PairHeadParams;
     static constexpr bool MULTI = false, OWN = true, RANK_B = false, ONE_CHAIN = false;
+    static constexpr int CHAIN = 0;
     struct Row {
         float by, less;   // e^(z - lse) = 2^(z by + less) / one
         float one, g;     // d = (2^(z by + less) - [j = target] one) g
@@ -466,6 +514,7 @@ cudaError_t head_prepare() {
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return e
 #define ANVIL_HEAD(T)                                                                                    \
     ANVIL_SMEM((pair_gemm_kernel<T, STATS_BOX, StatsPair>), Staging<STATS_BOX>::SMEM);                   \
+    ANVIL_SMEM((pair_chain_kernel<T, STATS_BOX, StatsChains>), Staging<STATS_BOX>::SMEM);                \
     ANVIL_SMEM((pair_gemm_kernel<T, DLOGITS_BOX, DlogitsPair>), Staging<DLOGITS_BOX>::SMEM);             \
     ANVIL_SMEM((head_token_kernel<T, 1>), 4 * (HEAD_TOKEN_VALUES + 8));                                  \
     ANVIL_SMEM((head_token_kernel<T, 2>), 4 * (HEAD_TOKEN_VALUES + 16));                                 \
@@ -478,8 +527,15 @@ cudaError_t head_prepare() {
     return cudaSuccess;
 }
 
+namespace {
+template <typename T>
+cudaError_t pick_stats(const PairHeadParams& p, int sm_count, cudaStream_t s) {
+    return p.k > HEAD_CHAIN_KB * GEMM_BK ? run_pair<T, STATS_BOX, StatsChains>(p, sm_count, s) : run_pair<T, STATS_BOX, StatsPair>(p, sm_count, s);
+}
+}  // namespace
+
 cudaError_t launch_head_stats(const PairHeadParams& p, int sm_count, cudaStream_t s) {
-    return p.f16 ? run_pair<__half, STATS_BOX, StatsPair>(p, sm_count, s) : run_pair<__nv_bfloat16, STATS_BOX, StatsPair>(p, sm_count, s);
+    return p.f16 ? pick_stats<__half>(p, sm_count, s) : pick_stats<__nv_bfloat16>(p, sm_count, s);
 }
 
 cudaError_t launch_head_dlogits(const PairHeadParams& p, int sm_count, cudaStream_t s) {

@@ -72,6 +72,35 @@ __device__ __forceinline__ void tmem_ld_8(uint32_t taddr, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+        ",%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st_8(uint32_t taddr, const float (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
+        "r"(__float_as_uint(v[7])), "r"(taddr)
+        : "memory");
+}
+
 // kind::f16 instruction descriptor with fp32 accumulation; the operands' type is both
 // bf16 (1) or both fp16 (0).
 __host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool a_mn, bool b_mn, bool f16) {
@@ -228,18 +257,22 @@ __device__ __forceinline__ void add_bias(const GemmEpilogue& e, int col0, int co
 // What a variant of it computes.  OWN: its tiles' epilogue is its own (Row load(p, unit, row of the
 // CTA's 128), ahead of the accumulator, and tile()).  RANK_B: the pair's CTAs load operand B through a
 // map each, both from the same rows (the tile is as wide as one CTA's share).  ONE_CHAIN: an fp32 result
-// is one chain of products, as a 16-bit one is (it is on its way to 16 bits).
+// is one chain of products, as a 16-bit one is (it is on its way to 16 bits).  CHAIN: not 0 where tile() gets its
+// values added up from chains of so many k-blocks, as fp32 results are of CHAIN_KB.
 struct PlainPair {
     using Params = PairGemmParams;
     static constexpr bool MULTI = false, OWN = false, RANK_B = false, ONE_CHAIN = false;
+    static constexpr int CHAIN = 0;
 };
 struct SumPair {
     using Params = PairGemmParams;
     static constexpr bool MULTI = false, OWN = false, RANK_B = false, ONE_CHAIN = true;
+    static constexpr int CHAIN = 0;
 };
 struct MultiPair {
     using Params = PairMultiParams;
     static constexpr bool MULTI = true, OWN = false, RANK_B = false, ONE_CHAIN = false;
+    static constexpr int CHAIN = 0;
 };
 // The parameters of result `res` (0 or 1).
 __device__ __forceinline__ const GemmEpilogue& epi_of(const PairGemmParams& p, int) { return p.epi; }
@@ -553,8 +586,9 @@ __device__ __forceinline__ void store_f32(const P& p, EpiState& x, const float* 
 
 // T: type of 16-bit results (float: fp32 results, taken in chains of CHAIN_KB k-blocks)
 template <typename T, int W, typename M>
-__global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid_constant__ typename M::Params p) {
-    constexpr bool F32 = sizeof(T) == 4 && !M::ONE_CHAIN;
+__device__ __forceinline__ void pair_gemm(const typename M::Params& p) {
+    constexpr bool F32 = (sizeof(T) == 4 && !M::ONE_CHAIN) || M::CHAIN > 0;
+    constexpr int CHAIN = M::CHAIN > 0 ? M::CHAIN : CHAIN_KB;
     constexpr int STAGES = Staging<W>::STAGES, COLS4 = W / 4;  // fp32 columns of a box
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[STAGES];
@@ -687,8 +721,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
             bool ready = false, ok = true;
             for (int u = pair; u < units && ok; u += npairs) {
                 const int nkb = u < p.split.whole ? whole_kb : unit_of(p, u).nkb;
-                for (int c0 = 0; c0 < nkb && ok; c0 += F32 ? CHAIN_KB : nkb, ++acc) {
-                    const int cn = F32 ? min(CHAIN_KB, nkb - c0) : nkb;
+                for (int c0 = 0; c0 < nkb && ok; c0 += F32 ? CHAIN : nkb, ++acc) {
+                    const int cn = F32 ? min(CHAIN, nkb - c0) : nkb;
                     const int ab = acc & 1;
                     if (!mbar_wait(&tempty_bar[ab], ((acc >> 1) & 1) ^ 1, p.err)) {
                         ok = false;
@@ -758,10 +792,25 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
             const int col0 = t.tc * BN + lcol;
             const uint32_t tlane = tmem + (static_cast<uint32_t>(x.quad * 32) << 16) + static_cast<uint32_t>(lcol);
             if constexpr (F32) {
+                [[maybe_unused]] const auto row = [&] {
+                    if constexpr (M::OWN) return M::load(p, t, lrow + x.r);
+                    else return 0;
+                }();
                 float sum[EPI_COLS];
+                int c0 = 0;
+                if constexpr (M::OWN) {  // the first chain as it is
+                    const int ab = acc & 1;
+                    if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
+                    tc_fence_after();
+                    tmem_ld_64(tlane + ab * BN, sum);
+                    release_acc(x, te[ab]);
+                    c0 = CHAIN;
+                    ++acc;
+                } else {
 #pragma unroll
-                for (int i = 0; i < EPI_COLS; ++i) sum[i] = 0.f;
-                for (int c0 = 0; c0 < t.nkb; c0 += CHAIN_KB, ++acc) {
+                    for (int i = 0; i < EPI_COLS; ++i) sum[i] = 0.f;
+                }
+                for (; c0 < t.nkb; c0 += CHAIN, ++acc) {
                     const int ab = acc & 1;
                     if (!mbar_wait(&tfull_bar[ab], (acc >> 1) & 1, p.err)) x.fail = true;
                     tc_fence_after();
@@ -774,9 +823,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
                     }
                     release_acc(x, te[ab]);
                 }
+                if constexpr (M::OWN) {
+                    M::tile(p, sum, t, col0, row);
+                } else {
 #pragma unroll
-                for (int q = 0; q < EPI_COLS / COLS4; ++q)
-                    store_f32<W, M::MULTI>(p, x, sum + COLS4 * q, t.part, lrow, lcol + COLS4 * q, row0, col0 + COLS4 * q, res);
+                    for (int q = 0; q < EPI_COLS / COLS4; ++q)
+                        store_f32<W, M::MULTI>(p, x, sum + COLS4 * q, t.part, lrow, lcol + COLS4 * q, row0, col0 + COLS4 * q, res);
+                }
             } else {
                 const int ab = acc & 1;
                 if constexpr (M::OWN) {
@@ -830,6 +883,16 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid
     if (warp == 1) tmem_dealloc_pair(tmem, PAIR_TMEM);
     if (p.overlap_previous) pdl_wait_previous();
 }
+template <typename T, int W, typename M>
+__global__ void __launch_bounds__(PAIR_THREADS, 1) pair_gemm_kernel(const __grid_constant__ typename M::Params p) {
+    pair_gemm<T, W, M>(p);
+}
+// The same in fewer registers than a block of its own may have, so that blocks of the kernel behind it are ready
+// beside it.
+template <typename T, int W, typename M>
+__global__ void __maxnreg__(88) pair_chain_kernel(const __grid_constant__ typename M::Params p) {
+    pair_gemm<T, W, M>(p);
+}
 
 template <typename T, int W, typename M>
 cudaError_t run_pair(const typename M::Params& p, int sm_count, cudaStream_t s) {
@@ -848,7 +911,8 @@ cudaError_t run_pair(const typename M::Params& p, int sm_count, cudaStream_t s) 
     cfg.numAttrs = 2;
     const int most = sm_count / 2;
     cfg.gridDim = dim3(2 * (p.units < most ? p.units : most));
-    return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<T, W, M>, p);
+    if constexpr (M::CHAIN > 0) return cudaLaunchKernelEx(&cfg, pair_chain_kernel<T, W, M>, p);
+    else return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<T, W, M>, p);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -906,7 +970,10 @@ __device__ __forceinline__ void finish_rows(const GemmEpilogue& e, float (&v)[N]
 }
 
 // What a variant of the row kernel computes.  HEAD: its eight results of a thread at a time go to
-// finish(p, v, column, exists, first row, rows, this block's shared memory), and the block's to end().
+// finish(p, v, column, exists, first row, rows, this block's shared memory), and the block's to end(); they are
+// fp32 results, so the products are taken in chains of HEAD_CHAIN_KB k-blocks: the first in the accumulator that is
+// finished, the others in two more by turns, which are added to it (in tensor memory: a thread's registers would
+// leave room for two blocks an SM), the last one on the way out.
 // GATED: its 128 weight rows are 64 of one weight (TMEM lanes 0 to 63) and the same 64 of another,
 // whose results finish one element together.
 struct PlainRows {
@@ -972,9 +1039,12 @@ __global__ void __launch_bounds__(ROW_THREADS, BN <= ROW_TWO_TOKENS ? M::BLOCKS 
     __shared__ __align__(8) uint64_t full_bar[S::STAGES];
     __shared__ __align__(8) uint64_t empty_bar[S::STAGES];
     __shared__ __align__(8) uint64_t done_bar;
+    __shared__ __align__(8) uint64_t tfull_bar[2];   // HEAD: the products of a chain but the first are done,
+    __shared__ __align__(8) uint64_t tempty_bar[2];  //       and added up
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int aborted;
     __shared__ volatile int armed[S::STAGES];  // 1 + the k-block last loaded into each stage (0: none)
+    constexpr uint32_t TMEM_COLS = M::HEAD ? 4 * BN : S::TMEM_COLS;
     __shared__ float2 stats[M::HEAD ? 4 : 1][M::HEAD ? BN : 1];
 
     pdl_allow_next();
@@ -995,12 +1065,18 @@ __global__ void __launch_bounds__(ROW_THREADS, BN <= ROW_TWO_TOKENS ? M::BLOCKS 
             armed[s] = 0;
         }
         mbar_init(&done_bar, 1);
+        if constexpr (M::HEAD) {
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&tfull_bar[b], 1);
+                mbar_init(&tempty_bar[b], 4);  // each epilogue warp
+            }
+        }
         fence_mbar_init();
         aborted = 0;
         tma_prefetch_desc(&p.tm_a);
         tma_prefetch_desc(&p.tm_b);
     }
-    if (warp == 1) tmem_alloc(&tmem_slot, S::TMEM_COLS);
+    if (warp == 1) tmem_alloc(&tmem_slot, TMEM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1041,6 +1117,12 @@ __global__ void __launch_bounds__(ROW_THREADS, BN <= ROW_TWO_TOKENS ? M::BLOCKS 
             uint32_t ph = 0;
             bool ready = false;
             for (int it = 0; it < nkb; ++it) {
+                const int chain = M::HEAD ? it / HEAD_CHAIN_KB - 1 : -1, in_chain = M::HEAD ? it % HEAD_CHAIN_KB : it, ab = chain & 1;
+                const uint32_t dacc = chain < 0 ? tmem : tmem + (1 + ab) * BN;
+                if (chain >= 0 && in_chain == 0 && !mbar_wait(&tempty_bar[ab], ((chain >> 1) & 1) ^ 1, p.err)) {
+                    aborted = 1;
+                    break;
+                }
                 if (!ready && !mbar_wait(&full_bar[s], ph, p.err)) {
                     aborted = 1;
                     break;
@@ -1050,12 +1132,13 @@ __global__ void __launch_bounds__(ROW_THREADS, BN <= ROW_TWO_TOKENS ? M::BLOCKS 
                 const uint32_t a_lo = sw128_desc_lo(sa, a_lbo), b_lo = sw128_desc_lo(sa + A_STAGE, 16);
 #pragma unroll
                 for (int kk = 0; kk < GEMM_BK / 16; ++kk)
-                    umma_bf16(tmem, sw128_desc(a_lo + kk * a_step), sw128_desc(b_lo + kk * (32 >> 4)), idesc,
-                              (it | kk) != 0 ? 1u : 0u);
+                    umma_bf16(dacc, sw128_desc(a_lo + kk * a_step), sw128_desc(b_lo + kk * (32 >> 4)), idesc,
+                              (in_chain | kk) != 0 ? 1u : 0u);
                 const int s_next = s + 1 == stages ? 0 : s + 1;
                 const uint32_t ph_next = s_next == 0 ? ph ^ 1u : ph;
                 ready = mbar_test_wait(smem_u32(&full_bar[s_next]), ph_next);
                 umma_commit(&empty_bar[s]);
+                if (chain >= 0 && in_chain == HEAD_CHAIN_KB - 1) umma_commit(&tfull_bar[ab]);
                 s = s_next;
                 ph = ph_next;
             }
@@ -1073,13 +1156,45 @@ __global__ void __launch_bounds__(ROW_THREADS, BN <= ROW_TWO_TOKENS ? M::BLOCKS 
         float bias = 0.f;
         if (live && p.epi.bias)
             bias = p.epi.bias_f32 ? static_cast<const float*>(p.epi.bias)[col] : Elem<T>::load(static_cast<const T*>(p.epi.bias)[col]);
+        const int later = M::HEAD ? (nkb - 1) / HEAD_CHAIN_KB : 0;  // chains but the first
+        for (int c = 0; c < later - 1; ++c) {
+            const int ab = c & 1;
+            const bool done = mbar_wait(&tfull_bar[ab], (c >> 1) & 1, p.err);
+            if (__any_sync(0xffffffffu, !done)) {  // (the loads below take whole warps)
+                aborted = 1;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < BN; q += 8) {
+                float v[8], more[8];
+                tmem_ld_8(tlane + q, v);
+                tmem_ld_8(tlane + (1 + ab) * BN + q, more);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += more[i];
+                tmem_st_8(tlane + q, v);
+            }
+            // (as release_acc: the loads have completed, and nothing else is ordered by it)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(&tempty_bar[ab]);
+        }
         mbar_wait(&done_bar, 0, p.err);
         tc_fence_after();
+        const auto results = [&](int q, float (&v)[8]) {  // of eight B rows
+            tmem_ld_8(tlane + q, v);
+            if (M::HEAD && later > 0) {
+                float more[8];
+                tmem_ld_8(tlane + (1 + ((later - 1) & 1)) * BN + q, more);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += more[i];
+            }
+        };
         if (!M::GATED && p.splits == 1) {
 #pragma unroll 1
             for (int q = 0; q < nb; q += 8) {
                 float v[8];
-                tmem_ld_8(tlane + q, v);
+                results(q, v);
                 if constexpr (M::HEAD) M::finish(p, v, col, live, b0 + q, nb - q, &stats[quad][q]);
                 else if (live) finish_rows<T, 8>(p.epi, v, bias, b0 + q, nb - q, col);
             }
@@ -1091,7 +1206,7 @@ __global__ void __launch_bounds__(ROW_THREADS, BN <= ROW_TWO_TOKENS ? M::BLOCKS 
 #pragma unroll 1
             for (int q = 0; q < quads; q += 2) {
                 float v[8];
-                tmem_ld_8(tlane + q * 4, v);
+                results(q * 4, v);
                 own[q * ROW_TILE_A + r] = make_float4(v[0], v[1], v[2], v[3]);
                 own[(q + 1) * ROW_TILE_A + r] = make_float4(v[4], v[5], v[6], v[7]);
             }
@@ -1139,7 +1254,7 @@ __global__ void __launch_bounds__(ROW_THREADS, BN <= ROW_TWO_TOKENS ? M::BLOCKS 
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, S::TMEM_COLS);
+    if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
 }
 
 template <typename T, int BN, typename M>

@@ -177,6 +177,7 @@ struct PairHeadParams : PairGemmParams {
     const float* scale;
 };
 constexpr int HEAD_STATS_COLS = 64;  // columns behind one pair of statistics
+constexpr int HEAD_CHAIN_KB = 16;    // k-blocks of a chain of the logits behind loss and lse
 // The same for few rows: statistics [blocks of 128 columns][rows].
 struct RowHeadParams : RowGemmParams {
     const void* targets;

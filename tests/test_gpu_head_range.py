@@ -1,4 +1,5 @@
-"""GPU tests of the head's cross entropy at the ends of its range, against 64 bits."""
+"""GPU tests of the head's cross entropy at the ends of its range: long contractions, logits beyond what their
+multiples of log2(e) resolve, row gradients that are not finite.  Against 64 bits."""
 import math
 
 import pytest
@@ -8,6 +9,40 @@ pytestmark = pytest.mark.gpu
 
 from test_gpu_block_ops import A, E, make_weight, randn  # noqa: E402,F401
 from test_gpu_head import backward_check, make_targets  # noqa: E402
+
+
+def uniform(seed, *shape, lo, hi, dtype):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.rand(*shape, generator=g, device="cuda") * (hi - lo) + lo).to({"bf16": torch.bfloat16, "f16": torch.float16}[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("rows", [1, 2, 3, 16, 20, 32, 33, 300, 700])
+@pytest.mark.parametrize("k", [512, 777, 4096, 16391, 65536])
+def test_long_contractions(A, k, rows, transposed, dtype):  # noqa: F811
+    """Products of one sign, where sums that are cut off drift the same way: the tensor cores' sums end after 1024
+    terms and are added up rounded to nearest."""
+    vocab = 1000
+    x = uniform(1, rows, k, lo=0.5, hi=1.5, dtype=dtype)
+    w = uniform(2, vocab, k, lo=5.0 / k, hi=15.0 / k, dtype=dtype)
+    if transposed:
+        w = w.t().contiguous().t()
+    t = make_targets(3, rows, vocab)
+    loss, lse = A.linear_cross_entropy(x, w, t)
+    z = x.double() @ w.double().t()  # every product is positive: its own magnitude
+    # chains of 64 steps at 2 E each and the chains' sum
+    ez = (2 * (64 + 4) + k / 1024 + 8) * E * z
+    want = torch.logsumexp(z, 1)
+    p = torch.exp(z - want[:, None])
+    parts = math.ceil(vocab / 256) * 4
+    bar = (p * ez).sum(1) + E * (4 + 2 + 24 + 11 * (parts / 8 + 9) + 4 * want.abs() + 4)  # forward_check's arithmetic
+    assert ((lse.double() - want).abs() <= 1.01 * bar).all(), float(((lse.double() - want).abs() / bar).max())
+    live = t >= 0
+    at = t.clamp_min(0)[:, None]
+    ref = want - z.gather(1, at)[:, 0]
+    bar = bar + ez.gather(1, at)[:, 0] + 2 * E * ref.abs()
+    assert ((loss.double() - ref).abs() <= 1.01 * bar)[live].all()
 
 
 SIZES = [3e3, 1.1e5, 1.3e6, 2.7e7, 7e8, 3.3e9, 5e12, 1e25, 3e37]
