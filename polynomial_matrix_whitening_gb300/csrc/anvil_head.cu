@@ -137,7 +137,8 @@ struct StatsChains {
     using Row = StatsPair::Row;
     static __device__ __forceinline__ Row load(const Params& p, const Unit& t, int r) { return StatsPair::load(p, t, r); }
     // v: this thread's row of the columns from col0 on
-    static __device__ __forceinline__ void tile(const Params& p, float (&v)[EPI_COLS], const Unit& t, int col0, const Row& row) {
+    template <typename T, int W>
+    static __device__ __forceinline__ void tile(const Params& p, EpiState&, float (&v)[EPI_COLS], int, int col0, const Row& row) {
         static_assert(EPI_COLS == HEAD_STATS_COLS, "one pair of statistics per group and row");
         const int at = row.target - col0;
         const bool mine = row.target >= 0 && at >= 0 && at < EPI_COLS;
@@ -199,6 +200,35 @@ struct DlogitsPair {
         }
         return x;
     }
+    // Sixteen logits from column c of the box on; hot: the target's number among them, if it is.
+    template <typename T, int W>
+    static __device__ __forceinline__ void sixteen(const EpiState& x, float (&v)[16], int c, int hot, const Row& row) {
+        const uint64_t by = f2_make(row.by, row.by), less = f2_make(row.less, row.less), g = f2_make(row.g, row.g);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) f2_split(exp2_of(f2_fma(f2_make(v[i], v[i + 1]), by, less)), &v[i], &v[i + 1]);
+        if (row.target >= 0 && hot >= 0 && hot < 16) {  // one warp and sixteen columns in a hundred, of 50,000
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (hot == i) v[i] -= row.one;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint64_t d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = f2_mul(f2_make(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]), g);
+            uint4 w = Elem<T>::pack_pairs(d);
+            w.x &= row.counts;
+            w.y &= row.counts;
+            w.z &= row.counts;
+            w.w &= row.counts;
+            sts128(Staging<W>::addr(x.box, x.r, c / 8 + j), w);
+        }
+    }
+    // (the buffer's rows go on in eights: no box ends inside 16 bytes)
+    template <int W>
+    static __device__ __forceinline__ void send(const Params& p, const EpiState& x, int row0, int col) {
+        send_box<uint16_t, W, true>(x, &p.tm_out, 1, p.epi.out, p.epi.ldout, row0, col, p.rows, (p.cols + 7) & ~7);
+    }
     template <typename T, int W>
     static __device__ __forceinline__ void tile(const Params& p, EpiState& x, uint32_t tacc, uint32_t tempty, const Unit& t,
                                                 int row0, const Row& row) {
@@ -213,31 +243,34 @@ struct DlogitsPair {
             for (int c = 0; c < COLS; c += 16) {
                 float v[16];
                 tmem_ld_16(ta + b * COLS + c, v);
-                const uint64_t by = f2_make(row.by, row.by), less = f2_make(row.less, row.less), g = f2_make(row.g, row.g);
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) f2_split(exp2_of(f2_fma(f2_make(v[i], v[i + 1]), by, less)), &v[i], &v[i + 1]);
-                const int hot = at - (b * COLS + c);
-                if (row.target >= 0 && hot >= 0 && hot < 16) {  // one warp and sixteen columns in a hundred, of 50,000
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (hot == i) v[i] -= row.one;
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint64_t d[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[i] = f2_mul(f2_make(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]), g);
-                    uint4 w = Elem<T>::pack_pairs(d);
-                    w.x &= row.counts;
-                    w.y &= row.counts;
-                    w.z &= row.counts;
-                    w.w &= row.counts;
-                    sts128(Staging<W>::addr(x.box, x.r, c / 8 + j), w);
-                }
+                sixteen<T, W>(x, v, c, at - (b * COLS + c), row);
             }
             if (b == N - 1) release_acc(x, tempty);
-            // (the buffer's rows go on in eights: no box ends inside 16 bytes)
-            send_box<uint16_t, W, true>(x, &p.tm_out, 1, p.epi.out, p.epi.ldout, row0, col0 + b * COLS, p.rows, (p.cols + 7) & ~7);
+            send<W>(p, x, row0, col0 + b * COLS);
+        }
+    }
+};
+
+// The same of the logits that StatsChains takes (from one chain the probabilities would not fit lse: at k = 65536
+// they would be 0.1% off).
+struct DlogitsChains {
+    using Params = PairHeadParams;
+    static constexpr bool MULTI = false, OWN = true, RANK_B = false, ONE_CHAIN = false;
+    static constexpr int CHAIN = HEAD_CHAIN_KB;
+    using Row = DlogitsPair::Row;
+    static __device__ __forceinline__ Row load(const Params& p, const Unit& t, int r) { return DlogitsPair::load(p, t, r); }
+    template <typename T, int W>
+    static __device__ __forceinline__ void tile(const Params& p, EpiState& x, float (&v)[EPI_COLS], int row0, int col0, const Row& row) {
+        constexpr int COLS = W / 2;
+        const int at = row.target - col0;
+#pragma unroll
+        for (int c = 0; c < EPI_COLS; c += 16) {
+            if (c % COLS == 0) box_free(x);
+            float u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = v[c + i];
+            DlogitsPair::sixteen<T, W>(x, u, c % COLS, at - c, row);
+            if (c % COLS == COLS - 16) DlogitsPair::send<W>(p, x, row0, col0 + c - c % COLS);
         }
     }
 };
@@ -516,6 +549,7 @@ cudaError_t head_prepare() {
     ANVIL_SMEM((pair_gemm_kernel<T, STATS_BOX, StatsPair>), Staging<STATS_BOX>::SMEM);                   \
     ANVIL_SMEM((pair_chain_kernel<T, STATS_BOX, StatsChains>), Staging<STATS_BOX>::SMEM);                \
     ANVIL_SMEM((pair_gemm_kernel<T, DLOGITS_BOX, DlogitsPair>), Staging<DLOGITS_BOX>::SMEM);             \
+    ANVIL_SMEM((pair_chain_kernel<T, DLOGITS_BOX, DlogitsChains>), Staging<DLOGITS_BOX>::SMEM);          \
     ANVIL_SMEM((head_token_kernel<T, 1>), 4 * (HEAD_TOKEN_VALUES + 8));                                  \
     ANVIL_SMEM((head_token_kernel<T, 2>), 4 * (HEAD_TOKEN_VALUES + 16));                                 \
     ANVIL_SMEM((row_gemm_kernel<T, 16, HeadRows>), RowShape<16>::smem(RowShape<16>::STAGES));            \
@@ -528,19 +562,20 @@ cudaError_t head_prepare() {
 }
 
 namespace {
-template <typename T>
-cudaError_t pick_stats(const PairHeadParams& p, int sm_count, cudaStream_t s) {
-    return p.k > HEAD_CHAIN_KB * GEMM_BK ? run_pair<T, STATS_BOX, StatsChains>(p, sm_count, s) : run_pair<T, STATS_BOX, StatsPair>(p, sm_count, s);
+template <typename T, int W, typename ONE, typename CHAINS>
+cudaError_t run_logits(const PairHeadParams& p, int sm_count, cudaStream_t s) {
+    return p.k > HEAD_CHAIN_KB * GEMM_BK ? run_pair<T, W, CHAINS>(p, sm_count, s) : run_pair<T, W, ONE>(p, sm_count, s);
 }
 }  // namespace
 
 cudaError_t launch_head_stats(const PairHeadParams& p, int sm_count, cudaStream_t s) {
-    return p.f16 ? pick_stats<__half>(p, sm_count, s) : pick_stats<__nv_bfloat16>(p, sm_count, s);
+    return p.f16 ? run_logits<__half, STATS_BOX, StatsPair, StatsChains>(p, sm_count, s)
+                 : run_logits<__nv_bfloat16, STATS_BOX, StatsPair, StatsChains>(p, sm_count, s);
 }
 
 cudaError_t launch_head_dlogits(const PairHeadParams& p, int sm_count, cudaStream_t s) {
-    return p.f16 ? run_pair<__half, DLOGITS_BOX, DlogitsPair>(p, sm_count, s)
-                 : run_pair<__nv_bfloat16, DLOGITS_BOX, DlogitsPair>(p, sm_count, s);
+    return p.f16 ? run_logits<__half, DLOGITS_BOX, DlogitsPair, DlogitsChains>(p, sm_count, s)
+                 : run_logits<__nv_bfloat16, DLOGITS_BOX, DlogitsPair, DlogitsChains>(p, sm_count, s);
 }
 
 namespace {

@@ -824,7 +824,7 @@ __device__ __forceinline__ void pair_gemm(const typename M::Params& p) {
                     release_acc(x, te[ab]);
                 }
                 if constexpr (M::OWN) {
-                    M::tile(p, sum, t, col0, row);
+                    M::template tile<T, W>(p, x, sum, row0, col0, row);
                 } else {
 #pragma unroll
                     for (int q = 0; q < EPI_COLS / COLS4; ++q)

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_block_ops import A, E, make_weight, randn  # noqa: E402,F401
+from test_gpu_block_ops import A, E, U, close, make_weight, randn  # noqa: E402,F401
 from test_gpu_head import backward_check, make_targets  # noqa: E402
 
 
@@ -43,6 +43,36 @@ def test_long_contractions(A, k, rows, transposed, dtype):  # noqa: F811
     ref = want - z.gather(1, at)[:, 0]
     bar = bar + ez.gather(1, at)[:, 0] + 2 * E * ref.abs()
     assert ((loss.double() - ref).abs() <= 1.01 * bar)[live].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("rows", [1, 40, 300])
+@pytest.mark.parametrize("k", [1024, 1100, 16391, 65536])
+def test_gradients_of_long_contractions(A, k, rows, transposed, dtype):  # noqa: F811
+    """The gradient's logits are added up as the forward pass's, or the probabilities would not fit lse."""
+    vocab = 1000
+    x = uniform(1, rows, k, lo=0.5, hi=1.5, dtype=dtype)
+    w = uniform(2, vocab, k, lo=5.0 / k, hi=15.0 / k, dtype=dtype)
+    if transposed:
+        w = w.t().contiguous().t()
+    t, gl = make_targets(3, rows, vocab), randn(4, rows).abs() + 0.5
+    _, lse = A.linear_cross_entropy(x, w, t)
+    dx, dw = A.linear_cross_entropy_backward(x, w, t, lse, gl, dweight_dtype=torch.float32)
+    z = x.double() @ w.double().t()
+    ez = (2 * (64 + 4) + k / 1024 + 8) * E * z  # as above
+    g = torch.where(t >= 0, gl.double(), 0.0)[:, None]
+    p = torch.exp(z - lse.double()[:, None])
+    d = (g * p).scatter_add(1, t.clamp_min(0)[:, None], -g)
+    # backward_check's: p's and d's errors, the products' sums
+    ep = p * (ez + 3 * E * (z + lse.double().abs()[:, None]) + 8 * E)
+    ed = g * ep * 1.01 + (5 * E + U[dtype]) * d.abs()
+    if dtype == "f16":
+        ed = ed + 2.0 ** -38 * float(g.max()) * (g != 0)
+    c = 2 * (vocab / 16 + 8)
+    close(dx, d @ w.double(), dtype, d.abs() @ w.double() + ed @ w.double() / E / c, c, "dx")
+    c = 2 * 36 + rows / 512 + 8
+    close(dw, d.t() @ x.double(), "f32", d.abs().t() @ x.double() + ed.t() @ x.double() / E / c, c, "dweight")
 
 
 SIZES = [3e3, 1.1e5, 1.3e6, 2.7e7, 7e8, 3.3e9, 5e12, 1e25, 3e37]
