@@ -456,6 +456,11 @@ PyObject* linear_backward(PyObject* const* a) {
     return tuple_of(std::move(dx), std::move(dw), std::move(db));
 }
 
+// A tensor of the caller's that a call has written to: a graph that saved it would use the new values.
+void overwritten(const at::Tensor* t) {
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // ---------------------------------------------------------------- the gated layer
 // The order (0 by rows, 1 by columns) that every given matrix of gate's shape is stored in.
 int common_order(const at::Tensor& gate, at::ScalarType type, int64_t k, std::initializer_list<const at::Tensor*> others) {
@@ -507,6 +512,7 @@ PyObject* gated_linear_forward(PyObject* const* a) {
     d.k = as_int(r.width, "gate");
     const Scratch scratch(ws ? 0 : api.gated_linear_workspace_bytes(&d), ws, here);
     check(api.gated_linear_forward(&d, scratch.p, scratch.bytes, here.stream), "anvil_gated_linear_forward");
+    overwritten(out);
     return tuple_of(std::move(y), std::move(g), std::move(u));
 }
 
@@ -576,6 +582,10 @@ PyObject* gated_linear_backward(PyObject* const* a) {
     if (truth(a[14])) d.activation |= ANVIL_DZ_TWO_PARTS;
     const Scratch scratch(ws ? 0 : api.gated_linear_backward_workspace_bytes(&d), ws, here);
     check(api.gated_linear_backward(&d, scratch.p, scratch.bytes, here.stream), "anvil_gated_linear_backward");
+    if (need_dw) {
+        overwritten(dg_in);
+        overwritten(du_in);
+    }
     return tuple_of(std::move(dx), std::move(dg), std::move(du));
 }
 
@@ -737,6 +747,7 @@ PyObject* linear_cross_entropy_backward(PyObject* const* a) {
     d.dweight_dtype = wt == type ? d.dtype : ANVIL_F32;
     const Scratch scratch(ws ? 0 : api.linear_cross_entropy_backward_workspace_bytes(&d), ws, here);
     check(api.linear_cross_entropy_backward(&d, scratch.p, scratch.bytes, here.stream), "anvil_linear_cross_entropy_backward");
+    if (need_dw) overwritten(dw_in);
     return tuple_of(std::move(dx), std::move(dw));
 }
 
@@ -773,9 +784,6 @@ void check_codes(const at::Tensor& m, const at::Tensor& v, const at::Tensor& sca
     const int64_t blocks = (count + ANVIL_ADAMW_BLOCK - 1) / ANVIL_ADAMW_BLOCK;
     plain_tensor(scales, device, 2 * blocks, where, "scales, [2, blocks],");
     if (scales.scalar_type() != at::kFloat) refuse("%s: scales must be fp32", where);
-}
-void overwritten(const at::Tensor& t) {
-    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();  // (a graph that saved it would use the new values)
 }
 at::Device current(const char* where, const at::Tensor* first) {
     if (!first || !first->is_cuda()) refuse("%s: every tensor must be on the current CUDA device", where);
@@ -838,7 +846,8 @@ PyObject* adamw_step(PyObject* const* a) {
     }
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     check(api.adamw_step(tensors.data(), static_cast<int>(params.n), &c, ds, stream), "anvil_adamw_step");
-    for (Py_ssize_t i = 0; i < params.n; ++i) overwritten(*params.at(i));
+    for (const Tensors* part : {&params, &ms, &vs, &lows, &scales})
+        for (Py_ssize_t i = 0; i < params.n; ++i) overwritten(part->at(i));
     return Py_NewRef(Py_None);
 }
 
@@ -865,6 +874,8 @@ PyObject* adamw_values(PyObject* const* a) {
     }
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     check(api.adamw_values(states.data(), static_cast<int>(ms.n), stream), "anvil_adamw_values");
+    for (const Tensors* part : {&om, &ov})
+        for (Py_ssize_t i = 0; i < ms.n; ++i) overwritten(part->at(i));
     return Py_NewRef(Py_None);
 }
 
