@@ -461,6 +461,18 @@ void overwritten(const at::Tensor* t) {
     if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
+// The same for many tensors, known before the call.
+struct Written {
+    std::vector<c10::TensorImpl*> all;
+    explicit Written(Py_ssize_t most) { all.reserve(static_cast<size_t>(most)); }
+    void add(const at::Tensor* t) {
+        if (t && !t->is_inference()) all.push_back(t->unsafeGetTensorImpl());
+    }
+    void done() const {
+        for (c10::TensorImpl* t : all) t->bump_version();
+    }
+};
+
 // ---------------------------------------------------------------- the gated layer
 // The order (0 by rows, 1 by columns) that every given matrix of gate's shape is stored in.
 int common_order(const at::Tensor& gate, at::ScalarType type, int64_t k, std::initializer_list<const at::Tensor*> others) {
@@ -808,6 +820,7 @@ PyObject* adamw_step(PyObject* const* a) {
     if (!params.n) return Py_NewRef(Py_None);
     const at::Device device = current(where, params.at(0));
     std::vector<anvil_adamw_tensor> tensors(static_cast<size_t>(params.n));
+    Written written(5 * params.n);
     for (Py_ssize_t i = 0; i < params.n; ++i) {
         const at::Tensor &p = *params.at(i), &g = *grads.at(i), &m = *ms.at(i), &v = *vs.at(i);
         const at::Tensor *low = lows.at(i), *sc = scales.at(i);
@@ -837,6 +850,7 @@ PyObject* adamw_step(PyObject* const* a) {
         t.exp_avg_sq = v.data_ptr();
         t.scales = sc ? static_cast<float*>(sc->data_ptr()) : nullptr;
         t.count = count;
+        for (const at::Tensor* w : {&p, &m, &v, low, sc}) written.add(w);
     }
     const float* ds = nullptr;
     if (scalars) {
@@ -846,8 +860,7 @@ PyObject* adamw_step(PyObject* const* a) {
     }
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     check(api.adamw_step(tensors.data(), static_cast<int>(params.n), &c, ds, stream), "anvil_adamw_step");
-    for (const Tensors* part : {&params, &ms, &vs, &lows, &scales})
-        for (Py_ssize_t i = 0; i < params.n; ++i) overwritten(part->at(i));
+    written.done();
     return Py_NewRef(Py_None);
 }
 
@@ -860,6 +873,7 @@ PyObject* adamw_values(PyObject* const* a) {
     if (!ms.n) return Py_NewRef(Py_None);
     const at::Device device = current(where, ms.at(0));
     std::vector<anvil_adamw_state> states(static_cast<size_t>(ms.n));
+    Written written(2 * ms.n);
     for (Py_ssize_t i = 0; i < ms.n; ++i) {
         const at::Tensor &m = *ms.at(i), &v = *vs.at(i), &sc = *scales.at(i), &to_m = *om.at(i), &to_v = *ov.at(i);
         const int64_t count = m.numel();
@@ -871,11 +885,12 @@ PyObject* adamw_values(PyObject* const* a) {
         if (to_m.scalar_type() != at::kFloat || to_v.scalar_type() != at::kFloat) refuse("adamw_values: out must be fp32");
         states[static_cast<size_t>(i)] = {m.data_ptr(), v.data_ptr(), static_cast<const float*>(sc.data_ptr()),
                                           static_cast<float*>(to_m.data_ptr()), static_cast<float*>(to_v.data_ptr()), count};
+        written.add(&to_m);
+        written.add(&to_v);
     }
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     check(api.adamw_values(states.data(), static_cast<int>(ms.n), stream), "anvil_adamw_values");
-    for (const Tensors* part : {&om, &ov})
-        for (Py_ssize_t i = 0; i < ms.n; ++i) overwritten(part->at(i));
+    written.done();
     return Py_NewRef(Py_None);
 }
 
