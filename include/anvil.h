@@ -261,7 +261,8 @@ typedef struct {
 /* d_scalars: NULL, or a DEVICE array of four fp32 that is read when the step runs in place of
  * config's lr, weight_decay, grad_scale and step: step_size, root, decay, grad_scale, as
  * anvil_adamw_scalars (host only) gives them; a captured graph then follows the schedule.  One
- * launch per kind of tensor (types, codes) and 448 tensors; allocates no device memory. */
+ * launch per kind of tensor (types, codes, all its arrays on boundaries of four elements or not; few of those
+ * that are go with those that are not) and 448 tensors; allocates no device memory. */
 anvil_status anvil_adamw_step(const anvil_adamw_tensor* tensors, int ntensors, const anvil_adamw_config* config,
                               const float* d_scalars, void* stream);
 anvil_status anvil_adamw_scalars(const anvil_adamw_config* config, float* scalars);

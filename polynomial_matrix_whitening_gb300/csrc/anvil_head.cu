@@ -7,13 +7,13 @@
 // Forward: the pair kernel (anvil_linear.cuh), whose epilogue takes each tile's logits out of tensor
 // memory once and leaves, per row and 64 columns, their maximum and the sum of their exponentials
 // over it (8 bytes for 64 logits), and the target's logit where it is among them.  A second kernel joins a
-// row's pairs.  8192 x 50304 x 768 bf16: 377 us, 1.68 PFLOP/s, the tensor pipe active 78% of the time; from
-// k = 256 down the epilogue bounds it (3205 x 98816 x 152: 135 us, about 4400 cycles a tile).
+// row's pairs.  8192 x 50304 x 768 bf16: 380 us, 1.67 PFLOP/s, the tensor pipe active 78% of the time; from
+// k = 256 down the epilogue bounds it (3205 x 98816 x 152: 155 us, about 4600 cycles a tile).
 //
 // Gradient: the logits again, a piece of the vocabulary at a time.  The epilogue turns them into d, 16
 // bits, the operand of both products that follow: dW's rows of the piece are complete, dx is added up
 // in fp32 over the pieces.  So the workspace is bounded whatever the vocabulary, and the flops are the
-// three products' 6 rows vocab k.  8192 x 50304 x 768 bf16: 1106 us, 1.72 PFLOP/s.
+// three products' 6 rows vocab k.  8192 x 50304 x 768 bf16: 1080 to 1130 us, 1.7 PFLOP/s.
 //
 // Exponentials in powers of two, one fused operation and one of the hardware's powers each (struct Base), over
 // the largest logit itself: lse = m + log S, so that a logit that stands alone is its row's lse to the bit.
@@ -126,7 +126,7 @@ struct StatsPair {
 };
 
 // The same of logits that are added up in registers, 1024 terms by the tensor cores at a time, for longer
-// contractions.  The tensor cores' sums are cut off, which takes about 1.3e-8 of a logit at every 16 terms: at k = 65536
+// contractions.  The tensor cores' sums are cut off, which takes about 1.5e-8 of a logit at every 16 terms: at k = 65536
 // one chain left lse 2.6e-4 too low (logits of deviation 2), this 3.5e-6.  512 terms would halve that, and cost 10% of the time
 // at 2048 x 32000 x 4096 where 1024 cost 4% (about 297, 309 and 323 us); up to 1024 one chain is taken, in the kernel above,
 // since the 64 sums of a thread hold its epilogue up (8192 x 50304 x 256: 173 us above, 187 here).

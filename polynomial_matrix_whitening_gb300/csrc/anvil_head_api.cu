@@ -63,8 +63,10 @@ anvil_status check_head(const anvil_head_desc* d) {
 }
 
 // The gradient's pieces: as many columns of the vocabulary as d takes 512 MB for, whole tiles, all but the
-// last of one size.  (8192 x 50304 x 768, us: pieces of 64 MB 1407, 128 MB 1304, 256 MB 1166, 512 MB 1121, the
-// whole of it 1125.)
+// last of one size.  (us, pieces of 128 MB, 256 MB, 512 MB, 1 GB, 2 GB: 8192 x 50304 x 768 1300, 1170, 1125, 1110,
+// 1110; 16384 x 50304 x 768 2740, 2410, 2410, 2320, 2230; 32768 x 32000 x 1024 4530, 4150, 3880, 3870, 3720; 4096 x
+// 65536 x 2048 2020, 1990, 1935, 1945, 1920; 2048 x 131072 x 4096 3855, 3730, 3855, 3725, 3675; 16384 x 131072 x 512
+// 5235, 4670, 4470, 4150, 4150: four times the memory would give 8% at most.)
 constexpr int64_t PIECE_BYTES = 512ll << 20;
 struct HeadGradLayout {
     Stored x, w;
