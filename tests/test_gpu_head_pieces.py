@@ -99,3 +99,20 @@ def test_a_column_that_cannot_be(A):  # noqa: F811
     assert n == 3 and not got[1][20000].any()
     keep = torch.arange(VOCAB, device="cuda") != 20000
     backward_check(x, w[keep], t - (t > 20000).long(), lse, gl, "bf16", "f32", (None, got[1][keep]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_pieces_of_long_contractions(A, transposed, dtype):  # noqa: F811
+    """More than 1024 features, where the logits are added up from several chains.  A hundred rows count, so that the
+    definition needs no others."""
+    k = 1100
+    x, w, t, gl = inputs(61, dtype, transposed, k=k)
+    keep = torch.zeros(ROWS, dtype=torch.bool, device="cuda")
+    keep[torch.arange(100, device="cuda") * 199 + 7] = True
+    t[~keep] = -1
+    t[keep] = torch.arange(100, device="cuda") * 330 + 5
+    _, lse = A.linear_cross_entropy(x, w, t)
+    n, (dx, dw) = pieces_of(A, lambda: A.linear_cross_entropy_backward(x, w, t, lse, gl, dweight_dtype=torch.float32))
+    assert n == 3 and not dx[~keep].any()
+    backward_check(x[keep], w, t[keep], lse[keep], gl[keep], dtype, "f32", (dx[keep], dw))
